@@ -30,6 +30,10 @@ MAX_LAYERS = 48
 
 STATUS_NONFINITE_LOGITS = 1
 STATUS_WAIT_TIMEOUT = 2
+STATUS_NONFINITE_KV = 4
+STATUS_BAD_BLOCK = 8
+KV_BLOCK = 64      # tokens of a KV-cache block
+ATTN_MAX_ROWS = 64  # query rows sharing a kv head: M * n_q_heads / n_kv_heads
 PATH_FUSED = 0    # one persistent cooperative kernel per call (TMA ring + mma.sync tiles; tcgen05 down products at M <= 5)
 PATH_STAGED = 1   # one launch per stage, fp32 CUDA-core arithmetic
 PATH_FUSED_TC = 2  # as PATH_FUSED, with the FP8 lm_head on tcgen05 tensor-memory tiles fed by TMA tensor copies
@@ -54,6 +58,11 @@ class fgm_mlp(ctypes.Structure):
                [("width", ctypes.c_int)]
 
 
+class fgm_kv_cache(ctypes.Structure):
+    _fields_ = [("k_q", ctypes.c_void_p), ("k_s", ctypes.c_void_p), ("v_q", ctypes.c_void_p), ("v_s", ctypes.c_void_p),
+                ("n_blocks", ctypes.c_int64), ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
 def lib() -> ctypes.CDLL:
     """The loaded CUDA library; raises if it has not been built."""
     global _lib
@@ -64,6 +73,7 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(LIB_PATH)
         vp, ci, i64, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
         LP = ctypes.POINTER(fgm_layer)
+        CP = ctypes.POINTER(fgm_kv_cache)
         sig = {
             "fgm_workspace_bytes": (sz, [ci, i64]),
             "fgm_workspace_init": (ci, [vp, sz, vp]),
@@ -83,6 +93,9 @@ def lib() -> ctypes.CDLL:
             "fgm_lm_head_sample": (ci, [vp, i64, vp, ci, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
             "fgm_verify_step_sample": (ci, [LP, ci, vp, i64, vp, vp, ci, ctypes.c_float, vp, vp, vp, vp, vp, vp,
                                             sz, vp]),
+            "fgm_kv_append": (ci, [CP, vp, vp, i64, ci, ci, vp, vp, ci, vp, sz, vp]),
+            "fgm_attn_workspace_bytes": (sz, [ci, ci, ci, ci, ci]),
+            "fgm_attn_fwd": (ci, [CP, vp, i64, ci, ci, ci, vp, vp, ci, ctypes.c_float, ci, vp, vp, vp, sz, vp]),
             "fgm_read_status": (ci, [vp, sz, ci, vp, vp]),
             "fgm_select_path": (ci, [ci]),
             "fgm_set_phase_trace": (ci, [vp, sz]),
@@ -179,10 +192,11 @@ def workspace_bytes(M: int = MAX_M, V: int = 0) -> int:
 
 
 class Workspace:
-    """Device scratch for the library's calls (one per concurrent stream)."""
+    """Device scratch for the library's calls (one per concurrent stream).
+    ``nbytes`` raises its size to what a call's own ``*_workspace_bytes`` says."""
 
-    def __init__(self, device=None, M: int = MAX_M, V: int = 0):
-        self.nbytes = workspace_bytes(M, V)
+    def __init__(self, device=None, M: int = MAX_M, V: int = 0, nbytes: int = 0):
+        self.nbytes = max(workspace_bytes(M, V), int(nbytes))
         self.buf = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device or "cuda")
         off = (-self.buf.data_ptr()) % 256
         self.t = self.buf[off:off + self.nbytes]
@@ -523,3 +537,144 @@ def verify_step_host(layers, emb: torch.Tensor, x_host: torch.Tensor, draft_host
 def layers_array(layers):
     """Pre-marshalled layer table, reusable across calls (pass as ``_arr``)."""
     return _layers_array(layers)
+
+
+# ---------------------------------------------------------------- 8-bit KV cache
+@dataclass
+class KVCache:
+    """One layer's 8-bit cache (see ``fgm_kv_cache`` in include/fgm.h): E4M3
+    codes k_q [blocks, kv heads, D / 64, 64, 64] and v_q [blocks, kv heads, D,
+    64] as uint8, fp32 scales k_s, v_s [blocks, kv heads]."""
+    k_q: torch.Tensor
+    v_q: torch.Tensor
+    k_s: torch.Tensor
+    v_s: torch.Tensor
+
+    @classmethod
+    def empty(cls, n_blocks: int, n_kv_heads: int, head_dim: int, device="cuda") -> "KVCache":
+        """A cache of n_blocks blocks of 64 tokens, not initialised: kv_append
+        writes a block's scales with its first token."""
+        if head_dim not in (64, 128, 256):
+            raise FgmError(f"head_dim must be 64, 128 or 256, got {head_dim}")
+        u8 = dict(dtype=torch.uint8, device=device)
+        return cls(torch.empty((n_blocks, n_kv_heads, head_dim // 64, KV_BLOCK, 64), **u8),
+                   torch.empty((n_blocks, n_kv_heads, head_dim, KV_BLOCK), **u8),
+                   torch.empty((n_blocks, n_kv_heads), dtype=torch.float32, device=device),
+                   torch.empty((n_blocks, n_kv_heads), dtype=torch.float32, device=device))
+
+    @property
+    def head_dim(self) -> int:
+        return int(self.v_q.shape[2])
+
+    @property
+    def n_kv_heads(self) -> int:
+        return int(self.v_q.shape[1])
+
+    def struct(self) -> fgm_kv_cache:
+        if self.v_q.dim() != 4:
+            raise FgmError(f"v_q: expected [blocks, kv heads, D, {KV_BLOCK}], got {tuple(self.v_q.shape)}")
+        n, h, d = (int(x) for x in self.v_q.shape[:3])
+        shapes = {"k_q": ((n, h, d // 64, KV_BLOCK, 64), torch.uint8), "v_q": ((n, h, d, KV_BLOCK), torch.uint8),
+                  "k_s": ((n, h), torch.float32), "v_s": ((n, h), torch.float32)}
+        for name, (shape, dt) in shapes.items():
+            t = getattr(self, name)
+            if tuple(t.shape) != shape or t.dtype != dt or t.device != self.v_q.device:
+                raise FgmError(f"{name}: expected {shape} {dt} on {self.v_q.device}, got {tuple(t.shape)} {t.dtype} "
+                               f"on {t.device}")
+        return fgm_kv_cache(_ptr(self.k_q).value, _ptr(self.k_s).value, _ptr(self.v_q).value, _ptr(self.v_s).value,
+                            n, h, d)
+
+
+def _on(device: torch.device, stream):
+    """Context that makes ``device`` and the call's stream current, so that
+    workspaces and outputs made inside belong to that stream."""
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    if s.device != device:
+        raise FgmError(f"the stream is on {s.device}, the tensors on {device}")
+    return torch.cuda.stream(s)
+
+
+def _token_rows(name: str, t: torch.Tensor, heads: int, D: int, device) -> int:
+    """bf16 [B, N, heads, D] whose tokens are dense and evenly spaced over the
+    whole batch (a slice of a fused projection's output qualifies); returns the
+    elements between tokens."""
+    if t.dim() != 4 or tuple(t.shape[2:]) != (heads, D) or t.dtype != torch.bfloat16 or t.device != device:
+        raise FgmError(f"{name}: expected bf16 [B, N, {heads}, {D}] on {device}, got {tuple(t.shape)} {t.dtype} "
+                       f"on {t.device}")
+    if not t.is_cuda:
+        raise FgmError("expected a CUDA tensor")
+    B, N = int(t.shape[0]), int(t.shape[1])
+    sb, sn, sh, sd = t.stride()
+    if (sd != 1) or (heads > 1 and sh != D):
+        raise FgmError(f"{name}: a token's heads must be contiguous, strides {t.stride()}")
+    step = sn if N > 1 else sb if B > 1 else heads * D
+    if N > 1 and B > 1 and sb != N * sn:
+        raise FgmError(f"{name}: sequences must follow each other at N token strides, strides {t.stride()}")
+    return int(step)
+
+
+def _seqs(B: int, lens: torch.Tensor, block_table: torch.Tensor | None, cache: KVCache, device) -> tuple[int, object]:
+    if tuple(lens.shape) != (B,) or lens.dtype != torch.int32 or lens.device != device:
+        raise FgmError(f"lens: expected int32 [{B}] on {device}, got {tuple(lens.shape)} {lens.dtype} on {lens.device}")
+    if block_table is None:
+        if int(cache.v_q.shape[0]) < B:
+            raise FgmError(f"without a block_table the cache's {int(cache.v_q.shape[0])} blocks are dealt to {B} "
+                           "sequences: too few")
+        return int(cache.v_q.shape[0]) // B, None
+    if block_table.dim() != 2 or block_table.shape[0] != B or block_table.dtype != torch.int32 or \
+            block_table.device != device:
+        raise FgmError(f"block_table: expected int32 [{B}, max_blocks] on {device}, got {tuple(block_table.shape)} "
+                       f"{block_table.dtype} on {block_table.device}")
+    return int(block_table.shape[1]), _ptr(block_table)
+
+
+def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, lens: torch.Tensor,
+              block_table: torch.Tensor | None = None, ws: Workspace | None = None, stream=None) -> None:
+    """Quantises the bf16 keys and values [B, N, kv heads, D] of each sequence's
+    last N tokens into the cache. lens int32 [B]: tokens per sequence, the new
+    ones included; block_table int32 [B, max_blocks] or None (each sequence owns
+    an equal run of blocks)."""
+    C = cache.struct()
+    dev = cache.v_q.device
+    step = _token_rows("k", k, cache.n_kv_heads, cache.head_dim, dev)
+    if _token_rows("v", v, cache.n_kv_heads, cache.head_dim, dev) != step or v.shape != k.shape:
+        raise FgmError(f"k and v must have one shape and token stride, got {tuple(k.shape)} {k.stride()} and "
+                       f"{tuple(v.shape)} {v.stride()}")
+    B, N = int(k.shape[0]), int(k.shape[1])
+    mb, table = _seqs(B, lens, block_table, cache, dev)
+    with _on(dev, stream):
+        ws = _ws(ws, dev)
+        _check(lib().fgm_kv_append(ctypes.byref(C), ctypes.c_void_p(k.data_ptr()), ctypes.c_void_p(v.data_ptr()), step,
+                                   B, N, _ptr(lens), table, mb, ws.ptr, ws.nbytes, _stream(None)))
+
+
+def attn_workspace_bytes(B: int, M: int, n_q_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    """Workspace bytes of attn_fwd (0 when the sizes are not valid)."""
+    return int(lib().fgm_attn_workspace_bytes(int(B), int(M), int(n_q_heads), int(n_kv_heads), int(head_dim)))
+
+
+def attn_fwd(cache: KVCache, q: torch.Tensor, lens: torch.Tensor, scale: float,
+             block_table: torch.Tensor | None = None, window: int = 0, out: torch.Tensor | None = None,
+             lse: torch.Tensor | None = None, ws: Workspace | None = None, stream=None) -> torch.Tensor:
+    """Attention of bf16 q [B, M, q heads, D], the last M tokens of each sequence
+    (already appended), over the cache; causal among them, with window > 0 over
+    that many positions. Returns bf16 [B, M, q heads, D]; lse fp32 [B, M, q
+    heads] receives the log of each row's sum of exponentials."""
+    C = cache.struct()
+    dev = cache.v_q.device
+    if q.dim() != 4:
+        raise FgmError(f"q: expected bf16 [B, M, q heads, D], got {tuple(q.shape)}")
+    B, M, Hq = (int(x) for x in q.shape[:3])
+    step = _token_rows("q", q, Hq, cache.head_dim, dev)
+    mb, table = _seqs(B, lens, block_table, cache, dev)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((B, M, Hq, cache.head_dim), dtype=torch.bfloat16, device=dev)
+        for name, t, shape, dt in (("out", out, tuple(q.shape), torch.bfloat16), ("lse", lse, (B, M, Hq), torch.float32)):
+            if t is not None and (tuple(t.shape) != shape or t.dtype != dt or t.device != dev):
+                raise FgmError(f"{name}: expected {dt} {shape} on {dev}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+        if ws is None:
+            ws = Workspace(dev, nbytes=attn_workspace_bytes(B, M, Hq, cache.n_kv_heads, cache.head_dim))
+        _check(lib().fgm_attn_fwd(ctypes.byref(C), ctypes.c_void_p(q.data_ptr()), step, B, M, Hq, _ptr(lens), table, mb,
+                                  float(scale), int(window), _ptr(out), _ptr(lse), ws.ptr, ws.nbytes, _stream(None)))
+    return out

@@ -10,6 +10,7 @@
 
 #include "basic_kernels.cuh"
 #include "fused_step.cuh"
+#include "host.h"
 #include "lm_head_fp8.cuh"
 #include "lm_head_fp8_tc.cuh"
 
@@ -134,6 +135,15 @@ int fused_grid()
         return fail(FGM_ERR_DEVICE, "the persistent kernel cannot be resident on this device");
     return G;
 }
+
+}  // namespace
+
+// What the other translation units share of the above (host.h).
+int host_fail(int code, const char *msg) { return fail(code, "%s", msg); }
+int host_device_ready(int *sms) { return device_ready(sms); }
+long long host_wait_limit_ns() { return g_timeout_ns; }
+
+namespace {
 
 // Launches the persistent kernel (cooperative: all CTAs co-resident).
 int tc_down_map(const uint8_t *down_q, CUtensorMap *map, bool dense);

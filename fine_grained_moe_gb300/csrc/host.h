@@ -1,0 +1,58 @@
+// Host-side helpers shared by the library's translation units.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdarg.h>
+#include <stddef.h>
+#include <stdint.h>
+#include <stdio.h>
+
+#include "common.cuh"
+
+namespace fgm {
+
+// Defined in fgm.cu: the calling thread's error message, the device check and
+// the bound of every wait inside a kernel.
+int host_fail(int code, const char *msg);
+int host_device_ready(int *sms);
+long long host_wait_limit_ns();
+
+inline int failf(int code, const char *fmt, ...)
+{
+    char buf[400];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return host_fail(code, buf);
+}
+
+#define FGM_HOST_TRY(expr)         \
+    do {                           \
+        int rc_ = (expr);          \
+        if (rc_ != FGM_OK)         \
+            return rc_;            \
+    } while (0)
+
+#define FGM_HOST_CUDA(call)                                                                     \
+    do {                                                                                        \
+        cudaError_t e_ = (call);                                                                \
+        if (e_ != cudaSuccess)                                                                  \
+            return failf(FGM_ERR_CUDA, "%s failed: %s", #call, cudaGetErrorString(e_));         \
+    } while (0)
+
+inline bool is_aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// A workspace of at least `need` bytes.
+inline int host_check_ws(const void *ws, size_t ws_bytes, size_t need)
+{
+    if (!ws)
+        return failf(FGM_ERR_WORKSPACE, "workspace is NULL");
+    if (!is_aligned(ws, 256))
+        return failf(FGM_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+    if (ws_bytes < need)
+        return failf(FGM_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", ws_bytes, need);
+    return FGM_OK;
+}
+
+}  // namespace fgm

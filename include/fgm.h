@@ -75,6 +75,11 @@ enum {
 enum {
     FGM_STATUS_NONFINITE_LOGITS = 1, /* a router or lm_head logit was NaN; treated as -inf */
     FGM_STATUS_WAIT_TIMEOUT = 2,     /* a grid-wide wait gave up; outputs are invalid */
+    FGM_STATUS_NONFINITE_KV = 4,     /* fgm_kv_append met a NaN (stored as 0) or an infinity (stored as
+                                        +-448 times the scale) */
+    FGM_STATUS_BAD_BLOCK = 8,        /* a sequence's length is negative or beyond its block table, or the
+                                        table names a block outside the cache: such blocks are neither
+                                        read nor written */
 };
 
 /* One MoE layer's weights (all device pointers).
@@ -322,6 +327,85 @@ int fgm_verify_step_sample(const fgm_layer *layers, int n_layers, const uint16_t
                            const uint16_t *x, const int32_t *draft, int M, float T, const float *u_acc,
                            const float *u_next, float *z, int32_t *argmax, int32_t *out, void *ws,
                            size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------- 8-bit KV cache and its attention
+ *
+ * The attention half of a layer's token mixing on M <= 8 new tokens per
+ * sequence ("llm-decoding", §"The exact architecture": grouped-query attention,
+ * sliding-window and full layers; §"Lever 1": the FP8 KV cache). Projections
+ * and rotary embedding are the caller's; the cache holds keys as they are
+ * attended to. One cache serves one layer. */
+
+#define FGM_KV_BLOCK 64        /* tokens of a cache block (a page, and the unit of a scale) */
+#define FGM_ATTN_MAX_ROWS 64   /* query rows that share a kv head: M * n_q_heads / n_kv_heads */
+
+/* A layer's cache: n_blocks blocks of 64 tokens for n_kv_heads heads of
+ * head_dim D (64, 128 or 256). Codes are E4M3; with s the fp32 scale of a
+ * (block, head), a value is e4m3(code) * s.
+ *  k_q  [n_blocks][n_kv_heads][D / 64][64 tokens][64]  dims of a token in 64-wide slices
+ *  v_q  [n_blocks][n_kv_heads][D][64 tokens]           tokens contiguous: the product with the
+ *                                                      probabilities contracts over them
+ *  k_s, v_s  [n_blocks][n_kv_heads]
+ * Codes 16-byte aligned. Bytes of tokens that no sequence holds may be
+ * anything, NaN codes included. */
+typedef struct fgm_kv_cache {
+    uint8_t *k_q;
+    float *k_s;
+    uint8_t *v_q;
+    float *v_s;
+    int64_t n_blocks;
+    int n_kv_heads;
+    int head_dim;
+} fgm_kv_cache;
+
+/* Writes the keys and values of N new tokens of each of B sequences: token i
+ * of sequence b is position p = lens[b] - N + i (skipped when negative), slot
+ * p % 64 of the sequence's block p / 64. Per (block, head), K and V apart:
+ *   s_new = the smallest power of two >= amax(the call's tokens there) / 448, at least 2^-60;
+ *   s     = max(s_new, old scale) if earlier tokens of the sequence stay in the block, else s_new;
+ *   new codes = e4m3(x / s); kept codes = e4m3(e4m3(code) * old / s), untouched while s = old.
+ * Scales are powers of two, so that growing one moves the kept codes by exact
+ * factors (values that become subnormal, below 2^-6 s, excepted). Slots
+ * behind the sequence's end are left as they are: to take rejected drafts
+ * back, call again with the smaller length. NaN is stored as 0 and infinities
+ * as the largest code, with FGM_STATUS_NONFINITE_KV; neither enters amax.
+ *  k, v         bf16 [B][N][n_kv_heads][D], 16-byte aligned; tokens token_stride elements
+ *               apart, sequences N * token_stride (a slice of a fused projection's output:
+ *               token_stride a multiple of 8, at least n_kv_heads * D)
+ *  lens         int32 [B] (device) tokens of each sequence, the new ones included
+ *  block_table  int32 [B][max_blocks] (device): cache block of a sequence's j-th block; NULL: block
+ *               b * max_blocks + j. Blocks that the call writes may not be shared by two sequences.
+ *  ws           any initialised workspace (for the status word) */
+int fgm_kv_append(const fgm_kv_cache *cache, const uint16_t *k, const uint16_t *v, int64_t token_stride, int B, int N,
+                  const int32_t *lens, const int32_t *block_table, int max_blocks, void *ws, size_t ws_bytes,
+                  void *stream);
+
+/* Bytes of workspace fgm_attn_fwd needs for these sizes on any sm_103 GPU
+ * (0 when they are not valid). Such a workspace serves every other entry
+ * point too, and fgm_workspace_init prepares it. */
+size_t fgm_attn_workspace_bytes(int B, int M, int n_q_heads, int n_kv_heads, int head_dim);
+
+/* Attention of the last M tokens of each of B sequences over the cache (the
+ * tokens themselves appended before). Query head h reads kv head
+ * h / (n_q_heads / n_kv_heads). Row i of sequence b stands at position
+ * p = lens[b] - M + i and sees positions t with 0 <= t <= p and, with
+ * window > 0, t > p - window:
+ *   s_t = scale * k_s * <q, e4m3(k_q[t])>,  P = softmax(s),  out = sum_t P_t v_s e4m3(v_q[t]),
+ *   lse = ln sum_t exp(s_t).
+ * A row that sees nothing (p < 0, lens[b] = 0) has out = 0 and lse = -inf.
+ * Scores and sums are fp32; queries enter the products exactly up to 2^-18 of
+ * their row's largest element, probabilities to 2^-8 of themselves. A row
+ * with a non-finite query element is NaN. The same call gives the same bits.
+ *  q            bf16 [B][M][n_q_heads][D], 16-byte aligned; tokens token_stride elements apart
+ *               (a multiple of 8, at least n_q_heads * D), sequences M * token_stride
+ *  lens, block_table, max_blocks   as fgm_kv_append; two sequences may share blocks
+ *  scale        finite, > 0
+ *  window       0: every earlier position; else that many, the row's own included
+ *  out          bf16 [B][M][n_q_heads][D] output, 16-byte aligned
+ *  lse          fp32 [B][M][n_q_heads] output or NULL */
+int fgm_attn_fwd(const fgm_kv_cache *cache, const uint16_t *q, int64_t token_stride, int B, int M, int n_q_heads,
+                 const int32_t *lens, const int32_t *block_table, int max_blocks, float scale, int window,
+                 uint16_t *out, float *lse, void *ws, size_t ws_bytes, void *stream);
 
 /* Selects the execution path of subsequent calls in this process; returns the
  * previous one. An unknown value leaves the path unchanged. Both paths compute
