@@ -400,6 +400,28 @@ int encode_tiled_fn(EncodeTiledFn *fn)
     return FGM_OK;
 }
 
+}  // namespace
+
+// Tensor map over rows of 64 bytes, boxes of box_rows of them in the 64-byte
+// swizzle (host.h).
+int host_rows64_map(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows)
+{
+    EncodeTiledFn encode = nullptr;
+    FGM_TRY(encode_tiled_fn(&encode));
+    const cuuint64_t dims[2] = {64, rows};
+    const cuuint64_t strides[1] = {64};
+    const cuuint32_t box[2] = {64, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(FGM_ERR_CUDA, "cuTensorMapEncodeTiled (64-byte rows) failed (%d)", static_cast<int>(r));
+    return FGM_OK;
+}
+
+namespace {
+
 // FP8 lm_head on the tensor-memory path (fp8tc): a 2-D tensor map over the
 // E4M3 rows, 128 x 128-byte boxes in the 128-byte swizzle.
 int run_lmhead_fp8_tc(const uint8_t *emb_q, const float *emb_s, int64_t V, const void *h, bool norm, int M,

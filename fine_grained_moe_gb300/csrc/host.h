@@ -1,6 +1,7 @@
 // Host-side helpers shared by the library's translation units.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdarg.h>
 #include <stddef.h>
@@ -16,6 +17,7 @@ namespace fgm {
 int host_fail(int code, const char *msg);
 int host_device_ready(int *sms);
 long long host_wait_limit_ns();
+int host_rows64_map(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows);
 
 inline int failf(int code, const char *fmt, ...)
 {

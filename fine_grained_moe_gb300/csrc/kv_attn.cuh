@@ -1,12 +1,73 @@
 // Attention of M <= 8 new tokens per sequence over the 8-bit cache
-// (fgm_attn_fwd): simplest form, one CTA per (query row, kv head, sequence),
-// fp32 on the CUDA cores, an online softmax over the blocks.
+// (fgm_attn_fwd).
+//
+//   s_t = scale k_s <q, kq_t>,  P = softmax(s),  out = sum_t P_t v_s vq_t
+//
+// Bytes bound it: a cached token costs 2 D bytes per kv head and feeds 4 R D
+// operations for the R = M n_q_heads / n_kv_heads <= 64 rows that share the
+// head, at most 128 per byte. So the kernel is built around the copies, and the
+// cache's codes go to the tensor cores as they lie in shared memory:
+//
+//  * Work is a list of units, two 64-token blocks of one (sequence, kv head),
+//    in that order. CTA c of G (one per SM) takes units [U c / G, U (c + 1) / G),
+//    whatever sequences they belong to: ragged batches, one long sequence and
+//    windows are balanced to a unit. Lengths are read on the device, so the
+//    launch does not depend on them and can be captured.
+//  * A producer warp streams a unit's K and V with TMA tensor copies (rows of
+//    64 bytes in the 64-byte swizzle) into two rings that fill the shared memory.
+//  * An issuing lane runs tcgen05.mma kind::f8f6f4 with the cache as the first
+//    operand: S^T = K Q^T (128 tokens x rows, K = D) and O^T += V^T P^T (D x rows,
+//    K = tokens; V lies token-contiguous in the cache for this). The rows are
+//    the narrow side, so 128 lanes are full whatever R is, both accumulators
+//    stay in tensor memory, and no cache byte passes through a register. (On
+//    sm_103 an E4M3 mma.sync is carried out as conversions and f16 products,
+//    about 15 instructions each: a kernel built on it, with the codes read from
+//    the same rings, ran the 32K verify step in 75 us, issue-bound.)
+//  * Eight softmax warps read S^T (a thread is a token and half of the rows),
+//    exponentiate and write P^T back to shared memory as the next operand. S
+//    and P have two buffers: the products of the next unit run under the
+//    softmax of this one.
+//
+// Precision. The second operands are split into two E4M3 terms in columns of
+// their own, hi and lo = 16 (x - hi), added in fp32 as hi + lo / 16. Queries:
+// scaled by a power of two to a largest element in (224, 448]; a bf16 has 8
+// significant bits and a term carries 4, so the split is exact down to half a
+// subnormal step of lo, 2^-14 / 224 of the row's largest. Probabilities: 64
+// exp2(s + log2 v_s - m), at most 256, within 2^-8 of themselves or
+// 2^-14 / 64 = 2^-20 of exp2(m). V's block scale rides in the exponent, so that
+// blocks of any scale add into one accumulator. The row sums use the unrounded
+// exponentials, in fp32.
+//
+// The reference m is not the running maximum but within 2 of it from below: a
+// unit whose scores stay under m + 2 (nearly all after the first few) needs no
+// maximum over its tokens, which are spread over the lanes, only a vote; one
+// that exceeds it computes the maxima and rescales the accumulator.
+//
+// A segment (the part of one (sequence, kv head) in one CTA) that is a whole
+// (sequence, head) is written out; one that spans CTAs leaves partial sums that
+// k_attn_join adds up in CTA order. No atomics: the same call gives the same
+// bits.
 #pragma once
+
+#include <cuda.h>
 
 #include "kv_append.cuh"
 
 namespace fgm {
 namespace kv {
+
+constexpr int kSoftWarps = 8;
+constexpr int kAttnThreads = 32 * (2 + kSoftWarps);    // copies, products, softmax
+constexpr int kTile = 2 * kBlock;                      // tokens of a unit
+constexpr int kMaxRing = 8;                            // stages of the K and of the V ring at most
+constexpr int kMetas = 16;                             // units' scales kept: ring depth + 2 and more
+constexpr int kMaxGrid = 160;                          // CTAs at most: the SMs of a full sm_103 part
+constexpr float kLowest = -1.0e30f;                    // stands for the maximum of nothing
+constexpr float kLift = 6.0f;                          // probabilities enter the product times 2^6
+constexpr float kSlack = 2.0f;                         // scores may exceed the reference by this much
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr size_t kSmemMax = 227 * 1024;
 
 struct AttnArgs {
     Cache c;
@@ -21,73 +82,861 @@ struct AttnArgs {
     uint16_t *out;
     float *lse;
     int32_t *status;
+    float *part;             // [G][2] partial segments: O [rows][D], m [rows], l [rows]
+    int4 *rec;               // [G] {b, h, last CTA, -} of the segment that starts in a CTA and goes on, b = -1: none
+    int rows;                // rows of the products: M * G rounded up to an instantiation
+    int k_ring, v_ring;      // stages
+    int min_units;           // units a CTA takes at least
+    long long timeout_ns;
 };
 
-template <int D>
-__global__ void __launch_bounds__(128) k_attn_simple(const AttnArgs p)
+// Floats of one partial segment.
+__host__ __device__ inline int64_t partial_floats(int rows, int D) { return static_cast<int64_t>(rows) * (D + 2); }
+
+// Shared memory of the operands that the kernel writes: query terms and two
+// buffers of probability terms; and 64 D bytes a block of K or V.
+__host__ __device__ inline int query_bytes(int rows, int D) { return 2 * rows * D; }
+__host__ __device__ inline int prob_bytes(int rows) { return 2 * rows * kTile; }
+
+struct Meta {                // a unit: block scales, first token, which of its blocks exist
+    float ks[2], vs[2];
+    int tok0;
+    int have;
+};
+
+struct AttnShared {
+    unsigned long long kfull[kMaxRing], kempty[kMaxRing], vfull[kMaxRing], vempty[kMaxRing];
+    unsigned long long mfull[kMetas];
+    unsigned long long sfull[2], sfree[2], pfull[2], pdone[2], qfull, drained;
+    Meta meta[kMetas];
+    float qf[FGM_ATTN_MAX_ROWS];                       // score of a unit product: 2^e scale log2(e)
+    float mx[4][FGM_ATTN_MAX_ROWS];                    // per lane quarter: a unit's maxima
+    float ls[4][FGM_ATTN_MAX_ROWS];                    // and the segment's sums
+    float m[FGM_ATTN_MAX_ROWS], l[FGM_ATTN_MAX_ROWS];
+    uint32_t tmem;
+    int abort;
+};
+
+__device__ __forceinline__ uint32_t saddr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+__device__ __forceinline__ long long now_ns()
 {
-    __shared__ float q[D], pr[64];
-    const int tid = threadIdx.x, h = blockIdx.y, b = blockIdx.z, i = blockIdx.x / p.G, g = blockIdx.x % p.G;
-    const int hq = h * p.G + g;
-    const int len = clamp_len(__ldg(p.lens + b), p.max_blocks, p.status, tid == 0 && blockIdx.x == 0 && h == 0);
-    for (int d = tid; d < D; d += 128)
-        q[d] = bf16_to_f32(p.q[(static_cast<int64_t>(b) * p.M + i) * p.stride + hq * D + d]);
-    const int pos = len - p.M + i;
-    const int t0 = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-    float m = -INFINITY, l = 0.0f, acc[(D + 127) / 128] = {};
-    for (int j = t0 / 64; j * 64 <= pos; ++j) {
-        const int64_t ph = phys_block(p.table, b, j, p.max_blocks, p.c.n_blocks);
-        if (ph < 0) {
-            if (tid == 0)
-                atomicOr(p.status, FGM_STATUS_BAD_BLOCK);
-            continue;
-        }
-        const uint8_t *k = p.c.k_q + (ph * p.c.heads + h) * (64 * D), *v = p.c.v_q + (ph * p.c.heads + h) * (64 * D);
-        __syncthreads();
-        if (tid < 64) {
-            const int t = j * 64 + tid;
-            float s = -INFINITY;
-            if (t >= t0 && t <= pos) {
-                float a = 0.0f, x[4];
-                for (int d = 0; d < D; d += 4) {
-                    e4m3x4_to_f32(*reinterpret_cast<const uint32_t *>(k + (d >> 6) * 4096 + tid * 64 + (d & 63)), x);
-                    a += q[d] * x[0] + q[d + 1] * x[1] + q[d + 2] * x[2] + q[d + 3] * x[3];
+    long long t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ void bar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Bounded wait on a barrier phase; false on timeout or abort.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, int *abort, long long deadline, int32_t *status,
+                                         int site, int index)
+{
+    for (int it = 0;; ++it) {
+        if (bar_try(bar, parity))
+            return true;
+        if ((it & 255) == 255) {
+            if (*reinterpret_cast<volatile int *>(abort))
+                return false;
+            if (now_ns() > deadline) {
+                *reinterpret_cast<volatile int *>(abort) = 1;
+                if ((atomicOr(status, FGM_STATUS_WAIT_TIMEOUT) & FGM_STATUS_WAIT_TIMEOUT) == 0) {
+                    status[1] = site;
+                    status[2] = blockIdx.x;
+                    status[3] = threadIdx.x >> 5;
+                    status[4] = index;
                 }
-                s = a * p.scale * p.c.k_s[ph * p.c.heads + h];
+                return false;
             }
-            pr[tid] = s;
         }
-        __syncthreads();
+    }
+}
+
+
+__device__ __forceinline__ void bar_init(unsigned long long *b, int count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(saddr(b)), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The tokens that row i of a sequence of length len sees: [lo, hi).
+__device__ __forceinline__ void row_range(int len, int M, int window, int i, int &lo, int &hi)
+{
+    const int pos = len - M + i;
+    hi = max(pos + 1, 0);
+    lo = window > 0 ? max(pos - window + 1, 0) : 0;
+}
+
+// Blocks [first, first + count) of a sequence that any row sees.
+__device__ __forceinline__ int seq_blocks(int len, int M, int window, int &first)
+{
+    int lo, hi;
+    row_range(len, M, window, 0, lo, hi);
+    first = lo / kBlock;
+    return (len + kBlock - 1) / kBlock - first;
+}
+
+
+// Descriptor of a K-major operand in the 64-byte swizzle: atoms of 8 rows x 64
+// bytes, 512 bytes apart; descriptor version 1, layout type 4.
+__device__ __forceinline__ uint64_t desc64(uint32_t addr)
+{
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (1ull << 16) | (32ull << 32) | (1ull << 46) | (4ull << 61);
+}
+
+// Byte of element k (0..63) of row n in such a slice: 16-byte unit k / 16 of row
+// n lies at unit (k / 16) ^ (n / 2 % 4).
+__device__ __forceinline__ uint32_t at64(int n, int k)
+{
+    return static_cast<uint32_t>(n * 64 + ((((k >> 4) ^ (n >> 1)) & 3) << 4) + (k & 15));
+}
+
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
+
+__device__ __forceinline__ void commit(unsigned long long *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(bar)) : "memory");
+}
+
+__device__ __forceinline__ void after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_ld4(uint32_t a, float *v)
+{
+    uint32_t r[4];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tmem_st4(uint32_t a, const float *v)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(__float_as_uint(v[0])),
+                 "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3]))
+                 : "memory");
+}
+
+// (the loaded registers pass through, so that no use of them moves ahead of the wait)
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(float (&v)[N])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        asm volatile("" : "+f"(v[i]));
+}
+
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap *map, int row, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t e4m3_pair(float a, float b)   // a in the low byte
+{
+    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+
+__device__ __forceinline__ float2 e4m3_values(uint32_t w)
+{
+    return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w), __NV_E4M3)));
+}
+
+// A place in the list of units.
+struct Cursor {
+    int b, h, u, n, first, blocks;    // sequence, kv head, unit of the segment, its units, first block and blocks
+};
+
+// D: head dim; R: rows of the products (8, 16, 32, 48 or 64).
+template <int D, int R>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    k_attn(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const AttnArgs p)
+{
+    constexpr int kSlices = D / 64, kN = 2 * R;
+    constexpr int kSide = kTile * D;                             // bytes of a unit's K or V
+    constexpr int kMTiles = D == 256 ? 2 : 1;                    // 128-lane tiles of O^T
+    constexpr int kNR = R / 2;                                   // rows of a softmax thread
+    constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(kN >> 3) << 17) | (8u << 24);   // fp32 += E4M3 x E4M3, M = 128
+    constexpr uint32_t kOCol = 2 * kN;                           // S buffers first, then O tiles
+    constexpr uint32_t kUsed = 2 * kN + kMTiles * kN;
+    constexpr uint32_t kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+    extern __shared__ uint8_t dsm_raw[];
+    __shared__ AttnShared sh;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int heads = p.c.heads;
+    uint8_t *dsm = dsm_raw + ((1024u - (saddr(dsm_raw) & 1023u)) & 1023u);
+    uint8_t *qs = dsm, *ps = qs + query_bytes(R, D), *kring = ps + 2 * prob_bytes(R);
+    uint8_t *vring = kring + p.k_ring * kSide;
+    // (for D = 64 the 128-row first operand of O^T runs 4 KB past a block's V: one more block's room behind the ring)
+    int *cum = reinterpret_cast<int *>(vring + p.v_ring * kSide + (D == 64 ? kBlock * D : 0));   // [B + 1] units before each sequence
+    int *lens = cum + p.B + 1;                                   // [B] clamped lengths
+    const long long deadline = now_ns() + p.timeout_ns;
+
+    if (tid == 0) {
+        for (int i = 0; i < kMaxRing; ++i) {
+            bar_init(&sh.kfull[i], 1);
+            bar_init(&sh.kempty[i], 1);
+            bar_init(&sh.vfull[i], 1);
+            bar_init(&sh.vempty[i], 1);
+        }
+        for (int i = 0; i < kMetas; ++i)
+            bar_init(&sh.mfull[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&sh.sfull[i], 1);
+            bar_init(&sh.sfree[i], kSoftWarps);
+            bar_init(&sh.pfull[i], kSoftWarps);
+            bar_init(&sh.pdone[i], 1);
+        }
+        bar_init(&sh.qfull, kSoftWarps);
+        bar_init(&sh.drained, 1);
+        sh.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&sh.tmem)), "r"(kCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (warp == 0) {
+        int base = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const int b = b0 + lane;
+            int n = 0, first;
+            if (b < p.B) {
+                const int len = clamp_len(__ldg(p.lens + b), p.max_blocks, p.status, blockIdx.x == 0);
+                lens[b] = len;
+                n = (seq_blocks(len, p.M, p.window, first) + 1) / 2 * heads;
+            }
+            int inc = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+                if (lane >= o)
+                    inc += v;
+            }
+            if (b < p.B)
+                cum[b] = base + inc - n;
+            base += __shfl_sync(0xFFFFFFFFu, inc, 31);
+        }
+        if (lane == 0)
+            cum[p.B] = base;
+    }
+    before_sync();
+    __syncthreads();
+    after_sync();
+    asm volatile("griddepcontrol.launch_dependents;");
+    const uint32_t tmem = sh.tmem;
+
+    const int64_t U = cum[p.B];
+    const int64_t by_min = (U + p.min_units - 1) / p.min_units;
+    const int64_t G = by_min < gridDim.x ? (by_min > 0 ? by_min : 1) : gridDim.x;   // CTAs that take units
+    const int u0 = blockIdx.x < G ? static_cast<int>(U * blockIdx.x / G) : 0;
+    const int u1 = blockIdx.x < G ? static_cast<int>(U * (blockIdx.x + 1) / G) : 0;
+    const int n_units = u1 - u0;
+
+    auto locate = [&](int u) -> Cursor {
+        int a = 0, z = p.B;                        // cum[a] <= u < cum[z]: ends on a sequence that has units
+        while (z - a > 1) {
+            const int mid = (a + z) >> 1;
+            if (cum[mid] <= u)
+                a = mid;
+            else
+                z = mid;
+        }
+        Cursor at;
+        at.b = a;
+        at.blocks = seq_blocks(lens[a], p.M, p.window, at.first);
+        at.n = (at.blocks + 1) / 2;
+        const int r = u - cum[a];
+        at.h = r / at.n;
+        at.u = r % at.n;
+        return at;
+    };
+    auto wait = [&](unsigned long long *bar, int phase, int site, int index) -> bool {
+        return bar_wait(saddr(bar), phase & 1, &sh.abort, deadline, p.status, site, index);
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ copies
+        // Lane i looks up unit 32 k + i (block table and scales) a round ahead.
+        int64_t at_n[2];
+        float ks_n[2], vs_n[2];
+        int tok_n = 0;
+        auto look = [&](int i) {
+            at_n[0] = at_n[1] = -1;
+            ks_n[0] = ks_n[1] = vs_n[0] = vs_n[1] = 1.0f;
+            if (i >= n_units)
+                return;
+            const Cursor cu = locate(u0 + i);
+            const int j = cu.first + 2 * cu.u;
+            tok_n = j * kBlock;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (j + k >= cu.first + cu.blocks)
+                    break;
+                const int64_t ph = phys_block(p.table, cu.b, j + k, p.max_blocks, p.c.n_blocks);
+                if (ph >= 0) {
+                    at_n[k] = ph * heads + cu.h;
+                    ks_n[k] = __ldg(p.c.k_s + at_n[k]);
+                    vs_n[k] = __ldg(p.c.v_s + at_n[k]);
+                } else {
+                    atomicOr(p.status, FGM_STATUS_BAD_BLOCK);
+                }
+            }
+        };
+        if (lane == 0) {
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
+        }
+        bool ok = true;
+        int k_issued = 0, v_issued = 0;
+        look(lane);
+        for (int r = 0; r < n_units && ok; r += 32) {
+            const int64_t a0 = at_n[0], a1 = at_n[1];
+            const float k0 = ks_n[0], k1 = ks_n[1], s0 = vs_n[0], s1 = vs_n[1];
+            const int tok0 = tok_n;
+            if (r + 32 < n_units)
+                look(r + 32 + lane);
+            const int m = min(32, n_units - r);
+            for (int i = 0; i < m && ok; ++i) {
+                const int u = r + i;
+                const int64_t at[2] = {__shfl_sync(0xFFFFFFFFu, a0, i), __shfl_sync(0xFFFFFFFFu, a1, i)};
+                if (lane == 0) {
+                    const uint32_t bytes = ((at[0] >= 0) + (at[1] >= 0)) * (kBlock * D);
+                    const int sk = u % p.k_ring, sv = u % p.v_ring;
+                    if (u >= p.k_ring)
+                        ok = wait(&sh.kempty[sk], u / p.k_ring - 1, 13, u);
+                    if (ok) {
+                        const uint32_t bar = saddr(&sh.kfull[sk]), dst = saddr(kring + sk * kSide);
+                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+                        for (int k = 0; k < 2; ++k)
+                            if (at[k] >= 0)
+#pragma unroll
+                                for (int c = 0; c < kSlices; ++c)
+                                    tma_rows(dst + c * (kTile * 64) + k * (kBlock * 64), &kmap,
+                                             static_cast<int>(at[k] * D) + c * kBlock, bar);
+                        k_issued = u + 1;
+                        if (u >= p.v_ring)
+                            ok = wait(&sh.vempty[sv], u / p.v_ring - 1, 14, u);
+                    }
+                    if (ok) {
+                        const uint32_t bar = saddr(&sh.vfull[sv]), dst = saddr(vring + sv * kSide);
+                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+                        for (int k = 0; k < 2; ++k)
+                            if (at[k] >= 0)
+                                tma_rows(dst + k * (kBlock * D), &vmap, static_cast<int>(at[k] * D), bar);
+                        v_issued = u + 1;
+                    }
+                }
+                // the scales last: the first units' copies are on their way before they arrive
+                const float ks[2] = {__shfl_sync(0xFFFFFFFFu, k0, i), __shfl_sync(0xFFFFFFFFu, k1, i)};
+                const float vs[2] = {__shfl_sync(0xFFFFFFFFu, s0, i), __shfl_sync(0xFFFFFFFFu, s1, i)};
+                const int t0 = __shfl_sync(0xFFFFFFFFu, tok0, i);
+                if (lane == 0 && ok) {
+                    // (entry u - 16 has been read: the ring is at most 8 deep and the softmax 2 behind the products)
+                    sh.meta[u % kMetas] = Meta{{ks[0], ks[1]}, {vs[0], vs[1]}, t0, (at[0] >= 0) | (at[1] >= 0) << 1};
+                    bar_arrive(saddr(&sh.mfull[u % kMetas]));
+                }
+                ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+            }
+        }
+        // every issued copy lands before the CTA may exit
+        if (lane == 0) {
+            for (int u = max(0, k_issued - p.k_ring); u < k_issued; ++u)
+                for (int it = 0; it < (1 << 22) && !bar_try(saddr(&sh.kfull[u % p.k_ring]), (u / p.k_ring) & 1); ++it)
+                    ;
+            for (int u = max(0, v_issued - p.v_ring); u < v_issued; ++u)
+                for (int it = 0; it < (1 << 22) && !bar_try(saddr(&sh.vfull[u % p.v_ring]), (u / p.v_ring) & 1); ++it)
+                    ;
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ products
+        if (lane == 0) {
+            bool ok = true;
+            auto scores = [&](int u) {             // S^T of unit u
+                const int slot = u % p.k_ring;
+                if (ok && u >= 2)
+                    ok = wait(&sh.sfree[u & 1], (u >> 1) - 1, 15, u);
+                if (ok)
+                    ok = wait(&sh.kfull[slot], u / p.k_ring, 16, u);
+                if (!ok)
+                    return;
+                after_sync();
+                const uint32_t a = saddr(kring + slot * kSide), b = saddr(qs), d = tmem + (u & 1) * kN;
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k)
+                    mma_f8(d, desc64(a + (k >> 1) * (kTile * 64) + (k & 1) * 32), desc64(b + (k >> 1) * (kN * 64) + (k & 1) * 32),
+                           kIdesc, k != 0);
+                commit(&sh.kempty[slot]);
+                commit(&sh.sfull[u & 1]);
+            };
+            int seg = 0;
+            for (int done = 0; done < n_units && ok; ++seg) {
+                const Cursor cu = locate(u0 + done);
+                const int n = min(cu.n - cu.u, n_units - done);
+                ok = wait(&sh.qfull, seg, 17, seg);
+                after_sync();
+                scores(done);
+                bool add = false;
+                for (int i = 0; i < n && ok; ++i) {
+                    const int u = done + i, slot = u % p.v_ring;
+                    if (i + 1 < n)
+                        scores(u + 1);
+                    if (ok)
+                        ok = wait(&sh.vfull[slot], u / p.v_ring, 18, u);
+                    if (ok)
+                        ok = wait(&sh.pfull[u & 1], u >> 1, 19, u);
+                    if (!ok)
+                        break;
+                    after_sync();
+                    const int have = sh.meta[u % kMetas].have;
+                    const uint32_t a = saddr(vring + slot * kSide), b = saddr(ps + (u & 1) * prob_bytes(R));
+                    for (int k = 0; k < 2; ++k) {
+                        if (!(have >> k & 1))
+                            continue;
+#pragma unroll
+                        for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+                            for (int t = 0; t < kMTiles; ++t)
+                                mma_f8(tmem + kOCol + t * kN, desc64(a + k * (kBlock * D) + t * (128 * 64) + kk * 32),
+                                       desc64(b + k * (kN * 64) + kk * 32), kIdesc, add);
+                            add = true;
+                        }
+                    }
+                    commit(&sh.vempty[slot]);
+                    commit(&sh.pdone[u & 1]);
+                }
+                done += n;
+            }
+            // every issued product completes before the tensor memory is released
+            commit(&sh.drained);
+            for (int it = 0; it < (1 << 22) && !bar_try(saddr(&sh.drained), 0); ++it)
+                ;
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax
+        const int w = warp - 2, quarter = warp & 3, half = w >> 2, stid = tid - 64;
+        const int tl = quarter * 32 + lane;        // token of a unit, lane of an accumulator
+        const int blk = quarter >> 1;
+        const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
+        const int rows = p.M * p.G;
+        bool alive = true;
+        int4 rec = make_int4(-1, 0, 0, 0);
+
+        // sequences without a token: zero rows
+        for (int b = blockIdx.x; b < p.B; b += gridDim.x)
+            if (cum[b + 1] == cum[b]) {
+                const int64_t row0 = static_cast<int64_t>(b) * p.M * p.Hq;
+                for (int i = stid; i < p.M * p.Hq * (D / 8); i += kSoftWarps * 32)
+                    reinterpret_cast<uint4 *>(p.out + row0 * D)[i] = make_uint4(0, 0, 0, 0);
+                if (p.lse)
+                    for (int i = stid; i < p.M * p.Hq; i += kSoftWarps * 32)
+                        p.lse[row0 + i] = -INFINITY;
+            }
+
+        for (int done = 0; done < n_units;) {
+            const Cursor cu = locate(u0 + done);
+            const int n = min(cu.n - cu.u, n_units - done);
+            const int len = lens[cu.b];
+
+            // query terms of this (sequence, head): a warp takes every 8th row
+            for (int r = w; r < R; r += kSoftWarps) {
+                const bool live = r < rows;
+                const uint16_t *src = p.q + (static_cast<int64_t>(cu.b) * p.M + r / p.G) * p.stride +
+                                      (cu.h * p.G + r % p.G) * D;
+                constexpr int kE = (D + 127) / 128;
+                uint2 x[kE];
+                unsigned amax = 0;
+#pragma unroll
+                for (int e = 0; e < kE; ++e) {
+                    const int d = (e * 32 + lane) * 4;
+                    x[e] = make_uint2(0, 0);
+                    if (live && d < D)
+                        x[e] = *reinterpret_cast<const uint2 *>(src + d);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const unsigned a = ((k < 2 ? x[e].x : x[e].y) >> (16 * (k & 1))) & 0x7FFFu;
+                        amax = max(amax, a < 0x7F80u ? a : 0u);
+                    }
+                }
+                amax = __reduce_max_sync(0xFFFFFFFFu, amax);
+                // 2^ex with the largest element in (224, 448] 2^ex; no lower than 2^-120
+                const unsigned u = amax << 16;
+                const int ex = max(static_cast<int>(u >> 23) + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0) - 8, 7);
+                const float up = __uint_as_float(static_cast<unsigned>(254 - ex) << 23);
+                if (lane == 0)
+                    sh.qf[r] = __uint_as_float(static_cast<unsigned>(ex) << 23) * (p.scale * kLog2e);
+#pragma unroll
+                for (int e = 0; e < kE; ++e) {
+                    const int d = (e * 32 + lane) * 4;
+                    if (d >= D)
+                        break;
+                    const float2 a = bf16x2_to_f32(x[e].x), b = bf16x2_to_f32(x[e].y);
+                    auto fin = [&](float v) { return fabsf(v) < INFINITY ? v * up : __int_as_float(0x7FC00000); };
+                    const float y[4] = {fin(a.x), fin(a.y), fin(b.x), fin(b.y)};
+                    const uint32_t hi = to_e4m3x4(y[0], y[1], y[2], y[3]);
+                    float z[4];
+                    e4m3x4_to_f32(hi, z);
+                    const uint32_t lo = to_e4m3x4(16.0f * (y[0] - z[0]), 16.0f * (y[1] - z[1]), 16.0f * (y[2] - z[2]),
+                                                  16.0f * (y[3] - z[3]));
+                    uint8_t *at = qs + (d >> 6) * (kN * 64);
+                    *reinterpret_cast<uint32_t *>(at + at64(r, d & 63)) = hi;
+                    *reinterpret_cast<uint32_t *>(at + at64(R + r, d & 63)) = lo;
+                }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            before_sync();                         // the last segment's accumulator has been read, too
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (lane == 0)
+                bar_arrive(saddr(&sh.qfull));
+
+            float m[kNR], l[kNR];
+#pragma unroll
+            for (int r = 0; r < kNR; ++r) {
+                m[r] = kLowest;
+                l[r] = 0.0f;
+            }
+            int lo_min, hi_min, lo_max, hi_max;
+            row_range(len, p.M, p.window, 0, lo_min, hi_min);
+            row_range(len, p.M, p.window, p.M - 1, lo_max, hi_max);
+            bool any_pv = false;                   // a product went into the accumulator
+
+            for (int i = 0; i < n; ++i) {
+                const int u = done + i;
+                float s[2 * kNR];                  // hi, then lo
+                if (alive)
+                    alive = wait(&sh.mfull[u % kMetas], u / kMetas, 20, u) && wait(&sh.sfull[u & 1], u >> 1, 21, u);
+                alive = __all_sync(0xFFFFFFFFu, alive);
+                after_sync();
+                const Meta me = sh.meta[u % kMetas];
+#pragma unroll
+                for (int r = 0; r < kNR; r += 4) {
+                    tmem_ld4(tmem + lanes + (u & 1) * kN + half * kNR + r, s + r);
+                    tmem_ld4(tmem + lanes + (u & 1) * kN + R + half * kNR + r, s + kNR + r);
+                }
+                tmem_wait_ld(s);
+                before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(saddr(&sh.sfree[u & 1]));
+
+                // scores in powers of two, with V's scale on top
+                const float ks = blk ? me.ks[1] : me.ks[0], vs = blk ? me.vs[1] : me.vs[0];
+                const float lv = log2f(vs), ivs = 1.0f / vs;
+                const int tok = me.tok0 + tl;
+                const bool here = me.have >> blk & 1;
+                const bool edge = me.tok0 + kTile > hi_min || me.tok0 < lo_max || me.have != 3;
+                bool over = false;
+#pragma unroll
+                for (int r = 0; r < kNR; ++r) {
+                    s[r] = fmaf(fmaf(s[kNR + r], 0.0625f, s[r]), sh.qf[half * kNR + r] * ks, lv);
+                    if (edge) {
+                        int lo = 0, hi = 0;
+                        if (half * kNR + r < rows)
+                            row_range(len, p.M, p.window, (half * kNR + r) / p.G, lo, hi);
+                        s[r] = here && tok >= lo && tok < hi ? s[r] : -INFINITY;
+                    }
+                    over |= s[r] > m[r] + kSlack;
+                }
+                int any;
+                asm volatile(
+                    "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 128, p;\n\t"
+                    "selp.s32 %0, 1, 0, q;\n\t}"
+                    : "=r"(any)
+                    : "r"(static_cast<int>(over)), "r"(2 + half)
+                    : "memory");
+                if (any) {
+                    // the unit's maxima over its 128 tokens; new references; the accumulator follows
+#pragma unroll
+                    for (int r = 0; r < kNR; ++r) {
+                        float x = s[r];
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1)
+                            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+                        if (lane == 0)
+                            sh.mx[quarter][half * kNR + r] = x;
+                    }
+                    asm volatile("barrier.cta.sync %0, 128;" ::"r"(2 + half) : "memory");
+                    float c[kNR];
+#pragma unroll
+                    for (int r = 0; r < kNR; ++r) {
+                        float x = m[r];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            x = fmaxf(x, sh.mx[k][half * kNR + r]);
+                        c[r] = ex2(m[r] - x);
+                        l[r] *= c[r];
+                        m[r] = x;
+                    }
+                    if (any_pv) {
+                        if (alive)
+                            alive = wait(&sh.pdone[(u - 1) & 1], (u - 1) >> 1, 22, u);
+                        alive = __all_sync(0xFFFFFFFFu, alive);
+                        after_sync();
+#pragma unroll
+                        for (int t = 0; t < kMTiles; ++t)
+#pragma unroll
+                            for (int r = 0; r < kNR; r += 4) {
+                                const uint32_t a = tmem + lanes + kOCol + t * kN + half * kNR + r;
+                                float o[8];
+                                tmem_ld4(a, o);
+                                tmem_ld4(a + R, o + 4);
+                                tmem_wait_ld(o);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    o[k] *= c[r + k];
+                                    o[4 + k] *= c[r + k];
+                                }
+                                tmem_st4(a, o);
+                                tmem_st4(a + R, o + 4);
+                            }
+                        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    }
+                    // (sh.mx is written again only after every reader has passed the next vote)
+                }
+                any_pv |= me.have != 0;
+                // the buffer's last product is done
+                if (alive && u >= 2)
+                    alive = wait(&sh.pdone[u & 1], (u >> 1) - 1, 23, u);
+                alive = __all_sync(0xFFFFFFFFu, alive);
+                uint8_t *pt = ps + (u & 1) * prob_bytes(R) + blk * (kN * 64);
+                const int kt = tl & 63;
+#pragma unroll
+                for (int r = 0; r < kNR; r += 2) {
+                    const float p0 = ex2(s[r] - (m[r] - kLift)), p1 = ex2(s[r + 1] - (m[r + 1] - kLift));
+                    l[r] = fmaf(p0, ivs, l[r]);
+                    l[r + 1] = fmaf(p1, ivs, l[r + 1]);
+                    const uint32_t hi = e4m3_pair(p0, p1);
+                    const float2 z = e4m3_values(hi);
+                    const uint32_t lo = e4m3_pair(16.0f * (p0 - z.x), 16.0f * (p1 - z.y));
+                    const int nr = half * kNR + r;
+                    pt[at64(nr, kt)] = static_cast<uint8_t>(hi);
+                    pt[at64(nr + 1, kt)] = static_cast<uint8_t>(hi >> 8);
+                    pt[at64(R + nr, kt)] = static_cast<uint8_t>(lo);
+                    pt[at64(R + nr + 1, kt)] = static_cast<uint8_t>(lo >> 8);
+                }
+                if (edge) {
+                    // V codes of tokens that no row sees may be anything, NaN included: zeros
+                    const int slot = u % p.v_ring;
+                    if (alive)
+                        alive = wait(&sh.vfull[slot], u / p.v_ring, 24, u);
+                    alive = __all_sync(0xFFFFFFFFu, alive);
+                    if (alive && here && (tok < lo_min || tok >= len)) {
+                        uint8_t *vt = vring + slot * kSide + blk * (kBlock * D);
+                        for (int d = half * (D / 2); d < (half + 1) * (D / 2); ++d)
+                            vt[at64(d, kt)] = 0;
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(saddr(&sh.pfull[u & 1]));
+            }
+
+            // -------------------------------------------------------- end of the segment
+#pragma unroll
+            for (int r = 0; r < kNR; ++r) {
+                const float x = warp_sum(l[r]);
+                if (lane == 0)
+                    sh.ls[quarter][half * kNR + r] = x;
+                if (quarter == 0 && lane == 0)
+                    sh.m[half * kNR + r] = m[r];
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (stid < R)
+                sh.l[stid] = (sh.ls[0][stid] + sh.ls[1][stid]) + (sh.ls[2][stid] + sh.ls[3][stid]);
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            const int last_u = done + n - 1;
+            if (alive)
+                alive = wait(&sh.pdone[last_u & 1], last_u >> 1, 25, last_u);
+            alive = __all_sync(0xFFFFFFFFu, alive);
+            after_sync();
+            const bool starts = cu.u == 0, ends = cu.u + n == cu.n, whole = starts && ends;
+            float *part = p.part + (blockIdx.x * 2 + (starts ? 1 : 0)) * partial_floats(R, D);
+            // a thread is a dim; D = 256: a half of the warps per lane tile, else per half of the rows
+            const int d = (D == 256 ? half * 128 : 0) + tl;
+            const int ra = D == 256 ? 0 : half * kNR, rz = D == 256 ? R : ra + kNR;
+            const uint32_t oa = tmem + lanes + kOCol + (D == 256 ? half * kN : 0);
+            if (D != 64 || quarter < 2) {
+#pragma unroll 4
+                for (int r = ra; r < rz; r += 4) {
+                    float o[8];
+                    tmem_ld4(oa + r, o);
+                    tmem_ld4(oa + R + r, o + 4);
+                    tmem_wait_ld(o);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float ls = sh.l[r + k];
+                        const float v = ls == 0.0f ? 0.0f : fmaf(o[4 + k], 0.0625f, o[k]);
+                        if (!whole) {
+                            part[(r + k) * D + d] = v;
+                        } else if (r + k < rows) {
+                            const int64_t row = (static_cast<int64_t>(cu.b) * p.M + (r + k) / p.G) * p.Hq + cu.h * p.G +
+                                                (r + k) % p.G;
+                            p.out[row * D + d] = f32_to_bf16(ls == 0.0f ? 0.0f : v / ls);
+                        }
+                    }
+                }
+            }
+            if (stid < R) {
+                const float ls = sh.l[stid], mm = sh.m[stid];
+                if (!whole) {
+                    part[R * D + stid] = mm;
+                    part[R * (D + 1) + stid] = ls;
+                } else if (p.lse && stid < rows) {
+                    const int64_t row = (static_cast<int64_t>(cu.b) * p.M + stid / p.G) * p.Hq + cu.h * p.G + stid % p.G;
+                    p.lse[row] = ls == 0.0f ? -INFINITY : (mm - kLift + log2f(ls)) * kLn2;
+                }
+            }
+            if (starts && !ends) {
+                // the CTA that holds the segment's last unit: the largest c with U c / G <= unit
+                const int64_t last = u0 + done - cu.u + cu.n - 1;
+                rec = make_int4(cu.b, cu.h, static_cast<int>(((last + 1) * G + U - 1) / U - 1), 0);
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");     // sh.m, sh.l, sh.qf are free again
+            done += n;
+        }
+        if (stid == 0)
+            p.rec[blockIdx.x] = rec;
+    }
+    before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        after_sync();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols) : "memory");
+    }
+}
+
+// Adds up the partial segments of every (sequence, kv head) that spans CTAs, in
+// CTA order. Items are (segment, row), dealt to the CTAs in turn; a thread owns
+// four output elements of every kLanes-th partial, and the lanes meet in shared
+// memory, also in order.
+template <int D>
+__global__ void __launch_bounds__(256) k_attn_join(const AttnArgs p, int ctas)
+{
+    constexpr int kCols = D / 4, kLanes = 256 / kCols;
+    __shared__ float4 acc[kLanes][kCols];
+    __shared__ float w[kMaxGrid], sm[8], sl[8];
+    __shared__ int list[kMaxGrid], n_list;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (warp == 0) {
+        int n = 0;
+        for (int c0 = 0; c0 < ctas; c0 += 32) {
+            const bool on = c0 + lane < ctas && __ldcg(p.rec + c0 + lane).x >= 0;
+            const unsigned bits = __ballot_sync(0xFFFFFFFFu, on);
+            if (on)
+                list[n + __popc(bits & ((1u << lane) - 1))] = c0 + lane;
+            n += __popc(bits);
+        }
+        if (lane == 0)
+            n_list = n;
+    }
+    __syncthreads();
+    const int R = p.M * p.G, rows = p.rows;
+    const int64_t pf = partial_floats(p.rows, D);
+    for (int item = blockIdx.x; item < n_list * R; item += gridDim.x) {
+        const int c0 = list[item / R], r = item % R;
+        const int4 rec = __ldcg(p.rec + c0);
+        const int n = rec.z - c0 + 1;
+        // partial i: the first CTA's second slot, then the others' first slots
+        auto part = [&](int i) { return p.part + ((c0 + i) * 2 + (i == 0 ? 1 : 0)) * pf; };
+        float m = kLowest, l = 0.0f;
+        if (tid < n) {
+            m = __ldcg(part(tid) + rows * D + r);
+            l = __ldcg(part(tid) + rows * (D + 1) + r);
+        }
         float mx = m;
-        for (int t = 0; t < 64; ++t)
-            mx = fmaxf(mx, pr[t]);
-        const float f = m == -INFINITY ? 0.0f : expf(m - mx), vs = p.c.v_s[ph * p.c.heads + h];
-        l *= f;
-        for (int e = 0; e < (D + 127) / 128; ++e)
-            acc[e] *= f;
-        for (int t = 0; t < 64; ++t) {
-            if (pr[t] == -INFINITY)
-                continue;
-            const float w = expf(pr[t] - mx);
-            l += w;
-            for (int e = 0; e < (D + 127) / 128; ++e) {
-                const int d = tid + e * 128;
-                if (d < D) {
-                    const __half_raw x = __nv_cvt_fp8_to_halfraw(v[d * 64 + t], __NV_E4M3);
-                    acc[e] += w * vs * __half2float(__half(x));
-                }
-            }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+        if (lane == 0)
+            sm[warp] = mx;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            mx = fmaxf(mx, sm[i]);
+        const float wt = ex2(m - mx);
+        if (tid < n)
+            w[tid] = wt;
+        l = warp_sum(tid < n ? l * wt : 0.0f);
+        if (lane == 0)
+            sl[warp] = l;
+        __syncthreads();
+        const int col = tid % kCols, k = tid / kCols;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+        for (int i = k; i < n; i += kLanes) {
+            const float4 o = __ldcg(reinterpret_cast<const float4 *>(part(i) + r * D + col * 4));
+            const float wi = w[i];
+            v.x += wi * o.x;
+            v.y += wi * o.y;
+            v.z += wi * o.z;
+            v.w += wi * o.w;
         }
-        m = mx;
+        acc[k][col] = v;
+        __syncthreads();
+        if (k == 0) {
+            l = 0.0f;
+            v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                l += sl[i];
+#pragma unroll
+            for (int i = 0; i < kLanes; ++i) {
+                const float4 o = acc[i][col];
+                v.x += o.x;
+                v.y += o.y;
+                v.z += o.z;
+                v.w += o.w;
+            }
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const int64_t row = (static_cast<int64_t>(rec.x) * p.M + r / p.G) * p.Hq + rec.y * p.G + r % p.G;
+            uint2 o;
+            o.x = f32_to_bf16(v.x * inv) | (static_cast<uint32_t>(f32_to_bf16(v.y * inv)) << 16);
+            o.y = f32_to_bf16(v.z * inv) | (static_cast<uint32_t>(f32_to_bf16(v.w * inv)) << 16);
+            *reinterpret_cast<uint2 *>(p.out + row * D + col * 4) = o;
+            if (col == 0 && p.lse)
+                p.lse[row] = l == 0.0f ? -INFINITY : (mx - kLift + log2f(l)) * kLn2;
+        }
+        __syncthreads();
     }
-    const int64_t row = (static_cast<int64_t>(b) * p.M + i) * p.Hq + hq;
-    for (int e = 0; e < (D + 127) / 128; ++e) {
-        const int d = tid + e * 128;
-        if (d < D)
-            p.out[row * D + d] = f32_to_bf16(l == 0.0f ? 0.0f : acc[e] / l);
-    }
-    if (tid == 0 && p.lse)
-        p.lse[row] = l == 0.0f ? -INFINITY : m + logf(l);
 }
 
 }  // namespace kv

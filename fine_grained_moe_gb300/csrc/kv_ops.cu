@@ -62,6 +62,77 @@ void launch_append(const kv::AppendArgs &a, dim3 grid, cudaStream_t st)
     kv::k_kv_append<D><<<grid, kv::Append<D>::kThreads, 0, st>>>(a);
 }
 
+// Rows of the products: the instantiations. Padding costs softmax work only (the
+// 128-lane products take the same time up to 64 columns, 1.3 times that at 128).
+int attn_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 48 ? 48 : 64; }
+
+// The attention's regions behind the common workspace.
+struct AttnWs {
+    size_t part, rec, total;
+};
+
+AttnWs attn_ws(int rows, int D)
+{
+    AttnWs o;
+    o.part = align_up(ws_offsets().total, 256);
+    o.rec = align_up(o.part + sizeof(float) * 2 * kv::kMaxGrid * kv::partial_floats(attn_rows(rows), D), 256);
+    o.total = align_up(o.rec + sizeof(int4) * kv::kMaxGrid, 256);
+    return o;
+}
+
+template <int D, int R>
+int launch_attn_t(kv::AttnArgs &a, int sms, cudaStream_t st)
+{
+    const int grid = sms < kv::kMaxGrid ? sms : kv::kMaxGrid;
+    // what is left of the shared memory goes to the rings, V's first: its stage is freed last
+    constexpr size_t side = static_cast<size_t>(kv::kTile) * D;
+    const size_t fixed = kv::query_bytes(R, D) + 2 * kv::prob_bytes(R) + (D == 64 ? kv::kBlock * D : 0) +
+                         align_up(sizeof(int) * (2 * static_cast<size_t>(a.B) + 1), 128) + 1024;
+    const size_t most = kv::kSmemMax - sizeof(kv::AttnShared) - 256;
+    const int stages = static_cast<int>((most - fixed) / side);
+    a.v_ring = (stages + 1) / 2 < kv::kMaxRing ? (stages + 1) / 2 : kv::kMaxRing;
+    a.k_ring = stages - a.v_ring < kv::kMaxRing ? stages - a.v_ring : kv::kMaxRing;
+    const size_t bytes = fixed + (a.k_ring + a.v_ring) * side;
+    CUtensorMap kmap, vmap;
+    const uint64_t n_rows = static_cast<uint64_t>(a.c.n_blocks) * a.c.heads * D;
+    FGM_HOST_TRY(host_rows64_map(&kmap, a.c.k_q, n_rows, kv::kBlock));
+    FGM_HOST_TRY(host_rows64_map(&vmap, a.c.v_q, n_rows, D));
+    static bool ready[64];                     // per device; setting it twice does no harm
+    int dev = 0;
+    FGM_HOST_CUDA(cudaGetDevice(&dev));
+    if (!ready[dev & 63]) {
+        FGM_HOST_CUDA(cudaFuncSetAttribute(kv::k_attn<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           static_cast<int>(most)));
+        ready[dev & 63] = true;
+    }
+    kv::k_attn<D, R><<<grid, kv::kAttnThreads, bytes, st>>>(kmap, vmap, a);
+    FGM_HOST_CUDA(cudaGetLastError());
+    // the join's launch overlaps the attention; it waits for its end itself
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * grid);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    FGM_HOST_CUDA(cudaLaunchKernelEx(&cfg, kv::k_attn_join<D>, a, grid));
+    return FGM_OK;
+}
+
+template <int D>
+int launch_attn(kv::AttnArgs &a, int sms, cudaStream_t st)
+{
+    switch (a.rows) {
+    case 8: return launch_attn_t<D, 8>(a, sms, st);
+    case 16: return launch_attn_t<D, 16>(a, sms, st);
+    case 32: return launch_attn_t<D, 32>(a, sms, st);
+    case 48: return launch_attn_t<D, 48>(a, sms, st);
+    default: return launch_attn_t<D, 64>(a, sms, st);
+    }
+}
+
 }  // namespace
 }  // namespace fgm
 
@@ -98,7 +169,7 @@ size_t fgm_attn_workspace_bytes(int B, int M, int n_q_heads, int n_kv_heads, int
     if (B < 1 || B > 1024 || M < 1 || M > kMaxM || n_kv_heads < 1 || n_kv_heads > 1024 || n_q_heads < 1 ||
         n_q_heads % n_kv_heads || !head_dim_ok(head_dim) || M * (n_q_heads / n_kv_heads) > FGM_ATTN_MAX_ROWS)
         return 0;
-    return ws_offsets().total;
+    return attn_ws(M * (n_q_heads / n_kv_heads), head_dim).total;
 }
 
 int fgm_attn_fwd(const fgm_kv_cache *cache, const uint16_t *q, int64_t token_stride, int B, int M, int n_q_heads,
@@ -122,19 +193,42 @@ int fgm_attn_fwd(const fgm_kv_cache *cache, const uint16_t *q, int64_t token_str
     if (!out || !is_aligned(out, 16) || !is_aligned(lse, 4))
         return failf(FGM_ERR_INVALID_ARG, "out NULL or not 16-byte aligned, or lse not 4-byte aligned");
     FGM_HOST_TRY(host_check_ws(ws, ws_bytes, fgm_attn_workspace_bytes(B, M, n_q_heads, cache->n_kv_heads, cache->head_dim)));
-    FGM_HOST_TRY(host_device_ready(nullptr));
-    const int G = n_q_heads / cache->n_kv_heads;
-    kv::AttnArgs a{device_cache(cache), q, token_stride, B, M, G, n_q_heads, lens, block_table, max_blocks, scale,
-                   window < (1 << 30) ? window : 1 << 30, out, lse, status_word(ws)};
+    if (static_cast<int64_t>(B) * max_blocks * cache->n_kv_heads > 0x7FFFFFFFLL)
+        return failf(FGM_ERR_INVALID_ARG, "B * max_blocks * n_kv_heads = %lld above 2^31 - 1",
+                     (long long)B * max_blocks * cache->n_kv_heads);
+    if (cache->n_blocks * cache->n_kv_heads > 0x7FFFFFFFLL / cache->head_dim)
+        return failf(FGM_ERR_INVALID_ARG, "cache of %lld blocks: n_blocks * n_kv_heads * head_dim above 2^31 - 1",
+                     (long long)cache->n_blocks);
+    int sms = 0;
+    FGM_HOST_TRY(host_device_ready(&sms));
+    kv::AttnArgs a = {};
+    a.c = device_cache(cache);
+    a.q = q;
+    a.stride = token_stride;
+    a.B = B;
+    a.M = M;
+    a.G = n_q_heads / cache->n_kv_heads;
+    a.Hq = n_q_heads;
+    a.lens = lens;
+    a.table = block_table;
+    a.max_blocks = max_blocks;
+    a.scale = scale;
+    a.window = window < (1 << 30) ? window : 1 << 30;
+    a.out = out;
+    a.lse = lse;
+    a.status = status_word(ws);
+    const AttnWs o = attn_ws(M * a.G, cache->head_dim);
+    a.part = reinterpret_cast<float *>(static_cast<char *>(ws) + o.part);
+    a.rec = reinterpret_cast<int4 *>(static_cast<char *>(ws) + o.rec);
+    a.rows = attn_rows(M * a.G);
+    a.min_units = 1;
+    a.timeout_ns = host_wait_limit_ns();
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const dim3 grid(M * G, cache->n_kv_heads, B);
     switch (cache->head_dim) {
-    case 64: kv::k_attn_simple<64><<<grid, 128, 0, st>>>(a); break;
-    case 128: kv::k_attn_simple<128><<<grid, 128, 0, st>>>(a); break;
-    default: kv::k_attn_simple<256><<<grid, 128, 0, st>>>(a); break;
+    case 64: return launch_attn<64>(a, sms, st);
+    case 128: return launch_attn<128>(a, sms, st);
+    default: return launch_attn<256>(a, sms, st);
     }
-    FGM_HOST_CUDA(cudaGetLastError());
-    return FGM_OK;
 }
 
 }  // extern "C"

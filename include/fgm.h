@@ -393,7 +393,7 @@ size_t fgm_attn_workspace_bytes(int B, int M, int n_q_heads, int n_kv_heads, int
  *   s_t = scale * k_s * <q, e4m3(k_q[t])>,  P = softmax(s),  out = sum_t P_t v_s e4m3(v_q[t]),
  *   lse = ln sum_t exp(s_t).
  * A row that sees nothing (p < 0, lens[b] = 0) has out = 0 and lse = -inf.
- * Scores and sums are fp32; queries enter the products exactly up to 2^-18 of
+ * Scores and sums are fp32; queries enter the products exactly up to 2^-21 of
  * their row's largest element, probabilities to 2^-8 of themselves. A row
  * with a non-finite query element is NaN. The same call gives the same bits.
  *  q            bf16 [B][M][n_q_heads][D], 16-byte aligned; tokens token_stride elements apart

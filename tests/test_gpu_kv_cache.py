@@ -5,19 +5,20 @@ Tolerances.
   * append: the scale is a power of two and a code one rounding of x / s, which
     is exact in fp32; codes and scales are compared bit for bit.
   * attention, per element, with A = sum P|v|, V = max |v| of the row's tokens:
-      - scores: a query element is held to 2^-18 of its row's largest (two E4M3
-        terms of 448 q / qmax, the second's half step 2^-10), products add up in
-        fp32 (D <= 256 terms, each add within 2^-23 of the running
-        sum, bounded by D * 2^-23 * sum|q k|), so
-        ds = 2^-18 qmax sum|k| + D 2^-23 sum|q k|, both times the scale;
-      - probabilities enter the product as two E4M3 terms of 256 P relative to
-        their block's maximum: 2^-4 of 2^-4 = 2^-8 of themselves, and 2^-18 of
-        the block's largest where the second term is subnormal; 64 tokens of a
-        block and the blocks' maxima summing to at most 1 make 64 * 2^-18 V;
+      - scores: a query element is held to 2^-21 of its row's largest (two E4M3
+        terms, the second times 16, of q scaled to a largest element above 224:
+        half a subnormal step is 2^-10, 2^-10 / 16 / 224 < 2^-21); D products
+        add up in fp32, each add within 2^-23 of a sum below sum|q k|:
+        ds = 2^-21 qmax sum|k| + D 2^-23 sum|q k|, both times the scale;
+      - probabilities enter the product as two E4M3 terms: 2^-4 of 2^-4 = 2^-8
+        of themselves, and where the second term is subnormal 2^-10 / 16 / 64 =
+        2^-20 of the largest that their CTA saw; a CTA holds at most 512 tokens
+        of a row in these cases and the CTAs' largest sum to at most 1:
+        512 * 2^-20 V;
       - exponentials and the sums of up to T terms: exp2 within 2^-21, sums in
         fp32, 2^-14 covers both at T <= 2^9 terms a partial;
       - the output is rounded to bf16: 2^-8 of itself.
-    |err| <= (2^-8 + 2^-14 + 2 ds) A + 2^-12 V + 2^-8 |out|.
+    |err| <= (2^-8 + 2^-14 + 2 ds) A + 2^-11 V + 2^-8 |out|.
   * lse: |err| <= ds + 2^-14 (1 + |lse| 2^-4).
 """
 
@@ -188,16 +189,16 @@ def check_attn(out, lse, q, kq, vq, ks, vs, lens, tab, scale, window):
     kv = oracle.e4m3_decode(kq) * ks.astype(np.float64)[:, :, None, None]
     vv = oracle.e4m3_decode(vq) * vs.astype(np.float64)[:, :, None, None]
     o, l, A, V, sqk, sk = plain64.attn(q.cpu().double().numpy(), kv, vv, lens, tab, scale, window)
-    ds = 2.0 ** -18 * sk + D * 2.0 ** -23 * sqk
+    ds = 2.0 ** -21 * sk + D * 2.0 ** -23 * sqk
     go, gl = out.cpu().double().numpy(), lse.cpu().double().numpy()
-    tol = (2.0 ** -8 + 2.0 ** -14 + 2 * ds[..., None]) * A + 2.0 ** -12 * V + 2.0 ** -8 * np.abs(o)
+    tol = (2.0 ** -8 + 2.0 ** -14 + 2 * ds[..., None]) * A + 2.0 ** -11 * V + 2.0 ** -8 * np.abs(o)
     assert np.isfinite(go).all()
     bad = np.abs(go - o) > tol
     assert not bad.any(), (np.argwhere(bad)[:4], go[bad][:4], o[bad][:4], tol[bad][:4])
     empty = np.isneginf(l)
     np.testing.assert_array_equal(np.isneginf(gl), empty)
     assert (go[empty] == 0).all()
-    err = np.abs(gl - l, where=~empty, out=np.zeros_like(l))
+    err = np.abs(np.where(empty, 0, gl) - np.where(empty, 0, l))
     lt = ds + 2.0 ** -14 * (1 + np.abs(np.where(empty, 0, l)) / 16)
     assert (err <= lt).all(), (err.max(), lt.min())
 
