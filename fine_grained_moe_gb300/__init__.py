@@ -540,7 +540,23 @@ def layers_array(layers):
 
 
 # ---------------------------------------------------------------- 8-bit KV cache
-@dataclass
+# (A call at a few microseconds of GPU time is bound by its host side: these
+# wrappers check what they must with plain attribute reads, pass addresses as
+# integers and enter a stream context only when the call names another stream
+# or device than the current one.)
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+def _expect(name: str, t: torch.Tensor, shape: tuple, dtype, device) -> int:
+    """Address of a contiguous tensor of this shape and type on ``device``."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
+        raise FgmError(f"{name}: expected {dtype} {tuple(shape)} on {device}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+    if not t.is_contiguous():
+        raise FgmError(f"{name}: expected a contiguous tensor, strides {t.stride()}")
+    return t.data_ptr()
+
+
+@dataclass(frozen=True, eq=False)
 class KVCache:
     """One layer's 8-bit cache (see ``fgm_kv_cache`` in include/fgm.h): E4M3
     codes k_q [blocks, kv heads, D / 64, 64, 64] and v_q [blocks, kv heads, D,
@@ -571,61 +587,65 @@ class KVCache:
         return int(self.v_q.shape[1])
 
     def struct(self) -> fgm_kv_cache:
-        if self.v_q.dim() != 4:
-            raise FgmError(f"v_q: expected [blocks, kv heads, D, {KV_BLOCK}], got {tuple(self.v_q.shape)}")
-        n, h, d = (int(x) for x in self.v_q.shape[:3])
-        shapes = {"k_q": ((n, h, d // 64, KV_BLOCK, 64), torch.uint8), "v_q": ((n, h, d, KV_BLOCK), torch.uint8),
-                  "k_s": ((n, h), torch.float32), "v_s": ((n, h), torch.float32)}
-        for name, (shape, dt) in shapes.items():
-            t = getattr(self, name)
-            if tuple(t.shape) != shape or t.dtype != dt or t.device != self.v_q.device:
-                raise FgmError(f"{name}: expected {shape} {dt} on {self.v_q.device}, got {tuple(t.shape)} {t.dtype} "
-                               f"on {t.device}")
-        return fgm_kv_cache(_ptr(self.k_q).value, _ptr(self.k_s).value, _ptr(self.v_q).value, _ptr(self.v_s).value,
-                            n, h, d)
+        """The C struct of the four tensors, checked on its first use."""
+        c = self.__dict__.get("_struct")
+        if c is None:
+            if self.v_q.dim() != 4 or self.v_q.shape[3] != KV_BLOCK:
+                raise FgmError(f"v_q: expected [blocks, kv heads, D, {KV_BLOCK}], got {tuple(self.v_q.shape)}")
+            if not self.v_q.is_cuda:
+                raise FgmError("expected a CUDA tensor")
+            n, h, d = (int(x) for x in self.v_q.shape[:3])
+            dev = self.v_q.device
+            c = fgm_kv_cache(_expect("k_q", self.k_q, (n, h, d // 64, KV_BLOCK, 64), _U8, dev),
+                             _expect("k_s", self.k_s, (n, h), _F32, dev),
+                             _expect("v_q", self.v_q, (n, h, d, KV_BLOCK), _U8, dev),
+                             _expect("v_s", self.v_s, (n, h), _F32, dev), n, h, d)
+            self.__dict__["_struct"] = c
+        return c
 
 
-def _on(device: torch.device, stream):
-    """Context that makes ``device`` and the call's stream current, so that
+def _call(device: torch.device, stream, body):
+    """Runs body(stream address) with ``device`` and the stream current, so that
     workspaces and outputs made inside belong to that stream."""
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    if s.device != device:
-        raise FgmError(f"the stream is on {s.device}, the tensors on {device}")
-    return torch.cuda.stream(s)
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+        if torch.cuda.current_device() == device.index:
+            return body(stream.cuda_stream)
+    elif stream.device != device:
+        raise FgmError(f"the stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.stream(stream):
+        return body(stream.cuda_stream)
 
 
 def _token_rows(name: str, t: torch.Tensor, heads: int, D: int, device) -> int:
     """bf16 [B, N, heads, D] whose tokens are dense and evenly spaced over the
     whole batch (a slice of a fused projection's output qualifies); returns the
     elements between tokens."""
-    if t.dim() != 4 or tuple(t.shape[2:]) != (heads, D) or t.dtype != torch.bfloat16 or t.device != device:
+    if t.dtype is not _BF16 or t.dim() != 4 or t.shape[2] != heads or t.shape[3] != D or t.device != device:
         raise FgmError(f"{name}: expected bf16 [B, N, {heads}, {D}] on {device}, got {tuple(t.shape)} {t.dtype} "
                        f"on {t.device}")
-    if not t.is_cuda:
-        raise FgmError("expected a CUDA tensor")
-    B, N = int(t.shape[0]), int(t.shape[1])
+    if t.is_contiguous():
+        return heads * D
+    B, N = t.shape[0], t.shape[1]
     sb, sn, sh, sd = t.stride()
     if (sd != 1) or (heads > 1 and sh != D):
         raise FgmError(f"{name}: a token's heads must be contiguous, strides {t.stride()}")
-    step = sn if N > 1 else sb if B > 1 else heads * D
     if N > 1 and B > 1 and sb != N * sn:
         raise FgmError(f"{name}: sequences must follow each other at N token strides, strides {t.stride()}")
-    return int(step)
+    return sn if N > 1 else sb if B > 1 else heads * D
 
 
-def _seqs(B: int, lens: torch.Tensor, block_table: torch.Tensor | None, cache: KVCache, device) -> tuple[int, object]:
-    if tuple(lens.shape) != (B,) or lens.dtype != torch.int32 or lens.device != device:
-        raise FgmError(f"lens: expected int32 [{B}] on {device}, got {tuple(lens.shape)} {lens.dtype} on {lens.device}")
+def _table(B: int, block_table: torch.Tensor | None, C: fgm_kv_cache, device) -> tuple[int, int | None]:
+    """(max_blocks, address) of a block table; without one each sequence owns an
+    equal run of the cache's blocks."""
     if block_table is None:
-        if int(cache.v_q.shape[0]) < B:
-            raise FgmError(f"without a block_table the cache's {int(cache.v_q.shape[0])} blocks are dealt to {B} "
-                           "sequences: too few")
-        return int(cache.v_q.shape[0]) // B, None
-    if block_table.dim() != 2 or block_table.shape[0] != B or block_table.dtype != torch.int32 or \
-            block_table.device != device:
-        raise FgmError(f"block_table: expected int32 [{B}, max_blocks] on {device}, got {tuple(block_table.shape)} "
-                       f"{block_table.dtype} on {block_table.device}")
-    return int(block_table.shape[1]), _ptr(block_table)
+        if C.n_blocks < B:
+            raise FgmError(f"without a block_table the cache's {C.n_blocks} blocks are dealt to {B} sequences: too few")
+        return C.n_blocks // B if B else 1, None
+    if block_table.dim() != 2:
+        raise FgmError(f"block_table: expected int32 [{B}, max_blocks], got {tuple(block_table.shape)}")
+    mb = block_table.shape[1]
+    return mb, _expect("block_table", block_table, (B, mb), _I32, device)
 
 
 def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, lens: torch.Tensor,
@@ -634,18 +654,19 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, lens: torch.Tens
     last N tokens into the cache. lens int32 [B]: tokens per sequence, the new
     ones included; block_table int32 [B, max_blocks] or None (each sequence owns
     an equal run of blocks)."""
-    C = cache.struct()
-    dev = cache.v_q.device
-    step = _token_rows("k", k, cache.n_kv_heads, cache.head_dim, dev)
-    if _token_rows("v", v, cache.n_kv_heads, cache.head_dim, dev) != step or v.shape != k.shape:
+    C, dev = cache.struct(), cache.v_q.device
+    step = _token_rows("k", k, C.n_kv_heads, C.head_dim, dev)
+    if _token_rows("v", v, C.n_kv_heads, C.head_dim, dev) != step or v.shape != k.shape:
         raise FgmError(f"k and v must have one shape and token stride, got {tuple(k.shape)} {k.stride()} and "
                        f"{tuple(v.shape)} {v.stride()}")
-    B, N = int(k.shape[0]), int(k.shape[1])
-    mb, table = _seqs(B, lens, block_table, cache, dev)
-    with _on(dev, stream):
-        ws = _ws(ws, dev)
-        _check(lib().fgm_kv_append(ctypes.byref(C), ctypes.c_void_p(k.data_ptr()), ctypes.c_void_p(v.data_ptr()), step,
-                                   B, N, _ptr(lens), table, mb, ws.ptr, ws.nbytes, _stream(None)))
+    B, N = k.shape[0], k.shape[1]
+    mb, table = _table(B, block_table, C, dev)
+    at = _expect("lens", lens, (B,), _I32, dev)
+
+    def body(s):
+        w = Workspace(dev) if ws is None else ws
+        _check(lib().fgm_kv_append(C, k.data_ptr(), v.data_ptr(), step, B, N, at, table, mb, w.t.data_ptr(), w.nbytes, s))
+    _call(dev, stream, body)
 
 
 def attn_workspace_bytes(B: int, M: int, n_q_heads: int, n_kv_heads: int, head_dim: int) -> int:
@@ -660,21 +681,19 @@ def attn_fwd(cache: KVCache, q: torch.Tensor, lens: torch.Tensor, scale: float,
     (already appended), over the cache; causal among them, with window > 0 over
     that many positions. Returns bf16 [B, M, q heads, D]; lse fp32 [B, M, q
     heads] receives the log of each row's sum of exponentials."""
-    C = cache.struct()
-    dev = cache.v_q.device
+    C, dev = cache.struct(), cache.v_q.device
     if q.dim() != 4:
         raise FgmError(f"q: expected bf16 [B, M, q heads, D], got {tuple(q.shape)}")
-    B, M, Hq = (int(x) for x in q.shape[:3])
-    step = _token_rows("q", q, Hq, cache.head_dim, dev)
-    mb, table = _seqs(B, lens, block_table, cache, dev)
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty((B, M, Hq, cache.head_dim), dtype=torch.bfloat16, device=dev)
-        for name, t, shape, dt in (("out", out, tuple(q.shape), torch.bfloat16), ("lse", lse, (B, M, Hq), torch.float32)):
-            if t is not None and (tuple(t.shape) != shape or t.dtype != dt or t.device != dev):
-                raise FgmError(f"{name}: expected {dt} {shape} on {dev}, got {tuple(t.shape)} {t.dtype} on {t.device}")
-        if ws is None:
-            ws = Workspace(dev, nbytes=attn_workspace_bytes(B, M, Hq, cache.n_kv_heads, cache.head_dim))
-        _check(lib().fgm_attn_fwd(ctypes.byref(C), ctypes.c_void_p(q.data_ptr()), step, B, M, Hq, _ptr(lens), table, mb,
-                                  float(scale), int(window), _ptr(out), _ptr(lse), ws.ptr, ws.nbytes, _stream(None)))
-    return out
+    B, M, Hq, D = q.shape
+    step = _token_rows("q", q, Hq, C.head_dim, dev)
+    mb, table = _table(B, block_table, C, dev)
+    at = _expect("lens", lens, (B,), _I32, dev)
+    lse_at = None if lse is None else _expect("lse", lse, (B, M, Hq), _F32, dev)
+
+    def body(s):
+        o = torch.empty((B, M, Hq, D), dtype=_BF16, device=dev) if out is None else out
+        w = Workspace(dev, nbytes=attn_workspace_bytes(B, M, Hq, C.n_kv_heads, D)) if ws is None else ws
+        _check(lib().fgm_attn_fwd(C, q.data_ptr(), step, B, M, Hq, at, table, mb, scale, window,
+                                  _expect("out", o, (B, M, Hq, D), _BF16, dev), lse_at, w.t.data_ptr(), w.nbytes, s))
+        return o
+    return _call(dev, stream, body)

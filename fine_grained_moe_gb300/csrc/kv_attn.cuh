@@ -15,7 +15,7 @@
 //    launch does not depend on them and can be captured.
 //  * A producer warp streams a unit's K and V with TMA tensor copies (rows of
 //    64 bytes in the 64-byte swizzle) into two rings that fill the shared memory.
-//  * An issuing lane runs tcgen05.mma kind::f8f6f4 with the cache as the first
+//  * Two issuing warps run tcgen05.mma kind::f8f6f4 with the cache as the first
 //    operand: S^T = K Q^T (128 tokens x rows, K = D) and O^T += V^T P^T (D x rows,
 //    K = tokens; V lies token-contiguous in the cache for this). The rows are
 //    the narrow side, so 128 lanes are full whatever R is, both accumulators
@@ -23,23 +23,23 @@
 //    sm_103 an E4M3 mma.sync is carried out as conversions and f16 products,
 //    about 15 instructions each: a kernel built on it, with the codes read from
 //    the same rings, ran the 32K verify step in 75 us, issue-bound.)
-//  * Eight softmax warps read S^T (a thread is a token and half of the rows),
+//  * Sixteen softmax warps read S^T (a thread is a token and a fourth of the rows),
 //    exponentiate and write P^T back to shared memory as the next operand. S
 //    and P have two buffers: the products of the next unit run under the
 //    softmax of this one.
 //
 // Precision. The second operands are split into two E4M3 terms in columns of
-// their own, hi and lo = 16 (x - hi), added in fp32 as hi + lo / 16. Queries:
-// scaled by a power of two to a largest element in (224, 448]; a bf16 has 8
-// significant bits and a term carries 4, so the split is exact down to half a
-// subnormal step of lo, 2^-14 / 224 of the row's largest. Probabilities: 64
-// exp2(s + log2 v_s - m), at most 256, within 2^-8 of themselves or
-// 2^-14 / 64 = 2^-20 of exp2(m). V's block scale rides in the exponent, so that
+// their own, hi and lo = c (x - hi), added in fp32 as hi + lo / c. Queries
+// (c = 16): scaled by a power of two to a largest element in (224, 448]; a bf16
+// has 8 significant bits and a term carries 4, so the split is exact down to
+// half a subnormal step of lo, 2^-14 / 224 of the row's largest. Probabilities
+// (c = 32): 32 exp2(s + log2 v_s - m), at most 256, within 2^-8 of themselves or
+// 2^-15 / 32 = 2^-20 of exp2(m). V's block scale rides in the exponent, so that
 // blocks of any scale add into one accumulator. The row sums use the unrounded
 // exponentials, in fp32.
 //
-// The reference m is not the running maximum but within 2 of it from below: a
-// unit whose scores stay under m + 2 (nearly all after the first few) needs no
+// The reference m is not the running maximum but within 3 of it from below: a
+// unit whose scores stay under m + 3 (most after the first few) needs no
 // maximum over its tokens, which are spread over the lanes, only a vote; one
 // that exceeds it computes the maxima and rescales the accumulator.
 //
@@ -56,15 +56,15 @@
 namespace fgm {
 namespace kv {
 
-constexpr int kSoftWarps = 8;
-constexpr int kAttnThreads = 32 * (2 + kSoftWarps);    // copies, products, softmax
+constexpr int kSoftWarps = 16;                         // four per lane quarter, a fourth of the rows each
+constexpr int kAttnThreads = 32 * (4 + kSoftWarps);    // copies, scores, outputs, (none), softmax
 constexpr int kTile = 2 * kBlock;                      // tokens of a unit
 constexpr int kMaxRing = 8;                            // stages of the K and of the V ring at most
 constexpr int kMetas = 16;                             // units' scales kept: ring depth + 2 and more
 constexpr int kMaxGrid = 160;                          // CTAs at most: the SMs of a full sm_103 part
 constexpr float kLowest = -1.0e30f;                    // stands for the maximum of nothing
-constexpr float kLift = 6.0f;                          // probabilities enter the product times 2^6
-constexpr float kSlack = 2.0f;                         // scores may exceed the reference by this much
+constexpr float kLift = 5.0f;                          // probabilities enter the product times 2^5
+constexpr float kSlack = 3.0f;                         // scores may exceed the reference by this much
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr size_t kSmemMax = 227 * 1024;
@@ -107,12 +107,14 @@ struct Meta {                // a unit: block scales, first token, which of its 
 struct AttnShared {
     unsigned long long kfull[kMaxRing], kempty[kMaxRing], vfull[kMaxRing], vempty[kMaxRing];
     unsigned long long mfull[kMetas];
-    unsigned long long sfull[2], sfree[2], pfull[2], pdone[2], qfull, drained;
+    unsigned long long sfull[2], sfree[2], pfull[2], pdone[2], qfull, drained[2];
     Meta meta[kMetas];
     float qf[FGM_ATTN_MAX_ROWS];                       // score of a unit product: 2^e scale log2(e)
     float mx[4][FGM_ATTN_MAX_ROWS];                    // per lane quarter: a unit's maxima
     float ls[4][FGM_ATTN_MAX_ROWS];                    // and the segment's sums
     float m[FGM_ATTN_MAX_ROWS], l[FGM_ATTN_MAX_ROWS];
+    int2 lim[FGM_ATTN_MAX_ROWS];                       // tokens [x, y) that a row sees
+    int orow[FGM_ATTN_MAX_ROWS];                       // a row's place among the (token, q head) of its sequence
     uint32_t tmem;
     int abort;
 };
@@ -211,6 +213,14 @@ __device__ __forceinline__ uint32_t at64(int n, int k)
     return static_cast<uint32_t>(n * 64 + ((((k >> 4) ^ (n >> 1)) & 3) << 4) + (k & 15));
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
 {
     asm volatile(
@@ -228,23 +238,34 @@ __device__ __forceinline__ void commit(unsigned long long *bar)
 __device__ __forceinline__ void after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
-__device__ __forceinline__ void tmem_ld4(uint32_t a, float *v)
+// N (2 or 4) accumulator columns of a thread's lane.
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t a, float *v)
 {
     uint32_t r[4];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(a)
-                 : "memory");
+    if constexpr (N == 2)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a) : "memory");
+    else
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(a)
+                     : "memory");
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < N; ++i)
         v[i] = __uint_as_float(r[i]);
 }
 
-__device__ __forceinline__ void tmem_st4(uint32_t a, const float *v)
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t a, const float *v)
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(__float_as_uint(v[0])),
-                 "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3]))
-                 : "memory");
+    if constexpr (N == 2)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(a), "r"(__float_as_uint(v[0])),
+                     "r"(__float_as_uint(v[1]))
+                     : "memory");
+    else
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(__float_as_uint(v[0])),
+                     "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3]))
+                     : "memory");
 }
 
 // (the loaded registers pass through, so that no use of them moves ahead of the wait)
@@ -275,6 +296,11 @@ __device__ __forceinline__ float2 e4m3_values(uint32_t w)
     return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w), __NV_E4M3)));
 }
 
+__device__ __forceinline__ void sts8(uint32_t a, uint32_t v)
+{
+    asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
 // A place in the list of units.
 struct Cursor {
     int b, h, u, n, first, blocks;    // sequence, kv head, unit of the segment, its units, first block and blocks
@@ -288,7 +314,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     constexpr int kSlices = D / 64, kN = 2 * R;
     constexpr int kSide = kTile * D;                             // bytes of a unit's K or V
     constexpr int kMTiles = D == 256 ? 2 : 1;                    // 128-lane tiles of O^T
-    constexpr int kNR = R / 2;                                   // rows of a softmax thread
+    constexpr int kNR = R / 4;                                   // rows of a softmax thread
+    constexpr int kCh = kNR < 4 ? kNR : 4;                       // accumulator columns read at a time
     constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(kN >> 3) << 17) | (8u << 24);   // fp32 += E4M3 x E4M3, M = 128
     constexpr uint32_t kOCol = 2 * kN;                           // S buffers first, then O tiles
     constexpr uint32_t kUsed = 2 * kN + kMTiles * kN;
@@ -321,7 +348,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             bar_init(&sh.pdone[i], 1);
         }
         bar_init(&sh.qfull, kSoftWarps);
-        bar_init(&sh.drained, 1);
+        bar_init(&sh.drained[0], 1);
+        bar_init(&sh.drained[1], 1);
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -330,6 +358,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    if (warp == 2)
+        for (int r = lane; r < R; r += 32)
+            sh.orow[r] = r / p.G * p.Hq + r % p.G;
     if (warp == 0) {
         int base = 0;
         for (int b0 = 0; b0 < p.B; b0 += 32) {
@@ -484,77 +515,92 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ------------------------------------------------------------ products
-        if (lane == 0) {
-            bool ok = true;
-            auto scores = [&](int u) {             // S^T of unit u
+        // ------------------------------------------------------------ scores
+        // (The whole warp waits and one lane issues. Scores and outputs have an
+        // issuing warp each: one thread gets a product of this size out every 50
+        // to 120 cycles, two threads two.)
+        const bool lead = elect_one();
+        bool ok = true;
+        int seg = 0;
+        const uint64_t b0 = desc64(saddr(qs));
+        for (int done = 0; done < n_units && ok; ++seg) {
+            const Cursor cu = locate(u0 + done);
+            const int n = min(cu.n - cu.u, n_units - done);
+            ok = wait(&sh.qfull, seg, 17, seg);
+            for (int u = done; u < done + n && ok; ++u) {
                 const int slot = u % p.k_ring;
-                if (ok && u >= 2)
+                if (u >= 2)
                     ok = wait(&sh.sfree[u & 1], (u >> 1) - 1, 15, u);
-                if (ok)
-                    ok = wait(&sh.kfull[slot], u / p.k_ring, 16, u);
-                if (!ok)
-                    return;
-                after_sync();
-                const uint32_t a = saddr(kring + slot * kSide), b = saddr(qs), d = tmem + (u & 1) * kN;
-#pragma unroll
-                for (int k = 0; k < D / 32; ++k)
-                    mma_f8(d, desc64(a + (k >> 1) * (kTile * 64) + (k & 1) * 32), desc64(b + (k >> 1) * (kN * 64) + (k & 1) * 32),
-                           kIdesc, k != 0);
-                commit(&sh.kempty[slot]);
-                commit(&sh.sfull[u & 1]);
-            };
-            int seg = 0;
-            for (int done = 0; done < n_units && ok; ++seg) {
-                const Cursor cu = locate(u0 + done);
-                const int n = min(cu.n - cu.u, n_units - done);
-                ok = wait(&sh.qfull, seg, 17, seg);
-                after_sync();
-                scores(done);
-                bool add = false;
-                for (int i = 0; i < n && ok; ++i) {
-                    const int u = done + i, slot = u % p.v_ring;
-                    if (i + 1 < n)
-                        scores(u + 1);
-                    if (ok)
-                        ok = wait(&sh.vfull[slot], u / p.v_ring, 18, u);
-                    if (ok)
-                        ok = wait(&sh.pfull[u & 1], u >> 1, 19, u);
-                    if (!ok)
-                        break;
+                ok = ok && wait(&sh.kfull[slot], u / p.k_ring, 16, u);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (ok && lead) {
                     after_sync();
-                    const int have = sh.meta[u % kMetas].have;
-                    const uint32_t a = saddr(vring + slot * kSide), b = saddr(ps + (u & 1) * prob_bytes(R));
-                    for (int k = 0; k < 2; ++k) {
-                        if (!(have >> k & 1))
-                            continue;
+                    const uint64_t a0 = desc64(saddr(kring + slot * kSide));
+                    const uint32_t d = tmem + (u & 1) * kN;
 #pragma unroll
-                        for (int kk = 0; kk < 2; ++kk) {
-#pragma unroll
-                            for (int t = 0; t < kMTiles; ++t)
-                                mma_f8(tmem + kOCol + t * kN, desc64(a + k * (kBlock * D) + t * (128 * 64) + kk * 32),
-                                       desc64(b + k * (kN * 64) + kk * 32), kIdesc, add);
-                            add = true;
-                        }
-                    }
-                    commit(&sh.vempty[slot]);
-                    commit(&sh.pdone[u & 1]);
+                    for (int k = 0; k < D / 32; ++k)
+                        mma_f8(d, a0 + (((k >> 1) * (kTile * 64) + (k & 1) * 32) >> 4),
+                               b0 + (((k >> 1) * (kN * 64) + (k & 1) * 32) >> 4), kIdesc, k != 0);
+                    commit(&sh.kempty[slot]);
+                    commit(&sh.sfull[u & 1]);
                 }
-                done += n;
+                __syncwarp();
             }
-            // every issued product completes before the tensor memory is released
-            commit(&sh.drained);
-            for (int it = 0; it < (1 << 22) && !bar_try(saddr(&sh.drained), 0); ++it)
+            done += n;
+        }
+        // every issued product completes before the tensor memory is released
+        if (lead) {
+            commit(&sh.drained[0]);
+            for (int it = 0; it < (1 << 22) && !bar_try(saddr(&sh.drained[0]), 0); ++it)
                 ;
         }
         __syncwarp();
-    } else {
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ outputs
+        const bool lead = elect_one();
+        bool ok = true;
+        for (int done = 0; done < n_units && ok;) {
+            const Cursor cu = locate(u0 + done);
+            const int n = min(cu.n - cu.u, n_units - done);
+            bool add = false;
+            for (int u = done; u < done + n && ok; ++u) {
+                const int slot = u % p.v_ring;
+                ok = wait(&sh.vfull[slot], u / p.v_ring, 18, u) && wait(&sh.pfull[u & 1], u >> 1, 19, u);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                const int have = sh.meta[u % kMetas].have;
+                if (ok && lead) {
+                    after_sync();
+                    const uint64_t a0 = desc64(saddr(vring + slot * kSide)), b0 = desc64(saddr(ps + (u & 1) * prob_bytes(R)));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (have >> (k >> 1) & 1) {
+#pragma unroll
+                            for (int t = 0; t < kMTiles; ++t)
+                                mma_f8(tmem + kOCol + t * kN, a0 + (((k >> 1) * (kBlock * D) + t * (128 * 64) + (k & 1) * 32) >> 4),
+                                       b0 + (((k >> 1) * (kN * 64) + (k & 1) * 32) >> 4), kIdesc, add);
+                            add = true;
+                        }
+                    commit(&sh.vempty[slot]);
+                    commit(&sh.pdone[u & 1]);
+                }
+                __syncwarp();
+            }
+            done += n;
+        }
+        if (lead) {
+            commit(&sh.drained[1]);
+            for (int it = 0; it < (1 << 22) && !bar_try(saddr(&sh.drained[1]), 0); ++it)
+                ;
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
         // ------------------------------------------------------------ softmax
-        const int w = warp - 2, quarter = warp & 3, half = w >> 2, stid = tid - 64;
+        const int w = warp - 4, quarter = warp & 3, part4 = w >> 2, stid = tid - 128;
         const int tl = quarter * 32 + lane;        // token of a unit, lane of an accumulator
         const int blk = quarter >> 1;
         const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
         const int rows = p.M * p.G;
+        const int n0 = part4 * kNR;                // the thread's rows: n0 .. n0 + kNR - 1
         bool alive = true;
         int4 rec = make_int4(-1, 0, 0, 0);
 
@@ -577,8 +623,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             // query terms of this (sequence, head): a warp takes every 8th row
             for (int r = w; r < R; r += kSoftWarps) {
                 const bool live = r < rows;
-                const uint16_t *src = p.q + (static_cast<int64_t>(cu.b) * p.M + r / p.G) * p.stride +
-                                      (cu.h * p.G + r % p.G) * D;
+                const int ri = r / p.G;
+                const uint16_t *src = p.q + (static_cast<int64_t>(cu.b) * p.M + ri) * p.stride + (cu.h * p.G + r - ri * p.G) * D;
                 constexpr int kE = (D + 127) / 128;
                 uint2 x[kE];
                 unsigned amax = 0;
@@ -599,8 +645,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const unsigned u = amax << 16;
                 const int ex = max(static_cast<int>(u >> 23) + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0) - 8, 7);
                 const float up = __uint_as_float(static_cast<unsigned>(254 - ex) << 23);
-                if (lane == 0)
+                if (lane == 0) {
+                    int2 lim = make_int2(0, 0);
+                    if (live)
+                        row_range(len, p.M, p.window, ri, lim.x, lim.y);
+                    sh.lim[r] = lim;
                     sh.qf[r] = __uint_as_float(static_cast<unsigned>(ex) << 23) * (p.scale * kLog2e);
+                }
 #pragma unroll
                 for (int e = 0; e < kE; ++e) {
                     const int d = (e * 32 + lane) * 4;
@@ -621,7 +672,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             before_sync();                         // the last segment's accumulator has been read, too
-            asm volatile("bar.sync 1, 256;" ::: "memory");
+            asm volatile("bar.sync 1, 512;" ::: "memory");
             if (lane == 0)
                 bar_arrive(saddr(&sh.qfull));
 
@@ -638,17 +689,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
             for (int i = 0; i < n; ++i) {
                 const int u = done + i;
-                float s[2 * kNR];                  // hi, then lo
                 if (alive)
                     alive = wait(&sh.mfull[u % kMetas], u / kMetas, 20, u) && wait(&sh.sfull[u & 1], u >> 1, 21, u);
                 alive = __all_sync(0xFFFFFFFFu, alive);
                 after_sync();
                 const Meta me = sh.meta[u % kMetas];
+                float s[2 * kNR];                  // hi, then lo
 #pragma unroll
-                for (int r = 0; r < kNR; r += 4) {
-                    tmem_ld4(tmem + lanes + (u & 1) * kN + half * kNR + r, s + r);
-                    tmem_ld4(tmem + lanes + (u & 1) * kN + R + half * kNR + r, s + kNR + r);
+                for (int r = 0; r < kNR; r += kCh) {
+                    tmem_ld<kCh>(tmem + lanes + (u & 1) * kN + n0 + r, s + r);
+                    tmem_ld<kCh>(tmem + lanes + (u & 1) * kN + R + n0 + r, s + kNR + r);
                 }
+                const float ks = blk ? me.ks[1] : me.ks[0], vs = blk ? me.vs[1] : me.vs[0];
+                const float lv = log2f(vs), ivs = 1.0f / vs;
+                const int tok = me.tok0 + tl;
+                const bool here = me.have >> blk & 1;
+                const bool edge = me.tok0 + kTile > hi_min || me.tok0 < lo_max || me.have != 3;
                 tmem_wait_ld(s);
                 before_sync();
                 __syncwarp();
@@ -656,29 +712,26 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     bar_arrive(saddr(&sh.sfree[u & 1]));
 
                 // scores in powers of two, with V's scale on top
-                const float ks = blk ? me.ks[1] : me.ks[0], vs = blk ? me.vs[1] : me.vs[0];
-                const float lv = log2f(vs), ivs = 1.0f / vs;
-                const int tok = me.tok0 + tl;
-                const bool here = me.have >> blk & 1;
-                const bool edge = me.tok0 + kTile > hi_min || me.tok0 < lo_max || me.have != 3;
                 bool over = false;
 #pragma unroll
-                for (int r = 0; r < kNR; ++r) {
-                    s[r] = fmaf(fmaf(s[kNR + r], 0.0625f, s[r]), sh.qf[half * kNR + r] * ks, lv);
-                    if (edge) {
-                        int lo = 0, hi = 0;
-                        if (half * kNR + r < rows)
-                            row_range(len, p.M, p.window, (half * kNR + r) / p.G, lo, hi);
-                        s[r] = here && tok >= lo && tok < hi ? s[r] : -INFINITY;
+                for (int r = 0; r < kNR; ++r)
+                    s[r] = fmaf(fmaf(s[kNR + r], 0.0625f, s[r]), sh.qf[n0 + r] * ks, lv);
+                if (edge) {
+#pragma unroll
+                    for (int r = 0; r < kNR; ++r) {
+                        const int2 lim = sh.lim[n0 + r];
+                        s[r] = here && tok >= lim.x && tok < lim.y ? s[r] : -INFINITY;
                     }
-                    over |= s[r] > m[r] + kSlack;
                 }
+#pragma unroll
+                for (int r = 0; r < kNR; ++r)
+                    over |= s[r] > m[r] + kSlack;
                 int any;
                 asm volatile(
                     "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 128, p;\n\t"
                     "selp.s32 %0, 1, 0, q;\n\t}"
                     : "=r"(any)
-                    : "r"(static_cast<int>(over)), "r"(2 + half)
+                    : "r"(static_cast<int>(over)), "r"(2 + part4)
                     : "memory");
                 if (any) {
                     // the unit's maxima over its 128 tokens; new references; the accumulator follows
@@ -689,16 +742,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         for (int o = 16; o > 0; o >>= 1)
                             x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
                         if (lane == 0)
-                            sh.mx[quarter][half * kNR + r] = x;
+                            sh.mx[quarter][n0 + r] = x;
                     }
-                    asm volatile("barrier.cta.sync %0, 128;" ::"r"(2 + half) : "memory");
+                    asm volatile("barrier.cta.sync %0, 128;" ::"r"(2 + part4) : "memory");
                     float c[kNR];
 #pragma unroll
                     for (int r = 0; r < kNR; ++r) {
                         float x = m[r];
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            x = fmaxf(x, sh.mx[k][half * kNR + r]);
+                            x = fmaxf(x, sh.mx[k][n0 + r]);
                         c[r] = ex2(m[r] - x);
                         l[r] *= c[r];
                         m[r] = x;
@@ -711,19 +764,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                         for (int t = 0; t < kMTiles; ++t)
 #pragma unroll
-                            for (int r = 0; r < kNR; r += 4) {
-                                const uint32_t a = tmem + lanes + kOCol + t * kN + half * kNR + r;
-                                float o[8];
-                                tmem_ld4(a, o);
-                                tmem_ld4(a + R, o + 4);
+                            for (int r = 0; r < kNR; r += kCh) {
+                                const uint32_t a = tmem + lanes + kOCol + t * kN + n0 + r;
+                                float o[2 * kCh];
+                                tmem_ld<kCh>(a, o);
+                                tmem_ld<kCh>(a + R, o + kCh);
                                 tmem_wait_ld(o);
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) {
+                                for (int k = 0; k < kCh; ++k) {
                                     o[k] *= c[r + k];
-                                    o[4 + k] *= c[r + k];
+                                    o[kCh + k] *= c[r + k];
                                 }
-                                tmem_st4(a, o);
-                                tmem_st4(a + R, o + 4);
+                                tmem_st<kCh>(a, o);
+                                tmem_st<kCh>(a + R, o + kCh);
                             }
                         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                     }
@@ -734,8 +787,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (alive && u >= 2)
                     alive = wait(&sh.pdone[u & 1], (u >> 1) - 1, 23, u);
                 alive = __all_sync(0xFFFFFFFFu, alive);
-                uint8_t *pt = ps + (u & 1) * prob_bytes(R) + blk * (kN * 64);
                 const int kt = tl & 63;
+                const uint32_t pt = saddr(ps + (u & 1) * prob_bytes(R) + blk * (kN * 64)) + (kt & 15);
 #pragma unroll
                 for (int r = 0; r < kNR; r += 2) {
                     const float p0 = ex2(s[r] - (m[r] - kLift)), p1 = ex2(s[r + 1] - (m[r + 1] - kLift));
@@ -743,12 +796,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     l[r + 1] = fmaf(p1, ivs, l[r + 1]);
                     const uint32_t hi = e4m3_pair(p0, p1);
                     const float2 z = e4m3_values(hi);
-                    const uint32_t lo = e4m3_pair(16.0f * (p0 - z.x), 16.0f * (p1 - z.y));
-                    const int nr = half * kNR + r;
-                    pt[at64(nr, kt)] = static_cast<uint8_t>(hi);
-                    pt[at64(nr + 1, kt)] = static_cast<uint8_t>(hi >> 8);
-                    pt[at64(R + nr, kt)] = static_cast<uint8_t>(lo);
-                    pt[at64(R + nr + 1, kt)] = static_cast<uint8_t>(lo >> 8);
+                    const uint32_t lo = e4m3_pair(32.0f * (p0 - z.x), 32.0f * (p1 - z.y));
+                    // rows n, n + 1 (n even) lie in one swizzle phase; the second term R rows on
+                    const int n = n0 + r;
+                    const uint32_t at = pt + n * 64 + ((((kt >> 4) ^ (n >> 1)) & 3) << 4);
+                    sts8(at, hi);
+                    sts8(at + 64, hi >> 8);
+                    sts8(at + R * 64, lo);
+                    sts8(at + R * 64 + 64, lo >> 8);
                 }
                 if (edge) {
                     // V codes of tokens that no row sees may be anything, NaN included: zeros
@@ -758,7 +813,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     alive = __all_sync(0xFFFFFFFFu, alive);
                     if (alive && here && (tok < lo_min || tok >= len)) {
                         uint8_t *vt = vring + slot * kSide + blk * (kBlock * D);
-                        for (int d = half * (D / 2); d < (half + 1) * (D / 2); ++d)
+                        for (int d = part4 * (D / 4); d < (part4 + 1) * (D / 4); ++d)
                             vt[at64(d, kt)] = 0;
                     }
                 }
@@ -774,14 +829,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             for (int r = 0; r < kNR; ++r) {
                 const float x = warp_sum(l[r]);
                 if (lane == 0)
-                    sh.ls[quarter][half * kNR + r] = x;
+                    sh.ls[quarter][n0 + r] = x;
                 if (quarter == 0 && lane == 0)
-                    sh.m[half * kNR + r] = m[r];
+                    sh.m[n0 + r] = m[r];
             }
-            asm volatile("bar.sync 1, 256;" ::: "memory");
+            asm volatile("bar.sync 1, 512;" ::: "memory");
             if (stid < R)
                 sh.l[stid] = (sh.ls[0][stid] + sh.ls[1][stid]) + (sh.ls[2][stid] + sh.ls[3][stid]);
-            asm volatile("bar.sync 1, 256;" ::: "memory");
+            asm volatile("bar.sync 1, 512;" ::: "memory");
             const int last_u = done + n - 1;
             if (alive)
                 alive = wait(&sh.pdone[last_u & 1], last_u >> 1, 25, last_u);
@@ -789,28 +844,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             after_sync();
             const bool starts = cu.u == 0, ends = cu.u + n == cu.n, whole = starts && ends;
             float *part = p.part + (blockIdx.x * 2 + (starts ? 1 : 0)) * partial_floats(R, D);
-            // a thread is a dim; D = 256: a half of the warps per lane tile, else per half of the rows
-            const int d = (D == 256 ? half * 128 : 0) + tl;
-            const int ra = D == 256 ? 0 : half * kNR, rz = D == 256 ? R : ra + kNR;
-            const uint32_t oa = tmem + lanes + kOCol + (D == 256 ? half * kN : 0);
+            // a thread is a dim and a share of the rows; D = 256: half of the warps per lane tile
+            const int mt = D == 256 ? part4 >> 1 : 0, d = mt * 128 + tl;
+            constexpr int kShare = D == 256 ? R / 2 : R / 4;
+            const int ra = (D == 256 ? part4 & 1 : part4) * kShare;
+            const uint32_t oa = tmem + lanes + kOCol + mt * kN;
+            const int64_t row0 = static_cast<int64_t>(cu.b) * p.M * p.Hq + cu.h * p.G;
             if (D != 64 || quarter < 2) {
-#pragma unroll 4
-                for (int r = ra; r < rz; r += 4) {
-                    float o[8];
-                    tmem_ld4(oa + r, o);
-                    tmem_ld4(oa + R + r, o + 4);
+#pragma unroll 2
+                for (int r = ra; r < ra + kShare; r += kCh) {
+                    float o[2 * kCh];
+                    tmem_ld<kCh>(oa + r, o);
+                    tmem_ld<kCh>(oa + R + r, o + kCh);
                     tmem_wait_ld(o);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < kCh; ++k) {
                         const float ls = sh.l[r + k];
-                        const float v = ls == 0.0f ? 0.0f : fmaf(o[4 + k], 0.0625f, o[k]);
-                        if (!whole) {
+                        const float v = ls == 0.0f ? 0.0f : fmaf(o[kCh + k], 1.0f / 32.0f, o[k]);
+                        if (!whole)
                             part[(r + k) * D + d] = v;
-                        } else if (r + k < rows) {
-                            const int64_t row = (static_cast<int64_t>(cu.b) * p.M + (r + k) / p.G) * p.Hq + cu.h * p.G +
-                                                (r + k) % p.G;
-                            p.out[row * D + d] = f32_to_bf16(ls == 0.0f ? 0.0f : v / ls);
-                        }
+                        else if (r + k < rows)
+                            p.out[(row0 + sh.orow[r + k]) * D + d] = f32_to_bf16(ls == 0.0f ? 0.0f : v / ls);
                     }
                 }
             }
@@ -820,8 +874,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     part[R * D + stid] = mm;
                     part[R * (D + 1) + stid] = ls;
                 } else if (p.lse && stid < rows) {
-                    const int64_t row = (static_cast<int64_t>(cu.b) * p.M + stid / p.G) * p.Hq + cu.h * p.G + stid % p.G;
-                    p.lse[row] = ls == 0.0f ? -INFINITY : (mm - kLift + log2f(ls)) * kLn2;
+                    p.lse[row0 + sh.orow[stid]] = ls == 0.0f ? -INFINITY : (mm - kLift + log2f(ls)) * kLn2;
                 }
             }
             if (starts && !ends) {
@@ -829,7 +882,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const int64_t last = u0 + done - cu.u + cu.n - 1;
                 rec = make_int4(cu.b, cu.h, static_cast<int>(((last + 1) * G + U - 1) / U - 1), 0);
             }
-            asm volatile("bar.sync 1, 256;" ::: "memory");     // sh.m, sh.l, sh.qf are free again
+            asm volatile("bar.sync 1, 512;" ::: "memory");     // sh.m, sh.l, sh.qf are free again
             done += n;
         }
         if (stid == 0)

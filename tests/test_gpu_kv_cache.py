@@ -11,7 +11,7 @@ Tolerances.
         add up in fp32, each add within 2^-23 of a sum below sum|q k|:
         ds = 2^-21 qmax sum|k| + D 2^-23 sum|q k|, both times the scale;
       - probabilities enter the product as two E4M3 terms: 2^-4 of 2^-4 = 2^-8
-        of themselves, and where the second term is subnormal 2^-10 / 16 / 64 =
+        of themselves, and where the second term is subnormal 2^-10 / 32 / 32 =
         2^-20 of the largest that their CTA saw; a CTA holds at most 512 tokens
         of a row in these cases and the CTAs' largest sum to at most 1:
         512 * 2^-20 V;
