@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
+from typing import NamedTuple
 
 import torch
 
@@ -32,6 +33,7 @@ STATUS_NONFINITE_LOGITS = 1
 STATUS_WAIT_TIMEOUT = 2
 STATUS_NONFINITE_KV = 4
 STATUS_BAD_BLOCK = 8
+MAX_TOP = 16       # alternatives per row of the log-probability calls
 KV_BLOCK = 64      # tokens of a KV-cache block
 ATTN_MAX_ROWS = 64  # query rows sharing a kv head: M * n_q_heads / n_kv_heads
 PATH_FUSED = 0    # one persistent cooperative kernel per call (TMA ring + mma.sync tiles; tcgen05 down products at M <= 5)
@@ -96,6 +98,8 @@ def lib() -> ctypes.CDLL:
             "fgm_kv_append": (ci, [CP, vp, vp, i64, ci, ci, vp, vp, ci, vp, sz, vp]),
             "fgm_attn_workspace_bytes": (sz, [ci, ci, ci, ci, ci]),
             "fgm_attn_fwd": (ci, [CP, vp, i64, ci, ci, ci, vp, vp, ci, ctypes.c_float, ci, vp, vp, vp, sz, vp]),
+            "fgm_logprobs_workspace_bytes": (sz, [i64, i64, ci]),
+            "fgm_logprobs": (ci, [vp, ci, i64, i64, i64, ctypes.c_float, vp, ci, vp, vp, vp, vp, vp, sz, vp]),
             "fgm_read_status": (ci, [vp, sz, ci, vp, vp]),
             "fgm_select_path": (ci, [ci]),
             "fgm_set_phase_trace": (ci, [vp, sz]),
@@ -696,4 +700,66 @@ def attn_fwd(cache: KVCache, q: torch.Tensor, lens: torch.Tensor, scale: float,
         _check(lib().fgm_attn_fwd(C, q.data_ptr(), step, B, M, Hq, at, table, mb, scale, window,
                                   _expect("out", o, (B, M, Hq, D), _BF16, dev), lse_at, w.t.data_ptr(), w.nbytes, s))
         return o
+    return _call(dev, stream, body)
+
+
+# ---------------------------------------------------------------- log probabilities
+class LogProbs(NamedTuple):
+    """Per row: ln p of the given token, entropy (both fp32 [N]), and the k most
+    likely words with their ln p (int32 and fp32 [N, k]); None where not asked for."""
+    logp: torch.Tensor | None
+    entropy: torch.Tensor | None
+    top_ids: torch.Tensor | None
+    top_logp: torch.Tensor | None
+
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _score_outs(N: int, k: int, tokens, entropy: bool, out: LogProbs | None, dev) -> LogProbs:
+    """The outputs of a log-probability call: ``out``'s tensors, checked, or new ones."""
+    if not 0 <= k <= MAX_TOP:
+        raise FgmError(f"k = {k} outside [0, {MAX_TOP}]")
+    if out is None:
+        f = torch.empty((2 + k, N) if k else (2, N), dtype=_F32, device=dev)      # one allocation for the fp32 ones
+        return LogProbs(None if tokens is None else f[0], f[1] if entropy else None,
+                        torch.empty((N, k), dtype=_I32, device=dev) if k else None, f[2:].view(N, k) if k else None)
+    for name, t, shape, dt, want in (("logp", out.logp, (N,), _F32, tokens is not None), ("entropy", out.entropy, (N,), _F32, entropy),
+                                     ("top_ids", out.top_ids, (N, k), _I32, k > 0), ("top_logp", out.top_logp, (N, k), _F32, k > 0)):
+        if want != (t is not None):
+            raise FgmError(f"out.{name}: {'missing' if want else 'given'}, though the call {'asks' if want else 'does not ask'} for it")
+        if want:
+            _expect("out." + name, t, shape, dt, dev)
+    return out
+
+
+def _at(t: torch.Tensor | None) -> int | None:
+    return None if t is None else t.data_ptr()
+
+
+def logprobs_workspace_bytes(N: int, V: int, k: int) -> int:
+    """Workspace bytes of logprobs (0 for sizes out of range)."""
+    return int(lib().fgm_logprobs_workspace_bytes(int(N), int(V), int(k)))
+
+
+def logprobs(z: torch.Tensor, tokens: torch.Tensor | None = None, k: int = 0, T: float = 1.0, entropy: bool = True,
+             out: LogProbs | None = None, ws: Workspace | None = None, stream=None) -> LogProbs:
+    """Log probabilities of rows of logits z [N, V] (fp32, bf16 or fp16; rows
+    dense, any distance apart) under softmax(z / T): of the given tokens (int32
+    [N]), with entropies and the k most likely words."""
+    if z.dim() != 2 or z.dtype not in _DTYPES or not z.is_cuda:
+        raise FgmError(f"z: expected CUDA fp32, bf16 or fp16 [N, V], got {tuple(z.shape)} {z.dtype} on {z.device}")
+    N, V = z.shape
+    stride, one = z.stride()
+    if (V > 1 and one != 1) or (N > 1 and stride < V):
+        raise FgmError(f"z: expected dense rows that do not overlap, strides {z.stride()}")
+    dev = z.device
+    at = None if tokens is None else _expect("tokens", tokens, (N,), _I32, dev)
+
+    def body(s):
+        r = _score_outs(N, k, tokens, entropy, out, dev)
+        w = Workspace(dev, nbytes=logprobs_workspace_bytes(N, V, k)) if ws is None else ws
+        _check(lib().fgm_logprobs(z.data_ptr(), _DTYPES[z.dtype], stride if N > 1 else V, N, V, T, at, k, _at(r.logp),
+                                  _at(r.entropy), _at(r.top_ids), _at(r.top_logp), w.t.data_ptr(), w.nbytes, s))
+        return r
     return _call(dev, stream, body)

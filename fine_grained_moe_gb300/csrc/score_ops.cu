@@ -1,0 +1,123 @@
+// C ABI of the log probabilities (declared in include/fgm.h): argument checks
+// and launches of logprobs.cuh.
+#include <cmath>
+
+#include "host.h"
+#include "logprobs.cuh"
+
+namespace fgm {
+namespace {
+
+constexpr int64_t kMaxRows = 1 << 24;
+
+bool score_sizes_ok(int64_t N, int64_t V, int k)
+{
+    return N >= 1 && N <= kMaxRows && V >= 1 && V <= 0x7FFFFFFFLL && k >= 0 && k <= FGM_MAX_TOP && k <= V;
+}
+
+int check_scores(int64_t N, int64_t V, float T, const int32_t *tokens, int k, const float *logp, const float *entropy,
+                 const int32_t *top_ids, const float *top_logp)
+{
+    if (N < 1 || N > kMaxRows)
+        return failf(FGM_ERR_INVALID_ARG, "N = %lld outside [1, 2^24]", (long long)N);
+    if (V < 1 || V > 0x7FFFFFFFLL)
+        return failf(FGM_ERR_INVALID_ARG, "V = %lld outside [1, 2^31)", (long long)V);
+    if (k < 0 || k > FGM_MAX_TOP || k > V)
+        return failf(FGM_ERR_INVALID_ARG, "k = %d outside [0, min(%d, V)]", k, FGM_MAX_TOP);
+    if (!(T > 0.0f) || !std::isfinite(T) || !std::isfinite(1.0f / T))
+        return failf(FGM_ERR_INVALID_ARG, "temperature T = %g: needs a finite T > 0 with 1/T finite", (double)T);
+    if (logp && !tokens)
+        return failf(FGM_ERR_INVALID_ARG, "logp without tokens");
+    if (k > 0 && (!top_ids || !top_logp))
+        return failf(FGM_ERR_INVALID_ARG, "top_ids/top_logp NULL with k = %d", k);
+    if (!is_aligned(tokens, 4) || !is_aligned(logp, 4) || !is_aligned(entropy, 4) || !is_aligned(top_ids, 4) ||
+        !is_aligned(top_logp, 4))
+        return failf(FGM_ERR_INVALID_ARG, "tokens or an output not 4-byte aligned");
+    return FGM_OK;
+}
+
+// Splits of a row: enough CTAs for about ten waves on a full sm_103 part at two
+// CTAs per SM (a short last wave then costs little), of 8,192 logits at least (one chunk a warp).
+// A function of the sizes alone, so that results do not depend on the device.
+int row_splits(int64_t N, int64_t V)
+{
+    const int64_t by_grid = (3200 + N - 1) / N, by_size = V / 8192;
+    const int64_t s = by_grid < by_size ? by_grid : by_size;
+    return s < 1 ? 1 : s > 64 ? 64 : static_cast<int>(s);
+}
+
+size_t part_offset() { return align_up(ws_offsets().total, 256); }
+
+score::Outs outs(const int32_t *tokens, float *logp, float *entropy, int32_t *top_ids, float *top_logp, int k, float T,
+                 int64_t V, void *ws)
+{
+    return score::Outs{tokens, logp, entropy, top_ids, top_logp, k, T, V,
+                       reinterpret_cast<int32_t *>(static_cast<char *>(ws) + ws_offsets().status)};
+}
+
+template <typename E>
+int launch_join(const E *z, int64_t stride, const float *ztok, int64_t N, int splits, const score::Part *part,
+                const score::Outs &o, cudaStream_t st)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((N + score::kWarps - 1) / score::kWarps));
+    cfg.blockDim = dim3(score::kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    FGM_HOST_CUDA(cudaLaunchKernelEx(&cfg, score::k_logprob_join<E>, z, stride, ztok, N, splits, part, o));
+    return FGM_OK;
+}
+
+template <typename E>
+int run_logprobs(const void *z, int64_t stride, int64_t N, const score::Outs &o, void *ws, cudaStream_t st)
+{
+    const int splits = row_splits(N, o.V);
+    score::Part *part = reinterpret_cast<score::Part *>(static_cast<char *>(ws) + part_offset());
+    score::k_logprobs<E><<<static_cast<unsigned>(N * splits), score::kThreads, 0, st>>>(static_cast<const E *>(z), stride,
+                                                                                         splits, part, o);
+    FGM_HOST_CUDA(cudaGetLastError());
+    return splits == 1 ? FGM_OK : launch_join<E>(static_cast<const E *>(z), stride, nullptr, N, splits, part, o, st);
+}
+
+}  // namespace
+}  // namespace fgm
+
+using namespace fgm;
+
+extern "C" {
+
+size_t fgm_logprobs_workspace_bytes(int64_t N, int64_t V, int k)
+{
+    if (!score_sizes_ok(N, V, k))
+        return 0;
+    const int s = row_splits(N, V);
+    return align_up(part_offset() + (s == 1 ? 0 : sizeof(score::Part) * static_cast<size_t>(N) * s), 256);
+}
+
+int fgm_logprobs(const void *z, int dtype, int64_t row_stride, int64_t N, int64_t V, float T, const int32_t *tokens,
+                 int k, float *logp, float *entropy, int32_t *top_ids, float *top_logp, void *ws, size_t ws_bytes,
+                 void *stream)
+{
+    FGM_HOST_TRY(check_scores(N, V, T, tokens, k, logp, entropy, top_ids, top_logp));
+    if (dtype != FGM_F32 && dtype != FGM_BF16 && dtype != FGM_F16)
+        return failf(FGM_ERR_INVALID_ARG, "dtype = %d: FGM_F32, FGM_BF16 or FGM_F16", dtype);
+    if (!z || !is_aligned(z, dtype == FGM_F32 ? 4 : 2))
+        return failf(FGM_ERR_INVALID_ARG, "z NULL or not aligned to an element");
+    if (row_stride < V || row_stride > (int64_t(1) << 40))
+        return failf(FGM_ERR_INVALID_ARG, "row_stride = %lld below V = %lld or above 2^40", (long long)row_stride, (long long)V);
+    FGM_HOST_TRY(host_check_ws(ws, ws_bytes, fgm_logprobs_workspace_bytes(N, V, k)));
+    FGM_HOST_TRY(host_device_ready(nullptr));
+    const score::Outs o = outs(tokens, logp, entropy, top_ids, top_logp, k, T, V, ws);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    switch (dtype) {
+    case FGM_F32: return run_logprobs<float>(z, row_stride, N, o, ws, st);
+    case FGM_BF16: return run_logprobs<__nv_bfloat16>(z, row_stride, N, o, ws, st);
+    default: return run_logprobs<__half>(z, row_stride, N, o, ws, st);
+    }
+}
+
+}  // extern "C"

@@ -407,6 +407,40 @@ int fgm_attn_fwd(const fgm_kv_cache *cache, const uint16_t *q, int64_t token_str
                  const int32_t *lens, const int32_t *block_table, int max_blocks, float scale, int window,
                  uint16_t *out, float *lse, void *ws, size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------- log probabilities
+ *
+ * What a served model says beside its tokens, and what scoring a text reads:
+ * for each row of logits z and p = softmax(z / T),
+ *   logp = ln p(token), entropy = -sum p ln p, and the k most likely words with
+ *   their ln p (descending, ties to the lower index).
+ * A token outside [0, V) has probability 0 (logp = -inf). A NaN logit counts as
+ * -inf, as a -inf logit does (probability 0); a row whose largest logit is not
+ * finite has no distribution: its logp, entropy and top_logp are NaN. Both raise
+ * FGM_STATUS_NONFINITE_LOGITS. */
+
+#define FGM_MAX_TOP 16 /* alternatives per row */
+
+/* Element types of fgm_logprobs. */
+enum { FGM_F32 = 0, FGM_BF16 = 1, FGM_F16 = 2 };
+
+/* Bytes of workspace fgm_logprobs needs (0 for sizes out of range). Such a
+ * workspace serves every other entry point too. */
+size_t fgm_logprobs_workspace_bytes(int64_t N, int64_t V, int k);
+
+/* Log probabilities of N rows of logits, such as the z of fgm_lm_head_sample.
+ * One pass over z; sums are fp32.
+ *  z           [N] rows of V elements of type dtype, row_stride elements apart (at least V),
+ *              aligned to an element; 1 <= N <= 2^24, 1 <= V < 2^31
+ *  T           temperature: finite, > 0, and 1/T finite
+ *  tokens      int32 [N] or NULL (then logp must be NULL)
+ *  k           alternatives, 0 <= k <= min(FGM_MAX_TOP, V)
+ *  logp        fp32 [N] output or NULL
+ *  entropy     fp32 [N] output or NULL
+ *  top_ids     int32 [N][k] and top_logp fp32 [N][k] outputs (NULL when k = 0) */
+int fgm_logprobs(const void *z, int dtype, int64_t row_stride, int64_t N, int64_t V, float T, const int32_t *tokens,
+                 int k, float *logp, float *entropy, int32_t *top_ids, float *top_logp, void *ws, size_t ws_bytes,
+                 void *stream);
+
 /* Selects the execution path of subsequent calls in this process; returns the
  * previous one. An unknown value leaves the path unchanged. Both paths compute
  * the same step; they differ in kernel design only. */

@@ -88,3 +88,24 @@ def attn(q, k_val, v_val, lens, table, scale, window):
                 dq[b, i, hq] = (np.abs(kk) @ np.abs(q[b, i, hq])).max() * scale
                 dk[b, i, hq] = np.abs(kk).sum(axis=1).max() * np.abs(q[b, i, hq]).max() * scale
     return out, lse, A, vmax, dq, dk
+
+
+def logprobs(z, tokens, k, T):
+    """z [N, V] fp64 (NaN counts as -inf). Returns logp, entropy, top ids, top logp."""
+    z = np.where(np.isnan(z), -np.inf, z)
+    m = z.max(axis=1, keepdims=True)
+    with np.errstate(invalid="ignore", over="ignore"):
+        x = (z - m) / T
+        e = np.exp(x)
+        l = e.sum(axis=1, keepdims=True)
+        lp = x - np.log(l)
+        ent = np.log(l)[:, 0] - np.where(e > 0, e * x, 0).sum(axis=1) / l[:, 0]
+    bad = ~np.isfinite(m[:, 0])
+    lp[bad], ent[bad] = np.nan, np.nan
+    ids = np.argsort(-z, axis=1, kind="stable")[:, :k]
+    V = z.shape[1]
+    tok = np.asarray(tokens)
+    inside = (tok >= 0) & (tok < V)
+    got = np.where(inside, np.take_along_axis(lp, np.where(inside, tok, 0)[:, None], 1)[:, 0], -np.inf)
+    got[bad] = np.nan
+    return got, ent, ids, np.take_along_axis(lp, ids, 1)
