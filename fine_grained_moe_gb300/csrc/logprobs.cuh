@@ -5,18 +5,18 @@
 //   H = ln l - (1 / l) sum_v exp((z_v - m) / T) (z_v - m) / T,  m = max z
 //
 // One pass over the logits, which bounds it: a lane keeps a running maximum m,
-// l and w = sum e d (d = (z - m) log2(e) / T, e = 2^d) over 32 logits at a time
+// l and w = sum e d (d = (z - m) log2(e) / T, e = 2^d) over 16 logits at a time
 // and rescales when its maximum grows. Differences are clamped at -200, where e
 // is 0 already, so that -inf (or a type's lowest value) adds 0 and not 0 * inf.
 // About 7 instructions and one exponential a logit, half of what HBM leaves
 // time for at 2 bytes.
 //
-// The k best are a list spread over a warp's lanes (lane i holds the i-th), and
-// a threshold: the best k-th value that any warp of the CTA holds. It starts as
-// the largest, over the warps, of the k-th largest of the 32 lane maxima of the
-// first chunk (k lanes reach it, so k logits do), so that hardly more than k
-// logits of the row are ever inserted. A chunk whose maximum is below it costs
-// one comparison a lane.
+// The k best cost nothing in that pass: the k-th largest of the threads' maxima
+// bounds the k-th best logit from below, so only the threads that reach it
+// (k of 256 unless logits tie) can hold one of the k best, and their warp reads
+// those threads' logits a second time, from the caches. (Lists kept during the
+// pass, with the same bound as a threshold, took 134 us on 1,013 x 50,021 bf16
+// logits, against 15 us of HBM time: the insertions were most of it.)
 //
 // Rows are cut into splits until the grid has several CTAs per SM; k_logprob_join
 // merges a row's splits in order (no atomics on results: the same call gives
@@ -31,7 +31,7 @@ namespace score {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxTop = FGM_MAX_TOP;
-constexpr int kVals = 32;                     // logits of a lane and chunk
+constexpr int kVals = 16;                     // logits of a lane and chunk
 constexpr float kClamp = -200.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -71,10 +71,10 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return y;
 }
 
-// An order of floats as unsigned integers (NaN does not occur).
+// An order of floats as unsigned integers (NaN does not occur; -0 is 0).
 __device__ __forceinline__ unsigned ordered(float x)
 {
-    const unsigned u = __float_as_uint(x);
+    const unsigned u = __float_as_uint(x + 0.0f);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
@@ -245,12 +245,12 @@ struct Load<__half> {
 
 // CTA (row, split): one pass over the split's logits.
 template <typename E>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 4)
     k_logprobs(const E *z, int64_t stride, int splits, Part *part, const Outs o)
 {
     using L = Load<E>;
-    constexpr int kVec = L::kVec, kLoads = kVals / kVec;
-    __shared__ unsigned s_thr;
+    constexpr int kVec = L::kVec, kLoads = kVals / kVec, kChunk = 32 * kLoads;      // vectors of a warp's chunk
+    __shared__ unsigned s_max[kThreads], s_bound;
     __shared__ Sums s_sum[kWarps];
     __shared__ float s_v[kWarps][kMaxTop];
     __shared__ int32_t s_i[kWarps][kMaxTop];
@@ -265,171 +265,168 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint4 *zv = reinterpret_cast<const uint4 *>(zr + head);
     const int v0 = static_cast<int>(static_cast<int64_t>(nvec) * split / splits);
     const int v1 = static_cast<int>(static_cast<int64_t>(nvec) * (split + 1) / splits);
-    const int chunks = (v1 - v0 + 32 * kLoads - 1) / (32 * kLoads);
     const float c = kLog2e / o.T;
-    if (tid == 0)
-        s_thr = 0;
 
     Sums s;
     s.clear();
-    TopList top;
-    top.clear();
     int nan = 0;
     uint4 raw[kLoads];
-    float v[kVals];
-    auto fetch = [&](int ch) {                 // one chunk's vectors of this lane
+    auto fetch = [&](int at) {                 // one chunk's vectors of this lane
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int at = v0 + (ch * kLoads + i) * 32 + lane;
-            if (at < v1)
-                raw[i] = __ldcs(zv + at);
-        }
+        for (int i = 0; i < kLoads; ++i)
+            if (at + i * 32 < v1)
+                raw[i] = __ldg(zv + at + i * 32);
     };
-    auto spread = [&](int ch) {                // to fp32; past the end: -inf
+    auto add = [&](float (&v)[kVals]) {        // 16 logits into the running sums
+        float mx = v[0];
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            L::unpack(raw[i], v + i * kVec);
-            if (v0 + (ch * kLoads + i) * 32 + lane >= v1)
+        for (int j = 1; j < kVals; ++j)
+            mx = max_nan(mx, v[j]);
+        if (mx != mx) {                        // NaN counts as -inf
+            nan = 1;
+            mx = -INFINITY;
 #pragma unroll
-                for (int j = 0; j < kVec; ++j)
-                    v[i * kVec + j] = -INFINITY;
+            for (int j = 0; j < kVals; ++j) {
+                v[j] = v[j] == v[j] ? v[j] : -INFINITY;
+                mx = fmaxf(mx, v[j]);
+            }
         }
-    };
-    // ch < 0: the logits before the first and after the last vector
-    auto index = [&](int ch, int j, int src) -> int32_t {
-        if (ch < 0)
-            return j == 0 ? src : V - tail + src;
-        return head + (v0 + (ch * kLoads + j / kVec) * 32 + src) * kVec + j % kVec;
+        if (mx > s.m)
+            s.rise(mx, c);
+        float l0 = 0.0f, l1 = 0.0f, w0 = 0.0f, w1 = 0.0f;
+        if (fabsf(s.m) < 1.0e30f) {            // one fused step: z c overflows only where the result is below the clamp
+            const float mc = s.m * c;
+#pragma unroll
+            for (int j = 0; j < kVals; j += 2) {
+                const float d0 = fmaxf(fmaf(v[j], c, -mc), kClamp), d1 = fmaxf(fmaf(v[j + 1], c, -mc), kClamp);
+                const float e0 = ex2(d0), e1 = ex2(d1);
+                l0 += e0;
+                l1 += e1;
+                w0 = fmaf(e0, d0, w0);
+                w1 = fmaf(e1, d1, w1);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kVals; ++j) {
+                const float d = fmaxf((v[j] - s.m) * c, kClamp), e = ex2(d);
+                l0 += e;
+                w0 = fmaf(e, d, w0);
+            }
+        }
+        s.l += l0 + l1;
+        s.w += w0 + w1;
     };
 
-    bool first = true;
-    const int begin = split == 0 && warp == 0 && head + tail > 0 ? -kWarps : warp;
-    int ch = begin;
-    if (ch >= 0 && ch < chunks)
-        fetch(ch);
-    for (;;) {
-        const bool work = ch < chunks;
-        if (work) {
-            if (ch >= 0) {
-                spread(ch);
-            } else {
+    int at = v0 + warp * kChunk + lane;
+    const int step = kWarps * kChunk;
+    const int first = at;
+    fetch(at);
+    const bool edges = split == 0 && warp == 0 && head + tail > 0;      // this warp takes the logits around the vectors
+    if (edges) {
+        float v[kVals];
 #pragma unroll
-                for (int j = 0; j < kVals; ++j)
-                    v[j] = -INFINITY;
-                if (lane < head)
-                    v[0] = L::one(zr + lane);
-                if (lane < tail)
-                    v[1] = L::one(zr + V - tail + lane);
-            }
-        } else if (!first) {
-            break;
+        for (int j = 0; j < kVals; ++j)
+            v[j] = -INFINITY;
+        if (lane < head)
+            v[0] = L::one(zr + lane);
+        if (lane < tail)
+            v[1] = L::one(zr + V - tail + lane);
+        add(v);
+    }
+    for (; at - lane < v1; at += step) {
+        float v[kVals];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            L::unpack(raw[i], v + i * kVec);
+        if (at - lane + kChunk > v1) {         // past the end: -inf
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                if (at + i * 32 >= v1)
+#pragma unroll
+                    for (int j = 0; j < kVec; ++j)
+                        v[i * kVec + j] = -INFINITY;
         }
-        const int next = ch + kWarps;
-        if (next >= 0 && next < chunks)
-            fetch(next);
-        float mx[4];
-        float cm = -INFINITY;
-        if (work) {
+        fetch(at + step);
+        add(v);
+    }
+
+    // ------------------------------------------------------------ the k best
+    TopList top;
+    top.clear();
+    if (k) {
+        s_max[tid] = ordered(s.m);
+        __syncthreads();
+        if (warp == 0) {
+            // the k-th largest of the threads' maxima, one round of removal each
+            unsigned x[kWarps], best = 0, kth = 0;
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                mx[g] = v[g * 8];
-#pragma unroll
-                for (int j = 1; j < 8; ++j)
-                    mx[g] = max_nan(mx[g], v[g * 8 + j]);
+            for (int i = 0; i < kWarps; ++i) {
+                x[i] = s_max[i * 32 + lane];
+                best = max(best, x[i]);
             }
-            cm = max_nan(max_nan(mx[0], mx[1]), max_nan(mx[2], mx[3]));
-            if (cm != cm) {                    // NaN counts as -inf
-                nan = 1;
+            for (int j = 0; j < k; ++j) {
+                kth = __reduce_max_sync(0xFFFFFFFFu, best);
+                const unsigned b = __ballot_sync(0xFFFFFFFFu, best == kth);
+                if (lane == __ffs(b) - 1) {
+                    bool gone = false;
 #pragma unroll
-                for (int j = 0; j < kVals; ++j)
-                    v[j] = v[j] == v[j] ? v[j] : -INFINITY;
-                cm = -INFINITY;
+                    for (int i = 0; i < kWarps; ++i)
+                        if (!gone && x[i] == kth) {
+                            x[i] = 0;
+                            gone = true;
+                        }
+                    best = 0;
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    mx[g] = -INFINITY;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        mx[g] = fmaxf(mx[g], v[g * 8 + j]);
-                    cm = fmaxf(cm, mx[g]);
+                    for (int i = 0; i < kWarps; ++i)
+                        best = max(best, x[i]);
                 }
+                __syncwarp();
             }
-            if (cm > s.m)
-                s.rise(cm, c);
-            float l0 = 0.0f, l1 = 0.0f, w0 = 0.0f, w1 = 0.0f;
-            if (fabsf(s.m) < 1.0e30f) {        // one fused step: z c cannot overflow unless the result is below the clamp
-                const float mc = s.m * c;
-#pragma unroll
-                for (int j = 0; j < kVals; j += 2) {
-                    const float d0 = fmaxf(fmaf(v[j], c, -mc), kClamp), d1 = fmaxf(fmaf(v[j + 1], c, -mc), kClamp);
-                    const float e0 = ex2(d0), e1 = ex2(d1);
-                    l0 += e0;
-                    l1 += e1;
-                    w0 = fmaf(e0, d0, w0);
-                    w1 = fmaf(e1, d1, w1);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < kVals; ++j) {
-                    const float d = fmaxf((v[j] - s.m) * c, kClamp), e = ex2(d);
-                    l0 += e;
-                    w0 = fmaf(e, d, w0);
-                }
-            }
-            s.l += l0 + l1;
-            s.w += w0 + w1;
+            if (lane == 0)
+                s_bound = kth;
         }
-        if (k) {
-            if (first) {
-                // a bound that k logits of the row reach, from the first chunk's lane maxima
-                float x = cm, kth = -INFINITY;
-                for (int j = 0; j < k; ++j) {
-                    kth = x;
-#pragma unroll
-                    for (int q = 16; q > 0; q >>= 1)
-                        kth = fmaxf(kth, __shfl_xor_sync(0xFFFFFFFFu, kth, q));
-                    const unsigned b = __ballot_sync(0xFFFFFFFFu, x == kth);
-                    if (lane == __ffs(b) - 1)
-                        x = -INFINITY;
+        __syncthreads();
+        const float bound = unordered(s_bound);
+        // the logits of every thread that reaches the bound, a vector a lane
+        for (unsigned who = __ballot_sync(0xFFFFFFFFu, s.m >= bound); who; who &= who - 1) {
+            const int src = __ffs(who) - 1;
+            if (edges) {
+                float v = -INFINITY;
+                int32_t i = kNone;
+                if (lane == 0 ? src < head : lane == 1 && src < tail) {
+                    i = lane == 0 ? src : V - tail + src;
+                    v = L::one(zr + i);
+                    v = v == v ? v : -INFINITY;
                 }
-                __syncthreads();               // s_thr is set
-                if (lane == 0)
-                    atomicMax(&s_thr, ordered(kth));
-                __syncthreads();
+                top.offer(v, i, k, lane);
             }
-            if (work) {
-                float bound = unordered(*reinterpret_cast<volatile unsigned *>(&s_thr));
-                if (__any_sync(0xFFFFFFFFu, cm >= bound)) {
+            for (int n0 = 0;; n0 += 32) {
+                const int n = n0 + lane;       // the thread's n-th vector
+                const int vec = first - lane + src + n / kLoads * step + n % kLoads * 32;
+                const bool in = vec < v1;
+                if (!__any_sync(0xFFFFFFFFu, in))
+                    break;
+                float v[kVec];
+                if (in)
+                    L::unpack(__ldg(zv + vec), v);
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        if (!__any_sync(0xFFFFFFFFu, mx[g] >= bound))
-                            continue;
-#pragma unroll
-                        for (int j = g * 8; j < g * 8 + 8; ++j)
-                            if (__any_sync(0xFFFFFFFFu, v[j] >= bound)) {
-                                const bool in = v[j] >= bound && (ch >= 0 || (j == 0 ? lane < head : j == 1 && lane < tail)) &&
-                                                (ch < 0 || v0 + (ch * kLoads + j / kVec) * 32 + lane < v1);
-                                top.offer(in ? v[j] : -INFINITY, in ? index(ch, j, lane) : kNone, k, lane);
-                            }
-                    }
-                    const float kth = __shfl_sync(0xFFFFFFFFu, top.v, k - 1);
-                    if (lane == 0 && kth > bound)
-                        atomicMax(&s_thr, ordered(kth));
+                for (int j = 0; j < kVec; ++j) {
+                    const float x = in && v[j] == v[j] ? v[j] : -INFINITY;
+                    if (__any_sync(0xFFFFFFFFu, in && x >= bound))
+                        top.offer(in && x >= bound ? x : -INFINITY, in && x >= bound ? head + vec * kVec + j : kNone, k, lane);
                 }
             }
         }
-        first = false;
-        ch = next;
+        if (lane < k) {
+            s_v[warp][lane] = top.v;
+            s_i[warp][lane] = top.i;
+        }
     }
 
     // ------------------------------------------------------------ the CTA's split
     s = warp_sums(s, c);
-    nan = __any_sync(0xFFFFFFFFu, nan);
     if (lane == 0)
         s_sum[warp] = s;
-    if (lane < k) {
-        s_v[warp][lane] = top.v;
-        s_i[warp][lane] = top.i;
-    }
     nan = __syncthreads_or(nan);
     if (warp)
         return;
@@ -463,8 +460,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 }
 
-// A warp per row merges its splits in order. The given token's logit comes from
-// z, or (z NULL) from ztok.
+// A warp per row merges its splits in order: the sums lane by lane and then
+// across the lanes, the lists as a k-way merge of 32 sorted lists at a time. The
+// given token's logit comes from z, or (z NULL) from ztok.
 template <typename E>
 __global__ void __launch_bounds__(kThreads)
     k_logprob_join(const E *z, int64_t stride, const float *ztok, int64_t N, int splits, const Part *part, const Outs o)
@@ -476,23 +474,6 @@ __global__ void __launch_bounds__(kThreads)
         return;
     const float c = kLog2e / o.T;
     const Part *p = part + row * splits;
-    Sums s;
-    s.clear();
-    int nan = 0;
-    TopList top;
-    top.clear();
-    for (int i = lane; i < splits; i += 32) {
-        s.add(Sums{__ldcg(&p[i].m), __ldcg(&p[i].l), __ldcg(&p[i].w)}, c);
-        nan |= __ldcg(&p[i].nan);
-    }
-    s = warp_sums(s, c);
-    nan = __any_sync(0xFFFFFFFFu, nan);
-    for (int i0 = 0; i0 < splits * k; i0 += 32) {
-        const int i = i0 + lane;
-        const bool in = i < splits * k;
-        const int sp = in ? i / k : 0, j = in ? i - sp * k : 0;
-        top.offer(in ? __ldcg(&p[sp].v[j]) : -INFINITY, in ? __ldcg(&p[sp].i[j]) : kNone, k, lane);
-    }
     float zt = -INFINITY;
     if (o.logp) {
         if (z) {
@@ -505,6 +486,63 @@ __global__ void __launch_bounds__(kThreads)
         if (zt != zt)
             zt = -INFINITY;
     }
+    Sums s;
+    s.clear();
+    int nan = 0;
+    TopList top;
+    top.clear();
+    for (int s0 = 0; s0 < splits; s0 += 32) {
+        const Part *mine = p + s0 + lane;
+        const bool in = s0 + lane < splits;
+        if (in) {
+            s.add(Sums{__ldcg(&mine->m), __ldcg(&mine->l), __ldcg(&mine->w)}, c);
+            nan |= __ldcg(&mine->nan);
+        }
+        if (!k)
+            continue;
+        // lane: the head of its list and the entry behind it
+        float hv = -INFINITY, nv = -INFINITY;
+        int32_t hi = kNone, ni = kNone;
+        int at = 2;
+        if (in) {
+            hv = __ldcg(&mine->v[0]);
+            hi = __ldcg(&mine->i[0]);
+            if (k > 1) {
+                nv = __ldcg(&mine->v[1]);
+                ni = __ldcg(&mine->i[1]);
+            }
+        }
+        float gv = -INFINITY;                  // lane j: the group's j-th best
+        int32_t gi = kNone;
+        for (int j = 0; j < k; ++j) {
+            const unsigned bv = __reduce_max_sync(0xFFFFFFFFu, ordered(hv));
+            const unsigned bi = __reduce_min_sync(0xFFFFFFFFu, ordered(hv) == bv ? static_cast<unsigned>(hi) : 0xFFFFFFFFu);
+            if (lane == j) {
+                gv = unordered(bv);
+                gi = static_cast<int32_t>(bi);
+            }
+            if (ordered(hv) == bv && static_cast<unsigned>(hi) == bi && hi != kNone) {
+                hv = nv;
+                hi = ni;
+                nv = -INFINITY;
+                ni = kNone;
+                if (at < k) {
+                    nv = __ldcg(&mine->v[at]);
+                    ni = __ldcg(&mine->i[at]);
+                }
+                ++at;
+            }
+            __syncwarp();
+        }
+        if (s0 == 0) {
+            top.v = gv;
+            top.i = gi;
+        } else {
+            top.offer(lane < k ? gv : -INFINITY, lane < k ? gi : kNone, k, lane);
+        }
+    }
+    s = warp_sums(s, c);
+    nan = __any_sync(0xFFFFFFFFu, nan);
     write_row(o, row, s, top, nan, zt, lane);
 }
 

@@ -114,9 +114,10 @@ def test_ties_and_orders(fgm, ws, dt):
     g = torch.Generator(device="cuda").manual_seed(8)
     rows = [torch.zeros(V), torch.full((V,), -7.5), torch.arange(V) / V * 8, -torch.arange(V) / V * 8,
             torch.randint(0, 3, (V,), generator=torch.Generator().manual_seed(1)).float(),
+            torch.where(torch.arange(V) % 3 == 0, 0.0, -0.0),
             torch.full((V,), float("-inf")).index_fill(0, torch.tensor([5, 20000]), 1.0)]
     z = torch.stack(rows).cuda().to(DT[dt])
-    check(fgm, ws, z, [0, V - 1, 3, 4, 5, 20000], 16, 1.0)
+    check(fgm, ws, z, [0, V - 1, 3, 4, 5, 6, 20000], 16, 1.0)
     del g
 
 
