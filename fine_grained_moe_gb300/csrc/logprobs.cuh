@@ -112,13 +112,12 @@ struct Sums {
     }
 };
 
+// The sums of 32 lanes: one reference for all, then plain sums in a fixed order.
 __device__ __forceinline__ Sums warp_sums(Sums s, float c)
 {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        s.add(Sums{__shfl_xor_sync(0xFFFFFFFFu, s.m, o), __shfl_xor_sync(0xFFFFFFFFu, s.l, o),
-                   __shfl_xor_sync(0xFFFFFFFFu, s.w, o)},
-              c);
+    s.rise(unordered(__reduce_max_sync(0xFFFFFFFFu, ordered(s.m))), c);
+    s.l = warp_sum(s.l);
+    s.w = warp_sum(s.w);
     return s;
 }
 
@@ -165,6 +164,33 @@ struct TopList {
         }
     }
 };
+
+// k-way merge of up to 32 sorted lists, one a lane (n entries, kNone past the
+// end): lane j gets the j-th best of all.
+__device__ __forceinline__ void merge_lists(const float *v, const int32_t *i, int n, int k, int lane, float &gv, int32_t &gi)
+{
+    float hv = n > 0 ? v[0] : -INFINITY, nv = n > 1 ? v[1] : -INFINITY;      // the head and the entry behind it
+    int32_t hi = n > 0 ? i[0] : kNone, ni = n > 1 ? i[1] : kNone;
+    int at = 2;
+    gv = -INFINITY;
+    gi = kNone;
+    for (int j = 0; j < k; ++j) {
+        const unsigned o = ordered(hv), bv = __reduce_max_sync(0xFFFFFFFFu, o);
+        const unsigned bi = __reduce_min_sync(0xFFFFFFFFu, o == bv ? static_cast<unsigned>(hi) : 0xFFFFFFFFu);
+        if (lane == j) {
+            gv = unordered(bv);
+            gi = static_cast<int32_t>(bi);
+        }
+        if (o == bv && static_cast<unsigned>(hi) == bi && hi != kNone) {
+            hv = nv;
+            hi = ni;
+            nv = at < n ? v[at] : -INFINITY;
+            ni = at < n ? i[at] : kNone;
+            ++at;
+        }
+        __syncwarp();
+    }
+}
 
 // A row's outputs from its sums and list (one warp). ztok: the given token's
 // logit (-inf outside the vocabulary).
@@ -430,11 +456,13 @@ __global__ void __launch_bounds__(kThreads, 4)
     nan = __syncthreads_or(nan);
     if (warp)
         return;
-    for (int w = 1; w < kWarps; ++w)
-        s.add(s_sum[w], c);
+    if (lane < kWarps)
+        s = s_sum[lane];
+    else
+        s.clear();
+    s = warp_sums(s, c);
     if (k)
-        for (int w = 1; w < kWarps; ++w)
-            top.offer(lane < k ? s_v[w][lane] : -INFINITY, lane < k ? s_i[w][lane] : kNone, k, lane);
+        merge_lists(s_v[lane & (kWarps - 1)], s_i[lane & (kWarps - 1)], lane < kWarps ? k : 0, k, lane, top.v, top.i);
     if (splits == 1) {
         float zt = -INFINITY;
         if (o.logp) {
@@ -500,40 +528,9 @@ __global__ void __launch_bounds__(kThreads)
         }
         if (!k)
             continue;
-        // lane: the head of its list and the entry behind it
-        float hv = -INFINITY, nv = -INFINITY;
-        int32_t hi = kNone, ni = kNone;
-        int at = 2;
-        if (in) {
-            hv = __ldcg(&mine->v[0]);
-            hi = __ldcg(&mine->i[0]);
-            if (k > 1) {
-                nv = __ldcg(&mine->v[1]);
-                ni = __ldcg(&mine->i[1]);
-            }
-        }
-        float gv = -INFINITY;                  // lane j: the group's j-th best
-        int32_t gi = kNone;
-        for (int j = 0; j < k; ++j) {
-            const unsigned bv = __reduce_max_sync(0xFFFFFFFFu, ordered(hv));
-            const unsigned bi = __reduce_min_sync(0xFFFFFFFFu, ordered(hv) == bv ? static_cast<unsigned>(hi) : 0xFFFFFFFFu);
-            if (lane == j) {
-                gv = unordered(bv);
-                gi = static_cast<int32_t>(bi);
-            }
-            if (ordered(hv) == bv && static_cast<unsigned>(hi) == bi && hi != kNone) {
-                hv = nv;
-                hi = ni;
-                nv = -INFINITY;
-                ni = kNone;
-                if (at < k) {
-                    nv = __ldcg(&mine->v[at]);
-                    ni = __ldcg(&mine->i[at]);
-                }
-                ++at;
-            }
-            __syncwarp();
-        }
+        float gv;
+        int32_t gi;
+        merge_lists(mine->v, mine->i, in ? k : 0, k, lane, gv, gi);
         if (s0 == 0) {
             top.v = gv;
             top.i = gi;

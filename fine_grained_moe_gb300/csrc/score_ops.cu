@@ -36,14 +36,24 @@ int check_scores(int64_t N, int64_t V, float T, const int32_t *tokens, int k, co
     return FGM_OK;
 }
 
-// Splits of a row: enough CTAs for about ten waves on a full sm_103 part at two
-// CTAs per SM (a short last wave then costs little), of 8,192 logits at least (one chunk a warp).
-// A function of the sizes alone, so that results do not depend on the device.
-int row_splits(int64_t N, int64_t V)
+// Splits of a row. 608 CTAs run at a time (152 SMs, four each); a CTA's start and
+// end (first loads, the k best, the sums) take about as long as 56 KB of its
+// share of HBM: the number of splits that makes waves * (56 KB + a split's bytes)
+// least. 1,013 rows of 100 KB: one split 28 us, four 51 us (measured); 600 rows
+// of 1 MB: one; 5 rows of 1 MB: 32. A split has 8,192 logits at least. A function
+// of the sizes alone, so that results do not depend on the device.
+int row_splits(int64_t N, int64_t V, int64_t elem)
 {
-    const int64_t by_grid = (3200 + N - 1) / N, by_size = V / 8192;
-    const int64_t s = by_grid < by_size ? by_grid : by_size;
-    return s < 1 ? 1 : s > 64 ? 64 : static_cast<int>(s);
+    const int64_t most = V / 8192;
+    int64_t best = 1, cost = 0;
+    for (int64_t s = 1; s == 1 || (s <= most && s <= 128); ++s) {
+        const int64_t c = (N * s + 607) / 608 * (56 * 1024 + V * elem / s);
+        if (s == 1 || c < cost) {
+            best = s;
+            cost = c;
+        }
+    }
+    return static_cast<int>(best);
 }
 
 size_t part_offset() { return align_up(ws_offsets().total, 256); }
@@ -75,7 +85,7 @@ int launch_join(const E *z, int64_t stride, const float *ztok, int64_t N, int sp
 template <typename E>
 int run_logprobs(const void *z, int64_t stride, int64_t N, const score::Outs &o, void *ws, cudaStream_t st)
 {
-    const int splits = row_splits(N, o.V);
+    const int splits = row_splits(N, o.V, sizeof(E));
     score::Part *part = reinterpret_cast<score::Part *>(static_cast<char *>(ws) + part_offset());
     score::k_logprobs<E><<<static_cast<unsigned>(N * splits), score::kThreads, 0, st>>>(static_cast<const E *>(z), stride,
                                                                                          splits, part, o);
@@ -94,7 +104,7 @@ size_t fgm_logprobs_workspace_bytes(int64_t N, int64_t V, int k)
 {
     if (!score_sizes_ok(N, V, k))
         return 0;
-    const int s = row_splits(N, V);
+    const int s4 = row_splits(N, V, 4), s2 = row_splits(N, V, 2), s = s4 > s2 ? s4 : s2;
     return align_up(part_offset() + (s == 1 ? 0 : sizeof(score::Part) * static_cast<size_t>(N) * s), 256);
 }
 
