@@ -100,6 +100,8 @@ def lib() -> ctypes.CDLL:
             "fgm_attn_fwd": (ci, [CP, vp, i64, ci, ci, ci, vp, vp, ci, ctypes.c_float, ci, vp, vp, vp, sz, vp]),
             "fgm_logprobs_workspace_bytes": (sz, [i64, i64, ci]),
             "fgm_logprobs": (ci, [vp, ci, i64, i64, i64, ctypes.c_float, vp, ci, vp, vp, vp, vp, vp, sz, vp]),
+            "fgm_lm_head_logprobs_workspace_bytes": (sz, [i64, i64, ci]),
+            "fgm_lm_head_logprobs": (ci, [vp, i64, vp, i64, ctypes.c_float, vp, ci, vp, vp, vp, vp, vp, sz, vp]),
             "fgm_read_status": (ci, [vp, sz, ci, vp, vp]),
             "fgm_select_path": (ci, [ci]),
             "fgm_set_phase_trace": (ci, [vp, sz]),
@@ -761,5 +763,34 @@ def logprobs(z: torch.Tensor, tokens: torch.Tensor | None = None, k: int = 0, T:
         w = Workspace(dev, nbytes=logprobs_workspace_bytes(N, V, k)) if ws is None else ws
         _check(lib().fgm_logprobs(z.data_ptr(), _DTYPES[z.dtype], stride if N > 1 else V, N, V, T, at, k, _at(r.logp),
                                   _at(r.entropy), _at(r.top_ids), _at(r.top_logp), w.t.data_ptr(), w.nbytes, s))
+        return r
+    return _call(dev, stream, body)
+
+
+def lm_head_logprobs_workspace_bytes(N: int, V: int, k: int) -> int:
+    """Workspace bytes of lm_head_logprobs (0 for sizes out of range)."""
+    return int(lib().fgm_lm_head_logprobs_workspace_bytes(int(N), int(V), int(k)))
+
+
+def lm_head_logprobs(emb: torch.Tensor, h: torch.Tensor, tokens: torch.Tensor | None = None, k: int = 0, T: float = 1.0,
+                     entropy: bool = True, out: LogProbs | None = None, ws: Workspace | None = None,
+                     stream=None) -> LogProbs:
+    """logprobs of the tied lm_head's logits emb . h of the bf16 rows h [N, 2816]
+    (any N: a decoded token, a verify step, a scored text), which are not stored."""
+    if not emb.is_cuda or emb.dim() != 2:
+        raise FgmError(f"emb: expected CUDA bf16 [V, {HIDDEN}], got {tuple(emb.shape)} on {emb.device}")
+    dev, V = emb.device, emb.shape[0]
+    e_at = _expect("emb", emb, (V, HIDDEN), _BF16, dev)
+    if h.dim() != 2:
+        raise FgmError(f"h: expected bf16 [N, {HIDDEN}], got {tuple(h.shape)}")
+    N = h.shape[0]
+    h_at = _expect("h", h, (N, HIDDEN), _BF16, dev)
+    at = None if tokens is None else _expect("tokens", tokens, (N,), _I32, dev)
+
+    def body(s):
+        r = _score_outs(N, k, tokens, entropy, out, dev)
+        w = Workspace(dev, nbytes=lm_head_logprobs_workspace_bytes(N, V, k)) if ws is None else ws
+        _check(lib().fgm_lm_head_logprobs(e_at, V, h_at, N, T, at, k, _at(r.logp), _at(r.entropy), _at(r.top_ids),
+                                          _at(r.top_logp), w.t.data_ptr(), w.nbytes, s))
         return r
     return _call(dev, stream, body)

@@ -139,6 +139,14 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
+// Waits up to a tenth of a second for what is in flight after an abort.
+__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity)
+{
+    const long long end = now_ns() + 100000000LL;
+    while (!bar_try(bar, parity) && now_ns() < end)
+        ;
+}
+
 __device__ __forceinline__ void bar_arrive(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -507,11 +515,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // every issued copy lands before the CTA may exit
         if (lane == 0) {
             for (int u = max(0, k_issued - p.k_ring); u < k_issued; ++u)
-                for (int it = 0; it < (1 << 22) && !bar_try(saddr(&sh.kfull[u % p.k_ring]), (u / p.k_ring) & 1); ++it)
-                    ;
+                bar_drain(saddr(&sh.kfull[u % p.k_ring]), (u / p.k_ring) & 1);
             for (int u = max(0, v_issued - p.v_ring); u < v_issued; ++u)
-                for (int it = 0; it < (1 << 22) && !bar_try(saddr(&sh.vfull[u % p.v_ring]), (u / p.v_ring) & 1); ++it)
-                    ;
+                bar_drain(saddr(&sh.vfull[u % p.v_ring]), (u / p.v_ring) & 1);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -551,8 +557,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // every issued product completes before the tensor memory is released
         if (lead) {
             commit(&sh.drained[0]);
-            for (int it = 0; it < (1 << 22) && !bar_try(saddr(&sh.drained[0]), 0); ++it)
-                ;
+            bar_drain(saddr(&sh.drained[0]), 0);
         }
         __syncwarp();
     } else if (warp == 2) {
@@ -589,8 +594,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         if (lead) {
             commit(&sh.drained[1]);
-            for (int it = 0; it < (1 << 22) && !bar_try(saddr(&sh.drained[1]), 0); ++it)
-                ;
+            bar_drain(saddr(&sh.drained[1]), 0);
         }
         __syncwarp();
     } else if (warp >= 4) {

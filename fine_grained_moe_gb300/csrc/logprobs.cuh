@@ -112,6 +112,48 @@ struct Sums {
     }
 };
 
+// 16 logits into the running sums of a lane; NaN becomes -inf, in v too.
+__device__ __forceinline__ void fold(Sums &s, float (&v)[kVals], float c, int &nan)
+{
+    float mx = v[0];
+#pragma unroll
+    for (int j = 1; j < kVals; ++j)
+        mx = max_nan(mx, v[j]);
+    if (mx != mx) {
+        nan = 1;
+        mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < kVals; ++j) {
+            v[j] = v[j] == v[j] ? v[j] : -INFINITY;
+            mx = fmaxf(mx, v[j]);
+        }
+    }
+    if (mx > s.m)
+        s.rise(mx, c);
+    float l0 = 0.0f, l1 = 0.0f, w0 = 0.0f, w1 = 0.0f;
+    if (fabsf(s.m) < 1.0e30f) {            // one fused step: z c overflows only where the result is below the clamp
+        const float mc = s.m * c;
+#pragma unroll
+        for (int j = 0; j < kVals; j += 2) {
+            const float d0 = fmaxf(fmaf(v[j], c, -mc), kClamp), d1 = fmaxf(fmaf(v[j + 1], c, -mc), kClamp);
+            const float e0 = ex2(d0), e1 = ex2(d1);
+            l0 += e0;
+            l1 += e1;
+            w0 = fmaf(e0, d0, w0);
+            w1 = fmaf(e1, d1, w1);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kVals; ++j) {
+            const float d = fmaxf((v[j] - s.m) * c, kClamp), e = ex2(d);
+            l0 += e;
+            w0 = fmaf(e, d, w0);
+        }
+    }
+    s.l += l0 + l1;
+    s.w += w0 + w1;
+}
+
 // The sums of 32 lanes: one reference for all, then plain sums in a fixed order.
 __device__ __forceinline__ Sums warp_sums(Sums s, float c)
 {
@@ -303,45 +345,6 @@ __global__ void __launch_bounds__(kThreads, 4)
             if (at + i * 32 < v1)
                 raw[i] = __ldg(zv + at + i * 32);
     };
-    auto add = [&](float (&v)[kVals]) {        // 16 logits into the running sums
-        float mx = v[0];
-#pragma unroll
-        for (int j = 1; j < kVals; ++j)
-            mx = max_nan(mx, v[j]);
-        if (mx != mx) {                        // NaN counts as -inf
-            nan = 1;
-            mx = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < kVals; ++j) {
-                v[j] = v[j] == v[j] ? v[j] : -INFINITY;
-                mx = fmaxf(mx, v[j]);
-            }
-        }
-        if (mx > s.m)
-            s.rise(mx, c);
-        float l0 = 0.0f, l1 = 0.0f, w0 = 0.0f, w1 = 0.0f;
-        if (fabsf(s.m) < 1.0e30f) {            // one fused step: z c overflows only where the result is below the clamp
-            const float mc = s.m * c;
-#pragma unroll
-            for (int j = 0; j < kVals; j += 2) {
-                const float d0 = fmaxf(fmaf(v[j], c, -mc), kClamp), d1 = fmaxf(fmaf(v[j + 1], c, -mc), kClamp);
-                const float e0 = ex2(d0), e1 = ex2(d1);
-                l0 += e0;
-                l1 += e1;
-                w0 = fmaf(e0, d0, w0);
-                w1 = fmaf(e1, d1, w1);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < kVals; ++j) {
-                const float d = fmaxf((v[j] - s.m) * c, kClamp), e = ex2(d);
-                l0 += e;
-                w0 = fmaf(e, d, w0);
-            }
-        }
-        s.l += l0 + l1;
-        s.w += w0 + w1;
-    };
 
     int at = v0 + warp * kChunk + lane;
     const int step = kWarps * kChunk;
@@ -357,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 4)
             v[0] = L::one(zr + lane);
         if (lane < tail)
             v[1] = L::one(zr + V - tail + lane);
-        add(v);
+        fold(s, v, c, nan);
     }
     for (; at - lane < v1; at += step) {
         float v[kVals];
@@ -373,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 4)
                         v[i * kVec + j] = -INFINITY;
         }
         fetch(at + step);
-        add(v);
+        fold(s, v, c, nan);
     }
 
     // ------------------------------------------------------------ the k best

@@ -3,6 +3,7 @@
 #include <cmath>
 
 #include "host.h"
+#include "lm_score.cuh"
 #include "logprobs.cuh"
 
 namespace fgm {
@@ -93,6 +94,37 @@ int run_logprobs(const void *z, int64_t stride, int64_t N, const score::Outs &o,
     return splits == 1 ? FGM_OK : launch_join<E>(static_cast<const E *>(z), stride, nullptr, N, splits, part, o, st);
 }
 
+// Word ranges of a row tile of fgm_lm_head_logprobs: the number that makes waves *
+// (a range's tiles + 1) least, for the 76 pairs of a 152-SM part; an item's start
+// and end cost about one tile.
+int word_splits(int64_t N, int64_t V)
+{
+    const int64_t tiles = (V + score::kLmWords - 1) / score::kLmWords, rows = (N + score::kLmRows - 1) / score::kLmRows;
+    int64_t best = 1, cost = 0;
+    for (int64_t s = 1; s <= tiles && s <= 152; ++s) {
+        const int64_t c = (rows * s + 75) / 76 * ((tiles + s - 1) / s + 1);
+        if (s == 1 || c < cost) {
+            best = s;
+            cost = c;
+        }
+    }
+    return static_cast<int>(best);
+}
+
+// The regions behind the common workspace: partial results, the given tokens' logits.
+struct LmWs {
+    size_t part, ztok, total;
+};
+
+LmWs lm_ws(int64_t N, int64_t V)
+{
+    LmWs o;
+    o.part = part_offset();
+    o.ztok = align_up(o.part + sizeof(score::Part) * static_cast<size_t>(N) * word_splits(N, V), 256);
+    o.total = align_up(o.ztok + sizeof(float) * static_cast<size_t>(N), 256);
+    return o;
+}
+
 }  // namespace
 }  // namespace fgm
 
@@ -128,6 +160,52 @@ int fgm_logprobs(const void *z, int dtype, int64_t row_stride, int64_t N, int64_
     case FGM_BF16: return run_logprobs<__nv_bfloat16>(z, row_stride, N, o, ws, st);
     default: return run_logprobs<__half>(z, row_stride, N, o, ws, st);
     }
+}
+
+size_t fgm_lm_head_logprobs_workspace_bytes(int64_t N, int64_t V, int k)
+{
+    return score_sizes_ok(N, V, k) ? lm_ws(N, V).total : 0;
+}
+
+int fgm_lm_head_logprobs(const uint16_t *emb, int64_t V, const uint16_t *h, int64_t N, float T, const int32_t *tokens,
+                         int k, float *logp, float *entropy, int32_t *top_ids, float *top_logp, void *ws,
+                         size_t ws_bytes, void *stream)
+{
+    FGM_HOST_TRY(check_scores(N, V, T, tokens, k, logp, entropy, top_ids, top_logp));
+    if (!emb || !is_aligned(emb, 16) || !h || !is_aligned(h, 16))
+        return failf(FGM_ERR_INVALID_ARG, "emb/h NULL or not 16-byte aligned");
+    FGM_HOST_TRY(host_check_ws(ws, ws_bytes, fgm_lm_head_logprobs_workspace_bytes(N, V, k)));
+    int sms = 0;
+    FGM_HOST_TRY(host_device_ready(&sms));
+    CUtensorMap hmap, emap;
+    FGM_HOST_TRY(host_hidden_map(&hmap, h, N));
+    FGM_HOST_TRY(host_hidden_map(&emap, emb, V));
+    const LmWs w = lm_ws(N, V);
+    const score::Outs o = outs(tokens, logp, entropy, top_ids, top_logp, k, T, V, ws);
+    score::LmArgs a = {};
+    a.N = N;
+    a.V = static_cast<int>(V);
+    a.tokens = tokens;
+    a.T = T;
+    a.k = k;
+    a.splits = word_splits(N, V);
+    a.items = (N + score::kLmRows - 1) / score::kLmRows * a.splits;
+    a.part = reinterpret_cast<score::Part *>(static_cast<char *>(ws) + w.part);
+    a.ztok = reinterpret_cast<float *>(static_cast<char *>(ws) + w.ztok);
+    a.status = o.status;
+    a.timeout_ns = host_wait_limit_ns();
+    static bool ready[64];                     // per device; setting it twice does no harm
+    int dev = 0;
+    FGM_HOST_CUDA(cudaGetDevice(&dev));
+    if (!ready[dev & 63]) {
+        FGM_HOST_CUDA(cudaFuncSetAttribute(score::k_lm_score, cudaFuncAttributeMaxDynamicSharedMemorySize, score::kLmSmem));
+        ready[dev & 63] = true;
+    }
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int64_t pairs = a.items < sms / 2 ? a.items : sms / 2;
+    score::k_lm_score<<<static_cast<unsigned>(2 * pairs), score::kLmThreads, score::kLmSmem, st>>>(hmap, emap, a);
+    FGM_HOST_CUDA(cudaGetLastError());
+    return launch_join<float>(nullptr, 0, a.ztok, N, a.splits, a.part, o, st);
 }
 
 }  // extern "C"

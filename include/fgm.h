@@ -441,6 +441,19 @@ int fgm_logprobs(const void *z, int dtype, int64_t row_stride, int64_t N, int64_
                  int k, float *logp, float *entropy, int32_t *top_ids, float *top_logp, void *ws, size_t ws_bytes,
                  void *stream);
 
+/* Bytes of workspace fgm_lm_head_logprobs needs (0 for sizes out of range). */
+size_t fgm_lm_head_logprobs_workspace_bytes(int64_t N, int64_t V, int k);
+
+/* The same from hidden rows: log probabilities under the tied lm_head's logits
+ * z[n][v] = sum_j emb[v][j] * h[n][j] (fp32 accumulation) of N rows, one for a
+ * decoded token, M for a verify step, thousands for a scored text. The logits
+ * are not stored; every sum over them is fp32. Arguments as fgm_logprobs, and
+ *  emb  bf16 [V][2816] (16-byte aligned), 1 <= V < 2^31
+ *  h    bf16 [N][2816] final hidden states (16-byte aligned), 1 <= N <= 2^24 */
+int fgm_lm_head_logprobs(const uint16_t *emb, int64_t V, const uint16_t *h, int64_t N, float T, const int32_t *tokens,
+                         int k, float *logp, float *entropy, int32_t *top_ids, float *top_logp, void *ws,
+                         size_t ws_bytes, void *stream);
+
 /* Selects the execution path of subsequent calls in this process; returns the
  * previous one. An unknown value leaves the path unchanged. Both paths compute
  * the same step; they differ in kernel design only. */

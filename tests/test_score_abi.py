@@ -35,7 +35,23 @@ def test_bad_calls(lib, bad):
     assert call(lib, **bad) == -1 and lib.fgm_last_error()
 
 
+def lm(lib, emb=AT, V=100, h=AT, N=2, T=1.0, tokens=AT, k=4, logp=AT, entropy=AT, ids=AT, tlp=AT, ws=AT, nws=1 << 40):
+    return lib.fgm_lm_head_logprobs(emb, V, h, N, T, tokens, k, logp, entropy, ids, tlp, ws, nws, None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(emb=None), dict(emb=AT + 8), dict(h=None), dict(h=AT + 2), dict(N=0), dict(N=(1 << 24) + 1), dict(V=0), dict(V=1 << 31),
+    dict(T=0.0), dict(T=float("nan")), dict(tokens=None), dict(k=-1), dict(k=17), dict(V=3, k=4), dict(ids=None),
+    dict(tlp=AT + 2)])
+def test_bad_lm_head_calls(lib, bad):
+    assert lm(lib, **bad) == -1 and lib.fgm_last_error()
+
+
 def test_bad_workspaces(lib):
+    assert lm(lib, ws=None) == -2 and lm(lib, ws=AT + 16) == -2 and lm(lib, nws=1024) == -2
+    assert fgm.lm_head_logprobs_workspace_bytes(5, 262144, 8) > fgm.workspace_bytes(8)
+    assert fgm.lm_head_logprobs_workspace_bytes(0, 10, 1) == 0
+
     assert call(lib, ws=None) == -2
     assert call(lib, ws=AT + 16) == -2
     assert call(lib, nws=1024) == -2
