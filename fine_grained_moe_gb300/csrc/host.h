@@ -18,7 +18,7 @@ int host_fail(int code, const char *msg);
 int host_device_ready(int *sms);
 long long host_wait_limit_ns();
 int host_rows64_map(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows);
-int host_hidden_map(CUtensorMap *map, const void *base, uint64_t rows);
+int host_hidden_map(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows);
 
 inline int failf(int code, const char *fmt, ...)
 {

@@ -13,13 +13,21 @@
 //  * The first CTA's issuing warp runs M = 256, N = 256, K = 16 products into one
 //    of two accumulators (2 x 256 columns), so that the next tile's products run
 //    under this tile's epilogue.
-//  * Four epilogue warps per CTA own a row a thread: 32 columns at a time they
-//    go into the running (m, l, w), and those that beat the row's k-th best into
-//    its list in shared memory (unsorted; the worst entry is replaced). A row
-//    meets about k (1 + ln(n / k)) such logits among n.
+//  * Eight epilogue warps per CTA own a row and half of a tile's columns a
+//    thread: 16 at a time the logits go into the running (m, l, w), and those that beat the row's L-th best (L =
+//    12, or 20 for more than 8 alternatives) into its list, sorted in registers.
+//    A row meets about L (1 + ln(n / L)) such logits among n.
 //  * An item is 256 rows x a range of words; a pair takes items in turn, a row's
-//    state stays in registers over the range, and k_logprob_join merges the
-//    ranges.
+//    state stays in registers over the range, and k_lm_join merges the ranges.
+//
+// Precision. The tensor pipe adds 16 products at a time to an fp32 accumulator
+// and truncates: 176 additions take up to 176 ulps off a logit, in one
+// direction, measured 2e-5 at logits near 10. That is too much for the few large
+// logits, which are what the outputs are made of, so the join computes them
+// again: the row's L best and the given token with fp32 multiply-adds (88 a lane
+// and a tree), orders the alternatives by these, and puts them in the place of
+// the first values in the row's sums. The others' share of the sums is small, or
+// their logits are, with their ulps.
 // Pairs whose items are the same words and other rows run at the same time, so
 // the embedding comes from HBM once and from L2 for the others.
 #pragma once
@@ -31,27 +39,24 @@
 namespace fgm {
 namespace score {
 
-constexpr int kLmThreads = 256;                  // copies, products, -, -, four epilogue warps
+constexpr int kLmThreads = 384;                  // copies, products, -, -, eight epilogue warps
 constexpr int kLmStages = 6;
 constexpr int kLmBox = 128 * 128;                // 128 rows x 128 bytes
 constexpr int kLmStage = 2 * kLmBox;             // rows and words
 constexpr int kLmWords = 256;                    // words of a tile
 constexpr int kLmRows = 256;                     // rows of a pair
 constexpr int kLmK = kH / 64;                    // stages of a tile
-constexpr int kLmListBytes = kMaxTop * 128 * 8;  // [k][128 rows] values, then indices
-constexpr int kLmSmem = kLmStages * kLmStage + kLmListBytes + 1024;
+constexpr int kLmSmem = kLmStages * kLmStage + 1024;
 static_assert(kH % 64 == 0, "K must split into whole stages");
 
 struct LmArgs {
     int64_t N;
     int V;
-    const int32_t *tokens;   // or NULL
     float T;
-    int k;
+    int h_rows;              // rows of a copy of hidden rows: 128, or all there are
     int splits;              // word ranges
     int64_t items;           // row tiles * splits
-    Part *part;              // [N][splits]
-    float *ztok;             // [N] the given token's logit
+    Part *part;              // [N][splits][2 halves of the columns]
     int32_t *status;
     long long timeout_ns;
 };
@@ -129,6 +134,8 @@ __device__ __forceinline__ void lm_copy(uint32_t dst, const CUtensorMap *map, in
         : "memory");
 }
 
+// L: entries of a row's list.
+template <int L>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
     k_lm_score(const __grid_constant__ CUtensorMap hmap, const __grid_constant__ CUtensorMap emap, const LmArgs p)
 {
@@ -142,8 +149,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     uint8_t *dsm = dsm_raw + ((1024u - (saddr(dsm_raw) & 1023u)) & 1023u);
     const uint32_t ring = saddr(dsm);
-    float *lv = reinterpret_cast<float *>(dsm + kLmStages * kLmStage);
-    int32_t *li = reinterpret_cast<int32_t *>(lv + kMaxTop * 128);
     const long long deadline = now_ns() + p.timeout_ns;
     const int pairs = gridDim.x / 2, pair = blockIdx.x / 2;
     const int tiles = (p.V + kLmWords - 1) / kLmWords;
@@ -158,7 +163,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             init(&sh.tfull[i], 1);
-            init(&sh.tempty[i], 8);              // the epilogue warps of both CTAs
+            init(&sh.tempty[i], 16);             // the epilogue warps of both CTAs
         }
         init(&sh.drained, 1);
         sh.abort = 0;
@@ -213,7 +218,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
             for (int64_t item = pair; item < p.items && ok; item += pairs) {
                 int t0, t1;
                 range(item, t0, t1);
-                const int y = static_cast<int>(item / p.splits) * kLmRows + rank * 128;
+                // (a CTA without rows copies none; its half of the accumulator is never read)
+                const int y0 = static_cast<int>(item / p.splits) * kLmRows, y = y0 + rank * 128;
+                const uint32_t both = 2 * kLmBox + ((y0 < p.N) + (y0 + 128 < p.N)) * p.h_rows * 128;
                 for (int t = t0; t < t1 && ok; ++t)
                     for (int ks = 0; ks < kLmK; ++ks, ++n) {
                         const int slot = n % kLmStages;
@@ -222,9 +229,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
                         const uint32_t bar = in_first(saddr(&sh.full[slot])), dst = ring + slot * kLmStage;
                         if (rank == 0)
                             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(&sh.full[slot])),
-                                         "r"(2 * kLmStage)
+                                         "r"(both)
                                          : "memory");
-                        lm_copy(dst, &hmap, ks * 64, y, bar);
+                        if (y < p.N)
+                            lm_copy(dst, &hmap, ks * 64, y, bar);
                         lm_copy(dst + kLmBox, &emap, ks * 64, t * kLmWords + rank * 128, bar);
                     }
             }
@@ -280,8 +288,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
             __syncwarp();
         }
     } else if (warp >= 4) {
-        // ------------------------------------------------------------ epilogue: a thread is a row
-        const int quarter = warp & 3, r = quarter * 32 + lane, k = p.k;
+        // ------------------------------------------------------------ epilogue: a thread is a row, of half the columns
+        const int quarter = warp & 3, r = quarter * 32 + lane, half = (warp - 4) >> 2;
         const float c = kLog2e / p.T;
         bool alive = true;
         uint32_t tile = 0;
@@ -290,24 +298,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
             range(item, t0, t1);
             const int64_t row = item / p.splits * kLmRows + rank * 128 + r;
             const int split = static_cast<int>(item % p.splits);
-            const int tok = p.tokens && row < p.N ? __ldg(p.tokens + row) : -1;
+            const bool live = row - lane < p.N;  // (of the warp: some row is one)
             Sums s;
             s.clear();
-            int nan = 0, worst = 0;              // the list's worst entry: its place, value and index
-            float wv = -INFINITY;
-            int32_t wi = kNone;
-            for (int j = 0; j < k; ++j) {
-                lv[j * 128 + r] = -INFINITY;
-                li[j * 128 + r] = kNone;
+            int nan = 0;
+            float lv[L];                         // best first
+            int32_t li[L];
+#pragma unroll
+            for (int j = 0; j < L; ++j) {
+                lv[j] = -INFINITY;
+                li[j] = kNone;
             }
-            float zt = -INFINITY;
             for (int t = t0; t < t1; ++t, ++tile) {
                 const uint32_t buf = tile & 1;
                 if (alive)
                     alive = wait(&sh.tfull[buf], tile >> 1, 33, t);
                 alive = __all_sync(0xFFFFFFFFu, alive);
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                for (int c0 = 0; c0 < kLmWords; c0 += 16) {
+                for (int c0 = half * (kLmWords / 2); live && c0 < (half + 1) * (kLmWords / 2); c0 += 16) {
                     uint32_t u[16];
                     asm volatile(
                         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
@@ -328,34 +336,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
                             v[j] = v0 + j < p.V ? v[j] : -INFINITY;
-                    if (tok >= v0 && tok < v0 + 16)
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            zt = tok == v0 + j ? v[j] : zt;
-                    fold(s, v, c, nan);
-                    if (k == 0)
+                    const float mx = fold(s, v, c, nan);
+                    if (mx <= lv[L - 1] && li[L - 1] != kNone)
                         continue;
-                    float mx = v[0];
+                    // (words come in order: an equal logit later does not replace an earlier one)
+                    unsigned in = 0;
 #pragma unroll
-                    for (int j = 1; j < 16; ++j)
-                        mx = fmaxf(mx, v[j]);
-                    if (mx > wv || wi == kNone) {
+                    for (int j = 0; j < 16; ++j)
+                        in |= v[j] > lv[L - 1] || (li[L - 1] == kNone && v0 + j < p.V) ? 1u << j : 0u;
+                    for (; in; in &= in - 1) {
+                        const int j = __ffs(in) - 1;
+                        float x = v[0];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (better(v[j], v0 + j, wv, wi) && v0 + j < p.V) {
-                                lv[worst * 128 + r] = v[j];
-                                li[worst * 128 + r] = v0 + j;
-                                wv = INFINITY;
-                                wi = -1;
-                                for (int q = 0; q < k; ++q) {
-                                    const float qv = lv[q * 128 + r];
-                                    const int32_t qi = li[q * 128 + r];
-                                    if (better(wv, wi, qv, qi)) {
-                                        wv = qv;
-                                        wi = qi;
-                                        worst = q;
-                                    }
-                                }
+                        for (int q = 1; q < 16; ++q)
+                            x = j == q ? v[q] : x;
+                        if (!better(x, v0 + j, lv[L - 1], li[L - 1]))
+                            continue;
+                        lv[L - 1] = x;
+                        li[L - 1] = v0 + j;
+#pragma unroll
+                        for (int q = L - 1; q > 0; --q)
+                            if (better(lv[q], li[q], lv[q - 1], li[q - 1])) {
+                                const float tv = lv[q];
+                                const int32_t ti = li[q];
+                                lv[q] = lv[q - 1];
+                                li[q] = li[q - 1];
+                                lv[q - 1] = tv;
+                                li[q - 1] = ti;
                             }
                     }
                 }
@@ -366,30 +373,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
                                  : "memory");
             }
             if (row < p.N) {
-                Part *o = p.part + row * p.splits + split;
+                Part *o = p.part + (row * p.splits + split) * 2 + half;
                 o->m = s.m;
                 o->l = s.l;
                 o->w = s.w;
                 o->nan = nan;
-                for (int j = 0; j < k; ++j) {    // the list in order
-                    float bv = -INFINITY;
-                    int32_t bi = kNone;
-                    int at = 0;
-                    for (int q = 0; q < k; ++q) {
-                        const float qv = lv[q * 128 + r];
-                        const int32_t qi = li[q * 128 + r];
-                        if (qi >= 0 && better(qv, qi, bv, bi)) {
-                            bv = qv;
-                            bi = qi;
-                            at = q;
-                        }
-                    }
-                    o->v[j] = bv;
-                    o->i[j] = bi;
-                    li[at * 128 + r] = -1;       // taken
+#pragma unroll
+                for (int j = 0; j < L; ++j) {
+                    o->v[j] = lv[j];
+                    o->i[j] = li[j];
                 }
-                if (tok >= 0 && tok < p.V ? tok / kLmWords >= t0 && tok / kLmWords < t1 : split == 0)
-                    p.ztok[row] = zt;
             }
         }
     }
@@ -401,6 +394,80 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
+}
+
+// A CTA per row: merges its ranges, computes the largest logits and the given
+// token's again in fp32, corrects the sums and writes the row.
+template <int L>
+__global__ void __launch_bounds__(kThreads) k_lm_join(const uint16_t *emb, const uint16_t *h, const LmArgs p, const Outs o)
+{
+    __shared__ float s_z[L + 1];
+    __shared__ int32_t s_i[L + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row = blockIdx.x;
+    const float c = kLog2e / o.T;
+    // the hidden row, 8 elements of every 256 a lane (the first kernel does not write it)
+    constexpr int kPer = kH / 256;
+    uint4 hr[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        hr[i] = __ldg(reinterpret_cast<const uint4 *>(h + row * kH) + i * 32 + lane);
+    const int32_t tok = o.logp ? __ldg(o.tokens + row) : -1;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    Sums s;
+    int nan = 0;
+    TopList top;
+    if (warp == 0) {
+        join_parts(p.part + row * p.splits * 2, p.splits * 2, L, c, lane, s, nan, top);
+        if (lane < L)
+            s_i[lane] = top.i;
+        if (lane == 0)
+            s_i[L] = tok >= 0 && tok < p.V ? tok : kNone;
+    }
+    __syncthreads();
+    for (int j = warp; j <= L; j += kWarps) {
+        const int32_t w = s_i[j];
+        float z = -INFINITY;
+        if (w != kNone) {
+            uint4 er[kPer];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                er[i] = __ldg(reinterpret_cast<const uint4 *>(emb + static_cast<int64_t>(w) * kH) + i * 32 + lane);
+            float a0 = 0.0f, a1 = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const uint32_t x[4] = {hr[i].x, hr[i].y, hr[i].z, hr[i].w}, y[4] = {er[i].x, er[i].y, er[i].z, er[i].w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float2 u = bf16x2_to_f32(x[q]), v = bf16x2_to_f32(y[q]);
+                    a0 = fmaf(u.x, v.x, a0);
+                    a1 = fmaf(u.y, v.y, a1);
+                }
+            }
+            z = warp_sum(a0 + a1);
+            z = z == z ? z : -INFINITY;
+        }
+        if (lane == 0)
+            s_z[j] = z;
+    }
+    __syncthreads();
+    if (warp)
+        return;
+    // the first values of the L best leave the sums, the second ones enter
+    const float z0 = top.v, z1 = lane < L ? s_z[lane] : -INFINITY;
+    float dl = 0.0f, dw = 0.0f;
+    if (lane < L && fabsf(s.m) < INFINITY) {
+        const float d0 = fmaxf((z0 - s.m) * c, kClamp), d1 = fmaxf((z1 - s.m) * c, kClamp);
+        const float e0 = ex2(d0), e1 = ex2(d1);
+        dl = e1 - e0;
+        dw = e1 * d1 - e0 * d0;
+    }
+    s.l += warp_sum(dl);
+    s.w += warp_sum(dw);
+    TopList best;
+    best.clear();
+    best.offer(lane < L ? z1 : -INFINITY, lane < L ? top.i : kNone, L, lane);
+    write_row(o, row, s, best, nan, s_z[L], lane);
 }
 
 }  // namespace score

@@ -31,6 +31,7 @@ namespace score {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxTop = FGM_MAX_TOP;
+constexpr int kMaxList = kMaxTop + 4;         // entries of a partial list (lm_score.cuh keeps a few more than asked for)
 constexpr int kVals = 16;                     // logits of a lane and chunk
 constexpr float kClamp = -200.0f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -41,8 +42,8 @@ constexpr int kNone = 0x7FFFFFFF;
 struct Part {
     float m, l, w;
     int nan;
-    float v[kMaxTop];
-    int32_t i[kMaxTop];
+    float v[kMaxList];
+    int32_t i[kMaxList];
 };
 
 struct Outs {
@@ -113,7 +114,8 @@ struct Sums {
 };
 
 // 16 logits into the running sums of a lane; NaN becomes -inf, in v too.
-__device__ __forceinline__ void fold(Sums &s, float (&v)[kVals], float c, int &nan)
+// Returns the largest.
+__device__ __forceinline__ float fold(Sums &s, float (&v)[kVals], float c, int &nan)
 {
     float mx = v[0];
 #pragma unroll
@@ -152,6 +154,7 @@ __device__ __forceinline__ void fold(Sums &s, float (&v)[kVals], float c, int &n
     }
     s.l += l0 + l1;
     s.w += w0 + w1;
+    return mx;
 }
 
 // The sums of 32 lanes: one reference for all, then plain sums in a fixed order.
@@ -491,40 +494,14 @@ __global__ void __launch_bounds__(kThreads, 4)
     }
 }
 
-// A warp per row merges its splits in order: the sums lane by lane and then
-// across the lanes, the lists as a k-way merge of 32 sorted lists at a time. The
-// given token's logit comes from z, or (z NULL) from ztok.
-template <typename E>
-__global__ void __launch_bounds__(kThreads)
-    k_logprob_join(const E *z, int64_t stride, const float *ztok, int64_t N, int splits, const Part *part, const Outs o)
+// One warp: the sums and the k best (at most 32) of a row's parts.
+__device__ __forceinline__ void join_parts(const Part *p, int n, int k, float c, int lane, Sums &s, int &nan, TopList &top)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = o.k;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-    if (row >= N)
-        return;
-    const float c = kLog2e / o.T;
-    const Part *p = part + row * splits;
-    float zt = -INFINITY;
-    if (o.logp) {
-        if (z) {
-            const int32_t t = __ldg(o.tokens + row);
-            if (t >= 0 && t < o.V)
-                zt = Load<E>::one(z + row * stride + t);
-        } else {
-            zt = __ldcg(ztok + row);
-        }
-        if (zt != zt)
-            zt = -INFINITY;
-    }
-    Sums s;
     s.clear();
-    int nan = 0;
-    TopList top;
     top.clear();
-    for (int s0 = 0; s0 < splits; s0 += 32) {
+    for (int s0 = 0; s0 < n; s0 += 32) {
         const Part *mine = p + s0 + lane;
-        const bool in = s0 + lane < splits;
+        const bool in = s0 + lane < n;
         if (in) {
             s.add(Sums{__ldcg(&mine->m), __ldcg(&mine->l), __ldcg(&mine->w)}, c);
             nan |= __ldcg(&mine->nan);
@@ -543,6 +520,32 @@ __global__ void __launch_bounds__(kThreads)
     }
     s = warp_sums(s, c);
     nan = __any_sync(0xFFFFFFFFu, nan);
+}
+
+// A warp per row merges its splits in order: the sums lane by lane and then
+// across the lanes, the lists as a k-way merge of 32 sorted lists at a time.
+template <typename E>
+__global__ void __launch_bounds__(kThreads)
+    k_logprob_join(const E *z, int64_t stride, int64_t N, int splits, const Part *part, const Outs o)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = o.k;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    if (row >= N)
+        return;
+    const float c = kLog2e / o.T;
+    float zt = -INFINITY;
+    if (o.logp) {
+        const int32_t t = __ldg(o.tokens + row);
+        if (t >= 0 && t < o.V)
+            zt = Load<E>::one(z + row * stride + t);
+        if (zt != zt)
+            zt = -INFINITY;
+    }
+    Sums s;
+    int nan = 0;
+    TopList top;
+    join_parts(part + row * splits, splits, k, c, lane, s, nan, top);
     write_row(o, row, s, top, nan, zt, lane);
 }
 

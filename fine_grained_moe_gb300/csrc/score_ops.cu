@@ -66,12 +66,12 @@ score::Outs outs(const int32_t *tokens, float *logp, float *entropy, int32_t *to
                        reinterpret_cast<int32_t *>(static_cast<char *>(ws) + ws_offsets().status)};
 }
 
-template <typename E>
-int launch_join(const E *z, int64_t stride, const float *ztok, int64_t N, int splits, const score::Part *part,
-                const score::Outs &o, cudaStream_t st)
+// A second kernel whose launch overlaps the first; it waits for the first's end itself.
+template <typename... P, typename... A>
+int launch_second(void (*kernel)(P...), int64_t ctas, cudaStream_t st, A... args)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((N + score::kWarps - 1) / score::kWarps));
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.blockDim = dim3(score::kThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -79,7 +79,7 @@ int launch_join(const E *z, int64_t stride, const float *ztok, int64_t N, int sp
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    FGM_HOST_CUDA(cudaLaunchKernelEx(&cfg, score::k_logprob_join<E>, z, stride, ztok, N, splits, part, o));
+    FGM_HOST_CUDA(cudaLaunchKernelEx(&cfg, kernel, args...));
     return FGM_OK;
 }
 
@@ -91,7 +91,9 @@ int run_logprobs(const void *z, int64_t stride, int64_t N, const score::Outs &o,
     score::k_logprobs<E><<<static_cast<unsigned>(N * splits), score::kThreads, 0, st>>>(static_cast<const E *>(z), stride,
                                                                                          splits, part, o);
     FGM_HOST_CUDA(cudaGetLastError());
-    return splits == 1 ? FGM_OK : launch_join<E>(static_cast<const E *>(z), stride, nullptr, N, splits, part, o, st);
+    return splits == 1 ? FGM_OK
+                       : launch_second(score::k_logprob_join<E>, (N + score::kWarps - 1) / score::kWarps, st,
+                                       static_cast<const E *>(z), stride, N, splits, static_cast<const score::Part *>(part), o);
 }
 
 // Word ranges of a row tile of fgm_lm_head_logprobs: the number that makes waves *
@@ -111,18 +113,24 @@ int word_splits(int64_t N, int64_t V)
     return static_cast<int>(best);
 }
 
-// The regions behind the common workspace: partial results, the given tokens' logits.
-struct LmWs {
-    size_t part, ztok, total;
-};
-
-LmWs lm_ws(int64_t N, int64_t V)
+template <int L>
+int run_lm_score(const uint16_t *emb, const uint16_t *h, score::LmArgs &a, const score::Outs &o, int sms, cudaStream_t st)
 {
-    LmWs o;
-    o.part = part_offset();
-    o.ztok = align_up(o.part + sizeof(score::Part) * static_cast<size_t>(N) * word_splits(N, V), 256);
-    o.total = align_up(o.ztok + sizeof(float) * static_cast<size_t>(N), 256);
-    return o;
+    CUtensorMap hmap, emap;
+    a.h_rows = a.N < 128 ? static_cast<int>(align_up(a.N, 8)) : 128;
+    FGM_HOST_TRY(host_hidden_map(&hmap, h, a.N, a.h_rows));
+    FGM_HOST_TRY(host_hidden_map(&emap, emb, a.V, 128));
+    static bool ready[64];                     // per device; setting it twice does no harm
+    int dev = 0;
+    FGM_HOST_CUDA(cudaGetDevice(&dev));
+    if (!ready[dev & 63]) {
+        FGM_HOST_CUDA(cudaFuncSetAttribute(score::k_lm_score<L>, cudaFuncAttributeMaxDynamicSharedMemorySize, score::kLmSmem));
+        ready[dev & 63] = true;
+    }
+    const int64_t pairs = a.items < sms / 2 ? a.items : sms / 2;
+    score::k_lm_score<L><<<static_cast<unsigned>(2 * pairs), score::kLmThreads, score::kLmSmem, st>>>(hmap, emap, a);
+    FGM_HOST_CUDA(cudaGetLastError());
+    return launch_second(score::k_lm_join<L>, a.N, st, emb, h, a, o);
 }
 
 }  // namespace
@@ -164,7 +172,7 @@ int fgm_logprobs(const void *z, int dtype, int64_t row_stride, int64_t N, int64_
 
 size_t fgm_lm_head_logprobs_workspace_bytes(int64_t N, int64_t V, int k)
 {
-    return score_sizes_ok(N, V, k) ? lm_ws(N, V).total : 0;
+    return score_sizes_ok(N, V, k) ? align_up(part_offset() + sizeof(score::Part) * 2 * static_cast<size_t>(N) * word_splits(N, V), 256) : 0;
 }
 
 int fgm_lm_head_logprobs(const uint16_t *emb, int64_t V, const uint16_t *h, int64_t N, float T, const int32_t *tokens,
@@ -177,35 +185,18 @@ int fgm_lm_head_logprobs(const uint16_t *emb, int64_t V, const uint16_t *h, int6
     FGM_HOST_TRY(host_check_ws(ws, ws_bytes, fgm_lm_head_logprobs_workspace_bytes(N, V, k)));
     int sms = 0;
     FGM_HOST_TRY(host_device_ready(&sms));
-    CUtensorMap hmap, emap;
-    FGM_HOST_TRY(host_hidden_map(&hmap, h, N));
-    FGM_HOST_TRY(host_hidden_map(&emap, emb, V));
-    const LmWs w = lm_ws(N, V);
     const score::Outs o = outs(tokens, logp, entropy, top_ids, top_logp, k, T, V, ws);
     score::LmArgs a = {};
     a.N = N;
     a.V = static_cast<int>(V);
-    a.tokens = tokens;
     a.T = T;
-    a.k = k;
     a.splits = word_splits(N, V);
     a.items = (N + score::kLmRows - 1) / score::kLmRows * a.splits;
-    a.part = reinterpret_cast<score::Part *>(static_cast<char *>(ws) + w.part);
-    a.ztok = reinterpret_cast<float *>(static_cast<char *>(ws) + w.ztok);
+    a.part = reinterpret_cast<score::Part *>(static_cast<char *>(ws) + part_offset());
     a.status = o.status;
     a.timeout_ns = host_wait_limit_ns();
-    static bool ready[64];                     // per device; setting it twice does no harm
-    int dev = 0;
-    FGM_HOST_CUDA(cudaGetDevice(&dev));
-    if (!ready[dev & 63]) {
-        FGM_HOST_CUDA(cudaFuncSetAttribute(score::k_lm_score, cudaFuncAttributeMaxDynamicSharedMemorySize, score::kLmSmem));
-        ready[dev & 63] = true;
-    }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int64_t pairs = a.items < sms / 2 ? a.items : sms / 2;
-    score::k_lm_score<<<static_cast<unsigned>(2 * pairs), score::kLmThreads, score::kLmSmem, st>>>(hmap, emap, a);
-    FGM_HOST_CUDA(cudaGetLastError());
-    return launch_join<float>(nullptr, 0, a.ztok, N, a.splits, a.part, o, st);
+    return k <= 8 ? run_lm_score<12>(emb, h, a, o, sms, st) : run_lm_score<20>(emb, h, a, o, sms, st);
 }
 
 }  // extern "C"
