@@ -8,7 +8,8 @@
 // its 128 rows and half of the words, 64 bytes per cycle and SM at the full rate
 // where one CTA on 128 x 256 would need 96.
 //  * TMA copies boxes of 128 rows x 128 bytes (64 elements of K) in the 128-byte
-//    swizzle into a 6-stage ring, the second CTA's bytes counted on the first's
+//    swizzle into a ring (6 stages; 11 for a few rows, whose copies are no larger
+//    than the rows), the second CTA's bytes counted on the first's
 //    barriers; rows past N and words past V arrive as zeros.
 //  * The first CTA's issuing warp runs M = 256, N = 256, K = 16 products into one
 //    of two accumulators (2 x 256 columns), so that the next tile's products run
@@ -40,20 +41,21 @@ namespace fgm {
 namespace score {
 
 constexpr int kLmThreads = 384;                  // copies, products, -, -, eight epilogue warps
-constexpr int kLmStages = 6;
-constexpr int kLmBox = 128 * 128;                // 128 rows x 128 bytes
-constexpr int kLmStage = 2 * kLmBox;             // rows and words
+constexpr int kLmStages = 12;                    // at most
+constexpr int kLmBox = 128 * 128;                // 128 words x 128 bytes
+constexpr int kLmBoxes = 2;                      // boxes of 64 elements of K in a stage
 constexpr int kLmWords = 256;                    // words of a tile
 constexpr int kLmRows = 256;                     // rows of a pair
-constexpr int kLmK = kH / 64;                    // stages of a tile
-constexpr int kLmSmem = kLmStages * kLmStage + 1024;
-static_assert(kH % 64 == 0, "K must split into whole stages");
+constexpr int kLmK = kH / (64 * kLmBoxes);       // stages of a tile
+constexpr int kLmSmem = 226 * 1024;
+static_assert(kH % (64 * kLmBoxes) == 0, "K must split into whole stages");
 
 struct LmArgs {
     int64_t N;
     int V;
     float T;
-    int h_rows;              // rows of a copy of hidden rows: 128, or all there are
+    int h_rows;              // rows of a copy of hidden rows: 128, or all there are rounded up to 8
+    int stages;              // of the ring: h_rows hidden rows, then 128 words
     int splits;              // word ranges
     int64_t items;           // row tiles * splits
     Part *part;              // [N][splits][2 halves of the columns]
@@ -148,7 +150,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
     uint32_t rank;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     uint8_t *dsm = dsm_raw + ((1024u - (saddr(dsm_raw) & 1023u)) & 1023u);
-    const uint32_t ring = saddr(dsm);
+    // (With few hidden rows the first operand's 128 run on into the stage's words:
+    // rows of the accumulator that nobody reads.)
+    const uint32_t ring = saddr(dsm), h_box = p.h_rows * 128, words_at = kLmBoxes * h_box,
+                   stage = words_at + kLmBoxes * kLmBox, stages = p.stages;
     const long long deadline = now_ns() + p.timeout_ns;
     const int pairs = gridDim.x / 2, pair = blockIdx.x / 2;
     const int tiles = (p.V + kLmWords - 1) / kLmWords;
@@ -220,26 +225,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
                 range(item, t0, t1);
                 // (a CTA without rows copies none; its half of the accumulator is never read)
                 const int y0 = static_cast<int>(item / p.splits) * kLmRows, y = y0 + rank * 128;
-                const uint32_t both = 2 * kLmBox + ((y0 < p.N) + (y0 + 128 < p.N)) * p.h_rows * 128;
+                const uint32_t both = kLmBoxes * (2 * kLmBox + ((y0 < p.N) + (y0 + 128 < p.N)) * h_box);
                 for (int t = t0; t < t1 && ok; ++t)
                     for (int ks = 0; ks < kLmK; ++ks, ++n) {
-                        const int slot = n % kLmStages;
-                        if (n >= kLmStages && !(ok = wait(&sh.empty[slot], n / kLmStages - 1, 30, ks)))
+                        const uint32_t slot = n % stages;
+                        if (n >= stages && !(ok = wait(&sh.empty[slot], n / stages - 1, 30, ks)))
                             break;
-                        const uint32_t bar = in_first(saddr(&sh.full[slot])), dst = ring + slot * kLmStage;
+                        const uint32_t bar = in_first(saddr(&sh.full[slot])), dst = ring + slot * stage;
                         if (rank == 0)
                             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(&sh.full[slot])),
                                          "r"(both)
                                          : "memory");
-                        if (y < p.N)
-                            lm_copy(dst, &hmap, ks * 64, y, bar);
-                        lm_copy(dst + kLmBox, &emap, ks * 64, t * kLmWords + rank * 128, bar);
+#pragma unroll
+                        for (int b = 0; b < kLmBoxes; ++b) {
+                            const int x = (ks * kLmBoxes + b) * 64;
+                            lm_copy(dst + words_at + b * kLmBox, &emap, x, t * kLmWords + rank * 128, bar);
+                            if (y < p.N)
+                                lm_copy(dst + b * h_box, &hmap, x, y, bar);
+                        }
                     }
             }
             // every issued copy lands before the pair may exit (the first CTA sees both CTAs' bytes)
             if (rank == 0)
-                for (uint32_t i = n > kLmStages ? n - kLmStages : 0; i < n; ++i)
-                    lm_drain(saddr(&sh.full[i % kLmStages]), (i / kLmStages) & 1);
+                for (uint32_t i = n > stages ? n - stages : 0; i < n; ++i)
+                    lm_drain(saddr(&sh.full[i % stages]), (i / stages) & 1);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -256,20 +265,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
                     if (tile >= 2)
                         ok = wait(&sh.tempty[buf], (tile >> 1) - 1, 31, t);
                     for (int ks = 0; ks < kLmK; ++ks, ++n) {
-                        const int slot = n % kLmStages;
-                        ok = ok && wait(&sh.full[slot], n / kLmStages, 32, ks);
+                        const uint32_t slot = n % stages;
+                        ok = ok && wait(&sh.full[slot], n / stages, 32, ks);
                         ok = __all_sync(0xFFFFFFFFu, ok);
                         if (!ok)
                             break;
                         if (lead) {
                             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                            const uint64_t a = lm_desc(ring + slot * kLmStage), b = lm_desc(ring + slot * kLmStage + kLmBox);
+                            const uint64_t a = lm_desc(ring + slot * stage), b = lm_desc(ring + slot * stage + words_at);
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
+                            for (int kk = 0; kk < 4 * kLmBoxes; ++kk)
                                 asm volatile(
                                     "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
                                     "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem + buf * kLmWords),
-                                    "l"(a + kk * 2), "l"(b + kk * 2), "r"(kIdesc), "r"(static_cast<uint32_t>((ks | kk) != 0))
+                                    "l"(a + (kk >> 2) * (h_box >> 4) + (kk & 3) * 2), "l"(b + (kk >> 2) * (kLmBox >> 4) + (kk & 3) * 2), "r"(kIdesc), "r"(static_cast<uint32_t>((ks | kk) != 0))
                                     : "memory");
                             lm_commit(&sh.empty[slot]);
                             if (ks == kLmK - 1)

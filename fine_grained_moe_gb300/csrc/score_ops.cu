@@ -1,6 +1,7 @@
 // C ABI of the log probabilities (declared in include/fgm.h): argument checks
 // and launches of logprobs.cuh.
 #include <cmath>
+#include <stdlib.h>
 
 #include "host.h"
 #include "lm_score.cuh"
@@ -96,16 +97,25 @@ int run_logprobs(const void *z, int64_t stride, int64_t N, const score::Outs &o,
                                        static_cast<const E *>(z), stride, N, splits, static_cast<const score::Part *>(part), o);
 }
 
-// Word ranges of a row tile of fgm_lm_head_logprobs: the number that makes waves *
-// (a range's tiles + 1) least, for the 76 pairs of a 152-SM part; an item's start
-// and end cost about one tile.
-int word_splits(int64_t N, int64_t V)
+constexpr int kMaxPairs = 80;                  // CTA pairs of a full sm_103 part
+
+int64_t row_tiles(int64_t N) { return (N + score::kLmRows - 1) / score::kLmRows; }
+
+// Word ranges of a row tile of fgm_lm_head_logprobs on a device that runs `pairs`
+// CTA pairs at a time: those that fill 1 to 4 waves of pairs, whichever makes
+// waves * (a range's tiles + 1) least; an item's start and end cost about a tile.
+// (The pairs that fit are fewer than half of the SMs where a GPC has an odd number
+// of them; items for half of the SMs left a short second wave: 1.00 ms on 1,021
+// rows and 330 us on 5, against the figures of lm_score.cuh.)
+int word_splits(int64_t N, int64_t V, int pairs)
 {
-    const int64_t tiles = (V + score::kLmWords - 1) / score::kLmWords, rows = (N + score::kLmRows - 1) / score::kLmRows;
+    const int64_t tiles = (V + score::kLmWords - 1) / score::kLmWords, rows = row_tiles(N);
     int64_t best = 1, cost = 0;
-    for (int64_t s = 1; s <= tiles && s <= 152; ++s) {
-        const int64_t c = (rows * s + 75) / 76 * ((tiles + s - 1) / s + 1);
-        if (s == 1 || c < cost) {
+    for (int w = 1; w <= 4; ++w) {
+        int64_t s = w * pairs / rows;
+        s = s < 1 ? 1 : s > tiles ? tiles : s;
+        const int64_t c = (rows * s + pairs - 1) / pairs * ((tiles + s - 1) / s + 1);
+        if (w == 1 || c < cost) {
             best = s;
             cost = c;
         }
@@ -113,21 +123,44 @@ int word_splits(int64_t N, int64_t V)
     return static_cast<int>(best);
 }
 
+// The most ranges that word_splits gives on any device.
+int64_t most_splits(int64_t N) { return N <= score::kLmRows ? kMaxPairs : 4 * kMaxPairs / row_tiles(N) + 1; }
+
 template <int L>
 int run_lm_score(const uint16_t *emb, const uint16_t *h, score::LmArgs &a, const score::Outs &o, int sms, cudaStream_t st)
 {
     CUtensorMap hmap, emap;
     a.h_rows = a.N < 128 ? static_cast<int>(align_up(a.N, 8)) : 128;
+    const int stage = score::kLmBoxes * (a.h_rows * 128 + score::kLmBox), fit = (score::kLmSmem - 1024) / stage;
+    a.stages = fit < score::kLmStages ? fit : score::kLmStages;
     FGM_HOST_TRY(host_hidden_map(&hmap, h, a.N, a.h_rows));
     FGM_HOST_TRY(host_hidden_map(&emap, emb, a.V, 128));
-    static bool ready[64];                     // per device; setting it twice does no harm
+    static int fit_pairs[64];                  // CTA pairs at a time, per device; finding it twice does no harm
     int dev = 0;
     FGM_HOST_CUDA(cudaGetDevice(&dev));
-    if (!ready[dev & 63]) {
+    int most = fit_pairs[dev & 63];
+    if (!most) {
         FGM_HOST_CUDA(cudaFuncSetAttribute(score::k_lm_score<L>, cudaFuncAttributeMaxDynamicSharedMemorySize, score::kLmSmem));
-        ready[dev & 63] = true;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(sms / 2 * 2);
+        cfg.blockDim = dim3(score::kLmThreads);
+        cfg.dynamicSmemBytes = score::kLmSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        FGM_HOST_CUDA(cudaOccupancyMaxActiveClusters(&most, score::k_lm_score<L>, &cfg));
+        if (most < 1)
+            return failf(FGM_ERR_DEVICE, "no CTA pair of the lm_head kernel fits this device");
+        most = most < kMaxPairs ? most : kMaxPairs;
+        fit_pairs[dev & 63] = most;
+        if (getenv("FGM_DBG")) fprintf(stderr, "pairs %d\n", most);
     }
-    const int64_t pairs = a.items < sms / 2 ? a.items : sms / 2;
+    a.splits = word_splits(a.N, a.V, most);
+    a.items = row_tiles(a.N) * a.splits;
+    const int64_t pairs = a.items < most ? a.items : most;
     score::k_lm_score<L><<<static_cast<unsigned>(2 * pairs), score::kLmThreads, score::kLmSmem, st>>>(hmap, emap, a);
     FGM_HOST_CUDA(cudaGetLastError());
     return launch_second(score::k_lm_join<L>, a.N, st, emb, h, a, o);
@@ -172,7 +205,7 @@ int fgm_logprobs(const void *z, int dtype, int64_t row_stride, int64_t N, int64_
 
 size_t fgm_lm_head_logprobs_workspace_bytes(int64_t N, int64_t V, int k)
 {
-    return score_sizes_ok(N, V, k) ? align_up(part_offset() + sizeof(score::Part) * 2 * static_cast<size_t>(N) * word_splits(N, V), 256) : 0;
+    return score_sizes_ok(N, V, k) ? align_up(part_offset() + sizeof(score::Part) * 2 * static_cast<size_t>(N) * most_splits(N), 256) : 0;
 }
 
 int fgm_lm_head_logprobs(const uint16_t *emb, int64_t V, const uint16_t *h, int64_t N, float T, const int32_t *tokens,
@@ -190,8 +223,6 @@ int fgm_lm_head_logprobs(const uint16_t *emb, int64_t V, const uint16_t *h, int6
     a.N = N;
     a.V = static_cast<int>(V);
     a.T = T;
-    a.splits = word_splits(N, V);
-    a.items = (N + score::kLmRows - 1) / score::kLmRows * a.splits;
     a.part = reinterpret_cast<score::Part *>(static_cast<char *>(ws) + part_offset());
     a.status = o.status;
     a.timeout_ns = host_wait_limit_ns();
