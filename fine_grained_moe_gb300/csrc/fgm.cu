@@ -918,6 +918,24 @@ void set_sample(fused::Params &prm, float T, const int32_t *draft, const float *
 }  // namespace
 }  // namespace fgm
 
+}  // extern "C"
+
+// Logits z [M][V] of at most 8 rows on the persistent kernel (host.h); arguments
+// checked by the caller.
+int fgm::host_lm_logits(const uint16_t *emb, int64_t V, const uint16_t *h, int M, float *z, void *ws, void *stream)
+{
+    Ws w = ws_carve(ws);
+    fused::Params prm = fused_params(fused::kModeLmHead, M, w);
+    prm.x = h;
+    prm.emb = emb;
+    prm.V = V;
+    prm.z = z;
+    prm.inv_t = 1.0f;
+    return launch_fused(prm, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" {
+
 int fgm_lm_head_sample(const uint16_t *emb, int64_t V, const uint16_t *h, int M, float T, const int32_t *draft,
                        const float *u_acc, const float *u_next, float *z, int32_t *argmax, int32_t *out,
                        void *ws, size_t ws_bytes, void *stream)

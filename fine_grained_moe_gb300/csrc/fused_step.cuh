@@ -2659,8 +2659,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_fused(const __grid_constant__ P
             }
         }
         consumer_sync();
-        if (p.z) {
-            if (is_mma)
+        if (p.z) {   // (without `out`: the logits alone)
+            if (is_mma && p.out)
                 sample_finish(p.z, p.V, M, G, p.inv_t, ws.part_val, ws.part_sum, p.draft, p.u_acc, p.u_next, arg,
                               p.out);
         } else if (tid == 0 && p.mode == kModeVerify) {

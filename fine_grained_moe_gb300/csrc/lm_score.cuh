@@ -405,59 +405,80 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
     }
 }
 
+constexpr int kJoinWarps = 4;
+
 // A CTA per row: merges its ranges, computes the largest logits and the given
-// token's again in fp32, corrects the sums and writes the row.
+// token's again in fp32, corrects the sums and writes the row. All of it is
+// latency (a few KB a row), so the warps share the parts, and a warp's words are
+// read side by side.
 template <int L>
-__global__ void __launch_bounds__(kThreads) k_lm_join(const uint16_t *emb, const uint16_t *h, const LmArgs p, const Outs o)
+__global__ void __launch_bounds__(32 * kJoinWarps) k_lm_join(const uint16_t *emb, const uint16_t *h, const LmArgs p, const Outs o)
 {
-    __shared__ float s_z[L + 1];
-    __shared__ int32_t s_i[L + 1];
+    constexpr int kMine = (L + 1 + kJoinWarps - 1) / kJoinWarps;      // words of a warp at most
+    __shared__ float s_v[kJoinWarps][L], s_z[L + 1];
+    __shared__ int32_t s_i[kJoinWarps][L], s_w[L + 1];
+    __shared__ Sums s_sum[kJoinWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t row = blockIdx.x;
     const float c = kLog2e / o.T;
-    // the hidden row, 8 elements of every 256 a lane (the first kernel does not write it)
-    constexpr int kPer = kH / 256;
-    uint4 hr[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-        hr[i] = __ldg(reinterpret_cast<const uint4 *>(h + row * kH) + i * 32 + lane);
     const int32_t tok = o.logp ? __ldg(o.tokens + row) : -1;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // a warp's share of the parts, in order
+    const int parts = p.splits * 2, p0 = parts * warp / kJoinWarps, p1 = parts * (warp + 1) / kJoinWarps;
     Sums s;
     int nan = 0;
     TopList top;
+    join_parts(p.part + row * parts + p0, p1 - p0, L, c, lane, s, nan, top);
+    if (lane == 0)
+        s_sum[warp] = s;
+    if (lane < L) {
+        s_v[warp][lane] = top.v;
+        s_i[warp][lane] = top.i;
+    }
+    nan = __syncthreads_or(nan);
     if (warp == 0) {
-        join_parts(p.part + row * p.splits * 2, p.splits * 2, L, c, lane, s, nan, top);
+        if (lane < kJoinWarps)
+            s = s_sum[lane];
+        else
+            s.clear();
+        s = warp_sums(s, c);
+        merge_lists(s_v[lane & (kJoinWarps - 1)], s_i[lane & (kJoinWarps - 1)], lane < kJoinWarps ? L : 0, L, lane, top.v, top.i);
         if (lane < L)
-            s_i[lane] = top.i;
+            s_w[lane] = top.i;
         if (lane == 0)
-            s_i[L] = tok >= 0 && tok < p.V ? tok : kNone;
+            s_w[L] = tok >= 0 && tok < p.V ? tok : kNone;
     }
     __syncthreads();
-    for (int j = warp; j <= L; j += kWarps) {
-        const int32_t w = s_i[j];
-        float z = -INFINITY;
-        if (w != kNone) {
-            uint4 er[kPer];
+    const uint4 *hr = reinterpret_cast<const uint4 *>(h + row * kH) + lane, *er[kMine];
+    float acc[kMine][2];
 #pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                er[i] = __ldg(reinterpret_cast<const uint4 *>(emb + static_cast<int64_t>(w) * kH) + i * 32 + lane);
-            float a0 = 0.0f, a1 = 0.0f;
+    for (int j = 0; j < kMine; ++j) {
+        const int32_t w = warp + j * kJoinWarps <= L ? s_w[warp + j * kJoinWarps] : kNone;
+        er[j] = reinterpret_cast<const uint4 *>(emb + static_cast<int64_t>(w == kNone ? 0 : w) * kH) + lane;
+        acc[j][0] = acc[j][1] = 0.0f;
+    }
+#pragma unroll 3
+    for (int i = 0; i < kH / 256; ++i) {
+        const uint4 x = __ldg(hr + i * 32);
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const uint32_t x[4] = {hr[i].x, hr[i].y, hr[i].z, hr[i].w}, y[4] = {er[i].x, er[i].y, er[i].z, er[i].w};
+        for (int j = 0; j < kMine; ++j) {
+            const uint4 y = __ldg(er[j] + i * 32);
+            const uint32_t ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float2 u = bf16x2_to_f32(x[q]), v = bf16x2_to_f32(y[q]);
-                    a0 = fmaf(u.x, v.x, a0);
-                    a1 = fmaf(u.y, v.y, a1);
-                }
+            for (int q = 0; q < 4; ++q) {
+                const float2 u = bf16x2_to_f32(xs[q]), v = bf16x2_to_f32(ys[q]);
+                acc[j][0] = fmaf(u.x, v.x, acc[j][0]);
+                acc[j][1] = fmaf(u.y, v.y, acc[j][1]);
             }
-            z = warp_sum(a0 + a1);
-            z = z == z ? z : -INFINITY;
         }
-        if (lane == 0)
-            s_z[j] = z;
+    }
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+        const float z = warp_sum(acc[j][0] + acc[j][1]);
+        const int at = warp + j * kJoinWarps;
+        if (lane == 0 && at <= L)
+            s_z[at] = s_w[at] != kNone && z == z ? z : -INFINITY;
     }
     __syncthreads();
     if (warp)

@@ -1,7 +1,6 @@
 // C ABI of the log probabilities (declared in include/fgm.h): argument checks
 // and launches of logprobs.cuh.
 #include <cmath>
-#include <stdlib.h>
 
 #include "host.h"
 #include "lm_score.cuh"
@@ -69,11 +68,11 @@ score::Outs outs(const int32_t *tokens, float *logp, float *entropy, int32_t *to
 
 // A second kernel whose launch overlaps the first; it waits for the first's end itself.
 template <typename... P, typename... A>
-int launch_second(void (*kernel)(P...), int64_t ctas, cudaStream_t st, A... args)
+int launch_second(void (*kernel)(P...), int64_t ctas, int threads, cudaStream_t st, A... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(score::kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -93,9 +92,11 @@ int run_logprobs(const void *z, int64_t stride, int64_t N, const score::Outs &o,
                                                                                          splits, part, o);
     FGM_HOST_CUDA(cudaGetLastError());
     return splits == 1 ? FGM_OK
-                       : launch_second(score::k_logprob_join<E>, (N + score::kWarps - 1) / score::kWarps, st,
+                       : launch_second(score::k_logprob_join<E>, (N + score::kWarps - 1) / score::kWarps, score::kThreads, st,
                                        static_cast<const E *>(z), stride, N, splits, static_cast<const score::Part *>(part), o);
 }
+
+size_t logits_bytes(int64_t N, int64_t V) { return align_up(sizeof(float) * static_cast<size_t>(N) * V, 256); }
 
 constexpr int kMaxPairs = 80;                  // CTA pairs of a full sm_103 part
 
@@ -156,14 +157,13 @@ int run_lm_score(const uint16_t *emb, const uint16_t *h, score::LmArgs &a, const
             return failf(FGM_ERR_DEVICE, "no CTA pair of the lm_head kernel fits this device");
         most = most < kMaxPairs ? most : kMaxPairs;
         fit_pairs[dev & 63] = most;
-        if (getenv("FGM_DBG")) fprintf(stderr, "pairs %d\n", most);
     }
     a.splits = word_splits(a.N, a.V, most);
     a.items = row_tiles(a.N) * a.splits;
     const int64_t pairs = a.items < most ? a.items : most;
     score::k_lm_score<L><<<static_cast<unsigned>(2 * pairs), score::kLmThreads, score::kLmSmem, st>>>(hmap, emap, a);
     FGM_HOST_CUDA(cudaGetLastError());
-    return launch_second(score::k_lm_join<L>, a.N, st, emb, h, a, o);
+    return launch_second(score::k_lm_join<L>, a.N, 32 * score::kJoinWarps, st, emb, h, a, o);
 }
 
 }  // namespace
@@ -205,7 +205,9 @@ int fgm_logprobs(const void *z, int dtype, int64_t row_stride, int64_t N, int64_
 
 size_t fgm_lm_head_logprobs_workspace_bytes(int64_t N, int64_t V, int k)
 {
-    return score_sizes_ok(N, V, k) ? align_up(part_offset() + sizeof(score::Part) * 2 * static_cast<size_t>(N) * most_splits(N), 256) : 0;
+    if (!score_sizes_ok(N, V, k))
+        return 0;
+    return N <= kMaxM ? fgm_logprobs_workspace_bytes(N, V, k) + logits_bytes(N, V) : align_up(part_offset() + sizeof(score::Part) * 2 * static_cast<size_t>(N) * most_splits(N), 256);
 }
 
 int fgm_lm_head_logprobs(const uint16_t *emb, int64_t V, const uint16_t *h, int64_t N, float T, const int32_t *tokens,
@@ -219,6 +221,13 @@ int fgm_lm_head_logprobs(const uint16_t *emb, int64_t V, const uint16_t *h, int6
     int sms = 0;
     FGM_HOST_TRY(host_device_ready(&sms));
     const score::Outs o = outs(tokens, logp, entropy, top_ids, top_logp, k, T, V, ws);
+    if (N <= kMaxM) {
+        // The persistent lm_head kernel, whose whole-row copies stream the embedding at 6.5 TB/s where the pair
+        // kernel's boxes reach 5.2, with its logits (0.4 % of the bytes) scored by k_logprobs.
+        char *z = static_cast<char *>(ws) + fgm_logprobs_workspace_bytes(N, V, k);
+        FGM_HOST_TRY(host_lm_logits(emb, V, h, static_cast<int>(N), reinterpret_cast<float *>(z), ws, stream));
+        return run_logprobs<float>(z, V, N, o, ws, static_cast<cudaStream_t>(stream));
+    }
     score::LmArgs a = {};
     a.N = N;
     a.V = static_cast<int>(V);
