@@ -11,8 +11,9 @@
 //  * Work is a list of units, two 64-token blocks of one (sequence, kv head),
 //    in that order. CTA c of G (one per SM) takes units [U c / G, U (c + 1) / G),
 //    whatever sequences they belong to: ragged batches, one long sequence and
-//    windows are balanced to a unit. Lengths are read on the device, so the
-//    launch does not depend on them and can be captured.
+//    windows are balanced to a unit. (Each (sequence, head) counts 256 / D units
+//    more, what starting and finishing it costs.) Lengths are read on the device,
+//    so the launch does not depend on them and can be captured.
 //  * A producer warp streams a unit's K and V with TMA tensor copies (rows of
 //    64 bytes in the 64-byte swizzle) into two rings that fill the shared memory.
 //  * Two issuing warps run tcgen05.mma kind::f8f6f4 with the cache as the first
@@ -26,7 +27,9 @@
 //  * Sixteen softmax warps read S^T (a thread is a token and a fourth of the rows),
 //    exponentiate and write P^T back to shared memory as the next operand. S
 //    and P have two buffers: the products of the next unit run under the
-//    softmax of this one.
+//    softmax of this one, and its scores are read while this one's
+//    probabilities are rounded.
+//  * A helper warp prepares the query terms of the next (sequence, head).
 //
 // Precision. The second operands are split into two E4M3 terms in columns of
 // their own, hi and lo = c (x - hi), added in fp32 as hi + lo / c. Queries
@@ -51,13 +54,15 @@
 
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "kv_append.cuh"
 
 namespace fgm {
 namespace kv {
 
 constexpr int kSoftWarps = 16;                         // four per lane quarter, a fourth of the rows each
-constexpr int kAttnThreads = 32 * (4 + kSoftWarps);    // copies, scores, outputs, (none), softmax
+constexpr int kAttnThreads = 32 * (4 + kSoftWarps);    // copies, scores, outputs, queries, softmax
 constexpr int kTile = 2 * kBlock;                      // tokens of a unit
 constexpr int kMaxRing = 8;                            // stages of the K and of the V ring at most
 constexpr int kMetas = 16;                             // units' scales kept: ring depth + 2 and more
@@ -86,7 +91,7 @@ struct AttnArgs {
     int4 *rec;               // [G] {b, h, last CTA, -} of the segment that starts in a CTA and goes on, b = -1: none
     int rows;                // rows of the products: M * G rounded up to an instantiation
     int k_ring, v_ring;      // stages
-    int min_units;           // units a CTA takes at least
+    int q_ring;              // query buffers: 2, or 1 where they are large
     long long timeout_ns;
 };
 
@@ -98,8 +103,8 @@ __host__ __device__ inline int64_t partial_floats(int rows, int D) { return stat
 __host__ __device__ inline int query_bytes(int rows, int D) { return 2 * rows * D; }
 __host__ __device__ inline int prob_bytes(int rows) { return 2 * rows * kTile; }
 
-struct Meta {                // a unit: block scales, first token, which of its blocks exist
-    float ks[2], vs[2];
+struct Meta {                // a unit: K's block scales, log2 and inverse of V's, first token, which of its blocks exist
+    float ks[2], lv[2], iv[2];
     int tok0;
     int have;
 };
@@ -107,14 +112,15 @@ struct Meta {                // a unit: block scales, first token, which of its 
 struct AttnShared {
     unsigned long long kfull[kMaxRing], kempty[kMaxRing], vfull[kMaxRing], vempty[kMaxRing];
     unsigned long long mfull[kMetas];
-    unsigned long long sfull[2], sfree[2], pfull[2], pdone[2], qfull, drained[2];
+    unsigned long long sfull[2], sfree[2], pfull[2], pdone[2], qfull[2], qempty[2], drained[2];
     Meta meta[kMetas];
-    float qf[FGM_ATTN_MAX_ROWS];                       // score of a unit product: 2^e scale log2(e)
+    float qf[2][FGM_ATTN_MAX_ROWS];                    // score of a unit product: 2^e scale log2(e)
     float mx[4][FGM_ATTN_MAX_ROWS];                    // per lane quarter: a unit's maxima
     float ls[4][FGM_ATTN_MAX_ROWS];                    // and the segment's sums
     float m[FGM_ATTN_MAX_ROWS], l[FGM_ATTN_MAX_ROWS];
-    int2 lim[FGM_ATTN_MAX_ROWS];                       // tokens [x, y) that a row sees
+    int2 lim[2][FGM_ATTN_MAX_ROWS];                       // tokens [x, y) that a row sees
     int orow[FGM_ATTN_MAX_ROWS];                       // a row's place among the (token, q head) of its sequence
+    int units[2];                                      // the CTA's units: [first, last + 1)
     uint32_t tmem;
     int abort;
 };
@@ -304,6 +310,11 @@ __device__ __forceinline__ float2 e4m3_values(uint32_t w)
     return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w), __NV_E4M3)));
 }
 
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t v)
+{
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
 __device__ __forceinline__ void sts8(uint32_t a, uint32_t v)
 {
     asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(v) : "memory");
@@ -314,16 +325,92 @@ struct Cursor {
     int b, h, u, n, first, blocks;    // sequence, kv head, unit of the segment, its units, first block and blocks
 };
 
+// Query terms of one (sequence, head), whose first row is at `q`, by `warps`
+// warps, of which this is number w: rows w, w + warps, ...; `batch` rows' loads at
+// a time. qs, qf, lims are shared-memory addresses.
+template <int D, int R, int kBatch>
+__device__ __forceinline__ void build_queries(const uint16_t *q, int64_t stride, int M, int G, int window, int len, float scale,
+                                              int w, int warps, int lane, uint32_t qs, uint32_t qf, uint32_t lims)
+{
+    constexpr int kN = 2 * R, kE = (D + 127) / 128;
+    const int rows = M * G;
+#pragma unroll 1
+    for (int r0 = w; r0 < R; r0 += warps * kBatch) {
+        uint2 x[kBatch][kE];
+        int at[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int r = r0 + i * warps;
+            at[i] = r / G;
+            const uint16_t *src = q + at[i] * stride + (r - at[i] * G) * D;
+#pragma unroll
+            for (int e = 0; e < kE; ++e) {
+                const int d = (e * 32 + lane) * 4;
+                x[i][e] = make_uint2(0, 0);
+                if (r < rows && d < D)
+                    x[i][e] = __ldg(reinterpret_cast<const uint2 *>(src + d));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int r = r0 + i * warps;
+            if (r >= R)
+                break;
+            unsigned amax = 0;
+#pragma unroll
+            for (int e = 0; e < kE; ++e)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const unsigned a = ((k < 2 ? x[i][e].x : x[i][e].y) >> (16 * (k & 1))) & 0x7FFFu;
+                    amax = max(amax, a < 0x7F80u ? a : 0u);
+                }
+            amax = __reduce_max_sync(0xFFFFFFFFu, amax);
+            // 2^ex with the largest element in (224, 448] 2^ex; no lower than 2^-120
+            const unsigned u = amax << 16;
+            const int ex = max(static_cast<int>(u >> 23) + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0) - 8, 7);
+            const float up = __uint_as_float(static_cast<unsigned>(254 - ex) << 23);
+            if (lane == 0) {
+                int lo = 0, hi = 0;
+                if (r < rows)
+                    row_range(len, M, window, at[i], lo, hi);
+                sts32(lims + r * 8, lo);
+                sts32(lims + r * 8 + 4, hi);
+                sts32(qf + r * 4, __float_as_uint(__uint_as_float(static_cast<unsigned>(ex) << 23) * (scale * kLog2e)));
+            }
+#pragma unroll
+            for (int e = 0; e < kE; ++e) {
+                const int d = (e * 32 + lane) * 4;
+                if (d >= D)
+                    break;
+                const float2 v0 = bf16x2_to_f32(x[i][e].x), v1 = bf16x2_to_f32(x[i][e].y);
+                auto fin = [&](float v) { return fabsf(v) < INFINITY ? v * up : __int_as_float(0x7FC00000); };
+                const float y[4] = {fin(v0.x), fin(v0.y), fin(v1.x), fin(v1.y)};
+                const uint32_t hi = to_e4m3x4(y[0], y[1], y[2], y[3]);
+                float z[4];
+                e4m3x4_to_f32(hi, z);
+                const uint32_t lo = to_e4m3x4(16.0f * (y[0] - z[0]), 16.0f * (y[1] - z[1]), 16.0f * (y[2] - z[2]),
+                                              16.0f * (y[3] - z[3]));
+                sts32(qs + (d >> 6) * (kN * 64) + at64(r, d & 63), hi);
+                sts32(qs + (d >> 6) * (kN * 64) + at64(R + r, d & 63), lo);
+            }
+        }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // D: head dim; R: rows of the products (8, 16, 32, 48 or 64).
 template <int D, int R>
 __global__ void __launch_bounds__(kAttnThreads, 1)
-    k_attn(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const AttnArgs p)
+    k_attn(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+           const __grid_constant__ AttnArgs p)
 {
     constexpr int kSlices = D / 64, kN = 2 * R;
     constexpr int kSide = kTile * D;                             // bytes of a unit's K or V
     constexpr int kMTiles = D == 256 ? 2 : 1;                    // 128-lane tiles of O^T
     constexpr int kNR = R / 4;                                   // rows of a softmax thread
+    constexpr bool kAhead = R <= 32;                             // the next unit's scores fit the registers beside this one's
     constexpr int kCh = kNR < 4 ? kNR : 4;                       // accumulator columns read at a time
+    constexpr int kG = kNR % 8 == 0 ? 8 : kCh;                   // rows rescaled at a time
     constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(kN >> 3) << 17) | (8u << 24);   // fp32 += E4M3 x E4M3, M = 128
     constexpr uint32_t kOCol = 2 * kN;                           // S buffers first, then O tiles
     constexpr uint32_t kUsed = 2 * kN + kMTiles * kN;
@@ -333,11 +420,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int heads = p.c.heads;
     uint8_t *dsm = dsm_raw + ((1024u - (saddr(dsm_raw) & 1023u)) & 1023u);
-    uint8_t *qs = dsm, *ps = qs + query_bytes(R, D), *kring = ps + 2 * prob_bytes(R);
+    uint8_t *qs = dsm, *ps = qs + p.q_ring * query_bytes(R, D), *kring = ps + 2 * prob_bytes(R);
     uint8_t *vring = kring + p.k_ring * kSide;
     // (for D = 64 the 128-row first operand of O^T runs 4 KB past a block's V: one more block's room behind the ring)
     int *cum = reinterpret_cast<int *>(vring + p.v_ring * kSide + (D == 64 ? kBlock * D : 0));   // [B + 1] units before each sequence
     int *lens = cum + p.B + 1;                                   // [B] clamped lengths
+    int *used = lens + p.B;                                      // [B + 1] (sequence, head)s with units before each sequence
+    constexpr int kCost = 256 / D;                               // a (sequence, head)'s start and end, in units
     const long long deadline = now_ns() + p.timeout_ns;
 
     if (tid == 0) {
@@ -355,7 +444,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             bar_init(&sh.pfull[i], kSoftWarps);
             bar_init(&sh.pdone[i], 1);
         }
-        bar_init(&sh.qfull, kSoftWarps);
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&sh.qfull[i], 1);
+            bar_init(&sh.qempty[i], 1 + kSoftWarps);
+        }
         bar_init(&sh.drained[0], 1);
         bar_init(&sh.drained[1], 1);
         sh.abort = 0;
@@ -370,7 +462,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         for (int r = lane; r < R; r += 32)
             sh.orow[r] = r / p.G * p.Hq + r % p.G;
     if (warp == 0) {
-        int base = 0;
+        int base = 0, ubase = 0;
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             const int b = b0 + lane;
             int n = 0, first;
@@ -386,12 +478,41 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (lane >= o)
                     inc += v;
             }
-            if (b < p.B)
+            const unsigned some = __ballot_sync(0xFFFFFFFFu, n > 0);
+            if (b < p.B) {
                 cum[b] = base + inc - n;
+                used[b] = ubase + __popc(some & ((1u << lane) - 1)) * heads;
+            }
             base += __shfl_sync(0xFFFFFFFFu, inc, 31);
+            ubase += __popc(some) * heads;
         }
-        if (lane == 0)
+        if (lane == 0) {
             cum[p.B] = base;
+            used[p.B] = ubase;
+        }
+        __syncwarp();
+        // Places: units, and kCost places before those of each (sequence, head).
+        // CTA c of G takes the units at places [P c / G, P (c + 1) / G): lanes 0 and
+        // 1 count the units below either end.
+        const int P = base + ubase * kCost, G = min(static_cast<int>(gridDim.x), max(P, 1)), c = blockIdx.x + lane;
+        if (lane < 2) {
+            const int place = P / G * c + P % G * c / G;      // floor(P c / G) in 32 bits
+            int units = base;
+            if (place < P && blockIdx.x < G) {
+                int a = 0, z = p.B;
+                while (z - a > 1) {
+                    const int mid = (a + z) >> 1;
+                    if (cum[mid] + used[mid] * kCost <= place)
+                        a = mid;
+                    else
+                        z = mid;
+                }
+                const int n = (cum[a + 1] - cum[a]) / heads;
+                const int r = place - cum[a] - used[a] * kCost, h = r / (n + kCost);
+                units = cum[a] + h * n + max(r - h * (n + kCost) - kCost, 0);
+            }
+            sh.units[lane] = units;
+        }
     }
     before_sync();
     __syncthreads();
@@ -399,12 +520,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     asm volatile("griddepcontrol.launch_dependents;");
     const uint32_t tmem = sh.tmem;
 
-    const int64_t U = cum[p.B];
-    const int64_t by_min = (U + p.min_units - 1) / p.min_units;
-    const int64_t G = by_min < gridDim.x ? (by_min > 0 ? by_min : 1) : gridDim.x;   // CTAs that take units
-    const int u0 = blockIdx.x < G ? static_cast<int>(U * blockIdx.x / G) : 0;
-    const int u1 = blockIdx.x < G ? static_cast<int>(U * (blockIdx.x + 1) / G) : 0;
-    const int n_units = u1 - u0;
+    const int n_places = cum[p.B] + used[p.B] * kCost, G = min(static_cast<int>(gridDim.x), max(n_places, 1));
+    const int u0 = sh.units[0], u1 = sh.units[1], n_units = u1 - u0;
 
     auto locate = [&](int u) -> Cursor {
         int a = 0, z = p.B;                        // cum[a] <= u < cum[z]: ends on a sequence that has units
@@ -426,6 +543,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     };
     auto wait = [&](unsigned long long *bar, int phase, int site, int index) -> bool {
         return bar_wait(saddr(bar), phase & 1, &sh.abort, deadline, p.status, site, index);
+    };
+
+    auto queries = [&](auto batch, const Cursor &cu, int w, int warps, int slot) {
+        build_queries<D, R, decltype(batch)::value>(p.q + static_cast<int64_t>(cu.b) * p.M * p.stride + cu.h * p.G * D, p.stride,
+                                                    p.M, p.G, p.window, lens[cu.b], p.scale, w, warps, lane,
+                                                    saddr(qs + slot * query_bytes(R, D)), saddr(sh.qf[slot]),
+                                                    saddr(sh.lim[slot]));
     };
 
     if (warp == 0) {
@@ -506,7 +630,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const int t0 = __shfl_sync(0xFFFFFFFFu, tok0, i);
                 if (lane == 0 && ok) {
                     // (entry u - 16 has been read: the ring is at most 8 deep and the softmax 2 behind the products)
-                    sh.meta[u % kMetas] = Meta{{ks[0], ks[1]}, {vs[0], vs[1]}, t0, (at[0] >= 0) | (at[1] >= 0) << 1};
+                    sh.meta[u % kMetas] = Meta{{ks[0], ks[1]}, {log2f(vs[0]), log2f(vs[1])}, {1.0f / vs[0], 1.0f / vs[1]}, t0,
+                                                 (at[0] >= 0) | (at[1] >= 0) << 1};
                     bar_arrive(saddr(&sh.mfull[u % kMetas]));
                 }
                 ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
@@ -528,11 +653,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const bool lead = elect_one();
         bool ok = true;
         int seg = 0;
-        const uint64_t b0 = desc64(saddr(qs));
         for (int done = 0; done < n_units && ok; ++seg) {
+            const int qslot = seg % p.q_ring;
+            const uint64_t b0 = desc64(saddr(qs + qslot * query_bytes(R, D)));
             const Cursor cu = locate(u0 + done);
             const int n = min(cu.n - cu.u, n_units - done);
-            ok = wait(&sh.qfull, seg, 17, seg);
+            ok = wait(&sh.qfull[qslot], seg / p.q_ring, 17, seg);
             for (int u = done; u < done + n && ok; ++u) {
                 const int slot = u % p.k_ring;
                 if (u >= 2)
@@ -549,6 +675,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                b0 + (((k >> 1) * (kN * 64) + (k & 1) * 32) >> 4), kIdesc, k != 0);
                     commit(&sh.kempty[slot]);
                     commit(&sh.sfull[u & 1]);
+                    if (u == done + n - 1)
+                        commit(&sh.qempty[qslot]);
                 }
                 __syncwarp();
             }
@@ -597,6 +725,26 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             bar_drain(saddr(&sh.drained[1]), 0);
         }
         __syncwarp();
+    } else if (warp == 3) {
+        // ------------------------------------------------------------ queries of the second segment and on
+        bool ok = true;
+        int seg = 0;
+        for (int done = 0; done < n_units && ok; ++seg) {
+            const Cursor cu = locate(u0 + done);
+            done += min(cu.n - cu.u, n_units - done);
+            if (seg == 0)
+                continue;
+            const int qslot = seg % p.q_ring;
+            if (seg >= p.q_ring)
+                ok = wait(&sh.qempty[qslot], seg / p.q_ring - 1, 26, seg);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok)
+                break;
+            queries(std::integral_constant<int, R / 8 < 4 ? R / 8 : 4>{}, cu, 0, 1, qslot);
+            __syncwarp();
+            if (lane == 0)
+                bar_arrive(saddr(&sh.qfull[qslot]));
+        }
     } else if (warp >= 4) {
         // ------------------------------------------------------------ softmax
         const int w = warp - 4, quarter = warp & 3, part4 = w >> 2, stid = tid - 128;
@@ -619,66 +767,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         p.lse[row0 + i] = -INFINITY;
             }
 
-        for (int done = 0; done < n_units;) {
+        int seg = 0;
+        for (int done = 0; done < n_units; ++seg) {
             const Cursor cu = locate(u0 + done);
             const int n = min(cu.n - cu.u, n_units - done);
-            const int len = lens[cu.b];
-
-            // query terms of this (sequence, head): a warp takes every 8th row
-            for (int r = w; r < R; r += kSoftWarps) {
-                const bool live = r < rows;
-                const int ri = r / p.G;
-                const uint16_t *src = p.q + (static_cast<int64_t>(cu.b) * p.M + ri) * p.stride + (cu.h * p.G + r - ri * p.G) * D;
-                constexpr int kE = (D + 127) / 128;
-                uint2 x[kE];
-                unsigned amax = 0;
-#pragma unroll
-                for (int e = 0; e < kE; ++e) {
-                    const int d = (e * 32 + lane) * 4;
-                    x[e] = make_uint2(0, 0);
-                    if (live && d < D)
-                        x[e] = *reinterpret_cast<const uint2 *>(src + d);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const unsigned a = ((k < 2 ? x[e].x : x[e].y) >> (16 * (k & 1))) & 0x7FFFu;
-                        amax = max(amax, a < 0x7F80u ? a : 0u);
-                    }
-                }
-                amax = __reduce_max_sync(0xFFFFFFFFu, amax);
-                // 2^ex with the largest element in (224, 448] 2^ex; no lower than 2^-120
-                const unsigned u = amax << 16;
-                const int ex = max(static_cast<int>(u >> 23) + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0) - 8, 7);
-                const float up = __uint_as_float(static_cast<unsigned>(254 - ex) << 23);
-                if (lane == 0) {
-                    int2 lim = make_int2(0, 0);
-                    if (live)
-                        row_range(len, p.M, p.window, ri, lim.x, lim.y);
-                    sh.lim[r] = lim;
-                    sh.qf[r] = __uint_as_float(static_cast<unsigned>(ex) << 23) * (p.scale * kLog2e);
-                }
-#pragma unroll
-                for (int e = 0; e < kE; ++e) {
-                    const int d = (e * 32 + lane) * 4;
-                    if (d >= D)
-                        break;
-                    const float2 a = bf16x2_to_f32(x[e].x), b = bf16x2_to_f32(x[e].y);
-                    auto fin = [&](float v) { return fabsf(v) < INFINITY ? v * up : __int_as_float(0x7FC00000); };
-                    const float y[4] = {fin(a.x), fin(a.y), fin(b.x), fin(b.y)};
-                    const uint32_t hi = to_e4m3x4(y[0], y[1], y[2], y[3]);
-                    float z[4];
-                    e4m3x4_to_f32(hi, z);
-                    const uint32_t lo = to_e4m3x4(16.0f * (y[0] - z[0]), 16.0f * (y[1] - z[1]), 16.0f * (y[2] - z[2]),
-                                                  16.0f * (y[3] - z[3]));
-                    uint8_t *at = qs + (d >> 6) * (kN * 64);
-                    *reinterpret_cast<uint32_t *>(at + at64(r, d & 63)) = hi;
-                    *reinterpret_cast<uint32_t *>(at + at64(R + r, d & 63)) = lo;
-                }
+            const int len = lens[cu.b], qslot = seg % p.q_ring;
+            const float *qf = sh.qf[qslot];
+            if (seg == 0) {
+                queries(std::integral_constant<int, (R + kSoftWarps - 1) / kSoftWarps>{}, cu, w, kSoftWarps, 0);
+                asm volatile("bar.sync 1, 512;" ::: "memory");
+                if (stid == 0)
+                    bar_arrive(saddr(&sh.qfull[0]));
+            } else if (alive) {
+                alive = wait(&sh.qfull[qslot], seg / p.q_ring, 27, seg);
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            before_sync();                         // the last segment's accumulator has been read, too
-            asm volatile("bar.sync 1, 512;" ::: "memory");
-            if (lane == 0)
-                bar_arrive(saddr(&sh.qfull));
 
             float m[kNR], l[kNR];
 #pragma unroll
@@ -691,39 +793,47 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             row_range(len, p.M, p.window, p.M - 1, lo_max, hi_max);
             bool any_pv = false;                   // a product went into the accumulator
 
-            for (int i = 0; i < n; ++i) {
-                const int u = done + i;
+            float s[2 * kNR];                      // a unit's scores: hi, then lo
+            auto arrived = [&](int u) {            // its scores and scales are there
                 if (alive)
                     alive = wait(&sh.mfull[u % kMetas], u / kMetas, 20, u) && wait(&sh.sfull[u & 1], u >> 1, 21, u);
                 alive = __all_sync(0xFFFFFFFFu, alive);
                 after_sync();
-                const Meta me = sh.meta[u % kMetas];
-                float s[2 * kNR];                  // hi, then lo
+            };
+            auto read = [&](int u, float *v) {
 #pragma unroll
                 for (int r = 0; r < kNR; r += kCh) {
-                    tmem_ld<kCh>(tmem + lanes + (u & 1) * kN + n0 + r, s + r);
-                    tmem_ld<kCh>(tmem + lanes + (u & 1) * kN + R + n0 + r, s + kNR + r);
+                    tmem_ld<kCh>(tmem + lanes + (u & 1) * kN + n0 + r, v + r);
+                    tmem_ld<kCh>(tmem + lanes + (u & 1) * kN + R + n0 + r, v + kNR + r);
                 }
-                const float ks = blk ? me.ks[1] : me.ks[0], vs = blk ? me.vs[1] : me.vs[0];
-                const float lv = log2f(vs), ivs = 1.0f / vs;
-                const int tok = me.tok0 + tl;
-                const bool here = me.have >> blk & 1;
-                const bool edge = me.tok0 + kTile > hi_min || me.tok0 < lo_max || me.have != 3;
-                tmem_wait_ld(s);
+            };
+            auto taken = [&](int u) {              // read: the buffer is free
                 before_sync();
                 __syncwarp();
                 if (lane == 0)
                     bar_arrive(saddr(&sh.sfree[u & 1]));
+            };
+            arrived(done);
+            read(done, s);
+            tmem_wait_ld(s);
+            taken(done);
+            for (int i = 0; i < n; ++i) {
+                const int u = done + i;
+                const Meta me = sh.meta[u % kMetas];
+                const float ks = blk ? me.ks[1] : me.ks[0], lv = blk ? me.lv[1] : me.lv[0], ivs = blk ? me.iv[1] : me.iv[0];
+                const int tok = me.tok0 + tl;
+                const bool here = me.have >> blk & 1;
+                const bool edge = me.tok0 + kTile > hi_min || me.tok0 < lo_max || me.have != 3;
 
                 // scores in powers of two, with V's scale on top
                 bool over = false;
 #pragma unroll
                 for (int r = 0; r < kNR; ++r)
-                    s[r] = fmaf(fmaf(s[kNR + r], 0.0625f, s[r]), sh.qf[n0 + r] * ks, lv);
+                    s[r] = fmaf(fmaf(s[kNR + r], 0.0625f, s[r]), qf[n0 + r] * ks, lv);
                 if (edge) {
 #pragma unroll
                     for (int r = 0; r < kNR; ++r) {
-                        const int2 lim = sh.lim[n0 + r];
+                        const int2 lim = sh.lim[qslot][n0 + r];
                         s[r] = here && tok >= lim.x && tok < lim.y ? s[r] : -INFINITY;
                     }
                 }
@@ -768,29 +878,46 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                         for (int t = 0; t < kMTiles; ++t)
 #pragma unroll
-                            for (int r = 0; r < kNR; r += kCh) {
-                                const uint32_t a = tmem + lanes + kOCol + t * kN + n0 + r;
-                                float o[2 * kCh];
-                                tmem_ld<kCh>(a, o);
-                                tmem_ld<kCh>(a + R, o + kCh);
+                            for (int r0 = 0; r0 < kNR; r0 += kG) {
+                                const uint32_t a = tmem + lanes + kOCol + t * kN + n0 + r0;
+                                float o[2 * kG];
+#pragma unroll
+                                for (int r = 0; r < kG; r += kCh) {
+                                    tmem_ld<kCh>(a + r, o + r);
+                                    tmem_ld<kCh>(a + R + r, o + kG + r);
+                                }
                                 tmem_wait_ld(o);
 #pragma unroll
-                                for (int k = 0; k < kCh; ++k) {
-                                    o[k] *= c[r + k];
-                                    o[kCh + k] *= c[r + k];
+                                for (int r = 0; r < kG; ++r) {
+                                    o[r] *= c[r0 + r];
+                                    o[kG + r] *= c[r0 + r];
                                 }
-                                tmem_st<kCh>(a, o);
-                                tmem_st<kCh>(a + R, o + kCh);
+#pragma unroll
+                                for (int r = 0; r < kG; r += kCh) {
+                                    tmem_st<kCh>(a + r, o + r);
+                                    tmem_st<kCh>(a + R + r, o + kG + r);
+                                }
                             }
                         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                     }
                     // (sh.mx is written again only after every reader has passed the next vote)
                 }
                 any_pv |= me.have != 0;
+                // the next unit's scores, if they are there, are read while this one's probabilities are made
+                float next[kAhead ? 2 * kNR : 1];
+                const bool more = i + 1 < n;
+                const bool early = kAhead && more &&
+                                   __all_sync(0xFFFFFFFFu, bar_try(saddr(&sh.sfull[(u + 1) & 1]), ((u + 1) >> 1) & 1) &&
+                                                               bar_try(saddr(&sh.mfull[(u + 1) % kMetas]), ((u + 1) / kMetas) & 1));
                 // the buffer's last product is done
                 if (alive && u >= 2)
                     alive = wait(&sh.pdone[u & 1], (u >> 1) - 1, 23, u);
                 alive = __all_sync(0xFFFFFFFFu, alive);
+                if constexpr (kAhead)
+                    if (early) {
+                        after_sync();
+                        read(u + 1, next);
+                    }
                 const int kt = tl & 63;
                 const uint32_t pt = saddr(ps + (u & 1) * prob_bytes(R) + blk * (kN * 64)) + (kt & 15);
 #pragma unroll
@@ -822,10 +949,26 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                if constexpr (kAhead)
+                    if (early) {
+                        tmem_wait_ld(next);
+#pragma unroll
+                        for (int r = 0; r < 2 * kNR; ++r)
+                            s[r] = next[r];
+                    }
                 before_sync();
                 __syncwarp();
-                if (lane == 0)
+                if (lane == 0) {
                     bar_arrive(saddr(&sh.pfull[u & 1]));
+                    if (early)
+                        bar_arrive(saddr(&sh.sfree[(u + 1) & 1]));
+                }
+                if (more && !early) {
+                    arrived(u + 1);
+                    read(u + 1, s);
+                    tmem_wait_ld(s);
+                    taken(u + 1);
+                }
             }
 
             // -------------------------------------------------------- end of the segment
@@ -882,11 +1025,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
             }
             if (starts && !ends) {
-                // the CTA that holds the segment's last unit: the largest c with U c / G <= unit
-                const int64_t last = u0 + done - cu.u + cu.n - 1;
-                rec = make_int4(cu.b, cu.h, static_cast<int>(((last + 1) * G + U - 1) / U - 1), 0);
+                // the CTA that holds the segment's last unit, at this place: the largest c with floor(P c / G) <= place
+                const int place = u0 + done - cu.u + cu.n - 1 + (used[cu.b] + cu.h + 1) * kCost;
+                rec = make_int4(cu.b, cu.h, static_cast<int>((static_cast<int64_t>(place + 1) * G - 1) / n_places), 0);
             }
-            asm volatile("bar.sync 1, 512;" ::: "memory");     // sh.m, sh.l, sh.qf are free again
+            if (lane == 0)
+                bar_arrive(saddr(&sh.qempty[qslot]));
+            asm volatile("bar.sync 1, 512;" ::: "memory");     // sh.m and sh.l are free again
             done += n;
         }
         if (stid == 0)

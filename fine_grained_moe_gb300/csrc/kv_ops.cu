@@ -86,8 +86,9 @@ int launch_attn_t(kv::AttnArgs &a, int sms, cudaStream_t st)
     const int grid = sms < kv::kMaxGrid ? sms : kv::kMaxGrid;
     // what is left of the shared memory goes to the rings, V's first: its stage is freed last
     constexpr size_t side = static_cast<size_t>(kv::kTile) * D;
-    const size_t fixed = kv::query_bytes(R, D) + 2 * kv::prob_bytes(R) + (D == 64 ? kv::kBlock * D : 0) +
-                         align_up(sizeof(int) * (2 * static_cast<size_t>(a.B) + 1), 128) + 1024;
+    a.q_ring = kv::query_bytes(R, D) <= 16384 ? 2 : 1;
+    const size_t fixed = a.q_ring * kv::query_bytes(R, D) + 2 * kv::prob_bytes(R) + (D == 64 ? kv::kBlock * D : 0) +
+                         align_up(sizeof(int) * (3 * static_cast<size_t>(a.B) + 2), 128) + 1024;
     const size_t most = kv::kSmemMax - sizeof(kv::AttnShared) - 256;
     const int stages = static_cast<int>((most - fixed) / side);
     a.v_ring = (stages + 1) / 2 < kv::kMaxRing ? (stages + 1) / 2 : kv::kMaxRing;
@@ -193,8 +194,8 @@ int fgm_attn_fwd(const fgm_kv_cache *cache, const uint16_t *q, int64_t token_str
     if (!out || !is_aligned(out, 16) || !is_aligned(lse, 4))
         return failf(FGM_ERR_INVALID_ARG, "out NULL or not 16-byte aligned, or lse not 4-byte aligned");
     FGM_HOST_TRY(host_check_ws(ws, ws_bytes, fgm_attn_workspace_bytes(B, M, n_q_heads, cache->n_kv_heads, cache->head_dim)));
-    if (static_cast<int64_t>(B) * max_blocks * cache->n_kv_heads > 0x7FFFFFFFLL)
-        return failf(FGM_ERR_INVALID_ARG, "B * max_blocks * n_kv_heads = %lld above 2^31 - 1",
+    if (static_cast<int64_t>(B) * max_blocks * cache->n_kv_heads > (1LL << 30))
+        return failf(FGM_ERR_INVALID_ARG, "B * max_blocks * n_kv_heads = %lld above 2^30",
                      (long long)B * max_blocks * cache->n_kv_heads);
     if (cache->n_blocks * cache->n_kv_heads > 0x7FFFFFFFLL / cache->head_dim)
         return failf(FGM_ERR_INVALID_ARG, "cache of %lld blocks: n_blocks * n_kv_heads * head_dim above 2^31 - 1",
@@ -221,7 +222,6 @@ int fgm_attn_fwd(const fgm_kv_cache *cache, const uint16_t *q, int64_t token_str
     a.part = reinterpret_cast<float *>(static_cast<char *>(ws) + o.part);
     a.rec = reinterpret_cast<int4 *>(static_cast<char *>(ws) + o.rec);
     a.rows = attn_rows(M * a.G);
-    a.min_units = 1;
     a.timeout_ns = host_wait_limit_ns();
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     switch (cache->head_dim) {
