@@ -117,7 +117,7 @@ struct AttnShared {
     float qf[2][FGM_ATTN_MAX_ROWS];                    // score of a unit product: 2^e scale log2(e)
     float mx[4][FGM_ATTN_MAX_ROWS];                    // per lane quarter: a unit's maxima
     float ls[4][FGM_ATTN_MAX_ROWS];                    // and the segment's sums
-    float m[FGM_ATTN_MAX_ROWS], l[FGM_ATTN_MAX_ROWS];
+    float m[FGM_ATTN_MAX_ROWS], l[FGM_ATTN_MAX_ROWS], inv[FGM_ATTN_MAX_ROWS];
     int2 lim[2][FGM_ATTN_MAX_ROWS];                       // tokens [x, y) that a row sees
     int orow[FGM_ATTN_MAX_ROWS];                       // a row's place among the (token, q head) of its sequence
     int units[2];                                      // the CTA's units: [first, last + 1)
@@ -292,11 +292,14 @@ __device__ __forceinline__ void tmem_wait_ld(float (&v)[N])
         asm volatile("" : "+f"(v[i]));
 }
 
-__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap *map, int row, uint32_t bar)
+// (Evict-first in L2: a cache is read once a step, and what every launch needs
+// again, its code above all, stays.)
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap *map, int row, uint32_t bar, uint64_t policy)
 {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(bar)
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3}], [%4], "
+        "%5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(bar), "l"(policy)
         : "memory");
 }
 
@@ -584,6 +587,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
         }
+        uint64_t policy;
+        asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
         bool ok = true;
         int k_issued = 0, v_issued = 0;
         look(lane);
@@ -610,7 +615,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                                 for (int c = 0; c < kSlices; ++c)
                                     tma_rows(dst + c * (kTile * 64) + k * (kBlock * 64), &kmap,
-                                             static_cast<int>(at[k] * D) + c * kBlock, bar);
+                                             static_cast<int>(at[k] * D) + c * kBlock, bar, policy);
                         k_issued = u + 1;
                         if (u >= p.v_ring)
                             ok = wait(&sh.vempty[sv], u / p.v_ring - 1, 14, u);
@@ -620,7 +625,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
                         for (int k = 0; k < 2; ++k)
                             if (at[k] >= 0)
-                                tma_rows(dst + k * (kBlock * D), &vmap, static_cast<int>(at[k] * D), bar);
+                                tma_rows(dst + k * (kBlock * D), &vmap, static_cast<int>(at[k] * D), bar, policy);
                         v_issued = u + 1;
                     }
                 }
@@ -981,8 +986,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     sh.m[n0 + r] = m[r];
             }
             asm volatile("bar.sync 1, 512;" ::: "memory");
-            if (stid < R)
-                sh.l[stid] = (sh.ls[0][stid] + sh.ls[1][stid]) + (sh.ls[2][stid] + sh.ls[3][stid]);
+            if (stid < R) {
+                const float ls = (sh.ls[0][stid] + sh.ls[1][stid]) + (sh.ls[2][stid] + sh.ls[3][stid]);
+                sh.l[stid] = ls;
+                sh.inv[stid] = ls == 0.0f ? 0.0f : 1.0f / ls;
+            }
             asm volatile("bar.sync 1, 512;" ::: "memory");
             const int last_u = done + n - 1;
             if (alive)
@@ -1006,12 +1014,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     tmem_wait_ld(o);
 #pragma unroll
                     for (int k = 0; k < kCh; ++k) {
-                        const float ls = sh.l[r + k];
-                        const float v = ls == 0.0f ? 0.0f : fmaf(o[kCh + k], 1.0f / 32.0f, o[k]);
+                        const float inv = sh.inv[r + k];
+                        const float v = inv == 0.0f ? 0.0f : fmaf(o[kCh + k], 1.0f / 32.0f, o[k]);
                         if (!whole)
                             part[(r + k) * D + d] = v;
                         else if (r + k < rows)
-                            p.out[(row0 + sh.orow[r + k]) * D + d] = f32_to_bf16(ls == 0.0f ? 0.0f : v / ls);
+                            p.out[(row0 + sh.orow[r + k]) * D + d] = f32_to_bf16(v * inv);
                     }
                 }
             }
