@@ -610,13 +610,21 @@ class KVCache:
         return c
 
 
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the same in a tenth of the time, where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
 def _call(device: torch.device, stream, body):
     """Runs body(stream address) with ``device`` and the stream current, so that
     workspaces and outputs made inside belong to that stream."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
         if torch.cuda.current_device() == device.index:
-            return body(stream.cuda_stream)
+            return body(_raw_stream(device.index))
+        stream = torch.cuda.current_stream(device)
     elif stream.device != device:
         raise FgmError(f"the stream is on {stream.device}, the tensors on {device}")
     with torch.cuda.stream(stream):
@@ -723,9 +731,10 @@ def _score_outs(N: int, k: int, tokens, entropy: bool, out: LogProbs | None, dev
     if not 0 <= k <= MAX_TOP:
         raise FgmError(f"k = {k} outside [0, {MAX_TOP}]")
     if out is None:
-        f = torch.empty((2 + k, N) if k else (2, N), dtype=_F32, device=dev)      # one allocation for the fp32 ones
-        return LogProbs(None if tokens is None else f[0], f[1] if entropy else None,
-                        torch.empty((N, k), dtype=_I32, device=dev) if k else None, f[2:].view(N, k) if k else None)
+        return LogProbs(None if tokens is None else torch.empty(N, dtype=_F32, device=dev),
+                        torch.empty(N, dtype=_F32, device=dev) if entropy else None,
+                        torch.empty((N, k), dtype=_I32, device=dev) if k else None,
+                        torch.empty((N, k), dtype=_F32, device=dev) if k else None)
     for name, t, shape, dt, want in (("logp", out.logp, (N,), _F32, tokens is not None), ("entropy", out.entropy, (N,), _F32, entropy),
                                      ("top_ids", out.top_ids, (N, k), _I32, k > 0), ("top_logp", out.top_logp, (N, k), _F32, k > 0)):
         if want != (t is not None):

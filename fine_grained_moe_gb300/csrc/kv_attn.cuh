@@ -65,7 +65,7 @@ constexpr int kSoftWarps = 16;                         // four per lane quarter,
 constexpr int kAttnThreads = 32 * (4 + kSoftWarps);    // copies, scores, outputs, queries, softmax
 constexpr int kTile = 2 * kBlock;                      // tokens of a unit
 constexpr int kMaxRing = 8;                            // stages of the K and of the V ring at most
-constexpr int kMetas = 16;                             // units' scales kept: ring depth + 2 and more
+constexpr int kMetas = 64;                             // units' scales kept, in two halves
 constexpr int kMaxGrid = 160;                          // CTAs at most: the SMs of a full sm_103 part
 constexpr float kLowest = -1.0e30f;                    // stands for the maximum of nothing
 constexpr float kLift = 5.0f;                          // probabilities enter the product times 2^5
@@ -111,7 +111,7 @@ struct Meta {                // a unit: K's block scales, log2 and inverse of V'
 
 struct AttnShared {
     unsigned long long kfull[kMaxRing], kempty[kMaxRing], vfull[kMaxRing], vempty[kMaxRing];
-    unsigned long long mfull[kMetas];
+    unsigned long long mfull[2];
     unsigned long long sfull[2], sfree[2], pfull[2], pdone[2], qfull[2], qempty[2], drained[2];
     Meta meta[kMetas];
     float qf[2][FGM_ATTN_MAX_ROWS];                    // score of a unit product: 2^e scale log2(e)
@@ -439,9 +439,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             bar_init(&sh.vfull[i], 1);
             bar_init(&sh.vempty[i], 1);
         }
-        for (int i = 0; i < kMetas; ++i)
-            bar_init(&sh.mfull[i], 1);
         for (int i = 0; i < 2; ++i) {
+            bar_init(&sh.mfull[i], 1);
             bar_init(&sh.sfull[i], 1);
             bar_init(&sh.sfree[i], kSoftWarps);
             bar_init(&sh.pfull[i], kSoftWarps);
@@ -557,12 +556,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------ copies
-        // Lane i looks up unit 32 k + i (block table and scales) a round ahead.
-        int64_t at_n[2];
+        // Lane i looks up unit 32 k + i (block table and scales) a round ahead; the
+        // round's scales are published together once its first copies are out.
+        int row_n[2], tok_n = 0;                   // first 64-byte row of a block's K and V, -1: none
         float ks_n[2], vs_n[2];
-        int tok_n = 0;
         auto look = [&](int i) {
-            at_n[0] = at_n[1] = -1;
+            row_n[0] = row_n[1] = -1;
             ks_n[0] = ks_n[1] = vs_n[0] = vs_n[1] = 1.0f;
             if (i >= n_units)
                 return;
@@ -575,9 +574,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     break;
                 const int64_t ph = phys_block(p.table, cu.b, j + k, p.max_blocks, p.c.n_blocks);
                 if (ph >= 0) {
-                    at_n[k] = ph * heads + cu.h;
-                    ks_n[k] = __ldg(p.c.k_s + at_n[k]);
-                    vs_n[k] = __ldg(p.c.v_s + at_n[k]);
+                    const int at = static_cast<int>(ph) * heads + cu.h;
+                    row_n[k] = at * D;
+                    ks_n[k] = __ldg(p.c.k_s + at);
+                    vs_n[k] = __ldg(p.c.v_s + at);
                 } else {
                     atomicOr(p.status, FGM_STATUS_BAD_BLOCK);
                 }
@@ -591,53 +591,60 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
         bool ok = true;
         int k_issued = 0, v_issued = 0;
+        int sk = 0, k_turn = 0, sv = 0, v_turn = 0;      // stages and the rings' turns
         look(lane);
         for (int r = 0; r < n_units && ok; r += 32) {
-            const int64_t a0 = at_n[0], a1 = at_n[1];
-            const float k0 = ks_n[0], k1 = ks_n[1], s0 = vs_n[0], s1 = vs_n[1];
-            const int tok0 = tok_n;
+            const int r0 = row_n[0], r1 = row_n[1], m = min(32, n_units - r), tok0 = tok_n;
+            const float ks0 = ks_n[0], ks1 = ks_n[1], vs0 = vs_n[0], vs1 = vs_n[1];
             if (r + 32 < n_units)
                 look(r + 32 + lane);
-            const int m = min(32, n_units - r);
             for (int i = 0; i < m && ok; ++i) {
                 const int u = r + i;
-                const int64_t at[2] = {__shfl_sync(0xFFFFFFFFu, a0, i), __shfl_sync(0xFFFFFFFFu, a1, i)};
+                const int row[2] = {__shfl_sync(0xFFFFFFFFu, r0, i), __shfl_sync(0xFFFFFFFFu, r1, i)};
                 if (lane == 0) {
-                    const uint32_t bytes = ((at[0] >= 0) + (at[1] >= 0)) * (kBlock * D);
-                    const int sk = u % p.k_ring, sv = u % p.v_ring;
-                    if (u >= p.k_ring)
-                        ok = wait(&sh.kempty[sk], u / p.k_ring - 1, 13, u);
+                    const uint32_t bytes = ((row[0] >= 0) + (row[1] >= 0)) * (kBlock * D);
+                    if (k_turn > 0)
+                        ok = wait(&sh.kempty[sk], k_turn - 1, 13, u);
                     if (ok) {
-                        const uint32_t bar = saddr(&sh.kfull[sk]), dst = saddr(kring + sk * kSide);
+                        const uint32_t bar = saddr(&sh.kfull[sk]), dst = saddr(kring) + sk * kSide;
                         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+#pragma unroll
                         for (int k = 0; k < 2; ++k)
-                            if (at[k] >= 0)
+                            if (row[k] >= 0)
 #pragma unroll
                                 for (int c = 0; c < kSlices; ++c)
-                                    tma_rows(dst + c * (kTile * 64) + k * (kBlock * 64), &kmap,
-                                             static_cast<int>(at[k] * D) + c * kBlock, bar, policy);
+                                    tma_rows(dst + c * (kTile * 64) + k * (kBlock * 64), &kmap, row[k] + c * kBlock, bar, policy);
                         k_issued = u + 1;
-                        if (u >= p.v_ring)
-                            ok = wait(&sh.vempty[sv], u / p.v_ring - 1, 14, u);
+                        if (v_turn > 0)
+                            ok = wait(&sh.vempty[sv], v_turn - 1, 14, u);
                     }
                     if (ok) {
-                        const uint32_t bar = saddr(&sh.vfull[sv]), dst = saddr(vring + sv * kSide);
+                        const uint32_t bar = saddr(&sh.vfull[sv]), dst = saddr(vring) + sv * kSide;
                         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+#pragma unroll
                         for (int k = 0; k < 2; ++k)
-                            if (at[k] >= 0)
-                                tma_rows(dst + k * (kBlock * D), &vmap, static_cast<int>(at[k] * D), bar, policy);
+                            if (row[k] >= 0)
+                                tma_rows(dst + k * (kBlock * D), &vmap, row[k], bar, policy);
                         v_issued = u + 1;
                     }
                 }
-                // the scales last: the first units' copies are on their way before they arrive
-                const float ks[2] = {__shfl_sync(0xFFFFFFFFu, k0, i), __shfl_sync(0xFFFFFFFFu, k1, i)};
-                const float vs[2] = {__shfl_sync(0xFFFFFFFFu, s0, i), __shfl_sync(0xFFFFFFFFu, s1, i)};
-                const int t0 = __shfl_sync(0xFFFFFFFFu, tok0, i);
-                if (lane == 0 && ok) {
-                    // (entry u - 16 has been read: the ring is at most 8 deep and the softmax 2 behind the products)
-                    sh.meta[u % kMetas] = Meta{{ks[0], ks[1]}, {log2f(vs[0]), log2f(vs[1])}, {1.0f / vs[0], 1.0f / vs[1]}, t0,
-                                                 (at[0] >= 0) | (at[1] >= 0) << 1};
-                    bar_arrive(saddr(&sh.mfull[u % kMetas]));
+                if (++sk == p.k_ring) {
+                    sk = 0;
+                    ++k_turn;
+                }
+                if (++sv == p.v_ring) {
+                    sv = 0;
+                    ++v_turn;
+                }
+                if (i == 0) {
+                    // (The half's last round was read long ago: its units are 33 and more behind this one, the
+                    // rings at most 8 deep and the softmax 3 units behind the scores.)
+                    if (lane < m)
+                        sh.meta[(r + lane) & (kMetas - 1)] =
+                            Meta{{ks0, ks1}, {log2f(vs0), log2f(vs1)}, {1.0f / vs0, 1.0f / vs1}, tok0, (r0 >= 0) | (r1 >= 0) << 1};
+                    __syncwarp();
+                    if (lane == 0)
+                        bar_arrive(saddr(&sh.mfull[(r >> 5) & 1]));
                 }
                 ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
             }
@@ -657,7 +664,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // to 120 cycles, two threads two.)
         const bool lead = elect_one();
         bool ok = true;
-        int seg = 0;
+        int seg = 0, slot = 0, turn = 0;
         for (int done = 0; done < n_units && ok; ++seg) {
             const int qslot = seg % p.q_ring;
             const uint64_t b0 = desc64(saddr(qs + qslot * query_bytes(R, D)));
@@ -665,10 +672,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int n = min(cu.n - cu.u, n_units - done);
             ok = wait(&sh.qfull[qslot], seg / p.q_ring, 17, seg);
             for (int u = done; u < done + n && ok; ++u) {
-                const int slot = u % p.k_ring;
                 if (u >= 2)
                     ok = wait(&sh.sfree[u & 1], (u >> 1) - 1, 15, u);
-                ok = ok && wait(&sh.kfull[slot], u / p.k_ring, 16, u);
+                ok = ok && wait(&sh.kfull[slot], turn, 16, u);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (ok && lead) {
                     after_sync();
@@ -684,6 +690,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         commit(&sh.qempty[qslot]);
                 }
                 __syncwarp();
+                if (++slot == p.k_ring) {
+                    slot = 0;
+                    ++turn;
+                }
             }
             done += n;
         }
@@ -697,15 +707,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // ------------------------------------------------------------ outputs
         const bool lead = elect_one();
         bool ok = true;
+        int slot = 0, turn = 0;
         for (int done = 0; done < n_units && ok;) {
             const Cursor cu = locate(u0 + done);
             const int n = min(cu.n - cu.u, n_units - done);
             bool add = false;
             for (int u = done; u < done + n && ok; ++u) {
-                const int slot = u % p.v_ring;
-                ok = wait(&sh.vfull[slot], u / p.v_ring, 18, u) && wait(&sh.pfull[u & 1], u >> 1, 19, u);
+                ok = wait(&sh.vfull[slot], turn, 18, u) && wait(&sh.pfull[u & 1], u >> 1, 19, u);
                 ok = __all_sync(0xFFFFFFFFu, ok);
-                const int have = sh.meta[u % kMetas].have;
+                const int have = sh.meta[u & (kMetas - 1)].have;
                 if (ok && lead) {
                     after_sync();
                     const uint64_t a0 = desc64(saddr(vring + slot * kSide)), b0 = desc64(saddr(ps + (u & 1) * prob_bytes(R)));
@@ -722,6 +732,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     commit(&sh.pdone[u & 1]);
                 }
                 __syncwarp();
+                if (++slot == p.v_ring) {
+                    slot = 0;
+                    ++turn;
+                }
             }
             done += n;
         }
@@ -759,6 +773,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int rows = p.M * p.G;
         const int n0 = part4 * kNR;                // the thread's rows: n0 .. n0 + kNR - 1
         bool alive = true;
+        int scales = -1;                           // the round whose scales are known to be there
         int4 rec = make_int4(-1, 0, 0, 0);
 
         // sequences without a token: zero rows
@@ -800,8 +815,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
             float s[2 * kNR];                      // a unit's scores: hi, then lo
             auto arrived = [&](int u) {            // its scores and scales are there
+                if (alive && (u >> 5) != scales) {
+                    alive = wait(&sh.mfull[(u >> 5) & 1], u >> 6, 20, u);
+                    scales = u >> 5;
+                }
                 if (alive)
-                    alive = wait(&sh.mfull[u % kMetas], u / kMetas, 20, u) && wait(&sh.sfull[u & 1], u >> 1, 21, u);
+                    alive = wait(&sh.sfull[u & 1], u >> 1, 21, u);
                 alive = __all_sync(0xFFFFFFFFu, alive);
                 after_sync();
             };
@@ -824,7 +843,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             taken(done);
             for (int i = 0; i < n; ++i) {
                 const int u = done + i;
-                const Meta me = sh.meta[u % kMetas];
+                const Meta me = sh.meta[u & (kMetas - 1)];
                 const float ks = blk ? me.ks[1] : me.ks[0], lv = blk ? me.lv[1] : me.lv[0], ivs = blk ? me.iv[1] : me.iv[0];
                 const int tok = me.tok0 + tl;
                 const bool here = me.have >> blk & 1;
@@ -911,9 +930,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 // the next unit's scores, if they are there, are read while this one's probabilities are made
                 float next[kAhead ? 2 * kNR : 1];
                 const bool more = i + 1 < n;
-                const bool early = kAhead && more &&
-                                   __all_sync(0xFFFFFFFFu, bar_try(saddr(&sh.sfull[(u + 1) & 1]), ((u + 1) >> 1) & 1) &&
-                                                               bar_try(saddr(&sh.mfull[(u + 1) % kMetas]), ((u + 1) / kMetas) & 1));
+                const bool early = kAhead && more && (u + 1) >> 5 == scales &&
+                                   __all_sync(0xFFFFFFFFu, bar_try(saddr(&sh.sfull[(u + 1) & 1]), ((u + 1) >> 1) & 1));
                 // the buffer's last product is done
                 if (alive && u >= 2)
                     alive = wait(&sh.pdone[u & 1], (u >> 1) - 1, 23, u);

@@ -43,11 +43,18 @@ int check_scores(int64_t N, int64_t V, float T, const int32_t *tokens, int k, co
 // least. 1,013 rows of 100 KB: one split 28 us, four 51 us (measured); 600 rows
 // of 1 MB: one; 5 rows of 1 MB: 32. A split has 8,192 logits at least. A function
 // of the sizes alone, so that results do not depend on the device.
+int64_t most_row_splits(int64_t N, int64_t V)
+{
+    const int64_t by_grid = 8 * 608 / N + 1, by_size = V / 8192;
+    const int64_t s = by_grid < by_size ? by_grid : by_size;
+    return s < 1 ? 1 : s > 128 ? 128 : s;
+}
+
 int row_splits(int64_t N, int64_t V, int64_t elem)
 {
-    const int64_t most = V / 8192;
+    const int64_t most = most_row_splits(N, V);
     int64_t best = 1, cost = 0;
-    for (int64_t s = 1; s == 1 || (s <= most && s <= 128); ++s) {
+    for (int64_t s = 1; s <= most; ++s) {
         const int64_t c = (N * s + 607) / 608 * (56 * 1024 + V * elem / s);
         if (s == 1 || c < cost) {
             best = s;
@@ -177,7 +184,7 @@ size_t fgm_logprobs_workspace_bytes(int64_t N, int64_t V, int k)
 {
     if (!score_sizes_ok(N, V, k))
         return 0;
-    const int s4 = row_splits(N, V, 4), s2 = row_splits(N, V, 2), s = s4 > s2 ? s4 : s2;
+    const int64_t s = most_row_splits(N, V);
     return align_up(part_offset() + (s == 1 ? 0 : sizeof(score::Part) * static_cast<size_t>(N) * s), 256);
 }
 
