@@ -759,7 +759,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok)
                 break;
-            queries(std::integral_constant<int, R / 8 < 4 ? R / 8 : 4>{}, cu, 0, 1, qslot);
+            queries(std::integral_constant<int, 8>{}, cu, 0, 1, qslot);      // (eight rows of loads in flight)
             __syncwarp();
             if (lane == 0)
                 bar_arrive(saddr(&sh.qfull[qslot]));
