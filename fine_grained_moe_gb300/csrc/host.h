@@ -47,6 +47,25 @@ inline int failf(int code, const char *fmt, ...)
 
 inline bool is_aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// Launches a kernel that may start while the one before it in the stream ends:
+// it waits for that end itself (griddepcontrol.wait) before it touches memory.
+template <typename... P, typename... A>
+int launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    FGM_HOST_CUDA(cudaLaunchKernelEx(&cfg, kernel, args...));
+    return FGM_OK;
+}
+
 // A workspace of at least `need` bytes.
 inline int host_check_ws(const void *ws, size_t ws_bytes, size_t need)
 {

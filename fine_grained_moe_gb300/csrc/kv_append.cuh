@@ -113,6 +113,8 @@ __global__ void __launch_bounds__(Append<D>::kThreads) k_kv_append(const AppendA
     __shared__ float smax[kThreads / 32];
     const int tid = threadIdx.x, h = blockIdx.y >> 1, b = blockIdx.z;
     const bool is_v = blockIdx.y & 1;
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int len0 = __ldg(p.lens + b);
     const int len = clamp_len(len0, p.max_blocks, p.status, tid == 0 && blockIdx.x == 0 && blockIdx.y == 0);
     // the call's tokens are positions [start, len); start counts from the length as given

@@ -460,6 +460,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == 2)
         for (int r = lane; r < R; r += 32)
             sh.orow[r] = r / p.G * p.Hq + r % p.G;
@@ -1071,40 +1072,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
 }
 
-// Adds up the partial segments of every (sequence, kv head) that spans CTAs, in
-// CTA order. Items are (segment, row), dealt to the CTAs in turn; a thread owns
-// four output elements of every kLanes-th partial, and the lanes meet in shared
-// memory, also in order.
+// Adds up the partial segments of the (sequence, kv head) that starts in CTA
+// blockIdx.x of the first kernel and goes on, in CTA order: rows blockIdx.y,
+// blockIdx.y + gridDim.y, ... A thread owns four output elements of every
+// kLanes-th partial, and the lanes meet in shared memory, also in order.
 template <int D>
-__global__ void __launch_bounds__(256) k_attn_join(const AttnArgs p, int ctas)
+__global__ void __launch_bounds__(256) k_attn_join(const AttnArgs p)
 {
     constexpr int kCols = D / 4, kLanes = 256 / kCols;
     __shared__ float4 acc[kLanes][kCols];
     __shared__ float w[kMaxGrid], sm[8], sl[8];
-    __shared__ int list[kMaxGrid], n_list;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (warp == 0) {
-        int n = 0;
-        for (int c0 = 0; c0 < ctas; c0 += 32) {
-            const bool on = c0 + lane < ctas && __ldcg(p.rec + c0 + lane).x >= 0;
-            const unsigned bits = __ballot_sync(0xFFFFFFFFu, on);
-            if (on)
-                list[n + __popc(bits & ((1u << lane) - 1))] = c0 + lane;
-            n += __popc(bits);
-        }
-        if (lane == 0)
-            n_list = n;
-    }
-    __syncthreads();
-    const int R = p.M * p.G, rows = p.rows;
+    const int4 rec = __ldcg(p.rec + blockIdx.x);
+    if (rec.x < 0)
+        return;
+    const int R = p.M * p.G, rows = p.rows, c0 = blockIdx.x, n = rec.z - c0 + 1;
     const int64_t pf = partial_floats(p.rows, D);
-    for (int item = blockIdx.x; item < n_list * R; item += gridDim.x) {
-        const int c0 = list[item / R], r = item % R;
-        const int4 rec = __ldcg(p.rec + c0);
-        const int n = rec.z - c0 + 1;
-        // partial i: the first CTA's second slot, then the others' first slots
-        auto part = [&](int i) { return p.part + ((c0 + i) * 2 + (i == 0 ? 1 : 0)) * pf; };
+    // partial i: the first CTA's second slot, then the others' first slots
+    auto part = [&](int i) { return p.part + ((c0 + i) * 2 + (i == 0 ? 1 : 0)) * pf; };
+    for (int r = blockIdx.y; r < R; r += gridDim.y) {
         float m = kLowest, l = 0.0f;
         if (tid < n) {
             m = __ldcg(part(tid) + rows * D + r);

@@ -57,9 +57,9 @@ kv::Cache device_cache(const fgm_kv_cache *c)
 }
 
 template <int D>
-void launch_append(const kv::AppendArgs &a, dim3 grid, cudaStream_t st)
+int launch_append(const kv::AppendArgs &a, dim3 grid, cudaStream_t st)
 {
-    kv::k_kv_append<D><<<grid, kv::Append<D>::kThreads, 0, st>>>(a);
+    return launch_overlapped(kv::k_kv_append<D>, grid, kv::Append<D>::kThreads, 0, st, a);
 }
 
 // Rows of the products: the instantiations. Padding costs softmax work only (the
@@ -106,20 +106,8 @@ int launch_attn_t(kv::AttnArgs &a, int sms, cudaStream_t st)
                                            static_cast<int>(most)));
         ready[dev & 63] = true;
     }
-    kv::k_attn<D, R><<<grid, kv::kAttnThreads, bytes, st>>>(kmap, vmap, a);
-    FGM_HOST_CUDA(cudaGetLastError());
-    // the join's launch overlaps the attention; it waits for its end itself
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * grid);
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    FGM_HOST_CUDA(cudaLaunchKernelEx(&cfg, kv::k_attn_join<D>, a, grid));
-    return FGM_OK;
+    FGM_HOST_TRY(launch_overlapped(kv::k_attn<D, R>, dim3(grid), kv::kAttnThreads, bytes, st, kmap, vmap, a));
+    return launch_overlapped(kv::k_attn_join<D>, dim3(grid, a.M * a.G < 16 ? a.M * a.G : 16), 256, 0, st, a);
 }
 
 template <int D>
@@ -157,12 +145,10 @@ int fgm_kv_append(const fgm_kv_cache *cache, const uint16_t *k, const uint16_t *
     const dim3 grid((N + FGM_KV_BLOCK - 2) / FGM_KV_BLOCK + 1, 2 * cache->n_kv_heads, B);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     switch (cache->head_dim) {
-    case 64: launch_append<64>(a, grid, st); break;
-    case 128: launch_append<128>(a, grid, st); break;
-    default: launch_append<256>(a, grid, st); break;
+    case 64: return launch_append<64>(a, grid, st);
+    case 128: return launch_append<128>(a, grid, st);
+    default: return launch_append<256>(a, grid, st);
     }
-    FGM_HOST_CUDA(cudaGetLastError());
-    return FGM_OK;
 }
 
 size_t fgm_attn_workspace_bytes(int B, int M, int n_q_heads, int n_kv_heads, int head_dim)

@@ -179,6 +179,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     __syncthreads();
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -421,8 +422,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_lm_join(const uint16_t *emb
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t row = blockIdx.x;
     const float c = kLog2e / o.T;
-    const int32_t tok = o.logp ? __ldg(o.tokens + row) : -1;
+    asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int32_t tok = o.logp ? __ldg(o.tokens + row) : -1;
     // a warp's share of the parts, in order
     const int parts = p.splits * 2, p0 = parts * warp / kJoinWarps, p1 = parts * (warp + 1) / kJoinWarps;
     Sums s;

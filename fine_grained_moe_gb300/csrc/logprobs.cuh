@@ -326,6 +326,8 @@ __global__ void __launch_bounds__(kThreads, 4)
     __shared__ float s_v[kWarps][kMaxTop];
     __shared__ int32_t s_i[kWarps][kMaxTop];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, k = o.k;
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t row = blockIdx.x / splits;
     const int split = static_cast<int>(blockIdx.x - row * splits);
     const E *zr = z + row * stride;
@@ -528,6 +530,7 @@ template <typename E>
 __global__ void __launch_bounds__(kThreads)
     k_logprob_join(const E *z, int64_t stride, int64_t N, int splits, const Part *part, const Outs o)
 {
+    asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = o.k;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + warp;

@@ -73,34 +73,18 @@ score::Outs outs(const int32_t *tokens, float *logp, float *entropy, int32_t *to
                        reinterpret_cast<int32_t *>(static_cast<char *>(ws) + ws_offsets().status)};
 }
 
-// A second kernel whose launch overlaps the first; it waits for the first's end itself.
-template <typename... P, typename... A>
-int launch_second(void (*kernel)(P...), int64_t ctas, int threads, cudaStream_t st, A... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(threads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    FGM_HOST_CUDA(cudaLaunchKernelEx(&cfg, kernel, args...));
-    return FGM_OK;
-}
-
 template <typename E>
 int run_logprobs(const void *z, int64_t stride, int64_t N, const score::Outs &o, void *ws, cudaStream_t st)
 {
     const int splits = row_splits(N, o.V, sizeof(E));
     score::Part *part = reinterpret_cast<score::Part *>(static_cast<char *>(ws) + part_offset());
-    score::k_logprobs<E><<<static_cast<unsigned>(N * splits), score::kThreads, 0, st>>>(static_cast<const E *>(z), stride,
-                                                                                         splits, part, o);
-    FGM_HOST_CUDA(cudaGetLastError());
-    return splits == 1 ? FGM_OK
-                       : launch_second(score::k_logprob_join<E>, (N + score::kWarps - 1) / score::kWarps, score::kThreads, st,
-                                       static_cast<const E *>(z), stride, N, splits, static_cast<const score::Part *>(part), o);
+    const E *zp = static_cast<const E *>(z);
+    FGM_HOST_TRY(launch_overlapped(score::k_logprobs<E>, dim3(static_cast<unsigned>(N * splits)), score::kThreads, 0, st, zp,
+                                   stride, splits, part, o));
+    if (splits == 1)
+        return FGM_OK;
+    return launch_overlapped(score::k_logprob_join<E>, dim3(static_cast<unsigned>((N + score::kWarps - 1) / score::kWarps)),
+                             score::kThreads, 0, st, zp, stride, N, splits, static_cast<const score::Part *>(part), o);
 }
 
 size_t logits_bytes(int64_t N, int64_t V) { return align_up(sizeof(float) * static_cast<size_t>(N) * V, 256); }
@@ -168,9 +152,9 @@ int run_lm_score(const uint16_t *emb, const uint16_t *h, score::LmArgs &a, const
     a.splits = word_splits(a.N, a.V, most);
     a.items = row_tiles(a.N) * a.splits;
     const int64_t pairs = a.items < most ? a.items : most;
-    score::k_lm_score<L><<<static_cast<unsigned>(2 * pairs), score::kLmThreads, score::kLmSmem, st>>>(hmap, emap, a);
-    FGM_HOST_CUDA(cudaGetLastError());
-    return launch_second(score::k_lm_join<L>, a.N, 32 * score::kJoinWarps, st, emb, h, a, o);
+    FGM_HOST_TRY(launch_overlapped(score::k_lm_score<L>, dim3(static_cast<unsigned>(2 * pairs)), score::kLmThreads,
+                                   score::kLmSmem, st, hmap, emap, a));
+    return launch_overlapped(score::k_lm_join<L>, dim3(static_cast<unsigned>(a.N)), 32 * score::kJoinWarps, 0, st, emb, h, a, o);
 }
 
 }  // namespace
