@@ -11,11 +11,13 @@
 //  * Work is a list of units, two 64-token blocks of one (sequence, kv head),
 //    in that order. CTA c of G (one per SM) takes units [U c / G, U (c + 1) / G),
 //    whatever sequences they belong to: ragged batches, one long sequence and
-//    windows are balanced to a unit. (Each (sequence, head) counts 256 / D units
+//    windows are balanced to a unit. (Each (sequence, head) counts 512 / D units
 //    more, what starting and finishing it costs.) Lengths are read on the device,
 //    so the launch does not depend on them and can be captured.
-//  * A producer warp streams a unit's K and V with TMA tensor copies (rows of
-//    64 bytes in the 64-byte swizzle) into two rings that fill the shared memory.
+//  * Two warps stream K and V with TMA tensor copies (rows of 64 bytes in the
+//    64-byte swizzle) into a ring each, which fill the shared memory. (One warp
+//    for both let the next keys wait for a value stage: 67 us a pass at 256K
+//    tokens and 40 rows, where the rings are 2 and 3 deep.)
 //  * Two issuing warps run tcgen05.mma kind::f8f6f4 with the cache as the first
 //    operand: S^T = K Q^T (128 tokens x rows, K = D) and O^T += V^T P^T (D x rows,
 //    K = tokens; V lies token-contiguous in the cache for this). The rows are
@@ -29,7 +31,7 @@
 //    and P have two buffers: the products of the next unit run under the
 //    softmax of this one, and its scores are read while this one's
 //    probabilities are rounded.
-//  * A helper warp prepares the query terms of the next (sequence, head).
+//  * The values' warp also prepares the query terms of the next (sequence, head).
 //
 // Precision. The second operands are split into two E4M3 terms in columns of
 // their own, hi and lo = c (x - hi), added in fp32 as hi + lo / c. Queries
@@ -62,7 +64,7 @@ namespace fgm {
 namespace kv {
 
 constexpr int kSoftWarps = 16;                         // four per lane quarter, a fourth of the rows each
-constexpr int kAttnThreads = 32 * (4 + kSoftWarps);    // copies, scores, outputs, queries, softmax
+constexpr int kAttnThreads = 32 * (4 + kSoftWarps);    // keys, scores, outputs, values and queries, softmax
 constexpr int kTile = 2 * kBlock;                      // tokens of a unit
 constexpr int kMaxRing = 8;                            // stages of the K and of the V ring at most
 constexpr int kMetas = 64;                             // units' scales kept, in two halves
@@ -88,7 +90,9 @@ struct AttnArgs {
     float *lse;
     int32_t *status;
     float *part;             // [G][2] partial segments: O [rows][D], m [rows], l [rows]
-    int4 *rec;               // [G] {b, h, last CTA, -} of the segment that starts in a CTA and goes on, b = -1: none
+    int4 *rec;               // {b, h, first CTA, last CTA} of each (sequence, head) that spans CTAs, b = -1: none; by
+                             // (sequence, head) or, where those are more than the CTAs, by the CTA it starts in
+    int n_rec;
     int rows;                // rows of the products: M * G rounded up to an instantiation
     int k_ring, v_ring;      // stages
     int q_ring;              // query buffers: 2, or 1 where they are large
@@ -103,10 +107,10 @@ __host__ __device__ inline int64_t partial_floats(int rows, int D) { return stat
 __host__ __device__ inline int query_bytes(int rows, int D) { return 2 * rows * D; }
 __host__ __device__ inline int prob_bytes(int rows) { return 2 * rows * kTile; }
 
-struct Meta {                // a unit: K's block scales, log2 and inverse of V's, first token, which of its blocks exist
+struct Meta {                // a unit: K's block scales, log2 and inverse of V's, first token, its blocks
     float ks[2], lv[2], iv[2];
     int tok0;
-    int have;
+    int row[2];              // first 64-byte row of a block's K and V, -1: there is no such block
 };
 
 struct AttnShared {
@@ -116,8 +120,8 @@ struct AttnShared {
     Meta meta[kMetas];
     float qf[2][FGM_ATTN_MAX_ROWS];                    // score of a unit product: 2^e scale log2(e)
     float mx[4][FGM_ATTN_MAX_ROWS];                    // per lane quarter: a unit's maxima
-    float ls[4][FGM_ATTN_MAX_ROWS];                    // and the segment's sums
-    float m[FGM_ATTN_MAX_ROWS], l[FGM_ATTN_MAX_ROWS], inv[FGM_ATTN_MAX_ROWS];
+    float4 ls[2][FGM_ATTN_MAX_ROWS];                   // the sums of a segment's rows per lane quarter
+    float m[2][FGM_ATTN_MAX_ROWS];                     // and their references
     int2 lim[2][FGM_ATTN_MAX_ROWS];                       // tokens [x, y) that a row sees
     int orow[FGM_ATTN_MAX_ROWS];                       // a row's place among the (token, q head) of its sequence
     int units[2];                                      // the CTA's units: [first, last + 1)
@@ -145,6 +149,18 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
+// The same without the pause that try_wait may take: for a look at one of several things to do.
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Waits up to a tenth of a second for what is in flight after an abort.
 __device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity)
 {
@@ -158,6 +174,24 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar)
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// Whether the CTA has given up, or the wait limit is over: then it gives up here,
+// and the first to do so says where.
+__device__ __forceinline__ bool gave_up(int *abort, long long deadline, int32_t *status, int site, int index)
+{
+    if (*reinterpret_cast<volatile int *>(abort))
+        return true;
+    if (now_ns() <= deadline)
+        return false;
+    *reinterpret_cast<volatile int *>(abort) = 1;
+    if ((atomicOr(status, FGM_STATUS_WAIT_TIMEOUT) & FGM_STATUS_WAIT_TIMEOUT) == 0) {
+        status[1] = site;
+        status[2] = blockIdx.x;
+        status[3] = threadIdx.x >> 5;
+        status[4] = index;
+    }
+    return true;
+}
+
 // Bounded wait on a barrier phase; false on timeout or abort.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, int *abort, long long deadline, int32_t *status,
                                          int site, int index)
@@ -165,23 +199,10 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, int *abo
     for (int it = 0;; ++it) {
         if (bar_try(bar, parity))
             return true;
-        if ((it & 255) == 255) {
-            if (*reinterpret_cast<volatile int *>(abort))
-                return false;
-            if (now_ns() > deadline) {
-                *reinterpret_cast<volatile int *>(abort) = 1;
-                if ((atomicOr(status, FGM_STATUS_WAIT_TIMEOUT) & FGM_STATUS_WAIT_TIMEOUT) == 0) {
-                    status[1] = site;
-                    status[2] = blockIdx.x;
-                    status[3] = threadIdx.x >> 5;
-                    status[4] = index;
-                }
-                return false;
-            }
-        }
+        if ((it & 255) == 255 && gave_up(abort, deadline, status, site, index))
+            return false;
     }
 }
-
 
 __device__ __forceinline__ void bar_init(unsigned long long *b, int count)
 {
@@ -429,7 +450,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     int *cum = reinterpret_cast<int *>(vring + p.v_ring * kSide + (D == 64 ? kBlock * D : 0));   // [B + 1] units before each sequence
     int *lens = cum + p.B + 1;                                   // [B] clamped lengths
     int *used = lens + p.B;                                      // [B + 1] (sequence, head)s with units before each sequence
-    constexpr int kCost = 256 / D;                               // a (sequence, head)'s start and end, in units
+    constexpr int kCost = 512 / D;                               // a (sequence, head)'s start and end, in units
     const long long deadline = now_ns() + p.timeout_ns;
 
     if (tid == 0) {
@@ -544,6 +565,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         at.u = r % at.n;
         return at;
     };
+    // The segment after this one.
+    auto next = [&](Cursor c) -> Cursor {
+        c.u = 0;
+        if (++c.h < heads)
+            return c;
+        c.h = 0;
+        do
+            ++c.b;
+        while (c.b < p.B - 1 && cum[c.b + 1] == cum[c.b]);
+        if (c.b < p.B) {
+            c.blocks = seq_blocks(lens[c.b], p.M, p.window, c.first);
+            c.n = (c.blocks + 1) / 2;
+        }
+        return c;
+    };
+    Cursor cu = {};                                // where a warp is
+    if (n_units > 0 && warp > 0)
+        cu = locate(u0);
     auto wait = [&](unsigned long long *bar, int phase, int site, int index) -> bool {
         return bar_wait(saddr(bar), phase & 1, &sh.abort, deadline, p.status, site, index);
     };
@@ -556,7 +595,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     };
 
     if (warp == 0) {
-        // ------------------------------------------------------------ copies
+        // ------------------------------------------------------------ keys
         // Lane i looks up unit 32 k + i (block table and scales) a round ahead; the
         // round's scales are published together once its first copies are out.
         int row_n[2], tok_n = 0;                   // first 64-byte row of a block's K and V, -1: none
@@ -586,13 +625,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         };
         if (lane == 0) {
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
-            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
         }
         uint64_t policy;
         asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
         bool ok = true;
-        int k_issued = 0, v_issued = 0;
-        int sk = 0, k_turn = 0, sv = 0, v_turn = 0;      // stages and the rings' turns
+        int issued = 0, slot = 0, turn = 0;
         look(lane);
         for (int r = 0; r < n_units && ok; r += 32) {
             const int r0 = row_n[0], r1 = row_n[1], m = min(32, n_units - r), tok0 = tok_n;
@@ -604,10 +641,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const int row[2] = {__shfl_sync(0xFFFFFFFFu, r0, i), __shfl_sync(0xFFFFFFFFu, r1, i)};
                 if (lane == 0) {
                     const uint32_t bytes = ((row[0] >= 0) + (row[1] >= 0)) * (kBlock * D);
-                    if (k_turn > 0)
-                        ok = wait(&sh.kempty[sk], k_turn - 1, 13, u);
+                    if (turn > 0)
+                        ok = wait(&sh.kempty[slot], turn - 1, 13, u);
                     if (ok) {
-                        const uint32_t bar = saddr(&sh.kfull[sk]), dst = saddr(kring) + sk * kSide;
+                        const uint32_t bar = saddr(&sh.kfull[slot]), dst = saddr(kring) + slot * kSide;
                         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
@@ -615,34 +652,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                                 for (int c = 0; c < kSlices; ++c)
                                     tma_rows(dst + c * (kTile * 64) + k * (kBlock * 64), &kmap, row[k] + c * kBlock, bar, policy);
-                        k_issued = u + 1;
-                        if (v_turn > 0)
-                            ok = wait(&sh.vempty[sv], v_turn - 1, 14, u);
-                    }
-                    if (ok) {
-                        const uint32_t bar = saddr(&sh.vfull[sv]), dst = saddr(vring) + sv * kSide;
-                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            if (row[k] >= 0)
-                                tma_rows(dst + k * (kBlock * D), &vmap, row[k], bar, policy);
-                        v_issued = u + 1;
+                        issued = u + 1;
                     }
                 }
-                if (++sk == p.k_ring) {
-                    sk = 0;
-                    ++k_turn;
-                }
-                if (++sv == p.v_ring) {
-                    sv = 0;
-                    ++v_turn;
+                if (++slot == p.k_ring) {
+                    slot = 0;
+                    ++turn;
                 }
                 if (i == 0) {
                     // (The half's last round was read long ago: its units are 33 and more behind this one, the
                     // rings at most 8 deep and the softmax 3 units behind the scores.)
                     if (lane < m)
                         sh.meta[(r + lane) & (kMetas - 1)] =
-                            Meta{{ks0, ks1}, {log2f(vs0), log2f(vs1)}, {1.0f / vs0, 1.0f / vs1}, tok0, (r0 >= 0) | (r1 >= 0) << 1};
+                            Meta{{ks0, ks1}, {log2f(vs0), log2f(vs1)}, {1.0f / vs0, 1.0f / vs1}, tok0, {r0, r1}};
                     __syncwarp();
                     if (lane == 0)
                         bar_arrive(saddr(&sh.mfull[(r >> 5) & 1]));
@@ -651,12 +673,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
         }
         // every issued copy lands before the CTA may exit
-        if (lane == 0) {
-            for (int u = max(0, k_issued - p.k_ring); u < k_issued; ++u)
+        if (lane == 0)
+            for (int u = max(0, issued - p.k_ring); u < issued; ++u)
                 bar_drain(saddr(&sh.kfull[u % p.k_ring]), (u / p.k_ring) & 1);
-            for (int u = max(0, v_issued - p.v_ring); u < v_issued; ++u)
-                bar_drain(saddr(&sh.vfull[u % p.v_ring]), (u / p.v_ring) & 1);
-        }
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ scores
@@ -669,7 +688,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         for (int done = 0; done < n_units && ok; ++seg) {
             const int qslot = seg % p.q_ring;
             const uint64_t b0 = desc64(saddr(qs + qslot * query_bytes(R, D)));
-            const Cursor cu = locate(u0 + done);
             const int n = min(cu.n - cu.u, n_units - done);
             ok = wait(&sh.qfull[qslot], seg / p.q_ring, 17, seg);
             for (int u = done; u < done + n && ok; ++u) {
@@ -697,6 +715,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
             }
             done += n;
+            cu = next(cu);
         }
         // every issued product completes before the tensor memory is released
         if (lead) {
@@ -710,13 +729,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         bool ok = true;
         int slot = 0, turn = 0;
         for (int done = 0; done < n_units && ok;) {
-            const Cursor cu = locate(u0 + done);
             const int n = min(cu.n - cu.u, n_units - done);
             bool add = false;
             for (int u = done; u < done + n && ok; ++u) {
                 ok = wait(&sh.vfull[slot], turn, 18, u) && wait(&sh.pfull[u & 1], u >> 1, 19, u);
                 ok = __all_sync(0xFFFFFFFFu, ok);
-                const int have = sh.meta[u & (kMetas - 1)].have;
+                const int *row = sh.meta[u & (kMetas - 1)].row;
+                const int have = (row[0] >= 0) | (row[1] >= 0) << 1;
                 if (ok && lead) {
                     after_sync();
                     const uint64_t a0 = desc64(saddr(vring + slot * kSide)), b0 = desc64(saddr(ps + (u & 1) * prob_bytes(R)));
@@ -739,6 +758,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
             }
             done += n;
+            cu = next(cu);
         }
         if (lead) {
             commit(&sh.drained[1]);
@@ -746,25 +766,64 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         __syncwarp();
     } else if (warp == 3) {
-        // ------------------------------------------------------------ queries of the second segment and on
-        bool ok = true;
-        int seg = 0;
-        for (int done = 0; done < n_units && ok; ++seg) {
-            const Cursor cu = locate(u0 + done);
-            done += min(cu.n - cu.u, n_units - done);
-            if (seg == 0)
-                continue;
-            const int qslot = seg % p.q_ring;
-            if (seg >= p.q_ring)
-                ok = wait(&sh.qempty[qslot], seg / p.q_ring - 1, 26, seg);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok)
+        // ------------------------------------------------------------ values, and queries of the second segment and on
+        if (lane == 0)
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
+        uint64_t policy;
+        asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+        int slot = 0, turn = 0, issued = 0;        // values: ring place and units out
+        int seg = 0, done = 0;                     // queries: segments prepared and the units before the next one
+        for (int spin = 0; issued < n_units || done < n_units;) {
+            // whichever can be done now: the queries of a segment whose buffer is free, a unit's values whose stage is
+            int can = 0;
+            if (lane == 0) {
+                if (done < n_units &&
+                    (seg < p.q_ring || bar_test(saddr(&sh.qempty[seg % p.q_ring]), (seg / p.q_ring - 1) & 1)))
+                    can = 1;
+                if (issued < n_units && (issued % 32 != 0 || bar_test(saddr(&sh.mfull[(issued >> 5) & 1]), (issued >> 6) & 1)) &&
+                    (turn == 0 || bar_test(saddr(&sh.vempty[slot]), (turn - 1) & 1)))
+                    can |= 2;
+                if (can == 0 && (++spin & 255) == 0 && gave_up(&sh.abort, deadline, p.status, 14, issued))
+                    can = 4;
+            }
+            can = __shfl_sync(0xFFFFFFFFu, can, 0);
+            if (can & 4)
                 break;
-            queries(std::integral_constant<int, 8>{}, cu, 0, 1, qslot);      // (eight rows of loads in flight)
-            __syncwarp();
-            if (lane == 0)
-                bar_arrive(saddr(&sh.qfull[qslot]));
+            if (can & 2) {
+                if (lane == 0) {
+                    const int *row = sh.meta[issued & (kMetas - 1)].row;
+                    const int row0 = row[0], row1 = row[1];
+                    const uint32_t bar = saddr(&sh.vfull[slot]), dst = saddr(vring) + slot * kSide;
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
+                                 "r"(((row0 >= 0) + (row1 >= 0)) * (kBlock * D))
+                                 : "memory");
+                    if (row0 >= 0)
+                        tma_rows(dst, &vmap, row0, bar, policy);
+                    if (row1 >= 0)
+                        tma_rows(dst + kBlock * D, &vmap, row1, bar, policy);
+                }
+                ++issued;
+                if (++slot == p.v_ring) {
+                    slot = 0;
+                    ++turn;
+                }
+            }
+            if (can & 1) {
+                if (seg > 0) {                     // (the first segment's are the softmax warps' work)
+                    queries(std::integral_constant<int, 8>{}, cu, 0, 1, seg % p.q_ring);      // (eight rows of loads in flight)
+                    __syncwarp();
+                    if (lane == 0)
+                        bar_arrive(saddr(&sh.qfull[seg % p.q_ring]));
+                }
+                done += min(cu.n - cu.u, n_units - done);
+                cu = next(cu);
+                ++seg;
+            }
         }
+        if (lane == 0)
+            for (int u = max(0, issued - p.v_ring); u < issued; ++u)
+                bar_drain(saddr(&sh.vfull[u % p.v_ring]), (u / p.v_ring) & 1);
+        __syncwarp();
     } else if (warp >= 4) {
         // ------------------------------------------------------------ softmax
         const int w = warp - 4, quarter = warp & 3, part4 = w >> 2, stid = tid - 128;
@@ -775,6 +834,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int n0 = part4 * kNR;                // the thread's rows: n0 .. n0 + kNR - 1
         bool alive = true;
         int scales = -1;                           // the round whose scales are known to be there
+        const bool by_head = p.B * heads <= p.n_rec;
         int4 rec = make_int4(-1, 0, 0, 0);
 
         // sequences without a token: zero rows
@@ -786,11 +846,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (p.lse)
                     for (int i = stid; i < p.M * p.Hq; i += kSoftWarps * 32)
                         p.lse[row0 + i] = -INFINITY;
+                if (by_head)
+                    for (int i = stid; i < heads; i += kSoftWarps * 32)
+                        p.rec[b * heads + i] = rec;
             }
 
         int seg = 0;
         for (int done = 0; done < n_units; ++seg) {
-            const Cursor cu = locate(u0 + done);
             const int n = min(cu.n - cu.u, n_units - done);
             const int len = lens[cu.b], qslot = seg % p.q_ring;
             const float *qf = sh.qf[qslot];
@@ -847,8 +909,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const Meta me = sh.meta[u & (kMetas - 1)];
                 const float ks = blk ? me.ks[1] : me.ks[0], lv = blk ? me.lv[1] : me.lv[0], ivs = blk ? me.iv[1] : me.iv[0];
                 const int tok = me.tok0 + tl;
-                const bool here = me.have >> blk & 1;
-                const bool edge = me.tok0 + kTile > hi_min || me.tok0 < lo_max || me.have != 3;
+                const bool here = (blk ? me.row[1] : me.row[0]) >= 0, whole_unit = me.row[0] >= 0 && me.row[1] >= 0;
+                const bool edge = me.tok0 + kTile > hi_min || me.tok0 < lo_max || !whole_unit;
 
                 // scores in powers of two, with V's scale on top
                 bool over = false;
@@ -927,12 +989,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                     // (sh.mx is written again only after every reader has passed the next vote)
                 }
-                any_pv |= me.have != 0;
+                any_pv |= me.row[0] >= 0 || me.row[1] >= 0;
                 // the next unit's scores, if they are there, are read while this one's probabilities are made
                 float next[kAhead ? 2 * kNR : 1];
                 const bool more = i + 1 < n;
                 const bool early = kAhead && more && (u + 1) >> 5 == scales &&
-                                   __all_sync(0xFFFFFFFFu, bar_try(saddr(&sh.sfull[(u + 1) & 1]), ((u + 1) >> 1) & 1));
+                                   __all_sync(0xFFFFFFFFu, bar_test(saddr(&sh.sfull[(u + 1) & 1]), ((u + 1) >> 1) & 1));
                 // the buffer's last product is done
                 if (alive && u >= 2)
                     alive = wait(&sh.pdone[u & 1], (u >> 1) - 1, 23, u);
@@ -996,21 +1058,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
 
             // -------------------------------------------------------- end of the segment
+            // (a second copy of the sums by segment parity, so that a warp may go on to the next segment's end
+            // while another still reads these)
+            float *ms = sh.m[seg & 1];
+            float4 *ls = sh.ls[seg & 1];
 #pragma unroll
             for (int r = 0; r < kNR; ++r) {
                 const float x = warp_sum(l[r]);
                 if (lane == 0)
-                    sh.ls[quarter][n0 + r] = x;
+                    reinterpret_cast<float *>(ls + n0 + r)[quarter] = x;
                 if (quarter == 0 && lane == 0)
-                    sh.m[n0 + r] = m[r];
+                    ms[n0 + r] = m[r];
             }
             asm volatile("bar.sync 1, 512;" ::: "memory");
-            if (stid < R) {
-                const float ls = (sh.ls[0][stid] + sh.ls[1][stid]) + (sh.ls[2][stid] + sh.ls[3][stid]);
-                sh.l[stid] = ls;
-                sh.inv[stid] = ls == 0.0f ? 0.0f : 1.0f / ls;
-            }
-            asm volatile("bar.sync 1, 512;" ::: "memory");
+            auto sum_of = [&](int r) -> float {
+                const float4 x = ls[r];
+                return (x.x + x.y) + (x.z + x.w);
+            };
             const int last_u = done + n - 1;
             if (alive)
                 alive = wait(&sh.pdone[last_u & 1], last_u >> 1, 25, last_u);
@@ -1033,35 +1097,41 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     tmem_wait_ld(o);
 #pragma unroll
                     for (int k = 0; k < kCh; ++k) {
-                        const float inv = sh.inv[r + k];
-                        const float v = inv == 0.0f ? 0.0f : fmaf(o[kCh + k], 1.0f / 32.0f, o[k]);
+                        const float sum = sum_of(r + k);
+                        const float v = sum == 0.0f ? 0.0f : fmaf(o[kCh + k], 1.0f / 32.0f, o[k]);
                         if (!whole)
                             part[(r + k) * D + d] = v;
                         else if (r + k < rows)
-                            p.out[(row0 + sh.orow[r + k]) * D + d] = f32_to_bf16(v * inv);
+                            p.out[(row0 + sh.orow[r + k]) * D + d] = f32_to_bf16(sum == 0.0f ? 0.0f : __fdividef(v, sum));
                     }
                 }
             }
             if (stid < R) {
-                const float ls = sh.l[stid], mm = sh.m[stid];
+                const float sum = sum_of(stid), mm = ms[stid];
                 if (!whole) {
                     part[R * D + stid] = mm;
-                    part[R * (D + 1) + stid] = ls;
+                    part[R * (D + 1) + stid] = sum;
                 } else if (p.lse && stid < rows) {
-                    p.lse[row0 + sh.orow[stid]] = ls == 0.0f ? -INFINITY : (mm - kLift + log2f(ls)) * kLn2;
+                    p.lse[row0 + sh.orow[stid]] = sum == 0.0f ? -INFINITY : (mm - kLift + log2f(sum)) * kLn2;
                 }
             }
-            if (starts && !ends) {
-                // the CTA that holds the segment's last unit, at this place: the largest c with floor(P c / G) <= place
-                const int place = u0 + done - cu.u + cu.n - 1 + (used[cu.b] + cu.h + 1) * kCost;
-                rec = make_int4(cu.b, cu.h, static_cast<int>((static_cast<int64_t>(place + 1) * G - 1) / n_places), 0);
+            if (starts) {
+                int4 mine = make_int4(-1, 0, 0, 0);
+                if (!ends) {
+                    // the CTA that holds the segment's last unit, at this place: the largest c with floor(P c / G) <= place
+                    const int place = u0 + done - cu.u + cu.n - 1 + (used[cu.b] + cu.h + 1) * kCost;
+                    mine = make_int4(cu.b, cu.h, blockIdx.x, static_cast<int>((static_cast<int64_t>(place + 1) * G - 1) / n_places));
+                    rec = mine;
+                }
+                if (by_head && stid == 0)
+                    p.rec[cu.b * heads + cu.h] = mine;
             }
             if (lane == 0)
                 bar_arrive(saddr(&sh.qempty[qslot]));
-            asm volatile("bar.sync 1, 512;" ::: "memory");     // sh.m and sh.l are free again
             done += n;
+            cu = next(cu);
         }
-        if (stid == 0)
+        if (stid == 0 && !by_head)
             p.rec[blockIdx.x] = rec;
     }
     before_sync();
@@ -1072,9 +1142,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
 }
 
-// Adds up the partial segments of the (sequence, kv head) that starts in CTA
-// blockIdx.x of the first kernel and goes on, in CTA order: rows blockIdx.y,
-// blockIdx.y + gridDim.y, ... A thread owns four output elements of every
+// Adds up the partial segments of one (sequence, kv head) that spans CTAs of the
+// first kernel, in CTA order; CTA (record, row). A thread owns four output elements of every
 // kLanes-th partial, and the lanes meet in shared memory, also in order.
 template <int D>
 __global__ void __launch_bounds__(256) k_attn_join(const AttnArgs p)
@@ -1088,7 +1157,7 @@ __global__ void __launch_bounds__(256) k_attn_join(const AttnArgs p)
     const int4 rec = __ldcg(p.rec + blockIdx.x);
     if (rec.x < 0)
         return;
-    const int R = p.M * p.G, rows = p.rows, c0 = blockIdx.x, n = rec.z - c0 + 1;
+    const int R = p.M * p.G, rows = p.rows, c0 = rec.z, n = rec.w - c0 + 1;
     const int64_t pf = partial_floats(p.rows, D);
     // partial i: the first CTA's second slot, then the others' first slots
     auto part = [&](int i) { return p.part + ((c0 + i) * 2 + (i == 0 ? 1 : 0)) * pf; };

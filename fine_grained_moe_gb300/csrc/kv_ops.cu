@@ -84,7 +84,8 @@ template <int D, int R>
 int launch_attn_t(kv::AttnArgs &a, int sms, cudaStream_t st)
 {
     const int grid = sms < kv::kMaxGrid ? sms : kv::kMaxGrid;
-    // what is left of the shared memory goes to the rings, V's first: its stage is freed last
+    a.n_rec = a.B * a.c.heads < grid ? a.B * a.c.heads : grid;
+    // what is left of the shared memory goes to the rings, V's first: its stages are freed last
     constexpr size_t side = static_cast<size_t>(kv::kTile) * D;
     a.q_ring = kv::query_bytes(R, D) <= 16384 ? 2 : 1;
     const size_t fixed = a.q_ring * kv::query_bytes(R, D) + 2 * kv::prob_bytes(R) + (D == 64 ? kv::kBlock * D : 0) +
@@ -107,7 +108,9 @@ int launch_attn_t(kv::AttnArgs &a, int sms, cudaStream_t st)
         ready[dev & 63] = true;
     }
     FGM_HOST_TRY(launch_overlapped(kv::k_attn<D, R>, dim3(grid), kv::kAttnThreads, bytes, st, kmap, vmap, a));
-    return launch_overlapped(kv::k_attn_join<D>, dim3(grid, a.M * a.G < 16 ? a.M * a.G : 16), 256, 0, st, a);
+    // a CTA a row where the records are few, else enough to fill the device
+    const int rows = a.M * a.G, y = a.n_rec * rows <= 2432 ? rows : 2432 / a.n_rec;
+    return launch_overlapped(kv::k_attn_join<D>, dim3(a.n_rec, y), 256, 0, st, a);
 }
 
 template <int D>
