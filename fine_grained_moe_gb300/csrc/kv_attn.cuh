@@ -118,7 +118,7 @@ struct AttnShared {
     unsigned long long mfull[2];
     unsigned long long sfull[2], sfree[2], pfull[2], pdone[2], qfull[2], qempty[2], drained[2];
     Meta meta[kMetas];
-    float qf[2][FGM_ATTN_MAX_ROWS];                    // score of a unit product: 2^e scale log2(e)
+    alignas(16) float qf[2][FGM_ATTN_MAX_ROWS];                    // score of a unit product: 2^e scale log2(e)
     float mx[4][FGM_ATTN_MAX_ROWS];                    // per lane quarter: a unit's maxima
     float4 ls[2][FGM_ATTN_MAX_ROWS];                   // the sums of a segment's rows per lane quarter
     float m[2][FGM_ATTN_MAX_ROWS];                     // and their references
@@ -324,14 +324,17 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap *map, i
         : "memory");
 }
 
-__device__ __forceinline__ uint32_t e4m3_pair(float a, float b)   // a in the low byte
+// Two E4M3 terms of two values below 448: hi + lo / 32 (a in the low bytes). By
+// way of f16, whose 11 bits hold hi, the difference and 32 times it exactly; the
+// values' own rounding to f16, 2^-12 of them and 2^-25, is below lo's.
+__device__ __forceinline__ void e4m3_terms(float a, float b, uint32_t &hi, uint32_t &lo)
 {
-    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-}
-
-__device__ __forceinline__ float2 e4m3_values(uint32_t w)
-{
-    return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w), __NV_E4M3)));
+    const __half2 x = __floats2half2_rn(a, b);
+    const __nv_fp8x2_storage_t h = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
+    const __half2 z = __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3));
+    const __half2 d = __hmul2(__hsub2(x, z), __float2half2_rn(32.0f));
+    hi = h;
+    lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(d), __NV_SATFINITE, __NV_E4M3);
 }
 
 __device__ __forceinline__ void sts32(uint32_t a, uint32_t v)
@@ -832,6 +835,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
         const int rows = p.M * p.G;
         const int n0 = part4 * kNR;                // the thread's rows: n0 .. n0 + kNR - 1
+        // where the thread's token goes in P^T, and the swizzle of its rows 2 j, 2 j + 1
+        const uint32_t probs = saddr(ps) + blk * (kN * 64) + n0 * 64 + (tl & 15);
+        uint32_t phase[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            phase[j] = ((((tl & 63) >> 4) ^ ((n0 >> 1) + j)) & 3) << 4;
         bool alive = true;
         int scales = -1;                           // the round whose scales are known to be there
         const bool by_head = p.B * heads <= p.n_rec;
@@ -855,7 +864,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         for (int done = 0; done < n_units; ++seg) {
             const int n = min(cu.n - cu.u, n_units - done);
             const int len = lens[cu.b], qslot = seg % p.q_ring;
-            const float *qf = sh.qf[qslot];
+            const float *qf = sh.qf[qslot] + n0;
             if (seg == 0) {
                 queries(std::integral_constant<int, (R + kSoftWarps - 1) / kSoftWarps>{}, cu, w, kSoftWarps, 0);
                 asm volatile("bar.sync 1, 512;" ::: "memory");
@@ -914,9 +923,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
                 // scores in powers of two, with V's scale on top
                 bool over = false;
+                float f[kNR];
+                if constexpr (kNR % 4 == 0) {
+#pragma unroll
+                    for (int r = 0; r < kNR; r += 4) {
+                        const float4 x = *reinterpret_cast<const float4 *>(qf + r);
+                        f[r] = x.x;
+                        f[r + 1] = x.y;
+                        f[r + 2] = x.z;
+                        f[r + 3] = x.w;
+                    }
+                } else {
+                    f[0] = qf[0];
+                    f[1] = qf[1];
+                }
 #pragma unroll
                 for (int r = 0; r < kNR; ++r)
-                    s[r] = fmaf(fmaf(s[kNR + r], 0.0625f, s[r]), qf[n0 + r] * ks, lv);
+                    s[r] = fmaf(fmaf(s[kNR + r], 0.0625f, s[r]), f[r] * ks, lv);
                 if (edge) {
 #pragma unroll
                     for (int r = 0; r < kNR; ++r) {
@@ -1004,19 +1027,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         after_sync();
                         read(u + 1, next);
                     }
-                const int kt = tl & 63;
-                const uint32_t pt = saddr(ps + (u & 1) * prob_bytes(R) + blk * (kN * 64)) + (kt & 15);
+                const uint32_t pt = probs + (u & 1) * prob_bytes(R);
 #pragma unroll
                 for (int r = 0; r < kNR; r += 2) {
                     const float p0 = ex2(s[r] - (m[r] - kLift)), p1 = ex2(s[r + 1] - (m[r + 1] - kLift));
                     l[r] = fmaf(p0, ivs, l[r]);
                     l[r + 1] = fmaf(p1, ivs, l[r + 1]);
-                    const uint32_t hi = e4m3_pair(p0, p1);
-                    const float2 z = e4m3_values(hi);
-                    const uint32_t lo = e4m3_pair(32.0f * (p0 - z.x), 32.0f * (p1 - z.y));
-                    // rows n, n + 1 (n even) lie in one swizzle phase; the second term R rows on
-                    const int n = n0 + r;
-                    const uint32_t at = pt + n * 64 + ((((kt >> 4) ^ (n >> 1)) & 3) << 4);
+                    uint32_t hi, lo;
+                    e4m3_terms(p0, p1, hi, lo);
+                    // rows r, r + 1 (r even) lie in one swizzle phase; the second term R rows on
+                    const uint32_t at = pt + phase[(r >> 1) & 3] + r * 64;
                     sts8(at, hi);
                     sts8(at + 64, hi >> 8);
                     sts8(at + R * 64, lo);
@@ -1031,7 +1051,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     if (alive && here && (tok < lo_min || tok >= len)) {
                         uint8_t *vt = vring + slot * kSide + blk * (kBlock * D);
                         for (int d = part4 * (D / 4); d < (part4 + 1) * (D / 4); ++d)
-                            vt[at64(d, kt)] = 0;
+                            vt[at64(d, tl & 63)] = 0;
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

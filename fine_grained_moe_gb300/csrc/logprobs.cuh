@@ -321,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 {
     using L = Load<E>;
     constexpr int kVec = L::kVec, kLoads = kVals / kVec, kChunk = 32 * kLoads;      // vectors of a warp's chunk
+    constexpr int kDepth = 4 / kLoads;         // chunks on their way: four vectors a lane, 64 KB an SM
     __shared__ unsigned s_max[kThreads], s_bound;
     __shared__ Sums s_sum[kWarps];
     __shared__ float s_v[kWarps][kMaxTop];
@@ -343,18 +344,20 @@ __global__ void __launch_bounds__(kThreads, 4)
     Sums s;
     s.clear();
     int nan = 0;
-    uint4 raw[kLoads];
-    auto fetch = [&](int at) {                 // one chunk's vectors of this lane
+    uint4 raw[kDepth][kLoads];
+    auto fetch = [&](int at, uint4 (&r)[kLoads]) {      // one chunk's vectors of this lane
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
             if (at + i * 32 < v1)
-                raw[i] = __ldg(zv + at + i * 32);
+                r[i] = __ldg(zv + at + i * 32);
     };
 
     int at = v0 + warp * kChunk + lane;
     const int step = kWarps * kChunk;
     const int first = at;
-    fetch(at);
+#pragma unroll
+    for (int q = 0; q < kDepth; ++q)
+        fetch(at + q * step, raw[q]);
     const bool edges = split == 0 && warp == 0 && head + tail > 0;      // this warp takes the logits around the vectors
     if (edges) {
         float v[kVals];
@@ -367,21 +370,27 @@ __global__ void __launch_bounds__(kThreads, 4)
             v[1] = L::one(zr + V - tail + lane);
         fold(s, v, c, nan);
     }
-    for (; at - lane < v1; at += step) {
-        float v[kVals];
+    while (at - lane < v1) {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            L::unpack(raw[i], v + i * kVec);
-        if (at - lane + kChunk > v1) {         // past the end: -inf
+        for (int q = 0; q < kDepth; ++q) {
+            if (at - lane < v1) {
+                float v[kVals];
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-                if (at + i * 32 >= v1)
+                for (int i = 0; i < kLoads; ++i)
+                    L::unpack(raw[q][i], v + i * kVec);
+                if (at - lane + kChunk > v1) { // past the end: -inf
 #pragma unroll
-                    for (int j = 0; j < kVec; ++j)
-                        v[i * kVec + j] = -INFINITY;
+                    for (int i = 0; i < kLoads; ++i)
+                        if (at + i * 32 >= v1)
+#pragma unroll
+                            for (int j = 0; j < kVec; ++j)
+                                v[i * kVec + j] = -INFINITY;
+                }
+                fetch(at + kDepth * step, raw[q]);
+                fold(s, v, c, nan);
+            }
+            at += step;
         }
-        fetch(at + step);
-        fold(s, v, c, nan);
     }
 
     // ------------------------------------------------------------ the k best

@@ -10,15 +10,15 @@ Tolerances.
         half a subnormal step is 2^-10, 2^-10 / 16 / 224 < 2^-21); D products
         add up in fp32, each add within 2^-23 of a sum below sum|q k|:
         ds = 2^-21 qmax sum|k| + D 2^-23 sum|q k|, both times the scale;
-      - probabilities enter the product as two E4M3 terms: 2^-4 of 2^-4 = 2^-8
-        of themselves, and where the second term is subnormal 2^-10 / 32 / 32 =
+      - probabilities are rounded to f16, 2^-12 of themselves, and enter the
+        product as two E4M3 terms: 2^-4 of 2^-4 = 2^-8 of themselves, and where the second term is subnormal 2^-10 / 32 / 32 =
         2^-20 of the largest that their CTA saw; a CTA holds at most 512 tokens
         of a row in these cases and the CTAs' largest sum to at most 1:
         512 * 2^-20 V;
       - exponentials and the sums of up to T terms: exp2 within 2^-21, sums in
         fp32, 2^-14 covers both at T <= 2^9 terms a partial;
       - the output is rounded to bf16: 2^-8 of itself.
-    |err| <= (2^-8 + 2^-14 + 2 ds) A + 2^-11 V + 2^-8 |out|.
+    |err| <= (2^-8 + 2^-12 + 2^-14 + 2 ds) A + 2^-11 V + 2^-8 |out|.
   * lse: |err| <= ds + 2^-14 (1 + |lse| 2^-4).
 """
 
@@ -191,7 +191,7 @@ def check_attn(out, lse, q, kq, vq, ks, vs, lens, tab, scale, window):
     o, l, A, V, sqk, sk = plain64.attn(q.cpu().double().numpy(), kv, vv, lens, tab, scale, window)
     ds = 2.0 ** -21 * sk + D * 2.0 ** -23 * sqk
     go, gl = out.cpu().double().numpy(), lse.cpu().double().numpy()
-    tol = (2.0 ** -8 + 2.0 ** -14 + 2 * ds[..., None]) * A + 2.0 ** -11 * V + 2.0 ** -8 * np.abs(o)
+    tol = (2.0 ** -8 + 2.0 ** -12 + 2.0 ** -14 + 2 * ds[..., None]) * A + 2.0 ** -11 * V + 2.0 ** -8 * np.abs(o)
     assert np.isfinite(go).all()
     bad = np.abs(go - o) > tol
     assert not bad.any(), (np.argwhere(bad)[:4], go[bad][:4], o[bad][:4], tol[bad][:4])
