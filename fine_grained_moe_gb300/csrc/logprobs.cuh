@@ -323,6 +323,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     constexpr int kVec = L::kVec, kLoads = kVals / kVec, kChunk = 32 * kLoads;      // vectors of a warp's chunk
     constexpr int kDepth = 4 / kLoads;         // chunks on their way: four vectors a lane, 64 KB an SM
     __shared__ unsigned s_max[kThreads], s_bound;
+    __shared__ int s_who[kThreads], s_many;
     __shared__ Sums s_sum[kWarps];
     __shared__ float s_v[kWarps][kMaxTop];
     __shared__ int32_t s_i[kWarps][kMaxTop];
@@ -341,6 +342,14 @@ __global__ void __launch_bounds__(kThreads, 4)
     const int v1 = static_cast<int>(static_cast<int64_t>(nvec) * (split + 1) / splits);
     const float c = kLog2e / o.T;
 
+    float zt = -INFINITY;                      // the given token's logit
+    if (splits == 1 && o.logp && tid == 0) {
+        const int32_t t = __ldg(o.tokens + row);
+        if (t >= 0 && t < V)
+            zt = L::one(zr + t);
+        if (zt != zt)
+            zt = -INFINITY;
+    }
     Sums s;
     s.clear();
     int nan = 0;
@@ -354,7 +363,6 @@ __global__ void __launch_bounds__(kThreads, 4)
 
     int at = v0 + warp * kChunk + lane;
     const int step = kWarps * kChunk;
-    const int first = at;
 #pragma unroll
     for (int q = 0; q < kDepth; ++q)
         fetch(at + q * step, raw[q]);
@@ -425,15 +433,20 @@ __global__ void __launch_bounds__(kThreads, 4)
                 }
                 __syncwarp();
             }
-            if (lane == 0)
+            if (lane == 0) {
                 s_bound = kth;
+                s_many = 0;
+            }
         }
         __syncthreads();
         const float bound = unordered(s_bound);
-        // the logits of every thread that reaches the bound, a vector a lane
-        for (unsigned who = __ballot_sync(0xFFFFFFFFu, s.m >= bound); who; who &= who - 1) {
-            const int src = __ffs(who) - 1;
-            if (edges) {
+        // the threads that reach the bound, in any order (the lists do not depend on it), dealt to the warps
+        if (s.m >= bound)
+            s_who[atomicAdd(&s_many, 1)] = tid;
+        __syncthreads();
+        for (int w = warp; w < s_many; w += kWarps) {
+            const int who = s_who[w], src = who & 31, start = v0 + (who >> 5) * kChunk + src;
+            if (who < 32 && split == 0 && head + tail > 0) {
                 float v = -INFINITY;
                 int32_t i = kNone;
                 if (lane == 0 ? src < head : lane == 1 && src < tail) {
@@ -443,9 +456,10 @@ __global__ void __launch_bounds__(kThreads, 4)
                 }
                 top.offer(v, i, k, lane);
             }
+            // its logits, a vector a lane
             for (int n0 = 0;; n0 += 32) {
                 const int n = n0 + lane;       // the thread's n-th vector
-                const int vec = first - lane + src + n / kLoads * step + n % kLoads * 32;
+                const int vec = start + n / kLoads * step + n % kLoads * 32;
                 const bool in = vec < v1;
                 if (!__any_sync(0xFFFFFFFFu, in))
                     break;
@@ -481,14 +495,6 @@ __global__ void __launch_bounds__(kThreads, 4)
     if (k)
         merge_lists(s_v[lane & (kWarps - 1)], s_i[lane & (kWarps - 1)], lane < kWarps ? k : 0, k, lane, top.v, top.i);
     if (splits == 1) {
-        float zt = -INFINITY;
-        if (o.logp) {
-            const int32_t t = __ldg(o.tokens + row);
-            if (t >= 0 && t < V)
-                zt = L::one(zr + t);
-            if (zt != zt)
-                zt = -INFINITY;
-        }
         write_row(o, row, s, top, nan, zt, lane);
         return;
     }
