@@ -15,7 +15,7 @@
 //
 // What bounds it: HBM, with the instructions close behind. The maximum is taken
 // and the scale applied two elements at a time in bf16 form (17.7 -> about 9
-// instructions an element; a prompt of 16,448 tokens, 8 heads of 256: 47.8 ->
+// instructions an element; a prompt of 16,381 tokens, 8 heads of 256: 47.8 ->
 // 35.8 us, 5.6 TB/s). A decode step's few tokens take a launch.
 #pragma once
 
