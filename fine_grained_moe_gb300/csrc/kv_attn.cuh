@@ -48,6 +48,14 @@
 // maximum over its tokens, which are spread over the lanes, only a vote; one
 // that exceeds it computes the maxima and rescales the accumulator.
 //
+// What bounds it, a pass being both kernels: HBM in the steady state up to R = 16,
+// where a unit takes 0.35 us a CTA at D = 128 and twice that at D = 256 (5 tokens
+// at 32K, 8 heads of 256: 134 MB in 32 us); the softmax warps' chain above (R = 48,
+// 2 heads at 256K tokens: 268 MB in 62 us). Around that 5 to 6 us to the first
+// product (cold code, then lens, block table and the first copies one after the
+// other) and 3 to 4 us of k_attn_join: the ragged batch of 9 (147 MB in 37 us)
+// has several starts a CTA, 1,000 tokens are little else (18 us).
+//
 // A segment (the part of one (sequence, kv head) in one CTA) that is a whole
 // (sequence, head) is written out; one that spans CTAs leaves partial sums that
 // k_attn_join adds up in CTA order. No atomics: the same call gives the same
@@ -174,13 +182,16 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar)
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Whether the CTA has given up, or the wait limit is over: then it gives up here,
-// and the first to do so says where.
-__device__ __forceinline__ bool gave_up(int *abort, long long deadline, int32_t *status, int site, int index)
+// Whether the CTA has given up, or this wait's limit is over (since: 0 before the
+// first look, then when that was): then it gives up here, and the first to do so
+// says where.
+__device__ __forceinline__ bool gave_up(int *abort, long long &since, long long limit, int32_t *status, int site, int index)
 {
     if (*reinterpret_cast<volatile int *>(abort))
         return true;
-    if (now_ns() <= deadline)
+    if (since == 0)
+        since = now_ns();
+    if (now_ns() - since <= limit)
         return false;
     *reinterpret_cast<volatile int *>(abort) = 1;
     if ((atomicOr(status, FGM_STATUS_WAIT_TIMEOUT) & FGM_STATUS_WAIT_TIMEOUT) == 0) {
@@ -193,13 +204,14 @@ __device__ __forceinline__ bool gave_up(int *abort, long long deadline, int32_t 
 }
 
 // Bounded wait on a barrier phase; false on timeout or abort.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, int *abort, long long deadline, int32_t *status,
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, int *abort, long long limit, int32_t *status,
                                          int site, int index)
 {
+    long long since = 0;
     for (int it = 0;; ++it) {
         if (bar_try(bar, parity))
             return true;
-        if ((it & 255) == 255 && gave_up(abort, deadline, status, site, index))
+        if ((it & 255) == 255 && gave_up(abort, since, limit, status, site, index))
             return false;
     }
 }
@@ -454,7 +466,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     int *lens = cum + p.B + 1;                                   // [B] clamped lengths
     int *used = lens + p.B;                                      // [B + 1] (sequence, head)s with units before each sequence
     constexpr int kCost = 512 / D;                               // a (sequence, head)'s start and end, in units
-    const long long deadline = now_ns() + p.timeout_ns;
 
     if (tid == 0) {
         for (int i = 0; i < kMaxRing; ++i) {
@@ -587,7 +598,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (n_units > 0 && warp > 0)
         cu = locate(u0);
     auto wait = [&](unsigned long long *bar, int phase, int site, int index) -> bool {
-        return bar_wait(saddr(bar), phase & 1, &sh.abort, deadline, p.status, site, index);
+        return bar_wait(saddr(bar), phase & 1, &sh.abort, p.timeout_ns, p.status, site, index);
     };
 
     auto queries = [&](auto batch, const Cursor &cu, int w, int warps, int slot) {
@@ -776,7 +787,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
         int slot = 0, turn = 0, issued = 0;        // values: ring place and units out
         int seg = 0, done = 0;                     // queries: segments prepared and the units before the next one
-        for (int spin = 0; issued < n_units || done < n_units;) {
+        int spin = 0;
+        long long since = 0;
+        while (issued < n_units || done < n_units) {
             // whichever can be done now: the queries of a segment whose buffer is free, a unit's values whose stage is
             int can = 0;
             if (lane == 0) {
@@ -786,7 +799,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (issued < n_units && (issued % 32 != 0 || bar_test(saddr(&sh.mfull[(issued >> 5) & 1]), (issued >> 6) & 1)) &&
                     (turn == 0 || bar_test(saddr(&sh.vempty[slot]), (turn - 1) & 1)))
                     can |= 2;
-                if (can == 0 && (++spin & 255) == 0 && gave_up(&sh.abort, deadline, p.status, 14, issued))
+                if (can != 0)
+                    since = 0;
+                else if ((++spin & 255) == 0 && gave_up(&sh.abort, since, p.timeout_ns, p.status, 14, issued))
                     can = 4;
             }
             can = __shfl_sync(0xFFFFFFFFu, can, 0);

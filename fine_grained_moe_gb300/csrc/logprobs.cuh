@@ -8,13 +8,16 @@
 // l and w = sum e d (d = (z - m) log2(e) / T, e = 2^d) over 16 logits at a time
 // and rescales when its maximum grows. Differences are clamped at -200, where e
 // is 0 already, so that -inf (or a type's lowest value) adds 0 and not 0 * inf.
-// About 7 instructions and one exponential a logit, half of what HBM leaves
-// time for at 2 bytes.
+// About 7 instructions and one exponential a logit. 600 rows of 262,144 fp32
+// logits: 96 us, 6.5 TB/s. 1,013 rows of 50,021 bf16 logits: 29 us, 3.5 TB/s,
+// where 1,013 CTAs are 1.7 rounds of the 608 that run at a time, each with a start
+// and an end. (Fewer instructions, six a logit, left both as they are; CTAs of
+// four warps, eight an SM, too, and took 19 to 38 us on 5 rows.)
 //
 // The k best cost nothing in that pass: the k-th largest of the threads' maxima
 // bounds the k-th best logit from below, so only the threads that reach it
-// (k of 256 unless logits tie) can hold one of the k best, and their warp reads
-// those threads' logits a second time, from the caches. (Lists kept during the
+// (k of 256 unless logits tie) can hold one of the k best, and the warps, which
+// share them out, read those threads' logits a second time, from the caches. (Lists kept during the
 // pass, with the same bound as a threshold, took 134 us on 1,013 x 50,021 bf16
 // logits, against 15 us of HBM time: the insertions were most of it.)
 //

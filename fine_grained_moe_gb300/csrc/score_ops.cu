@@ -1,5 +1,5 @@
 // C ABI of the log probabilities (declared in include/fgm.h): argument checks
-// and launches of logprobs.cuh.
+// and launches of logprobs.cuh and lm_score.cuh.
 #include <cmath>
 
 #include "host.h"
@@ -96,9 +96,7 @@ int64_t row_tiles(int64_t N) { return (N + score::kLmRows - 1) / score::kLmRows;
 // Word ranges of a row tile of fgm_lm_head_logprobs on a device that runs `pairs`
 // CTA pairs at a time: those that fill 1 to 4 waves of pairs, whichever makes
 // waves * (a range's tiles + 1) least; an item's start and end cost about a tile.
-// (The pairs that fit are fewer than half of the SMs where a GPC has an odd number
-// of them; items for half of the SMs left a short second wave: 1.00 ms on 1,021
-// rows and 330 us on 5, against the figures of lm_score.cuh.)
+// (How many pairs fit is asked of the device: 76 on one with 152 SMs.)
 int word_splits(int64_t N, int64_t V, int pairs)
 {
     const int64_t tiles = (V + score::kLmWords - 1) / score::kLmWords, rows = row_tiles(N);
@@ -198,7 +196,9 @@ size_t fgm_lm_head_logprobs_workspace_bytes(int64_t N, int64_t V, int k)
 {
     if (!score_sizes_ok(N, V, k))
         return 0;
-    return N <= kMaxM ? fgm_logprobs_workspace_bytes(N, V, k) + logits_bytes(N, V) : align_up(part_offset() + sizeof(score::Part) * 2 * static_cast<size_t>(N) * most_splits(N), 256);
+    if (N <= kMaxM)
+        return fgm_logprobs_workspace_bytes(N, V, k) + logits_bytes(N, V);
+    return align_up(part_offset() + sizeof(score::Part) * 2 * static_cast<size_t>(N) * most_splits(N), 256);
 }
 
 int fgm_lm_head_logprobs(const uint16_t *emb, int64_t V, const uint16_t *h, int64_t N, float T, const int32_t *tokens,

@@ -346,8 +346,10 @@ int fgm_verify_step_sample(const fgm_layer *layers, int n_layers, const uint16_t
  *  v_q  [n_blocks][n_kv_heads][D][64 tokens]           tokens contiguous: the product with the
  *                                                      probabilities contracts over them
  *  k_s, v_s  [n_blocks][n_kv_heads]
- * Codes 16-byte aligned. Bytes of tokens that no sequence holds may be
- * anything, NaN codes included. */
+ * Codes 16-byte aligned. Bytes of tokens that no row of an attention call sees
+ * may be anything, NaN codes included; the codes that a row sees must be
+ * numbers, and the scales of their blocks positive powers of two (what
+ * fgm_kv_append writes). */
 typedef struct fgm_kv_cache {
     uint8_t *k_q;
     float *k_s;
@@ -374,7 +376,9 @@ typedef struct fgm_kv_cache {
  *               token_stride a multiple of 8, at least n_kv_heads * D)
  *  lens         int32 [B] (device) tokens of each sequence, the new ones included
  *  block_table  int32 [B][max_blocks] (device): cache block of a sequence's j-th block; NULL: block
- *               b * max_blocks + j. Blocks that the call writes may not be shared by two sequences.
+ *               b * max_blocks + j. Blocks that the call writes may not be shared by two sequences,
+ *               nor by two blocks of one.
+ *  1 <= B <= 1024, 1 <= N <= 2^24, 1 <= max_blocks <= 2^24
  *  ws           any initialised workspace (for the status word) */
 int fgm_kv_append(const fgm_kv_cache *cache, const uint16_t *k, const uint16_t *v, int64_t token_stride, int B, int N,
                   const int32_t *lens, const int32_t *block_table, int max_blocks, void *ws, size_t ws_bytes,
@@ -398,7 +402,9 @@ size_t fgm_attn_workspace_bytes(int B, int M, int n_q_heads, int n_kv_heads, int
  * with a non-finite query element is NaN. The same call gives the same bits.
  *  q            bf16 [B][M][n_q_heads][D], 16-byte aligned; tokens token_stride elements apart
  *               (a multiple of 8, at least n_q_heads * D), sequences M * token_stride
- *  lens, block_table, max_blocks   as fgm_kv_append; two sequences may share blocks
+ *  lens, block_table, max_blocks   as fgm_kv_append; two sequences may share blocks.
+ *               B * max_blocks * n_kv_heads <= 2^30, n_blocks * n_kv_heads * D < 2^31
+ *  M            1 <= M <= 8, and M * n_q_heads / n_kv_heads <= FGM_ATTN_MAX_ROWS
  *  scale        finite, > 0
  *  window       0: every earlier position; else that many, the row's own included
  *  out          bf16 [B][M][n_q_heads][D] output, 16-byte aligned
@@ -446,8 +452,10 @@ size_t fgm_lm_head_logprobs_workspace_bytes(int64_t N, int64_t V, int k);
 
 /* The same from hidden rows: log probabilities under the tied lm_head's logits
  * z[n][v] = sum_j emb[v][j] * h[n][j] (fp32 accumulation) of N rows, one for a
- * decoded token, M for a verify step, thousands for a scored text. The logits
- * are not stored; every sum over them is fp32. Arguments as fgm_logprobs, and
+ * decoded token, M for a verify step, thousands for a scored text. Every sum over
+ * the logits is fp32. More than 8 rows: they are not stored. Up to 8 rows: the
+ * persistent lm_head kernel writes them into the workspace, which must be
+ * initialised and in use by no other call meanwhile. Arguments as fgm_logprobs, and
  *  emb  bf16 [V][2816] (16-byte aligned), 1 <= V < 2^31
  *  h    bf16 [N][2816] final hidden states (16-byte aligned), 1 <= N <= 2^24 */
 int fgm_lm_head_logprobs(const uint16_t *emb, int64_t V, const uint16_t *h, int64_t N, float T, const int32_t *tokens,
@@ -460,7 +468,8 @@ int fgm_lm_head_logprobs(const uint16_t *emb, int64_t V, const uint16_t *h, int6
 int fgm_select_path(int path);
 
 /* Upper bound, in ns of GPU time, on every wait inside the persistent kernel
- * (grid barriers, ring slots). When a wait runs out the kernel raises
+ * (grid barriers, ring slots) and inside those of fgm_attn_fwd and
+ * fgm_lm_head_logprobs (there each wait has the limit to itself). When a wait runs out the kernel raises
  * FGM_STATUS_WAIT_TIMEOUT, skips its remaining work and exits; its outputs are
  * then invalid. Default 2 s; ns < 0 only queries. Returns the previous value. */
 long long fgm_set_wait_limit_ns(long long ns);
@@ -503,7 +512,9 @@ int fgm_read_status(void *ws, size_t ws_bytes, int clear, int32_t *status, void 
  * (index = slot), 12 = second home slot's operand built (9 is no longer
  * reported). When every CTA stops at a grid barrier, the first report may
  * come from the barrier (6) or from a producer waiting for the routing that
- * the barrier holds back (2). Synchronises the stream. */
+ * the barrier holds back (2). 13 to 28: a wait of fgm_attn_fwd (index = the
+ * CTA's unit of 128 tokens); 30 to 33: of fgm_lm_head_logprobs on more than 8
+ * rows (30 copies, 31 and 32 products, 33 sums). Synchronises the stream. */
 int fgm_read_wait_report(void *ws, size_t ws_bytes, int32_t *report, void *stream);
 
 /* Message describing the last error returned on the calling thread. */

@@ -238,6 +238,27 @@ def test_attn_many_short_and_one_long(fgm, ws):
     assert ws.status() == 0
 
 
+@pytest.mark.parametrize("H,G,M,D,B", [(1, 8, 8, 256, 260), (2, 8, 8, 128, 150), (1, 6, 8, 256, 200), (3, 4, 8, 64, 130),
+                                       (1, 1, 1, 64, 1024)])
+def test_attn_many_sequences_of_many_rows(fgm, H, G, M, D, B):
+    """More (sequence, head)s than CTAs at the widest products, where a CTA goes
+    through several with one or two query buffers; empty ones in between."""
+    rs = np.random.RandomState(B)
+    lens = [int(n) if e else 0 for n, e in zip(rs.randint(1, 300, B), rs.randint(0, 5, B))]
+    tab = torch.zeros(B, 5, dtype=torch.int32)
+    at = 0
+    for b, n in enumerate(lens):
+        m = (n + 63) // 64
+        tab[b, :m] = torch.arange(at, at + m)
+        at += m
+    c = random_cache(fgm, at, H, D, seed=B)
+    ws = fgm.Workspace("cuda", nbytes=fgm.attn_workspace_bytes(B, M, H * G, H, D))
+    q = (torch.randn(B, M, H * G, D, generator=torch.Generator().manual_seed(B)) * 2).bfloat16().cuda()
+    for window in (0, 70):
+        attn_case(fgm, ws, c, q, lens, tab, D ** -0.5, window)
+    assert ws.status() == 0
+
+
 def test_attn_sink_and_extreme_scores(fgm, ws):
     """A first token far above a flat body; scores of hundreds; uneven block scales."""
     H, G, M, D, L = 1, 4, 5, 128, 3000
