@@ -420,17 +420,17 @@ int host_rows64_map(CUtensorMap *map, const void *base, uint64_t rows, uint32_t 
     return FGM_OK;
 }
 
-// Tensor map over bf16 rows of the hidden width, boxes of box_rows rows x 64
-// elements in the 128-byte swizzle (host.h).
-int host_hidden_map(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows)
+// Tensor map over bf16 rows of the hidden width as slices of 64 elements (x: element, y: row, z: slice), boxes of
+// `slices` slices of box_rows rows, one slice after the other in the 128-byte swizzle (host.h).
+int host_hidden_map(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows, uint32_t slices)
 {
     EncodeTiledFn encode = nullptr;
     FGM_TRY(encode_tiled_fn(&encode));
-    const cuuint64_t dims[2] = {kH, rows};
-    const cuuint64_t strides[1] = {2 * kH};
-    const cuuint32_t box[2] = {64, box_rows};
-    const cuuint32_t estr[2] = {1, 1};
-    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+    const cuuint64_t dims[3] = {64, rows, kH / 64};
+    const cuuint64_t strides[2] = {2 * kH, 128};
+    const cuuint32_t box[3] = {64, box_rows, slices};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)

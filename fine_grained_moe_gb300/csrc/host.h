@@ -19,7 +19,7 @@ int host_device_ready(int *sms);
 long long host_wait_limit_ns();
 int host_rows64_map(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows);
 int host_lm_logits(const uint16_t *emb, int64_t V, const uint16_t *h, int M, float *z, void *ws, void *stream);
-int host_hidden_map(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows);
+int host_hidden_map(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows, uint32_t slices);
 
 inline int failf(int code, const char *fmt, ...)
 {

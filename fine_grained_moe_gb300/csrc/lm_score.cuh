@@ -131,12 +131,12 @@ __device__ __forceinline__ void lm_commit(unsigned long long *bar)
         : "memory");
 }
 
-__device__ __forceinline__ void lm_copy(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
+__device__ __forceinline__ void lm_copy(uint32_t dst, const CUtensorMap *map, int y, int z, uint32_t bar, uint64_t policy)
 {
     asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(
             dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(bar), "l"(policy)
         : "memory");
 }
 
@@ -225,6 +225,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
         if (lane == 0) {
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&hmap)) : "memory");
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&emap)) : "memory");
+            uint64_t words, rows;
+            asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(rows));
+            if (p.items == p.splits)
+                asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(words));
+            else
+                asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(words));
             bool ok = true;
             uint32_t n = 0;
             for (int64_t item = pair; item < p.items && ok; item += pairs) {
@@ -243,13 +249,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
                             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(&sh.full[slot])),
                                          "r"(both)
                                          : "memory");
-#pragma unroll
-                        for (int b = 0; b < kLmBoxes; ++b) {
-                            const int x = (ks * kLmBoxes + b) * 64;
-                            lm_copy(dst + words_at + b * kLmBox, &emap, x, t * kLmWords + rank * 128, bar);
-                            if (y < p.N)
-                                lm_copy(dst + b * h_box, &hmap, x, y, bar);
-                        }
+                        lm_copy(dst + words_at, &emap, t * kLmWords + rank * 128, ks * kLmBoxes, bar, words);
+                        if (y < p.N)
+                            lm_copy(dst, &hmap, y, ks * kLmBoxes, bar, rows);
                     }
             }
             // every issued copy lands before the pair may exit (the first CTA sees both CTAs' bytes)
@@ -322,7 +324,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
             int32_t li[L];
 #pragma unroll
             for (int j = 0; j < L; ++j) {
-                lv[j] = -INFINITY;
+                lv[j] = __int_as_float(0x7FC00000);
                 li[j] = kNone;
             }
             for (int t = t0; t < t1; ++t, ++tile) {
@@ -353,33 +355,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
                         for (int j = 0; j < 16; ++j)
                             v[j] = v0 + j < p.V ? v[j] : -INFINITY;
                     const float mx = fold(s, v, c, nan);
-                    if (mx <= lv[L - 1] && li[L - 1] != kNone)
+                    if (mx <= lv[L - 1])
                         continue;
-                    // (words come in order: an equal logit later does not replace an earlier one)
+                    // (words come in order: an equal logit later does not replace an earlier one; an empty place's NaN
+                    // is below everything)
                     unsigned in = 0;
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        in |= v[j] > lv[L - 1] || (li[L - 1] == kNone && v0 + j < p.V) ? 1u << j : 0u;
+                        in |= !(v[j] <= lv[L - 1]) ? 1u << j : 0u;
+                    if (v0 + 16 > p.V)
+                        in &= v0 < p.V ? (1u << (p.V - v0)) - 1 : 0u;
                     for (; in; in &= in - 1) {
                         const int j = __ffs(in) - 1;
-                        float x = v[0];
+                        float x[8];
 #pragma unroll
-                        for (int q = 1; q < 16; ++q)
-                            x = j == q ? v[q] : x;
-                        if (!better(x, v0 + j, lv[L - 1], li[L - 1]))
-                            continue;
-                        lv[L - 1] = x;
-                        li[L - 1] = v0 + j;
+                        for (int q = 0; q < 8; ++q)
+                            x[q] = j & 8 ? v[q + 8] : v[q];
 #pragma unroll
-                        for (int q = L - 1; q > 0; --q)
-                            if (better(lv[q], li[q], lv[q - 1], li[q - 1])) {
-                                const float tv = lv[q];
-                                const int32_t ti = li[q];
-                                lv[q] = lv[q - 1];
-                                li[q] = li[q - 1];
-                                lv[q - 1] = tv;
-                                li[q - 1] = ti;
-                            }
+                        for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+                            for (int q = 0; q < o; ++q)
+                                x[q] = j & o ? x[q + o] : x[q];
+                        // every place at once: the one above's entry where that is beaten, else the new one or its own
+#pragma unroll
+                        for (int q = L - 1; q >= 0; --q) {
+                            const bool here = !(x[0] <= lv[q]), above = q > 0 && !(x[0] <= lv[q > 0 ? q - 1 : 0]);
+                            lv[q] = above ? lv[q > 0 ? q - 1 : 0] : here ? x[0] : lv[q];
+                            li[q] = above ? li[q > 0 ? q - 1 : 0] : here ? v0 + j : li[q];
+                        }
                     }
                 }
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -396,7 +399,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
                 o->nan = nan;
 #pragma unroll
                 for (int j = 0; j < L; ++j) {
-                    o->v[j] = lv[j];
+                    o->v[j] = lv[j] == lv[j] ? lv[j] : -INFINITY;
                     o->i[j] = li[j];
                 }
             }

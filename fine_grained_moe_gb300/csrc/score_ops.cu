@@ -123,8 +123,8 @@ int run_lm_score(const uint16_t *emb, const uint16_t *h, score::LmArgs &a, const
     a.h_rows = a.N < 128 ? static_cast<int>(align_up(a.N, 8)) : 128;
     const int stage = score::kLmBoxes * (a.h_rows * 128 + score::kLmBox), fit = (score::kLmSmem - 1024) / stage;
     a.stages = fit < score::kLmStages ? fit : score::kLmStages;
-    FGM_HOST_TRY(host_hidden_map(&hmap, h, a.N, a.h_rows));
-    FGM_HOST_TRY(host_hidden_map(&emap, emb, a.V, 128));
+    FGM_HOST_TRY(host_hidden_map(&hmap, h, a.N, a.h_rows, score::kLmBoxes));
+    FGM_HOST_TRY(host_hidden_map(&emap, emb, a.V, 128, score::kLmBoxes));
     static int fit_pairs[64];                  // CTA pairs at a time, per device; finding it twice does no harm
     int dev = 0;
     FGM_HOST_CUDA(cudaGetDevice(&dev));
