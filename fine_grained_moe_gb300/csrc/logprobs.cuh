@@ -68,10 +68,39 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-__device__ __forceinline__ float max_nan(float a, float b)
+__device__ __forceinline__ float max_nan(float a, float b, float c)
 {
     float y;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+// Two fp32 in a register pair, for the packed multiply-add.
+__device__ __forceinline__ uint64_t pack2(float a, float b)
+{
+    uint64_t y;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+__device__ __forceinline__ float2 unpack2(uint64_t x)
+{
+    float2 y;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t y;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(a), "l"(b), "l"(c));
+    return y;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t y;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
     return y;
 }
 
@@ -122,8 +151,8 @@ __device__ __forceinline__ float fold(Sums &s, float (&v)[kVals], float c, int &
 {
     float mx = v[0];
 #pragma unroll
-    for (int j = 1; j < kVals; ++j)
-        mx = max_nan(mx, v[j]);
+    for (int j = 1; j < kVals; j += 2)
+        mx = max_nan(mx, v[j], v[j + 1 < kVals ? j + 1 : j]);
     if (mx != mx) {
         nan = 1;
         mx = -INFINITY;
@@ -137,16 +166,21 @@ __device__ __forceinline__ float fold(Sums &s, float (&v)[kVals], float c, int &
         s.rise(mx, c);
     float l0 = 0.0f, l1 = 0.0f, w0 = 0.0f, w1 = 0.0f;
     if (fabsf(s.m) < 1.0e30f) {            // one fused step: z c overflows only where the result is below the clamp
-        const float mc = s.m * c;
+        const uint64_t cc = pack2(c, c), mc = pack2(-s.m * c, -s.m * c);
+        uint64_t l2[2] = {0, 0}, w2[2] = {0, 0};
 #pragma unroll
         for (int j = 0; j < kVals; j += 2) {
-            const float d0 = fmaxf(fmaf(v[j], c, -mc), kClamp), d1 = fmaxf(fmaf(v[j + 1], c, -mc), kClamp);
-            const float e0 = ex2(d0), e1 = ex2(d1);
-            l0 += e0;
-            l1 += e1;
-            w0 = fmaf(e0, d0, w0);
-            w1 = fmaf(e1, d1, w1);
+            const float2 d = unpack2(fma2(pack2(v[j], v[j + 1]), cc, mc));
+            const float d0 = fmaxf(d.x, kClamp), d1 = fmaxf(d.y, kClamp);
+            const uint64_t e = pack2(ex2(d0), ex2(d1));
+            l2[j >> 1 & 1] = add2(l2[j >> 1 & 1], e);
+            w2[j >> 1 & 1] = fma2(e, pack2(d0, d1), w2[j >> 1 & 1]);
         }
+        const float2 l = unpack2(add2(l2[0], l2[1])), w = unpack2(add2(w2[0], w2[1]));
+        l0 = l.x;
+        l1 = l.y;
+        w0 = w.x;
+        w1 = w.y;
     } else {
 #pragma unroll
         for (int j = 0; j < kVals; ++j) {
