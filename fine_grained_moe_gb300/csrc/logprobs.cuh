@@ -149,10 +149,12 @@ struct Sums {
 // Returns the largest.
 __device__ __forceinline__ float fold(Sums &s, float (&v)[kVals], float c, int &nan)
 {
-    float mx = v[0];
-#pragma unroll
-    for (int j = 1; j < kVals; j += 2)
-        mx = max_nan(mx, v[j], v[j + 1 < kVals ? j + 1 : j]);
+    float mx;                              // in three levels
+    {
+        const float a = max_nan(v[0], v[1], v[2]), b = max_nan(v[3], v[4], v[5]), d = max_nan(v[6], v[7], v[8]);
+        const float e = max_nan(v[9], v[10], v[11]), f = max_nan(v[12], v[13], v[14]);
+        mx = max_nan(max_nan(a, b, d), max_nan(e, f, v[15]), v[15]);
+    }
     if (mx != mx) {
         nan = 1;
         mx = -INFINITY;
