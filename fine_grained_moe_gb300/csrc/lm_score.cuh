@@ -3,25 +3,29 @@
 // with the sums of logprobs.cuh in its epilogue, so that logits are never stored.
 //
 // 2 * 2816 operations a logit: bound by the tensor pipe from about 300 rows on,
-// by the embedding's 1.48 GB below. 1,021 rows of 262,144 words take 0.99 ms, 1.5
-// PFLOP/s: the products 0.87 to 0.89, with the tensor pipe 70 to 74 % busy and the
-// copies from L2 at 56 of the 64 bytes a cycle and SM, the last epilogue and the
-// join 0.02 each. (Smaller calls: fgm_lm_head_logprobs gives up to 8 rows to the
-// persistent lm_head kernel.) Built for the tensor pipe: a pair of CTAs
+// by the embedding's 1.48 GB below. 1,021 rows of 262,144 words take 0.85 ms, 1.77
+// PFLOP/s: the products 0.80 with the tensor pipe 92 % busy, the join 0.02, the
+// rest starts and the last epilogue. 16 rows take 247 us, 6.0 TB/s, and 256 rows
+// 273 us. (Up to 8 rows are the persistent lm_head kernel's.) Rows are taken 256 at
+// a time: 300 cost what 512 do, 0.43 ms. Built for the tensor pipe: a pair of CTAs
 // (cta_group::2) holds 256 rows x 256 words in tensor memory, each CTA loading
 // its 128 rows and half of the words, 64 bytes per cycle and SM at the full rate
 // where one CTA on 128 x 256 would need 96.
-//  * TMA copies boxes of 128 rows x 128 bytes (64 elements of K) in the 128-byte
-//    swizzle into a ring (6 stages; 11 for a few rows, whose copies are no larger
-//    than the rows), the second CTA's bytes counted on the first's
+//  * TMA copies boxes of two slices of 128 rows x 128 bytes (64 elements of K) in
+//    the 128-byte swizzle into a ring (3 stages; 6 for a few rows, whose copies are
+//    no larger than the rows), the second CTA's bytes counted on the first's
 //    barriers; rows past N and words past V arrive as zeros.
 //  * The first CTA's issuing warp runs M = 256, N = 256, K = 16 products into one
 //    of two accumulators (2 x 256 columns), so that the next tile's products run
 //    under this tile's epilogue.
 //  * Eight epilogue warps per CTA own a row and half of a tile's columns a
-//    thread: 16 at a time the logits go into the running (m, l, w), and those that beat the row's L-th best (L =
-//    12, or 20 for more than 8 alternatives) into its list, sorted in registers.
-//    A row meets about L (1 + ln(n / L)) such logits among n.
+//    thread: 16 at a time the logits go into the running (m, l, w), and those that
+//    beat the row's L-th best (L = 12, or 20 for more than 8 alternatives) into
+//    its list, sorted in registers. A row meets about L (1 + ln(n / L)) such logits
+//    among n, and a warp waits for each of its 32 rows' in turn, so an insertion
+//    decides every place of the list at once (five instructions a place and none
+//    that waits for another: with a bubble pass through the list the epilogue was
+//    longer than the products, 333 us on 16 rows, 0.91 ms on 1,021).
 //  * An item is 256 rows x a range of words; a pair takes items in turn, a row's
 //    state stays in registers over the range, and k_lm_join merges the ranges.
 //

@@ -39,10 +39,12 @@ int check_scores(int64_t N, int64_t V, float T, const int32_t *tokens, int k, co
 
 // Splits of a row. 608 CTAs run at a time (152 SMs, four each); a CTA's start and
 // end (first loads, the k best, the sums) take about as long as 56 KB of its
-// share of HBM: the number of splits that makes waves * (56 KB + a split's bytes)
-// least. 1,013 rows of 100 KB: one split 28 us, four 51 us (measured); 600 rows
-// of 1 MB: one; 5 rows of 1 MB: 32. A split has 8,192 logits at least. A function
-// of the sizes alone, so that results do not depend on the device.
+// share of HBM, and the join of split rows as long as 80 KB: the number of splits
+// that makes waves * (56 KB + a split's bytes) + 80 KB least. Measured: 1,013 rows
+// of 100 KB, one split 28 us, four 51 us; 300 rows of 100 KB, one 13.9 us, two
+// 17.0; 152 rows of 64 KB, one 7.7 us, three 10.0; 5 rows of 1 MB: 32. A split has
+// 8,192 logits at least. A function of the sizes alone, so that results do not
+// depend on the device.
 int64_t most_row_splits(int64_t N, int64_t V)
 {
     const int64_t by_grid = 8 * 608 / N + 1, by_size = V / 8192;
@@ -55,7 +57,7 @@ int row_splits(int64_t N, int64_t V, int64_t elem)
     const int64_t most = most_row_splits(N, V);
     int64_t best = 1, cost = 0;
     for (int64_t s = 1; s <= most; ++s) {
-        const int64_t c = (N * s + 607) / 608 * (56 * 1024 + V * elem / s);
+        const int64_t c = (N * s + 607) / 608 * (56 * 1024 + V * elem / s) + (s > 1 ? 80 * 1024 : 0);
         if (s == 1 || c < cost) {
             best = s;
             cost = c;
@@ -213,8 +215,8 @@ int fgm_lm_head_logprobs(const uint16_t *emb, int64_t V, const uint16_t *h, int6
     FGM_HOST_TRY(host_device_ready(&sms));
     const score::Outs o = outs(tokens, logp, entropy, top_ids, top_logp, k, T, V, ws);
     if (N <= kMaxM) {
-        // The persistent lm_head kernel, whose whole-row copies stream the embedding at 6.5 TB/s where the pair
-        // kernel's boxes reach 5.2, with its logits (0.4 % of the bytes) scored by k_logprobs.
+        // The persistent lm_head kernel, whose whole-row copies stream the embedding at 6.8 TB/s where the pair
+        // kernel's boxes reach 6.0 (5 rows 217 us, 9 rows 247), with its logits (0.4 % of the bytes) scored by k_logprobs.
         char *z = static_cast<char *>(ws) + fgm_logprobs_workspace_bytes(N, V, k);
         FGM_HOST_TRY(host_lm_logits(emb, V, h, static_cast<int>(N), reinterpret_cast<float *>(z), ws, stream));
         return run_logprobs<float>(z, V, N, o, ws, static_cast<cudaStream_t>(stream));
