@@ -312,7 +312,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
     } else if (warp >= 4) {
         // ------------------------------------------------------------ epilogue: a thread is a row, of half the columns
         const int quarter = warp & 3, r = quarter * 32 + lane, half = (warp - 4) >> 2;
-        const float c = kLog2e / p.T;
+        const float c = per_nat(p.T);
         bool alive = true;
         uint32_t tile = 0;
         for (int64_t item = pair; item < p.items; item += pairs) {
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_lm_join(const uint16_t *emb
     __shared__ Sums s_sum[kJoinWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t row = blockIdx.x;
-    const float c = kLog2e / o.T;
+    const float c = per_nat(o.T);
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int32_t tok = o.logp ? __ldg(o.tokens + row) : -1;

@@ -97,12 +97,22 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
     return y;
 }
 
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t y;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+    return y;
+}
+
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 {
     uint64_t y;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
     return y;
 }
+
+// log2(e) / T, held to a finite number (T down to the smallest with 1 / T finite).
+__device__ __forceinline__ float per_nat(float T) { return fminf(kLog2e / T, 3.4028235e38f); }
 
 // An order of floats as unsigned integers (NaN does not occur; -0 is 0).
 __device__ __forceinline__ unsigned ordered(float x)
@@ -166,33 +176,21 @@ __device__ __forceinline__ float fold(Sums &s, float (&v)[kVals], float c, int &
     }
     if (mx > s.m)
         s.rise(mx, c);
-    float l0 = 0.0f, l1 = 0.0f, w0 = 0.0f, w1 = 0.0f;
-    if (fabsf(s.m) < 1.0e30f) {            // one fused step: z c overflows only where the result is below the clamp
-        const uint64_t cc = pack2(c, c), mc = pack2(-s.m * c, -s.m * c);
-        uint64_t l2[2] = {0, 0}, w2[2] = {0, 0};
+    // (z - m) c, the difference first: it is exact near the maximum, where z c - m c would be off by m c's rounding, all
+    // of a term at a low temperature. (What is not a number, -inf from -inf, the clamp takes too.)
+    const uint64_t cc = pack2(c, c), nm = pack2(-s.m, -s.m);
+    uint64_t l2[2] = {0, 0}, w2[2] = {0, 0};
 #pragma unroll
-        for (int j = 0; j < kVals; j += 2) {
-            const float2 d = unpack2(fma2(pack2(v[j], v[j + 1]), cc, mc));
-            const float d0 = fmaxf(d.x, kClamp), d1 = fmaxf(d.y, kClamp);
-            const uint64_t e = pack2(ex2(d0), ex2(d1));
-            l2[j >> 1 & 1] = add2(l2[j >> 1 & 1], e);
-            w2[j >> 1 & 1] = fma2(e, pack2(d0, d1), w2[j >> 1 & 1]);
-        }
-        const float2 l = unpack2(add2(l2[0], l2[1])), w = unpack2(add2(w2[0], w2[1]));
-        l0 = l.x;
-        l1 = l.y;
-        w0 = w.x;
-        w1 = w.y;
-    } else {
-#pragma unroll
-        for (int j = 0; j < kVals; ++j) {
-            const float d = fmaxf((v[j] - s.m) * c, kClamp), e = ex2(d);
-            l0 += e;
-            w0 = fmaf(e, d, w0);
-        }
+    for (int j = 0; j < kVals; j += 2) {
+        const float2 d = unpack2(mul2(add2(pack2(v[j], v[j + 1]), nm), cc));
+        const float d0 = fmaxf(d.x, kClamp), d1 = fmaxf(d.y, kClamp);
+        const uint64_t e = pack2(ex2(d0), ex2(d1));
+        l2[j >> 1 & 1] = add2(l2[j >> 1 & 1], e);
+        w2[j >> 1 & 1] = fma2(e, pack2(d0, d1), w2[j >> 1 & 1]);
     }
-    s.l += l0 + l1;
-    s.w += w0 + w1;
+    const float2 l = unpack2(add2(l2[0], l2[1])), w = unpack2(add2(w2[0], w2[1]));
+    s.l += l.x + l.y;
+    s.w += w.x + w.y;
     return mx;
 }
 
@@ -379,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     const uint4 *zv = reinterpret_cast<const uint4 *>(zr + head);
     const int v0 = static_cast<int>(static_cast<int64_t>(nvec) * split / splits);
     const int v1 = static_cast<int>(static_cast<int64_t>(nvec) * (split + 1) / splits);
-    const float c = kLog2e / o.T;
+    const float c = per_nat(o.T);
 
     float zt = -INFINITY;                      // the given token's logit
     if (splits == 1 && o.logp && tid == 0) {
@@ -590,7 +588,7 @@ __global__ void __launch_bounds__(kThreads)
     const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
     if (row >= N)
         return;
-    const float c = kLog2e / o.T;
+    const float c = per_nat(o.T);
     float zt = -INFINITY;
     if (o.logp) {
         const int32_t t = __ldg(o.tokens + row);

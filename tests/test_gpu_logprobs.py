@@ -84,6 +84,32 @@ def test_matches_plain(fgm, ws, dt, N, V, k, T):
     check(fgm, ws, z.to(DT[dt]), tokens, k, T)
 
 
+@pytest.mark.parametrize("T", [2.95e-39, 1e-38, 1e-30, 1e-6, 1e-3, 0.05, 1e4, 1e30])
+@pytest.mark.parametrize("N,V", [(3, 1000), (2, 70001)])
+def test_extreme_temperatures(fgm, ws, N, V, T):
+    """From a one-hot to a uniform distribution. Differences from the largest
+    logit carry 2^-24 of themselves and their product with log2(e) / T 2^-22, up
+    to 200 binary places down: e |d| <= 0.54, so a term's error is below 2^-22 of
+    the sum and the bounds need no part that grows with |z| / T, but the given
+    token's own (z - m) / T: |err| <= 2^-18 + 2^-22 (|logp| + ln V)."""
+    g = torch.Generator().manual_seed(V)
+    z = torch.randn(N, V, generator=g) * 3 + 9
+    top = z.argmax(dim=1)
+    z[0, 5] = z[0, top[0]]                     # a tie for the first place
+    tokens = [int(top[0]), 7, int(top[2])][:N] if N == 3 else [int(top[0]), int(top[1])]
+    r = fgm.logprobs(z.cuda(), torch.tensor(tokens, dtype=torch.int32, device="cuda"), k=4, T=T, ws=ws)
+    assert ws.status() == 0
+    T32 = float(np.float32(T))
+    lp, ent, ids, tlp = plain64.logprobs(z.double().numpy(), tokens, 4, T32)
+    np.testing.assert_array_equal(r.top_ids.cpu().numpy(), ids)
+    for got, want in ((r.logp, lp), (r.top_logp, tlp), (r.entropy, ent)):
+        got = got.cpu().double().numpy()
+        want = np.where(want < -3.4028235677973366e38, -np.inf, want)
+        fin = np.isfinite(want)
+        np.testing.assert_array_equal(got[~fin], want[~fin])
+        assert (np.abs(got[fin] - want[fin]) <= 2.0 ** -18 + 2.0 ** -22 * (np.abs(want[fin]) + np.log(V))).all(), (got, want)
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
 def test_rows_of_any_alignment_and_distance(fgm, ws, dt):
     """Views whose rows start at every offset within 16 bytes; what lies between the rows is not read as logits."""
