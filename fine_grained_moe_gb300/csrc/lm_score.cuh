@@ -3,11 +3,11 @@
 // with the sums of logprobs.cuh in its epilogue, so that logits are never stored.
 //
 // 2 * 2816 operations a logit: bound by the tensor pipe from about 300 rows on,
-// by the embedding's 1.48 GB below. 1,021 rows of 262,144 words take 0.85 ms, 1.77
+// by the embedding's 1.48 GB below. 1,021 rows of 262,144 words take 0.84 ms, 1.80
 // PFLOP/s: the products 0.80 with the tensor pipe 92 % busy, the join 0.02, the
-// rest starts and the last epilogue. 16 rows take 247 us, 6.0 TB/s, and 256 rows
-// 273 us. (Up to 8 rows are the persistent lm_head kernel's.) Rows are taken 256 at
-// a time: 300 cost what 512 do, 0.43 ms. Built for the tensor pipe: a pair of CTAs
+// rest starts and the last epilogue. 16 rows take 253 us, 5.8 TB/s, and 256 rows
+// 279 us. (Up to 8 rows are the persistent lm_head kernel's.) Rows are taken 256 at
+// a time: 300 cost what 512 do, 0.44 ms. Built for the tensor pipe: a pair of CTAs
 // (cta_group::2) holds 256 rows x 256 words in tensor memory, each CTA loading
 // its 128 rows and half of the words, 64 bytes per cycle and SM at the full rate
 // where one CTA on 128 x 256 would need 96.
@@ -337,8 +337,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
                     alive = wait(&sh.tfull[buf], tile >> 1, 33, t);
                 alive = __all_sync(0xFFFFFFFFu, alive);
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                for (int c0 = half * (kLmWords / 2); live && c0 < (half + 1) * (kLmWords / 2); c0 += 16) {
-                    uint32_t u[16];
+                // 16 columns at a time, the next on their way meanwhile
+                uint32_t u[2][16];
+                const int c_end = live ? (half + 1) * (kLmWords / 2) : 0;
+                auto load = [&](int c0, uint32_t (&u)[16]) {
                     asm volatile(
                         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
                         "%14, %15}, [%16];"
@@ -346,6 +348,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
                           "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
                         : "r"(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kLmWords + c0)
                         : "memory");
+                };
+                auto columns = [&](int c0, uint32_t (&u)[16], uint32_t (&ahead)[16]) {
+                    __syncwarp();
                     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
                     float v[kVals];
 #pragma unroll
@@ -353,6 +358,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
                         asm volatile("" : "+r"(u[j]));
                         v[j] = __uint_as_float(u[j]);
                     }
+                    if (c0 + 16 < c_end)
+                        load(c0 + 16, ahead);
                     const int v0 = t * kLmWords + c0;
                     if (v0 + 16 > p.V)
 #pragma unroll
@@ -360,7 +367,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
                             v[j] = v0 + j < p.V ? v[j] : -INFINITY;
                     const float mx = fold(s, v, c, nan);
                     if (mx <= lv[L - 1])
-                        continue;
+                        return;
                     // (words come in order: an equal logit later does not replace an earlier one; an empty place's NaN
                     // is below everything)
                     unsigned in = 0;
@@ -387,6 +394,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
                             lv[q] = above ? lv[q > 0 ? q - 1 : 0] : here ? x[0] : lv[q];
                             li[q] = above ? li[q > 0 ? q - 1 : 0] : here ? v0 + j : li[q];
                         }
+                    }
+                };
+                if (live) {
+                    load(half * (kLmWords / 2), u[0]);
+                    for (int c0 = half * (kLmWords / 2); c0 < c_end; c0 += 32) {
+                        columns(c0, u[0], u[1]);
+                        columns(c0 + 16, u[1], u[0]);
                     }
                 }
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");

@@ -216,7 +216,7 @@ int fgm_lm_head_logprobs(const uint16_t *emb, int64_t V, const uint16_t *h, int6
     const score::Outs o = outs(tokens, logp, entropy, top_ids, top_logp, k, T, V, ws);
     if (N <= kMaxM) {
         // The persistent lm_head kernel, whose whole-row copies stream the embedding at 6.8 TB/s where the pair
-        // kernel's boxes reach 6.0 (5 rows 217 us, 9 rows 247), with its logits (0.4 % of the bytes) scored by k_logprobs.
+        // kernel's boxes reach 5.9 (5 rows 217 us, 9 rows 251), with its logits (0.4 % of the bytes) scored by k_logprobs.
         char *z = static_cast<char *>(ws) + fgm_logprobs_workspace_bytes(N, V, k);
         FGM_HOST_TRY(host_lm_logits(emb, V, h, static_cast<int>(N), reinterpret_cast<float *>(z), ws, stream));
         return run_logprobs<float>(z, V, N, o, ws, static_cast<cudaStream_t>(stream));
