@@ -1,5 +1,6 @@
 // C ABI of the 8-bit KV cache (declared in include/fgm.h): argument checks and
 // launches of kv_append.cuh and kv_attn.cuh.
+#include <atomic>
 #include <cmath>
 
 #include "host.h"
@@ -99,7 +100,7 @@ int launch_attn_t(kv::AttnArgs &a, int sms, cudaStream_t st)
     const uint64_t n_rows = static_cast<uint64_t>(a.c.n_blocks) * a.c.heads * D;
     FGM_HOST_TRY(host_rows64_map(&kmap, a.c.k_q, n_rows, kv::kBlock));
     FGM_HOST_TRY(host_rows64_map(&vmap, a.c.v_q, n_rows, D));
-    static bool ready[64];                     // per device; setting it twice does no harm
+    static std::atomic<bool> ready[64];        // per device; setting it twice does no harm
     int dev = 0;
     FGM_HOST_CUDA(cudaGetDevice(&dev));
     if (!ready[dev & 63]) {

@@ -1,5 +1,6 @@
 // C ABI of the log probabilities (declared in include/fgm.h): argument checks
 // and launches of logprobs.cuh and lm_score.cuh.
+#include <atomic>
 #include <cmath>
 
 #include "host.h"
@@ -127,7 +128,7 @@ int run_lm_score(const uint16_t *emb, const uint16_t *h, score::LmArgs &a, const
     a.stages = fit < score::kLmStages ? fit : score::kLmStages;
     FGM_HOST_TRY(host_hidden_map(&hmap, h, a.N, a.h_rows, score::kLmBoxes));
     FGM_HOST_TRY(host_hidden_map(&emap, emb, a.V, 128, score::kLmBoxes));
-    static int fit_pairs[64];                  // CTA pairs at a time, per device; finding it twice does no harm
+    static std::atomic<int> fit_pairs[64];     // CTA pairs at a time, per device; finding it twice does no harm
     int dev = 0;
     FGM_HOST_CUDA(cudaGetDevice(&dev));
     int most = fit_pairs[dev & 63];

@@ -407,7 +407,7 @@ size_t fgm_attn_workspace_bytes(int B, int M, int n_q_heads, int n_kv_heads, int
  *  M            1 <= M <= 8, and M * n_q_heads / n_kv_heads <= FGM_ATTN_MAX_ROWS
  *  scale        finite, > 0
  *  window       0: every earlier position; else that many, the row's own included
- *  out          bf16 [B][M][n_q_heads][D] output, 16-byte aligned
+ *  out          bf16 [B][M][n_q_heads][D] output, 16-byte aligned, apart from q
  *  lse          fp32 [B][M][n_q_heads] output or NULL */
 int fgm_attn_fwd(const fgm_kv_cache *cache, const uint16_t *q, int64_t token_stride, int B, int M, int n_q_heads,
                  const int32_t *lens, const int32_t *block_table, int max_blocks, float scale, int window,
