@@ -14,10 +14,11 @@
 // and an end. (Fewer instructions, six a logit, left both as they are; CTAs of
 // four warps, eight an SM, too, and took 19 to 38 us on 5 rows.)
 //
-// The k best cost nothing in that pass: the k-th largest of the threads' maxima
-// bounds the k-th best logit from below, so only the threads that reach it
-// (k of 256 unless logits tie) can hold one of the k best, and the warps, which
-// share them out, read those threads' logits a second time, from the caches. (Lists kept during the
+// The k best cost nothing in that pass: the k-th largest of 32 maxima, each of 8
+// threads, bounds the k-th best logit from below, so only the threads that reach
+// it (little more than k of 256 unless logits tie) can hold one of the k best, and
+// the warps, which share them out, read those threads' logits a second time, from
+// the caches; the few at or above the bound are ranked by counting. (Lists kept during the
 // pass, with the same bound as a threshold, took 134 us on 1,013 x 50,021 bf16
 // logits, against 15 us of HBM time: the insertions were most of it.)
 //
@@ -36,6 +37,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxTop = FGM_MAX_TOP;
 constexpr int kMaxList = kMaxTop + 4;         // entries of a partial list (lm_score.cuh keeps a few more than asked for)
 constexpr int kVals = 16;                     // logits of a lane and chunk
+constexpr int kCands = 64;                    // logits at or above the bound that are ranked as they are
 constexpr float kClamp = -200.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -360,7 +362,9 @@ __global__ void __launch_bounds__(kThreads, 4)
     constexpr int kVec = L::kVec, kLoads = kVals / kVec, kChunk = 32 * kLoads;      // vectors of a warp's chunk
     constexpr int kDepth = 4 / kLoads;         // chunks on their way: four vectors a lane, 64 KB an SM
     __shared__ unsigned s_max[kThreads], s_bound;
-    __shared__ int s_who[kThreads], s_many;
+    __shared__ int s_who[kThreads], s_many, s_n;
+    __shared__ float s_cv[kCands];
+    __shared__ int32_t s_ci[kCands];
     __shared__ Sums s_sum[kWarps];
     __shared__ float s_v[kWarps][kMaxTop];
     __shared__ int32_t s_i[kWarps][kMaxTop];
@@ -445,35 +449,21 @@ __global__ void __launch_bounds__(kThreads, 4)
         s_max[tid] = ordered(s.m);
         __syncthreads();
         if (warp == 0) {
-            // the k-th largest of the threads' maxima, one round of removal each
-            unsigned x[kWarps], best = 0, kth = 0;
+            // the k-th largest of 32 maxima, of 8 threads each, by counting the larger ones
+            unsigned best = 0;
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) {
-                x[i] = s_max[i * 32 + lane];
-                best = max(best, x[i]);
-            }
-            for (int j = 0; j < k; ++j) {
-                kth = __reduce_max_sync(0xFFFFFFFFu, best);
-                const unsigned b = __ballot_sync(0xFFFFFFFFu, best == kth);
-                if (lane == __ffs(b) - 1) {
-                    bool gone = false;
+            for (int i = 0; i < kWarps; ++i)
+                best = max(best, s_max[i * 32 + lane]);
+            int above = 0;
 #pragma unroll
-                    for (int i = 0; i < kWarps; ++i)
-                        if (!gone && x[i] == kth) {
-                            x[i] = 0;
-                            gone = true;
-                        }
-                    best = 0;
-#pragma unroll
-                    for (int i = 0; i < kWarps; ++i)
-                        best = max(best, x[i]);
-                }
-                __syncwarp();
+            for (int q = 0; q < 32; ++q) {
+                const unsigned x = __shfl_sync(0xFFFFFFFFu, best, q);
+                above += x > best || (x == best && q < lane);
             }
-            if (lane == 0) {
-                s_bound = kth;
-                s_many = 0;
-            }
+            if (above == k - 1)
+                s_bound = best;
+            if (lane == 0)
+                s_many = s_n = 0;
         }
         __syncthreads();
         const float bound = unordered(s_bound);
@@ -481,39 +471,90 @@ __global__ void __launch_bounds__(kThreads, 4)
         if (s.m >= bound)
             s_who[atomicAdd(&s_many, 1)] = tid;
         __syncthreads();
-        for (int w = warp; w < s_many; w += kWarps) {
-            const int who = s_who[w], src = who & 31, start = v0 + (who >> 5) * kChunk + src;
-            if (who < 32 && split == 0 && head + tail > 0) {
-                float v = -INFINITY;
-                int32_t i = kNone;
-                if (lane == 0 ? src < head : lane == 1 && src < tail) {
-                    i = lane == 0 ? src : V - tail + src;
-                    v = L::one(zr + i);
-                    v = v == v ? v : -INFINITY;
+        // every logit of theirs that reaches the bound goes to `take`, which the whole warp calls
+        auto look_again = [&](auto &&take) {
+            for (int w = warp; w < s_many; w += kWarps) {
+                const int who = s_who[w], src = who & 31, start = v0 + (who >> 5) * kChunk + src;
+                if (who < 32 && split == 0 && head + tail > 0) {
+                    float v = -INFINITY;
+                    const int i = lane == 0 ? src : V - tail + src;
+                    const bool in = lane == 0 ? src < head : lane == 1 && src < tail;
+                    if (in) {
+                        v = L::one(zr + i);
+                        v = v == v ? v : -INFINITY;
+                    }
+                    take(in && v >= bound, v, i);
                 }
-                top.offer(v, i, k, lane);
-            }
-            // its logits, a vector a lane
-            for (int n0 = 0;; n0 += 32) {
-                const int n = n0 + lane;       // the thread's n-th vector
-                const int vec = start + n / kLoads * step + n % kLoads * 32;
-                const bool in = vec < v1;
-                if (!__any_sync(0xFFFFFFFFu, in))
-                    break;
-                float v[kVec];
-                if (in)
-                    L::unpack(__ldg(zv + vec), v);
+                // its logits, a vector a lane
+                for (int n0 = 0;; n0 += 32) {
+                    const int n = n0 + lane;   // the thread's n-th vector
+                    const int vec = start + n / kLoads * step + n % kLoads * 32;
+                    const bool in = vec < v1;
+                    if (!__any_sync(0xFFFFFFFFu, in))
+                        break;
+                    float v[kVec];
+                    if (in)
+                        L::unpack(__ldg(zv + vec), v);
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) {
-                    const float x = in && v[j] == v[j] ? v[j] : -INFINITY;
-                    if (__any_sync(0xFFFFFFFFu, in && x >= bound))
-                        top.offer(in && x >= bound ? x : -INFINITY, in && x >= bound ? head + vec * kVec + j : kNone, k, lane);
+                    for (int j = 0; j < kVec; ++j) {
+                        const float x = in && v[j] == v[j] ? v[j] : -INFINITY;
+                        take(in && x >= bound, x, head + vec * kVec + j);
+                    }
                 }
             }
-        }
-        if (lane < k) {
-            s_v[warp][lane] = top.v;
-            s_i[warp][lane] = top.i;
+        };
+        look_again([&](bool in, float x, int i) {
+            if (in) {
+                const int at = atomicAdd(&s_n, 1);
+                if (at < kCands) {
+                    s_cv[at] = x;
+                    s_ci[at] = i;
+                }
+            }
+        });
+        __syncthreads();
+        const int n = s_n;
+        if (n <= kCands) {
+            // few: the first warp ranks them (their order in the list does not matter)
+            if (warp == 0) {
+                float v[2];
+                int32_t i[2];
+                int above[2] = {0, 0};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const bool in = lane + 32 * h < n;
+                    v[h] = in ? s_cv[lane + 32 * h] : -INFINITY;
+                    i[h] = in ? s_ci[lane + 32 * h] : kNone;
+                }
+                for (int q = 0; q < n; ++q)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        above[h] += better(s_cv[q], s_ci[q], v[h], i[h]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (lane + 32 * h < n && above[h] < k) {
+                        s_v[0][above[h]] = v[h];
+                        s_i[0][above[h]] = i[h];
+                    }
+                __syncwarp();
+                if (lane < min(n, k)) {
+                    top.v = s_v[0][lane];
+                    top.i = s_i[0][lane];
+                }
+            }
+        } else {
+            // many that tie: lists of the warps' own, merged
+            look_again([&](bool in, float x, int i) {
+                if (__any_sync(0xFFFFFFFFu, in))
+                    top.offer(in ? x : -INFINITY, in ? i : kNone, k, lane);
+            });
+            if (lane < k) {
+                s_v[warp][lane] = top.v;
+                s_i[warp][lane] = top.i;
+            }
+            __syncthreads();
+            if (warp == 0)
+                merge_lists(s_v[lane & (kWarps - 1)], s_i[lane & (kWarps - 1)], lane < kWarps ? k : 0, k, lane, top.v, top.i);
         }
     }
 
@@ -529,8 +570,6 @@ __global__ void __launch_bounds__(kThreads, 4)
     else
         s.clear();
     s = warp_sums(s, c);
-    if (k)
-        merge_lists(s_v[lane & (kWarps - 1)], s_i[lane & (kWarps - 1)], lane < kWarps ? k : 0, k, lane, top.v, top.i);
     if (splits == 1) {
         write_row(o, row, s, top, nan, zt, lane);
         return;
