@@ -9,7 +9,7 @@
 // and rescales when its maximum grows. Differences are clamped at -200, where e
 // is 0 already, so that -inf (or a type's lowest value) adds 0 and not 0 * inf.
 // About 7 instructions and one exponential a logit. 600 rows of 262,144 fp32
-// logits: 96 us, 6.5 TB/s. 1,013 rows of 50,021 bf16 logits: 29 us, 3.5 TB/s,
+// logits: 96 us, 6.5 TB/s. 1,013 rows of 50,021 bf16 logits: 28 us, 3.6 TB/s,
 // where 1,013 CTAs are 1.7 rounds of the 608 that run at a time, each with a start
 // and an end. (Fewer instructions, six a logit, left both as they are; CTAs of
 // four warps, eight an SM, too, and took 19 to 38 us on 5 rows.)
@@ -22,7 +22,7 @@
 // pass, with the same bound as a threshold, took 134 us on 1,013 x 50,021 bf16
 // logits, against 15 us of HBM time: the insertions were most of it.)
 //
-// Rows are cut into splits until the grid has several CTAs per SM; k_logprob_join
+// Short rows in large numbers have a warp each (k_logprob_rows). Long rows are cut into splits until the grid has several CTAs per SM; k_logprob_join
 // merges a row's splits in order (no atomics on results: the same call gives
 // the same bits).
 #pragma once
@@ -585,6 +585,172 @@ __global__ void __launch_bounds__(kThreads, 4)
         p->v[lane] = top.v;
         p->i[lane] = top.i;
     }
+}
+
+// The same with a warp per row and no split, for rows too short to be worth a
+// CTA's barriers: 57,788 rows of 715 fp32 logits take 83 us where a CTA each took
+// 402 us, 4,000 rows of 8,000 bf16 21 us where it took 35.
+template <typename E>
+__global__ void __launch_bounds__(kThreads, 4) k_logprob_rows(const E *z, int64_t stride, int64_t N, const Outs o)
+{
+    using L = Load<E>;
+    constexpr int kVec = L::kVec, kLoads = kVals / kVec, kChunk = 32 * kLoads;      // vectors of a chunk
+    constexpr int kDepth = 4 / kLoads;         // chunks on their way
+    __shared__ float s_cands[kWarps][kCands], s_tops[kWarps][kMaxTop];
+    __shared__ int32_t s_candi[kWarps][kCands], s_topi[kWarps][kMaxTop];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = o.k;
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    if (row >= N)
+        return;
+    const E *zr = z + row * stride;
+    const int V = static_cast<int>(o.V);
+    // logits before the first 16-byte boundary, whole vectors, the rest
+    const int off = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(zr) & 15u)) & 15u) / static_cast<int>(sizeof(E));
+    const int head = min(V, off), nvec = (V - head) / kVec, tail = V - head - nvec * kVec;
+    const uint4 *zv = reinterpret_cast<const uint4 *>(zr + head);
+    const float c = per_nat(o.T);
+
+    uint4 raw[kDepth][kLoads];
+    auto fetch = [&](int at, uint4 (&r)[kLoads]) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            if (at + i * 32 < nvec)
+                r[i] = __ldg(zv + at + i * 32);
+    };
+    int at = lane;
+#pragma unroll
+    for (int q = 0; q < kDepth; ++q)
+        fetch(at + q * kChunk, raw[q]);
+    float zt = -INFINITY;                      // the given token's logit
+    if (o.logp && lane == 0) {
+        const int32_t t = __ldg(o.tokens + row);
+        if (t >= 0 && t < V)
+            zt = L::one(zr + t);
+        if (zt != zt)
+            zt = -INFINITY;
+    }
+    Sums s;
+    s.clear();
+    int nan = 0;
+    if (head + tail > 0) {
+        float v[kVals];
+#pragma unroll
+        for (int j = 0; j < kVals; ++j)
+            v[j] = -INFINITY;
+        if (lane < head)
+            v[0] = L::one(zr + lane);
+        if (lane < tail)
+            v[1] = L::one(zr + V - tail + lane);
+        fold(s, v, c, nan);
+    }
+    while (at - lane < nvec) {
+#pragma unroll
+        for (int q = 0; q < kDepth; ++q) {
+            if (at - lane < nvec) {
+                float v[kVals];
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i)
+                    L::unpack(raw[q][i], v + i * kVec);
+                if (at - lane + kChunk > nvec) {
+#pragma unroll
+                    for (int i = 0; i < kLoads; ++i)
+                        if (at + i * 32 >= nvec)
+#pragma unroll
+                            for (int j = 0; j < kVec; ++j)
+                                v[i * kVec + j] = -INFINITY;
+                }
+                fetch(at + kDepth * kChunk, raw[q]);
+                fold(s, v, c, nan);
+            }
+            at += kChunk;
+        }
+    }
+
+    TopList top;
+    top.clear();
+    if (k) {
+        // the k-th largest of the lanes' maxima bounds the k-th best logit
+        const unsigned best = ordered(s.m);
+        int above = 0;
+#pragma unroll
+        for (int q = 0; q < 32; ++q) {
+            const unsigned x = __shfl_sync(0xFFFFFFFFu, best, q);
+            above += x > best || (x == best && q < lane);
+        }
+        const float bound = __shfl_sync(0xFFFFFFFFu, s.m, __ffs(__ballot_sync(0xFFFFFFFFu, above == k - 1)) - 1);
+        const unsigned who_mask = __ballot_sync(0xFFFFFFFFu, s.m >= bound);
+        // every logit of the lanes that reach it, read again
+        auto look_again = [&](auto &&take) {
+            for (unsigned left = who_mask; left; left &= left - 1) {
+                const int who = __ffs(left) - 1;
+                if (head + tail > 0) {
+                    float v = -INFINITY;
+                    const int i = lane == 0 ? who : V - tail + who;
+                    const bool in = lane == 0 ? who < head : lane == 1 && who < tail;
+                    if (in) {
+                        v = L::one(zr + i);
+                        v = v == v ? v : -INFINITY;
+                    }
+                    take(in && v >= bound, v, i);
+                }
+                for (int n0 = 0;; n0 += 32) {
+                    const int n = n0 + lane;   // its n-th vector
+                    const int vec = who + n / kLoads * kChunk + n % kLoads * 32;
+                    const bool in = vec < nvec;
+                    if (!__any_sync(0xFFFFFFFFu, in))
+                        break;
+                    float v[kVec];
+                    if (in)
+                        L::unpack(__ldg(zv + vec), v);
+#pragma unroll
+                    for (int j = 0; j < kVec; ++j) {
+                        const float x = in && v[j] == v[j] ? v[j] : -INFINITY;
+                        take(in && x >= bound, x, head + vec * kVec + j);
+                    }
+                }
+            }
+        };
+        float *const cv = s_cands[warp];
+        int32_t *const ci = s_candi[warp];
+        int n = 0;
+        look_again([&](bool in, float x, int i) {
+            const unsigned b = __ballot_sync(0xFFFFFFFFu, in);
+            const int to = n + __popc(b & ((1u << lane) - 1));
+            n += __popc(b);
+            if (in && to < kCands) {
+                cv[to] = x;
+                ci[to] = i;
+            }
+        });
+        __syncwarp();
+        if (n <= kCands) {
+            for (int h = lane; h < n; h += 32) {
+                const float v = cv[h];
+                const int32_t i = ci[h];
+                int ahead = 0;
+                for (int q = 0; q < n; ++q)
+                    ahead += better(cv[q], ci[q], v, i);
+                if (ahead < k) {
+                    s_tops[warp][ahead] = v;
+                    s_topi[warp][ahead] = i;
+                }
+            }
+            __syncwarp();
+            if (lane < min(n, k)) {
+                top.v = s_tops[warp][lane];
+                top.i = s_topi[warp][lane];
+            }
+        } else {
+            look_again([&](bool in, float x, int i) {
+                if (__any_sync(0xFFFFFFFFu, in))
+                    top.offer(in ? x : -INFINITY, in ? i : kNone, k, lane);
+            });
+        }
+    }
+    s = warp_sums(s, c);
+    write_row(o, row, s, top, __any_sync(0xFFFFFFFFu, nan), zt, lane);
 }
 
 // One warp: the sums and the k best (at most 32) of a row's parts.

@@ -67,6 +67,16 @@ int row_splits(int64_t N, int64_t V, int64_t elem)
     return static_cast<int>(best);
 }
 
+// Whether a warp takes a row: the same measure of both, a warp having an eighth of
+// a CTA's share of HBM and 4,864 of them running at a time. Rows above 32 KB stay
+// with a CTA, as the k best would have a warp read k / 32 of its row again.
+bool row_a_warp(int64_t N, int64_t V, int64_t elem)
+{
+    const int64_t bytes = V * elem;
+    return bytes <= 32 * 1024 && row_splits(N, V, elem) == 1 &&
+           (N + 4863) / 4864 * (56 * 1024 + 8 * bytes) < (N + 607) / 608 * (56 * 1024 + bytes);
+}
+
 size_t part_offset() { return align_up(ws_offsets().total, 256); }
 
 score::Outs outs(const int32_t *tokens, float *logp, float *entropy, int32_t *top_ids, float *top_logp, int k, float T,
@@ -82,6 +92,9 @@ int run_logprobs(const void *z, int64_t stride, int64_t N, const score::Outs &o,
     const int splits = row_splits(N, o.V, sizeof(E));
     score::Part *part = reinterpret_cast<score::Part *>(static_cast<char *>(ws) + part_offset());
     const E *zp = static_cast<const E *>(z);
+    if (row_a_warp(N, o.V, sizeof(E)))
+        return launch_overlapped(score::k_logprob_rows<E>, dim3(static_cast<unsigned>((N + score::kWarps - 1) / score::kWarps)),
+                                 score::kThreads, 0, st, zp, stride, N, o);
     FGM_HOST_TRY(launch_overlapped(score::k_logprobs<E>, dim3(static_cast<unsigned>(N * splits)), score::kThreads, 0, st, zp,
                                    stride, splits, part, o));
     if (splits == 1)

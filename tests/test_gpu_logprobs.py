@@ -84,6 +84,28 @@ def test_matches_plain(fgm, ws, dt, N, V, k, T):
     check(fgm, ws, z.to(DT[dt]), tokens, k, T)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("N,V,k", [(701, 1, 1), (1300, 2, 2), (700, 5, 3), (900, 31, 16), (1217, 129, 0), (5000, 300, 4), (700, 715, 16),
+                                   (4867, 1021, 3), (2000, 4099, 8)])
+def test_many_short_rows(fgm, dt, N, V, k):
+    """More rows than CTAs run at a time, short enough for a warp each; among them
+    rows that tie throughout, that hold infinities and NaN, or nothing else."""
+    g = torch.Generator().manual_seed(N + V)
+    z = (torch.randn(N, V, generator=g) * 2).to(DT[dt])
+    z[3] = 1.5                                 # ties everywhere
+    z[5, 1:] = float("-inf")
+    z[7] = float("-inf")
+    z[11, V // 2] = float("nan")
+    z[13, V - 1] = float("inf")
+    z[17] = float("nan")
+    z[19] = torch.finfo(DT[dt]).min
+    if V > 80:
+        z[23, ::2] = 9.0                       # more ties for the first places than a list of candidates holds
+    tokens = torch.randint(-1, V + 1, (N,), generator=g).tolist()
+    ws = fgm.Workspace("cuda", nbytes=fgm.logprobs_workspace_bytes(N, V, k))
+    check(fgm, ws, z.cuda(), tokens, k, 0.9, status=fgm.STATUS_NONFINITE_LOGITS)
+
+
 @pytest.mark.parametrize("T", [2.95e-39, 1e-38, 1e-30, 1e-6, 1e-3, 0.05, 1e4, 1e30])
 @pytest.mark.parametrize("N,V", [(3, 1000), (2, 70001)])
 def test_extreme_temperatures(fgm, ws, N, V, T):
