@@ -22,9 +22,9 @@
 // pass, with the same bound as a threshold, took 134 us on 1,013 x 50,021 bf16
 // logits, against 15 us of HBM time: the insertions were most of it.)
 //
-// Short rows in large numbers have a warp each (k_logprob_rows). Long rows are cut into splits until the grid has several CTAs per SM; k_logprob_join
-// merges a row's splits in order (no atomics on results: the same call gives
-// the same bits).
+// Short rows in large numbers have a warp each (k_logprob_rows). Long rows are cut
+// into splits until the grid has several CTAs per SM; k_logprob_join merges a row's
+// splits in order (no atomics on results: the same call gives the same bits).
 #pragma once
 
 #include "common.cuh"
