@@ -33,15 +33,20 @@
 //    probabilities are rounded.
 //  * The values' warp also prepares the query terms of the next (sequence, head).
 //
-// Precision. The second operands are split into two E4M3 terms in columns of
-// their own, hi and lo = c (x - hi), added in fp32 as hi + lo / c. Queries
-// (c = 16): scaled by a power of two to a largest element in (224, 448]; a bf16
-// has 8 significant bits and a term carries 4, so the split is exact down to
-// half a subnormal step of lo, 2^-14 / 224 of the row's largest. Probabilities
-// (c = 32): 32 exp2(s + log2 v_s - m), at most 256, within 2^-8 of themselves or
-// 2^-15 / 32 = 2^-20 of exp2(m). V's block scale rides in the exponent, so that
-// blocks of any scale add into one accumulator. The row sums use the unrounded
-// exponentials, in fp32.
+// Precision. The second operands are split into 8-bit terms in columns of their
+// own, each the rounding of what the ones before left, and added in fp32.
+// Queries: two E4M3 terms, hi + lo / 16, of the row scaled by a power of two to a
+// largest element in (224, 448]; a bf16 has 8 significant bits and a term carries
+// 4, so the split is exact down to half a subnormal step of lo, 2^-14 / 224 of the
+// row's largest. Probabilities: three E5M2 terms, t0 + t1 / 8 + t2 / 64, of 2^12
+// exp2(s + log2 v_s - m), at most 2^15. A term carries 3 bits, so they are within
+// 2^-9 of themselves or, where the last is subnormal, 2^-17 / 64 / 2^12 = 2^-35 of
+// exp2(m); the f16 on the way adds 2^-12 and 2^-37. The wide range is what E5M2 is
+// taken for: the row sums use the unrounded exponentials, so a body of many small
+// probabilities under one large one must not be dropped from the product (two E4M3
+// terms held 2^-20 of exp2(m): a first token 15 nats above 32,768 others, its value
+// zero, left nothing of the output). V's block scale rides in the exponent, so that
+// blocks of any scale add into one accumulator. The row sums are fp32.
 //
 // The reference m is not the running maximum but within 3 of it from below: a
 // unit whose scores stay under m + 3 (most after the first few) needs no
@@ -78,7 +83,7 @@ constexpr int kMaxRing = 8;                            // stages of the K and of
 constexpr int kMetas = 64;                             // units' scales kept, in two halves
 constexpr int kMaxGrid = 160;                          // CTAs at most: the SMs of a full sm_103 part
 constexpr float kLowest = -1.0e30f;                    // stands for the maximum of nothing
-constexpr float kLift = 5.0f;                          // probabilities enter the product times 2^5
+constexpr float kLift = 12.0f;                         // probabilities enter the product times 2^12
 constexpr float kSlack = 3.0f;                         // scores may exceed the reference by this much
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -110,10 +115,13 @@ struct AttnArgs {
 // Floats of one partial segment.
 __host__ __device__ inline int64_t partial_floats(int rows, int D) { return static_cast<int64_t>(rows) * (D + 2); }
 
+// Columns of the probabilities' product: three terms a row, a multiple of 16.
+__host__ __device__ constexpr int prob_cols(int rows) { return (3 * rows + 15) / 16 * 16; }
+
 // Shared memory of the operands that the kernel writes: query terms and two
 // buffers of probability terms; and 64 D bytes a block of K or V.
 __host__ __device__ inline int query_bytes(int rows, int D) { return 2 * rows * D; }
-__host__ __device__ inline int prob_bytes(int rows) { return 2 * rows * kTile; }
+__host__ __device__ inline int prob_bytes(int rows) { return prob_cols(rows) * kTile; }
 
 struct Meta {                // a unit: K's block scales, log2 and inverse of V's, first token, its blocks
     float ks[2], lv[2], iv[2];
@@ -336,17 +344,15 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap *map, i
         : "memory");
 }
 
-// Two E4M3 terms of two values below 448: hi + lo / 32 (a in the low bytes). By
-// way of f16, whose 11 bits hold hi, the difference and 32 times it exactly; the
-// values' own rounding to f16, 2^-12 of them and 2^-25, is below lo's.
-__device__ __forceinline__ void e4m3_terms(float a, float b, uint32_t &hi, uint32_t &lo)
+// The E5M2 roundings of two f16, and 8 times what they leave: an E5M2 is the upper
+// half of an f16, and the difference and its multiple have no more bits than x, so
+// both are exact (below 2^15 the difference is at most 2^12).
+__device__ __forceinline__ uint32_t e5m2_term(__half2 &x)
 {
-    const __half2 x = __floats2half2_rn(a, b);
-    const __nv_fp8x2_storage_t h = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
-    const __half2 z = __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3));
-    const __half2 d = __hmul2(__hsub2(x, z), __float2half2_rn(32.0f));
-    hi = h;
-    lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(d), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t t = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E5M2);
+    const uint32_t w = __byte_perm(t, 0u, 0x1404);
+    x = __hmul2(__hsub2(x, *reinterpret_cast<const __half2 *>(&w)), __float2half2_rn(8.0f));
+    return t;
 }
 
 __device__ __forceinline__ void sts32(uint32_t a, uint32_t v)
@@ -443,16 +449,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     k_attn(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
            const __grid_constant__ AttnArgs p)
 {
-    constexpr int kSlices = D / 64, kN = 2 * R;
+    constexpr int kSlices = D / 64, kN = 2 * R, kNP = prob_cols(R);
     constexpr int kSide = kTile * D;                             // bytes of a unit's K or V
     constexpr int kMTiles = D == 256 ? 2 : 1;                    // 128-lane tiles of O^T
     constexpr int kNR = R / 4;                                   // rows of a softmax thread
     constexpr bool kAhead = R <= 32;                             // the next unit's scores fit the registers beside this one's
     constexpr int kCh = kNR < 4 ? kNR : 4;                       // accumulator columns read at a time
-    constexpr int kG = kNR % 8 == 0 ? 8 : kCh;                   // rows rescaled at a time
-    constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(kN >> 3) << 17) | (8u << 24);   // fp32 += E4M3 x E4M3, M = 128
-    constexpr uint32_t kOCol = 2 * kN;                           // S buffers first, then O tiles
-    constexpr uint32_t kUsed = 2 * kN + kMTiles * kN;
+    constexpr int kG = kNR == 8 ? 8 : kCh;                       // rows rescaled at a time
+    constexpr uint32_t kIdesc = (1u << 4) | (8u << 24);          // fp32 += E4M3 x ..., M = 128
+    constexpr uint32_t kIdescS = kIdesc | (static_cast<uint32_t>(kN >> 3) << 17);                  // ... E4M3
+    constexpr uint32_t kIdescO = kIdesc | (1u << 10) | (static_cast<uint32_t>(kNP >> 3) << 17);    // ... E5M2
+    // Buffers of S: two, but one where O leaves no room (64 rows at D = 256). The
+    // softmax then still reads a unit's scores before it works on them, so the
+    // next unit's product runs meanwhile.
+    constexpr int kSBuf = 2 * kN + kMTiles * kNP <= 512 ? 2 : 1;
+    constexpr uint32_t kOCol = kSBuf * kN;                       // S buffers first, then O tiles
+    constexpr uint32_t kUsed = kOCol + kMTiles * kNP;
+    static_assert(kUsed <= 512, "tensor memory has 512 columns");
+    static_assert(kSBuf == 2 || !kAhead, "scores are read ahead from a second buffer");
     constexpr uint32_t kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
     extern __shared__ uint8_t dsm_raw[];
     __shared__ AttnShared sh;
@@ -597,6 +611,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     Cursor cu = {};                                // where a warp is
     if (n_units > 0 && warp > 0)
         cu = locate(u0);
+    auto sbuf = [](int u) { return kSBuf == 2 ? u & 1 : 0; };       // a unit's buffer of S, and its turn of it
+    auto sturn = [](int u) { return kSBuf == 2 ? u >> 1 : u; };
     auto wait = [&](unsigned long long *bar, int phase, int site, int index) -> bool {
         return bar_wait(saddr(bar), phase & 1, &sh.abort, p.timeout_ns, p.status, site, index);
     };
@@ -705,20 +721,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int n = min(cu.n - cu.u, n_units - done);
             ok = wait(&sh.qfull[qslot], seg / p.q_ring, 17, seg);
             for (int u = done; u < done + n && ok; ++u) {
-                if (u >= 2)
-                    ok = wait(&sh.sfree[u & 1], (u >> 1) - 1, 15, u);
+                if (u >= kSBuf)
+                    ok = wait(&sh.sfree[sbuf(u)], sturn(u) - 1, 15, u);
                 ok = ok && wait(&sh.kfull[slot], turn, 16, u);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (ok && lead) {
                     after_sync();
                     const uint64_t a0 = desc64(saddr(kring + slot * kSide));
-                    const uint32_t d = tmem + (u & 1) * kN;
+                    const uint32_t d = tmem + sbuf(u) * kN;
 #pragma unroll
                     for (int k = 0; k < D / 32; ++k)
                         mma_f8(d, a0 + (((k >> 1) * (kTile * 64) + (k & 1) * 32) >> 4),
-                               b0 + (((k >> 1) * (kN * 64) + (k & 1) * 32) >> 4), kIdesc, k != 0);
+                               b0 + (((k >> 1) * (kN * 64) + (k & 1) * 32) >> 4), kIdescS, k != 0);
                     commit(&sh.kempty[slot]);
-                    commit(&sh.sfull[u & 1]);
+                    commit(&sh.sfull[sbuf(u)]);
                     if (u == done + n - 1)
                         commit(&sh.qempty[qslot]);
                 }
@@ -758,8 +774,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         if (have >> (k >> 1) & 1) {
 #pragma unroll
                             for (int t = 0; t < kMTiles; ++t)
-                                mma_f8(tmem + kOCol + t * kN, a0 + (((k >> 1) * (kBlock * D) + t * (128 * 64) + (k & 1) * 32) >> 4),
-                                       b0 + (((k >> 1) * (kN * 64) + (k & 1) * 32) >> 4), kIdesc, add);
+                                mma_f8(tmem + kOCol + t * kNP, a0 + (((k >> 1) * (kBlock * D) + t * (128 * 64) + (k & 1) * 32) >> 4),
+                                       b0 + (((k >> 1) * (kNP * 64) + (k & 1) * 32) >> 4), kIdescO, add);
                             add = true;
                         }
                     commit(&sh.vempty[slot]);
@@ -851,7 +867,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int rows = p.M * p.G;
         const int n0 = part4 * kNR;                // the thread's rows: n0 .. n0 + kNR - 1
         // where the thread's token goes in P^T, and the swizzle of its rows 2 j, 2 j + 1
-        const uint32_t probs = saddr(ps) + blk * (kN * 64) + n0 * 64 + (tl & 15);
+        const uint32_t probs = saddr(ps) + blk * (kNP * 64) + n0 * 64 + (tl & 15);
         uint32_t phase[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -907,22 +923,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     scales = u >> 5;
                 }
                 if (alive)
-                    alive = wait(&sh.sfull[u & 1], u >> 1, 21, u);
+                    alive = wait(&sh.sfull[sbuf(u)], sturn(u), 21, u);
                 alive = __all_sync(0xFFFFFFFFu, alive);
                 after_sync();
             };
             auto read = [&](int u, float *v) {
 #pragma unroll
                 for (int r = 0; r < kNR; r += kCh) {
-                    tmem_ld<kCh>(tmem + lanes + (u & 1) * kN + n0 + r, v + r);
-                    tmem_ld<kCh>(tmem + lanes + (u & 1) * kN + R + n0 + r, v + kNR + r);
+                    tmem_ld<kCh>(tmem + lanes + sbuf(u) * kN + n0 + r, v + r);
+                    tmem_ld<kCh>(tmem + lanes + sbuf(u) * kN + R + n0 + r, v + kNR + r);
                 }
             };
             auto taken = [&](int u) {              // read: the buffer is free
                 before_sync();
                 __syncwarp();
                 if (lane == 0)
-                    bar_arrive(saddr(&sh.sfree[u & 1]));
+                    bar_arrive(saddr(&sh.sfree[sbuf(u)]));
             };
             arrived(done);
             read(done, s);
@@ -1004,24 +1020,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         for (int t = 0; t < kMTiles; ++t)
 #pragma unroll
                             for (int r0 = 0; r0 < kNR; r0 += kG) {
-                                const uint32_t a = tmem + lanes + kOCol + t * kN + n0 + r0;
-                                float o[2 * kG];
+                                const uint32_t a = tmem + lanes + kOCol + t * kNP + n0 + r0;
+                                float o[3 * kG];
 #pragma unroll
-                                for (int r = 0; r < kG; r += kCh) {
-                                    tmem_ld<kCh>(a + r, o + r);
-                                    tmem_ld<kCh>(a + R + r, o + kG + r);
-                                }
+                                for (int r = 0; r < kG; r += kCh)
+#pragma unroll
+                                    for (int k = 0; k < 3; ++k)
+                                        tmem_ld<kCh>(a + k * R + r, o + k * kG + r);
                                 tmem_wait_ld(o);
 #pragma unroll
-                                for (int r = 0; r < kG; ++r) {
-                                    o[r] *= c[r0 + r];
-                                    o[kG + r] *= c[r0 + r];
-                                }
+                                for (int r = 0; r < kG; ++r)
 #pragma unroll
-                                for (int r = 0; r < kG; r += kCh) {
-                                    tmem_st<kCh>(a + r, o + r);
-                                    tmem_st<kCh>(a + R + r, o + kG + r);
-                                }
+                                    for (int k = 0; k < 3; ++k)
+                                        o[k * kG + r] *= c[r0 + r];
+#pragma unroll
+                                for (int r = 0; r < kG; r += kCh)
+#pragma unroll
+                                    for (int k = 0; k < 3; ++k)
+                                        tmem_st<kCh>(a + k * R + r, o + k * kG + r);
                             }
                         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                     }
@@ -1032,7 +1048,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 float next[kAhead ? 2 * kNR : 1];
                 const bool more = i + 1 < n;
                 const bool early = kAhead && more && (u + 1) >> 5 == scales &&
-                                   __all_sync(0xFFFFFFFFu, bar_test(saddr(&sh.sfull[(u + 1) & 1]), ((u + 1) >> 1) & 1));
+                                   __all_sync(0xFFFFFFFFu, bar_test(saddr(&sh.sfull[sbuf(u + 1)]), sturn(u + 1) & 1));
                 // the buffer's last product is done
                 if (alive && u >= 2)
                     alive = wait(&sh.pdone[u & 1], (u >> 1) - 1, 23, u);
@@ -1048,14 +1064,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     const float p0 = ex2(s[r] - (m[r] - kLift)), p1 = ex2(s[r + 1] - (m[r + 1] - kLift));
                     l[r] = fmaf(p0, ivs, l[r]);
                     l[r + 1] = fmaf(p1, ivs, l[r + 1]);
-                    uint32_t hi, lo;
-                    e4m3_terms(p0, p1, hi, lo);
-                    // rows r, r + 1 (r even) lie in one swizzle phase; the second term R rows on
+                    __half2 x = __floats2half2_rn(p0, p1);
+                    // rows r, r + 1 (r even) lie in one swizzle phase; the next term R rows on
                     const uint32_t at = pt + phase[(r >> 1) & 3] + r * 64;
-                    sts8(at, hi);
-                    sts8(at + 64, hi >> 8);
-                    sts8(at + R * 64, lo);
-                    sts8(at + R * 64 + 64, lo >> 8);
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) {
+                        const uint32_t t = e5m2_term(x);
+                        sts8(at + k * R * 64, t);
+                        sts8(at + k * R * 64 + 64, t >> 8);
+                    }
                 }
                 if (edge) {
                     // V codes of tokens that no row sees may be anything, NaN included: zeros
@@ -1082,7 +1099,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (lane == 0) {
                     bar_arrive(saddr(&sh.pfull[u & 1]));
                     if (early)
-                        bar_arrive(saddr(&sh.sfree[(u + 1) & 1]));
+                        bar_arrive(saddr(&sh.sfree[sbuf(u + 1)]));
                 }
                 if (more && !early) {
                     arrived(u + 1);
@@ -1121,19 +1138,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int mt = D == 256 ? part4 >> 1 : 0, d = mt * 128 + tl;
             constexpr int kShare = D == 256 ? R / 2 : R / 4;
             const int ra = (D == 256 ? part4 & 1 : part4) * kShare;
-            const uint32_t oa = tmem + lanes + kOCol + mt * kN;
+            const uint32_t oa = tmem + lanes + kOCol + mt * kNP;
             const int64_t row0 = static_cast<int64_t>(cu.b) * p.M * p.Hq + cu.h * p.G;
             if (D != 64 || quarter < 2) {
 #pragma unroll 2
                 for (int r = ra; r < ra + kShare; r += kCh) {
-                    float o[2 * kCh];
-                    tmem_ld<kCh>(oa + r, o);
-                    tmem_ld<kCh>(oa + R + r, o + kCh);
+                    float o[3 * kCh];
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)
+                        tmem_ld<kCh>(oa + k * R + r, o + k * kCh);
                     tmem_wait_ld(o);
 #pragma unroll
                     for (int k = 0; k < kCh; ++k) {
                         const float sum = sum_of(r + k);
-                        const float v = sum == 0.0f ? 0.0f : fmaf(o[kCh + k], 1.0f / 32.0f, o[k]);
+                        const float v = sum == 0.0f ? 0.0f : fmaf(fmaf(o[2 * kCh + k], 0.125f, o[kCh + k]), 0.125f, o[k]);
                         if (!whole)
                             part[(r + k) * D + d] = v;
                         else if (r + k < rows)

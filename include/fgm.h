@@ -398,8 +398,9 @@ size_t fgm_attn_workspace_bytes(int B, int M, int n_q_heads, int n_kv_heads, int
  *   lse = ln sum_t exp(s_t).
  * A row that sees nothing (p < 0, lens[b] = 0) has out = 0 and lse = -inf.
  * Scores and sums are fp32; queries enter the products exactly up to 2^-21 of
- * their row's largest element, probabilities to 2^-8 of themselves. A row
- * with a non-finite query element is NaN. The same call gives the same bits.
+ * their row's largest element, probabilities to 2^-8 of themselves or, times
+ * their v_s, 2^-34 of the row's largest P_t v_s. A row with a non-finite query
+ * element is NaN. The same call gives the same bits.
  *  q            bf16 [B][M][n_q_heads][D], 16-byte aligned; tokens token_stride elements apart
  *               (a multiple of 8, at least n_q_heads * D), sequences M * token_stride
  *  lens, block_table, max_blocks   as fgm_kv_append; two sequences may share blocks.
