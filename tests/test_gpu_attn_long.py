@@ -123,3 +123,33 @@ def test_widest_products_of_a_full_batch(fgm):
         for i in range(M):
             seen = int(lens[b]) - M + i + 1
             check_rows(out[b, i], lse[b, i], q[b, i], k[:seen], v[:seen], 448 * 2.0 ** -6, 0.0625)
+
+
+def test_many_units_a_cta(fgm):
+    """Eight sequences of about 65,000 tokens with four heads: 108 units of 128
+    tokens a CTA, more than three rounds of 32 block scales. Scales differ from
+    block to block, keys are small enough that every token counts."""
+    B, H, D, G, M = 8, 4, 64, 2, 3
+    g = torch.Generator(device="cuda").manual_seed(3)
+    lens = [65536 - 61 * b for b in range(B)]
+    per = 1024
+    n = B * per
+    ks = torch.pow(2.0, torch.randint(-9, -5, (n, H), generator=g, device="cuda").float())
+    vs = torch.pow(2.0, torch.randint(-9, -5, (n, H), generator=g, device="cuda").float())
+    k = torch.randn(n, H, BLOCK, D, generator=g, device="cuda") * 24
+    v = 60 + 20 * torch.randn(n, H, BLOCK, D, generator=g, device="cuda").clamp(-2, 2)
+    c = make_cache(fgm, k, v, ks, vs)
+    del k, v
+    tab = torch.randperm(n, generator=g, device="cuda").to(torch.int32).view(B, per)
+    q = torch.randn(B, M, H * G, D, generator=g, device="cuda").bfloat16()
+    ws = fgm.Workspace("cuda", nbytes=fgm.attn_workspace_bytes(B, M, H * G, H, D))
+    lse = torch.empty(B, M, H * G, device="cuda")
+    out = fgm.attn_fwd(c, q, torch.tensor(lens, dtype=torch.int32, device="cuda"), 0.25, block_table=tab, lse=lse, ws=ws)
+    assert ws.status() == 0
+    for b in range(B):
+        for h in range(H):
+            kk, vv = values(c, tab[b].long(), h)
+            for i in range(M):
+                seen = lens[b] - M + i + 1
+                at = slice(h * G, (h + 1) * G)
+                check_rows(out[b, i, at], lse[b, i, at], q[b, i, at], kk[:seen], vv[:seen], 448 * 2.0 ** -6, 0.25)
