@@ -82,7 +82,7 @@ constexpr int kTile = 2 * kBlock;                      // tokens of a unit
 constexpr int kMaxRing = 8;                            // stages of the K and of the V ring at most
 constexpr int kMetas = 64;                             // units' scales kept, in two halves
 constexpr int kMaxGrid = 160;                          // CTAs at most: the SMs of a full sm_103 part
-constexpr float kLowest = -1.0e30f;                    // stands for the maximum of nothing
+constexpr float kLowest = -3.0e38f;                    // stands for the maximum of nothing, below every finite score that counts
 constexpr float kLift = 12.0f;                         // probabilities enter the product times 2^12
 constexpr float kSlack = 3.0f;                         // scores may exceed the reference by this much
 constexpr float kLog2e = 1.4426950408889634f;

@@ -153,3 +153,27 @@ def test_many_units_a_cta(fgm):
                 seen = lens[b] - M + i + 1
                 at = slice(h * G, (h + 1) * G)
                 check_rows(out[b, i, at], lse[b, i, at], q[b, i, at], kk[:seen], vv[:seen], 448 * 2.0 ** -6, 0.25)
+
+
+@pytest.mark.parametrize("n", [1, 64, 200])
+@pytest.mark.parametrize("scale", [1e28, 1e32, 1e36])
+def test_scores_far_below_zero(fgm, n, scale):
+    """Every score equal and hugely negative: the mean of the values, whatever the size of the scores."""
+    D, k0 = 64, -1.0
+    nb = (n + BLOCK - 1) // BLOCK
+    g = torch.Generator(device="cuda").manual_seed(n)
+    k = torch.full((nb, 1, BLOCK, D), k0, device="cuda")
+    v = torch.randint(1, 16, (nb, 1, BLOCK, D), generator=g, device="cuda").float()
+    one = torch.ones(nb, 1, device="cuda")
+    c = make_cache(fgm, k, v, one, one)
+    q = torch.full((1, 1, 1, D), 0.5, device="cuda").bfloat16()
+    lse = torch.empty(1, 1, 1, device="cuda")
+    ws = fgm.Workspace("cuda", nbytes=fgm.attn_workspace_bytes(1, 1, 1, 1, D))
+    out = fgm.attn_fwd(c, q, torch.tensor([n], dtype=torch.int32, device="cuda"), scale, lse=lse, ws=ws)
+    vals = values(c, slice(0, nb), 0)[1][:n]
+    want = vals.mean(dim=0)
+    # (equal scores: no error in P but the probabilities' 2^-8 and the sums')
+    assert ((out[0, 0, 0].double() - want).abs() <= (2.0 ** -7 + 2.0 ** -12) * want).all()
+    s = -0.5 * D * float(torch.tensor(scale, dtype=torch.float32))
+    assert abs(float(lse) - s) <= 2.0 ** -21 * abs(s)
+    assert ws.status() == 0
