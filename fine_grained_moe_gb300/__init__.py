@@ -696,6 +696,9 @@ def attn_fwd(cache: KVCache, q: torch.Tensor, lens: torch.Tensor, scale: float,
     that many positions. Returns bf16 [B, M, q heads, D]; lse fp32 [B, M, q
     heads] receives the log of each row's sum of exponentials."""
     C, dev = cache.struct(), cache.v_q.device
+    if window < 0:
+        raise FgmError(f"window = {window}: 0 (none) or a positive number of tokens")
+    window = min(window, 1 << 30)       # (no sequence is longer; a C int holds it)
     if q.dim() != 4:
         raise FgmError(f"q: expected bf16 [B, M, q heads, D], got {tuple(q.shape)}")
     B, M, Hq, D = q.shape

@@ -177,3 +177,19 @@ def test_scores_far_below_zero(fgm, n, scale):
     s = -0.5 * D * float(torch.tensor(scale, dtype=torch.float32))
     assert abs(float(lse) - s) <= 2.0 ** -21 * abs(s)
     assert ws.status() == 0
+
+
+def test_windows_beyond_32_bits(fgm):
+    """A window of any size is taken as it is."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    one = torch.full((4, 1), 2.0 ** -6, device="cuda")
+    c = make_cache(fgm, torch.randn(4, 1, BLOCK, 64, generator=g, device="cuda") * 20,
+                   torch.randn(4, 1, BLOCK, 64, generator=g, device="cuda") * 20, one, one)
+    q = torch.randn(1, 2, 2, 64, generator=g, device="cuda").bfloat16()
+    lens = torch.tensor([250], dtype=torch.int32, device="cuda")
+    ref = fgm.attn_fwd(c, q, lens, 0.125)
+    for window in (2 ** 31, 2 ** 32 + 5, 2 ** 40):
+        assert torch.equal(fgm.attn_fwd(c, q, lens, 0.125, window=window), ref)
+    for window in (-1, -2 ** 32, 3 - 2 ** 32):
+        with pytest.raises(fgm.FgmError):
+            fgm.attn_fwd(c, q, lens, 0.125, window=window)
