@@ -158,7 +158,7 @@ int fgm_kv_append(const fgm_kv_cache *cache, const uint16_t *k, const uint16_t *
 size_t fgm_attn_workspace_bytes(int B, int M, int n_q_heads, int n_kv_heads, int head_dim)
 {
     if (B < 1 || B > 1024 || M < 1 || M > kMaxM || n_kv_heads < 1 || n_kv_heads > 1024 || n_q_heads < 1 ||
-        n_q_heads % n_kv_heads || !head_dim_ok(head_dim) || M * (n_q_heads / n_kv_heads) > FGM_ATTN_MAX_ROWS)
+        n_q_heads % n_kv_heads || !head_dim_ok(head_dim) || n_q_heads / n_kv_heads > FGM_ATTN_MAX_ROWS / M)
         return 0;
     return attn_ws(M * (n_q_heads / n_kv_heads), head_dim).total;
 }
@@ -173,9 +173,9 @@ int fgm_attn_fwd(const fgm_kv_cache *cache, const uint16_t *q, int64_t token_str
         return failf(FGM_ERR_INVALID_ARG, "M = %d outside [1, %d]", M, kMaxM);
     if (n_q_heads < 1 || n_q_heads % cache->n_kv_heads)
         return failf(FGM_ERR_INVALID_ARG, "n_q_heads = %d: a multiple of n_kv_heads = %d", n_q_heads, cache->n_kv_heads);
-    if (M * (n_q_heads / cache->n_kv_heads) > FGM_ATTN_MAX_ROWS)
-        return failf(FGM_ERR_INVALID_ARG, "M * n_q_heads / n_kv_heads = %d above %d", M * (n_q_heads / cache->n_kv_heads),
-                     FGM_ATTN_MAX_ROWS);
+    if (n_q_heads / cache->n_kv_heads > FGM_ATTN_MAX_ROWS / M)
+        return failf(FGM_ERR_INVALID_ARG, "M * n_q_heads / n_kv_heads = %lld above %d",
+                     static_cast<long long>(M) * (n_q_heads / cache->n_kv_heads), FGM_ATTN_MAX_ROWS);
     FGM_HOST_TRY(check_rows("q", q, token_stride, n_q_heads, cache->head_dim));
     if (!(scale > 0.0f) || !std::isfinite(scale))
         return failf(FGM_ERR_INVALID_ARG, "scale = %g: needs a finite scale > 0", (double)scale);
