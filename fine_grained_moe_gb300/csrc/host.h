@@ -49,6 +49,8 @@ inline bool is_aligned(const void *p, size_t a) { return (reinterpret_cast<uintp
 
 // Launches a kernel that may start while the one before it in the stream ends:
 // it waits for that end itself (griddepcontrol.wait) before it touches memory.
+// What the one before may write is therefore not constant while the kernel lives,
+// and is never read by the read-only path (__ldg), which asks for that.
 template <typename... P, typename... A>
 int launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args)
 {

@@ -62,7 +62,7 @@ __device__ __forceinline__ int clamp_len(int len, int max_blocks, int32_t *statu
 __device__ __forceinline__ int64_t phys_block(const int32_t *table, int b, int j, int max_blocks, int64_t n_blocks)
 {
     const int64_t at = static_cast<int64_t>(b) * max_blocks + j;
-    const int64_t p = table ? __ldg(table + at) : at;
+    const int64_t p = table ? __ldcg(table + at) : at;
     return p >= 0 && p < n_blocks ? p : -1;
 }
 
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(Append<D>::kThreads) k_kv_append(const AppendA
     const bool is_v = blockIdx.y & 1;
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int len0 = __ldg(p.lens + b);
+    const int len0 = __ldcg(p.lens + b);
     const int len = clamp_len(len0, p.max_blocks, p.status, tid == 0 && blockIdx.x == 0 && blockIdx.y == 0);
     // the call's tokens are positions [start, len); start counts from the length as given
     const int64_t first = static_cast<int64_t>(len0) - p.N;

@@ -393,7 +393,7 @@ __device__ __forceinline__ void build_queries(const uint16_t *q, int64_t stride,
                 const int d = (e * 32 + lane) * 4;
                 x[i][e] = make_uint2(0, 0);
                 if (r < rows && d < D)
-                    x[i][e] = __ldg(reinterpret_cast<const uint2 *>(src + d));
+                    x[i][e] = __ldcg(reinterpret_cast<const uint2 *>(src + d));
             }
         }
 #pragma unroll
@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int b = b0 + lane;
             int n = 0, first;
             if (b < p.B) {
-                const int len = clamp_len(__ldg(p.lens + b), p.max_blocks, p.status, blockIdx.x == 0);
+                const int len = clamp_len(__ldcg(p.lens + b), p.max_blocks, p.status, blockIdx.x == 0);
                 lens[b] = len;
                 n = (seq_blocks(len, p.M, p.window, first) + 1) / 2 * heads;
             }
@@ -646,8 +646,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (ph >= 0) {
                     const int at = static_cast<int>(ph) * heads + cu.h;
                     row_n[k] = at * D;
-                    ks_n[k] = __ldg(p.c.k_s + at);
-                    vs_n[k] = __ldg(p.c.v_s + at);
+                    ks_n[k] = __ldcg(p.c.k_s + at);
+                    vs_n[k] = __ldcg(p.c.v_s + at);
                 } else {
                     atomicOr(p.status, FGM_STATUS_BAD_BLOCK);
                 }

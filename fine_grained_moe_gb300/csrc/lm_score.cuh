@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_lm_join(const uint16_t *emb
     const float c = per_nat(o.T);
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int32_t tok = o.logp ? __ldg(o.tokens + row) : -1;
+    const int32_t tok = o.logp ? __ldcg(o.tokens + row) : -1;
     // a warp's share of the parts, in order
     const int parts = p.splits * 2, p0 = parts * warp / kJoinWarps, p1 = parts * (warp + 1) / kJoinWarps;
     Sums s;
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_lm_join(const uint16_t *emb
     }
 #pragma unroll 3
     for (int i = 0; i < kH / 256; ++i) {
-        const uint4 x = __ldg(hr + i * 32);
+        const uint4 x = __ldcg(hr + i * 32);
         const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int j = 0; j < kMine; ++j) {

@@ -302,7 +302,7 @@ struct Load;
 template <>
 struct Load<float> {
     static constexpr int kVec = 4;
-    static __device__ float one(const float *p) { return __ldg(p); }
+    static __device__ float one(const float *p) { return *p; }
     static __device__ void unpack(const uint4 &r, float *v)
     {
         v[0] = __uint_as_float(r.x);
@@ -316,7 +316,7 @@ struct Load<__nv_bfloat16> {
     static constexpr int kVec = 8;
     static __device__ float one(const __nv_bfloat16 *p)
     {
-        return bf16_to_f32(__ldg(reinterpret_cast<const uint16_t *>(p)));
+        return bf16_to_f32(*reinterpret_cast<const uint16_t *>(p));
     }
     static __device__ void unpack(const uint4 &r, float *v)
     {
@@ -335,7 +335,7 @@ struct Load<__half> {
     static __device__ float one(const __half *p)
     {
         __half_raw r;
-        r.x = __ldg(reinterpret_cast<const uint16_t *>(p));
+        r.x = *reinterpret_cast<const uint16_t *>(p);
         return __half2float(__half(r));
     }
     static __device__ void unpack(const uint4 &r, float *v)
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 
     float zt = -INFINITY;                      // the given token's logit
     if (splits == 1 && o.logp && tid == 0) {
-        const int32_t t = __ldg(o.tokens + row);
+        const int32_t t = __ldcg(o.tokens + row);
         if (t >= 0 && t < V)
             zt = L::one(zr + t);
         if (zt != zt)
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
             if (at + i * 32 < v1)
-                r[i] = __ldg(zv + at + i * 32);
+                r[i] = zv[at + i * 32];
     };
 
     int at = v0 + warp * kChunk + lane;
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 4)
                         break;
                     float v[kVec];
                     if (in)
-                        L::unpack(__ldg(zv + vec), v);
+                        L::unpack(zv[vec], v);
 #pragma unroll
                     for (int j = 0; j < kVec; ++j) {
                         const float x = in && v[j] == v[j] ? v[j] : -INFINITY;
@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob_rows(const E *z, int64_
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
             if (at + i * 32 < nvec)
-                r[i] = __ldg(zv + at + i * 32);
+                r[i] = zv[at + i * 32];
     };
     int at = lane;
 #pragma unroll
@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob_rows(const E *z, int64_
         fetch(at + q * kChunk, raw[q]);
     float zt = -INFINITY;                      // the given token's logit
     if (o.logp && lane == 0) {
-        const int32_t t = __ldg(o.tokens + row);
+        const int32_t t = __ldcg(o.tokens + row);
         if (t >= 0 && t < V)
             zt = L::one(zr + t);
         if (zt != zt)
@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob_rows(const E *z, int64_
                         break;
                     float v[kVec];
                     if (in)
-                        L::unpack(__ldg(zv + vec), v);
+                        L::unpack(zv[vec], v);
 #pragma unroll
                     for (int j = 0; j < kVec; ++j) {
                         const float x = in && v[j] == v[j] ? v[j] : -INFINITY;
@@ -796,7 +796,7 @@ __global__ void __launch_bounds__(kThreads)
     const float c = per_nat(o.T);
     float zt = -INFINITY;
     if (o.logp) {
-        const int32_t t = __ldg(o.tokens + row);
+        const int32_t t = __ldcg(o.tokens + row);
         if (t >= 0 && t < o.V)
             zt = Load<E>::one(z + row * stride + t);
         if (zt != zt)
