@@ -5,9 +5,9 @@
 // 2 * 2816 operations a logit: bound by the tensor pipe from about 300 rows on,
 // by the embedding's 1.48 GB below. 1,021 rows of 262,144 words take 0.84 ms, 1.80
 // PFLOP/s: the products 0.80 with the tensor pipe 92 % busy, the join 0.02, the
-// rest starts and the last epilogue. 16 rows take 253 us, 5.8 TB/s, and 256 rows
-// 279 us. (Up to 8 rows are the persistent lm_head kernel's.) Rows are taken 256 at
-// a time: 300 cost what 512 do, 0.44 ms. Built for the tensor pipe: a pair of CTAs
+// rest starts and the last epilogue. 16 rows take 270 us, 5.5 TB/s, and 256 rows
+// 295 us. (Up to 8 rows are the persistent lm_head kernel's.) Rows are taken 256 at
+// a time: 300 cost what 512 do, 0.45 ms. Built for the tensor pipe: a pair of CTAs
 // (cta_group::2) holds 256 rows x 256 words in tensor memory, each CTA loading
 // its 128 rows and half of the words, 64 bytes per cycle and SM at the full rate
 // where one CTA on 128 x 256 would need 96.
@@ -20,13 +20,14 @@
 //    of two accumulators (2 x 256 columns), so that the next tile's products run
 //    under this tile's epilogue.
 //  * Eight epilogue warps per CTA own a row and half of a tile's columns a
-//    thread: 16 at a time the logits go into the running (m, l, w), and those that
+//    thread: 16 at a time the logits go into the running (m, l, w), but those that
 //    beat the row's L-th best (L = 12, or 20 for more than 8 alternatives) into
-//    its list, sorted in registers. A row meets about L (1 + ln(n / L)) such logits
-//    among n, and a warp waits for each of its 32 rows' in turn, so an insertion
-//    decides every place of the list at once (five instructions a place and none
-//    that waits for another: with a bubble pass through the list the epilogue was
-//    longer than the products, 333 us on 16 rows, 0.91 ms on 1,021).
+//    its list, sorted in registers, and what they push out of it into the sums (13
+//    us of 16 rows' 270). A row meets about L (1 + ln(n / L)) such logits among n,
+//    and a warp waits for each of its 32 rows' in turn, so an insertion decides
+//    every place of the list at once (five instructions a place and none that waits
+//    for another: with a bubble pass through the list the epilogue was longer than
+//    the products, 333 us on 16 rows, 0.91 ms on 1,021).
 //  * An item is 256 rows x a range of words; a pair takes items in turn, a row's
 //    state stays in registers over the range, and k_lm_join merges the ranges.
 //
@@ -35,9 +36,11 @@
 // direction, measured 2e-5 at logits near 10. That is too much for the few large
 // logits, which are what the outputs are made of, so the join computes them
 // again: the row's L best and the given token with fp32 multiply-adds (88 a lane
-// and a tree), orders the alternatives by these, and puts them in the place of
-// the first values in the row's sums. The others' share of the sums is small, or
-// their logits are, with their ulps.
+// and a tree), orders the alternatives by these and adds them to the sums of all
+// others. (Listed logits are never in those sums: taken out of a sum by their first
+// values they would leave its rounding, and at a low temperature the first value of
+// the largest is far from the second: T = 1e-6 gave infinities.) The others' share
+// of the sums is small, or their logits are, with their ulps over T.
 // Pairs whose items are the same words and other rows run at the same time, so
 // the embedding comes from HBM once and from L2 for the others.
 #pragma once
@@ -377,36 +380,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
                             v[j] = v0 + j < p.V ? v[j] : -INFINITY;
-                    const float mx = fold(s, v, c, nan);
-                    if (mx <= lv[L - 1])
-                        return;
-                    // (words come in order: an equal logit later does not replace an earlier one; an empty place's NaN
-                    // is below everything)
-                    unsigned in = 0;
+                    float mx = largest(v, nan);
+                    if (!(mx <= lv[L - 1])) {
+                        // (words come in order: an equal logit later does not replace an earlier one; an empty place's NaN
+                        // is below everything)
+                        unsigned in = 0;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        in |= !(v[j] <= lv[L - 1]) ? 1u << j : 0u;
-                    if (v0 + 16 > p.V)
-                        in &= v0 < p.V ? (1u << (p.V - v0)) - 1 : 0u;
-                    for (; in; in &= in - 1) {
-                        const int j = __ffs(in) - 1;
-                        float x[8];
+                        for (int j = 0; j < 16; ++j)
+                            in |= !(v[j] <= lv[L - 1]) ? 1u << j : 0u;
+                        if (v0 + 16 > p.V)
+                            in &= v0 < p.V ? (1u << (p.V - v0)) - 1 : 0u;
+                        for (; in; in &= in - 1) {
+                            const int j = __ffs(in) - 1;
+                            float x[8];
 #pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            x[q] = j & 8 ? v[q + 8] : v[q];
+                            for (int q = 0; q < 8; ++q)
+                                x[q] = j & 8 ? v[q + 8] : v[q];
 #pragma unroll
-                        for (int o = 4; o > 0; o >>= 1)
+                            for (int o = 4; o > 0; o >>= 1)
 #pragma unroll
-                            for (int q = 0; q < o; ++q)
-                                x[q] = j & o ? x[q + o] : x[q];
-                        // every place at once: the one above's entry where that is beaten, else the new one or its own
+                                for (int q = 0; q < o; ++q)
+                                    x[q] = j & o ? x[q + o] : x[q];
+                            // the list's last leaves it for the sums, in the new one's place among the 16
+                            const float last = lv[L - 1] == lv[L - 1] ? lv[L - 1] : -INFINITY, left = !(x[0] <= lv[L - 1]) ? last : x[0];
 #pragma unroll
-                        for (int q = L - 1; q >= 0; --q) {
-                            const bool here = !(x[0] <= lv[q]), above = q > 0 && !(x[0] <= lv[q > 0 ? q - 1 : 0]);
-                            lv[q] = above ? lv[q > 0 ? q - 1 : 0] : here ? x[0] : lv[q];
-                            li[q] = above ? li[q > 0 ? q - 1 : 0] : here ? v0 + j : li[q];
+                            for (int q = 0; q < 16; ++q)
+                                v[q] = q == j ? left : v[q];
+                            // every place at once: the one above's entry where that is beaten, else the new one or its own
+#pragma unroll
+                            for (int q = L - 1; q >= 0; --q) {
+                                const bool here = !(x[0] <= lv[q]), above = q > 0 && !(x[0] <= lv[q > 0 ? q - 1 : 0]);
+                                lv[q] = above ? lv[q > 0 ? q - 1 : 0] : here ? x[0] : lv[q];
+                                li[q] = above ? li[q > 0 ? q - 1 : 0] : here ? v0 + j : li[q];
+                            }
                         }
+                        mx = max16(v);
                     }
+                    fold(s, v, mx, c);
                 };
                 if (live) {
                     load(half * (kLmWords / 2), u[0]);
@@ -466,14 +476,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLmThreads, 1)
 constexpr int kJoinWarps = 4;
 
 // A CTA per row: merges its ranges, computes the largest logits and the given
-// token's again in fp32, corrects the sums and writes the row. All of it is
-// latency (a few KB a row), so the warps share the parts, and a warp's words are
-// read side by side.
+// token's again in fp32, adds them to the others' sums and writes the row. All of
+// it is latency (a few KB a row), so the warps share the parts, and a warp's words
+// are read side by side.
 template <int L>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_lm_join(const uint16_t *emb, const uint16_t *h, const LmArgs p, const Outs o)
 {
     constexpr int kMine = (L + 1 + kJoinWarps - 1) / kJoinWarps;      // words of a warp at most
-    __shared__ float s_v[kJoinWarps][L], s_z[L + 1];
+    __shared__ float s_v[kJoinWarps][L], s_z[L + 1], s_last;
     __shared__ int32_t s_i[kJoinWarps][L], s_w[L + 1];
     __shared__ Sums s_sum[kJoinWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -484,30 +494,50 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_lm_join(const uint16_t *emb
     const int32_t tok = o.logp ? __ldcg(o.tokens + row) : -1;
     // a warp's share of the parts, in order
     const int parts = p.splits * 2, p0 = parts * warp / kJoinWarps, p1 = parts * (warp + 1) / kJoinWarps;
+    const Part *part = p.part + row * parts;
     Sums s;
     int nan = 0;
     TopList top;
-    join_parts(p.part + row * parts + p0, p1 - p0, L, c, lane, s, nan, top);
-    if (lane == 0)
-        s_sum[warp] = s;
+    join_parts(part + p0, p1 - p0, L, c, lane, s, nan, top);
     if (lane < L) {
         s_v[warp][lane] = top.v;
         s_i[warp][lane] = top.i;
     }
     nan = __syncthreads_or(nan);
     if (warp == 0) {
-        if (lane < kJoinWarps)
-            s = s_sum[lane];
-        else
-            s.clear();
-        s = warp_sums(s, c);
         merge_lists(s_v[lane & (kJoinWarps - 1)], s_i[lane & (kJoinWarps - 1)], lane < kJoinWarps ? L : 0, L, lane, top.v, top.i);
         if (lane < L)
             s_w[lane] = top.i;
+        if (lane == L - 1)
+            s_last = top.v;
         if (lane == 0)
             s_w[L] = tok >= 0 && tok < p.V ? tok : kNone;
     }
     __syncthreads();
+    // listed logits that are not among the row's L best go to the others' sums
+    Sums more;
+    more.clear();
+    const float last = s_last;
+    const int32_t last_i = s_w[L - 1];
+    constexpr int kAtOnce = 8;                 // loads on their way
+    for (int e0 = threadIdx.x; e0 < parts * L; e0 += 32 * kJoinWarps * kAtOnce) {
+        float v[kAtOnce];
+        int32_t i[kAtOnce];
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q) {
+            const int e = e0 + q * 32 * kJoinWarps;
+            const bool in = e < parts * L;
+            v[q] = in ? __ldcg(part[e / L].v + e % L) : -INFINITY;
+            i[q] = in ? __ldcg(part[e / L].i + e % L) : kNone;
+        }
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q)
+            if (v[q] > -INFINITY && better(last, last_i, v[q], i[q]))
+                more.add(v[q], c);
+    }
+    s.add(warp_sums(more, c), c);
+    if (lane == 0)
+        s_sum[warp] = s;
     const uint4 *hr = reinterpret_cast<const uint4 *>(h + row * kH) + lane, *er[kMine];
     float acc[kMine][2];
 #pragma unroll
@@ -542,17 +572,17 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_lm_join(const uint16_t *emb
     __syncthreads();
     if (warp)
         return;
-    // the first values of the L best leave the sums, the second ones enter
-    const float z0 = top.v, z1 = lane < L ? s_z[lane] : -INFINITY;
-    float dl = 0.0f, dw = 0.0f;
-    if (lane < L && fabsf(s.m) < INFINITY) {
-        const float d0 = fmaxf((z0 - s.m) * c, kClamp), d1 = fmaxf((z1 - s.m) * c, kClamp);
-        const float e0 = ex2(d0), e1 = ex2(d1);
-        dl = e1 - e0;
-        dw = e1 * d1 - e0 * d0;
-    }
-    s.l += warp_sum(dl);
-    s.w += warp_sum(dw);
+    if (lane < kJoinWarps)
+        s = s_sum[lane];
+    else
+        s.clear();
+    s = warp_sums(s, c);
+    // the L best enter the sums, which refer to the largest of all
+    const float z1 = lane < L ? s_z[lane] : -INFINITY;
+    s.rise(fmaxf(s.m, unordered(__reduce_max_sync(0xFFFFFFFFu, ordered(z1)))), c);
+    const float d = fmaxf((z1 - s.m) * c, kClamp), e = ex2(d);
+    s.l += warp_sum(e);
+    s.w += warp_sum(e * d);
     TopList best;
     best.clear();
     best.offer(lane < L ? z1 : -INFINITY, lane < L ? top.i : kNone, L, lane);

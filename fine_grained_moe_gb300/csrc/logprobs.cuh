@@ -155,18 +155,30 @@ struct Sums {
         l += o.l;
         w += o.w;
     }
+
+    // One logit.
+    __device__ void add(float z, float c)
+    {
+        if (z > m)
+            rise(z, c);
+        const float d = fmaxf((z - m) * c, kClamp), e = ex2(d);
+        l += e;
+        w = fmaf(e, d, w);
+    }
 };
 
-// 16 logits into the running sums of a lane; NaN becomes -inf, in v too.
-// Returns the largest.
-__device__ __forceinline__ float fold(Sums &s, float (&v)[kVals], float c, int &nan)
+// The largest of 16 logits, in three levels; NaN if one is.
+__device__ __forceinline__ float max16(const float (&v)[kVals])
 {
-    float mx;                              // in three levels
-    {
-        const float a = max_nan(v[0], v[1], v[2]), b = max_nan(v[3], v[4], v[5]), d = max_nan(v[6], v[7], v[8]);
-        const float e = max_nan(v[9], v[10], v[11]), f = max_nan(v[12], v[13], v[14]);
-        mx = max_nan(max_nan(a, b, d), max_nan(e, f, v[15]), v[15]);
-    }
+    const float a = max_nan(v[0], v[1], v[2]), b = max_nan(v[3], v[4], v[5]), d = max_nan(v[6], v[7], v[8]);
+    const float e = max_nan(v[9], v[10], v[11]), f = max_nan(v[12], v[13], v[14]);
+    return max_nan(max_nan(a, b, d), max_nan(e, f, v[15]), v[15]);
+}
+
+// The largest of 16 logits; NaN becomes -inf, in v too.
+__device__ __forceinline__ float largest(float (&v)[kVals], int &nan)
+{
+    float mx = max16(v);
     if (mx != mx) {
         nan = 1;
         mx = -INFINITY;
@@ -176,6 +188,12 @@ __device__ __forceinline__ float fold(Sums &s, float (&v)[kVals], float c, int &
             mx = fmaxf(mx, v[j]);
         }
     }
+    return mx;
+}
+
+// 16 logits, the largest of them mx, into the running sums of a lane.
+__device__ __forceinline__ void fold(Sums &s, const float (&v)[kVals], float mx, float c)
+{
     if (mx > s.m)
         s.rise(mx, c);
     // (z - m) c, the difference first: it is exact near the maximum, where z c - m c would be off by m c's rounding, all
@@ -193,7 +211,6 @@ __device__ __forceinline__ float fold(Sums &s, float (&v)[kVals], float c, int &
     const float2 l = unpack2(add2(l2[0], l2[1])), w = unpack2(add2(w2[0], w2[1]));
     s.l += l.x + l.y;
     s.w += w.x + w.y;
-    return mx;
 }
 
 // The sums of 32 lanes: one reference for all, then plain sums in a fixed order.
@@ -417,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 4)
             v[0] = L::one(zr + lane);
         if (lane < tail)
             v[1] = L::one(zr + V - tail + lane);
-        fold(s, v, c, nan);
+        fold(s, v, largest(v, nan), c);
     }
     while (at - lane < v1) {
 #pragma unroll
@@ -436,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 4)
                                 v[i * kVec + j] = -INFINITY;
                 }
                 fetch(at + kDepth * step, raw[q]);
-                fold(s, v, c, nan);
+                fold(s, v, largest(v, nan), c);
             }
             at += step;
         }
@@ -643,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob_rows(const E *z, int64_
             v[0] = L::one(zr + lane);
         if (lane < tail)
             v[1] = L::one(zr + V - tail + lane);
-        fold(s, v, c, nan);
+        fold(s, v, largest(v, nan), c);
     }
     while (at - lane < nvec) {
 #pragma unroll
@@ -662,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob_rows(const E *z, int64_
                                 v[i * kVec + j] = -INFINITY;
                 }
                 fetch(at + kDepth * kChunk, raw[q]);
-                fold(s, v, c, nan);
+                fold(s, v, largest(v, nan), c);
             }
             at += kChunk;
         }
