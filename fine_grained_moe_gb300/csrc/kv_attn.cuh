@@ -504,12 +504,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // (behind the wait: a kernel before this one that lets it start early may not have taken its own tensor memory yet)
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&sh.tmem)), "r"(kCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == 2)
         for (int r = lane; r < R; r += 32)
             sh.orow[r] = r / p.G * p.Hq + r % p.G;

@@ -38,3 +38,17 @@ def test_no_read_only_loads_but_of_weights():
         for load in re.findall(r"__ldg\(([^;]*);", code):
             assert load.startswith("er[j]"), f"{name}: __ldg({load}"      # a word's row of the embedding
         assert not re.search(r"\.nc\b|__restrict__|__ldlu|__nv_ldg", code), name
+
+
+def test_tensor_memory_is_taken_behind_the_wait():
+    """A kernel that holds tensor memory while it waits for the one before it to end
+    would hang with one that lets it start before taking its own."""
+    found = 0
+    for name, text in units_that_overlap().items():
+        code = re.sub(r"//[^\n]*", "", text)
+        if "tcgen05.alloc" in code and "griddepcontrol.wait" in code:
+            for kernel in code.split("__global__")[1:]:
+                if "tcgen05.alloc" in kernel:
+                    found += 1
+                    assert kernel.index("griddepcontrol.wait") < kernel.index("tcgen05.alloc"), name
+    assert found == 2
