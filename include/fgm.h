@@ -349,7 +349,8 @@ int fgm_verify_step_sample(const fgm_layer *layers, int n_layers, const uint16_t
  * Codes 16-byte aligned. Bytes of tokens that no row of an attention call sees
  * may be anything, NaN codes included; the codes that a row sees must be
  * numbers, and the scales of their blocks positive powers of two (what
- * fgm_kv_append writes). */
+ * fgm_kv_append writes), those of values within 2^80 of one another (so beside a
+ * block of zeros, whose scale is 2^-60, values stay below 448 * 2^20). */
 typedef struct fgm_kv_cache {
     uint8_t *k_q;
     float *k_s;

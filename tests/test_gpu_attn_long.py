@@ -193,3 +193,30 @@ def test_windows_beyond_32_bits(fgm):
     for window in (-1, -2 ** 32, 3 - 2 ** 32):
         with pytest.raises(fgm.FgmError):
             fgm.attn_fwd(c, q, lens, 0.125, window=window)
+
+
+@pytest.mark.parametrize("n", [200, 5000])
+def test_block_scales_of_values_far_apart(fgm, n):
+    """Blocks of zeros (scale 2^-60) between loud ones, 2^80 apart: the zeros keep
+    their weight, in one CTA and over several."""
+    H, G, M, D, B = 1, 2, 3, 64, 3
+    g = torch.Generator(device="cuda").manual_seed(n)
+    nb = (n + BLOCK - 1) // BLOCK
+    quiet = torch.arange(nb, device="cuda") % 2 == 0
+    k = torch.randn(nb, H, BLOCK, D, generator=g, device="cuda") * 24
+    v = torch.where(quiet[:, None, None, None], torch.zeros((), device="cuda"),
+                    200 + 60 * torch.randn(nb, H, BLOCK, D, generator=g, device="cuda").clamp(-3, 3))
+    ks = torch.full((nb, H), 2.0 ** -6, device="cuda")
+    vs = torch.where(quiet, 2.0 ** -60, 2.0 ** 20)[:, None].float().contiguous()
+    c = make_cache(fgm, k, v, ks, vs)
+    q = torch.randn(B, M, H * G, D, generator=g, device="cuda").bfloat16()
+    tab = torch.arange(nb, dtype=torch.int32, device="cuda").repeat(B, 1)
+    lse = torch.empty(B, M, H * G, device="cuda")
+    ws = fgm.Workspace("cuda", nbytes=fgm.attn_workspace_bytes(B, M, H * G, H, D))
+    out = fgm.attn_fwd(c, q, torch.full((B,), n, dtype=torch.int32, device="cuda"), 0.125, block_table=tab, lse=lse, ws=ws)
+    assert ws.status() == 0
+    kk, vv = values(c, slice(0, nb), 0)
+    for b in range(B):
+        for i in range(M):
+            seen = n - M + i + 1
+            check_rows(out[b, i], lse[b, i], q[b, i], kk[:seen], vv[:seen], 448 * 2.0 ** 20, 0.125)
