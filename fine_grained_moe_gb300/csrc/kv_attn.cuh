@@ -56,10 +56,14 @@
 // What bounds it, a pass being both kernels: HBM in the steady state up to R = 16,
 // where a unit takes 0.35 us a CTA at D = 128 and twice that at D = 256 (5 tokens
 // at 32K, 8 heads of 256: 134 MB in 32 us); the softmax warps' chain above (R = 48,
-// 2 heads at 256K tokens: 268 MB in 62 us). Around that 5 to 6 us to the first
-// product (cold code, then lens, block table and the first copies one after the
-// other) and 3 to 4 us of k_attn_join: the ragged batch of 9 (147 MB in 37 us)
-// has several starts a CTA, 1,000 tokens are little else (18 us).
+// 2 heads at 256K tokens: 268 MB in 65 us). That chain does not shrink with D as the
+// copies do: 2 heads at 128K tokens take 20, 22, 28, 32 and 58 us at D = 64 with 8,
+// 16, 32, 48 and 64 rows, 33, 34, 38, 40 and 69 at D = 256 (copies: 5 and 20 us).
+// Around that 5 to 6 us to the first product (cold code, then lens, block table and
+// the first copies one after the other) and 3 to 4 us of k_attn_join: the ragged
+// batch of 9 (147 MB in 37 us) has several starts a CTA, 1,000 tokens are little
+// else (10 us in a captured graph). The third probability term costs 40 rows at 256K
+// 6 %, 64 rows 11 % (D = 256) to 30 % (D = 64) over two E4M3 terms, 16 rows 0 to 6.
 //
 // A segment (the part of one (sequence, kv head) in one CTA) that is a whole
 // (sequence, head) is written out; one that spans CTAs leaves partial sums that

@@ -4,10 +4,11 @@
 //
 // 2 * 2816 operations a logit: bound by the tensor pipe from about 300 rows on,
 // by the embedding's 1.48 GB below. 1,021 rows of 262,144 words take 0.84 ms, 1.80
-// PFLOP/s: the products 0.80 with the tensor pipe 92 % busy, the join 0.02, the
-// rest starts and the last epilogue. 16 rows take 270 us, 5.5 TB/s, and 256 rows
-// 295 us. (Up to 8 rows are the persistent lm_head kernel's.) Rows are taken 256 at
-// a time: 300 cost what 512 do, 0.45 ms. Built for the tensor pipe: a pair of CTAs
+// PFLOP/s, in short runs (0.95 ms, 1.59, where the part settles at its sustained
+// rate): the products 0.81 with the tensor pipe 92 % busy, the join 0.02, the rest
+// starts and the last epilogue. 16 rows take 264 us, 5.6 TB/s, and 256 rows 288 us.
+// (Up to 8 rows are the persistent lm_head kernel's.) Rows are taken 256 at a time:
+// 300 cost what 512 do, 0.45 ms. Built for the tensor pipe: a pair of CTAs
 // (cta_group::2) holds 256 rows x 256 words in tensor memory, each CTA loading
 // its 128 rows and half of the words, 64 bytes per cycle and SM at the full rate
 // where one CTA on 128 x 256 would need 96.
@@ -22,8 +23,8 @@
 //  * Eight epilogue warps per CTA own a row and half of a tile's columns a
 //    thread: 16 at a time the logits go into the running (m, l, w), but those that
 //    beat the row's L-th best (L = 12, or 20 for more than 8 alternatives) into
-//    its list, sorted in registers, and what they push out of it into the sums (13
-//    us of 16 rows' 270). A row meets about L (1 + ln(n / L)) such logits among n,
+//    its list, sorted in registers, and what they push out of it into the sums (14
+//    us of 16 rows' 264). A row meets about L (1 + ln(n / L)) such logits among n,
 //    and a warp waits for each of its 32 rows' in turn, so an insertion decides
 //    every place of the list at once (five instructions a place and none that waits
 //    for another: with a bubble pass through the list the epilogue was longer than

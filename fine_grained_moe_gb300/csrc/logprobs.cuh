@@ -605,8 +605,10 @@ __global__ void __launch_bounds__(kThreads, 4)
 }
 
 // The same with a warp per row and no split, for rows too short to be worth a
-// CTA's barriers: 57,788 rows of 715 fp32 logits take 83 us where a CTA each took
-// 402 us, 4,000 rows of 8,000 bf16 21 us where it took 35.
+// CTA's barriers: 20,000 rows of 3 KB take 39 us at k = 8 where a CTA each takes
+// 136 (17 and 81 at k = 0), 4,864 rows of 16 KB 21 us where it takes 39 (fp32) and 26
+// where it takes 46 (bf16). 57,788 rows of 715 fp32 logits: 91 us, 1.8 TB/s, bound by
+// a row's end (count, second look, ranking), under which a warp loads nothing.
 template <typename E>
 __global__ void __launch_bounds__(kThreads, 4) k_logprob_rows(const E *z, int64_t stride, int64_t N, const Outs o)
 {

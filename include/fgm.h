@@ -370,7 +370,8 @@ typedef struct fgm_kv_cache {
  * Scales are powers of two, so that growing one moves the kept codes by exact
  * factors (values that become subnormal, below 2^-6 s, excepted). Slots
  * behind the sequence's end are left as they are: to take rejected drafts
- * back, call again with the smaller length. NaN is stored as 0 and infinities
+ * back, call again with the smaller length (a scale that a rejected draft made
+ * grow stays grown for the tokens kept in its block). NaN is stored as 0 and infinities
  * as the largest code, with FGM_STATUS_NONFINITE_KV; neither enters amax.
  *  k, v         bf16 [B][N][n_kv_heads][D], 16-byte aligned; tokens token_stride elements
  *               apart, sequences N * token_stride (a slice of a fused projection's output:
@@ -453,11 +454,16 @@ int fgm_logprobs(const void *z, int dtype, int64_t row_stride, int64_t N, int64_
 size_t fgm_lm_head_logprobs_workspace_bytes(int64_t N, int64_t V, int k);
 
 /* The same from hidden rows: log probabilities under the tied lm_head's logits
- * z[n][v] = sum_j emb[v][j] * h[n][j] (fp32 accumulation) of N rows, one for a
- * decoded token, M for a verify step, thousands for a scored text. Every sum over
- * the logits is fp32. More than 8 rows: they are not stored. Up to 8 rows: the
- * persistent lm_head kernel writes them into the workspace, which must be
- * initialised and in use by no other call meanwhile. Arguments as fgm_logprobs, and
+ * z[n][v] = sum_j emb[v][j] * h[n][j] of N rows, one for a decoded token, M for a
+ * verify step, thousands for a scored text. Every sum over the logits is fp32. More
+ * than 8 rows: they are not stored; a row's 12 largest (20 for k > 8), from which
+ * the alternatives are ranked, and the given token's are sums in fp32; the others,
+ * which only enter the sums over the logits, carry the truncation of the tensor
+ * pipe's accumulator, up to 176 units in the last place of their partial sums
+ * (2e-5 at logits near 10), which counts over T. Up to 8 rows: the persistent
+ * lm_head kernel writes z, as fgm_lm_head_sample does, into the workspace, which
+ * must be initialised and in use by no other call meanwhile. Arguments as
+ * fgm_logprobs, and
  *  emb  bf16 [V][2816] (16-byte aligned), 1 <= V < 2^31
  *  h    bf16 [N][2816] final hidden states (16-byte aligned), 1 <= N <= 2^24 */
 int fgm_lm_head_logprobs(const uint16_t *emb, int64_t V, const uint16_t *h, int64_t N, float T, const int32_t *tokens,
@@ -471,9 +477,9 @@ int fgm_select_path(int path);
 
 /* Upper bound, in ns of GPU time, on every wait inside the persistent kernel
  * (grid barriers, ring slots) and inside those of fgm_attn_fwd and
- * fgm_lm_head_logprobs (there each wait has the limit to itself). When a wait runs out the kernel raises
- * FGM_STATUS_WAIT_TIMEOUT, skips its remaining work and exits; its outputs are
- * then invalid. Default 2 s; ns < 0 only queries. Returns the previous value. */
+ * fgm_lm_head_logprobs (there each wait has the limit to itself). When a wait runs
+ * out the kernel raises FGM_STATUS_WAIT_TIMEOUT, skips its remaining work and
+ * exits; its outputs are then invalid. Default 2 s; ns < 0 only queries. Returns the previous value. */
 long long fgm_set_wait_limit_ns(long long ns);
 
 /* Profiling aid: when buf (DEVICE, n int64 entries) is non-NULL, each later
