@@ -55,3 +55,46 @@ def test_appends_and_attentions_back_to_back(fgm):
         for name in ("k_q", "v_q", "k_s", "v_s"):
             assert torch.equal(getattr(a, name), getattr(b, name)), name
     assert ws.status() == 0
+
+
+def test_streams_at_once(fgm):
+    """Three streams with a workspace each run every operator at the same time; the
+    bits are those of the calls one after another."""
+    def job(seed):
+        g = torch.Generator().manual_seed(seed)
+        H, G, M, D = 2, 4, 5, 64 << (seed % 3)
+        V, N = 9001, (3, 20, 300)[seed % 3]
+        q = torch.randn(2, M, H * G, D, generator=g).bfloat16().cuda()
+        k, v = (torch.randn(2, M, H, D, generator=g).bfloat16().cuda() for _ in range(2))
+        lens = torch.tensor([900 + seed, 70], dtype=torch.int32, device="cuda")
+        tab = torch.randperm(32, generator=g).view(2, 16).to(torch.int32).cuda()
+        emb = (torch.randn(V, 2816, generator=g) * 0.02).bfloat16().cuda()
+        h = torch.randn(N, 2816, generator=g).bfloat16().cuda()
+        z = torch.randn(40, V, generator=g).cuda()
+        t = torch.randint(0, V, (300,), generator=g).to(torch.int32).cuda()
+        ws = fgm.Workspace("cuda", nbytes=max(fgm.attn_workspace_bytes(2, M, H * G, H, D), fgm.logprobs_workspace_bytes(40, V, 5),
+                                              fgm.lm_head_logprobs_workspace_bytes(N, V, 5)))
+        cache = random_cache(fgm, 32, H, D, seed=seed)
+
+        def run():
+            fgm.kv_append(cache, k, v, lens, block_table=tab, ws=ws)
+            out = fgm.attn_fwd(cache, q, lens, D ** -0.5, block_table=tab, ws=ws)
+            a = fgm.logprobs(z, t[:40], k=5, ws=ws)
+            b = fgm.lm_head_logprobs(emb, h, t[:N], k=5, ws=ws)
+            return [out, *a, *b, cache.k_q, cache.v_q, cache.k_s, cache.v_s]
+        return run, ws
+
+    jobs = [job(s) for s in range(3)]
+    want = [[x.clone() for x in run()] for run, _ in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(20):
+        got = []
+        for s, (run, _) in zip(streams, jobs):
+            with torch.cuda.stream(s):
+                got.append(run())
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            for x, y in zip(a, b):
+                assert torch.equal(x, y)
+    assert all(ws.status() == 0 for _, ws in jobs)
