@@ -33,6 +33,9 @@ STATUS_NONFINITE_LOGITS = 1
 STATUS_WAIT_TIMEOUT = 2
 STATUS_NONFINITE_KV = 4
 STATUS_BAD_BLOCK = 8
+MAX_TOKENS = 1 << 18  # tokens of moe_route and moe_experts_fwd
+MAX_GROUPS = 1024  # experts of moe_group and grouped_gemm
+E4M3 = 3           # element type of 8-bit weights in the C ABI
 MAX_TOP = 16       # alternatives per row of the log-probability calls
 KV_BLOCK = 64      # tokens of a KV-cache block
 ATTN_MAX_ROWS = 64  # query rows sharing a kv head: M * n_q_heads / n_kv_heads
@@ -63,6 +66,15 @@ class fgm_mlp(ctypes.Structure):
 class fgm_kv_cache(ctypes.Structure):
     _fields_ = [("k_q", ctypes.c_void_p), ("k_s", ctypes.c_void_p), ("v_q", ctypes.c_void_p), ("v_s", ctypes.c_void_p),
                 ("n_blocks", ctypes.c_int64), ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
+class fgm_block(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("D", ctypes.c_int)] + \
+               [(n, ctypes.c_int) for n in ("h_type", "y_type", "gate_type", "gain_type", "xn_type")] + \
+               [(n, ctypes.c_void_p) for n in ("h", "y", "gate", "post_gain", "pre_gain", "h_out", "xn")] + \
+               [(n, ctypes.c_int64) for n in ("h_stride", "y_stride", "gate_row_stride", "h_out_stride", "xn_stride")] + \
+               [("gate_col_stride", ctypes.c_int), ("post_norm", ctypes.c_int)] + \
+               [(n, ctypes.c_float) for n in ("residual_scale", "block_scale", "gain_offset", "eps")]
 
 
 def lib() -> ctypes.CDLL:
@@ -102,6 +114,15 @@ def lib() -> ctypes.CDLL:
             "fgm_logprobs": (ci, [vp, ci, i64, i64, i64, ctypes.c_float, vp, ci, vp, vp, vp, vp, vp, sz, vp]),
             "fgm_lm_head_logprobs_workspace_bytes": (sz, [i64, i64, ci]),
             "fgm_lm_head_logprobs": (ci, [vp, i64, vp, i64, ctypes.c_float, vp, ci, vp, vp, vp, vp, vp, sz, vp]),
+            "fgm_moe_route_workspace_bytes": (sz, [i64]),
+            "fgm_moe_route": (ci, [vp, vp, vp, i64, i64, vp, vp, vp, vp, vp, sz, vp]),
+            "fgm_moe_group_workspace_bytes": (sz, [i64, ci]),
+            "fgm_moe_group": (ci, [vp, i64, ci, vp, vp, vp, sz, vp]),
+            "fgm_grouped_gemm_workspace_bytes": (sz, [i64, i64, ci, ci, ci]),
+            "fgm_grouped_gemm": (ci, [vp, i64, i64, vp, ci, vp, vp, ci, vp, ci, ci, ci, vp, i64, vp, sz, vp]),
+            "fgm_moe_experts_workspace_bytes": (sz, [i64]),
+            "fgm_moe_experts_fwd": (ci, [LP, vp, i64, i64, vp, vp, ci, vp, vp, sz, vp]),
+            "fgm_block_norm": (ci, [ctypes.POINTER(fgm_block), vp]),
             "fgm_read_status": (ci, [vp, sz, ci, vp, vp]),
             "fgm_select_path": (ci, [ci]),
             "fgm_set_phase_trace": (ci, [vp, sz]),
@@ -805,4 +826,204 @@ def lm_head_logprobs(emb: torch.Tensor, h: torch.Tensor, tokens: torch.Tensor | 
         _check(lib().fgm_lm_head_logprobs(e_at, V, h_at, N, T, at, k, _at(r.logp), _at(r.entropy), _at(r.top_ids),
                                           _at(r.top_logp), w.t.data_ptr(), w.nbytes, s))
         return r
+    return _call(dev, stream, body)
+
+
+# ---------------------------------------------------------------- a prompt through the experts
+class Routing(NamedTuple):
+    """Of T tokens: chosen experts int32 [T, 8], their weights fp32 [T, 8], and the
+    slots 8 * token + choice grouped by expert: offsets int32 [129], order int32 [8 T]."""
+    ids: torch.Tensor
+    weights: torch.Tensor
+    offsets: torch.Tensor
+    order: torch.Tensor
+
+
+def _dense_rows(name: str, t: torch.Tensor, width: int | None, device=None) -> int:
+    """Elements between the rows of a bf16 [n, width] tensor with dense rows."""
+    if t.dtype is not _BF16 or t.dim() != 2 or (width is not None and t.shape[1] != width) or not t.is_cuda or \
+            (device is not None and t.device != device):
+        raise FgmError(f"{name}: expected CUDA bf16 [n, {'K' if width is None else width}]"
+                       f"{'' if device is None else f' on {device}'}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+    n, w = t.shape
+    sn, sw = t.stride()
+    if w > 1 and sw != 1 or n > 1 and sn < w:
+        raise FgmError(f"{name}: expected dense rows that do not overlap, strides {t.stride()}")
+    return sn if n > 1 else (w + 7) // 8 * 8
+
+
+def moe_route_workspace_bytes(T: int) -> int:
+    """Workspace bytes of moe_route (0 for sizes out of range)."""
+    return int(lib().fgm_moe_route_workspace_bytes(int(T)))
+
+
+def moe_route(router_w: torch.Tensor, x: torch.Tensor, router_b: torch.Tensor | None = None, out: Routing | None = None,
+              ws: Workspace | None = None, stream=None) -> Routing:
+    """Routes the bf16 rows x [T, 2816] (any T): top 8 of 128 by the exact logits
+    router_w . x + router_b, softmax over the 8, and the slots grouped by expert."""
+    dev = x.device
+    stride = _dense_rows("x", x, HIDDEN)
+    T = x.shape[0]
+    w_at = _expect("router_w", router_w, (EXPERTS, HIDDEN), _BF16, dev)
+    b_at = None if router_b is None else _expect("router_b", router_b, (EXPERTS,), _F32, dev)
+
+    def body(s):
+        i32 = dict(dtype=_I32, device=dev)
+        r = Routing(torch.empty((T, TOPK), **i32), torch.empty((T, TOPK), dtype=_F32, device=dev),
+                    torch.empty(EXPERTS + 1, **i32), torch.empty(T * TOPK, **i32)) if out is None else out
+        w = Workspace(dev, nbytes=moe_route_workspace_bytes(T)) if ws is None else ws
+        _check(lib().fgm_moe_route(w_at, b_at, x.data_ptr(), stride, T, _expect("out.ids", r.ids, (T, TOPK), _I32, dev),
+                                   _expect("out.weights", r.weights, (T, TOPK), _F32, dev),
+                                   _expect("out.offsets", r.offsets, (EXPERTS + 1,), _I32, dev),
+                                   _expect("out.order", r.order, (T * TOPK,), _I32, dev), w.t.data_ptr(), w.nbytes, s))
+        return r
+    return _call(dev, stream, body)
+
+
+def moe_group_workspace_bytes(n: int, E: int) -> int:
+    """Workspace bytes of moe_group (0 for sizes out of range)."""
+    return int(lib().fgm_moe_group_workspace_bytes(int(n), int(E)))
+
+
+def moe_group(ids: torch.Tensor, E: int, offsets: torch.Tensor | None = None, order: torch.Tensor | None = None,
+              ws: Workspace | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Groups the slots of int32 ids (any shape, flat order) by expert 0 .. E - 1: (offsets
+    int32 [E + 1], order int32 [slots]); ids outside belong to none, and the places
+    behind the last expert's are not written."""
+    dev = ids.device
+    if not ids.is_cuda:
+        raise FgmError("expected a CUDA tensor")
+    n = ids.numel()
+    at = _expect("ids", ids, tuple(ids.shape), _I32, dev)
+
+    def body(s):
+        o = torch.empty(E + 1, dtype=_I32, device=dev) if offsets is None else offsets
+        r = torch.empty(n, dtype=_I32, device=dev) if order is None else order
+        w = Workspace(dev, nbytes=moe_group_workspace_bytes(n, E)) if ws is None else ws
+        _check(lib().fgm_moe_group(at, n, E, _expect("offsets", o, (E + 1,), _I32, dev), _expect("order", r, (n,), _I32, dev),
+                                   w.t.data_ptr(), w.nbytes, s))
+        return o, r
+    if not 1 <= E <= MAX_GROUPS:
+        raise FgmError(f"E = {E} outside [1, {MAX_GROUPS}]")
+    return _call(dev, stream, body)
+
+
+def grouped_gemm_workspace_bytes(x_rows: int, R: int, E: int, N: int, K: int) -> int:
+    """Workspace bytes of grouped_gemm (0 for sizes out of range)."""
+    return int(lib().fgm_grouped_gemm_workspace_bytes(int(x_rows), int(R), int(E), int(N), int(K)))
+
+
+def grouped_gemm(x: torch.Tensor, w: torch.Tensor, w_s: torch.Tensor | None, offsets: torch.Tensor,
+                 rows: torch.Tensor | None = None, per: int = 1, out: torch.Tensor | None = None,
+                 ws: Workspace | None = None, stream=None) -> torch.Tensor:
+    """Products grouped by expert: rows offsets[e] .. offsets[e + 1] of the result are
+    bf16 x[rows // per] (or x itself) times w[e] [N, K] transposed, times w_s[e]. w is uint8
+    [E, N, K] E4M3 codes or bf16; w_s fp32 [E, N] or None. Returns bf16 [R, N], whose rows of
+    no expert are as they were in ``out``."""
+    dev = x.device
+    stride = _dense_rows("x", x, None)
+    if w.dim() != 3 or w.dtype not in (_U8, _BF16):
+        raise FgmError(f"w: expected uint8 (E4M3) or bf16 [E, N, K], got {tuple(w.shape)} {w.dtype}")
+    E, N, K = w.shape
+    if x.shape[1] != K:
+        raise FgmError(f"x: expected rows of K = {K}, got {tuple(x.shape)}")
+    w_at = _expect("w", w, (E, N, K), w.dtype, dev)
+    s_at = None if w_s is None else _expect("w_s", w_s, (E, N), _F32, dev)
+    o_at = _expect("offsets", offsets, (E + 1,), _I32, dev)
+    if rows is not None and rows.dim() != 1:
+        raise FgmError(f"rows: expected int32 [R], got {tuple(rows.shape)}")
+    R = x.shape[0] if rows is None else rows.shape[0]
+    r_at = None if rows is None else _expect("rows", rows, (R,), _I32, dev)
+
+    def body(s):
+        o = torch.empty((R, N), dtype=_BF16, device=dev) if out is None else out
+        v = Workspace(dev, nbytes=grouped_gemm_workspace_bytes(x.shape[0], R, E, N, K)) if ws is None else ws
+        _check(lib().fgm_grouped_gemm(x.data_ptr(), stride, x.shape[0], r_at, per, o_at, w_at, E4M3 if w.dtype is _U8 else 1, s_at,
+                                      E, N, K, _expect("out", o, (R, N), _BF16, dev), R, v.t.data_ptr(), v.nbytes, s))
+        return o
+    return _call(dev, stream, body)
+
+
+def moe_experts_workspace_bytes(T: int) -> int:
+    """Workspace bytes of moe_experts_fwd (0 for sizes out of range)."""
+    return int(lib().fgm_moe_experts_workspace_bytes(int(T)))
+
+
+def moe_experts_fwd(layer, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, y: torch.Tensor | None = None,
+                    shared: bool = True, ws: Workspace | None = None, stream=None) -> torch.Tensor:
+    """A layer's experts on the bf16 rows x [T, 2816] (any T), each token's experts
+    int32 ids [T, 8] (outside [0, 128): none) weighted by fp32 weights [T, 8], plus
+    the shared expert; returns bf16 y [T, 2816]."""
+    dev = x.device
+    stride = _dense_rows("x", x, HIDDEN)
+    T = x.shape[0]
+    L = (layer if isinstance(layer, Layer) else Layer.from_dict(layer)).struct()
+    i_at = _expect("ids", ids, (T, TOPK), _I32, dev)
+    w_at = _expect("weights", weights, (T, TOPK), _F32, dev)
+
+    def body(s):
+        o = torch.empty((T, HIDDEN), dtype=_BF16, device=dev) if y is None else y
+        w = Workspace(dev, nbytes=moe_experts_workspace_bytes(T)) if ws is None else ws
+        _check(lib().fgm_moe_experts_fwd(ctypes.byref(L), x.data_ptr(), stride, T, i_at, w_at, int(shared),
+                                         _expect("y", o, (T, HIDDEN), _BF16, dev), w.t.data_ptr(), w.nbytes, s))
+        return o
+    return _call(dev, stream, body)
+
+
+def _norm_rows(name: str, t: torch.Tensor, shape: tuple, device) -> tuple[int, int, int]:
+    """(address, type, elements between rows) of a tensor with dense rows."""
+    if t.dtype not in _DTYPES or t.shape != shape or t.device != device:
+        raise FgmError(f"{name}: expected fp32, bf16 or fp16 {tuple(shape)} on {device}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+    sn, sd = t.stride()
+    if shape[1] > 1 and sd != 1:
+        raise FgmError(f"{name}: expected dense rows, strides {t.stride()}")
+    return t.data_ptr(), _DTYPES[t.dtype], sn if shape[0] > 1 else max(sn, shape[1])
+
+
+def block_norm(h: torch.Tensor, y: torch.Tensor | None = None, post_gain: torch.Tensor | None = None,
+               gate: torch.Tensor | None = None, pre_gain: torch.Tensor | None = None, post_norm: bool = True,
+               pre_norm: bool = True, residual_scale: float = 1.0, block_scale: float = 1.0, gain_offset: float = 0.0,
+               eps: float = 1e-6, h_out: torch.Tensor | None = None, xn: torch.Tensor | None = None,
+               stream=None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """The norms around a block: h' = residual_scale * h + block_scale * gate * post(y) and
+    xn = pre(h') (RMS norms with gains post_gain, pre_gain [D]); gate [D] a channel, [N, 1] a
+    token or [N, D]. Returns (h', xn): h' in h's type (``h_out`` may be h), xn in bf16 or in the type of
+    ``xn``; xn is None without pre_norm."""
+    if h.dim() != 2 or not h.is_cuda:
+        raise FgmError(f"h: expected CUDA [N, D], got {tuple(h.shape)} on {h.device}")
+    dev, (N, D) = h.device, h.shape
+    b = fgm_block(N=N, D=D, post_norm=int(post_norm and y is not None), residual_scale=residual_scale, block_scale=block_scale,
+                  gain_offset=gain_offset, eps=eps)
+    b.h, b.h_type, b.h_stride = _norm_rows("h", h, (N, D), dev)
+    if y is not None:
+        b.y, b.y_type, b.y_stride = _norm_rows("y", y, (N, D), dev)
+    if gate is not None:
+        if gate.dtype not in _DTYPES or gate.device != dev or tuple(gate.shape) not in ((D,), (N, 1), (N, D)):
+            raise FgmError(f"gate: expected [{D}], [{N}, 1] or [{N}, {D}] on {dev}, got {tuple(gate.shape)} {gate.dtype} on {gate.device}")
+        per_row = gate.dim() == 2 and gate.shape[1] == 1
+        if not per_row and D > 1 and gate.stride(-1) != 1:
+            raise FgmError(f"gate: expected dense rows, strides {gate.stride()}")
+        b.gate, b.gate_type, b.gate_col_stride = gate.data_ptr(), _DTYPES[gate.dtype], int(not per_row)
+        b.gate_row_stride = gate.stride(0) if gate.dim() == 2 and N > 1 else 0
+    gains = [t for t in (post_gain, pre_gain) if t is not None]
+    for t in gains:
+        if t.dtype not in _DTYPES or t.shape != (D,) or t.device != dev or not t.is_contiguous() or t.dtype is not gains[0].dtype:
+            raise FgmError(f"gains: expected contiguous [{D}] of one type on {dev}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+    if gains:
+        b.gain_type = _DTYPES[gains[0].dtype]
+    b.post_gain, b.pre_gain = _at(post_gain), _at(pre_gain)
+
+    def body(s):
+        o = torch.empty((N, D), dtype=h.dtype, device=dev) if h_out is None else h_out
+        b.h_out, t, b.h_out_stride = _norm_rows("h_out", o, (N, D), dev)
+        if t != b.h_type:
+            raise FgmError(f"h_out: expected {h.dtype}, got {o.dtype}")
+        n = None
+        if pre_norm:
+            n = torch.empty((N, D), dtype=_BF16, device=dev) if xn is None else xn
+            b.xn, b.xn_type, b.xn_stride = _norm_rows("xn", n, (N, D), dev)
+        elif xn is not None:
+            raise FgmError("xn without pre_norm")
+        _check(lib().fgm_block_norm(b, s))
+        return o, n
     return _call(dev, stream, body)

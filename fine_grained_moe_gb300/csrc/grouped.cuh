@@ -1,0 +1,422 @@
+// Matrix products grouped by expert (fgm_grouped_gemm, and the two products of
+// fgm_moe_experts_fwd): with rows [off[e], off[e + 1]) belonging to expert e,
+//   D[n][r] = sum_k W_e[n][k] x[src(r)][k],
+// W_e in E4M3 codes or bf16, x in bf16.
+//
+// 8-bit weights go to the tensor pipe as they are stored. An activation enters as
+// two E4M3 terms under a power of two per row, t1 = e4m3(x / s), t2 = e4m3(x / s - t1):
+// a bf16 number has 8 significant bits and a term 4, so t1 + t2 is x / s exactly
+// where that is 1/4 or more, else to 2^-10 (s puts the row's largest element into
+// [128, 256), moe_rows.cuh). Two
+// 8-bit products take as long as one bf16 product would, and the weights as half the
+// bytes, without a conversion anywhere.
+#pragma once
+
+#include <cuda.h>
+
+#include "pair_copies.h"
+#include "tensor.cuh"
+
+namespace fgm {
+namespace grouped {
+
+constexpr int kThreads = 384;                    // copies, products, -, -, eight epilogue warps
+constexpr int kMaxStages = 12;
+constexpr int kMaxExperts = 1024;
+constexpr int kStageK = 128;                     // elements of K in a stage
+constexpr int kBox = 128 * 128;                  // 128 weight rows x 128 bytes
+constexpr int kRing = 208 * 1024;                // bytes of the ring at most
+
+enum Mode {
+    kGemm = 0,   // out[r][n] = bf16(s[n] xs[r] D)
+    kGated = 1,  // a[r][n] = gelu(s_g[n] xs[r] D_g) * (s_u[n] xs[r] D_u), f16 under a power of two per 32 of n
+    kDown = 2,   // y[r][n] = f16(s[n] / smax[e] 2^-12 D)
+};
+
+struct Args {
+    const int32_t *offsets;  // [E + 1]
+    int E;
+    int64_t R;               // rows at most
+    const int32_t *src;      // row r takes x row src[r] / per; NULL: x row r
+    int per;
+    int x_rows;
+    int N, K;
+    const float *s0, *s1;    // [E][N] row scales (gate and up), or NULL
+    const float *xs;         // [x_rows] scales of the terms
+    uint16_t *out;           // [R][N]
+    uint8_t *exps;           // kGated: [R][N / 32] exponents
+    const float *smax;       // kDown: [E] a power of two not below the expert's scales
+    int cols;                // rows of a tile at most, a multiple of 32
+    int stages;
+    int32_t *status;
+    long long timeout_ns;
+};
+
+struct Shared {
+    unsigned long long full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], drained;
+    uint32_t tmem;
+    int abort;
+    uint32_t issued;
+    uint32_t bytes[kMaxStages], others[kMaxStages];
+    int row0[kMaxExperts], count[kMaxExperts], cum[kMaxExperts + 1];   // rows and tiles before, by expert
+};
+
+// Weight boxes of a stage: gate and up rows, or one of 8-bit rows (128 of K), or two of bf16 (64 of K each).
+template <Mode MODE, bool BYTES>
+__host__ __device__ constexpr int weight_boxes() { return MODE == kGated || !BYTES ? 2 : 1; }
+
+// Bytes of a stage whose tiles have up to `cols` rows (half of them in each CTA, 2 x 128 bytes a row).
+template <Mode MODE, bool BYTES>
+__host__ __device__ constexpr int stage_bytes(int cols) { return weight_boxes<MODE, BYTES>() * kBox + cols * 128; }
+
+__device__ __forceinline__ void copy_weights(uint32_t dst, const CUtensorMap *map, int k, int n, int e, uint32_t bar, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(k), "r"(n), "r"(e), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+// 8 rows x 128 bytes,
+__device__ __forceinline__ void copy_rows(uint32_t dst, const CUtensorMap *map, int at, int row, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(at), "r"(row), "r"(bar)
+        : "memory");
+}
+
+// or four rows anywhere.
+__device__ __forceinline__ void copy_gathered(uint32_t dst, const CUtensorMap *map, int at, int4 rows, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(at), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(bar)
+        : "memory");
+}
+
+// A tile: rows [r0, r0 + live) of expert e against 256 of its output features (of
+// each product) from n0 on. A pair's items come in ascending order.
+struct Tile {
+    int e, n0, r0, live;
+
+    __device__ __forceinline__ void find(const Shared &sh, const Args &p, int item)
+    {
+        while (item >= sh.cum[e + 1])
+            ++e;
+        const int c = sh.count[e], nt = (c + p.cols - 1) / p.cols, local = item - sh.cum[e], n = local % nt;
+        n0 = local / nt * 256;
+        const int a = static_cast<int>(static_cast<int64_t>(c) * n / nt), b = static_cast<int>(static_cast<int64_t>(c) * (n + 1) / nt);
+        r0 = sh.row0[e] + a;
+        live = b - a;
+    }
+
+    // columns of the products in each CTA's half of the second operand
+    __device__ __forceinline__ int half() const { return (live + 15) / 16 * 8; }
+};
+
+template <Mode MODE, bool BYTES>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    k_grouped(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap wmap2, const __grid_constant__ CUtensorMap xmap,
+              const Args p)
+{
+    constexpr int kWBoxes = weight_boxes<MODE, BYTES>();
+    extern __shared__ uint8_t dsm_raw[];
+    __shared__ Shared sh;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = tc::cluster_rank();
+    const uint32_t ring = (tc::saddr(dsm_raw) + 1023u) & ~1023u, xbox = p.cols * 64, rows_at = kWBoxes * kBox,
+                   stage = rows_at + 2 * xbox, stages = p.stages;
+    const int pairs = gridDim.x / 2, pair = blockIdx.x / 2, steps = (p.K + kStageK - 1) / kStageK;
+
+    if (tid == 0) {
+        for (int i = 0; i < kMaxStages; ++i) {
+            tc::bar_init(&sh.full[i], 1);
+            tc::bar_init(&sh.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::bar_init(&sh.tfull[i], 1);
+            tc::bar_init(&sh.tempty[i], 16);     // the epilogue warps of both CTAs
+        }
+        tc::bar_init(&sh.drained, 1);
+        sh.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    tc::after_previous();
+    if (warp == 1)
+        tc::memory_take<2>(&sh.tmem);
+    if (warp == 2) {
+        // tiles before each expert
+        const int across = (p.N + 255) / 256;
+        int base = 0;
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+            const int e = e0 + lane;
+            int64_t a = 0, b = 0;
+            if (e < p.E) {
+                a = __ldcg(p.offsets + e);
+                b = __ldcg(p.offsets + e + 1);
+                a = a < 0 ? 0 : a > p.R ? p.R : a;
+                b = b < a ? a : b > p.R ? p.R : b;
+            }
+            int v = (static_cast<int>(b - a) + p.cols - 1) / p.cols * across, sum = v;
+            if (e < p.E) {
+                sh.row0[e] = static_cast<int>(a);
+                sh.count[e] = static_cast<int>(b - a);
+            }
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+                sum += lane >= o ? u : 0;
+            }
+            if (e < p.E)
+                sh.cum[e + 1] = base + sum;
+            base += __shfl_sync(0xFFFFFFFFu, sum, 31);
+        }
+        if (lane == 0)
+            sh.cum[0] = 0;
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::cluster_sync();
+    tc::fence_after();
+    tc::let_next_start();
+    const uint32_t tmem = sh.tmem;
+    const tc::Waiter wait{&sh.abort, p.status, p.timeout_ns};
+    const int items = sh.cum[p.E];
+    Tile t;
+    t.e = 0;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ copies (each CTA its own weights and rows)
+        if (lane == 0) {
+            tc::prefetch_map(&wmap);
+            tc::prefetch_map(&wmap2);
+            tc::prefetch_map(&xmap);
+        }
+        uint64_t once, again;
+        asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+        asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(again));
+        bool ok = true;
+        uint32_t n = 0;
+        for (int item = pair; item < items && ok; item += pairs) {
+            t.find(sh, p, item);
+            const int half = t.half(), at = rank * half;
+            const uint32_t mine = kWBoxes * kBox + half * 256;
+            const uint64_t policy = sh.count[t.e] <= p.cols ? once : again;
+            int4 idx = make_int4(0, 0, 0, 0);
+            if (p.src && 4 * lane < half) {
+                // (places behind the tile's rows, and rows of x that are not there, take row 0: never stored)
+                int v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int c = at + 4 * lane + j;
+                    const int s = c < t.live ? __ldcg(p.src + t.r0 + c) : 0;
+                    v[j] = s >= 0 && s / p.per < p.x_rows ? s / p.per : 0;
+                }
+                idx = make_int4(v[0], v[1], v[2], v[3]);
+            }
+            for (int ks = 0; ks < steps; ++ks, ++n) {
+                const uint32_t slot = n % stages;
+                if (n >= stages)
+                    ok = wait(&sh.empty[slot], n / stages - 1, 34, ks);
+                if (!(ok = __all_sync(0xFFFFFFFFu, ok)))
+                    break;
+                const uint32_t bar = tc::in_first(tc::saddr(&sh.full[slot])), dst = ring + slot * stage;
+                if (lane == 0) {
+                    if (rank == 0)
+                        tc::bar_expect(tc::saddr(&sh.full[slot]), 2 * mine);
+                    sh.bytes[slot] = sh.others[slot] = mine;
+                    const int w0 = t.n0 + rank * 128;
+                    copy_weights(dst, &wmap, ks * kStageK, w0, t.e, bar, policy);
+                    if (MODE == kGated)
+                        copy_weights(dst + kBox, &wmap2, ks * kStageK, w0, t.e, bar, policy);
+                    else if (!BYTES)
+                        copy_weights(dst + kBox, &wmap, ks * kStageK + 64, w0, t.e, bar, policy);
+                }
+                __syncwarp();
+                if (p.src) {
+                    if (4 * lane < half) {
+                        copy_gathered(dst + rows_at + lane * 512, &xmap, ks * 256, idx, bar);
+                        copy_gathered(dst + rows_at + xbox + lane * 512, &xmap, ks * 256 + 128, idx, bar);
+                    }
+                } else if (8 * lane < half) {
+                    copy_rows(dst + rows_at + lane * 1024, &xmap, ks * 256, t.r0 + at + 8 * lane, bar);
+                    copy_rows(dst + rows_at + xbox + lane * 1024, &xmap, ks * 256 + 128, t.r0 + at + 8 * lane, bar);
+                }
+            }
+        }
+        if (lane == 0)
+            sh.issued = n;
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ products (the first CTA's warp for both)
+        if (rank == 0) {
+            const bool lead = tc::elect();
+            bool ok = true;
+            uint32_t n = 0, tile = 0;
+            for (int item = pair; item < items && ok; item += pairs, ++tile) {
+                t.find(sh, p, item);
+                const uint32_t buf = tile & 1, d = tmem + buf * 256, idesc = tc::product_desc(256, 2 * t.half(), BYTES);
+                if (tile >= 2)
+                    ok = wait(&sh.tempty[buf], (tile >> 1) - 1, 35, t.e);
+                for (int ks = 0; ks < steps; ++ks, ++n) {
+                    const uint32_t slot = n % stages;
+                    ok = ok && wait(&sh.full[slot], n / stages, 36, ks);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok)
+                        break;
+                    if (lead) {
+                        tc::fence_after();
+                        const uint64_t a = tc::operand(ring + slot * stage), b = tc::operand(ring + slot * stage + rows_at);
+                        const int left = p.K - ks * kStageK;
+                        if constexpr (BYTES) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (j * 32 < left) {
+                                    const uint64_t aj = a + j * 2, bj = b + (j >> 1) * (xbox >> 4) + (j & 1) * 4;
+                                    const bool add = (ks | j) != 0;
+                                    tc::product<2, true>(d, aj, bj, idesc, add);
+                                    tc::product<2, true>(d, aj, bj + 2, idesc, true);
+                                    if constexpr (MODE == kGated) {
+                                        tc::product<2, true>(d + 128, aj + (kBox >> 4), bj, idesc, add);
+                                        tc::product<2, true>(d + 128, aj + (kBox >> 4), bj + 2, idesc, true);
+                                    }
+                                }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (j * 16 < left)
+                                    tc::product<2, false>(d, a + (j >> 2) * (kBox >> 4) + (j & 3) * 2,
+                                                          b + (j >> 2) * (xbox >> 4) + (j & 3) * 2, idesc, (ks | j) != 0);
+                        }
+                        tc::commit_both(&sh.empty[slot]);
+                        if (ks == steps - 1)
+                            tc::commit_both(&sh.tfull[buf]);
+                    }
+                    __syncwarp();
+                }
+            }
+            // every issued product completes before the tensor memory is released
+            if (lead) {
+                tc::commit<2>(&sh.drained);
+                tc::bar_drain(tc::saddr(&sh.drained), 0);
+            }
+            __syncwarp();
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ epilogue: a lane is an output feature, a column a row of x
+        const int quarter = warp & 3, side = (warp - 4) >> 2;
+        bool alive = true;
+        uint32_t tile = 0;
+        for (int item = pair; item < items; item += pairs, ++tile) {
+            t.find(sh, p, item);
+            const uint32_t buf = tile & 1;
+            const int half = t.half(), c0 = side * half, nw = t.n0 + rank * 128 + quarter * 32, n = nw + lane;
+            // what the columns and lanes are multiplied by, on its way while the products end
+            float xs[4], s0 = 1.0f, s1 = 1.0f;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int c = c0 + g * 32 + lane;
+                xs[g] = 1.0f;
+                if (MODE != kDown && g * 32 < half && g * 32 + lane < half && c < t.live) {
+                    int row = t.r0 + c;
+                    bool there = true;
+                    if (p.src) {
+                        row = __ldcg(p.src + row);
+                        there = row >= 0 && row / p.per < p.x_rows;
+                        row = there ? row / p.per : 0;
+                    }
+                    // (negative: no such row of x, the output is zero)
+                    xs[g] = there ? (BYTES ? __ldcg(p.xs + row) : 1.0f) : -1.0f;
+                }
+            }
+            if (n < p.N && p.s0) {
+                s0 = __ldcg(p.s0 + static_cast<int64_t>(t.e) * p.N + n);
+                if (MODE == kGated)
+                    s1 = __ldcg(p.s1 + static_cast<int64_t>(t.e) * p.N + n);
+            }
+            if (MODE == kDown)
+                s0 *= 0x1p-12f / __ldcg(p.smax + t.e);
+            if (alive)
+                alive = wait(&sh.tfull[buf], tile >> 1, 37, t.e);
+            alive = __all_sync(0xFFFFFFFFu, alive);
+            tc::fence_after();
+            if (alive && nw < p.N) {
+                const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * 256 + c0;
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    for (int j = 0; j < 32 && g * 32 + j < half && c0 + g * 32 + j < t.live; j += 8) {
+                        uint32_t u[8], v[8];
+                        tc::read8(from + g * 32 + j, u);
+                        if (MODE == kGated)
+                            tc::read8(from + 128 + g * 32 + j, v);
+                        tc::read_wait();
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            asm volatile("" : "+r"(u[q]));
+                            if (MODE == kGated)
+                                asm volatile("" : "+r"(v[q]));
+                        }
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const int c = c0 + g * 32 + j + q;
+                            const float x = MODE == kDown ? 1.0f : __shfl_sync(0xFFFFFFFFu, xs[g], j + q);
+                            if (c >= t.live)
+                                break;
+                            const int64_t row = t.r0 + c;
+                            const float d = __uint_as_float(u[q]);
+                            if (MODE == kGated) {
+                                const float a = x < 0.0f ? 0.0f : gelu_tanh(d * s0 * x) * (__uint_as_float(v[q]) * s1 * x);
+                                // |a| < 2^(e - 126) for all 32: below 2^15 in f16, which has 11 bits down to 2^-14
+                                const uint32_t bits = n < p.N ? __float_as_uint(a) & 0x7FFFFFFFu : 0;
+                                int e = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, bits) >> 23);
+                                e = e < 14 ? 14 : e;
+                                const __half h = __float2half_rn(a * __uint_as_float(static_cast<uint32_t>(268 - e) << 23));
+                                if (n < p.N)
+                                    p.out[row * p.N + n] = __half_as_ushort(h);
+                                if (lane == 0)
+                                    p.exps[row * (p.N >> 5) + (nw >> 5)] = static_cast<uint8_t>(e);
+                            } else if (n < p.N) {
+                                p.out[row * p.N + n] = MODE == kDown ? __half_as_ushort(__float2half_rn(d * s0))
+                                                                     : f32_to_bf16(x < 0.0f ? 0.0f : d * s0 * x);
+                            }
+                        }
+                    }
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0)
+                asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(tc::in_first(tc::saddr(&sh.tempty[buf])))
+                             : "memory");
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    // neither CTA leaves while the other's products or arrivals may reach it,
+    tc::cluster_sync();
+    // nor before every copy that either issued has landed (the first sees both CTAs' bytes)
+    if (rank == 0 && tid == 0) {
+        const uint32_t here = sh.issued;
+        const score::PairEnd e = score::pair_end(here, tc::of_second(tc::saddr(&sh.issued)), stages);
+        for (uint32_t i = e.only_from; i < e.to; ++i) {
+            const uint32_t slot = i % stages, bar = tc::saddr(&sh.full[slot]);
+            if (i < here)
+                asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(sh.others[slot]) : "memory");
+            else
+                tc::bar_expect(bar, tc::of_second(tc::saddr(&sh.bytes[slot])));
+        }
+        for (uint32_t i = e.first; i < e.to; ++i)
+            tc::bar_drain(tc::saddr(&sh.full[i % stages]), (i / stages) & 1);
+    }
+    __syncthreads();
+    tc::cluster_sync();
+    if (warp == 1) {
+        tc::fence_after();
+        tc::memory_free<2>(tmem);
+    }
+}
+
+}  // namespace grouped
+}  // namespace fgm

@@ -1,0 +1,146 @@
+// C ABI of the block norms (declared in include/fgm.h): argument checks and launches
+// of block_norm.cuh.
+#include <cmath>
+
+#include "block_norm.cuh"
+#include "host.h"
+
+namespace fgm {
+namespace {
+
+int64_t elem_bytes(int type) { return type == FGM_F32 ? 4 : 2; }
+bool type_ok(int type) { return type == FGM_F32 || type == FGM_BF16 || type == FGM_F16; }
+
+// The bytes of a tensor's rows: `rows` of them, `width` bytes each, `stride` bytes apart.
+struct Span {
+    uintptr_t at;
+    int64_t rows, stride, width;
+};
+
+Span span(const void *p, int64_t rows, int64_t stride, int64_t cols, int type)
+{
+    return Span{reinterpret_cast<uintptr_t>(p), rows, stride * elem_bytes(type), cols * elem_bytes(type)};
+}
+
+bool same(const Span &a, const Span &b) { return a.at == b.at && a.width == b.width && (a.rows == 1 || a.stride == b.stride); }
+
+// Whether two tensors share no byte: apart, or interleaved rows at one stride.
+bool apart(const Span &a, const Span &b)
+{
+    const uintptr_t a1 = a.at + (a.rows - 1) * a.stride + a.width, b1 = b.at + (b.rows - 1) * b.stride + b.width;
+    if (a1 <= b.at || b1 <= a.at)
+        return true;
+    if (a.stride != b.stride || a.stride <= 0)
+        return false;
+    const int64_t s = a.stride, d = a.at <= b.at ? static_cast<int64_t>((b.at - a.at) % s)
+                                                 : static_cast<int64_t>((s - (a.at - b.at) % s) % s);
+    return d >= a.width && d + b.width <= s;
+}
+
+int check_tensor(const char *name, const void *p, int type, int64_t stride, int D)
+{
+    if (!type_ok(type))
+        return failf(FGM_ERR_INVALID_ARG, "%s: type %d is not FGM_F32, FGM_BF16 or FGM_F16", name, type);
+    if (!p || !is_aligned(p, elem_bytes(type)))
+        return failf(FGM_ERR_INVALID_ARG, "%s NULL or not aligned to an element", name);
+    if (stride < D || stride > (int64_t(1) << 32))
+        return failf(FGM_ERR_INVALID_ARG, "%s: stride %lld below D = %d or above 2^32", name, (long long)stride, D);
+    return FGM_OK;
+}
+
+bool wide(const void *p, int64_t stride, int type) { return !p || (is_aligned(p, 16) && stride * elem_bytes(type) % 16 == 0); }
+
+template <int TPR, int VPT, int VEC>
+int launch_norm(const norm::Args &a, cudaStream_t st)
+{
+    constexpr int kThreads = TPR < norm::kMinThreads ? norm::kMinThreads : TPR, kRows = kThreads / TPR;
+    return launch_overlapped(norm::k_block_norm<TPR, VPT, VEC>, dim3(static_cast<unsigned>((a.N + kRows - 1) / kRows)), kThreads, 0, st, a);
+}
+
+}  // namespace
+}  // namespace fgm
+
+using namespace fgm;
+
+extern "C" int fgm_block_norm(const fgm_block *b, void *stream)
+{
+    if (!b)
+        return failf(FGM_ERR_INVALID_ARG, "block is NULL");
+    if (b->N < 1 || b->N > 0x7FFFFFFFLL)
+        return failf(FGM_ERR_INVALID_ARG, "N = %lld outside [1, 2^31)", (long long)b->N);
+    if (b->D < 1 || b->D > 16384)
+        return failf(FGM_ERR_INVALID_ARG, "D = %d outside [1, 16384]", b->D);
+    if (!std::isfinite(b->residual_scale) || !std::isfinite(b->block_scale) || !std::isfinite(b->gain_offset) || !std::isfinite(b->eps) || b->eps < 0)
+        return failf(FGM_ERR_INVALID_ARG, "scales and gain_offset must be finite, eps finite and not negative");
+    if (!b->h_out && !b->xn)
+        return failf(FGM_ERR_INVALID_ARG, "h_out and xn both NULL: no output");
+    FGM_HOST_TRY(check_tensor("h", b->h, b->h_type, b->h_stride, b->D));
+    if (b->y)
+        FGM_HOST_TRY(check_tensor("y", b->y, b->y_type, b->y_stride, b->D));
+    if (!b->y && (b->gate || b->post_gain))
+        return failf(FGM_ERR_INVALID_ARG, "gate or post_gain without y");
+    if (b->post_gain && !b->post_norm)
+        return failf(FGM_ERR_INVALID_ARG, "post_gain without post_norm");
+    if (b->pre_gain && !b->xn)
+        return failf(FGM_ERR_INVALID_ARG, "pre_gain without xn");
+    if (b->h_out)
+        FGM_HOST_TRY(check_tensor("h_out", b->h_out, b->h_type, b->h_out_stride, b->D));
+    if (b->xn)
+        FGM_HOST_TRY(check_tensor("xn", b->xn, b->xn_type, b->xn_stride, b->D));
+    const int64_t gate_cols = b->gate_col_stride ? b->D : 1;
+    if (b->gate) {
+        if (!type_ok(b->gate_type) || !is_aligned(b->gate, elem_bytes(b->gate_type)))
+            return failf(FGM_ERR_INVALID_ARG, "gate: type %d, or not aligned to an element", b->gate_type);
+        if (b->gate_col_stride != 0 && b->gate_col_stride != 1)
+            return failf(FGM_ERR_INVALID_ARG, "gate_col_stride = %d: 0 or 1", b->gate_col_stride);
+        if (b->gate_row_stride != 0 && (b->gate_row_stride < gate_cols || b->gate_row_stride > (int64_t(1) << 32)))
+            return failf(FGM_ERR_INVALID_ARG, "gate_row_stride = %lld: 0, or at least %lld and at most 2^32", (long long)b->gate_row_stride, (long long)gate_cols);
+    }
+    const void *gains[2] = {b->post_gain, b->pre_gain};
+    for (const void *g : gains)
+        if (g && (!type_ok(b->gain_type) || !is_aligned(g, elem_bytes(b->gain_type))))
+            return failf(FGM_ERR_INVALID_ARG, "gains: type %d, or not aligned to an element", b->gain_type);
+    // outputs: no byte of theirs is another tensor's, but for rows taken over whole
+    const Span h = span(b->h, b->N, b->h_stride, b->D, b->h_type), y = span(b->y, b->N, b->y_stride, b->D, b->y_type),
+               ho = span(b->h_out, b->N, b->h_out_stride, b->D, b->h_type), xn = span(b->xn, b->N, b->xn_stride, b->D, b->xn_type),
+               gate = span(b->gate, b->gate_row_stride ? b->N : 1, b->gate_row_stride, gate_cols, b->gate_type);
+    bool clash = false;
+    if (b->h_out)
+        clash |= !(same(ho, h) || apart(ho, h)) || (b->y && !apart(ho, y)) || (b->gate && !apart(ho, gate)) || (b->xn && !apart(ho, xn));
+    if (b->xn)
+        clash |= !(same(xn, h) || apart(xn, h)) || (b->y && !(same(xn, y) || apart(xn, y))) || (b->gate && !apart(xn, gate));
+    for (const void *g : gains)
+        if (g) {
+            const Span s = span(g, 1, 0, b->D, b->gain_type);
+            clash |= (b->h_out && !apart(ho, s)) || (b->xn && !apart(xn, s));
+        }
+    if (clash)
+        return failf(FGM_ERR_INVALID_ARG, "an output overlaps another tensor (h_out may be h; xn may be y or h)");
+    FGM_HOST_TRY(host_device_ready(nullptr));
+
+    norm::Args a = {};
+    a.h = {const_cast<void *>(b->h), b->h_stride, b->h_type, 1};
+    a.y = {const_cast<void *>(b->y), b->y_stride, b->y_type, 1};
+    a.gate = {const_cast<void *>(b->gate), b->gate_row_stride, b->gate_type, b->gate_col_stride};
+    a.h_out = {b->h_out, b->h_out_stride, b->h_type, 1};
+    a.xn = {b->xn, b->xn_stride, b->xn_type, 1};
+    a.post = b->post_gain;
+    a.pre = b->pre_gain;
+    a.gain_type = b->gain_type;
+    a.N = b->N;
+    a.D = b->D;
+    a.post_norm = b->post_norm;
+    a.a = b->residual_scale;
+    a.b = b->block_scale;
+    a.offset = b->gain_offset;
+    a.eps = b->eps;
+    const bool vec = b->D % 8 == 0 && wide(b->h, b->h_stride, b->h_type) && wide(b->y, b->y_stride, b->y_type) &&
+                     (!b->gate_col_stride || wide(b->gate, b->gate_row_stride, b->gate_type)) && wide(b->h_out, b->h_out_stride, b->h_type) &&
+                     wide(b->xn, b->xn_stride, b->xn_type) && wide(b->post_gain, 0, b->gain_type) && wide(b->pre_gain, 0, b->gain_type);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (vec)
+        return b->D <= 4096 ? launch_norm<128, 4, 8>(a, st) : launch_norm<512, 4, 8>(a, st);
+    if (b->D <= 1024)
+        return launch_norm<128, 8, 1>(a, st);
+    return b->D <= 4096 ? launch_norm<512, 8, 1>(a, st) : launch_norm<512, 32, 1>(a, st);
+}

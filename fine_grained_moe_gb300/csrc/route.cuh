@@ -1,0 +1,423 @@
+// Routing of any number of tokens (fgm_moe_route): logits l = W x + b of 128 experts,
+// the 8 largest (ties to the lower index) and their softmax.
+//
+// 2 * 128 * 2816 operations and 5.6 KB a token: bound by HBM at long prompts, by
+// latency at a few tokens, so K is split over CTAs while there are fewer tiles of
+// 128 tokens than SMs. k_router_logits runs M = 128 tokens x N = 128 experts on
+// tcgen05 and takes the accumulator out every 256 elements of K, to add it in fp32
+// registers: the tensor pipe truncates each addition, and 16 of them at a time stay
+// within 2^-18 |x| |w| in all.
+//
+// Precision. Which experts a token takes is a whole number that hangs on logits that
+// may lie next to each other, so it goes by the exact ones. k_route_top knows a bound
+// d on the error of its logits (from |x| and the largest |w|, which the products'
+// helper warps sum up from the tiles in shared memory). Chosen experts further than
+// 2 d from every other candidate are in order; the others' logits are summed again
+// without rounding error to speak of (each addition's error is kept, 2^-40 of the sum
+// remains), and the 8 chosen by these. About one token in ten has such a pair.
+#pragma once
+
+#include "tensor.cuh"
+
+namespace fgm {
+namespace route {
+
+constexpr int kThreads = 384;                    // copies, products, two for norms, eight epilogue warps
+constexpr int kStages = 6;
+constexpr int kBox = 128 * 128;                  // 128 rows x 64 elements
+constexpr int kChunkBoxes = 4;                   // 256 elements of K between readings of the accumulator
+constexpr int kChunks = kH / 256;
+constexpr int kSmem = kStages * 2 * kBox + 1024;
+static_assert(kH % 256 == 0 && kE == 128 && kK == 8, "the tiles are cut for these");
+
+struct LogitArgs {
+    int64_t T;
+    int splits;              // of K
+    float *part;             // [splits][T][128]
+    float *xn2;              // [splits][T] sums of squares
+    float *wn2;              // [splits][128]
+    int32_t *status;
+    long long timeout_ns;
+};
+
+struct Shared {
+    unsigned long long full[kStages], empty[kStages], tfull[2], tempty[2], drained;
+    uint32_t tmem;
+    int abort;
+    uint32_t issued;
+};
+
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int k, int row, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(k), "r"(row), "r"(bar)
+        : "memory");
+}
+
+// Sum of squares of a row of 64 bf16 at `at`, whatever their order.
+__device__ __forceinline__ float squares(uint32_t at, int first, float s)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(at + ((first + i) & 7) * 16)
+                     : "memory");
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float2 f = bf16x2_to_f32(w[q]);
+            s = fmaf(f.x, f.x, s);
+            s = fmaf(f.y, f.y, s);
+        }
+    }
+    return s;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    k_router_logits_tc(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap, const LogitArgs p)
+{
+    extern __shared__ uint8_t dsm_raw[];
+    __shared__ Shared sh;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t ring = (tc::saddr(dsm_raw) + 1023u) & ~1023u;
+    const int64_t tile = blockIdx.x;
+    const int split = blockIdx.y, b0 = kChunks * split / p.splits * kChunkBoxes, b1 = kChunks * (split + 1) / p.splits * kChunkBoxes;
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            tc::bar_init(&sh.full[i], 1);
+            tc::bar_init(&sh.empty[i], 3);       // the products and both norm warps
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::bar_init(&sh.tfull[i], 1);
+            tc::bar_init(&sh.tempty[i], 8);
+        }
+        tc::bar_init(&sh.drained, 1);
+        sh.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    tc::after_previous();
+    if (warp == 1)
+        tc::memory_take<1>(&sh.tmem);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    tc::let_next_start();
+    const uint32_t tmem = sh.tmem;
+    const tc::Waiter wait{&sh.abort, p.status, p.timeout_ns};
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t n = 0;
+            for (int b = b0; b < b1; ++b, ++n) {
+                const uint32_t slot = n % kStages, bar = tc::saddr(&sh.full[slot]), dst = ring + slot * 2 * kBox;
+                if (n >= kStages && !wait(&sh.empty[slot], n / kStages - 1, 38, b))
+                    break;
+                tc::bar_expect(bar, 2 * kBox);
+                copy_box(dst, &xmap, b * 64, static_cast<int>(tile * 128), bar);
+                copy_box(dst + kBox, &wmap, b * 64, 0, bar);
+            }
+            sh.issued = n;
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        const bool lead = tc::elect();
+        bool ok = true;
+        uint32_t n = 0;
+        for (int b = b0; b < b1 && ok; ++b, ++n) {
+            const uint32_t slot = n % kStages, chunk = n / kChunkBoxes, buf = chunk & 1;
+            if (chunk >= 2 && n % kChunkBoxes == 0)
+                ok = wait(&sh.tempty[buf], (chunk >> 1) - 1, 39, b);
+            ok = ok && wait(&sh.full[slot], n / kStages, 40, b);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (ok && lead) {
+                tc::fence_after();
+                const uint64_t x = tc::operand(ring + slot * 2 * kBox), w = tc::operand(ring + slot * 2 * kBox + kBox);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    tc::product<1, false>(tmem + buf * 128, x + j * 2, w + j * 2, tc::product_desc(128, 128, false),
+                                          n % kChunkBoxes != 0 || j != 0);
+                tc::commit<1>(&sh.empty[slot]);
+                if (n % kChunkBoxes == kChunkBoxes - 1)
+                    tc::commit<1>(&sh.tfull[buf]);
+            }
+            __syncwarp();
+        }
+        if (lead) {
+            tc::commit<1>(&sh.drained);
+            tc::bar_drain(tc::saddr(&sh.drained), 0);
+        }
+        __syncwarp();
+    } else if (warp < 4) {
+        // norms of the tile's tokens, and of the experts' rows once
+        const int r = (warp - 2) * 32 + lane;
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        bool ok = true;
+        uint32_t n = 0;
+        for (int b = b0; b < b1 && ok; ++b, ++n) {
+            const uint32_t slot = n % kStages, at = ring + slot * 2 * kBox + r * 128;
+            ok = wait(&sh.full[slot], n / kStages, 41, b);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok)
+                break;
+            s[0] = squares(at, r, s[0]);
+            s[1] = squares(at + 64 * 128, r, s[1]);
+            if (tile == 0) {
+                s[2] = squares(at + kBox, r, s[2]);
+                s[3] = squares(at + kBox + 64 * 128, r, s[3]);
+            }
+            __syncwarp();
+            if (lane == 0)
+                tc::bar_arrive(tc::saddr(&sh.empty[slot]));
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (tile * 128 + r + h * 64 < p.T)
+                p.xn2[split * p.T + tile * 128 + r + h * 64] = s[h];
+            if (tile == 0)
+                p.wn2[split * kE + r + h * 64] = s[2 + h];
+        }
+    } else {
+        const int quarter = warp & 3, side = (warp - 4) >> 2;
+        float acc[64];
+#pragma unroll
+        for (int j = 0; j < 64; ++j)
+            acc[j] = 0.0f;
+        bool ok = true;
+        for (int chunk = 0; chunk < (b1 - b0) / kChunkBoxes; ++chunk) {
+            const uint32_t buf = chunk & 1;
+            if (ok)
+                ok = wait(&sh.tfull[buf], chunk >> 1, 42, chunk);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            tc::fence_after();
+            if (ok)
+#pragma unroll
+                for (int j = 0; j < 64; j += 8) {
+                    uint32_t u[8];
+                    tc::read8(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * 128 + side * 64 + j, u);
+                    tc::read_wait();
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        asm volatile("" : "+r"(u[q]));
+                        acc[j + q] += __uint_as_float(u[q]);
+                    }
+                }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0)
+                tc::bar_arrive(tc::saddr(&sh.tempty[buf]));
+        }
+        const int64_t t = tile * 128 + quarter * 32 + lane;
+        if (t < p.T) {
+            float4 *to = reinterpret_cast<float4 *>(p.part + (split * p.T + t) * kE + side * 64);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                to[j] = make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    if (tid == 0) {                              // every issued copy lands before the CTA ends
+        const uint32_t n = sh.issued;
+        for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)
+            tc::bar_drain(tc::saddr(&sh.full[i % kStages]), (i / kStages) & 1);
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc::fence_after();
+        tc::memory_free<1>(tmem);
+    }
+}
+
+struct TopArgs {
+    const float *part, *xn2, *wn2;
+    const float *b;          // [128] or NULL
+    const uint16_t *x;
+    int64_t stride;
+    const uint16_t *w;       // [128][2816]
+    int64_t T;
+    int splits;
+    int32_t *ids;            // [T][8]
+    float *wts;              // [T][8]
+    int32_t *status;
+};
+
+constexpr int kTopWarps = 8;
+
+// x . w_e by one warp, each addition's rounding error added up beside the sum.
+__device__ __forceinline__ double exact_dot(const uint16_t *x, const uint16_t *w, int lane)
+{
+    float s = 0.0f, c = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kH / 256; ++i) {
+        const uint4 a = __ldcg(reinterpret_cast<const uint4 *>(x) + i * 32 + lane), b = __ldcg(reinterpret_cast<const uint4 *>(w) + i * 32 + lane);
+        const uint32_t as[4] = {a.x, a.y, a.z, a.w}, bs[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float2 u = bf16x2_to_f32(as[q]), v = bf16x2_to_f32(bs[q]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float prod = __fmul_rn(h ? u.y : u.x, h ? v.y : v.x);    // (16 bits: exact)
+                const float t = __fadd_rn(s, prod), z = __fsub_rn(t, s);
+                c = __fadd_rn(c, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(prod, z)));
+                s = t;
+            }
+        }
+    }
+    double d = static_cast<double>(s) + static_cast<double>(c);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
+    return d;
+}
+
+// A warp per token; lane l has experts l, l + 32, l + 64, l + 96.
+__global__ void __launch_bounds__(32 * kTopWarps) k_route_top(const TopArgs p)
+{
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kTopWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    tc::after_previous();
+    tc::let_next_start();
+    if (t >= p.T)
+        return;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, b[4], x2 = 0.0f, w2 = 0.0f;
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s) {
+        x2 += __ldcg(p.xn2 + s * p.T + t);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            v[q] += __ldcg(p.part + (s * p.T + t) * kE + lane + 32 * q);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        float n2 = 0.0f;
+        for (int s = 0; s < p.splits; ++s)
+            n2 += __ldcg(p.wn2 + s * kE + lane + 32 * q);
+        w2 = fmaxf(w2, n2);
+        b[q] = p.b ? __ldcg(p.b + lane + 32 * q) : 0.0f;
+    }
+    bool bad = false;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        v[q] += b[q];
+        if (isnan(v[q])) {
+            v[q] = -INFINITY;
+            bad = true;
+        }
+    }
+    if (__any_sync(0xFFFFFFFFu, bad) && lane == 0)
+        atomicOr(p.status, FGM_STATUS_NONFINITE_LOGITS);
+    w2 = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(w2)));
+
+    double z[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        z[q] = static_cast<double>(v[q]);
+    int top_i[kK];
+    float top_v[kK];
+    auto choose = [&]() {
+        unsigned taken = 0;
+#pragma unroll
+        for (int r = 0; r < kK; ++r) {
+            float bv = -INFINITY;
+            int bi = 0x7FFFFFFF;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (!(taken & (1u << q)) && better(v[q], lane + 32 * q, bv, bi)) {
+                    bv = v[q];
+                    bi = lane + 32 * q;
+                }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                const float ov = __shfl_xor_sync(0xFFFFFFFFu, bv, o);
+                const int oi = __shfl_xor_sync(0xFFFFFFFFu, bi, o);
+                if (better(ov, oi, bv, bi)) {
+                    bv = ov;
+                    bi = oi;
+                }
+            }
+            if ((bi & 31) == lane)
+                taken |= 1u << (bi >> 5);
+            top_v[r] = bv;
+            top_i[r] = bi;
+        }
+    };
+    choose();
+    // twice the bound of a candidate's error: 2^-17 |x| |w| of its products, 2^-23 of the sum with the bias
+    // (without an x the logits are the biases; experts masked by a bias of -inf have no near one)
+    float most = 0.0f;
+#pragma unroll
+    for (int r = 0; r < kK; ++r)
+        most = fabsf(top_v[r]) < INFINITY ? fmaxf(most, fabsf(top_v[r])) : most;
+    const float gap = x2 > 0.0f ? 2.0f * (0x1p-17f * sqrtf(x2) * sqrtf(w2) + 0x1p-23f * most) : 0.0f;
+    if (gap > 0.0f && gap < INFINITY) {
+        // candidates with another candidate within the gap
+        unsigned cand = 0, near = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            cand |= v[q] >= top_v[kK - 1] - gap ? 1u << q : 0u;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            for (unsigned m = __ballot_sync(0xFFFFFFFFu, cand >> q & 1); m; m &= m - 1) {
+                const int who = __ffs(m) - 1;
+                const float other = __shfl_sync(0xFFFFFFFFu, v[q], who);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if ((cand >> j & 1) && !(who == lane && q == j) && fabsf(v[j] - other) <= gap)
+                        near |= 1u << j;
+            }
+        if (__any_sync(0xFFFFFFFFu, near != 0)) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                for (unsigned m = __ballot_sync(0xFFFFFFFFu, near >> q & 1); m; m &= m - 1) {
+                    const int who = __ffs(m) - 1;
+                    const double d = exact_dot(p.x + t * p.stride, p.w + static_cast<int64_t>(who + 32 * q) * kH, lane);
+                    if (lane == who)
+                        z[q] = d + static_cast<double>(b[q]);
+                }
+            // the same choice by these
+            unsigned taken = 0;
+#pragma unroll
+            for (int r = 0; r < kK; ++r) {
+                double bv = -INFINITY;
+                int bi = 0x7FFFFFFF;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (!(taken & (1u << q)) && (z[q] > bv || (z[q] == bv && lane + 32 * q < bi))) {
+                        bv = z[q];
+                        bi = lane + 32 * q;
+                    }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    const double ov = __shfl_xor_sync(0xFFFFFFFFu, bv, o);
+                    const int oi = __shfl_xor_sync(0xFFFFFFFFu, bi, o);
+                    if (ov > bv || (ov == bv && oi < bi)) {
+                        bv = ov;
+                        bi = oi;
+                    }
+                }
+                if ((bi & 31) == lane)
+                    taken |= 1u << (bi >> 5);
+                top_v[r] = static_cast<float>(bv);
+                top_i[r] = bi;
+            }
+        }
+    }
+    float ex[kK], sum = 0.0f;
+#pragma unroll
+    for (int r = 0; r < kK; ++r) {
+        ex[r] = top_v[0] == -INFINITY ? 1.0f : expf(top_v[r] - top_v[0]);
+        sum += ex[r];
+    }
+#pragma unroll
+    for (int r = 0; r < kK; ++r)
+        if (lane == r) {
+            p.ids[t * kK + r] = top_i[r];
+            p.wts[t * kK + r] = ex[r] / sum;
+        }
+}
+
+}  // namespace route
+}  // namespace fgm

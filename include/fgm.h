@@ -470,6 +470,114 @@ int fgm_lm_head_logprobs(const uint16_t *emb, int64_t V, const uint16_t *h, int6
                          int k, float *logp, float *entropy, int32_t *top_ids, float *top_logp, void *ws,
                          size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------- a prompt through the experts
+ *
+ * The layer's experts on any number of tokens ("llm-decoding", §"The exact
+ * architecture": top 8 of 128 and one shared): a prompt, or a batch of requests with
+ * a token each. A slot is a (token, choice) pair, numbered 8 * token + choice.
+ * Every call gives the same bits again. */
+
+/* Also an element type, of fgm_grouped_gemm's weights: codes with a scale per row. */
+enum { FGM_E4M3 = 3 };
+
+#define FGM_MAX_TOKENS (1 << 18)  /* tokens of fgm_moe_route and fgm_moe_experts_fwd */
+#define FGM_MAX_GROUPS 1024       /* experts of fgm_moe_group and fgm_grouped_gemm */
+
+/* Bytes of workspace of fgm_moe_route, fgm_moe_group, fgm_grouped_gemm and
+ * fgm_moe_experts_fwd (0 for sizes out of range). Such a workspace serves every other
+ * entry point too, and fgm_workspace_init prepares it. */
+size_t fgm_moe_route_workspace_bytes(int64_t T);
+size_t fgm_moe_group_workspace_bytes(int64_t n, int E);
+size_t fgm_grouped_gemm_workspace_bytes(int64_t x_rows, int64_t R, int E, int N, int K);
+size_t fgm_moe_experts_workspace_bytes(int64_t T);
+
+/* Routing of T tokens: l = router_w x + router_b, the 8 experts with the largest
+ * logits (descending; ties to the lower index) and w = softmax over these 8, which is
+ * the renormalised softmax over all. Chosen by the exact logits: where fp32 could
+ * misplace two, they are summed again to 2^-40. A NaN logit counts as -inf
+ * (FGM_STATUS_NONFINITE_LOGITS); a bias of -inf masks an expert.
+ *  router_w  bf16 [128][2816], router_b fp32 [128] or NULL
+ *  x         bf16 [T] rows of 2816, x_stride elements apart (a multiple of 8, at least
+ *            2816), 16-byte aligned; 1 <= T <= FGM_MAX_TOKENS
+ *  ids       int32 [T][8] output;  w  fp32 [T][8] output
+ *  offsets   int32 [129] and order int32 [8 T] outputs or both NULL: as fgm_moe_group's
+ *            on ids */
+int fgm_moe_route(const uint16_t *router_w, const float *router_b, const uint16_t *x, int64_t x_stride, int64_t T, int32_t *ids,
+                  float *w, int32_t *offsets, int32_t *order, void *ws, size_t ws_bytes, void *stream);
+
+/* Groups n slots by expert: expert e's are order[offsets[e]] .. order[offsets[e + 1] - 1],
+ * in ascending order. Slots whose id is outside [0, E) belong to none; the places
+ * behind offsets[E] are left as they are.
+ *  ids      int32 [n], 1 <= n <= 8 * FGM_MAX_TOKENS;  1 <= E <= FGM_MAX_GROUPS
+ *  offsets  int32 [E + 1] output;  order  int32 [n] output */
+int fgm_moe_group(const int32_t *ids, int64_t n, int E, int32_t *offsets, int32_t *order, void *ws, size_t ws_bytes, void *stream);
+
+/* Products grouped by expert: for the rows r of expert e, offsets[e] <= r < offsets[e + 1],
+ *   out[r][n] = w_s[e][n] * sum_k W_e[n][k] x[src(r)][k],
+ * src(r) = rows[r] / per, or r without `rows`. With E4M3 weights x enters exactly
+ * where an element is 2^-10 of its row's largest or more, the others to 2^-18 of that;
+ * fp32 accumulation on the tensor pipe, which truncates (each addition within 2^-22
+ * of a partial sum). An x row with an element that is not finite gives NaN (E4M3).
+ * Rows of no expert, and behind offsets[E], are left as they are; a row whose src(r)
+ * is outside x is zero. Offsets are taken within [0, R].
+ *  x        bf16 [x_rows] rows of K, x_stride elements apart (a multiple of 8, at least K),
+ *           16-byte aligned; 1 <= x_rows <= 2^24
+ *  rows     int32 [R] or NULL (then x_rows = R);  per >= 1
+ *  offsets  int32 [E + 1] (device), ascending
+ *  w        [E][N][K] of w_type FGM_E4M3 (K a multiple of 16) or FGM_BF16 (K a multiple of
+ *           8), 16-byte aligned;  1 <= N, K <= 65536
+ *  w_s      fp32 [E][N], or NULL: 1
+ *  out      bf16 [R][N] output, 1 <= R <= 2^24, apart from x */
+int fgm_grouped_gemm(const uint16_t *x, int64_t x_stride, int64_t x_rows, const int32_t *rows, int per, const int32_t *offsets,
+                     const void *w, int w_type, const float *w_s, int E, int N, int K, uint16_t *out, int64_t R, void *ws,
+                     size_t ws_bytes, void *stream);
+
+/* A layer's experts on T tokens whose experts are chosen (by fgm_moe_route, or otherwise):
+ *   y_t = sum_{i < 8} w[t][i] * expert_{ids[t][i]}(x_t) (+ expert_128(x_t) with `shared`),
+ * expert_e as in fgm_moe_layer_fwd. An id outside [0, 128) adds nothing (a place of a
+ * padded batch); an expert chosen twice counts twice. Activations enter the down
+ * products as two E4M3 terms (2^-9 of themselves), an expert's output is rounded to 11
+ * bits before the weighted sum, which is fp32.
+ *  layer  the experts' weights (router_w and router_b are not read)
+ *  x      bf16 [T] rows of 2816, x_stride elements apart (a multiple of 8, at least 2816),
+ *         16-byte aligned; 1 <= T <= FGM_MAX_TOKENS
+ *  ids    int32 [T][8];  w  fp32 [T][8]
+ *  y      bf16 [T][2816] output, 16-byte aligned, apart from x */
+int fgm_moe_experts_fwd(const fgm_layer *layer, const uint16_t *x, int64_t x_stride, int64_t T, const int32_t *ids, const float *w,
+                        int shared, uint16_t *y, void *ws, size_t ws_bytes, void *stream);
+
+/* The norms around a block, its gate, and the residual stream h, in one pass:
+ *   h' = residual_scale * h + block_scale * gate * post(y),   xn = pre(h'),
+ *   post(y) = y / sqrt(mean(y^2) + eps) * (post_gain + gain_offset), pre alike.
+ * post is left out with post_norm = 0, y with y = NULL, pre with xn = NULL. Sums are
+ * fp32 (squares must stay within its range), and xn goes by h' before it is rounded.
+ * Rows are N, of D elements, each tensor's `stride` elements apart (at least D);
+ * types FGM_F32, FGM_BF16, FGM_F16; tensors aligned to an element (all of them, and
+ * their rows, to 16 bytes, and D a multiple of 8, run four times as wide).
+ *  h         h_type [N][D]
+ *  y         y_type [N][D] or NULL
+ *  gate      gate_type or NULL: element d of row n is gate[n * gate_row_stride + d *
+ *            gate_col_stride]; gate_col_stride 0 (a value a row) or 1; gate_row_stride 0
+ *            (a value a channel) or at least D, or at least 1 with a value a row
+ *  post_gain, pre_gain  gain_type [D] or NULL (all ones; gain_offset is then unused)
+ *  h_out     h_type output [N][D] or NULL; may be h itself
+ *  xn        xn_type output [N][D] or NULL; may be y or h itself, if of the same element size and
+ *            stride (h: and no h_out there)
+ *  1 <= N < 2^31, 1 <= D <= 16384; scales, offset finite; eps >= 0 finite */
+typedef struct fgm_block {
+    int64_t N;
+    int D;
+    int h_type, y_type, gate_type, gain_type, xn_type;
+    const void *h, *y, *gate, *post_gain, *pre_gain;
+    void *h_out, *xn;
+    int64_t h_stride, y_stride, gate_row_stride, h_out_stride, xn_stride;
+    int gate_col_stride;
+    int post_norm;
+    float residual_scale, block_scale, gain_offset, eps;
+} fgm_block;
+
+int fgm_block_norm(const fgm_block *b, void *stream);
+
 /* Selects the execution path of subsequent calls in this process; returns the
  * previous one. An unknown value leaves the path unchanged. Both paths compute
  * the same step; they differ in kernel design only. */
