@@ -20,7 +20,9 @@
 namespace fgm {
 namespace grouped {
 
-constexpr int kThreads = 384;                    // copies, products, -, -, eight epilogue warps
+constexpr int kThreads = 384;                    // copies, products, -, -, eight epilogue warps,
+constexpr int kGatherThreads = 576;              // six more where rows are gathered: with the idle two, eight that copy rows
+constexpr int kGatherWarps = 8;
 constexpr int kMaxStages = 12;
 constexpr int kMaxExperts = 1024;
 constexpr int kStageK = 128;                     // elements of K in a stage
@@ -78,7 +80,7 @@ __device__ __forceinline__ void copy_weights(uint32_t dst, const CUtensorMap *ma
         : "memory");
 }
 
-// 8 rows x 128 bytes,
+// A box of rows x 128 bytes,
 __device__ __forceinline__ void copy_rows(uint32_t dst, const CUtensorMap *map, int at, int row, uint32_t bar)
 {
     asm volatile(
@@ -96,6 +98,27 @@ __device__ __forceinline__ void copy_gathered(uint32_t dst, const CUtensorMap *m
         "l"(reinterpret_cast<uint64_t>(map)), "r"(at), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(bar)
         : "memory");
 }
+
+// The tensor maps of a launch. x: boxes of 8, 16, .. 128 rows; for gathering the first, of one row.
+struct Maps {
+    CUtensorMap w, w2, x[5];
+};
+
+// Rows of the boxes that bring `half` (a multiple of 8, at most 128) rows or a few
+// more: the next power of two, or three quarters of it in two boxes. (A copy costs its
+// warp about 80 cycles to issue, whatever it brings.)
+struct RowBoxes {
+    int first, second;       // log2 of the rows / 8; second < 0: none
+
+    __device__ __forceinline__ explicit RowBoxes(int half)
+    {
+        const int up = 32 - __clz((half >> 3) - 1);
+        const bool three = up >= 2 && half * 4 <= (8 << up) * 3;
+        first = three ? up - 1 : up;
+        second = three ? up - 2 : -1;
+    }
+    __device__ __forceinline__ int rows() const { return (8 << first) + (second < 0 ? 0 : 8 << second); }
+};
 
 // A tile: rows [r0, r0 + live) of expert e against 256 of its output features (of
 // each product) from n0 on. A pair's items come in ascending order.
@@ -118,9 +141,7 @@ struct Tile {
 };
 
 template <Mode MODE, bool BYTES>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    k_grouped(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap wmap2, const __grid_constant__ CUtensorMap xmap,
-              const Args p)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k_grouped(const __grid_constant__ Maps maps, const Args p)
 {
     constexpr int kWBoxes = weight_boxes<MODE, BYTES>();
     extern __shared__ uint8_t dsm_raw[];
@@ -191,64 +212,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         // ------------------------------------------------------------ copies (each CTA its own weights and rows)
         if (lane == 0) {
-            tc::prefetch_map(&wmap);
-            tc::prefetch_map(&wmap2);
-            tc::prefetch_map(&xmap);
-        }
-        uint64_t once, again;
-        asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
-        asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(again));
-        bool ok = true;
-        uint32_t n = 0;
-        for (int item = pair; item < items && ok; item += pairs) {
-            t.find(sh, p, item);
-            const int half = t.half(), at = rank * half;
-            const uint32_t mine = kWBoxes * kBox + half * 256;
-            const uint64_t policy = sh.count[t.e] <= p.cols ? once : again;
-            int4 idx = make_int4(0, 0, 0, 0);
-            if (p.src && 4 * lane < half) {
-                // (places behind the tile's rows, and rows of x that are not there, take row 0: never stored)
-                int v[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int c = at + 4 * lane + j;
-                    const int s = c < t.live ? __ldcg(p.src + t.r0 + c) : 0;
-                    v[j] = s >= 0 && s / p.per < p.x_rows ? s / p.per : 0;
-                }
-                idx = make_int4(v[0], v[1], v[2], v[3]);
-            }
-            for (int ks = 0; ks < steps; ++ks, ++n) {
-                const uint32_t slot = n % stages;
-                if (n >= stages)
-                    ok = wait(&sh.empty[slot], n / stages - 1, 34, ks);
-                if (!(ok = __all_sync(0xFFFFFFFFu, ok)))
-                    break;
-                const uint32_t bar = tc::in_first(tc::saddr(&sh.full[slot])), dst = ring + slot * stage;
-                if (lane == 0) {
+            tc::prefetch_map(&maps.w);
+            tc::prefetch_map(&maps.w2);
+            uint64_t once, again;
+            asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+            asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(again));
+            bool ok = true;
+            uint32_t n = 0;
+            for (int item = pair; item < items && ok; item += pairs) {
+                t.find(sh, p, item);
+                const int half = t.half(), row = t.r0 + rank * half;
+                const RowBoxes box(half);
+                const uint32_t mine = kWBoxes * kBox + (p.src ? half : box.rows()) * 256;
+                const uint64_t policy = sh.count[t.e] <= p.cols ? once : again;
+                for (int ks = 0; ks < steps; ++ks, ++n) {
+                    const uint32_t slot = n % stages;
+                    if (n >= stages && !(ok = wait(&sh.empty[slot], n / stages - 1, 34, ks)))
+                        break;
+                    const uint32_t bar = tc::in_first(tc::saddr(&sh.full[slot])), dst = ring + slot * stage;
                     if (rank == 0)
                         tc::bar_expect(tc::saddr(&sh.full[slot]), 2 * mine);
                     sh.bytes[slot] = sh.others[slot] = mine;
                     const int w0 = t.n0 + rank * 128;
-                    copy_weights(dst, &wmap, ks * kStageK, w0, t.e, bar, policy);
+                    copy_weights(dst, &maps.w, ks * kStageK, w0, t.e, bar, policy);
                     if (MODE == kGated)
-                        copy_weights(dst + kBox, &wmap2, ks * kStageK, w0, t.e, bar, policy);
+                        copy_weights(dst + kBox, &maps.w2, ks * kStageK, w0, t.e, bar, policy);
                     else if (!BYTES)
-                        copy_weights(dst + kBox, &wmap, ks * kStageK + 64, w0, t.e, bar, policy);
-                }
-                __syncwarp();
-                if (p.src) {
-                    if (4 * lane < half) {
-                        copy_gathered(dst + rows_at + lane * 512, &xmap, ks * 256, idx, bar);
-                        copy_gathered(dst + rows_at + xbox + lane * 512, &xmap, ks * 256 + 128, idx, bar);
-                    }
-                } else if (8 * lane < half) {
-                    copy_rows(dst + rows_at + lane * 1024, &xmap, ks * 256, t.r0 + at + 8 * lane, bar);
-                    copy_rows(dst + rows_at + xbox + lane * 1024, &xmap, ks * 256 + 128, t.r0 + at + 8 * lane, bar);
+                        copy_weights(dst + kBox, &maps.w, ks * kStageK + 64, w0, t.e, bar, policy);
+                    if (!p.src)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            copy_rows(dst + rows_at + h * xbox, &maps.x[box.first], ks * 256 + h * 128, row, bar);
+                            if (box.second >= 0)
+                                copy_rows(dst + rows_at + h * xbox + (1024 << box.first), &maps.x[box.second], ks * 256 + h * 128,
+                                          row + (8 << box.first), bar);
+                        }
                 }
             }
-        }
-        if (lane == 0)
             sh.issued = n;
+        }
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ products (the first CTA's warp for both)
@@ -305,7 +307,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         }
-    } else if (warp >= 4) {
+    } else if (warp < 4 || warp >= 12) {
+        // ------------------------------------------------------------ gathered rows, four a copy: a lane's are four of one half of K
+        if (p.src) {
+            const int mate = warp < 4 ? warp - 2 : warp - 10, h = lane & 1, group = (lane >> 1) * kGatherWarps + mate;
+            bool ok = true;
+            uint32_t n = 0;
+            for (int item = pair; item < items && ok; item += pairs) {
+                t.find(sh, p, item);
+                const int half = t.half(), at = rank * half + 4 * group;
+                const bool mine = 4 * group < half;
+                int v[4] = {0, 0, 0, 0};
+                // (places behind the tile's rows, and rows of x that are not there, take row 0: never stored)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (mine && at + j < t.live) {
+                        const int s = __ldcg(p.src + t.r0 + at + j);
+                        v[j] = s >= 0 && s / p.per < p.x_rows ? s / p.per : 0;
+                    }
+                const int4 idx = make_int4(v[0], v[1], v[2], v[3]);
+                for (int ks = 0; ks < steps; ++ks, ++n) {
+                    const uint32_t slot = n % stages;
+                    if (n >= stages)
+                        ok = wait(&sh.empty[slot], n / stages - 1, 43, ks);
+                    if (!(ok = __all_sync(0xFFFFFFFFu, ok)))
+                        break;
+                    if (mine)
+                        copy_gathered(ring + slot * stage + rows_at + h * xbox + group * 512, &maps.x[0], ks * 256 + h * 128, idx,
+                                      tc::in_first(tc::saddr(&sh.full[slot])));
+                    __syncwarp();
+                }
+            }
+        }
+    } else {
         // ------------------------------------------------------------ epilogue: a lane is an output feature, a column a row of x
         const int quarter = warp & 3, side = (warp - 4) >> 2;
         bool alive = true;

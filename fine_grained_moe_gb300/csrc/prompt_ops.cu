@@ -94,12 +94,15 @@ int tile_cols(int64_t R, int E, int most)
     return c < most ? c : most;
 }
 
-// bf16 rows or terms as 128-byte boxes: single rows for gathering, else 8 at a time.
-int x_map(CUtensorMap *map, const void *x, int64_t row_bytes, int64_t stride_bytes, int64_t n, bool gathered)
+// bf16 rows or terms as 128-byte boxes: single rows for gathering, else 8 to 128 at a time.
+int x_maps(grouped::Maps &m, const void *x, int64_t row_bytes, int64_t stride_bytes, int64_t n, bool gathered)
 {
     const uint64_t dims[2] = {static_cast<uint64_t>(row_bytes), static_cast<uint64_t>(n)}, strides[1] = {static_cast<uint64_t>(stride_bytes)};
-    const uint32_t box[2] = {128, gathered ? 1u : 8u};
-    return host_map128(map, x, 1, 2, dims, strides, box);
+    for (int i = 0; i < (gathered ? 1 : 5); ++i) {
+        const uint32_t box[2] = {128, gathered ? 1u : 8u << i};
+        FGM_HOST_TRY(host_map128(&m.x[i], x, 1, 2, dims, strides, box));
+    }
+    return FGM_OK;
 }
 
 int weight_map(CUtensorMap *map, const void *w, int elem, int E, int N, int K)
@@ -111,7 +114,7 @@ int weight_map(CUtensorMap *map, const void *w, int elem, int E, int N, int K)
 }
 
 template <grouped::Mode MODE, bool BYTES>
-int launch_grouped(const CUtensorMap &w, const CUtensorMap &w2, const CUtensorMap &x, grouped::Args a, int sms, cudaStream_t st)
+int launch_grouped(const grouped::Maps &m, grouped::Args a, int sms, cudaStream_t st)
 {
     const auto kernel = grouped::k_grouped<MODE, BYTES>;
     constexpr int kSmem = grouped::kRing + 1024;
@@ -123,7 +126,7 @@ int launch_grouped(const CUtensorMap &w, const CUtensorMap &w2, const CUtensorMa
         FGM_HOST_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(sms / 2 * 2);
-        cfg.blockDim = dim3(grouped::kThreads);
+        cfg.blockDim = dim3(grouped::kGatherThreads);
         cfg.dynamicSmemBytes = kSmem;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -142,7 +145,7 @@ int launch_grouped(const CUtensorMap &w, const CUtensorMap &w2, const CUtensorMa
     // tiles: an expert has at most its rows / cols, rounded up, and no more experts than rows have any
     const int64_t across = (a.N + 255) / 256, tiles = (a.R / a.cols + (a.E < a.R ? a.E : a.R)) * across;
     const int64_t pairs = tiles < most ? tiles : most;
-    return launch_overlapped(kernel, dim3(static_cast<unsigned>(2 * pairs)), grouped::kThreads, kSmem, st, w, w2, x, a);
+    return launch_overlapped(kernel, dim3(static_cast<unsigned>(2 * pairs)), a.src ? grouped::kGatherThreads : grouped::kThreads, kSmem, st, m, a);
 }
 
 int launch_terms(const uint16_t *x, int64_t stride, int64_t n, int K, uint8_t *terms, float *scale, cudaStream_t st)
@@ -347,10 +350,11 @@ int fgm_grouped_gemm(const uint16_t *x, int64_t x_stride, int64_t x_rows, const 
     FGM_HOST_TRY(host_device_ready(&sms));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool bytes = w_type == FGM_E4M3;
-    CUtensorMap wmap, xmap;
-    FGM_HOST_TRY(weight_map(&wmap, w, bytes ? 1 : 2, E, N, K));
+    grouped::Maps m;
+    FGM_HOST_TRY(weight_map(&m.w, w, bytes ? 1 : 2, E, N, K));
+    m.w2 = m.w;
     const int64_t row = 2 * static_cast<int64_t>(bytes ? align_up(K, 32) : K);
-    FGM_HOST_TRY(x_map(&xmap, bytes ? region<void>(ws, o.terms) : static_cast<const void *>(x), row, bytes ? row : 2 * x_stride, x_rows, src != nullptr));
+    FGM_HOST_TRY(x_maps(m, bytes ? region<void>(ws, o.terms) : static_cast<const void *>(x), row, bytes ? row : 2 * x_stride, x_rows, src != nullptr));
     if (bytes)
         FGM_HOST_TRY(launch_terms(x, x_stride, x_rows, K, region<uint8_t>(ws, o.terms), region<float>(ws, o.xs), st));
     grouped::Args a = {};
@@ -368,8 +372,8 @@ int fgm_grouped_gemm(const uint16_t *x, int64_t x_stride, int64_t x_rows, const 
     a.cols = tile_cols(R, E, 256);
     a.status = status_word(ws);
     a.timeout_ns = host_wait_limit_ns();
-    return bytes ? launch_grouped<grouped::kGemm, true>(wmap, wmap, xmap, a, sms, st)
-                 : launch_grouped<grouped::kGemm, false>(wmap, wmap, xmap, a, sms, st);
+    return bytes ? launch_grouped<grouped::kGemm, true>(m, a, sms, st)
+                 : launch_grouped<grouped::kGemm, false>(m, a, sms, st);
 }
 
 size_t fgm_moe_experts_workspace_bytes(int64_t T) { return T < 1 || T > kMaxT ? 0 : experts_ws(T).total; }
@@ -399,12 +403,13 @@ int fgm_moe_experts_fwd(const fgm_layer *layer, const uint16_t *x, int64_t x_str
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int E = shared ? kNE : kE;
     const int64_t R = T * (shared ? kK + 1 : kK);
-    CUtensorMap gmap, umap, dmap, xmap, amap;
-    FGM_HOST_TRY(weight_map(&gmap, layer->gate_q, 1, kNE, kF, kH));
-    FGM_HOST_TRY(weight_map(&umap, layer->up_q, 1, kNE, kF, kH));
-    FGM_HOST_TRY(weight_map(&dmap, layer->down_q, 1, kNE, kH, kF));
-    FGM_HOST_TRY(x_map(&xmap, region<void>(ws, o.terms), 2 * kH, 2 * kH, T, true));
-    FGM_HOST_TRY(x_map(&amap, region<void>(ws, o.act_terms), 2 * kF, 2 * kF, R, false));
+    grouped::Maps up, down;
+    FGM_HOST_TRY(weight_map(&up.w, layer->gate_q, 1, kNE, kF, kH));
+    FGM_HOST_TRY(weight_map(&up.w2, layer->up_q, 1, kNE, kF, kH));
+    FGM_HOST_TRY(weight_map(&down.w, layer->down_q, 1, kNE, kH, kF));
+    down.w2 = down.w;
+    FGM_HOST_TRY(x_maps(up, region<void>(ws, o.terms), 2 * kH, 2 * kH, T, true));
+    FGM_HOST_TRY(x_maps(down, region<void>(ws, o.act_terms), 2 * kF, 2 * kF, R, false));
 
     rows::GroupArgs g = {};
     g.ids = ids;
@@ -437,7 +442,7 @@ int fgm_moe_experts_fwd(const fgm_layer *layer, const uint16_t *x, int64_t x_str
     a.cols = tile_cols(R, E, 128);
     a.status = status_word(ws);
     a.timeout_ns = host_wait_limit_ns();
-    FGM_HOST_TRY((launch_grouped<grouped::kGated, true>(gmap, umap, xmap, a, sms, st)));
+    FGM_HOST_TRY((launch_grouped<grouped::kGated, true>(up, a, sms, st)));
     FGM_HOST_TRY(launch_overlapped(rows::k_act_terms, dim3(static_cast<unsigned>((R + rows::kTermWarps - 1) / rows::kTermWarps)),
                                    32 * rows::kTermWarps, 0, st, static_cast<const uint16_t *>(a.out), static_cast<const uint8_t *>(a.exps),
                                    a.offsets + E, region<uint8_t>(ws, o.act_terms), region<float>(ws, o.sa)));
@@ -452,7 +457,7 @@ int fgm_moe_experts_fwd(const fgm_layer *layer, const uint16_t *x, int64_t x_str
     d.exps = nullptr;
     d.smax = region<float>(ws, o.smax);
     d.cols = tile_cols(R, E, 256);
-    FGM_HOST_TRY((launch_grouped<grouped::kDown, true>(dmap, dmap, amap, d, sms, st)));
+    FGM_HOST_TRY((launch_grouped<grouped::kDown, true>(down, d, sms, st)));
     const rows::CombineArgs c{d.out, region<float>(ws, o.sa), d.smax, ids, w, g.pos, g.offsets, shared ? 1 : 0, y};
     return launch_overlapped(rows::k_combine, dim3(static_cast<unsigned>(T)), rows::kCombineThreads, 0, st, c);
 }
