@@ -48,6 +48,7 @@ struct Args {
     uint16_t *out;           // [R][N]
     uint8_t *exps;           // kGated: [R][N / 32] exponents
     const float *smax;       // kDown: [E] a power of two not below the expert's scales
+    int wide;                // 16-byte stores to out
     int cols;                // rows of a tile at most, a multiple of 32
     int stages;
     int32_t *status;
@@ -99,6 +100,47 @@ __device__ __forceinline__ void copy_gathered(uint32_t dst, const CUtensorMap *m
         : "memory");
 }
 
+// 16-bit values of a feature a lane and eight rows, two rows a word, to eight features
+// of one row a lane: lane l gets row l & 7, features (l >> 3) * 8 .. + 7.
+__device__ __forceinline__ uint4 transposed(const uint32_t (&p)[4], int lane)
+{
+    uint32_t q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {                // features in pairs: even lanes keep the first row of two
+        const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, p[i], 1);
+        q[i] = __byte_perm(p[i], o, lane & 1 ? 0x3276 : 0x5410);
+    }
+    uint2 r[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {                // in fours
+        const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, lane & 2 ? q[2 * i] : q[2 * i + 1], 2);
+        r[i] = lane & 2 ? make_uint2(o, q[2 * i + 1]) : make_uint2(q[2 * i], o);
+    }
+    const uint32_t x = __shfl_xor_sync(0xFFFFFFFFu, lane & 4 ? r[0].x : r[1].x, 4), y = __shfl_xor_sync(0xFFFFFFFFu, lane & 4 ? r[0].y : r[1].y, 4);
+    return lane & 4 ? make_uint4(x, y, r[1].x, r[1].y) : make_uint4(r[0].x, r[0].y, x, y);
+}
+
+// gelu_tanh (common.cuh) as x times a sigmoid: 0.5 (1 + tanh z) = 1 / (1 + exp(-2 z)).
+__device__ __forceinline__ float gelu(float x)
+{
+    const float z = 0.7978845608028654f * (x + 0.044715f * x * x * x);
+    return __fdividef(x, 1.0f + __expf(-2.0f * z));
+}
+
+// A place in the ring and the parity of its round, counted: a thread that divides for
+// them takes longer than a stage of few rows (122 us where it now takes 105).
+struct Place {
+    uint32_t slot = 0, phase = 0;
+
+    __device__ __forceinline__ void next(uint32_t stages)
+    {
+        if (++slot == stages) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
+
 // The tensor maps of a launch. x: boxes of 8, 16, .. 128 rows; for gathering the first, of one row.
 struct Maps {
     CUtensorMap w, w2, x[5];
@@ -129,8 +171,8 @@ struct Tile {
     {
         while (item >= sh.cum[e + 1])
             ++e;
-        const int c = sh.count[e], nt = (c + p.cols - 1) / p.cols, local = item - sh.cum[e], n = local % nt;
-        n0 = local / nt * 256;
+        const int c = sh.count[e], nt = (c + p.cols - 1) / p.cols, across = (p.N + 255) / 256, local = item - sh.cum[e], n = local / across;
+        n0 = (local - n * across) * 256;
         const int a = static_cast<int>(static_cast<int64_t>(c) * n / nt), b = static_cast<int>(static_cast<int64_t>(c) * (n + 1) / nt);
         r0 = sh.row0[e] + a;
         live = b - a;
@@ -206,11 +248,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
     const uint32_t tmem = sh.tmem;
     const tc::Waiter wait{&sh.abort, p.status, p.timeout_ns};
     const int items = sh.cum[p.E];
+    const uint32_t bar0 = tc::saddr(&sh.full[0]), full0 = tc::in_first(bar0);
     Tile t;
     t.e = 0;
 
     if (warp == 0) {
-        // ------------------------------------------------------------ copies (each CTA its own weights and rows)
+        // ------------------------------------------------------------ copies of weights (each CTA its own; rows below)
         if (lane == 0) {
             tc::prefetch_map(&maps.w);
             tc::prefetch_map(&maps.w2);
@@ -219,34 +262,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
             asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(again));
             bool ok = true;
             uint32_t n = 0;
+            Place at;
             for (int item = pair; item < items && ok; item += pairs) {
                 t.find(sh, p, item);
-                const int half = t.half(), row = t.r0 + rank * half;
-                const RowBoxes box(half);
-                const uint32_t mine = kWBoxes * kBox + (p.src ? half : box.rows()) * 256;
+                const int half = t.half();
+                const uint32_t mine = kWBoxes * kBox + (p.src ? half : RowBoxes(half).rows()) * 256;
                 const uint64_t policy = sh.count[t.e] <= p.cols ? once : again;
-                for (int ks = 0; ks < steps; ++ks, ++n) {
-                    const uint32_t slot = n % stages;
-                    if (n >= stages && !(ok = wait(&sh.empty[slot], n / stages - 1, 34, ks)))
+                const int w0 = t.n0 + rank * 128;
+                for (int ks = 0; ks < steps; ++ks, ++n, at.next(stages)) {
+                    if (n >= stages && !(ok = wait(&sh.empty[at.slot], at.phase ^ 1, 34, ks)))
                         break;
-                    const uint32_t bar = tc::in_first(tc::saddr(&sh.full[slot])), dst = ring + slot * stage;
+                    const uint32_t bar = full0 + at.slot * 8, dst = ring + at.slot * stage;
                     if (rank == 0)
-                        tc::bar_expect(tc::saddr(&sh.full[slot]), 2 * mine);
-                    sh.bytes[slot] = sh.others[slot] = mine;
-                    const int w0 = t.n0 + rank * 128;
+                        tc::bar_expect(bar0 + at.slot * 8, 2 * mine);
+                    sh.bytes[at.slot] = sh.others[at.slot] = mine;
                     copy_weights(dst, &maps.w, ks * kStageK, w0, t.e, bar, policy);
                     if (MODE == kGated)
                         copy_weights(dst + kBox, &maps.w2, ks * kStageK, w0, t.e, bar, policy);
                     else if (!BYTES)
                         copy_weights(dst + kBox, &maps.w, ks * kStageK + 64, w0, t.e, bar, policy);
-                    if (!p.src)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            copy_rows(dst + rows_at + h * xbox, &maps.x[box.first], ks * 256 + h * 128, row, bar);
-                            if (box.second >= 0)
-                                copy_rows(dst + rows_at + h * xbox + (1024 << box.first), &maps.x[box.second], ks * 256 + h * 128,
-                                          row + (8 << box.first), bar);
-                        }
                 }
             }
             sh.issued = n;
@@ -257,15 +291,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
         if (rank == 0) {
             const bool lead = tc::elect();
             bool ok = true;
-            uint32_t n = 0, tile = 0;
+            uint32_t tile = 0;
+            Place at;
             for (int item = pair; item < items && ok; item += pairs, ++tile) {
                 t.find(sh, p, item);
                 const uint32_t buf = tile & 1, d = tmem + buf * 256, idesc = tc::product_desc(256, 2 * t.half(), BYTES);
                 if (tile >= 2)
                     ok = wait(&sh.tempty[buf], (tile >> 1) - 1, 35, t.e);
-                for (int ks = 0; ks < steps; ++ks, ++n) {
-                    const uint32_t slot = n % stages;
-                    ok = ok && wait(&sh.full[slot], n / stages, 36, ks);
+                for (int ks = 0; ks < steps; ++ks, at.next(stages)) {
+                    const uint32_t slot = at.slot;
+                    ok = ok && wait(&sh.full[slot], at.phase, 36, ks);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok)
                         break;
@@ -308,11 +343,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
             __syncwarp();
         }
     } else if (warp < 4 || warp >= 12) {
-        // ------------------------------------------------------------ gathered rows, four a copy: a lane's are four of one half of K
+        // ------------------------------------------------------------ rows: gathered ones four a copy, a lane's of one half of K; else boxes
         if (p.src) {
             const int mate = warp < 4 ? warp - 2 : warp - 10, h = lane & 1, group = (lane >> 1) * kGatherWarps + mate;
             bool ok = true;
             uint32_t n = 0;
+            Place place;
             for (int item = pair; item < items && ok; item += pairs) {
                 t.find(sh, p, item);
                 const int half = t.half(), at = rank * half + 4 * group;
@@ -326,16 +362,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
                         v[j] = s >= 0 && s / p.per < p.x_rows ? s / p.per : 0;
                     }
                 const int4 idx = make_int4(v[0], v[1], v[2], v[3]);
-                for (int ks = 0; ks < steps; ++ks, ++n) {
-                    const uint32_t slot = n % stages;
+                for (int ks = 0; ks < steps; ++ks, ++n, place.next(stages)) {
                     if (n >= stages)
-                        ok = wait(&sh.empty[slot], n / stages - 1, 43, ks);
+                        ok = wait(&sh.empty[place.slot], place.phase ^ 1, 43, ks);
                     if (!(ok = __all_sync(0xFFFFFFFFu, ok)))
                         break;
                     if (mine)
-                        copy_gathered(ring + slot * stage + rows_at + h * xbox + group * 512, &maps.x[0], ks * 256 + h * 128, idx,
-                                      tc::in_first(tc::saddr(&sh.full[slot])));
+                        copy_gathered(ring + place.slot * stage + rows_at + h * xbox + group * 512, &maps.x[0], ks * 256 + h * 128, idx,
+                                      full0 + place.slot * 8);
                     __syncwarp();
+                }
+            }
+        } else if (warp == 2 && lane == 0) {
+            bool ok = true;
+            uint32_t n = 0;
+            Place place;
+            for (int item = pair; item < items && ok; item += pairs) {
+                t.find(sh, p, item);
+                const int half = t.half(), row = t.r0 + rank * half;
+                const RowBoxes box(half);
+                for (int ks = 0; ks < steps; ++ks, ++n, place.next(stages)) {
+                    if (n >= stages && !(ok = wait(&sh.empty[place.slot], place.phase ^ 1, 43, ks)))
+                        break;
+                    const uint32_t dst = ring + place.slot * stage + rows_at, bar = full0 + place.slot * 8;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        copy_rows(dst + h * xbox, &maps.x[box.first], ks * 256 + h * 128, row, bar);
+                        if (box.second >= 0)
+                            copy_rows(dst + h * xbox + (1024 << box.first), &maps.x[box.second], ks * 256 + h * 128, row + (8 << box.first), bar);
+                    }
                 }
             }
         }
@@ -379,44 +434,99 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
             tc::fence_after();
             if (alive && nw < p.N) {
                 const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * 256 + c0;
+                uint32_t u[2][8], v[2][8];
+                const int many = min(half, t.live - c0);     // columns of this warp
+                auto read = [&](int c, uint32_t (&u)[8], uint32_t (&v)[8]) {
+                    tc::read8(from + c, u);
+                    if (MODE == kGated)
+                        tc::read8(from + 128 + c, v);
+                };
+                // columns c .. c + 7, the next eight on their way meanwhile; xg: the scales of c & ~31 .. | 31, a lane each
+                auto columns = [&](int c, float xg, uint32_t (&u)[8], uint32_t (&v)[8], uint32_t (&u1)[8], uint32_t (&v1)[8]) {
+                    __syncwarp();
+                    tc::read_wait();
 #pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    for (int j = 0; j < 32 && g * 32 + j < half && c0 + g * 32 + j < t.live; j += 8) {
-                        uint32_t u[8], v[8];
-                        tc::read8(from + g * 32 + j, u);
+                    for (int q = 0; q < 8; ++q) {
+                        asm volatile("" : "+r"(u[q]));
                         if (MODE == kGated)
-                            tc::read8(from + 128 + g * 32 + j, v);
-                        tc::read_wait();
+                            asm volatile("" : "+r"(v[q]));
+                    }
+                    if (c + 8 < many)
+                        read(c + 8, u1, v1);
+                    uint32_t pk[4];
+                    int e_mine = 0;
+                    if (MODE == kGated) {
+                        float a[8];
 #pragma unroll
                         for (int q = 0; q < 8; ++q) {
-                            asm volatile("" : "+r"(u[q]));
-                            if (MODE == kGated)
-                                asm volatile("" : "+r"(v[q]));
+                            const float x = __shfl_sync(0xFFFFFFFFu, xg, (c & 24) + q);
+                            a[q] = gelu(__uint_as_float(u[q]) * s0 * x) * (__uint_as_float(v[q]) * s1 * x);
+                            // |a| < 2^(e - 126) for all 32: below 2^15 in f16, which has 11 bits down to 2^-14
+                            const uint32_t bits = n < p.N ? __float_as_uint(a[q]) & 0x7FFFFFFFu : 0;
+                            int e = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, bits) >> 23);
+                            e = e < 14 ? 14 : e;
+                            e_mine = (lane & 7) == q ? e : e_mine;
+                            a[q] *= __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
                         }
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const int c = c0 + g * 32 + j + q;
-                            const float x = MODE == kDown ? 1.0f : __shfl_sync(0xFFFFFFFFu, xs[g], j + q);
-                            if (c >= t.live)
-                                break;
-                            const int64_t row = t.r0 + c;
-                            const float d = __uint_as_float(u[q]);
-                            if (MODE == kGated) {
-                                const float a = x < 0.0f ? 0.0f : gelu_tanh(d * s0 * x) * (__uint_as_float(v[q]) * s1 * x);
-                                // |a| < 2^(e - 126) for all 32: below 2^15 in f16, which has 11 bits down to 2^-14
-                                const uint32_t bits = n < p.N ? __float_as_uint(a) & 0x7FFFFFFFu : 0;
-                                int e = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, bits) >> 23);
-                                e = e < 14 ? 14 : e;
-                                const __half h = __float2half_rn(a * __uint_as_float(static_cast<uint32_t>(268 - e) << 23));
-                                if (n < p.N)
-                                    p.out[row * p.N + n] = __half_as_ushort(h);
-                                if (lane == 0)
-                                    p.exps[row * (p.N >> 5) + (nw >> 5)] = static_cast<uint8_t>(e);
-                            } else if (n < p.N) {
-                                p.out[row * p.N + n] = MODE == kDown ? __half_as_ushort(__float2half_rn(d * s0))
-                                                                     : f32_to_bf16(x < 0.0f ? 0.0f : d * s0 * x);
+                        for (int q = 0; q < 4; ++q) {
+                            const __half2 h = __floats2half2_rn(a[2 * q], a[2 * q + 1]);
+                            pk[q] = *reinterpret_cast<const uint32_t *>(&h);
+                        }
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float a = __uint_as_float(u[2 * q]) * s0, b = __uint_as_float(u[2 * q + 1]) * s0;
+                            if (MODE == kDown) {
+                                const __half2 h = __floats2half2_rn(a, b);
+                                pk[q] = *reinterpret_cast<const uint32_t *>(&h);
+                            } else {
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+                                pk[q] = *reinterpret_cast<const uint32_t *>(&h);
                             }
                         }
+                    }
+                    // (a row's scale is a power of two: it may follow the rounding)
+                    const float x = MODE == kGemm ? __shfl_sync(0xFFFFFFFFu, xg, (c & 24) + (lane & 7)) : 1.0f;
+                    auto scaled = [&](uint32_t w) {
+                        if (MODE != kGemm)
+                            return w;
+                        __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162 *>(&w);
+                        const float2 f = __bfloat1622float2(h);
+                        h = __floats2bfloat162_rn(f.x * x, f.y * x);
+                        return x < 0.0f ? 0u : *reinterpret_cast<const uint32_t *>(&h);
+                    };
+                    const int mine = c + (lane & 7);
+                    const int64_t row = t.r0 + c0 + mine;
+                    const uint4 o = transposed(pk, lane);
+                    if (mine < many) {
+                        const uint32_t w[4] = {scaled(o.x), scaled(o.y), scaled(o.z), scaled(o.w)};
+                        uint16_t *to = p.out + row * p.N + nw + (lane >> 3) * 8;
+                        if (p.wide) {
+                            if (nw + (lane >> 3) * 8 < p.N)
+                                *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                if (nw + (lane >> 3) * 8 + q < p.N)
+                                    to[q] = static_cast<uint16_t>(q & 1 ? w[q >> 1] >> 16 : w[q >> 1]);
+                        }
+                        if (MODE == kGated && lane < 8)
+                            p.exps[row * (p.N >> 5) + (nw >> 5)] = static_cast<uint8_t>(e_mine);
+                    }
+                };
+                if (many > 0)
+                    read(0, u[0], v[0]);
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    if (g * 32 < many) {
+                        columns(g * 32, xs[g], u[0], v[0], u[1], v[1]);
+                        if (g * 32 + 8 < many)
+                            columns(g * 32 + 8, xs[g], u[1], v[1], u[0], v[0]);
+                        if (g * 32 + 16 < many)
+                            columns(g * 32 + 16, xs[g], u[0], v[0], u[1], v[1]);
+                        if (g * 32 + 24 < many)
+                            columns(g * 32 + 24, xs[g], u[1], v[1], u[0], v[0]);
                     }
             }
             tc::fence_before();

@@ -369,6 +369,7 @@ int fgm_grouped_gemm(const uint16_t *x, int64_t x_stride, int64_t x_rows, const 
     a.s0 = w_s;
     a.xs = region<float>(ws, o.xs);
     a.out = out;
+    a.wide = N % 8 == 0 && is_aligned(out, 16);
     a.cols = tile_cols(R, E, 256);
     a.status = status_word(ws);
     a.timeout_ns = host_wait_limit_ns();
@@ -438,6 +439,7 @@ int fgm_moe_experts_fwd(const fgm_layer *layer, const uint16_t *x, int64_t x_str
     a.s1 = layer->up_s;
     a.xs = region<float>(ws, o.xs);
     a.out = region<uint16_t>(ws, o.rows);
+    a.wide = 1;
     a.exps = region<uint8_t>(ws, o.exps);
     a.cols = tile_cols(R, E, 128);
     a.status = status_word(ws);
