@@ -402,15 +402,15 @@ int encode_tiled_fn(EncodeTiledFn *fn)
 
 }  // namespace
 
-// Tensor map over an array of `rank` dimensions of 1- or 2-byte elements (innermost
-// first, strides in bytes from the second on) with boxes in the 128-byte swizzle (host.h).
-int host_map128(CUtensorMap *map, const void *base, int elem, int rank, const uint64_t *dims, const uint64_t *strides, const uint32_t *box)
+// Tensor map over an array of up to 4 dimensions of 1- or 2-byte elements (innermost
+// first, strides in bytes from the second on), boxes as they lie or in the 128-byte swizzle (host.h).
+int host_map(CUtensorMap *map, const void *base, int elem, int rank, const uint64_t *dims, const uint64_t *strides, const uint32_t *box, bool swizzled)
 {
     EncodeTiledFn encode = nullptr;
     FGM_TRY(encode_tiled_fn(&encode));
-    cuuint64_t d[3], st[2];
-    cuuint32_t b[3];
-    const cuuint32_t estr[3] = {1, 1, 1};
+    cuuint64_t d[4], st[3];
+    cuuint32_t b[4];
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
     for (int i = 0; i < rank; ++i) {
         d[i] = dims[i];
         b[i] = box[i];
@@ -418,10 +418,11 @@ int host_map128(CUtensorMap *map, const void *base, int elem, int rank, const ui
             st[i - 1] = strides[i - 1];
     }
     const CUresult r = encode(map, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base),
-                              d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                              swizzled ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
-        return fail(FGM_ERR_CUDA, "cuTensorMapEncodeTiled (128-byte boxes) failed (%d)", static_cast<int>(r));
+        return fail(FGM_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
     return FGM_OK;
 }
 

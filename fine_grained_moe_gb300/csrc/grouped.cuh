@@ -35,8 +35,14 @@ enum Mode {
     kDown = 2,   // y[r][n] = f16(s[n] / smax[e] 2^-12 D)
 };
 
+// What kGated and kDown write lies in blocks of 8 rows x 32 features, 512 bytes that a
+// warp stores at once: row-major rows get 64 bytes from each warp, which cost it 50
+// cycles per 512 bytes instead of 18. Their experts' rows begin at multiples of 8.
+__device__ __forceinline__ int64_t blocked(int64_t row, int n, int N) { return ((row >> 3) * (N >> 5) + (n >> 5)) * 256 + (row & 7) * 32 + (n & 31); }
+
 struct Args {
     const int32_t *offsets;  // [E + 1]
+    const int32_t *counts;   // [E] rows of each expert, or NULL: up to the next one's
     int E;
     int64_t R;               // rows at most
     const int32_t *src;      // row r takes x row src[r] / per; NULL: x row r
@@ -45,8 +51,8 @@ struct Args {
     int N, K;
     const float *s0, *s1;    // [E][N] row scales (gate and up), or NULL
     const float *xs;         // [x_rows] scales of the terms
-    uint16_t *out;           // [R][N]
-    uint8_t *exps;           // kGated: [R][N / 32] exponents
+    uint16_t *out;           // [R][N], or blocked
+    uint8_t *exps;           // kGated: exponents [R / 8][N / 32][8]
     const float *smax;       // kDown: [E] a power of two not below the expert's scales
     int wide;                // 16-byte stores to out
     int cols;                // rows of a tile at most, a multiple of 32
@@ -173,9 +179,11 @@ struct Tile {
             ++e;
         const int c = sh.count[e], nt = (c + p.cols - 1) / p.cols, across = (p.N + 255) / 256, local = item - sh.cum[e], n = local / across;
         n0 = (local - n * across) * 256;
-        const int a = static_cast<int>(static_cast<int64_t>(c) * n / nt), b = static_cast<int>(static_cast<int64_t>(c) * (n + 1) / nt);
+        // (the expert's eights of rows, shared out)
+        const int eights = (c + 7) / 8, a = static_cast<int>(static_cast<int64_t>(eights) * n / nt) * 8,
+                  b = static_cast<int>(static_cast<int64_t>(eights) * (n + 1) / nt) * 8;
         r0 = sh.row0[e] + a;
-        live = b - a;
+        live = (b < c ? b : c) - a;
     }
 
     // columns of the products in each CTA's half of the second operand
@@ -211,31 +219,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
     if (warp == 1)
         tc::memory_take<2>(&sh.tmem);
     if (warp == 2) {
-        // tiles before each expert
+        // tiles before each expert: 32 experts at a time, their loads ahead
         const int across = (p.N + 255) / 256;
         int base = 0;
-        for (int e0 = 0; e0 < p.E; e0 += 32) {
-            const int e = e0 + lane;
-            int64_t a = 0, b = 0;
-            if (e < p.E) {
-                a = __ldcg(p.offsets + e);
-                b = __ldcg(p.offsets + e + 1);
-                a = a < 0 ? 0 : a > p.R ? p.R : a;
-                b = b < a ? a : b > p.R ? p.R : b;
-            }
-            int v = (static_cast<int>(b - a) + p.cols - 1) / p.cols * across, sum = v;
-            if (e < p.E) {
-                sh.row0[e] = static_cast<int>(a);
-                sh.count[e] = static_cast<int>(b - a);
+        constexpr int kAhead = 4;
+        for (int e1 = 0; e1 < p.E; e1 += 32 * kAhead) {
+            int32_t from[kAhead], to[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int e = e1 + i * 32 + lane;
+                from[i] = e < p.E ? __ldcg(p.offsets + e) : 0;
+                to[i] = e < p.E ? __ldcg(p.counts ? p.counts + e : p.offsets + e + 1) : 0;
             }
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-                sum += lane >= o ? u : 0;
+            for (int i = 0; i < kAhead; ++i) {
+                const int e = e1 + i * 32 + lane;
+                int64_t a = from[i], b = p.counts ? a + to[i] : to[i];
+                a = a < 0 ? 0 : a > p.R ? p.R : a;
+                b = b < a ? a : b > p.R ? p.R : b;
+                int sum = (static_cast<int>(b - a) + p.cols - 1) / p.cols * across;
+                if (e < p.E) {
+                    sh.row0[e] = static_cast<int>(a);
+                    sh.count[e] = static_cast<int>(b - a);
+                }
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int u = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+                    sum += lane >= o ? u : 0;
+                }
+                if (e < p.E)
+                    sh.cum[e + 1] = base + sum;
+                base += __shfl_sync(0xFFFFFFFFu, sum, 31);
             }
-            if (e < p.E)
-                sh.cum[e + 1] = base + sum;
-            base += __shfl_sync(0xFFFFFFFFu, sum, 31);
         }
         if (lane == 0)
             sh.cum[0] = 0;
@@ -434,25 +449,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
             tc::fence_after();
             if (alive && nw < p.N) {
                 const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * 256 + c0;
-                uint32_t u[2][8], v[2][8];
+                constexpr int kCols = MODE == kGated ? 8 : 16;
+                uint32_t u[2][kCols], v[2][kCols];
                 const int many = min(half, t.live - c0);     // columns of this warp
-                auto read = [&](int c, uint32_t (&u)[8], uint32_t (&v)[8]) {
-                    tc::read8(from + c, u);
+                auto read = [&](int c, uint32_t (&u)[kCols], uint32_t (&v)[kCols]) {
+                    tc::read(from + c, u);
                     if (MODE == kGated)
-                        tc::read8(from + 128 + c, v);
+                        tc::read(from + 128 + c, v);
                 };
-                // columns c .. c + 7, the next eight on their way meanwhile; xg: the scales of c & ~31 .. | 31, a lane each
-                auto columns = [&](int c, float xg, uint32_t (&u)[8], uint32_t (&v)[8], uint32_t (&u1)[8], uint32_t (&v1)[8]) {
-                    __syncwarp();
-                    tc::read_wait();
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        asm volatile("" : "+r"(u[q]));
-                        if (MODE == kGated)
-                            asm volatile("" : "+r"(v[q]));
-                    }
-                    if (c + 8 < many)
-                        read(c + 8, u1, v1);
+                // eight columns; xg: the scales of columns c & ~31 .. c | 31, a lane each
+                auto eight = [&](int c, float xg, const uint32_t *u, const uint32_t *v) {
                     uint32_t pk[4];
                     int e_mine = 0;
                     if (MODE == kGated) {
@@ -462,8 +468,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
                             const float x = __shfl_sync(0xFFFFFFFFu, xg, (c & 24) + q);
                             a[q] = gelu(__uint_as_float(u[q]) * s0 * x) * (__uint_as_float(v[q]) * s1 * x);
                             // |a| < 2^(e - 126) for all 32: below 2^15 in f16, which has 11 bits down to 2^-14
-                            const uint32_t bits = n < p.N ? __float_as_uint(a[q]) & 0x7FFFFFFFu : 0;
-                            int e = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, bits) >> 23);
+                            int e = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(a[q]) & 0x7FFFFFFFu) >> 23);
                             e = e < 14 ? 14 : e;
                             e_mine = (lane & 7) == q ? e : e_mine;
                             a[q] *= __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
@@ -486,48 +491,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
                             }
                         }
                     }
+                    const uint4 o = transposed(pk, lane);
+                    const int64_t row = t.r0 + c0 + c;
+                    if (MODE != kGemm) {
+                        // (rows of the eight behind the expert's last are its own too)
+                        *reinterpret_cast<uint4 *>(p.out + blocked(row, nw, p.N) + (lane & 7) * 32 + (lane >> 3) * 8) = o;
+                        if (MODE == kGated && lane < 8)
+                            p.exps[((row >> 3) * (p.N >> 5) + (nw >> 5)) * 8 + lane] = static_cast<uint8_t>(e_mine);
+                        return;
+                    }
                     // (a row's scale is a power of two: it may follow the rounding)
-                    const float x = MODE == kGemm ? __shfl_sync(0xFFFFFFFFu, xg, (c & 24) + (lane & 7)) : 1.0f;
+                    const float x = __shfl_sync(0xFFFFFFFFu, xg, (c & 24) + (lane & 7));
                     auto scaled = [&](uint32_t w) {
-                        if (MODE != kGemm)
-                            return w;
-                        __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162 *>(&w);
-                        const float2 f = __bfloat1622float2(h);
-                        h = __floats2bfloat162_rn(f.x * x, f.y * x);
+                        const float2 f = bf16x2_to_f32(w);
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(f.x * x, f.y * x);
                         return x < 0.0f ? 0u : *reinterpret_cast<const uint32_t *>(&h);
                     };
-                    const int mine = c + (lane & 7);
-                    const int64_t row = t.r0 + c0 + mine;
-                    const uint4 o = transposed(pk, lane);
-                    if (mine < many) {
+                    if (c + (lane & 7) < many) {
                         const uint32_t w[4] = {scaled(o.x), scaled(o.y), scaled(o.z), scaled(o.w)};
-                        uint16_t *to = p.out + row * p.N + nw + (lane >> 3) * 8;
+                        const int first = nw + (lane >> 3) * 8;
+                        uint16_t *to = p.out + (row + (lane & 7)) * p.N + first;
                         if (p.wide) {
-                            if (nw + (lane >> 3) * 8 < p.N)
+                            if (first < p.N)
                                 *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
                         } else {
 #pragma unroll
                             for (int q = 0; q < 8; ++q)
-                                if (nw + (lane >> 3) * 8 + q < p.N)
+                                if (first + q < p.N)
                                     to[q] = static_cast<uint16_t>(q & 1 ? w[q >> 1] >> 16 : w[q >> 1]);
                         }
-                        if (MODE == kGated && lane < 8)
-                            p.exps[row * (p.N >> 5) + (nw >> 5)] = static_cast<uint8_t>(e_mine);
                     }
+                };
+                // kCols columns, the next on their way meanwhile
+                auto columns = [&](int c, float xg, uint32_t (&u)[kCols], uint32_t (&v)[kCols], uint32_t (&u1)[kCols], uint32_t (&v1)[kCols]) {
+                    __syncwarp();
+                    tc::read_wait();
+#pragma unroll
+                    for (int q = 0; q < kCols; ++q) {
+                        asm volatile("" : "+r"(u[q]));
+                        if (MODE == kGated)
+                            asm volatile("" : "+r"(v[q]));
+                    }
+                    if (c + kCols < many)
+                        read(c + kCols, u1, v1);
+                    eight(c, xg, u, v);
+                    if (kCols == 16 && (MODE == kGemm || c + 8 < many))
+                        eight(c + 8, xg, u + 8, v + 8);
                 };
                 if (many > 0)
                     read(0, u[0], v[0]);
 #pragma unroll
                 for (int g = 0; g < 4; ++g)
-                    if (g * 32 < many) {
-                        columns(g * 32, xs[g], u[0], v[0], u[1], v[1]);
-                        if (g * 32 + 8 < many)
-                            columns(g * 32 + 8, xs[g], u[1], v[1], u[0], v[0]);
-                        if (g * 32 + 16 < many)
-                            columns(g * 32 + 16, xs[g], u[0], v[0], u[1], v[1]);
-                        if (g * 32 + 24 < many)
-                            columns(g * 32 + 24, xs[g], u[1], v[1], u[0], v[0]);
-                    }
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2 * kCols)
+                        if (g * 32 + j < many) {
+                            columns(g * 32 + j, xs[g], u[0], v[0], u[1], v[1]);
+                            if (g * 32 + j + kCols < many)
+                                columns(g * 32 + j + kCols, xs[g], u[1], v[1], u[0], v[0]);
+                        }
             }
             tc::fence_before();
             __syncwarp();

@@ -17,7 +17,7 @@ namespace fgm {
 int host_fail(int code, const char *msg);
 int host_device_ready(int *sms);
 long long host_wait_limit_ns();
-int host_map128(CUtensorMap *map, const void *base, int elem, int rank, const uint64_t *dims, const uint64_t *strides, const uint32_t *box);
+int host_map(CUtensorMap *map, const void *base, int elem, int rank, const uint64_t *dims, const uint64_t *strides, const uint32_t *box, bool swizzled);
 int host_rows64_map(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows);
 int host_lm_logits(const uint16_t *emb, int64_t V, const uint16_t *h, int M, float *z, void *ws, void *stream);
 int host_hidden_map(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows, uint32_t slices);

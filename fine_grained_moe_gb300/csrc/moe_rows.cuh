@@ -33,6 +33,7 @@ struct GroupArgs {
     int32_t *pos;            // [n] each slot's place, -1 without an expert, or NULL
     int per;                 // slots of a token
     int shared;              // tokens that one more expert takes behind the others (offsets has E + 2 entries), 0: none
+    int32_t *counts;         // [E], or [E + 1] with `shared`, and experts begin at multiples of 8; or NULL: they follow each other
 };
 
 // Counts of a warp's run of slots in its own row of hist.
@@ -47,47 +48,43 @@ __device__ __forceinline__ void count_run(const GroupArgs &p, int64_t i0, int64_
     }
 }
 
-__device__ __forceinline__ void run_of(const GroupArgs &p, int warp, int64_t &i0, int64_t &i1)
+__device__ __forceinline__ void run_of(const GroupArgs &p, int chunk, int warp, int64_t &i0, int64_t &i1)
 {
     const int64_t each = p.chunk / kGroupWarps;
-    i0 = static_cast<int64_t>(blockIdx.x) * p.chunk + warp * each;
+    i0 = static_cast<int64_t>(chunk) * p.chunk + warp * each;
     i1 = i0 + each < p.n ? i0 + each : p.n;
 }
 
-__global__ void __launch_bounds__(kGroupThreads) k_group_count(const GroupArgs p)
+// Of chunk `chunk`, by a CTA; hist: shared, [kGroupWarps][E].
+__device__ __forceinline__ void group_count(const GroupArgs &p, int chunk, int *hist)
 {
-    extern __shared__ int hist[];                // [kGroupWarps][E]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = threadIdx.x; i < kGroupWarps * p.E; i += kGroupThreads)
         hist[i] = 0;
-    tc::after_previous();
-    tc::let_next_start();
     __syncthreads();
     int64_t i0, i1;
-    run_of(p, warp, i0, i1);
+    run_of(p, chunk, warp, i0, i1);
     count_run(p, i0, i1, hist + warp * p.E, lane);
     __syncthreads();
     for (int e = threadIdx.x; e < p.E; e += kGroupThreads) {
         int s = 0;
         for (int w = 0; w < kGroupWarps; ++w)
             s += hist[w * p.E + e];
-        p.count[static_cast<int64_t>(blockIdx.x) * p.E + e] = s;
+        p.count[static_cast<int64_t>(chunk) * p.E + e] = s;
     }
 }
 
-__global__ void __launch_bounds__(kGroupThreads) k_group_deal(const GroupArgs p)
+// The same CTA's slots dealt; hist: [kGroupWarps][E], then [E] totals.
+__device__ __forceinline__ void group_deal(const GroupArgs &p, int chunk, int *hist)
 {
-    extern __shared__ int hist[];                // [kGroupWarps][E], then [E] totals
     __shared__ int warp_sum[kGroupWarps];
     int *total = hist + kGroupWarps * p.E;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = threadIdx.x; i < kGroupWarps * p.E; i += kGroupThreads)
         hist[i] = 0;
-    tc::after_previous();
-    tc::let_next_start();
     __syncthreads();
     int64_t i0, i1;
-    run_of(p, warp, i0, i1);
+    run_of(p, chunk, warp, i0, i1);
     count_run(p, i0, i1, hist + warp * p.E, lane);
     __syncthreads();
     // a warp's first place of each expert, from the chunk's first, and the expert's slots in all
@@ -97,7 +94,7 @@ __global__ void __launch_bounds__(kGroupThreads) k_group_deal(const GroupArgs p)
 #pragma unroll 8
             for (int c = 0; c < p.chunks; ++c) {
                 const int v = __ldcg(p.count + static_cast<int64_t>(c) * p.E + e);
-                before += c < static_cast<int>(blockIdx.x) ? v : 0;
+                before += c < chunk ? v : 0;
                 all += v;
             }
         for (int w = 0; w < kGroupWarps; ++w) {
@@ -105,7 +102,10 @@ __global__ void __launch_bounds__(kGroupThreads) k_group_deal(const GroupArgs p)
             hist[w * p.E + e] = before + mine;
             mine += v;
         }
-        total[e] = p.chunks > 1 ? all : mine;
+        all = p.chunks > 1 ? all : mine;
+        if (p.counts && chunk == 0)
+            p.counts[e] = all;
+        total[e] = p.counts ? (all + 7) & ~7 : all;
     }
     __syncthreads();
     // places before each expert: a thread scans E / 256 experts, rounded up
@@ -128,17 +128,19 @@ __global__ void __launch_bounds__(kGroupThreads) k_group_deal(const GroupArgs p)
     for (int e = e0; e < e0 + each && e < p.E; ++e) {
         const int v = total[e];
         total[e] = base;
-        if (blockIdx.x == 0)
+        if (chunk == 0)
             p.offsets[e] = base;
         base += v;
     }
     int all = 0;
     for (int w = 0; w < kGroupWarps; ++w)
         all += warp_sum[w];
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (chunk == 0 && threadIdx.x == 0) {
         p.offsets[p.E] = all;
-        if (p.shared)
+        if (p.shared) {
             p.offsets[p.E + 1] = all + p.shared;
+            p.counts[p.E] = p.shared;
+        }
     }
     __syncthreads();
     int *at = hist + warp * p.E;
@@ -163,10 +165,26 @@ __global__ void __launch_bounds__(kGroupThreads) k_group_deal(const GroupArgs p)
         }
     }
     if (p.shared) {
-        const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.chunk / p.per;
+        const int64_t t0 = static_cast<int64_t>(chunk) * p.chunk / p.per;
         for (int64_t t = t0 + threadIdx.x; t < t0 + p.chunk / p.per && t < p.shared; t += kGroupThreads)
             p.src[all + t] = static_cast<int32_t>(t);
     }
+}
+
+__global__ void __launch_bounds__(kGroupThreads) k_group_count(const GroupArgs p)
+{
+    extern __shared__ int hist[];
+    tc::after_previous();
+    tc::let_next_start();
+    group_count(p, blockIdx.x, hist);
+}
+
+__global__ void __launch_bounds__(kGroupThreads) k_group_deal(const GroupArgs p)
+{
+    extern __shared__ int hist[];
+    tc::after_previous();
+    tc::let_next_start();
+    group_deal(p, blockIdx.x, hist);
 }
 
 // ---------------------------------------------------------------- terms
@@ -207,93 +225,144 @@ __device__ __forceinline__ void write_terms(uint8_t *row, int k, const float *v)
 // 2^(e - 134), for a row whose largest exponent field is e: below 2^(e - 126), above 2^8 times less.
 __device__ __forceinline__ float row_scale(int e) { return e == 255 ? __int_as_float(0x7FC00000) : __int_as_float((e - 7) << 23); }
 
-constexpr int kTermWarps = 8;
+constexpr int kTermThreads = 256;
+constexpr int kTermRow = 128;                    // threads of a row
+constexpr int kTermHeld = 4;                     // vectors of 8 that each holds (longer rows are read twice)
 
-// Rows of bf16: a warp each.
-__global__ void __launch_bounds__(32 * kTermWarps) k_terms(const uint16_t *x, int64_t stride, int64_t n, int K, uint8_t *terms, float *scale)
+struct TermArgs {
+    const uint16_t *x;       // bf16 rows of K, `stride` apart
+    int64_t stride, n;
+    int K;
+    uint8_t *terms;          // [n][2 K rounded up to 32]
+    float *scale;            // [n]
+};
+
+// Two rows of bf16 by a CTA, from row0 on. All of a row is on its way before its
+// largest element is known.
+__device__ __forceinline__ void row_terms(const TermArgs &p, int64_t row0)
 {
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kTermWarps + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31, K32 = (K + 31) & ~31;
-    tc::after_previous();
-    tc::let_next_start();
-    if (row >= n)
-        return;
-    const uint16_t *xr = x + row * stride;
+    __shared__ uint32_t most[kTermThreads / 32];
+    const int t = threadIdx.x % kTermRow, warp = threadIdx.x >> 5, K32 = (p.K + 31) & ~31;
+    const int64_t row = row0 + threadIdx.x / kTermRow;
+    const uint16_t *xr = p.x + row * p.stride;
+    uint4 u[kTermHeld];
     uint32_t m = 0;
-    for (int k = lane * 8; k < K; k += 256) {
-        const uint4 u = __ldcg(reinterpret_cast<const uint4 *>(xr + k));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    auto largest = [&](const uint4 &v) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int q = 0; q < 4; ++q)
             m = max(m, max(w[q] & 0x7FFFu, w[q] >> 16 & 0x7FFFu));
-    }
-    int e = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, m) >> 7);
+    };
+    auto take = [&](int k) { return row < p.n && k < p.K ? __ldcg(reinterpret_cast<const uint4 *>(xr + k)) : make_uint4(0, 0, 0, 0); };
+#pragma unroll
+    for (int i = 0; i < kTermHeld; ++i)
+        u[i] = take((i * kTermRow + t) * 8);
+#pragma unroll
+    for (int i = 0; i < kTermHeld; ++i)
+        largest(u[i]);
+    for (int k = (kTermHeld * kTermRow + t) * 8; k < p.K; k += kTermRow * 8)
+        largest(take(k));
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if ((threadIdx.x & 31) == 0)
+        most[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kTermRow / 32; ++w)
+        m = max(m, most[(warp & ~(kTermRow / 32 - 1)) + w]);
+    if (row >= p.n)
+        return;
+    int e = static_cast<int>(m >> 7);
     e = e < 14 ? 14 : e;
-    if (lane == 0)
-        scale[row] = row_scale(e);
+    if (t == 0)
+        p.scale[row] = row_scale(e);
     const float up = __int_as_float((261 - e) << 23);         // 1 / s (e = 255: whatever it is, s is NaN)
-    for (int k = lane * 8; k < K32; k += 256) {
+    uint8_t *to = p.terms + row * (2 * static_cast<int64_t>(K32));
+    auto write = [&](const uint4 &x, int k) {
         float v[8];
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (k < K)
-            u = __ldcg(reinterpret_cast<const uint4 *>(xr + k));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const float2 f = bf16x2_to_f32(w[q]);
             v[2 * q] = f.x * up;
             v[2 * q + 1] = f.y * up;
         }
-        write_terms(terms + row * (2 * static_cast<int64_t>(K32)), k, v);
-    }
+        write_terms(to, k, v);
+    };
+#pragma unroll
+    for (int i = 0; i < kTermHeld; ++i)
+        if ((i * kTermRow + t) * 8 < K32)
+            write(u[i], (i * kTermRow + t) * 8);
+    for (int k = (kTermHeld * kTermRow + t) * 8; k < K32; k += kTermRow * 8)
+        write(take(k), k);
 }
 
-// Rows of the gated activations (grouped.cuh: f16 under a power of two per 32), a
-// warp each; only those of some expert.
-__global__ void __launch_bounds__(32 * kTermWarps) k_act_terms(const uint16_t *act, const uint8_t *exps, const int32_t *n, uint8_t *terms,
-                                                               float *scale)
+__global__ void __launch_bounds__(kTermThreads) k_terms(const TermArgs p)
 {
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kTermWarps + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
     tc::after_previous();
     tc::let_next_start();
-    if (row >= __ldcg(n))
+    row_terms(p, static_cast<int64_t>(blockIdx.x) * (kTermThreads / kTermRow));
+}
+
+// Rows of the gated activations (grouped.cuh: f16 under a power of two per 32, in blocks
+// of 8 rows x 32), eight of them a CTA, a block a warp at a time; only those of some
+// expert, and those that fill an expert's last eight, which nobody reads.
+__global__ void __launch_bounds__(256) k_act_terms(const uint16_t *act, const uint8_t *exps, const int32_t *n, uint8_t *terms, float *scale)
+{
+    constexpr int kBlocks = kF / 32, kMine = (kBlocks + 7) / 8;
+    const int64_t eight = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2;
+    tc::after_previous();
+    tc::let_next_start();
+    if (eight * 8 >= __ldcg(n))
         return;
-    constexpr int kBlocks = kF / 32;
-    const int mine = lane < kBlocks ? __ldcg(exps + row * kBlocks + lane) : 14;
-    const int e = __reduce_max_sync(0xFFFFFFFFu, mine);
-    if (lane == 0)
-        scale[row] = row_scale(e);
+    const uint8_t *ex = exps + eight * (kBlocks * 8) + r;
+    const uint4 *a = reinterpret_cast<const uint4 *>(act + eight * (kBlocks * 256)) + lane;
+    uint4 u[kMine];
+    int eb[kMine], e = 0;
 #pragma unroll
-    for (int i = 0; i < (kF + 255) / 256; ++i) {
-        const int k = i * 256 + lane * 8, eb = __shfl_sync(0xFFFFFFFFu, mine, (k >> 5) & 31);
-        if (k < kF) {
-            const uint4 u = __ldcg(reinterpret_cast<const uint4 *>(act + row * kF + k));
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-            // a = f16 2^(eb - 141); over s: 2^(eb - e - 7)
-            const int d = eb - e - 7 + 127;
-            const float up = d > 0 ? __int_as_float(d << 23) : 0.0f;
-            float v[8];
+    for (int i = 0; i < kMine; ++i) {
+        const int b = i * 8 + warp;
+        u[i] = b < kBlocks ? __ldcg(a + b * 32) : make_uint4(0, 0, 0, 0);
+        eb[i] = b < kBlocks ? __ldcg(ex + b * 8) : 0;
+    }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[q]));
-                v[2 * q] = f.x * up;
-                v[2 * q + 1] = f.y * up;
-            }
-            write_terms(terms + row * (2 * kF), k, v);
+    for (int i = 0; i < (kBlocks + 3) / 4; ++i) {
+        const int b = i * 4 + (lane & 3);
+        e = max(e, b < kBlocks ? static_cast<int>(__ldcg(ex + b * 8)) : 0);
+    }
+    e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, 1));
+    e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, 2));
+    if (warp == 0 && (lane & 3) == 0)
+        scale[eight * 8 + r] = row_scale(e);
+    uint8_t *to = terms + (eight * 8 + r) * (2 * kF);
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int b = i * 8 + warp;
+        if (b >= kBlocks)
+            break;
+        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+        // a = f16 2^(eb - 141); over s: 2^(eb - e - 7)
+        const int d = eb[i] - e - 7 + 127;
+        const float up = d > 0 ? __int_as_float(d << 23) : 0.0f;
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[q]));
+            v[2 * q] = f.x * up;
+            v[2 * q + 1] = f.y * up;
         }
+        write_terms(to, b * 32 + (lane & 3) * 8, v);
     }
 }
 
-// A power of two that is not below any of an expert's scales (its absolute value), 1 for none.
-__global__ void __launch_bounds__(256) k_scale_max(const float *s, int n, float *smax)
+// A power of two that is not below any of an expert's n scales (their absolute values), 1 for none; by a CTA.
+__device__ __forceinline__ void scale_max(const float *s, int n, float *smax, int e)
 {
     __shared__ uint32_t part[8];
-    tc::after_previous();
-    tc::let_next_start();
     uint32_t m = 0;
+#pragma unroll 4
     for (int i = threadIdx.x; i < n; i += 256)
-        m = max(m, __float_as_uint(__ldcg(s + static_cast<int64_t>(blockIdx.x) * n + i)) & 0x7FFFFFFFu);
+        m = max(m, __float_as_uint(__ldcg(s + static_cast<int64_t>(e) * n + i)) & 0x7FFFFFFFu);
     m = __reduce_max_sync(0xFFFFFFFFu, m);
     if ((threadIdx.x & 31) == 0)
         part[threadIdx.x >> 5] = m;
@@ -302,8 +371,36 @@ __global__ void __launch_bounds__(256) k_scale_max(const float *s, int n, float 
         for (int w = 1; w < 8; ++w)
             m = max(m, part[w]);
         // (of scales beyond 2^126, infinite or NaN ones 2^127: what they give shows in the products)
-        const uint32_t e = (m >> 23) + 1;
-        smax[blockIdx.x] = m == 0 ? 1.0f : __uint_as_float((e > 254 ? 254 : e) << 23);
+        const uint32_t b = (m >> 23) + 1;
+        smax[e] = m == 0 ? 1.0f : __uint_as_float((b > 254 ? 254 : b) << 23);
+    }
+}
+
+// What the experts' products wait for, side by side: slots grouped (or counted, where
+// they take several CTAs), x as terms, the experts' largest down scales.
+struct PrepArgs {
+    GroupArgs group;
+    TermArgs terms;
+    const float *down_s;
+    float *smax;
+};
+
+__global__ void __launch_bounds__(256) k_prep(const PrepArgs p)
+{
+    extern __shared__ int hist[];
+    static_assert(kGroupThreads == 256 && kTermThreads == 256, "one block size");
+    tc::after_previous();
+    tc::let_next_start();
+    int b = blockIdx.x;
+    if (b < p.group.chunks) {
+        if (p.group.chunks == 1)
+            group_deal(p.group, 0, hist);
+        else
+            group_count(p.group, b, hist);
+    } else if ((b -= p.group.chunks) < kNE) {
+        scale_max(p.down_s, kH, p.smax, b);
+    } else {
+        row_terms(p.terms, static_cast<int64_t>(b - kNE) * (kTermThreads / kTermRow));
     }
 }
 
@@ -312,7 +409,6 @@ __global__ void __launch_bounds__(256) k_scale_max(const float *s, int n, float 
 // y_t = sum_k w_tk y[pos_tk] (+ the shared expert's row), k in order: rows of f16,
 // which grouped.cuh wrote as f16(a 2^-12 / (sa smax)).
 struct CombineArgs {
-    const uint16_t *rows;    // [.][2816] f16
     const float *sa;         // [.] scales of the activations' terms
     const float *smax;       // [129]
     const int32_t *ids;      // [T][8]
@@ -320,58 +416,119 @@ struct CombineArgs {
     const int32_t *pos;      // [T][8]
     const int32_t *offsets;  // [129] or more; the shared expert's rows begin at offsets[128]
     int shared;
+    int64_t T;
     uint16_t *y;             // [T][2816]
+    int32_t *status;
+    long long timeout_ns;
 };
 
-constexpr int kCombineThreads = kH / 8;
+// A CTA takes tokens in turn: one warp brings their rows, nine copies of 88 pieces of
+// 64 bytes a token (read by lanes, the pieces cost an SM 2.6 us a token: 428 us for
+// 16,381 where this takes 160), into a ring of four tokens; the others add them up.
+constexpr int kCombineThreads = kH / 8 + 32;
+constexpr int kCombineStages = 4;
+constexpr int kCombineStage = (kK + 1) * 2 * kH;
+constexpr int kCombineSmem = kCombineStages * kCombineStage + 128;
 
-__global__ void __launch_bounds__(kCombineThreads) k_combine(const CombineArgs p)
+__global__ void __launch_bounds__(kCombineThreads, 1) k_combine(const __grid_constant__ CUtensorMap rows, const CombineArgs p)
 {
+    extern __shared__ uint8_t dsm_raw[];
+    __shared__ unsigned long long full[kCombineStages], empty[kCombineStages];
+    __shared__ float factor[kCombineStages][kK + 1];
+    __shared__ uint32_t present[kCombineStages];
+    __shared__ int abort_;
+    const uint32_t ring = (tc::saddr(dsm_raw) + 127u) & ~127u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kCombineStages; ++i) {
+            tc::bar_init(&full[i], 1);
+            tc::bar_init(&empty[i], kH / 8 / 32);
+        }
+        abort_ = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
     tc::after_previous();
     tc::let_next_start();
-    const int64_t t = blockIdx.x;
-    const int k0 = threadIdx.x * 8;
-    uint4 u[kK + 1];
-    float f[kK + 1];
-#pragma unroll
-    for (int k = 0; k <= kK; ++k) {
-        int at = -1, e = kE;
-        float w = 1.0f;
-        if (k < kK) {
-            at = __ldcg(p.pos + t * kK + k);
-            if (at >= 0) {
-                e = __ldcg(p.ids + t * kK + k);
-                w = __ldcg(p.w + t * kK + k);
+    const tc::Waiter wait{&abort_, p.status, p.timeout_ns};
+    uint32_t n = 0;
+    if (warp == kH / 8 / 32) {
+        bool ok = true;
+        for (int64_t t = blockIdx.x; t < p.T && ok; t += gridDim.x, ++n) {
+            const uint32_t slot = n % kCombineStages;
+            // lane k: choice k's row, and what its elements are multiplied by; lane 8: the shared expert's
+            int at = -1, e = kE;
+            float w = 1.0f;
+            if (lane < kK) {
+                at = __ldcg(p.pos + t * kK + lane);
+                e = __ldcg(p.ids + t * kK + lane);
+                w = __ldcg(p.w + t * kK + lane);
+            } else if (lane == kK && p.shared) {
+                at = __ldcg(p.offsets + kE) + static_cast<int>(t);
             }
-        } else if (p.shared) {
-            at = __ldcg(p.offsets + kE) + static_cast<int>(t);
+            const float f = at >= 0 ? w * (__ldcg(p.sa + at) * (__ldcg(p.smax + e) * 4096.0f)) : 0.0f;
+            const uint32_t rows_of = __ballot_sync(0xFFFFFFFFu, at >= 0);
+            if (n >= kCombineStages)
+                ok = wait(&empty[slot], n / kCombineStages - 1, 44, static_cast<int>(t));
+            if (!(ok = __all_sync(0xFFFFFFFFu, ok)))
+                break;
+            const uint32_t bar = tc::saddr(&full[slot]);
+            if (lane <= kK)
+                factor[slot][lane] = f;
+            if (lane == 0)
+                present[slot] = rows_of;         // (without a row a place of the ring holds anything)
+            __syncwarp();
+            if (lane == 0)
+                tc::bar_expect(bar, __popc(rows_of) * 2 * kH);
+            __syncwarp();
+            if (at >= 0)
+                asm volatile(
+                    "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+                        ring + slot * kCombineStage + lane * 2 * kH),
+                    "l"(reinterpret_cast<uint64_t>(&rows)), "r"(0), "r"(at & 7), "r"(0), "r"(at >> 3), "r"(bar)
+                    : "memory");
         }
-        u[k] = make_uint4(0, 0, 0, 0);
-        f[k] = 0.0f;
-        if (at >= 0) {
-            u[k] = __ldcg(reinterpret_cast<const uint4 *>(p.rows + static_cast<int64_t>(at) * kH + k0));
-            f[k] = w * (__ldcg(p.sa + at) * (__ldcg(p.smax + e) * 4096.0f));
-        }
+        // every copy lands before the CTA ends
+        for (uint32_t i = n > kCombineStages ? n - kCombineStages : 0; i < n; ++i)
+            tc::bar_drain(tc::saddr(&full[i % kCombineStages]), (i / kCombineStages) & 1);
+        return;
     }
-    float o[8];
+    const int k0 = threadIdx.x * 8;
+    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, ++n) {
+        const uint32_t slot = n % kCombineStages;
+        if (!__all_sync(0xFFFFFFFFu, wait(&full[slot], n / kCombineStages, 45, static_cast<int>(t))))
+            break;
+        float o[8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-        o[q] = 0.0f;
+        for (int q = 0; q < 8; ++q)
+            o[q] = 0.0f;
+        const uint32_t rows_of = present[slot];
 #pragma unroll
-    for (int k = 0; k <= kK; ++k) {
-        const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+        for (int k = 0; k <= kK; ++k) {
+            if (!(rows_of >> k & 1))
+                continue;
+            const float f = factor[slot][k];
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(ring + slot * kCombineStage + k * 2 * kH + threadIdx.x * 16)
+                         : "memory");
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w[q]));
-            o[2 * q] = fmaf(f[k], v.x, o[2 * q]);
-            o[2 * q + 1] = fmaf(f[k], v.y, o[2 * q + 1]);
+            for (int q = 0; q < 4; ++q) {
+                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w[q]));
+                o[2 * q] = fmaf(f, v.x, o[2 * q]);
+                o[2 * q + 1] = fmaf(f, v.y, o[2 * q + 1]);
+            }
         }
-    }
-    uint32_t r[4];
+        __syncwarp();
+        if (lane == 0)
+            tc::bar_arrive(tc::saddr(&empty[slot]));
+        uint32_t r[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-        r[q] = f32_to_bf16(o[2 * q]) | static_cast<uint32_t>(f32_to_bf16(o[2 * q + 1])) << 16;
-    *reinterpret_cast<uint4 *>(p.y + t * kH + k0) = make_uint4(r[0], r[1], r[2], r[3]);
+        for (int q = 0; q < 4; ++q)
+            r[q] = f32_to_bf16(o[2 * q]) | static_cast<uint32_t>(f32_to_bf16(o[2 * q + 1])) << 16;
+        *reinterpret_cast<uint4 *>(p.y + t * kH + k0) = make_uint4(r[0], r[1], r[2], r[3]);
+    }
 }
 
 }  // namespace rows

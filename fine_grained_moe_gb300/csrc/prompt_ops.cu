@@ -48,14 +48,25 @@ size_t group_count_bytes(int64_t n, int E)
     return chunks > 1 ? sizeof(int32_t) * chunks * E : 0;
 }
 
-int launch_group(rows::GroupArgs a, cudaStream_t st)
+void cut_group(rows::GroupArgs &a)
 {
     a.chunk = group_chunk(a.n);
     a.chunks = static_cast<int>((a.n + a.chunk - 1) / a.chunk);
-    const size_t hist = sizeof(int) * rows::kGroupWarps * a.E;
+}
+
+size_t group_smem(int E) { return sizeof(int) * (rows::kGroupWarps + 1) * E; }
+
+int launch_deal(const rows::GroupArgs &a, cudaStream_t st)
+{
+    return launch_overlapped(rows::k_group_deal, dim3(a.chunks), rows::kGroupThreads, group_smem(a.E), st, a);
+}
+
+int launch_group(rows::GroupArgs a, cudaStream_t st)
+{
+    cut_group(a);
     if (a.chunks > 1)
-        FGM_HOST_TRY(launch_overlapped(rows::k_group_count, dim3(a.chunks), rows::kGroupThreads, hist, st, a));
-    return launch_overlapped(rows::k_group_deal, dim3(a.chunks), rows::kGroupThreads, hist + sizeof(int) * a.E, st, a);
+        FGM_HOST_TRY(launch_overlapped(rows::k_group_count, dim3(a.chunks), rows::kGroupThreads, group_smem(a.E), st, a));
+    return launch_deal(a, st);
 }
 
 // ---------------------------------------------------------------- routing
@@ -100,7 +111,7 @@ int x_maps(grouped::Maps &m, const void *x, int64_t row_bytes, int64_t stride_by
     const uint64_t dims[2] = {static_cast<uint64_t>(row_bytes), static_cast<uint64_t>(n)}, strides[1] = {static_cast<uint64_t>(stride_bytes)};
     for (int i = 0; i < (gathered ? 1 : 5); ++i) {
         const uint32_t box[2] = {128, gathered ? 1u : 8u << i};
-        FGM_HOST_TRY(host_map128(&m.x[i], x, 1, 2, dims, strides, box));
+        FGM_HOST_TRY(host_map(&m.x[i], x, 1, 2, dims, strides, box, true));
     }
     return FGM_OK;
 }
@@ -110,7 +121,7 @@ int weight_map(CUtensorMap *map, const void *w, int elem, int E, int N, int K)
     const uint64_t dims[3] = {static_cast<uint64_t>(K), static_cast<uint64_t>(N), static_cast<uint64_t>(E)},
                    strides[2] = {static_cast<uint64_t>(K) * elem, static_cast<uint64_t>(K) * elem * N};
     const uint32_t box[3] = {128u / elem, 128, 1};
-    return host_map128(map, w, elem, 3, dims, strides, box);
+    return host_map(map, w, elem, 3, dims, strides, box, true);
 }
 
 template <grouped::Mode MODE, bool BYTES>
@@ -148,11 +159,7 @@ int launch_grouped(const grouped::Maps &m, grouped::Args a, int sms, cudaStream_
     return launch_overlapped(kernel, dim3(static_cast<unsigned>(2 * pairs)), a.src ? grouped::kGatherThreads : grouped::kThreads, kSmem, st, m, a);
 }
 
-int launch_terms(const uint16_t *x, int64_t stride, int64_t n, int K, uint8_t *terms, float *scale, cudaStream_t st)
-{
-    return launch_overlapped(rows::k_terms, dim3(static_cast<unsigned>((n + rows::kTermWarps - 1) / rows::kTermWarps)), 32 * rows::kTermWarps, 0,
-                             st, x, stride, n, K, terms, scale);
-}
+constexpr int kTermRows = rows::kTermThreads / rows::kTermRow;
 
 bool gemm_sizes_ok(int64_t x_rows, int64_t R, int E, int N, int K)
 {
@@ -175,15 +182,23 @@ GemmWs gemm_ws(int64_t x_rows, int K)
 }
 
 struct ExpertsWs {
-    size_t offsets, src, pos, count, terms, xs, exps, act_terms, sa, rows, smax, total;
+    size_t offsets, counts, src, pos, count, terms, xs, exps, act_terms, sa, rows, smax, total;
 };
+
+// Places of T tokens' slots, an expert's beginning at a multiple of 8.
+int64_t experts_rows(int64_t T)
+{
+    const int64_t active = T * kK < kE ? T * kK : kE;
+    return static_cast<int64_t>(align_up(T * kK + 7 * active + T, 8));
+}
 
 ExpertsWs experts_ws(int64_t T)
 {
     ExpertsWs o;
     Carve c;
-    const int64_t R = T * (kK + 1);
+    const int64_t R = experts_rows(T);
     o.offsets = c.take(sizeof(int32_t) * (kE + 2));
+    o.counts = c.take(sizeof(int32_t) * (kE + 1));
     o.src = c.take(sizeof(int32_t) * R);
     o.pos = c.take(sizeof(int32_t) * T * kK);
     o.count = c.take(group_count_bytes(T * kK, kE));
@@ -251,8 +266,8 @@ int fgm_moe_route(const uint16_t *router_w, const float *router_b, const uint16_
     CUtensorMap xmap, wmap;
     const uint64_t xdims[2] = {kH, static_cast<uint64_t>(T)}, xstr[1] = {2 * static_cast<uint64_t>(x_stride)}, wdims[2] = {kH, kE}, wstr[1] = {2 * kH};
     const uint32_t box[2] = {64, 128};
-    FGM_HOST_TRY(host_map128(&xmap, x, 2, 2, xdims, xstr, box));
-    FGM_HOST_TRY(host_map128(&wmap, router_w, 2, 2, wdims, wstr, box));
+    FGM_HOST_TRY(host_map(&xmap, x, 2, 2, xdims, xstr, box, true));
+    FGM_HOST_TRY(host_map(&wmap, router_w, 2, 2, wdims, wstr, box, true));
     static std::atomic<bool> ready[64];          // per device; setting it twice does no harm
     int dev = 0;
     FGM_HOST_CUDA(cudaGetDevice(&dev));
@@ -356,7 +371,8 @@ int fgm_grouped_gemm(const uint16_t *x, int64_t x_stride, int64_t x_rows, const 
     const int64_t row = 2 * static_cast<int64_t>(bytes ? align_up(K, 32) : K);
     FGM_HOST_TRY(x_maps(m, bytes ? region<void>(ws, o.terms) : static_cast<const void *>(x), row, bytes ? row : 2 * x_stride, x_rows, src != nullptr));
     if (bytes)
-        FGM_HOST_TRY(launch_terms(x, x_stride, x_rows, K, region<uint8_t>(ws, o.terms), region<float>(ws, o.xs), st));
+        FGM_HOST_TRY(launch_overlapped(rows::k_terms, dim3(static_cast<unsigned>((x_rows + kTermRows - 1) / kTermRows)), rows::kTermThreads, 0, st,
+                                       rows::TermArgs{x, x_stride, x_rows, K, region<uint8_t>(ws, o.terms), region<float>(ws, o.xs)}));
     grouped::Args a = {};
     a.offsets = offsets;
     a.E = E;
@@ -403,7 +419,7 @@ int fgm_moe_experts_fwd(const fgm_layer *layer, const uint16_t *x, int64_t x_str
     FGM_HOST_TRY(host_device_ready(&sms));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int E = shared ? kNE : kE;
-    const int64_t R = T * (shared ? kK + 1 : kK);
+    const int64_t R = experts_rows(T);
     grouped::Maps up, down;
     FGM_HOST_TRY(weight_map(&up.w, layer->gate_q, 1, kNE, kF, kH));
     FGM_HOST_TRY(weight_map(&up.w2, layer->up_q, 1, kNE, kF, kH));
@@ -412,7 +428,13 @@ int fgm_moe_experts_fwd(const fgm_layer *layer, const uint16_t *x, int64_t x_str
     FGM_HOST_TRY(x_maps(up, region<void>(ws, o.terms), 2 * kH, 2 * kH, T, true));
     FGM_HOST_TRY(x_maps(down, region<void>(ws, o.act_terms), 2 * kF, 2 * kF, R, false));
 
-    rows::GroupArgs g = {};
+    CUtensorMap rmap;
+    const uint64_t rdims[4] = {2 * 32, 8, kH / 32, static_cast<uint64_t>(R / 8)}, rstr[3] = {64, 512, 16 * kH};
+    const uint32_t rbox[4] = {2 * 32, 1, kH / 32, 1};
+    FGM_HOST_TRY(host_map(&rmap, region<void>(ws, o.rows), 1, 4, rdims, rstr, rbox, false));
+
+    rows::PrepArgs prep = {};
+    rows::GroupArgs &g = prep.group;
     g.ids = ids;
     g.n = T * kK;
     g.E = kE;
@@ -422,12 +444,19 @@ int fgm_moe_experts_fwd(const fgm_layer *layer, const uint16_t *x, int64_t x_str
     g.pos = region<int32_t>(ws, o.pos);
     g.per = kK;
     g.shared = shared ? static_cast<int>(T) : 0;
-    FGM_HOST_TRY(launch_group(g, st));
-    FGM_HOST_TRY(launch_overlapped(rows::k_scale_max, dim3(kNE), 256, 0, st, layer->down_s, static_cast<int>(kH), region<float>(ws, o.smax)));
-    FGM_HOST_TRY(launch_terms(x, x_stride, T, kH, region<uint8_t>(ws, o.terms), region<float>(ws, o.xs), st));
+    g.counts = region<int32_t>(ws, o.counts);
+    cut_group(g);
+    prep.terms = rows::TermArgs{x, x_stride, T, kH, region<uint8_t>(ws, o.terms), region<float>(ws, o.xs)};
+    prep.down_s = layer->down_s;
+    prep.smax = region<float>(ws, o.smax);
+    FGM_HOST_TRY(launch_overlapped(rows::k_prep, dim3(static_cast<unsigned>(g.chunks + kNE + (T + kTermRows - 1) / kTermRows)), 256, group_smem(kE), st,
+                                   prep));
+    if (g.chunks > 1)
+        FGM_HOST_TRY(launch_deal(g, st));
 
     grouped::Args a = {};
     a.offsets = g.offsets;
+    a.counts = g.counts;
     a.E = E;
     a.R = R;
     a.src = g.src;
@@ -441,12 +470,11 @@ int fgm_moe_experts_fwd(const fgm_layer *layer, const uint16_t *x, int64_t x_str
     a.out = region<uint16_t>(ws, o.rows);
     a.wide = 1;
     a.exps = region<uint8_t>(ws, o.exps);
-    a.cols = tile_cols(R, E, 128);
+    a.cols = tile_cols(T * kK, E, 128);
     a.status = status_word(ws);
     a.timeout_ns = host_wait_limit_ns();
     FGM_HOST_TRY((launch_grouped<grouped::kGated, true>(up, a, sms, st)));
-    FGM_HOST_TRY(launch_overlapped(rows::k_act_terms, dim3(static_cast<unsigned>((R + rows::kTermWarps - 1) / rows::kTermWarps)),
-                                   32 * rows::kTermWarps, 0, st, static_cast<const uint16_t *>(a.out), static_cast<const uint8_t *>(a.exps),
+    FGM_HOST_TRY(launch_overlapped(rows::k_act_terms, dim3(static_cast<unsigned>(R / 8)), 256, 0, st, static_cast<const uint16_t *>(a.out), static_cast<const uint8_t *>(a.exps),
                                    a.offsets + E, region<uint8_t>(ws, o.act_terms), region<float>(ws, o.sa)));
     grouped::Args d = a;
     d.src = nullptr;
@@ -458,10 +486,17 @@ int fgm_moe_experts_fwd(const fgm_layer *layer, const uint16_t *x, int64_t x_str
     d.xs = nullptr;
     d.exps = nullptr;
     d.smax = region<float>(ws, o.smax);
-    d.cols = tile_cols(R, E, 256);
+    d.cols = tile_cols(T * kK, E, 256);
     FGM_HOST_TRY((launch_grouped<grouped::kDown, true>(down, d, sms, st)));
-    const rows::CombineArgs c{d.out, region<float>(ws, o.sa), d.smax, ids, w, g.pos, g.offsets, shared ? 1 : 0, y};
-    return launch_overlapped(rows::k_combine, dim3(static_cast<unsigned>(T)), rows::kCombineThreads, 0, st, c);
+    const rows::CombineArgs c{region<float>(ws, o.sa), d.smax, ids, w, g.pos, g.offsets, shared ? 1 : 0, T, y, a.status, a.timeout_ns};
+    static std::atomic<bool> ready[64];          // per device; setting it twice does no harm
+    int dev = 0;
+    FGM_HOST_CUDA(cudaGetDevice(&dev));
+    if (!ready[dev & 63]) {
+        FGM_HOST_CUDA(cudaFuncSetAttribute(rows::k_combine, cudaFuncAttributeMaxDynamicSharedMemorySize, rows::kCombineSmem));
+        ready[dev & 63] = true;
+    }
+    return launch_overlapped(rows::k_combine, dim3(static_cast<unsigned>(T < sms ? T : sms)), rows::kCombineThreads, rows::kCombineSmem, st, rmap, c);
 }
 
 }  // extern "C"

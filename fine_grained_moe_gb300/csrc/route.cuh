@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 64; j += 8) {
                     uint32_t u[8];
-                    tc::read8(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * 128 + side * 64 + j, u);
+                    tc::read(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * 128 + side * 64 + j, u);
                     tc::read_wait();
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {

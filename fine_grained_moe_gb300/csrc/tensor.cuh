@@ -185,13 +185,23 @@ __device__ __forceinline__ void commit(unsigned long long *bar)
     asm volatile("tcgen05.commit.cta_group::%1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(bar)), "n"(G) : "memory");
 }
 
-// Eight columns of this warp's 32 lanes.
-__device__ __forceinline__ void read8(uint32_t at, uint32_t (&u)[8])
+// Eight columns of this warp's 32 lanes, or sixteen.
+__device__ __forceinline__ void read(uint32_t at, uint32_t (&u)[8])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
                  : "r"(at)
                  : "memory");
+}
+
+__device__ __forceinline__ void read(uint32_t at, uint32_t (&u)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]), "=r"(u[9]),
+          "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(at)
+        : "memory");
 }
 
 __device__ __forceinline__ void read_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
