@@ -20,14 +20,19 @@
 namespace fgm {
 namespace grouped {
 
-constexpr int kThreads = 384;                    // copies, products, -, -, eight epilogue warps,
-constexpr int kGatherThreads = 576;              // six more where rows are gathered: with the idle two, eight that copy rows
-constexpr int kGatherWarps = 8;
+constexpr int kSides = 4;                        // epilogue warps of a 32-lane quarter, which share out its columns
+constexpr int kEpilogue = 4 * kSides;
+constexpr int kThreads = 128 + 32 * kEpilogue;   // weights, products, rows (two warps), epilogue,
+constexpr int kGatherThreads = kThreads + 128;   // and four more warps for rows where they are gathered
+constexpr int kGatherWarps = 6;
 constexpr int kMaxStages = 12;
 constexpr int kMaxExperts = 1024;
 constexpr int kStageK = 128;                     // elements of K in a stage
 constexpr int kBox = 128 * 128;                  // 128 weight rows x 128 bytes
-constexpr int kRing = 208 * 1024;                // bytes of the ring at most
+constexpr int kRing = 192 * 1024;                // bytes of the ring at most
+constexpr int kOutBuf = 8 * 256;                 // eight rows of 128 features on their way out, twice for each side
+constexpr int kOutBytes = kSides * 2 * kOutBuf;
+constexpr int kSmem = kRing + kOutBytes + 1024;
 
 enum Mode {
     kGemm = 0,   // out[r][n] = bf16(s[n] xs[r] D)
@@ -35,14 +40,8 @@ enum Mode {
     kDown = 2,   // y[r][n] = f16(s[n] / smax[e] 2^-12 D)
 };
 
-// What kGated and kDown write lies in blocks of 8 rows x 32 features, 512 bytes that a
-// warp stores at once: row-major rows get 64 bytes from each warp, which cost it 50
-// cycles per 512 bytes instead of 18. Their experts' rows begin at multiples of 8.
-__device__ __forceinline__ int64_t blocked(int64_t row, int n, int N) { return ((row >> 3) * (N >> 5) + (n >> 5)) * 256 + (row & 7) * 32 + (n & 31); }
-
 struct Args {
     const int32_t *offsets;  // [E + 1]
-    const int32_t *counts;   // [E] rows of each expert, or NULL: up to the next one's
     int E;
     int64_t R;               // rows at most
     const int32_t *src;      // row r takes x row src[r] / per; NULL: x row r
@@ -51,11 +50,11 @@ struct Args {
     int N, K;
     const float *s0, *s1;    // [E][N] row scales (gate and up), or NULL
     const float *xs;         // [x_rows] scales of the terms
-    uint16_t *out;           // [R][N], or blocked
-    uint8_t *exps;           // kGated: exponents [R / 8][N / 32][8]
+    uint16_t *out;           // [R][N]
+    uint8_t *exps;           // kGated: [R][N / 32] exponents
     const float *smax;       // kDown: [E] a power of two not below the expert's scales
     int wide;                // 16-byte stores to out
-    int cols;                // rows of a tile at most, a multiple of 32
+    int cols, log_cols;      // rows of a tile at most: a power of two, 32 to 256
     int stages;
     int32_t *status;
     long long timeout_ns;
@@ -106,26 +105,6 @@ __device__ __forceinline__ void copy_gathered(uint32_t dst, const CUtensorMap *m
         : "memory");
 }
 
-// 16-bit values of a feature a lane and eight rows, two rows a word, to eight features
-// of one row a lane: lane l gets row l & 7, features (l >> 3) * 8 .. + 7.
-__device__ __forceinline__ uint4 transposed(const uint32_t (&p)[4], int lane)
-{
-    uint32_t q[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {                // features in pairs: even lanes keep the first row of two
-        const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, p[i], 1);
-        q[i] = __byte_perm(p[i], o, lane & 1 ? 0x3276 : 0x5410);
-    }
-    uint2 r[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {                // in fours
-        const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, lane & 2 ? q[2 * i] : q[2 * i + 1], 2);
-        r[i] = lane & 2 ? make_uint2(o, q[2 * i + 1]) : make_uint2(q[2 * i], o);
-    }
-    const uint32_t x = __shfl_xor_sync(0xFFFFFFFFu, lane & 4 ? r[0].x : r[1].x, 4), y = __shfl_xor_sync(0xFFFFFFFFu, lane & 4 ? r[0].y : r[1].y, 4);
-    return lane & 4 ? make_uint4(x, y, r[1].x, r[1].y) : make_uint4(r[0].x, r[0].y, x, y);
-}
-
 // gelu_tanh (common.cuh) as x times a sigmoid: 0.5 (1 + tanh z) = 1 / (1 + exp(-2 z)).
 __device__ __forceinline__ float gelu(float x)
 {
@@ -168,6 +147,23 @@ struct RowBoxes {
     __device__ __forceinline__ int rows() const { return (8 << first) + (second < 0 ? 0 : 8 << second); }
 };
 
+// Whether all four warps of a side say so, and the same without a question.
+__device__ __forceinline__ bool side_all(int side, bool yes)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(yes)), "r"(1 + side)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ void side_sync(int side) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + side) : "memory"); }
+
+// A feature's value of a row (its low or high half) to shared memory.
+__device__ __forceinline__ void put16(uint32_t at, uint32_t v) { asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(v)) : "memory"); }
+
 // A tile: rows [r0, r0 + live) of expert e against 256 of its output features (of
 // each product) from n0 on. A pair's items come in ascending order.
 struct Tile {
@@ -177,13 +173,14 @@ struct Tile {
     {
         while (item >= sh.cum[e + 1])
             ++e;
-        const int c = sh.count[e], nt = (c + p.cols - 1) / p.cols, across = (p.N + 255) / 256, local = item - sh.cum[e], n = local / across;
+        const unsigned c = sh.count[e], nt = (c + p.cols - 1) >> p.log_cols, across = (p.N + 255u) >> 8, local = item - sh.cum[e],
+                       n = local / across;
         n0 = (local - n * across) * 256;
         // (the expert's eights of rows, shared out)
-        const int eights = (c + 7) / 8, a = static_cast<int>(static_cast<int64_t>(eights) * n / nt) * 8,
-                  b = static_cast<int>(static_cast<int64_t>(eights) * (n + 1) / nt) * 8;
-        r0 = sh.row0[e] + a;
-        live = (b < c ? b : c) - a;
+        const unsigned eights = (c + 7) >> 3, each = eights / nt, more = eights - each * nt, a = n * each + min(n, more),
+                       b = a + each + (n < more);
+        r0 = sh.row0[e] + a * 8;
+        live = min(b * 8, c) - a * 8;
     }
 
     // columns of the products in each CTA's half of the second operand
@@ -209,7 +206,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
         }
         for (int i = 0; i < 2; ++i) {
             tc::bar_init(&sh.tfull[i], 1);
-            tc::bar_init(&sh.tempty[i], 16);     // the epilogue warps of both CTAs
+            tc::bar_init(&sh.tempty[i], 2 * kEpilogue);      // of both CTAs
         }
         tc::bar_init(&sh.drained, 1);
         sh.abort = 0;
@@ -229,12 +226,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
             for (int i = 0; i < kAhead; ++i) {
                 const int e = e1 + i * 32 + lane;
                 from[i] = e < p.E ? __ldcg(p.offsets + e) : 0;
-                to[i] = e < p.E ? __ldcg(p.counts ? p.counts + e : p.offsets + e + 1) : 0;
+                to[i] = e < p.E ? __ldcg(p.offsets + e + 1) : 0;
             }
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 const int e = e1 + i * 32 + lane;
-                int64_t a = from[i], b = p.counts ? a + to[i] : to[i];
+                int64_t a = from[i], b = to[i];
                 a = a < 0 ? 0 : a > p.R ? p.R : a;
                 b = b < a ? a : b > p.R ? p.R : b;
                 int sum = (static_cast<int>(b - a) + p.cols - 1) / p.cols * across;
@@ -357,10 +354,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
             }
             __syncwarp();
         }
-    } else if (warp < 4 || warp >= 12) {
+    } else if (warp < 4 || warp >= 4 + kEpilogue) {
         // ------------------------------------------------------------ rows: gathered ones four a copy, a lane's of one half of K; else boxes
         if (p.src) {
-            const int mate = warp < 4 ? warp - 2 : warp - 10, h = lane & 1, group = (lane >> 1) * kGatherWarps + mate;
+            const int mate = warp < 4 ? warp - 2 : warp - kEpilogue - 2, h = lane & 1, group = (lane >> 1) * kGatherWarps + mate;
             bool ok = true;
             uint32_t n = 0;
             Place place;
@@ -411,20 +408,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
         }
     } else {
         // ------------------------------------------------------------ epilogue: a lane is an output feature, a column a row of x
+        // (columns by eights, a side's each fourth: with two sides, what a warp waits for itself took longer than the products)
         const int quarter = warp & 3, side = (warp - 4) >> 2;
+        constexpr int kEights = (MODE == kGated ? 128 : 256) / 8 / kSides;
+        const uint32_t out0 = ring + kRing + side * 2 * kOutBuf, put_at = out0 + quarter * 64 + lane * 2,
+                       take_at = out0 + quarter * 512 + lane * 16;
+        uint32_t outs = 0;
         bool alive = true;
         uint32_t tile = 0;
         for (int item = pair; item < items; item += pairs, ++tile) {
             t.find(sh, p, item);
             const uint32_t buf = tile & 1;
-            const int half = t.half(), c0 = side * half, nw = t.n0 + rank * 128 + quarter * 32, n = nw + lane;
-            // what the columns and lanes are multiplied by, on its way while the products end
-            float xs[4], s0 = 1.0f, s1 = 1.0f;
+            const int n0 = t.n0 + rank * 128, nw = n0 + quarter * 32, n = nw + lane;
+            // what rows (those of this lane, see below) and features are multiplied by, on its way while the products end
+            float xs[kEights], s0 = 1.0f, s1 = 1.0f;
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int c = c0 + g * 32 + lane;
-                xs[g] = 1.0f;
-                if (MODE != kDown && g * 32 < half && g * 32 + lane < half && c < t.live) {
+            for (int i = 0; i < kEights; ++i) {
+                const int c = (i * kSides + side) * 8 + (MODE == kGated ? lane & 7 : quarter * 2 + (lane >> 4));
+                xs[i] = 1.0f;
+                if (MODE != kDown && c < t.live) {
                     int row = t.r0 + c;
                     bool there = true;
                     if (p.src) {
@@ -433,7 +435,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
                         row = there ? row / p.per : 0;
                     }
                     // (negative: no such row of x, the output is zero)
-                    xs[g] = there ? (BYTES ? __ldcg(p.xs + row) : 1.0f) : -1.0f;
+                    xs[i] = there ? (BYTES ? __ldcg(p.xs + row) : 1.0f) : -1.0f;
                 }
             }
             if (n < p.N && p.s0) {
@@ -445,34 +447,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
                 s0 *= 0x1p-12f / __ldcg(p.smax + t.e);
             if (alive)
                 alive = wait(&sh.tfull[buf], tile >> 1, 37, t.e);
-            alive = __all_sync(0xFFFFFFFFu, alive);
+            alive = side_all(side, alive);       // (a side's warps meet at barriers below)
             tc::fence_after();
-            if (alive && nw < p.N) {
-                const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * 256 + c0;
-                constexpr int kCols = MODE == kGated ? 8 : 16;
-                uint32_t u[2][kCols], v[2][kCols];
-                const int many = min(half, t.live - c0);     // columns of this warp
-                auto read = [&](int c, uint32_t (&u)[kCols], uint32_t (&v)[kCols]) {
+            if (alive && n0 < p.N) {
+                const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * 256;
+                auto read = [&](int c, uint32_t (&u)[8], uint32_t (&v)[8]) {
                     tc::read(from + c, u);
                     if (MODE == kGated)
                         tc::read(from + 128 + c, v);
                 };
-                // eight columns; xg: the scales of columns c & ~31 .. c | 31, a lane each
-                auto eight = [&](int c, float xg, const uint32_t *u, const uint32_t *v) {
-                    uint32_t pk[4];
-                    int e_mine = 0;
+                // this side's eights, the next on its way meanwhile
+                uint32_t u[2][8], v[2][8];
+                if (side * 8 < t.live)
+                    read(side * 8, u[0], v[0]);
+#pragma unroll
+                for (int i = 0; i < kEights; ++i) {
+                    const int c = (i * kSides + side) * 8;
+                    if (c >= t.live)
+                        break;
+                    const uint32_t ob = (outs++ & 1) * kOutBuf;
+                    __syncwarp();
+                    tc::read_wait();
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        asm volatile("" : "+r"(u[i & 1][q]));
+                        if (MODE == kGated)
+                            asm volatile("" : "+r"(v[i & 1][q]));
+                    }
+                    if (i + 1 < kEights && c + kSides * 8 < t.live)
+                        read(c + kSides * 8, u[(i + 1) & 1], v[(i + 1) & 1]);
+                    uint32_t pk[4];              // eight rows of this lane's feature, in 16 bits
                     if (MODE == kGated) {
                         float a[8];
+                        int e_mine = 0;
 #pragma unroll
                         for (int q = 0; q < 8; ++q) {
-                            const float x = __shfl_sync(0xFFFFFFFFu, xg, (c & 24) + q);
-                            a[q] = gelu(__uint_as_float(u[q]) * s0 * x) * (__uint_as_float(v[q]) * s1 * x);
+                            const float x = __shfl_sync(0xFFFFFFFFu, xs[i], q);
+                            a[q] = gelu(__uint_as_float(u[i & 1][q]) * s0 * x) * (__uint_as_float(v[i & 1][q]) * s1 * x);
                             // |a| < 2^(e - 126) for all 32: below 2^15 in f16, which has 11 bits down to 2^-14
                             int e = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(a[q]) & 0x7FFFFFFFu) >> 23);
                             e = e < 14 ? 14 : e;
                             e_mine = (lane & 7) == q ? e : e_mine;
                             a[q] *= __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
                         }
+                        if (lane < 8 && c + lane < t.live && nw < p.N)
+                            p.exps[static_cast<int64_t>(t.r0 + c + lane) * (p.N >> 5) + (nw >> 5)] = static_cast<uint8_t>(e_mine);
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const __half2 h = __floats2half2_rn(a[2 * q], a[2 * q + 1]);
@@ -481,7 +500,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
                     } else {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const float a = __uint_as_float(u[2 * q]) * s0, b = __uint_as_float(u[2 * q + 1]) * s0;
+                            const float a = __uint_as_float(u[i & 1][2 * q]) * s0, b = __uint_as_float(u[i & 1][2 * q + 1]) * s0;
                             if (MODE == kDown) {
                                 const __half2 h = __floats2half2_rn(a, b);
                                 pk[q] = *reinterpret_cast<const uint32_t *>(&h);
@@ -491,26 +510,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
                             }
                         }
                     }
-                    const uint4 o = transposed(pk, lane);
-                    const int64_t row = t.r0 + c0 + c;
-                    if (MODE != kGemm) {
-                        // (rows of the eight behind the expert's last are its own too)
-                        *reinterpret_cast<uint4 *>(p.out + blocked(row, nw, p.N) + (lane & 7) * 32 + (lane >> 3) * 8) = o;
-                        if (MODE == kGated && lane < 8)
-                            p.exps[((row >> 3) * (p.N >> 5) + (nw >> 5)) * 8 + lane] = static_cast<uint8_t>(e_mine);
-                        return;
+                    // The side's four warps lay 128 features of eight rows side by side, and each takes two rows of
+                    // them out again: whole lines, where a warp's own 32 features are 64 bytes of a row (50
+                    // cycles a store of 512 bytes instead of 18).
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        put16(put_at + ob + 2 * q * 256, pk[q]);
+                        put16(put_at + ob + (2 * q + 1) * 256, pk[q] >> 16);
                     }
-                    // (a row's scale is a power of two: it may follow the rounding)
-                    const float x = __shfl_sync(0xFFFFFFFFu, xg, (c & 24) + (lane & 7));
-                    auto scaled = [&](uint32_t w) {
-                        const float2 f = bf16x2_to_f32(w);
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(f.x * x, f.y * x);
-                        return x < 0.0f ? 0u : *reinterpret_cast<const uint32_t *>(&h);
-                    };
-                    if (c + (lane & 7) < many) {
-                        const uint32_t w[4] = {scaled(o.x), scaled(o.y), scaled(o.z), scaled(o.w)};
-                        const int first = nw + (lane >> 3) * 8;
-                        uint16_t *to = p.out + (row + (lane & 7)) * p.N + first;
+                    side_sync(side);
+                    uint32_t w[4];
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                 : "r"(take_at + ob)
+                                 : "memory");
+                    if (MODE == kGemm) {
+                        // (a row's scale is a power of two: it may follow the rounding)
+                        const __nv_bfloat162 x2 = __float2bfloat162_rn(xs[i]);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            if (BYTES) {
+                                const __nv_bfloat162 h = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&w[q]), x2);
+                                w[q] = *reinterpret_cast<const uint32_t *>(&h);
+                            }
+                            w[q] = xs[i] < 0.0f ? 0u : w[q];
+                        }
+                    }
+                    const int r = c + quarter * 2 + (lane >> 4), first = n0 + (lane & 15) * 8;
+                    if (r < t.live) {
+                        uint16_t *to = p.out + static_cast<int64_t>(t.r0 + r) * p.N + first;
                         if (p.wide) {
                             if (first < p.N)
                                 *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -521,34 +549,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
                                     to[q] = static_cast<uint16_t>(q & 1 ? w[q >> 1] >> 16 : w[q >> 1]);
                         }
                     }
-                };
-                // kCols columns, the next on their way meanwhile
-                auto columns = [&](int c, float xg, uint32_t (&u)[kCols], uint32_t (&v)[kCols], uint32_t (&u1)[kCols], uint32_t (&v1)[kCols]) {
-                    __syncwarp();
-                    tc::read_wait();
-#pragma unroll
-                    for (int q = 0; q < kCols; ++q) {
-                        asm volatile("" : "+r"(u[q]));
-                        if (MODE == kGated)
-                            asm volatile("" : "+r"(v[q]));
-                    }
-                    if (c + kCols < many)
-                        read(c + kCols, u1, v1);
-                    eight(c, xg, u, v);
-                    if (kCols == 16 && (MODE == kGemm || c + 8 < many))
-                        eight(c + 8, xg, u + 8, v + 8);
-                };
-                if (many > 0)
-                    read(0, u[0], v[0]);
-#pragma unroll
-                for (int g = 0; g < 4; ++g)
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2 * kCols)
-                        if (g * 32 + j < many) {
-                            columns(g * 32 + j, xs[g], u[0], v[0], u[1], v[1]);
-                            if (g * 32 + j + kCols < many)
-                                columns(g * 32 + j + kCols, xs[g], u[1], v[1], u[0], v[0]);
-                        }
+                }
             }
             tc::fence_before();
             __syncwarp();

@@ -33,7 +33,6 @@ struct GroupArgs {
     int32_t *pos;            // [n] each slot's place, -1 without an expert, or NULL
     int per;                 // slots of a token
     int shared;              // tokens that one more expert takes behind the others (offsets has E + 2 entries), 0: none
-    int32_t *counts;         // [E], or [E + 1] with `shared`, and experts begin at multiples of 8; or NULL: they follow each other
 };
 
 // Counts of a warp's run of slots in its own row of hist.
@@ -102,10 +101,7 @@ __device__ __forceinline__ void group_deal(const GroupArgs &p, int chunk, int *h
             hist[w * p.E + e] = before + mine;
             mine += v;
         }
-        all = p.chunks > 1 ? all : mine;
-        if (p.counts && chunk == 0)
-            p.counts[e] = all;
-        total[e] = p.counts ? (all + 7) & ~7 : all;
+        total[e] = p.chunks > 1 ? all : mine;
     }
     __syncthreads();
     // places before each expert: a thread scans E / 256 experts, rounded up
@@ -137,10 +133,8 @@ __device__ __forceinline__ void group_deal(const GroupArgs &p, int chunk, int *h
         all += warp_sum[w];
     if (chunk == 0 && threadIdx.x == 0) {
         p.offsets[p.E] = all;
-        if (p.shared) {
+        if (p.shared)
             p.offsets[p.E + 1] = all + p.shared;
-            p.counts[p.E] = p.shared;
-        }
     }
     __syncthreads();
     int *at = hist + warp * p.E;
@@ -226,8 +220,10 @@ __device__ __forceinline__ void write_terms(uint8_t *row, int k, const float *v)
 __device__ __forceinline__ float row_scale(int e) { return e == 255 ? __int_as_float(0x7FC00000) : __int_as_float((e - 7) << 23); }
 
 constexpr int kTermThreads = 256;
-constexpr int kTermRow = 128;                    // threads of a row
-constexpr int kTermHeld = 4;                     // vectors of 8 that each holds (longer rows are read twice)
+constexpr int kTermHeld = 4;                     // vectors of 8 that a thread holds (longer rows are read twice)
+
+// Threads of a row: a warp up to 1,024 elements, else four.
+__host__ __device__ __forceinline__ int term_row(int K) { return K <= 32 * 8 * kTermHeld ? 32 : 128; }
 
 struct TermArgs {
     const uint16_t *x;       // bf16 rows of K, `stride` apart
@@ -237,13 +233,14 @@ struct TermArgs {
     float *scale;            // [n]
 };
 
-// Two rows of bf16 by a CTA, from row0 on. All of a row is on its way before its
-// largest element is known.
-__device__ __forceinline__ void row_terms(const TermArgs &p, int64_t row0)
+// Eight or two rows of bf16, the CTA's `part`th of them. All of a row is on its way
+// before its largest element is known.
+template <int kTermRow>
+__device__ __forceinline__ void row_terms(const TermArgs &p, int64_t part)
 {
     __shared__ uint32_t most[kTermThreads / 32];
     const int t = threadIdx.x % kTermRow, warp = threadIdx.x >> 5, K32 = (p.K + 31) & ~31;
-    const int64_t row = row0 + threadIdx.x / kTermRow;
+    const int64_t row = part * (kTermThreads / kTermRow) + threadIdx.x / kTermRow;
     const uint16_t *xr = p.x + row * p.stride;
     uint4 u[kTermHeld];
     uint32_t m = 0;
@@ -263,12 +260,14 @@ __device__ __forceinline__ void row_terms(const TermArgs &p, int64_t row0)
     for (int k = (kTermHeld * kTermRow + t) * 8; k < p.K; k += kTermRow * 8)
         largest(take(k));
     m = __reduce_max_sync(0xFFFFFFFFu, m);
-    if ((threadIdx.x & 31) == 0)
-        most[warp] = m;
-    __syncthreads();
+    if (kTermRow > 32) {
+        if ((threadIdx.x & 31) == 0)
+            most[warp] = m;
+        __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kTermRow / 32; ++w)
-        m = max(m, most[(warp & ~(kTermRow / 32 - 1)) + w]);
+        for (int w = 0; w < kTermRow / 32; ++w)
+            m = max(m, most[(warp & ~(kTermRow / 32 - 1)) + w]);
+    }
     if (row >= p.n)
         return;
     int e = static_cast<int>(m >> 7);
@@ -300,49 +299,38 @@ __global__ void __launch_bounds__(kTermThreads) k_terms(const TermArgs p)
 {
     tc::after_previous();
     tc::let_next_start();
-    row_terms(p, static_cast<int64_t>(blockIdx.x) * (kTermThreads / kTermRow));
+    if (term_row(p.K) == 32)
+        row_terms<32>(p, blockIdx.x);
+    else
+        row_terms<128>(p, blockIdx.x);
 }
 
-// Rows of the gated activations (grouped.cuh: f16 under a power of two per 32, in blocks
-// of 8 rows x 32), eight of them a CTA, a block a warp at a time; only those of some
-// expert, and those that fill an expert's last eight, which nobody reads.
-__global__ void __launch_bounds__(256) k_act_terms(const uint16_t *act, const uint8_t *exps, const int32_t *n, uint8_t *terms, float *scale)
+// Rows of the gated activations (grouped.cuh: f16 under a power of two per 32), a
+// warp each; only those of some expert.
+__global__ void __launch_bounds__(kTermThreads) k_act_terms(const uint16_t *act, const uint8_t *exps, const int32_t *n, uint8_t *terms,
+                                                            float *scale)
 {
-    constexpr int kBlocks = kF / 32, kMine = (kBlocks + 7) / 8;
-    const int64_t eight = blockIdx.x;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2;
+    constexpr int kBlocks = kF / 32, kMine = (kF / 8 + 31) / 32;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kTermThreads / 32) + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
     tc::after_previous();
     tc::let_next_start();
-    if (eight * 8 >= __ldcg(n))
+    if (row >= __ldcg(n))
         return;
-    const uint8_t *ex = exps + eight * (kBlocks * 8) + r;
-    const uint4 *a = reinterpret_cast<const uint4 *>(act + eight * (kBlocks * 256)) + lane;
+    const int mine = lane < kBlocks ? __ldcg(exps + row * kBlocks + lane) : 0;
     uint4 u[kMine];
-    int eb[kMine], e = 0;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+        u[i] = i * 32 + lane < kF / 8 ? __ldcg(reinterpret_cast<const uint4 *>(act + row * kF) + i * 32 + lane) : make_uint4(0, 0, 0, 0);
+    const int e = __reduce_max_sync(0xFFFFFFFFu, mine);
+    if (lane == 0)
+        scale[row] = row_scale(e);
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
-        const int b = i * 8 + warp;
-        u[i] = b < kBlocks ? __ldcg(a + b * 32) : make_uint4(0, 0, 0, 0);
-        eb[i] = b < kBlocks ? __ldcg(ex + b * 8) : 0;
-    }
-#pragma unroll
-    for (int i = 0; i < (kBlocks + 3) / 4; ++i) {
-        const int b = i * 4 + (lane & 3);
-        e = max(e, b < kBlocks ? static_cast<int>(__ldcg(ex + b * 8)) : 0);
-    }
-    e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, 1));
-    e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, 2));
-    if (warp == 0 && (lane & 3) == 0)
-        scale[eight * 8 + r] = row_scale(e);
-    uint8_t *to = terms + (eight * 8 + r) * (2 * kF);
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-        const int b = i * 8 + warp;
-        if (b >= kBlocks)
-            break;
+        const int at = i * 32 + lane, eb = __shfl_sync(0xFFFFFFFFu, mine, at >> 2);
         const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
         // a = f16 2^(eb - 141); over s: 2^(eb - e - 7)
-        const int d = eb[i] - e - 7 + 127;
+        const int d = eb - e - 7 + 127;
         const float up = d > 0 ? __int_as_float(d << 23) : 0.0f;
         float v[8];
 #pragma unroll
@@ -351,7 +339,8 @@ __global__ void __launch_bounds__(256) k_act_terms(const uint16_t *act, const ui
             v[2 * q] = f.x * up;
             v[2 * q + 1] = f.y * up;
         }
-        write_terms(to, b * 32 + (lane & 3) * 8, v);
+        if (at < kF / 8)
+            write_terms(terms + row * (2 * kF), at * 8, v);
     }
 }
 
@@ -400,7 +389,7 @@ __global__ void __launch_bounds__(256) k_prep(const PrepArgs p)
     } else if ((b -= p.group.chunks) < kNE) {
         scale_max(p.down_s, kH, p.smax, b);
     } else {
-        row_terms(p.terms, static_cast<int64_t>(b - kNE) * (kTermThreads / kTermRow));
+        row_terms<128>(p.terms, b - kNE);
     }
 }
 
@@ -409,6 +398,7 @@ __global__ void __launch_bounds__(256) k_prep(const PrepArgs p)
 // y_t = sum_k w_tk y[pos_tk] (+ the shared expert's row), k in order: rows of f16,
 // which grouped.cuh wrote as f16(a 2^-12 / (sa smax)).
 struct CombineArgs {
+    const uint16_t *rows;    // [.][2816] f16
     const float *sa;         // [.] scales of the activations' terms
     const float *smax;       // [129]
     const int32_t *ids;      // [T][8]
@@ -422,15 +412,17 @@ struct CombineArgs {
     long long timeout_ns;
 };
 
-// A CTA takes tokens in turn: one warp brings their rows, nine copies of 88 pieces of
-// 64 bytes a token (read by lanes, the pieces cost an SM 2.6 us a token: 428 us for
-// 16,381 where this takes 160), into a ring of four tokens; the others add them up.
-constexpr int kCombineThreads = kH / 8 + 32;
+// A CTA takes tokens in turn: one warp brings their rows, nine copies of 5,632 bytes a
+// token, into a ring of four tokens; two teams of the others add them up by turns (one
+// alone is bound by what it waits for itself: 251 us for 16,381 tokens).
+constexpr int kCombineTeam = kH / 8;
+constexpr int kCombineTeams = 2;
+constexpr int kCombineThreads = kCombineTeams * kCombineTeam + 32;
 constexpr int kCombineStages = 4;
 constexpr int kCombineStage = (kK + 1) * 2 * kH;
 constexpr int kCombineSmem = kCombineStages * kCombineStage + 128;
 
-__global__ void __launch_bounds__(kCombineThreads, 1) k_combine(const __grid_constant__ CUtensorMap rows, const CombineArgs p)
+__global__ void __launch_bounds__(kCombineThreads, 1) k_combine(const CombineArgs p)
 {
     extern __shared__ uint8_t dsm_raw[];
     __shared__ unsigned long long full[kCombineStages], empty[kCombineStages];
@@ -442,7 +434,7 @@ __global__ void __launch_bounds__(kCombineThreads, 1) k_combine(const __grid_con
     if (threadIdx.x == 0) {
         for (int i = 0; i < kCombineStages; ++i) {
             tc::bar_init(&full[i], 1);
-            tc::bar_init(&empty[i], kH / 8 / 32);
+            tc::bar_init(&empty[i], kCombineTeam / 32);
         }
         abort_ = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -452,7 +444,7 @@ __global__ void __launch_bounds__(kCombineThreads, 1) k_combine(const __grid_con
     tc::let_next_start();
     const tc::Waiter wait{&abort_, p.status, p.timeout_ns};
     uint32_t n = 0;
-    if (warp == kH / 8 / 32) {
+    if (warp == kCombineThreads / 32 - 1) {
         bool ok = true;
         for (int64_t t = blockIdx.x; t < p.T && ok; t += gridDim.x, ++n) {
             const uint32_t slot = n % kCombineStages;
@@ -482,40 +474,42 @@ __global__ void __launch_bounds__(kCombineThreads, 1) k_combine(const __grid_con
                 tc::bar_expect(bar, __popc(rows_of) * 2 * kH);
             __syncwarp();
             if (at >= 0)
-                asm volatile(
-                    "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
-                        ring + slot * kCombineStage + lane * 2 * kH),
-                    "l"(reinterpret_cast<uint64_t>(&rows)), "r"(0), "r"(at & 7), "r"(0), "r"(at >> 3), "r"(bar)
-                    : "memory");
+                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                                 ring + slot * kCombineStage + lane * 2 * kH),
+                             "l"(reinterpret_cast<uint64_t>(p.rows + static_cast<int64_t>(at) * kH)), "r"(2 * kH), "r"(bar)
+                             : "memory");
         }
         // every copy lands before the CTA ends
         for (uint32_t i = n > kCombineStages ? n - kCombineStages : 0; i < n; ++i)
             tc::bar_drain(tc::saddr(&full[i % kCombineStages]), (i / kCombineStages) & 1);
         return;
     }
-    const int k0 = threadIdx.x * 8;
-    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, ++n) {
+    const int team = threadIdx.x / kCombineTeam, at = threadIdx.x - team * kCombineTeam;
+    n = team;
+    for (int64_t t = blockIdx.x + static_cast<int64_t>(team) * gridDim.x; t < p.T; t += static_cast<int64_t>(kCombineTeams) * gridDim.x, n += kCombineTeams) {
         const uint32_t slot = n % kCombineStages;
         if (!__all_sync(0xFFFFFFFFu, wait(&full[slot], n / kCombineStages, 45, static_cast<int>(t))))
             break;
+        const uint32_t rows_of = present[slot];
+        uint32_t w[kK + 1][4];
+#pragma unroll
+        for (int k = 0; k <= kK; ++k)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[k][0]), "=r"(w[k][1]), "=r"(w[k][2]), "=r"(w[k][3])
+                         : "r"(ring + slot * kCombineStage + k * 2 * kH + at * 16)
+                         : "memory");
         float o[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q)
             o[q] = 0.0f;
-        const uint32_t rows_of = present[slot];
 #pragma unroll
         for (int k = 0; k <= kK; ++k) {
-            if (!(rows_of >> k & 1))
-                continue;
             const float f = factor[slot][k];
-            uint32_t w[4];
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "r"(ring + slot * kCombineStage + k * 2 * kH + threadIdx.x * 16)
-                         : "memory");
+            const bool in = rows_of >> k & 1;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w[q]));
+                const uint32_t x = in ? w[k][q] : 0u;
+                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&x));
                 o[2 * q] = fmaf(f, v.x, o[2 * q]);
                 o[2 * q + 1] = fmaf(f, v.y, o[2 * q + 1]);
             }
@@ -527,7 +521,7 @@ __global__ void __launch_bounds__(kCombineThreads, 1) k_combine(const __grid_con
 #pragma unroll
         for (int q = 0; q < 4; ++q)
             r[q] = f32_to_bf16(o[2 * q]) | static_cast<uint32_t>(f32_to_bf16(o[2 * q + 1])) << 16;
-        *reinterpret_cast<uint4 *>(p.y + t * kH + k0) = make_uint4(r[0], r[1], r[2], r[3]);
+        *reinterpret_cast<uint4 *>(p.y + t * kH + at * 8) = make_uint4(r[0], r[1], r[2], r[3]);
     }
 }
 

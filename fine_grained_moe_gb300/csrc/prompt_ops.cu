@@ -128,7 +128,7 @@ template <grouped::Mode MODE, bool BYTES>
 int launch_grouped(const grouped::Maps &m, grouped::Args a, int sms, cudaStream_t st)
 {
     const auto kernel = grouped::k_grouped<MODE, BYTES>;
-    constexpr int kSmem = grouped::kRing + 1024;
+    constexpr int kSmem = grouped::kSmem;
     static std::atomic<int> fit_pairs[64];       // CTA pairs at a time, per device; finding it twice does no harm
     int dev = 0;
     FGM_HOST_CUDA(cudaGetDevice(&dev));
@@ -152,6 +152,8 @@ int launch_grouped(const grouped::Maps &m, grouped::Args a, int sms, cudaStream_
         fit_pairs[dev & 63] = most;
     }
     const int fit = grouped::kRing / grouped::stage_bytes<MODE, BYTES>(a.cols);
+    for (a.log_cols = 0; 1 << a.log_cols < a.cols; ++a.log_cols)
+        ;
     a.stages = fit < grouped::kMaxStages ? fit : grouped::kMaxStages;
     // tiles: an expert has at most its rows / cols, rounded up, and no more experts than rows have any
     const int64_t across = (a.N + 255) / 256, tiles = (a.R / a.cols + (a.E < a.R ? a.E : a.R)) * across;
@@ -159,7 +161,12 @@ int launch_grouped(const grouped::Maps &m, grouped::Args a, int sms, cudaStream_
     return launch_overlapped(kernel, dim3(static_cast<unsigned>(2 * pairs)), a.src ? grouped::kGatherThreads : grouped::kThreads, kSmem, st, m, a);
 }
 
-constexpr int kTermRows = rows::kTermThreads / rows::kTermRow;
+// CTAs for the terms of n rows.
+unsigned term_ctas(int64_t n, int K)
+{
+    const int each = rows::kTermThreads / rows::term_row(K);
+    return static_cast<unsigned>((n + each - 1) / each);
+}
 
 bool gemm_sizes_ok(int64_t x_rows, int64_t R, int E, int N, int K)
 {
@@ -182,23 +189,15 @@ GemmWs gemm_ws(int64_t x_rows, int K)
 }
 
 struct ExpertsWs {
-    size_t offsets, counts, src, pos, count, terms, xs, exps, act_terms, sa, rows, smax, total;
+    size_t offsets, src, pos, count, terms, xs, exps, act_terms, sa, rows, smax, total;
 };
-
-// Places of T tokens' slots, an expert's beginning at a multiple of 8.
-int64_t experts_rows(int64_t T)
-{
-    const int64_t active = T * kK < kE ? T * kK : kE;
-    return static_cast<int64_t>(align_up(T * kK + 7 * active + T, 8));
-}
 
 ExpertsWs experts_ws(int64_t T)
 {
     ExpertsWs o;
     Carve c;
-    const int64_t R = experts_rows(T);
+    const int64_t R = T * (kK + 1);
     o.offsets = c.take(sizeof(int32_t) * (kE + 2));
-    o.counts = c.take(sizeof(int32_t) * (kE + 1));
     o.src = c.take(sizeof(int32_t) * R);
     o.pos = c.take(sizeof(int32_t) * T * kK);
     o.count = c.take(group_count_bytes(T * kK, kE));
@@ -371,7 +370,7 @@ int fgm_grouped_gemm(const uint16_t *x, int64_t x_stride, int64_t x_rows, const 
     const int64_t row = 2 * static_cast<int64_t>(bytes ? align_up(K, 32) : K);
     FGM_HOST_TRY(x_maps(m, bytes ? region<void>(ws, o.terms) : static_cast<const void *>(x), row, bytes ? row : 2 * x_stride, x_rows, src != nullptr));
     if (bytes)
-        FGM_HOST_TRY(launch_overlapped(rows::k_terms, dim3(static_cast<unsigned>((x_rows + kTermRows - 1) / kTermRows)), rows::kTermThreads, 0, st,
+        FGM_HOST_TRY(launch_overlapped(rows::k_terms, dim3(term_ctas(x_rows, K)), rows::kTermThreads, 0, st,
                                        rows::TermArgs{x, x_stride, x_rows, K, region<uint8_t>(ws, o.terms), region<float>(ws, o.xs)}));
     grouped::Args a = {};
     a.offsets = offsets;
@@ -419,7 +418,7 @@ int fgm_moe_experts_fwd(const fgm_layer *layer, const uint16_t *x, int64_t x_str
     FGM_HOST_TRY(host_device_ready(&sms));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int E = shared ? kNE : kE;
-    const int64_t R = experts_rows(T);
+    const int64_t R = T * (shared ? kK + 1 : kK);
     grouped::Maps up, down;
     FGM_HOST_TRY(weight_map(&up.w, layer->gate_q, 1, kNE, kF, kH));
     FGM_HOST_TRY(weight_map(&up.w2, layer->up_q, 1, kNE, kF, kH));
@@ -427,11 +426,6 @@ int fgm_moe_experts_fwd(const fgm_layer *layer, const uint16_t *x, int64_t x_str
     down.w2 = down.w;
     FGM_HOST_TRY(x_maps(up, region<void>(ws, o.terms), 2 * kH, 2 * kH, T, true));
     FGM_HOST_TRY(x_maps(down, region<void>(ws, o.act_terms), 2 * kF, 2 * kF, R, false));
-
-    CUtensorMap rmap;
-    const uint64_t rdims[4] = {2 * 32, 8, kH / 32, static_cast<uint64_t>(R / 8)}, rstr[3] = {64, 512, 16 * kH};
-    const uint32_t rbox[4] = {2 * 32, 1, kH / 32, 1};
-    FGM_HOST_TRY(host_map(&rmap, region<void>(ws, o.rows), 1, 4, rdims, rstr, rbox, false));
 
     rows::PrepArgs prep = {};
     rows::GroupArgs &g = prep.group;
@@ -444,19 +438,16 @@ int fgm_moe_experts_fwd(const fgm_layer *layer, const uint16_t *x, int64_t x_str
     g.pos = region<int32_t>(ws, o.pos);
     g.per = kK;
     g.shared = shared ? static_cast<int>(T) : 0;
-    g.counts = region<int32_t>(ws, o.counts);
     cut_group(g);
     prep.terms = rows::TermArgs{x, x_stride, T, kH, region<uint8_t>(ws, o.terms), region<float>(ws, o.xs)};
     prep.down_s = layer->down_s;
     prep.smax = region<float>(ws, o.smax);
-    FGM_HOST_TRY(launch_overlapped(rows::k_prep, dim3(static_cast<unsigned>(g.chunks + kNE + (T + kTermRows - 1) / kTermRows)), 256, group_smem(kE), st,
-                                   prep));
+    FGM_HOST_TRY(launch_overlapped(rows::k_prep, dim3(g.chunks + kNE + term_ctas(T, kH)), 256, group_smem(kE), st, prep));
     if (g.chunks > 1)
         FGM_HOST_TRY(launch_deal(g, st));
 
     grouped::Args a = {};
     a.offsets = g.offsets;
-    a.counts = g.counts;
     a.E = E;
     a.R = R;
     a.src = g.src;
@@ -474,7 +465,7 @@ int fgm_moe_experts_fwd(const fgm_layer *layer, const uint16_t *x, int64_t x_str
     a.status = status_word(ws);
     a.timeout_ns = host_wait_limit_ns();
     FGM_HOST_TRY((launch_grouped<grouped::kGated, true>(up, a, sms, st)));
-    FGM_HOST_TRY(launch_overlapped(rows::k_act_terms, dim3(static_cast<unsigned>(R / 8)), 256, 0, st, static_cast<const uint16_t *>(a.out), static_cast<const uint8_t *>(a.exps),
+    FGM_HOST_TRY(launch_overlapped(rows::k_act_terms, dim3(static_cast<unsigned>((R + 7) / 8)), rows::kTermThreads, 0, st, static_cast<const uint16_t *>(a.out), static_cast<const uint8_t *>(a.exps),
                                    a.offsets + E, region<uint8_t>(ws, o.act_terms), region<float>(ws, o.sa)));
     grouped::Args d = a;
     d.src = nullptr;
@@ -488,7 +479,7 @@ int fgm_moe_experts_fwd(const fgm_layer *layer, const uint16_t *x, int64_t x_str
     d.smax = region<float>(ws, o.smax);
     d.cols = tile_cols(T * kK, E, 256);
     FGM_HOST_TRY((launch_grouped<grouped::kDown, true>(down, d, sms, st)));
-    const rows::CombineArgs c{region<float>(ws, o.sa), d.smax, ids, w, g.pos, g.offsets, shared ? 1 : 0, T, y, a.status, a.timeout_ns};
+    const rows::CombineArgs c{d.out, region<float>(ws, o.sa), d.smax, ids, w, g.pos, g.offsets, shared ? 1 : 0, T, y, a.status, a.timeout_ns};
     static std::atomic<bool> ready[64];          // per device; setting it twice does no harm
     int dev = 0;
     FGM_HOST_CUDA(cudaGetDevice(&dev));
@@ -496,7 +487,7 @@ int fgm_moe_experts_fwd(const fgm_layer *layer, const uint16_t *x, int64_t x_str
         FGM_HOST_CUDA(cudaFuncSetAttribute(rows::k_combine, cudaFuncAttributeMaxDynamicSharedMemorySize, rows::kCombineSmem));
         ready[dev & 63] = true;
     }
-    return launch_overlapped(rows::k_combine, dim3(static_cast<unsigned>(T < sms ? T : sms)), rows::kCombineThreads, rows::kCombineSmem, st, rmap, c);
+    return launch_overlapped(rows::k_combine, dim3(static_cast<unsigned>(T < sms ? T : sms)), rows::kCombineThreads, rows::kCombineSmem, st, c);
 }
 
 }  // extern "C"
