@@ -412,13 +412,14 @@ struct CombineArgs {
     long long timeout_ns;
 };
 
-// A CTA takes tokens in turn: one warp brings their rows, nine copies of 5,632 bytes a
-// token, into a ring of four tokens; two teams of the others add them up by turns (one
-// alone is bound by what it waits for itself: 251 us for 16,381 tokens).
+// A CTA takes tokens in turn, four at a time on their way: four warps each bring a
+// token's rows, nine copies of 5,632 bytes (one warp for all was bound by the two loads
+// that lead to a row's place: 253 us for 16,381 tokens), and two teams of others add
+// them up by turns.
 constexpr int kCombineTeam = kH / 8;
 constexpr int kCombineTeams = 2;
-constexpr int kCombineThreads = kCombineTeams * kCombineTeam + 32;
 constexpr int kCombineStages = 4;
+constexpr int kCombineThreads = kCombineTeams * kCombineTeam + 32 * kCombineStages;
 constexpr int kCombineStage = (kK + 1) * 2 * kH;
 constexpr int kCombineSmem = kCombineStages * kCombineStage + 128;
 
@@ -443,11 +444,11 @@ __global__ void __launch_bounds__(kCombineThreads, 1) k_combine(const CombineArg
     tc::after_previous();
     tc::let_next_start();
     const tc::Waiter wait{&abort_, p.status, p.timeout_ns};
-    uint32_t n = 0;
-    if (warp == kCombineThreads / 32 - 1) {
+    uint32_t n = 0;                              // round of a stage, then the CTA's n-th token
+    if (warp >= kCombineTeams * kCombineTeam / 32) {
+        const int slot = warp - kCombineTeams * kCombineTeam / 32;
         bool ok = true;
-        for (int64_t t = blockIdx.x; t < p.T && ok; t += gridDim.x, ++n) {
-            const uint32_t slot = n % kCombineStages;
+        for (int64_t t = blockIdx.x + static_cast<int64_t>(slot) * gridDim.x; t < p.T; t += static_cast<int64_t>(kCombineStages) * gridDim.x, ++n) {
             // lane k: choice k's row, and what its elements are multiplied by; lane 8: the shared expert's
             int at = -1, e = kE;
             float w = 1.0f;
@@ -460,8 +461,8 @@ __global__ void __launch_bounds__(kCombineThreads, 1) k_combine(const CombineArg
             }
             const float f = at >= 0 ? w * (__ldcg(p.sa + at) * (__ldcg(p.smax + e) * 4096.0f)) : 0.0f;
             const uint32_t rows_of = __ballot_sync(0xFFFFFFFFu, at >= 0);
-            if (n >= kCombineStages)
-                ok = wait(&empty[slot], n / kCombineStages - 1, 44, static_cast<int>(t));
+            if (n)
+                ok = wait(&empty[slot], n - 1, 44, static_cast<int>(t));
             if (!(ok = __all_sync(0xFFFFFFFFu, ok)))
                 break;
             const uint32_t bar = tc::saddr(&full[slot]);
@@ -479,9 +480,8 @@ __global__ void __launch_bounds__(kCombineThreads, 1) k_combine(const CombineArg
                              "l"(reinterpret_cast<uint64_t>(p.rows + static_cast<int64_t>(at) * kH)), "r"(2 * kH), "r"(bar)
                              : "memory");
         }
-        // every copy lands before the CTA ends
-        for (uint32_t i = n > kCombineStages ? n - kCombineStages : 0; i < n; ++i)
-            tc::bar_drain(tc::saddr(&full[i % kCombineStages]), (i / kCombineStages) & 1);
+        if (n)                                   // the last copies land before the CTA ends
+            tc::bar_drain(tc::saddr(&full[slot]), (n - 1) & 1);
         return;
     }
     const int team = threadIdx.x / kCombineTeam, at = threadIdx.x - team * kCombineTeam;
