@@ -30,7 +30,8 @@ constexpr int kMaxExperts = 1024;
 constexpr int kStageK = 128;                     // elements of K in a stage
 constexpr int kBox = 128 * 128;                  // 128 weight rows x 128 bytes
 constexpr int kRing = 192 * 1024;                // bytes of the ring at most
-constexpr int kOutBuf = 8 * 256;                 // eight rows of 128 features on their way out, twice for each side
+constexpr int kOutRow = 256 + 16;                // 128 features of a row on their way out (and 16 bytes: rows begin in other banks),
+constexpr int kOutBuf = 8 * kOutRow;             // eight rows, twice for each side
 constexpr int kOutBytes = kSides * 2 * kOutBuf;
 constexpr int kSmem = kRing + kOutBytes + 1024;
 
@@ -161,8 +162,14 @@ __device__ __forceinline__ bool side_all(int side, bool yes)
 
 __device__ __forceinline__ void side_sync(int side) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + side) : "memory"); }
 
-// A feature's value of a row (its low or high half) to shared memory.
-__device__ __forceinline__ void put16(uint32_t at, uint32_t v) { asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(v)) : "memory"); }
+// Four words of two rows x a feature a lane, as products hold them (a word: features l / 4,
+// + 8, + 16, + 24), to shared memory by rows: lane l names where row l % 8's features 8 (l / 8) to
+// + 7 go.
+__device__ __forceinline__ void put_rows(uint32_t at, const uint32_t (&w)[4])
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                 : "memory");
+}
 
 // A tile: rows [r0, r0 + live) of expert e against 256 of its output features (of
 // each product) from n0 on. A pair's items come in ascending order.
@@ -326,12 +333,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
                                 if (j * 32 < left) {
                                     const uint64_t aj = a + j * 2, bj = b + (j >> 1) * (xbox >> 4) + (j & 1) * 4;
                                     const bool add = (ks | j) != 0;
-                                    tc::product<2, true>(d, aj, bj, idesc, add);
-                                    tc::product<2, true>(d, aj, bj + 2, idesc, true);
-                                    if constexpr (MODE == kGated) {
-                                        tc::product<2, true>(d + 128, aj + (kBox >> 4), bj, idesc, add);
-                                        tc::product<2, true>(d + 128, aj + (kBox >> 4), bj + 2, idesc, true);
-                                    }
+                                    tc::product_twice<2>(d, aj, bj, bj + 2, idesc, add);
+                                    if constexpr (MODE == kGated)
+                                        tc::product_twice<2>(d + 128, aj + (kBox >> 4), bj, bj + 2, idesc, add);
                                 }
                         } else {
 #pragma unroll
@@ -411,40 +415,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
         // (columns by eights, a side's each fourth: with two sides, what a warp waits for itself took longer than the products)
         const int quarter = warp & 3, side = (warp - 4) >> 2;
         constexpr int kEights = (MODE == kGated ? 128 : 256) / 8 / kSides;
-        const uint32_t out0 = ring + kRing + side * 2 * kOutBuf, put_at = out0 + quarter * 64 + lane * 2,
-                       take_at = out0 + quarter * 512 + lane * 16;
+        const uint32_t out0 = ring + kRing + side * 2 * kOutBuf, put_at = out0 + (lane & 7) * kOutRow + quarter * 64 + (lane >> 3) * 16,
+                       take_at = out0 + (quarter * 2 + (lane >> 4)) * kOutRow + (lane & 15) * 16;
         uint32_t outs = 0;
         bool alive = true;
         uint32_t tile = 0;
         for (int item = pair; item < items; item += pairs, ++tile) {
             t.find(sh, p, item);
             const uint32_t buf = tile & 1;
-            const int n0 = t.n0 + rank * 128, nw = n0 + quarter * 32, n = nw + lane;
-            // what rows (those of this lane, see below) and features are multiplied by, on its way while the products end
-            float xs[kEights], s0 = 1.0f, s1 = 1.0f;
+            const int n0 = t.n0 + rank * 128, nw = n0 + quarter * 32;
+            // what this lane's rows and features (see below) are multiplied by, on its way while the products end
+            constexpr int kX = MODE == kGated ? 2 : 1;
+            float xs[kEights][kX], s0[4], s1[4];
 #pragma unroll
-            for (int i = 0; i < kEights; ++i) {
-                const int c = (i * kSides + side) * 8 + (MODE == kGated ? lane & 7 : quarter * 2 + (lane >> 4));
-                xs[i] = 1.0f;
-                if (MODE != kDown && c < t.live) {
-                    int row = t.r0 + c;
-                    bool there = true;
-                    if (p.src) {
-                        row = __ldcg(p.src + row);
-                        there = row >= 0 && row / p.per < p.x_rows;
-                        row = there ? row / p.per : 0;
+            for (int i = 0; i < kEights; ++i)
+#pragma unroll
+                for (int j = 0; j < kX; ++j) {
+                    const int c = (i * kSides + side) * 8 + (MODE == kGated ? 2 * (lane & 3) + j : quarter * 2 + (lane >> 4));
+                    xs[i][j] = 1.0f;
+                    if (MODE != kDown && c < t.live) {
+                        int row = t.r0 + c;
+                        bool there = true;
+                        if (p.src) {
+                            row = __ldcg(p.src + row);
+                            there = row >= 0 && row / p.per < p.x_rows;
+                            row = there ? row / p.per : 0;
+                        }
+                        // (negative: no such row of x, the output is zero)
+                        xs[i][j] = there ? (BYTES ? __ldcg(p.xs + row) : 1.0f) : -1.0f;
                     }
-                    // (negative: no such row of x, the output is zero)
-                    xs[i] = there ? (BYTES ? __ldcg(p.xs + row) : 1.0f) : -1.0f;
+                }
+            const float norm = MODE == kDown ? 0x1p-12f / __ldcg(p.smax + t.e) : 1.0f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int n = nw + (lane >> 2) + 8 * q;
+                s0[q] = s1[q] = norm;
+                if (n < p.N && p.s0) {
+                    s0[q] *= __ldcg(p.s0 + static_cast<int64_t>(t.e) * p.N + n);
+                    if (MODE == kGated)
+                        s1[q] = __ldcg(p.s1 + static_cast<int64_t>(t.e) * p.N + n);
                 }
             }
-            if (n < p.N && p.s0) {
-                s0 = __ldcg(p.s0 + static_cast<int64_t>(t.e) * p.N + n);
-                if (MODE == kGated)
-                    s1 = __ldcg(p.s1 + static_cast<int64_t>(t.e) * p.N + n);
-            }
-            if (MODE == kDown)
-                s0 *= 0x1p-12f / __ldcg(p.smax + t.e);
             if (alive)
                 alive = wait(&sh.tfull[buf], tile >> 1, 37, t.e);
             alive = side_all(side, alive);       // (a side's warps meet at barriers below)
@@ -452,9 +463,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
             if (alive && n0 < p.N) {
                 const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * 256;
                 auto read = [&](int c, uint32_t (&u)[8], uint32_t (&v)[8]) {
-                    tc::read(from + c, u);
+                    tc::read_pairs(from + c, u);
                     if (MODE == kGated)
-                        tc::read(from + 128 + c, v);
+                        tc::read_pairs(from + 128 + c, v);
                 };
                 // this side's eights, the next on its way meanwhile
                 uint32_t u[2][8], v[2][8];
@@ -476,31 +487,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
                     }
                     if (i + 1 < kEights && c + kSides * 8 < t.live)
                         read(c + kSides * 8, u[(i + 1) & 1], v[(i + 1) & 1]);
-                    uint32_t pk[4];              // eight rows of this lane's feature, in 16 bits
+                    // (of features l / 4 + 8 q rows 2 (l % 4) and the next: u[2 q], u[2 q + 1])
+                    uint32_t pk[4];
                     if (MODE == kGated) {
                         float a[8];
-                        int e_mine = 0;
+                        uint32_t m[2] = {0, 0};
 #pragma unroll
                         for (int q = 0; q < 8; ++q) {
-                            const float x = __shfl_sync(0xFFFFFFFFu, xs[i], q);
-                            a[q] = gelu(__uint_as_float(u[i & 1][q]) * s0 * x) * (__uint_as_float(v[i & 1][q]) * s1 * x);
-                            // |a| < 2^(e - 126) for all 32: below 2^15 in f16, which has 11 bits down to 2^-14
-                            int e = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(a[q]) & 0x7FFFFFFFu) >> 23);
-                            e = e < 14 ? 14 : e;
-                            e_mine = (lane & 7) == q ? e : e_mine;
-                            a[q] *= __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
+                            const float x = xs[i][kX == 2 ? q & 1 : 0];
+                            a[q] = gelu(__uint_as_float(u[i & 1][q]) * s0[q >> 1] * x) * (__uint_as_float(v[i & 1][q]) * s1[q >> 1] * x);
+                            m[q & 1] = max(m[q & 1], __float_as_uint(a[q]) & 0x7FFFFFFFu);
                         }
-                        if (lane < 8 && c + lane < t.live && nw < p.N)
-                            p.exps[static_cast<int64_t>(t.r0 + c + lane) * (p.N >> 5) + (nw >> 5)] = static_cast<uint8_t>(e_mine);
+                        // |a| < 2^(e - 126) for all 32 features of a row: below 2^15 in f16, which has 11 bits down to 2^-14
+                        float up[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1)
+                                m[j] = max(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], o));
+                            const uint32_t e = max(m[j] >> 23, 14u);
+                            up[j] = __uint_as_float((268 - e) << 23);
+                            const int r = c + 2 * lane + j;
+                            if (lane < 4 && r < t.live && nw < p.N)
+                                p.exps[static_cast<int64_t>(t.r0 + r) * (p.N >> 5) + (nw >> 5)] = static_cast<uint8_t>(e);
+                        }
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const __half2 h = __floats2half2_rn(a[2 * q], a[2 * q + 1]);
+                            const __half2 h = __floats2half2_rn(a[2 * q] * up[0], a[2 * q + 1] * up[1]);
                             pk[q] = *reinterpret_cast<const uint32_t *>(&h);
                         }
                     } else {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const float a = __uint_as_float(u[i & 1][2 * q]) * s0, b = __uint_as_float(u[i & 1][2 * q + 1]) * s0;
+                            const float a = __uint_as_float(u[i & 1][2 * q]) * s0[q], b = __uint_as_float(u[i & 1][2 * q + 1]) * s0[q];
                             if (MODE == kDown) {
                                 const __half2 h = __floats2half2_rn(a, b);
                                 pk[q] = *reinterpret_cast<const uint32_t *>(&h);
@@ -512,12 +531,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
                     }
                     // The side's four warps lay 128 features of eight rows side by side, and each takes two rows of
                     // them out again: whole lines, where a warp's own 32 features are 64 bytes of a row (50
-                    // cycles a store of 512 bytes instead of 18).
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        put16(put_at + ob + 2 * q * 256, pk[q]);
-                        put16(put_at + ob + (2 * q + 1) * 256, pk[q] >> 16);
-                    }
+                    // cycles a store of 512 bytes instead of 18). The products read their operands over the same
+                    // wires, so that what passes through shared memory here is to be little.
+                    put_rows(put_at + ob, pk);
                     side_sync(side);
                     uint32_t w[4];
                     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -526,14 +542,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
                                  : "memory");
                     if (MODE == kGemm) {
                         // (a row's scale is a power of two: it may follow the rounding)
-                        const __nv_bfloat162 x2 = __float2bfloat162_rn(xs[i]);
+                        const __nv_bfloat162 x2 = __float2bfloat162_rn(xs[i][0]);
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             if (BYTES) {
                                 const __nv_bfloat162 h = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&w[q]), x2);
                                 w[q] = *reinterpret_cast<const uint32_t *>(&h);
                             }
-                            w[q] = xs[i] < 0.0f ? 0u : w[q];
+                            w[q] = xs[i][0] < 0.0f ? 0u : w[q];
                         }
                     }
                     const int r = c + quarter * 2 + (lane >> 4), first = n0 + (lane & 15) * 8;

@@ -162,6 +162,18 @@ __device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint
             : "memory");
 }
 
+// d (+)= a b0 + a b1 in 8 bits: a is read from shared memory once and kept for the second product.
+template <int G>
+__device__ __forceinline__ void product_twice(uint32_t d, uint64_t a, uint64_t b0, uint64_t b1, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.eq.u32 q, 0, 0;\n\t"
+        "tcgen05.mma.cta_group::%6.kind::f8f6f4.collector::a::fill [%0], %1, %2, %4, p;\n\t"
+        "tcgen05.mma.cta_group::%6.kind::f8f6f4.collector::a::lastuse [%0], %1, %3, %4, q;\n\t}" ::"r"(d),
+        "l"(a), "l"(b0), "l"(b1), "r"(idesc), "r"(static_cast<uint32_t>(add)), "n"(G)
+        : "memory");
+}
+
 // M x N accumulators; both operands E4M3 or both bf16.
 __device__ __forceinline__ constexpr uint32_t product_desc(int M, int N, bool bytes)
 {
@@ -185,7 +197,7 @@ __device__ __forceinline__ void commit(unsigned long long *bar)
     asm volatile("tcgen05.commit.cta_group::%1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(bar)), "n"(G) : "memory");
 }
 
-// Eight columns of this warp's 32 lanes, or sixteen.
+// Eight columns of this warp's 32 lanes: a lane's own,
 __device__ __forceinline__ void read(uint32_t at, uint32_t (&u)[8])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -194,14 +206,17 @@ __device__ __forceinline__ void read(uint32_t at, uint32_t (&u)[8])
                  : "memory");
 }
 
-__device__ __forceinline__ void read(uint32_t at, uint32_t (&u)[16])
+// or as products hold them: of lanes l / 4, l / 4 + 8, + 16 and + 24 the columns 2 (l % 4) and the next.
+__device__ __forceinline__ void read_pairs(uint32_t at, uint32_t (&u)[8])
 {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]), "=r"(u[9]),
-          "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
-        : "r"(at)
-        : "memory");
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+                 : "r"(at)
+                 : "memory");
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                 : "r"(at + (16u << 16))
+                 : "memory");
 }
 
 __device__ __forceinline__ void read_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
