@@ -970,14 +970,17 @@ def moe_experts_fwd(layer, x: torch.Tensor, ids: torch.Tensor, weights: torch.Te
     return _call(dev, stream, body)
 
 
-def _norm_rows(name: str, t: torch.Tensor, shape: tuple, device) -> tuple[int, int, int]:
+def _norm_rows(name: str, t: torch.Tensor, shape, device) -> tuple[int, int, int]:
     """(address, type, elements between rows) of a tensor with dense rows."""
-    if t.dtype not in _DTYPES or t.shape != shape or t.device != device:
+    kind = _DTYPES.get(t.dtype)
+    if kind is None or t.shape != shape or t.device != device:
         raise FgmError(f"{name}: expected fp32, bf16 or fp16 {tuple(shape)} on {device}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+    if t.is_contiguous():
+        return t.data_ptr(), kind, shape[1]
     sn, sd = t.stride()
     if shape[1] > 1 and sd != 1:
         raise FgmError(f"{name}: expected dense rows, strides {t.stride()}")
-    return t.data_ptr(), _DTYPES[t.dtype], sn if shape[0] > 1 else max(sn, shape[1])
+    return t.data_ptr(), kind, sn if shape[0] > 1 else max(sn, shape[1])
 
 
 def block_norm(h: torch.Tensor, y: torch.Tensor | None = None, post_gain: torch.Tensor | None = None,
@@ -991,39 +994,40 @@ def block_norm(h: torch.Tensor, y: torch.Tensor | None = None, post_gain: torch.
     ``xn``; xn is None without pre_norm."""
     if h.dim() != 2 or not h.is_cuda:
         raise FgmError(f"h: expected CUDA [N, D], got {tuple(h.shape)} on {h.device}")
-    dev, (N, D) = h.device, h.shape
-    b = fgm_block(N=N, D=D, post_norm=int(post_norm and y is not None), residual_scale=residual_scale, block_scale=block_scale,
-                  gain_offset=gain_offset, eps=eps)
-    b.h, b.h_type, b.h_stride = _norm_rows("h", h, (N, D), dev)
-    if y is not None:
-        b.y, b.y_type, b.y_stride = _norm_rows("y", y, (N, D), dev)
+    dev, shape = h.device, h.shape
+    N, D = shape
+    h_at, h_type, h_step = _norm_rows("h", h, shape, dev)
+    y_at, y_type, y_step = (None, 0, 0) if y is None else _norm_rows("y", y, shape, dev)
+    g_at = g_type = g_rows = g_cols = 0
     if gate is not None:
         if gate.dtype not in _DTYPES or gate.device != dev or tuple(gate.shape) not in ((D,), (N, 1), (N, D)):
             raise FgmError(f"gate: expected [{D}], [{N}, 1] or [{N}, {D}] on {dev}, got {tuple(gate.shape)} {gate.dtype} on {gate.device}")
-        per_row = gate.dim() == 2 and gate.shape[1] == 1
-        if not per_row and D > 1 and gate.stride(-1) != 1:
+        g_cols = int(gate.dim() == 1 or gate.shape[1] != 1 or D == 1)
+        if g_cols and D > 1 and gate.stride(-1) != 1:
             raise FgmError(f"gate: expected dense rows, strides {gate.stride()}")
-        b.gate, b.gate_type, b.gate_col_stride = gate.data_ptr(), _DTYPES[gate.dtype], int(not per_row)
-        b.gate_row_stride = gate.stride(0) if gate.dim() == 2 and N > 1 else 0
-    gains = [t for t in (post_gain, pre_gain) if t is not None]
-    for t in gains:
-        if t.dtype not in _DTYPES or t.shape != (D,) or t.device != dev or not t.is_contiguous() or t.dtype is not gains[0].dtype:
-            raise FgmError(f"gains: expected contiguous [{D}] of one type on {dev}, got {tuple(t.shape)} {t.dtype} on {t.device}")
-    if gains:
-        b.gain_type = _DTYPES[gains[0].dtype]
-    b.post_gain, b.pre_gain = _at(post_gain), _at(pre_gain)
+        g_at, g_type = gate.data_ptr(), _DTYPES[gate.dtype]
+        g_rows = gate.stride(0) if gate.dim() == 2 and N > 1 else 0
+    gain_type = 0
+    for t in (post_gain, pre_gain):
+        if t is not None:
+            one = post_gain if post_gain is not None else pre_gain
+            if t.dtype not in _DTYPES or t.shape != (D,) or t.device != dev or not t.is_contiguous() or t.dtype is not one.dtype:
+                raise FgmError(f"gains: expected contiguous [{D}] of one type on {dev}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+            gain_type = _DTYPES[t.dtype]
+    if xn is not None and not pre_norm:
+        raise FgmError("xn without pre_norm")
 
     def body(s):
-        o = torch.empty((N, D), dtype=h.dtype, device=dev) if h_out is None else h_out
-        b.h_out, t, b.h_out_stride = _norm_rows("h_out", o, (N, D), dev)
-        if t != b.h_type:
+        o = torch.empty(shape, dtype=h.dtype, device=dev) if h_out is None else h_out
+        o_at, o_type, o_step = _norm_rows("h_out", o, shape, dev)
+        if o_type != h_type:
             raise FgmError(f"h_out: expected {h.dtype}, got {o.dtype}")
-        n = None
+        n, n_at, n_type, n_step = None, None, 0, 0
         if pre_norm:
-            n = torch.empty((N, D), dtype=_BF16, device=dev) if xn is None else xn
-            b.xn, b.xn_type, b.xn_stride = _norm_rows("xn", n, (N, D), dev)
-        elif xn is not None:
-            raise FgmError("xn without pre_norm")
-        _check(lib().fgm_block_norm(b, s))
+            n = torch.empty(shape, dtype=_BF16, device=dev) if xn is None else xn
+            n_at, n_type, n_step = _norm_rows("xn", n, shape, dev)
+        _check(lib().fgm_block_norm(fgm_block(
+            N, D, h_type, y_type, g_type, gain_type, n_type, h_at, y_at, g_at, _at(post_gain), _at(pre_gain), o_at, n_at, h_step,
+            y_step, g_rows, o_step, n_step, g_cols, post_norm and y is not None, residual_scale, block_scale, gain_offset, eps), s))
         return o, n
     return _call(dev, stream, body)

@@ -35,15 +35,28 @@ struct GroupArgs {
     int shared;              // tokens that one more expert takes behind the others (offsets has E + 2 entries), 0: none
 };
 
+constexpr int kIdsAhead = 4;
+
+__device__ __forceinline__ void load_ids(const GroupArgs &p, int64_t i, int64_t i1, int (&id)[kIdsAhead])
+{
+#pragma unroll
+    for (int j = 0; j < kIdsAhead; ++j)
+        id[j] = i + 32 * j < i1 ? __ldcg(p.ids + i + 32 * j) : -1;
+}
+
 // Counts of a warp's run of slots in its own row of hist.
 __device__ __forceinline__ void count_run(const GroupArgs &p, int64_t i0, int64_t i1, int *hist, int lane)
 {
-    for (int64_t i = i0; i < i1; i += 32) {
-        const int id = i + lane < i1 ? __ldcg(p.ids + i + lane) : -1;
-        const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
-        if (id >= 0 && id < p.E && lane == __ffs(same) - 1)
-            hist[id] += __popc(same);
-        __syncwarp();
+    for (int64_t i = i0; i < i1; i += 32 * kIdsAhead) {
+        int id[kIdsAhead];
+        load_ids(p, i + lane, i1, id);
+#pragma unroll
+        for (int j = 0; j < kIdsAhead; ++j) {
+            const unsigned same = __match_any_sync(0xFFFFFFFFu, id[j]);
+            if (id[j] >= 0 && id[j] < p.E && lane == __ffs(same) - 1)
+                hist[id[j]] += __popc(same);
+            __syncwarp();
+        }
     }
 }
 
@@ -73,7 +86,7 @@ __device__ __forceinline__ void group_count(const GroupArgs &p, int chunk, int *
     }
 }
 
-// The same CTA's slots dealt; hist: [kGroupWarps][E], then [E] totals.
+// The same CTA's slots dealt; hist: [kGroupWarps][E], then [2][E] totals.
 __device__ __forceinline__ void group_deal(const GroupArgs &p, int chunk, int *hist)
 {
     __shared__ int warp_sum[kGroupWarps];
@@ -86,22 +99,36 @@ __device__ __forceinline__ void group_deal(const GroupArgs &p, int chunk, int *h
     run_of(p, chunk, warp, i0, i1);
     count_run(p, i0, i1, hist + warp * p.E, lane);
     __syncthreads();
-    // a warp's first place of each expert, from the chunk's first, and the expert's slots in all
-    for (int e = threadIdx.x; e < p.E; e += kGroupThreads) {
-        int before = 0, all = 0, mine = 0;
-        if (p.chunks > 1)
-#pragma unroll 8
-            for (int c = 0; c < p.chunks; ++c) {
+    // slots of each expert in all chunks and in those before: threads share out the chunks where experts are few
+    int *before = total + p.E;
+    const int parts = p.E < kGroupThreads ? kGroupThreads / p.E : 1;
+    for (int e = threadIdx.x; e < p.E; e += kGroupThreads)
+        total[e] = before[e] = 0;
+    __syncthreads();
+    if (p.chunks > 1)
+        for (int i = threadIdx.x; i < p.E * parts; i += kGroupThreads) {
+            const int e = i % p.E, part = i / p.E;
+            int sum = 0, sum_before = 0;
+#pragma unroll 16
+            for (int c = part; c < p.chunks; c += parts) {
                 const int v = __ldcg(p.count + static_cast<int64_t>(c) * p.E + e);
-                before += c < chunk ? v : 0;
-                all += v;
+                sum_before += c < chunk ? v : 0;
+                sum += v;
             }
+            atomicAdd(total + e, sum);
+            atomicAdd(before + e, sum_before);
+        }
+    __syncthreads();
+    // a warp's first place of each expert
+    for (int e = threadIdx.x; e < p.E; e += kGroupThreads) {
+        int mine = before[e];
         for (int w = 0; w < kGroupWarps; ++w) {
             const int v = hist[w * p.E + e];
-            hist[w * p.E + e] = before + mine;
+            hist[w * p.E + e] = mine;
             mine += v;
         }
-        total[e] = p.chunks > 1 ? all : mine;
+        if (p.chunks == 1)
+            total[e] = mine;
     }
     __syncthreads();
     // places before each expert: a thread scans E / 256 experts, rounded up
@@ -138,24 +165,30 @@ __device__ __forceinline__ void group_deal(const GroupArgs &p, int chunk, int *h
     }
     __syncthreads();
     int *at = hist + warp * p.E;
-    for (int64_t i = i0; i < i1; i += 32) {
-        const int id = i + lane < i1 ? __ldcg(p.ids + i + lane) : -1;
-        const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
-        const bool in = id >= 0 && id < p.E;
-        int to = -1;
-        if (in)
-            to = total[id] + at[id] + __popc(same & ((1u << lane) - 1u));
-        __syncwarp();
-        if (in && lane == __ffs(same) - 1)
-            at[id] += __popc(same);
-        __syncwarp();
-        if (i + lane < i1) {
-            if (p.pos)
-                p.pos[i + lane] = to;
-            if (in && p.order)
-                p.order[to] = static_cast<int32_t>(i + lane);
-            if (in && p.src)
-                p.src[to] = static_cast<int32_t>((i + lane) / p.per);
+    for (int64_t i = i0; i < i1; i += 32 * kIdsAhead) {
+        int ids[kIdsAhead];
+        load_ids(p, i + lane, i1, ids);
+#pragma unroll
+        for (int j = 0; j < kIdsAhead; ++j) {
+            const int id = ids[j];
+            const int64_t slot = i + 32 * j + lane;
+            const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
+            const bool in = id >= 0 && id < p.E;
+            int to = -1;
+            if (in)
+                to = total[id] + at[id] + __popc(same & ((1u << lane) - 1u));
+            __syncwarp();
+            if (in && lane == __ffs(same) - 1)
+                at[id] += __popc(same);
+            __syncwarp();
+            if (slot < i1) {
+                if (p.pos)
+                    p.pos[slot] = to;
+                if (in && p.order)
+                    p.order[to] = static_cast<int32_t>(slot);
+                if (in && p.src)
+                    p.src[to] = static_cast<int32_t>(slot / p.per);
+            }
         }
     }
     if (p.shared) {

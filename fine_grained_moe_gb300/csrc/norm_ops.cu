@@ -1,5 +1,6 @@
 // C ABI of the block norms (declared in include/fgm.h): argument checks and launches
 // of block_norm.cuh.
+#include <atomic>
 #include <cmath>
 
 #include "block_norm.cuh"
@@ -7,6 +8,8 @@
 
 namespace fgm {
 namespace {
+
+constexpr int kNormSmem = 226 * 1024;            // dynamic shared memory at most
 
 int64_t elem_bytes(int type) { return type == FGM_F32 ? 4 : 2; }
 bool type_ok(int type) { return type == FGM_F32 || type == FGM_BF16 || type == FGM_F16; }
@@ -50,11 +53,70 @@ int check_tensor(const char *name, const void *p, int type, int64_t stride, int 
 
 bool wide(const void *p, int64_t stride, int type) { return !p || (is_aligned(p, 16) && stride * elem_bytes(type) % 16 == 0); }
 
-template <int TPR, int VPT, int VEC>
-int launch_norm(const norm::Args &a, cudaStream_t st)
+// CTAs of a kernel at a time on this device; found once per device (twice does no harm) for its most shared memory and asked for less.
+template <typename K>
+int norm_grid(K kernel, std::atomic<bool> (&ready)[64], int threads, size_t smem, int sms, int64_t N, int64_t *grid)
 {
-    constexpr int kThreads = TPR < norm::kMinThreads ? norm::kMinThreads : TPR, kRows = kThreads / TPR;
-    return launch_overlapped(norm::k_block_norm<TPR, VPT, VEC>, dim3(static_cast<unsigned>((a.N + kRows - 1) / kRows)), kThreads, 0, st, a);
+    int dev = 0, each = 0;
+    FGM_HOST_CUDA(cudaGetDevice(&dev));
+    if (!ready[dev & 63]) {
+        FGM_HOST_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem));
+        ready[dev & 63] = true;
+    }
+    *grid = N;
+    if (N > sms) {
+        FGM_HOST_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&each, kernel, threads, smem));
+        *grid = N < static_cast<int64_t>(each) * sms ? N : static_cast<int64_t>(each) * sms;
+    }
+    return FGM_OK;
+}
+
+size_t gain_bytes(const norm::Args &a) { return sizeof(float) * (a.pre ? 2 : a.post ? 1 : 0) * a.D; }
+
+template <int VPT, int STAGES>
+int launch_staged(norm::Args &a, int threads, size_t row, int sms, cudaStream_t st)
+{
+    static std::atomic<bool> ready[64];
+    int64_t grid = 0;
+    a.keep = STAGES * row + gain_bytes(a) <= kNormSmem;
+    const size_t smem = STAGES * row + (a.keep ? gain_bytes(a) : 0);
+    FGM_HOST_TRY(norm_grid(norm::k_block_norm<VPT, STAGES>, ready, threads, smem, sms, a.N, &grid));
+    return launch_overlapped(norm::k_block_norm<VPT, STAGES>, dim3(static_cast<unsigned>(grid)), threads, smem, st, a);
+}
+
+// Three rows in shared memory, or one where three do not fit.
+template <int VPT>
+int launch_norm(norm::Args &a, int sms, cudaStream_t st)
+{
+    const int threads = (a.D + 256 * VPT - 1) / (256 * VPT) * 32, n = threads * VPT;
+    const size_t row = norm::piece_bytes(a.y, a.y.type, n) + norm::piece_bytes(a.h, a.h.type, n) + norm::piece_bytes(a.gate, a.gate.type, n);
+    if (3 * row + gain_bytes(a) <= kNormSmem)
+        return launch_staged<VPT, 3>(a, threads, row, sms, st);
+    return launch_staged<VPT, 1>(a, threads, row, sms, st);
+}
+
+template <bool F32>
+int launch_usual(const norm::Args &a, int sms, cudaStream_t st)
+{
+    static std::atomic<bool> ready[64];
+    int64_t grid = 0;
+    const int threads = (a.D + 255) / 256 * 32;
+    const bool scaled = a.post || (a.gate.p && a.gate.step);
+    const size_t smem = threads * (norm::kUsualStages * (F32 ? 48 : 32) + 32 * (a.pre ? 2 : scaled ? 1 : 0));
+    FGM_HOST_TRY(norm_grid(norm::k_block_norm_usual<F32>, ready, threads, smem, sms, a.N, &grid));
+    return launch_overlapped(norm::k_block_norm_usual<F32>, dim3(static_cast<unsigned>(grid)), threads, smem, st, a);
+}
+
+template <int VPT>
+int launch_any(norm::Args &a, int sms, cudaStream_t st)
+{
+    static std::atomic<bool> ready[64];
+    int64_t grid = 0;
+    const int threads = (a.D + 32 * VPT - 1) / (32 * VPT) * 32;
+    a.keep = 1;
+    const size_t smem = gain_bytes(a);
+    FGM_HOST_TRY(norm_grid(norm::k_block_norm_any<VPT>, ready, threads, smem, sms, a.N, &grid));
+    return launch_overlapped(norm::k_block_norm_any<VPT>, dim3(static_cast<unsigned>(grid)), threads, smem, st, a);
 }
 
 }  // namespace
@@ -116,7 +178,8 @@ extern "C" int fgm_block_norm(const fgm_block *b, void *stream)
         }
     if (clash)
         return failf(FGM_ERR_INVALID_ARG, "an output overlaps another tensor (h_out may be h; xn may be y or h)");
-    FGM_HOST_TRY(host_device_ready(nullptr));
+    int sms = 0;
+    FGM_HOST_TRY(host_device_ready(&sms));
 
     norm::Args a = {};
     a.h = {const_cast<void *>(b->h), b->h_stride, b->h_type, 1};
@@ -134,13 +197,19 @@ extern "C" int fgm_block_norm(const fgm_block *b, void *stream)
     a.b = b->block_scale;
     a.offset = b->gain_offset;
     a.eps = b->eps;
+    a.per_d = 1.0f / b->D;
     const bool vec = b->D % 8 == 0 && wide(b->h, b->h_stride, b->h_type) && wide(b->y, b->y_stride, b->y_type) &&
                      (!b->gate_col_stride || wide(b->gate, b->gate_row_stride, b->gate_type)) && wide(b->h_out, b->h_out_stride, b->h_type) &&
                      wide(b->xn, b->xn_stride, b->xn_type) && wide(b->post_gain, 0, b->gain_type) && wide(b->pre_gain, 0, b->gain_type);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (vec)
-        return b->D <= 4096 ? launch_norm<128, 4, 8>(a, st) : launch_norm<512, 4, 8>(a, st);
-    if (b->D <= 1024)
-        return launch_norm<128, 8, 1>(a, st);
-    return b->D <= 4096 ? launch_norm<512, 8, 1>(a, st) : launch_norm<512, 32, 1>(a, st);
+    if (vec) {
+        const bool usual = b->D <= 8 * norm::kUsualThreads && (!b->y || b->y_type == FGM_BF16) && (!b->xn || b->xn_type == FGM_BF16) &&
+                           (!b->gate || !b->gate_col_stride || !b->gate_row_stride || b->N == 1);
+        if (usual && b->h_type == FGM_BF16)
+            return launch_usual<false>(a, sms, st);
+        if (usual && b->h_type == FGM_F32)
+            return launch_usual<true>(a, sms, st);
+        return b->D <= 8192 ? launch_norm<1>(a, sms, st) : launch_norm<2>(a, sms, st);
+    }
+    return b->D <= 4096 ? launch_any<4>(a, sms, st) : launch_any<16>(a, sms, st);
 }

@@ -54,7 +54,7 @@ void cut_group(rows::GroupArgs &a)
     a.chunks = static_cast<int>((a.n + a.chunk - 1) / a.chunk);
 }
 
-size_t group_smem(int E) { return sizeof(int) * (rows::kGroupWarps + 1) * E; }
+size_t group_smem(int E) { return sizeof(int) * (rows::kGroupWarps + 2) * E; }
 
 int launch_deal(const rows::GroupArgs &a, cudaStream_t st)
 {
@@ -89,7 +89,7 @@ RouteWs route_ws(int64_t T)
     const int64_t s = route_splits(T);
     o.part = c.take(sizeof(float) * s * T * kE);
     o.xn2 = c.take(sizeof(float) * s * T);
-    o.wn2 = c.take(sizeof(float) * s * kE);
+    o.wn2 = c.take(sizeof(float) * s * 4);
     o.count = c.take(group_count_bytes(T * kK, kE));
     o.total = c.at;
     return o;

@@ -6,7 +6,7 @@
 // 128 tokens than SMs. k_router_logits runs M = 128 tokens x N = 128 experts on
 // tcgen05 and takes the accumulator out every 256 elements of K, to add it in fp32
 // registers: the tensor pipe truncates each addition, and 16 of them at a time stay
-// within 2^-18 |x| |w| in all.
+// within 2^-18 |x| |w| in all (16 of 2^-23 of a partial sum, twice over).
 //
 // Precision. Which experts a token takes is a whole number that hangs on logits that
 // may lie next to each other, so it goes by the exact ones. k_route_top knows a bound
@@ -14,7 +14,7 @@
 // helper warps sum up from the tiles in shared memory). Chosen experts further than
 // 2 d from every other candidate are in order; the others' logits are summed again
 // without rounding error to speak of (each addition's error is kept, 2^-40 of the sum
-// remains), and the 8 chosen by these. About one token in ten has such a pair.
+// remains), and the 8 chosen by these. About one token in twenty has such a pair.
 #pragma once
 
 #include "tensor.cuh"
@@ -22,7 +22,8 @@
 namespace fgm {
 namespace route {
 
-constexpr int kThreads = 384;                    // copies, products, two for norms, eight epilogue warps
+constexpr int kThreads = 576;                    // copies, products, eight epilogue warps; four for the tokens' norms, and
+                                                 // four for the experts' in the first tile's CTAs
 constexpr int kStages = 6;
 constexpr int kBox = 128 * 128;                  // 128 rows x 64 elements
 constexpr int kChunkBoxes = 4;                   // 256 elements of K between readings of the accumulator
@@ -35,7 +36,7 @@ struct LogitArgs {
     int splits;              // of K
     float *part;             // [splits][T][128]
     float *xn2;              // [splits][T] sums of squares
-    float *wn2;              // [splits][128]
+    float *wn2;              // [splits][4] the largest of each 32 experts
     int32_t *status;
     long long timeout_ns;
 };
@@ -88,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             tc::bar_init(&sh.full[i], 1);
-            tc::bar_init(&sh.empty[i], 3);       // the products and both norm warps
+            tc::bar_init(&sh.empty[i], tile == 0 ? 9 : 5);   // the products and the norm warps
         }
         for (int i = 0; i < 2; ++i) {
             tc::bar_init(&sh.tfull[i], 1);
@@ -150,34 +151,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::bar_drain(tc::saddr(&sh.drained), 0);
         }
         __syncwarp();
-    } else if (warp < 4) {
-        // norms of the tile's tokens, and of the experts' rows once
-        const int r = (warp - 2) * 32 + lane;
-        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        bool ok = true;
+    } else if (warp < 4 || warp >= 12) {
+        // norms: a thread a row
+        const int norm = warp < 4 ? warp - 2 : warp - 10, r = (norm & 3) * 32 + lane;
+        const bool experts = norm >= 4;
+        float sum = 0.0f;
+        bool ok = !experts || tile == 0;
         uint32_t n = 0;
         for (int b = b0; b < b1 && ok; ++b, ++n) {
-            const uint32_t slot = n % kStages, at = ring + slot * 2 * kBox + r * 128;
+            const uint32_t slot = n % kStages;
             ok = wait(&sh.full[slot], n / kStages, 41, b);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok)
                 break;
-            s[0] = squares(at, r, s[0]);
-            s[1] = squares(at + 64 * 128, r, s[1]);
-            if (tile == 0) {
-                s[2] = squares(at + kBox, r, s[2]);
-                s[3] = squares(at + kBox + 64 * 128, r, s[3]);
-            }
+            sum = squares(ring + slot * 2 * kBox + (experts ? kBox : 0) + r * 128, r, sum);
             __syncwarp();
             if (lane == 0)
                 tc::bar_arrive(tc::saddr(&sh.empty[slot]));
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (tile * 128 + r + h * 64 < p.T)
-                p.xn2[split * p.T + tile * 128 + r + h * 64] = s[h];
-            if (tile == 0)
-                p.wn2[split * kE + r + h * 64] = s[2 + h];
+        if (experts) {
+            const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(sum));
+            if (tile == 0 && lane == 0)
+                p.wn2[split * 4 + (norm & 3)] = __uint_as_float(most);
+        } else if (tile * 128 + r < p.T) {
+            p.xn2[split * p.T + tile * 128 + r] = sum;
         }
     } else {
         const int quarter = warp & 3, side = (warp - 4) >> 2;
@@ -246,32 +243,51 @@ struct TopArgs {
 
 constexpr int kTopWarps = 8;
 
-// x . w_e by one warp, each addition's rounding error added up beside the sum.
+// x . w_e by one warp: four sums a lane, each addition's rounding error added up beside it.
 __device__ __forceinline__ double exact_dot(const uint16_t *x, const uint16_t *w, int lane)
 {
-    float s = 0.0f, c = 0.0f;
+    float s[4], c[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        s[q] = c[q] = 0.0f;
+    uint4 a[kH / 256], b[kH / 256];
 #pragma unroll
     for (int i = 0; i < kH / 256; ++i) {
-        const uint4 a = __ldcg(reinterpret_cast<const uint4 *>(x) + i * 32 + lane), b = __ldcg(reinterpret_cast<const uint4 *>(w) + i * 32 + lane);
-        const uint32_t as[4] = {a.x, a.y, a.z, a.w}, bs[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const float2 u = bf16x2_to_f32(as[q]), v = bf16x2_to_f32(bs[q]);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float prod = __fmul_rn(h ? u.y : u.x, h ? v.y : v.x);    // (16 bits: exact)
-                const float t = __fadd_rn(s, prod), z = __fsub_rn(t, s);
-                c = __fadd_rn(c, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(prod, z)));
-                s = t;
-            }
-        }
+        a[i] = __ldcg(reinterpret_cast<const uint4 *>(x) + i * 32 + lane);
+        b[i] = __ldcg(reinterpret_cast<const uint4 *>(w) + i * 32 + lane);
     }
-    double d = static_cast<double>(s) + static_cast<double>(c);
+#pragma unroll
+    for (int i = 0; i < kH / 256; ++i) {
+        const uint32_t as[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, bs[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float2 u = bf16x2_to_f32(as[q]), v = bf16x2_to_f32(bs[q]);
+                const float prod = __fmul_rn(h ? u.y : u.x, h ? v.y : v.x);    // (16 bits: exact)
+                const float t = __fadd_rn(s[q], prod), z = __fsub_rn(t, s[q]);
+                c[q] = __fadd_rn(c[q], __fadd_rn(__fsub_rn(s[q], __fsub_rn(t, z)), __fsub_rn(prod, z)));
+                s[q] = t;
+            }
+    }
+    double d = 0.0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        d += static_cast<double>(s[q]) + static_cast<double>(c[q]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
     return d;
 }
+
+// Order-preserving whole numbers of floats (-0 as +0; NaNs do not occur here).
+__device__ __forceinline__ uint32_t order_key(float v)
+{
+    const int b = __float_as_int(v + 0.0f);
+    return static_cast<uint32_t>(b ^ ((b >> 31) | 0x80000000));
+}
+
+__device__ __forceinline__ float key_value(uint32_t k) { return __int_as_float(static_cast<int>(k & 0x80000000u ? k ^ 0x80000000u : ~k)); }
 
 // A warp per token; lane l has experts l, l + 32, l + 64, l + 96.
 __global__ void __launch_bounds__(32 * kTopWarps) k_route_top(const TopArgs p)
@@ -282,22 +298,28 @@ __global__ void __launch_bounds__(32 * kTopWarps) k_route_top(const TopArgs p)
     tc::let_next_start();
     if (t >= p.T)
         return;
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, b[4], x2 = 0.0f, w2 = 0.0f;
-#pragma unroll 4
-    for (int s = 0; s < p.splits; ++s) {
-        x2 += __ldcg(p.xn2 + s * p.T + t);
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, b[4], part[kChunks][4];
+    // (all of a token's parts on their way at once)
+    const float x2_part = lane < p.splits ? __ldcg(p.xn2 + lane * p.T + t) : 0.0f;
+    float w2_part = 0.0f;
+    if (lane < 4)
+#pragma unroll
+        for (int s = 0; s < kChunks; ++s)
+            w2_part += s < p.splits ? __ldcg(p.wn2 + s * 4 + lane) : 0.0f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        b[q] = p.b ? __ldcg(p.b + lane + 32 * q) : 0.0f;
+#pragma unroll
+    for (int s = 0; s < kChunks; ++s)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            v[q] += __ldcg(p.part + (s * p.T + t) * kE + lane + 32 * q);
-    }
+            part[s][q] = s < p.splits ? __ldcg(p.part + (s * p.T + t) * kE + lane + 32 * q) : 0.0f;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        float n2 = 0.0f;
-        for (int s = 0; s < p.splits; ++s)
-            n2 += __ldcg(p.wn2 + s * kE + lane + 32 * q);
-        w2 = fmaxf(w2, n2);
-        b[q] = p.b ? __ldcg(p.b + lane + 32 * q) : 0.0f;
-    }
+    for (int s = 0; s < kChunks; ++s)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            v[q] += part[s][q];
+    const float x2 = warp_sum(x2_part), w2 = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(w2_part)));
     bool bad = false;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -309,49 +331,39 @@ __global__ void __launch_bounds__(32 * kTopWarps) k_route_top(const TopArgs p)
     }
     if (__any_sync(0xFFFFFFFFu, bad) && lane == 0)
         atomicOr(p.status, FGM_STATUS_NONFINITE_LOGITS);
-    w2 = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(w2)));
 
-    double z[4];
+    // the 8 largest: the largest key left, and the lowest expert that has it
+    uint32_t key[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-        z[q] = static_cast<double>(v[q]);
+        key[q] = order_key(v[q]);
+    unsigned taken = 0;
     int top_i[kK];
     float top_v[kK];
-    auto choose = [&]() {
-        unsigned taken = 0;
 #pragma unroll
-        for (int r = 0; r < kK; ++r) {
-            float bv = -INFINITY;
-            int bi = 0x7FFFFFFF;
+    for (int r = 0; r < kK; ++r) {
+        uint32_t best = 0;
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (!(taken & (1u << q)) && better(v[q], lane + 32 * q, bv, bi)) {
-                    bv = v[q];
-                    bi = lane + 32 * q;
-                }
+        for (int q = 0; q < 4; ++q)
+            best = taken >> q & 1 ? best : max(best, key[q]);
+        best = __reduce_max_sync(0xFFFFFFFFu, best);
+        int e = kE;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                const float ov = __shfl_xor_sync(0xFFFFFFFFu, bv, o);
-                const int oi = __shfl_xor_sync(0xFFFFFFFFu, bi, o);
-                if (better(ov, oi, bv, bi)) {
-                    bv = ov;
-                    bi = oi;
-                }
-            }
-            if ((bi & 31) == lane)
-                taken |= 1u << (bi >> 5);
-            top_v[r] = bv;
-            top_i[r] = bi;
+        for (int q = 3; q >= 0; --q) {
+            const unsigned m = __ballot_sync(0xFFFFFFFFu, !(taken >> q & 1) && key[q] == best);
+            e = m ? q * 32 + __ffs(m) - 1 : e;
         }
-    };
-    choose();
-    // twice the bound of a candidate's error: 2^-17 |x| |w| of its products, 2^-23 of the sum with the bias
-    // (without an x the logits are the biases; experts masked by a bias of -inf have no near one)
+        taken |= (e & 31) == lane ? 1u << (e >> 5) : 0u;
+        top_v[r] = key_value(best);
+        top_i[r] = e;
+    }
+    // Twice the bound of a candidate's error: 2^-18 |x| |w| of its products, 2^-23 of the sum with the bias
+    // (without an x the logits are the biases; experts masked by a bias of -inf have no near one).
     float most = 0.0f;
 #pragma unroll
     for (int r = 0; r < kK; ++r)
         most = fabsf(top_v[r]) < INFINITY ? fmaxf(most, fabsf(top_v[r])) : most;
-    const float gap = x2 > 0.0f ? 2.0f * (0x1p-17f * sqrtf(x2) * sqrtf(w2) + 0x1p-23f * most) : 0.0f;
+    const float gap = x2 > 0.0f ? 2.0f * (0x1p-18f * sqrtf(x2) * sqrtf(w2) + 0x1p-23f * most) : 0.0f;
     if (gap > 0.0f && gap < INFINITY) {
         // candidates with another candidate within the gap
         unsigned cand = 0, near = 0;
@@ -369,6 +381,10 @@ __global__ void __launch_bounds__(32 * kTopWarps) k_route_top(const TopArgs p)
                         near |= 1u << j;
             }
         if (__any_sync(0xFFFFFFFFu, near != 0)) {
+            double z[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                z[q] = static_cast<double>(v[q]);
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 for (unsigned m = __ballot_sync(0xFFFFFFFFu, near >> q & 1); m; m &= m - 1) {
@@ -377,32 +393,27 @@ __global__ void __launch_bounds__(32 * kTopWarps) k_route_top(const TopArgs p)
                     if (lane == who)
                         z[q] = d + static_cast<double>(b[q]);
                 }
-            // the same choice by these
-            unsigned taken = 0;
+            // each candidate's place by these: as many as are before it
+            int place[4] = {0, 0, 0, 0};
 #pragma unroll
-            for (int r = 0; r < kK; ++r) {
-                double bv = -INFINITY;
-                int bi = 0x7FFFFFFF;
+            for (int q = 0; q < 4; ++q)
+                for (unsigned m = __ballot_sync(0xFFFFFFFFu, cand >> q & 1); m; m &= m - 1) {
+                    const int who = __ffs(m) - 1;
+                    const double other = __shfl_sync(0xFFFFFFFFu, z[q], who);
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (!(taken & (1u << q)) && (z[q] > bv || (z[q] == bv && lane + 32 * q < bi))) {
-                        bv = z[q];
-                        bi = lane + 32 * q;
-                    }
+                    for (int j = 0; j < 4; ++j)
+                        place[j] += other > z[j] || (other == z[j] && who + 32 * q < lane + 32 * j);
+                }
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    const double ov = __shfl_xor_sync(0xFFFFFFFFu, bv, o);
-                    const int oi = __shfl_xor_sync(0xFFFFFFFFu, bi, o);
-                    if (ov > bv || (ov == bv && oi < bi)) {
-                        bv = ov;
-                        bi = oi;
+            for (int r = 0; r < kK; ++r)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const unsigned m = __ballot_sync(0xFFFFFFFFu, (cand >> q & 1) && place[q] == r);
+                    if (m) {
+                        top_i[r] = q * 32 + __ffs(m) - 1;
+                        top_v[r] = __shfl_sync(0xFFFFFFFFu, static_cast<float>(z[q]), __ffs(m) - 1);
                     }
                 }
-                if ((bi & 31) == lane)
-                    taken |= 1u << (bi >> 5);
-                top_v[r] = static_cast<float>(bv);
-                top_i[r] = bi;
-            }
         }
     }
     float ex[kK], sum = 0.0f;
