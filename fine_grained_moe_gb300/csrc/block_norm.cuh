@@ -150,9 +150,15 @@ __device__ __forceinline__ void gain(const Args &p, const float *gains, int whic
     }
 }
 
+// Whether the usual types are built in (bf16 y, gate and xn; h in bf16 or fp32), a third of
+// an element-wise row's instructions.
+enum Types { kAnyTypes = 0, kBf16H = 1, kF32H = 2 };
+
+__device__ __forceinline__ constexpr int type_or(int built_in, int given, bool known) { return known ? built_in : given; }
+
 // One row: y, h and, where it has an element each, the gate in registers (fp32); `one`: its
 // gate where that is a value a row. VPT vectors of VEC elements a thread.
-template <int VPT, int VEC>
+template <int VPT, int VEC, Types T>
 __device__ __forceinline__ void one_row(const Args &p, int64_t row, float (&y)[VPT][VEC], float (&h)[VPT][VEC], float (&gate)[VPT][VEC], float one,
                                         const float *gains, float (*part)[32])
 {
@@ -197,7 +203,7 @@ __device__ __forceinline__ void one_row(const Args &p, int64_t row, float (&y)[V
         for (int i = 0; i < VPT; ++i) {
             const int d = (i * TPR + t) * VEC;
             if (d < p.D)
-                store<VEC>(p.h_out.p, p.h.type, row * p.h_out.stride + d, h[i]);
+                store<VEC>(p.h_out.p, type_or(T == kBf16H ? FGM_BF16 : FGM_F32, p.h.type, T != kAnyTypes), row * p.h_out.stride + d, h[i]);
         }
     if (!p.xn.p)
         return;
@@ -218,7 +224,7 @@ __device__ __forceinline__ void one_row(const Args &p, int64_t row, float (&y)[V
 #pragma unroll
             for (int q = 0; q < VEC; ++q)
                 g[q] = p.pre ? g[q] * (h[i][q] * r) : h[i][q] * r;
-            store<VEC>(p.xn.p, p.xn.type, row * p.xn.stride + d, g);
+            store<VEC>(p.xn.p, type_or(FGM_BF16, p.xn.type, T != kAnyTypes), row * p.xn.stride + d, g);
         }
     }
 }
@@ -315,7 +321,7 @@ __global__ void __launch_bounds__(1024) k_block_norm(const Args p)
         if (gb)
             take(p.gate.type, at + yb + hb, g);
         slot = slot + 1 < STAGES ? slot + 1 : 0;
-        one_row<VPT, 8>(p, row, y, h, g, one, gains, part);
+        one_row<VPT, 8, kAnyTypes>(p, row, y, h, g, one, gains, part);
         if (!(p.post_norm && p.y.p && p.xn.p))   // (the barriers of two sums keep rows apart; without one of them this does)
             __syncthreads();
     }
@@ -526,7 +532,7 @@ __global__ void __launch_bounds__(kUsualThreads, 4) k_block_norm_usual(const Arg
 }
 
 // Rows of any alignment, element by element, the next row's on their way (VPT = 4).
-template <int VPT>
+template <int VPT, Types T>
 __global__ void __launch_bounds__(1024) k_block_norm_any(const Args p)
 {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -536,20 +542,21 @@ __global__ void __launch_bounds__(1024) k_block_norm_any(const Args p)
     float *gains = reinterpret_cast<float *>(smem);
     tc::after_previous();
     tc::let_next_start();
-    auto bring = [&](const Rows &r, int64_t row, float (&v)[VPT][1]) {
+    auto bring = [&](const Rows &r, int built_in, int64_t row, float (&v)[VPT][1]) {
+        const int64_t first = row * r.stride + t;
+        const bool live = r.p && r.step && row < p.N;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int d = i * TPR + t;
             v[i][0] = 0.0f;
-            if (r.p && r.step && row < p.N && d < p.D)
-                load<1>(r.p, r.type, row * r.stride + d, v[i]);
+            if (live && i * TPR + t < p.D)
+                load<1>(r.p, type_or(built_in, r.type, T != kAnyTypes), first + i * TPR, v[i]);
         }
     };
     float y[VPT][1], h[VPT][1], g[VPT][1], y1[VPT][1], h1[VPT][1], g1[VPT][1];
     auto bring_all = [&](int64_t row, float (&y)[VPT][1], float (&h)[VPT][1], float (&g)[VPT][1]) {
-        bring(p.y, row, y);
-        bring(p.h, row, h);
-        bring(p.gate, row, g);
+        bring(p.y, FGM_BF16, row, y);
+        bring(p.h, T == kBf16H ? FGM_BF16 : FGM_F32, row, h);
+        bring(p.gate, FGM_BF16, row, g);
     };
     if (kAhead)
         bring_all(blockIdx.x, y1, h1, g1);
@@ -568,7 +575,7 @@ __global__ void __launch_bounds__(1024) k_block_norm_any(const Args p)
         } else {
             bring_all(row, y, h, g);
         }
-        one_row<VPT, 1>(p, row, y, h, g, one, gains, part);
+        one_row<VPT, 1, T>(p, row, y, h, g, one, gains, part);
         if (!(p.post_norm && p.y.p && p.xn.p))
             __syncthreads();
     }
