@@ -592,6 +592,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
         for (uint32_t i = e.first; i < e.to; ++i)
             tc::bar_drain(tc::saddr(&sh.full[i % stages]), (i / stages) & 1);
     }
+    // (the count goes by the weights' copies: after a wait that ran out, rows may have been sent for further on; a
+    // millisecond is a thousand times what they take)
+    if (tid == 0 && sh.abort) {
+        const long long end = tc::now_ns() + 1000000;
+        while (tc::now_ns() < end)
+            ;
+    }
     __syncthreads();
     tc::cluster_sync();
     if (warp == 1) {
