@@ -13,7 +13,8 @@ namespace rows {
 // Slots 0 .. n - 1 with ids[i] in [0, E) (others belong to no expert), stably sorted
 // by id: each chunk of slots is counted by a CTA; then each adds up the counts before
 // it (of smaller ids, and of its own id in earlier chunks) and deals its slots, a
-// warp a run of consecutive ones. No order of CTAs or atomics enters the result.
+// warp a run of consecutive ones. From 33 chunks on a kernel between them adds up the
+// counts once for all. No order of CTAs or atomics enters the result.
 
 constexpr int kGroupThreads = 256;
 constexpr int kGroupWarps = kGroupThreads / 32;
@@ -86,6 +87,67 @@ __device__ __forceinline__ void group_count(const GroupArgs &p, int chunk, int *
     }
 }
 
+constexpr int kDirectChunks = 32;
+
+// Counts to sums: count[c][e] becomes those of earlier chunks, offsets all of smaller experts; one CTA. (Each
+// dealing CTA adding up 128 chunks for itself: 21 us for 131,048 slots, where the three kernels take 14.)
+constexpr int kScanThreads = 1024;
+
+__global__ void __launch_bounds__(kScanThreads) k_group_scan(const GroupArgs p)
+{
+    __shared__ int part_sum[kScanThreads], warp_sum[32];
+    const int parts = kScanThreads / p.E, e = threadIdx.x % p.E, part = threadIdx.x / p.E, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c0 = p.chunks * part / parts, c1 = p.chunks * (part + 1) / parts;
+    int32_t *at = p.count + e;
+    tc::after_previous();
+    tc::let_next_start();
+    int sum = 0;
+    if (part < parts)
+#pragma unroll 16
+        for (int c = c0; c < c1; ++c)
+            sum += __ldcg(at + static_cast<int64_t>(c) * p.E);
+    part_sum[threadIdx.x] = sum;
+    __syncthreads();
+    int before = 0, all = 0;
+    if (part < parts)
+        for (int q = 0; q < parts; ++q) {
+            const int v = part_sum[q * p.E + e];
+            before += q < part ? v : 0;
+            all += v;
+        }
+    if (part < parts)
+        for (int c = c0; c < c1; c += 16) {
+            int v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                v[i] = c + i < c1 ? __ldcg(at + static_cast<int64_t>(c + i) * p.E) : 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                if (c + i < c1)
+                    at[static_cast<int64_t>(c + i) * p.E] = before;
+                before += v[i];
+            }
+        }
+    int mine = part == 0 ? all : 0, incl = mine; // (the first E threads have an expert each)
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        incl += lane >= o ? u : 0;
+    }
+    if (lane == 31)
+        warp_sum[warp] = incl;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w)
+        incl += warp_sum[w];
+    if (part == 0) {
+        if (e == 0)
+            p.offsets[0] = 0;
+        p.offsets[e + 1] = incl;
+        if (e == p.E - 1 && p.shared)
+            p.offsets[p.E + 1] = incl + p.shared;
+    }
+}
+
 // The same CTA's slots dealt; hist: [kGroupWarps][E], then [2][E] totals.
 __device__ __forceinline__ void group_deal(const GroupArgs &p, int chunk, int *hist)
 {
@@ -102,10 +164,13 @@ __device__ __forceinline__ void group_deal(const GroupArgs &p, int chunk, int *h
     // slots of each expert in all chunks and in those before: threads share out the chunks where experts are few
     int *before = total + p.E;
     const int parts = p.E < kGroupThreads ? kGroupThreads / p.E : 1;
-    for (int e = threadIdx.x; e < p.E; e += kGroupThreads)
-        total[e] = before[e] = 0;
+    const bool scanned = p.chunks > kDirectChunks;
+    for (int e = threadIdx.x; e < p.E; e += kGroupThreads) {
+        total[e] = scanned ? __ldcg(p.offsets + e) : 0;
+        before[e] = scanned ? __ldcg(p.count + static_cast<int64_t>(chunk) * p.E + e) : 0;
+    }
     __syncthreads();
-    if (p.chunks > 1)
+    if (p.chunks > 1 && !scanned)
         for (int i = threadIdx.x; i < p.E * parts; i += kGroupThreads) {
             const int e = i % p.E, part = i / p.E;
             int sum = 0, sum_before = 0;
@@ -131,37 +196,39 @@ __device__ __forceinline__ void group_deal(const GroupArgs &p, int chunk, int *h
             total[e] = mine;
     }
     __syncthreads();
-    // places before each expert: a thread scans E / 256 experts, rounded up
-    const int each = (p.E + kGroupThreads - 1) / kGroupThreads, e0 = threadIdx.x * each;
-    int sum = 0;
-    for (int e = e0; e < e0 + each && e < p.E; ++e)
-        sum += total[e];
-    int incl = sum;
+    int all = scanned ? __ldcg(p.offsets + p.E) : 0;
+    if (!scanned) {
+        // places before each expert: a thread scans E / 256 experts, rounded up
+        const int each = (p.E + kGroupThreads - 1) / kGroupThreads, e0 = threadIdx.x * each;
+        int sum = 0;
+        for (int e = e0; e < e0 + each && e < p.E; ++e)
+            sum += total[e];
+        int incl = sum;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        incl += lane >= o ? u : 0;
-    }
-    if (lane == 31)
-        warp_sum[warp] = incl;
-    __syncthreads();
-    int base = incl - sum;
-    for (int w = 0; w < warp; ++w)
-        base += warp_sum[w];
-    for (int e = e0; e < e0 + each && e < p.E; ++e) {
-        const int v = total[e];
-        total[e] = base;
-        if (chunk == 0)
-            p.offsets[e] = base;
-        base += v;
-    }
-    int all = 0;
-    for (int w = 0; w < kGroupWarps; ++w)
-        all += warp_sum[w];
-    if (chunk == 0 && threadIdx.x == 0) {
-        p.offsets[p.E] = all;
-        if (p.shared)
-            p.offsets[p.E + 1] = all + p.shared;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            incl += lane >= o ? u : 0;
+        }
+        if (lane == 31)
+            warp_sum[warp] = incl;
+        __syncthreads();
+        int base = incl - sum;
+        for (int w = 0; w < warp; ++w)
+            base += warp_sum[w];
+        for (int e = e0; e < e0 + each && e < p.E; ++e) {
+            const int v = total[e];
+            total[e] = base;
+            if (chunk == 0)
+                p.offsets[e] = base;
+            base += v;
+        }
+        for (int w = 0; w < kGroupWarps; ++w)
+            all += warp_sum[w];
+        if (chunk == 0 && threadIdx.x == 0) {
+            p.offsets[p.E] = all;
+            if (p.shared)
+                p.offsets[p.E + 1] = all + p.shared;
+        }
     }
     __syncthreads();
     int *at = hist + warp * p.E;

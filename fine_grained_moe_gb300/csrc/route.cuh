@@ -241,43 +241,44 @@ struct TopArgs {
     int32_t *status;
 };
 
-constexpr int kTopWarps = 8;
+constexpr int kTopWarps = 2;                    // (a CTA holds its place until its last token is done, one in twenty of which takes longer)
 
-// x . w_e by one warp: four sums a lane, each addition's rounding error added up beside it.
-__device__ __forceinline__ double exact_dot(const uint16_t *x, const uint16_t *w, int lane)
+// x . w of two experts by one warp: two sums a lane of each, each addition's rounding error
+// added up beside it.
+__device__ __forceinline__ void exact_dots(const uint16_t *x, const uint16_t *w0, const uint16_t *w1, int lane, double &d0, double &d1)
 {
-    float s[4], c[4];
+    float s[2][2], c[2][2];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-        s[q] = c[q] = 0.0f;
-    uint4 a[kH / 256], b[kH / 256];
-#pragma unroll
+    for (int q = 0; q < 2; ++q)
+        s[0][q] = s[1][q] = c[0][q] = c[1][q] = 0.0f;
+#pragma unroll 4
     for (int i = 0; i < kH / 256; ++i) {
-        a[i] = __ldcg(reinterpret_cast<const uint4 *>(x) + i * 32 + lane);
-        b[i] = __ldcg(reinterpret_cast<const uint4 *>(w) + i * 32 + lane);
-    }
+        const uint4 a = __ldcg(reinterpret_cast<const uint4 *>(x) + i * 32 + lane), b0 = __ldcg(reinterpret_cast<const uint4 *>(w0) + i * 32 + lane),
+                    b1 = __ldcg(reinterpret_cast<const uint4 *>(w1) + i * 32 + lane);
+        const uint32_t as[4] = {a.x, a.y, a.z, a.w}, bs[2][4] = {{b0.x, b0.y, b0.z, b0.w}, {b1.x, b1.y, b1.z, b1.w}};
 #pragma unroll
-    for (int i = 0; i < kH / 256; ++i) {
-        const uint32_t as[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, bs[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+        for (int q = 0; q < 4; ++q) {
+            const float2 u = bf16x2_to_f32(as[q]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+            for (int k = 0; k < 2; ++k) {
+                const float2 v = bf16x2_to_f32(bs[k][q]);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float2 u = bf16x2_to_f32(as[q]), v = bf16x2_to_f32(bs[q]);
-                const float prod = __fmul_rn(h ? u.y : u.x, h ? v.y : v.x);    // (16 bits: exact)
-                const float t = __fadd_rn(s[q], prod), z = __fsub_rn(t, s[q]);
-                c[q] = __fadd_rn(c[q], __fadd_rn(__fsub_rn(s[q], __fsub_rn(t, z)), __fsub_rn(prod, z)));
-                s[q] = t;
+                for (int h = 0; h < 2; ++h) {
+                    const float prod = __fmul_rn(h ? u.y : u.x, h ? v.y : v.x);    // (16 bits: exact)
+                    const float t = __fadd_rn(s[k][h], prod), z = __fsub_rn(t, s[k][h]);
+                    c[k][h] = __fadd_rn(c[k][h], __fadd_rn(__fsub_rn(s[k][h], __fsub_rn(t, z)), __fsub_rn(prod, z)));
+                    s[k][h] = t;
+                }
             }
+        }
     }
-    double d = 0.0;
+    d0 = (static_cast<double>(s[0][0]) + static_cast<double>(c[0][0])) + (static_cast<double>(s[0][1]) + static_cast<double>(c[0][1]));
+    d1 = (static_cast<double>(s[1][0]) + static_cast<double>(c[1][0])) + (static_cast<double>(s[1][1]) + static_cast<double>(c[1][1]));
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-        d += static_cast<double>(s[q]) + static_cast<double>(c[q]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
-    return d;
+    for (int o = 16; o > 0; o >>= 1) {
+        d0 += __shfl_xor_sync(0xFFFFFFFFu, d0, o);
+        d1 += __shfl_xor_sync(0xFFFFFFFFu, d1, o);
+    }
 }
 
 // Order-preserving whole numbers of floats (-0 as +0; NaNs do not occur here).
@@ -289,8 +290,9 @@ __device__ __forceinline__ uint32_t order_key(float v)
 
 __device__ __forceinline__ float key_value(uint32_t k) { return __int_as_float(static_cast<int>(k & 0x80000000u ? k ^ 0x80000000u : ~k)); }
 
-// A warp per token; lane l has experts l, l + 32, l + 64, l + 96.
-__global__ void __launch_bounds__(32 * kTopWarps) k_route_top(const TopArgs p)
+// A warp per token; lane l has experts l, l + 32, l + 64, l + 96. MOST: splits at most.
+template <int MOST>
+__global__ void __launch_bounds__(32 * kTopWarps, 14) k_route_top(const TopArgs p)
 {
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kTopWarps + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
@@ -298,24 +300,24 @@ __global__ void __launch_bounds__(32 * kTopWarps) k_route_top(const TopArgs p)
     tc::let_next_start();
     if (t >= p.T)
         return;
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, b[4], part[kChunks][4];
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, b[4], part[MOST][4];
     // (all of a token's parts on their way at once)
     const float x2_part = lane < p.splits ? __ldcg(p.xn2 + lane * p.T + t) : 0.0f;
     float w2_part = 0.0f;
     if (lane < 4)
 #pragma unroll
-        for (int s = 0; s < kChunks; ++s)
+        for (int s = 0; s < MOST; ++s)
             w2_part += s < p.splits ? __ldcg(p.wn2 + s * 4 + lane) : 0.0f;
 #pragma unroll
     for (int q = 0; q < 4; ++q)
         b[q] = p.b ? __ldcg(p.b + lane + 32 * q) : 0.0f;
 #pragma unroll
-    for (int s = 0; s < kChunks; ++s)
+    for (int s = 0; s < MOST; ++s)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
             part[s][q] = s < p.splits ? __ldcg(p.part + (s * p.T + t) * kE + lane + 32 * q) : 0.0f;
 #pragma unroll
-    for (int s = 0; s < kChunks; ++s)
+    for (int s = 0; s < MOST; ++s)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
             v[q] += part[s][q];
@@ -385,14 +387,34 @@ __global__ void __launch_bounds__(32 * kTopWarps) k_route_top(const TopArgs p)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 z[q] = static_cast<double>(v[q]);
+            // (two at a time: near ones come in pairs)
+            unsigned left[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                for (unsigned m = __ballot_sync(0xFFFFFFFFu, near >> q & 1); m; m &= m - 1) {
-                    const int who = __ffs(m) - 1;
-                    const double d = exact_dot(p.x + t * p.stride, p.w + static_cast<int64_t>(who + 32 * q) * kH, lane);
-                    if (lane == who)
-                        z[q] = d + static_cast<double>(b[q]);
+                left[q] = __ballot_sync(0xFFFFFFFFu, near >> q & 1);
+            auto first = [&]() {
+                int e = -1;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (e < 0 && left[q]) {
+                        e = q * 32 + __ffs(left[q]) - 1;
+                        left[q] &= left[q] - 1;
+                    }
+                return e;
+            };
+            for (int e0 = first(); e0 >= 0; e0 = first()) {
+                int e1 = first();
+                e1 = e1 < 0 ? e0 : e1;
+                double d0, d1;
+                exact_dots(p.x + t * p.stride, p.w + static_cast<int64_t>(e0) * kH, p.w + static_cast<int64_t>(e1) * kH, lane, d0, d1);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (lane + 32 * q == e0)
+                        z[q] = d0 + static_cast<double>(b[q]);
+                    if (lane + 32 * q == e1)
+                        z[q] = d1 + static_cast<double>(b[q]);
                 }
+            }
             // each candidate's place by these: as many as are before it
             int place[4] = {0, 0, 0, 0};
 #pragma unroll

@@ -45,9 +45,12 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar)
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Waits up to a tenth of a second for what is in flight after an abort.
+// Waits up to a tenth of a second for what is in flight after an abort. (The timer is
+// read when there is something to wait for: it takes a fifth of a microsecond.)
 __device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity)
 {
+    if (bar_try(bar, parity))
+        return;
     const long long end = now_ns() + 100000000LL;
     while (!bar_try(bar, parity) && now_ns() < end)
         ;
