@@ -189,7 +189,8 @@ def select_path(path: int) -> int:
 
 
 def set_wait_limit_ns(ns: int) -> int:
-    """Bound on every wait inside the persistent kernel, attn_fwd's and lm_head_logprobs' (ns < 0 only queries)."""
+    """Bound on every wait inside the persistent kernel, attn_fwd's, lm_head_logprobs', moe_route's, grouped_gemm's and
+    moe_experts_fwd's (ns < 0 only queries)."""
     return int(lib().fgm_set_wait_limit_ns(int(ns)))
 
 

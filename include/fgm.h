@@ -584,8 +584,9 @@ int fgm_block_norm(const fgm_block *b, void *stream);
 int fgm_select_path(int path);
 
 /* Upper bound, in ns of GPU time, on every wait inside the persistent kernel
- * (grid barriers, ring slots) and inside those of fgm_attn_fwd and
- * fgm_lm_head_logprobs (there each wait has the limit to itself). When a wait runs
+ * (grid barriers, ring slots) and inside those of fgm_attn_fwd,
+ * fgm_lm_head_logprobs, fgm_moe_route, fgm_grouped_gemm and fgm_moe_experts_fwd
+ * (there each wait has the limit to itself). When a wait runs
  * out the kernel raises FGM_STATUS_WAIT_TIMEOUT, skips its remaining work and
  * exits; its outputs are then invalid. Default 2 s; ns < 0 only queries. Returns the previous value. */
 long long fgm_set_wait_limit_ns(long long ns);
@@ -630,7 +631,10 @@ int fgm_read_status(void *ws, size_t ws_bytes, int clear, int32_t *status, void 
  * come from the barrier (6) or from a producer waiting for the routing that
  * the barrier holds back (2). 13 to 28: a wait of fgm_attn_fwd (index = the
  * CTA's unit of 128 tokens); 30 to 33: of fgm_lm_head_logprobs on more than 8
- * rows (30 copies, 31 and 32 products, 33 sums). Synchronises the stream. */
+ * rows (30 copies, 31 and 32 products, 33 sums); 34 to 37 and 43: of the grouped
+ * products (34 and 43 copies, 35 and 36 products, 37 results); 38 to 42: of
+ * fgm_moe_route's logits; 44 and 45: of the experts' weighted sum. Synchronises the
+ * stream. */
 int fgm_read_wait_report(void *ws, size_t ws_bytes, int32_t *report, void *stream);
 
 /* Message describing the last error returned on the calling thread. */
