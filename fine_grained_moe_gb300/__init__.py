@@ -868,15 +868,21 @@ def moe_route(router_w: torch.Tensor, x: torch.Tensor, router_b: torch.Tensor | 
     w_at = _expect("router_w", router_w, (EXPERTS, HIDDEN), _BF16, dev)
     b_at = None if router_b is None else _expect("router_b", router_b, (EXPERTS,), _F32, dev)
 
+    if out is not None:
+        for name, shape, dt in (("ids", (T, TOPK), _I32), ("weights", (T, TOPK), _F32), ("offsets", (EXPERTS + 1,), _I32),
+                                ("order", (T * TOPK,), _I32)):
+            _expect("out." + name, getattr(out, name), shape, dt, dev)
+
     def body(s):
-        i32 = dict(dtype=_I32, device=dev)
-        r = Routing(torch.empty((T, TOPK), **i32), torch.empty((T, TOPK), dtype=_F32, device=dev),
-                    torch.empty(EXPERTS + 1, **i32), torch.empty(T * TOPK, **i32)) if out is None else out
+        if out is None:
+            r = Routing(torch.empty((T, TOPK), dtype=_I32, device=dev), torch.empty((T, TOPK), dtype=_F32, device=dev),
+                        torch.empty(EXPERTS + 1, dtype=_I32, device=dev), torch.empty(T * TOPK, dtype=_I32, device=dev))
+        else:
+            r = out
         w = Workspace(dev, nbytes=moe_route_workspace_bytes(T)) if ws is None else ws
-        _check(lib().fgm_moe_route(w_at, b_at, x.data_ptr(), stride, T, _expect("out.ids", r.ids, (T, TOPK), _I32, dev),
-                                   _expect("out.weights", r.weights, (T, TOPK), _F32, dev),
-                                   _expect("out.offsets", r.offsets, (EXPERTS + 1,), _I32, dev),
-                                   _expect("out.order", r.order, (T * TOPK,), _I32, dev), w.t.data_ptr(), w.nbytes, s))
+        i, t, o, n = r
+        _check(lib().fgm_moe_route(w_at, b_at, x.data_ptr(), stride, T, i.data_ptr(), t.data_ptr(), o.data_ptr(), n.data_ptr(),
+                                   w.t.data_ptr(), w.nbytes, s))
         return r
     return _call(dev, stream, body)
 
@@ -936,11 +942,14 @@ def grouped_gemm(x: torch.Tensor, w: torch.Tensor, w_s: torch.Tensor | None, off
     R = x.shape[0] if rows is None else rows.shape[0]
     r_at = None if rows is None else _expect("rows", rows, (R,), _I32, dev)
 
+    if out is not None:
+        _expect("out", out, (R, N), _BF16, dev)
+
     def body(s):
         o = torch.empty((R, N), dtype=_BF16, device=dev) if out is None else out
         v = Workspace(dev, nbytes=grouped_gemm_workspace_bytes(x.shape[0], R, E, N, K)) if ws is None else ws
         _check(lib().fgm_grouped_gemm(x.data_ptr(), stride, x.shape[0], r_at, per, o_at, w_at, E4M3 if w.dtype is _U8 else 1, s_at,
-                                      E, N, K, _expect("out", o, (R, N), _BF16, dev), R, v.t.data_ptr(), v.nbytes, s))
+                                      E, N, K, o.data_ptr(), R, v.t.data_ptr(), v.nbytes, s))
         return o
     return _call(dev, stream, body)
 
@@ -984,6 +993,14 @@ def _norm_rows(name: str, t: torch.Tensor, shape, device) -> tuple[int, int, int
     return t.data_ptr(), kind, sn if shape[0] > 1 else max(sn, shape[1])
 
 
+def _gain(t: torch.Tensor, D: int, device, dtype) -> tuple[int, int]:
+    """(address, type) of a norm's gains."""
+    kind = _DTYPES.get(t.dtype)
+    if kind is None or t.shape != (D,) or t.device != device or not t.is_contiguous() or t.dtype is not dtype:
+        raise FgmError(f"gains: expected contiguous [{D}] of one type on {device}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr(), kind
+
+
 def block_norm(h: torch.Tensor, y: torch.Tensor | None = None, post_gain: torch.Tensor | None = None,
                gate: torch.Tensor | None = None, pre_gain: torch.Tensor | None = None, post_norm: bool = True,
                pre_norm: bool = True, residual_scale: float = 1.0, block_scale: float = 1.0, gain_offset: float = 0.0,
@@ -1008,27 +1025,31 @@ def block_norm(h: torch.Tensor, y: torch.Tensor | None = None, post_gain: torch.
             raise FgmError(f"gate: expected dense rows, strides {gate.stride()}")
         g_at, g_type = gate.data_ptr(), _DTYPES[gate.dtype]
         g_rows = gate.stride(0) if gate.dim() == 2 and N > 1 else 0
-    gain_type = 0
-    for t in (post_gain, pre_gain):
-        if t is not None:
-            one = post_gain if post_gain is not None else pre_gain
-            if t.dtype not in _DTYPES or t.shape != (D,) or t.device != dev or not t.is_contiguous() or t.dtype is not one.dtype:
-                raise FgmError(f"gains: expected contiguous [{D}] of one type on {dev}, got {tuple(t.shape)} {t.dtype} on {t.device}")
-            gain_type = _DTYPES[t.dtype]
+    gain_type, p_at, q_at = 0, None, None
+    if post_gain is not None:
+        p_at, gain_type = _gain(post_gain, D, dev, post_gain.dtype)
+    if pre_gain is not None:
+        q_at, gain_type = _gain(pre_gain, D, dev, pre_gain.dtype if post_gain is None else post_gain.dtype)
     if xn is not None and not pre_norm:
         raise FgmError("xn without pre_norm")
 
     def body(s):
-        o = torch.empty(shape, dtype=h.dtype, device=dev) if h_out is None else h_out
-        o_at, o_type, o_step = _norm_rows("h_out", o, shape, dev)
-        if o_type != h_type:
-            raise FgmError(f"h_out: expected {h.dtype}, got {o.dtype}")
-        n, n_at, n_type, n_step = None, None, 0, 0
-        if pre_norm:
-            n = torch.empty(shape, dtype=_BF16, device=dev) if xn is None else xn
+        if h_out is None:
+            o = torch.empty(shape, dtype=h.dtype, device=dev)
+            o_at, o_step = o.data_ptr(), D
+        else:
+            o = h_out
+            o_at, o_type, o_step = _norm_rows("h_out", o, shape, dev)
+            if o_type != h_type:
+                raise FgmError(f"h_out: expected {h.dtype}, got {o.dtype}")
+        n, n_at, n_type, n_step = xn, None, 0, 0
+        if xn is not None:
             n_at, n_type, n_step = _norm_rows("xn", n, shape, dev)
+        elif pre_norm:
+            n = torch.empty(shape, dtype=_BF16, device=dev)
+            n_at, n_type, n_step = n.data_ptr(), 1, D
         _check(lib().fgm_block_norm(fgm_block(
-            N, D, h_type, y_type, g_type, gain_type, n_type, h_at, y_at, g_at, _at(post_gain), _at(pre_gain), o_at, n_at, h_step,
+            N, D, h_type, y_type, g_type, gain_type, n_type, h_at, y_at, g_at, p_at, q_at, o_at, n_at, h_step,
             y_step, g_rows, o_step, n_step, g_cols, post_norm and y is not None, residual_scale, block_scale, gain_offset, eps), s))
         return o, n
     return _call(dev, stream, body)

@@ -150,6 +150,31 @@ def test_rows_apart_and_odd_outputs(fgm):
     assert room[0] == 0
 
 
+@pytest.mark.parametrize("K", [8, 24, 56, 72, 200, 1000])
+def test_bf16_rows_that_end_inside_a_step(fgm, K):
+    """16 elements of K are a step of the products; what lies behind K, here infinities, is not read."""
+    g = torch.Generator(device="cuda").manual_seed(K)
+    w, _ = weights(3, 50, K, "bf16", g)
+    wide = torch.full((90, K + 64), math.inf, dtype=torch.bfloat16, device="cuda")
+    wide[:, :K] = torch.randn(90, K, generator=g, device="cuda").bfloat16()
+    x = wide[:, :K]
+    off = torch.tensor([0, 30, 33, 90], dtype=torch.int32, device="cuda")
+    check(fgm.grouped_gemm(x, w, None, off), x, w, None, off.tolist())
+    rows = torch.randperm(90, generator=g, device="cuda").int()
+    check(fgm.grouped_gemm(x, w, None, off, rows=rows), x, w, None, off.tolist(), rows=rows.long())
+
+
+@pytest.mark.parametrize("K", [16, 48, 112, 1040])
+def test_e4m3_rows_that_end_inside_a_step(fgm, K):
+    g = torch.Generator(device="cuda").manual_seed(K)
+    w, s = weights(3, 50, K, "e4m3", g)
+    wide = torch.full((90, K + 64), math.nan, dtype=torch.bfloat16, device="cuda")
+    wide[:, :K] = torch.randn(90, K, generator=g, device="cuda").bfloat16()
+    x = wide[:, :K]
+    off = torch.tensor([0, 30, 33, 90], dtype=torch.int32, device="cuda")
+    check(fgm.grouped_gemm(x, w, s, off), x, w, s, off.tolist())
+
+
 def test_the_same_bits_again(fgm):
     g = torch.Generator(device="cuda").manual_seed(7)
     w, s = weights(20, 320, 512, "e4m3", g)
