@@ -107,7 +107,17 @@ int launch_usual(const norm::Args &a, int sms, cudaStream_t st)
     return launch_overlapped(norm::k_block_norm_usual<F32>, dim3(static_cast<unsigned>(grid)), threads, smem, st, a);
 }
 
-template <int VPT, norm::Types T>
+template <bool F32, bool GATE>
+int launch_odd(const norm::Args &a, int sms, cudaStream_t st)
+{
+    static std::atomic<bool> ready[64];
+    int64_t grid = 0;
+    const int threads = (a.D + 32 * norm::kOddVals - 1) / (32 * norm::kOddVals) * 32;
+    FGM_HOST_TRY(norm_grid(norm::k_block_norm_odd<F32, GATE>, ready, threads, 0, sms, a.N, &grid));
+    return launch_overlapped(norm::k_block_norm_odd<F32, GATE>, dim3(static_cast<unsigned>(grid)), threads, 0, st, a);
+}
+
+template <int VPT>
 int launch_any(norm::Args &a, int sms, cudaStream_t st)
 {
     static std::atomic<bool> ready[64];
@@ -115,8 +125,8 @@ int launch_any(norm::Args &a, int sms, cudaStream_t st)
     const int threads = (a.D + 32 * VPT - 1) / (32 * VPT) * 32;
     a.keep = 1;
     const size_t smem = gain_bytes(a);
-    FGM_HOST_TRY(norm_grid(norm::k_block_norm_any<VPT, T>, ready, threads, smem, sms, a.N, &grid));
-    return launch_overlapped(norm::k_block_norm_any<VPT, T>, dim3(static_cast<unsigned>(grid)), threads, smem, st, a);
+    FGM_HOST_TRY(norm_grid(norm::k_block_norm_any<VPT>, ready, threads, smem, sms, a.N, &grid));
+    return launch_overlapped(norm::k_block_norm_any<VPT>, dim3(static_cast<unsigned>(grid)), threads, smem, st, a);
 }
 
 }  // namespace
@@ -212,11 +222,12 @@ extern "C" int fgm_block_norm(const fgm_block *b, void *stream)
         return b->D <= 8192 ? launch_norm<1>(a, sms, st) : launch_norm<2>(a, sms, st);
     }
     if (b->D > 4096)
-        return launch_any<16, norm::kAnyTypes>(a, sms, st);
-    const bool usual = (!b->y || b->y_type == FGM_BF16) && (!b->xn || b->xn_type == FGM_BF16) && (!b->gate || b->gate_type == FGM_BF16);
+        return launch_any<16>(a, sms, st);
+    const bool full = b->gate && b->gate_col_stride && b->gate_row_stride,
+               usual = (!b->y || b->y_type == FGM_BF16) && (!b->xn || b->xn_type == FGM_BF16) && (!full || b->gate_type == FGM_BF16);
     if (usual && b->h_type == FGM_BF16)
-        return launch_any<4, norm::kBf16H>(a, sms, st);
+        return full ? launch_odd<false, true>(a, sms, st) : launch_odd<false, false>(a, sms, st);
     if (usual && b->h_type == FGM_F32)
-        return launch_any<4, norm::kF32H>(a, sms, st);
-    return launch_any<4, norm::kAnyTypes>(a, sms, st);
+        return full ? launch_odd<true, true>(a, sms, st) : launch_odd<true, false>(a, sms, st);
+    return launch_any<4>(a, sms, st);
 }
