@@ -293,7 +293,7 @@ __device__ __forceinline__ float key_value(uint32_t k) { return __int_as_float(s
 
 // A warp per token; lane l has experts l, l + 32, l + 64, l + 96. MOST: splits at most.
 template <int MOST>
-__global__ void __launch_bounds__(32 * kTopWarps, 14) k_route_top(const TopArgs p)
+__global__ void __launch_bounds__(32 * kTopWarps, MOST == 1 ? 20 : 14) k_route_top(const TopArgs p)
 {
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kTopWarps + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
