@@ -416,16 +416,25 @@ __global__ void __launch_bounds__(32 * kTopWarps, MOST == 1 ? 20 : 14) k_route_t
                         z[q] = d1 + static_cast<double>(b[q]);
                 }
             }
-            // each candidate's place by these: as many as are before it
+            // each candidate's place by these: as many as are before it (as whole numbers in their order: a comparison of
+            // doubles takes this GPU 16 cycles)
+            uint64_t order[4];
+            float near_v[4];
             int place[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const long long bits = __double_as_longlong(z[q] + 0.0);
+                order[q] = static_cast<uint64_t>(bits ^ ((bits >> 63) | (1LL << 63)));
+                near_v[q] = static_cast<float>(z[q]);
+            }
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 for (unsigned m = __ballot_sync(0xFFFFFFFFu, cand >> q & 1); m; m &= m - 1) {
                     const int who = __ffs(m) - 1;
-                    const double other = __shfl_sync(0xFFFFFFFFu, z[q], who);
+                    const uint64_t other = __shfl_sync(0xFFFFFFFFu, order[q], who);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        place[j] += other > z[j] || (other == z[j] && who + 32 * q < lane + 32 * j);
+                        place[j] += other > order[j] || (other == order[j] && who + 32 * q < lane + 32 * j);
                 }
 #pragma unroll
             for (int r = 0; r < kK; ++r)
@@ -434,7 +443,7 @@ __global__ void __launch_bounds__(32 * kTopWarps, MOST == 1 ? 20 : 14) k_route_t
                     const unsigned m = __ballot_sync(0xFFFFFFFFu, (cand >> q & 1) && place[q] == r);
                     if (m) {
                         top_i[r] = q * 32 + __ffs(m) - 1;
-                        top_v[r] = __shfl_sync(0xFFFFFFFFu, static_cast<float>(z[q]), __ffs(m) - 1);
+                        top_v[r] = __shfl_sync(0xFFFFFFFFu, near_v[q], __ffs(m) - 1);
                     }
                 }
         }
