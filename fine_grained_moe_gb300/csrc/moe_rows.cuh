@@ -45,12 +45,16 @@ __device__ __forceinline__ void load_ids(const GroupArgs &p, int64_t i, int64_t 
         id[j] = i + 32 * j < i1 ? __ldcg(p.ids + i + 32 * j) : -1;
 }
 
-// Counts of a warp's run of slots in its own row of hist.
-__device__ __forceinline__ void count_run(const GroupArgs &p, int64_t i0, int64_t i1, int *hist, int lane)
+// Counts of a warp's run of slots in its own row of hist; the run's first ids are in `head`.
+__device__ __forceinline__ void count_run(const GroupArgs &p, int64_t i0, int64_t i1, const int (&head)[kIdsAhead], int *hist, int lane)
 {
     for (int64_t i = i0; i < i1; i += 32 * kIdsAhead) {
         int id[kIdsAhead];
-        load_ids(p, i + lane, i1, id);
+#pragma unroll
+        for (int j = 0; j < kIdsAhead; ++j)
+            id[j] = head[j];
+        if (i > i0)
+            load_ids(p, i + lane, i1, id);
 #pragma unroll
         for (int j = 0; j < kIdsAhead; ++j) {
             const unsigned same = __match_any_sync(0xFFFFFFFFu, id[j]);
@@ -72,12 +76,14 @@ __device__ __forceinline__ void run_of(const GroupArgs &p, int chunk, int warp, 
 __device__ __forceinline__ void group_count(const GroupArgs &p, int chunk, int *hist)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int64_t i0, i1;
+    int head[kIdsAhead];
+    run_of(p, chunk, warp, i0, i1);
+    load_ids(p, i0 + lane, i1, head);
     for (int i = threadIdx.x; i < kGroupWarps * p.E; i += kGroupThreads)
         hist[i] = 0;
     __syncthreads();
-    int64_t i0, i1;
-    run_of(p, chunk, warp, i0, i1);
-    count_run(p, i0, i1, hist + warp * p.E, lane);
+    count_run(p, i0, i1, head, hist + warp * p.E, lane);
     __syncthreads();
     for (int e = threadIdx.x; e < p.E; e += kGroupThreads) {
         int s = 0;
@@ -154,12 +160,14 @@ __device__ __forceinline__ void group_deal(const GroupArgs &p, int chunk, int *h
     __shared__ int warp_sum[kGroupWarps];
     int *total = hist + kGroupWarps * p.E;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int64_t i0, i1;
+    int head[kIdsAhead];
+    run_of(p, chunk, warp, i0, i1);
+    load_ids(p, i0 + lane, i1, head);
     for (int i = threadIdx.x; i < kGroupWarps * p.E; i += kGroupThreads)
         hist[i] = 0;
     __syncthreads();
-    int64_t i0, i1;
-    run_of(p, chunk, warp, i0, i1);
-    count_run(p, i0, i1, hist + warp * p.E, lane);
+    count_run(p, i0, i1, head, hist + warp * p.E, lane);
     __syncthreads();
     // slots of each expert in all chunks and in those before: threads share out the chunks where experts are few
     int *before = total + p.E;
@@ -234,7 +242,11 @@ __device__ __forceinline__ void group_deal(const GroupArgs &p, int chunk, int *h
     int *at = hist + warp * p.E;
     for (int64_t i = i0; i < i1; i += 32 * kIdsAhead) {
         int ids[kIdsAhead];
-        load_ids(p, i + lane, i1, ids);
+#pragma unroll
+        for (int j = 0; j < kIdsAhead; ++j)
+            ids[j] = head[j];
+        if (i > i0)
+            load_ids(p, i + lane, i1, ids);
 #pragma unroll
         for (int j = 0; j < kIdsAhead; ++j) {
             const int id = ids[j];
@@ -408,21 +420,24 @@ __global__ void __launch_bounds__(kTermThreads) k_terms(const TermArgs p)
 
 // Rows of the gated activations (grouped.cuh: f16 under a power of two per 32), a
 // warp each; only those of some expert.
-__global__ void __launch_bounds__(kTermThreads) k_act_terms(const uint16_t *act, const uint8_t *exps, const int32_t *n, uint8_t *terms,
-                                                            float *scale)
+__global__ void __launch_bounds__(kTermThreads) k_act_terms(const uint16_t *act, const uint8_t *exps, const int32_t *n, int64_t most,
+                                                            uint8_t *terms, float *scale)
 {
     constexpr int kBlocks = kF / 32, kMine = (kF / 8 + 31) / 32;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * (kTermThreads / 32) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     tc::after_previous();
     tc::let_next_start();
-    if (row >= __ldcg(n))
+    if (row >= most)
         return;
+    const int rows = __ldcg(n);                  // (known when the row's values are: they are there, whatever they are)
     const int mine = lane < kBlocks ? __ldcg(exps + row * kBlocks + lane) : 0;
     uint4 u[kMine];
 #pragma unroll
     for (int i = 0; i < kMine; ++i)
         u[i] = i * 32 + lane < kF / 8 ? __ldcg(reinterpret_cast<const uint4 *>(act + row * kF) + i * 32 + lane) : make_uint4(0, 0, 0, 0);
+    if (row >= rows)
+        return;
     const int e = __reduce_max_sync(0xFFFFFFFFu, mine);
     if (lane == 0)
         scale[row] = row_scale(e);
@@ -535,7 +550,7 @@ __global__ void __launch_bounds__(kCombineThreads, 1) k_combine(const CombineArg
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kCombineStages; ++i) {
-            tc::bar_init(&full[i], 1);
+            tc::bar_init(&full[i], 2);           // the copies' bytes, and the factors
             tc::bar_init(&empty[i], kCombineTeam / 32);
         }
         abort_ = 0;
@@ -560,18 +575,11 @@ __global__ void __launch_bounds__(kCombineThreads, 1) k_combine(const CombineArg
             } else if (lane == kK && p.shared) {
                 at = __ldcg(p.offsets + kE) + static_cast<int>(t);
             }
-            const float f = at >= 0 ? w * (__ldcg(p.sa + at) * (__ldcg(p.smax + e) * 4096.0f)) : 0.0f;
-            const uint32_t rows_of = __ballot_sync(0xFFFFFFFFu, at >= 0);
+            const uint32_t rows_of = __ballot_sync(0xFFFFFFFFu, at >= 0), bar = tc::saddr(&full[slot]);
             if (n)
                 ok = wait(&empty[slot], n - 1, 44, static_cast<int>(t));
             if (!(ok = __all_sync(0xFFFFFFFFu, ok)))
                 break;
-            const uint32_t bar = tc::saddr(&full[slot]);
-            if (lane <= kK)
-                factor[slot][lane] = f;
-            if (lane == 0)
-                present[slot] = rows_of;         // (without a row a place of the ring holds anything)
-            __syncwarp();
             if (lane == 0)
                 tc::bar_expect(bar, __popc(rows_of) * 2 * kH);
             __syncwarp();
@@ -580,6 +588,13 @@ __global__ void __launch_bounds__(kCombineThreads, 1) k_combine(const CombineArg
                                  ring + slot * kCombineStage + lane * 2 * kH),
                              "l"(reinterpret_cast<uint64_t>(p.rows + static_cast<int64_t>(at) * kH)), "r"(2 * kH), "r"(bar)
                              : "memory");
+            if (lane <= kK)
+                factor[slot][lane] = at >= 0 ? w * (__ldcg(p.sa + at) * (__ldcg(p.smax + e) * 4096.0f)) : 0.0f;
+            if (lane == 0)
+                present[slot] = rows_of;         // (without a row a place of the ring holds anything)
+            __syncwarp();
+            if (lane == 0)
+                tc::bar_arrive(bar);
         }
         if (n)                                   // the last copies land before the CTA ends
             tc::bar_drain(tc::saddr(&full[slot]), (n - 1) & 1);

@@ -466,7 +466,7 @@ int fgm_moe_experts_fwd(const fgm_layer *layer, const uint16_t *x, int64_t x_str
     a.timeout_ns = host_wait_limit_ns();
     FGM_HOST_TRY((launch_grouped<grouped::kGated, true>(up, a, sms, st)));
     FGM_HOST_TRY(launch_overlapped(rows::k_act_terms, dim3(static_cast<unsigned>((R + 7) / 8)), rows::kTermThreads, 0, st, static_cast<const uint16_t *>(a.out), static_cast<const uint8_t *>(a.exps),
-                                   a.offsets + E, region<uint8_t>(ws, o.act_terms), region<float>(ws, o.sa)));
+                                   a.offsets + E, R, region<uint8_t>(ws, o.act_terms), region<float>(ws, o.sa)));
     grouped::Args d = a;
     d.src = nullptr;
     d.x_rows = static_cast<int>(R);
