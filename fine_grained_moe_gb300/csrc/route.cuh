@@ -293,7 +293,7 @@ __device__ __forceinline__ float key_value(uint32_t k) { return __int_as_float(s
 
 // A warp per token; lane l has experts l, l + 32, l + 64, l + 96. MOST: splits at most.
 template <int MOST>
-__global__ void __launch_bounds__(32 * kTopWarps, MOST == 1 ? 20 : 14) k_route_top(const TopArgs p)
+__global__ void __launch_bounds__(32 * kTopWarps, MOST == 1 ? 16 : 14) k_route_top(const TopArgs p)
 {
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kTopWarps + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
@@ -335,52 +335,67 @@ __global__ void __launch_bounds__(32 * kTopWarps, MOST == 1 ? 20 : 14) k_route_t
     if (__any_sync(0xFFFFFFFFu, bad) && lane == 0)
         atomicOr(p.status, FGM_STATUS_NONFINITE_LOGITS);
 
-    // the 8 largest: the largest key left, and the lowest expert that has it
+    // The 9 largest: a lane's keys in falling order, equal ones by expert, and the largest head of all in
+    // turn, of the lowest expert that has it. Lane r keeps the r-th.
     uint32_t key[4];
+    int who[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int q = 0; q < 4; ++q) {
         key[q] = order_key(v[q]);
-    unsigned taken = 0;
-    int top_i[kK];
-    float top_v[kK];
-#pragma unroll
-    for (int r = 0; r < kK; ++r) {
-        uint32_t best = 0;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            best = taken >> q & 1 ? best : max(best, key[q]);
-        best = __reduce_max_sync(0xFFFFFFFFu, best);
-        int e = kE;
-#pragma unroll
-        for (int q = 3; q >= 0; --q) {
-            const unsigned m = __ballot_sync(0xFFFFFFFFu, !(taken >> q & 1) && key[q] == best);
-            e = m ? q * 32 + __ffs(m) - 1 : e;
-        }
-        taken |= (e & 31) == lane ? 1u << (e >> 5) : 0u;
-        top_v[r] = key_value(best);
-        top_i[r] = e;
+        who[q] = q * 32 + lane;
     }
+#pragma unroll
+    for (int r = 0; r < 3; ++r)
+#pragma unroll
+        for (int q = 0; q < 3 - r; ++q) {
+            const bool swap = key[q + 1] > key[q];
+            const uint32_t k = key[q];
+            const int w = who[q];
+            key[q] = swap ? key[q + 1] : k;
+            who[q] = swap ? who[q + 1] : w;
+            key[q + 1] = swap ? k : key[q + 1];
+            who[q + 1] = swap ? w : who[q + 1];
+        }
+    uint32_t top_k = 0;
+    int top_i = 0;
+#pragma unroll
+    for (int r = 0; r <= kK; ++r) {
+        const uint32_t best = __reduce_max_sync(0xFFFFFFFFu, key[0]);
+        const int e = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, key[0] == best ? static_cast<unsigned>(who[0]) : ~0u));
+        const bool mine = who[0] == e;
+        top_k = lane == r ? best : top_k;
+        top_i = lane == r ? e : top_i;
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+            key[q] = mine ? key[q + 1] : key[q];
+            who[q] = mine ? who[q + 1] : who[q];
+        }
+        key[3] = mine ? 0u : key[3];             // (below every number's)
+    }
+    float top_v = key_value(top_k);
     // Twice the bound of a candidate's error: 2^-18 |x| |w| of its products, 2^-23 of the sum with the bias
     // (without an x the logits are the biases; experts masked by a bias of -inf have no near one).
-    float most = 0.0f;
-#pragma unroll
-    for (int r = 0; r < kK; ++r)
-        most = fabsf(top_v[r]) < INFINITY ? fmaxf(most, fabsf(top_v[r])) : most;
+    const float most = __uint_as_float(
+        __reduce_max_sync(0xFFFFFFFFu, lane < kK && fabsf(top_v) < INFINITY ? __float_as_uint(fabsf(top_v)) : 0u));
     const float gap = x2 > 0.0f ? 2.0f * (0x1p-18f * sqrtf(x2) * sqrtf(w2) + 0x1p-23f * most) : 0.0f;
-    if (gap > 0.0f && gap < INFINITY) {
+    // (in order, only neighbours can be the nearest)
+    const float next = __shfl_down_sync(0xFFFFFFFFu, top_v, 1);
+    const bool close = lane < kK && next > -INFINITY && (top_v - next <= gap || next >= top_v - gap);
+    if (gap > 0.0f && gap < INFINITY && __any_sync(0xFFFFFFFFu, close)) {
         // candidates with another candidate within the gap
+        const float last = __shfl_sync(0xFFFFFFFFu, top_v, kK - 1);
         unsigned cand = 0, near = 0;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            cand |= v[q] >= top_v[kK - 1] - gap ? 1u << q : 0u;
+            cand |= v[q] >= last - gap ? 1u << q : 0u;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
             for (unsigned m = __ballot_sync(0xFFFFFFFFu, cand >> q & 1); m; m &= m - 1) {
-                const int who = __ffs(m) - 1;
-                const float other = __shfl_sync(0xFFFFFFFFu, v[q], who);
+                const int at = __ffs(m) - 1;
+                const float other = __shfl_sync(0xFFFFFFFFu, v[q], at);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if ((cand >> j & 1) && !(who == lane && q == j) && fabsf(v[j] - other) <= gap)
+                    if ((cand >> j & 1) && !(at == lane && q == j) && fabsf(v[j] - other) <= gap)
                         near |= 1u << j;
             }
         if (__any_sync(0xFFFFFFFFu, near != 0)) {
@@ -419,47 +434,40 @@ __global__ void __launch_bounds__(32 * kTopWarps, MOST == 1 ? 20 : 14) k_route_t
             // each candidate's place by these: as many as are before it (as whole numbers in their order: a comparison of
             // doubles takes this GPU 16 cycles)
             uint64_t order[4];
-            float near_v[4];
             int place[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const long long bits = __double_as_longlong(z[q] + 0.0);
                 order[q] = static_cast<uint64_t>(bits ^ ((bits >> 63) | (1LL << 63)));
-                near_v[q] = static_cast<float>(z[q]);
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 for (unsigned m = __ballot_sync(0xFFFFFFFFu, cand >> q & 1); m; m &= m - 1) {
-                    const int who = __ffs(m) - 1;
-                    const uint64_t other = __shfl_sync(0xFFFFFFFFu, order[q], who);
+                    const int at = __ffs(m) - 1;
+                    const uint64_t other = __shfl_sync(0xFFFFFFFFu, order[q], at);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        place[j] += other > order[j] || (other == order[j] && who + 32 * q < lane + 32 * j);
+                        place[j] += other > order[j] || (other == order[j] && at + 32 * q < lane + 32 * j);
                 }
 #pragma unroll
-            for (int r = 0; r < kK; ++r)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const unsigned m = __ballot_sync(0xFFFFFFFFu, (cand >> q & 1) && place[q] == r);
-                    if (m) {
-                        top_i[r] = q * 32 + __ffs(m) - 1;
-                        top_v[r] = __shfl_sync(0xFFFFFFFFu, near_v[q], __ffs(m) - 1);
-                    }
+            for (int q = 0; q < 4; ++q)
+                for (unsigned m = __ballot_sync(0xFFFFFFFFu, cand >> q & 1); m; m &= m - 1) {
+                    const int at = __ffs(m) - 1, r = __shfl_sync(0xFFFFFFFFu, place[q], at);
+                    const float value = __shfl_sync(0xFFFFFFFFu, static_cast<float>(z[q]), at);
+                    top_i = lane == r ? q * 32 + at : top_i;
+                    top_v = lane == r ? value : top_v;
                 }
         }
     }
-    float ex[kK], sum = 0.0f;
-#pragma unroll
-    for (int r = 0; r < kK; ++r) {
-        ex[r] = top_v[0] == -INFINITY ? 1.0f : expf(top_v[r] - top_v[0]);
-        sum += ex[r];
-    }
+    const float largest = __shfl_sync(0xFFFFFFFFu, top_v, 0), ex = largest == -INFINITY ? 1.0f : expf(top_v - largest);
+    float sum = 0.0f;
 #pragma unroll
     for (int r = 0; r < kK; ++r)
-        if (lane == r) {
-            p.ids[t * kK + r] = top_i[r];
-            p.wts[t * kK + r] = ex[r] / sum;
-        }
+        sum += __shfl_sync(0xFFFFFFFFu, ex, r);
+    if (lane < kK) {
+        p.ids[t * kK + lane] = top_i;
+        p.wts[t * kK + lane] = ex / sum;
+    }
 }
 
 }  // namespace route
