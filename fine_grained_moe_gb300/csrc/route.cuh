@@ -7,7 +7,7 @@
 // tcgen05 and takes the accumulator out every 256 elements of K, to add it in fp32
 // registers: the tensor pipe truncates each addition, and 16 of them at a time stay
 // within 2^-18 |x| |w| in all (16 of 2^-23 of a partial sum, twice over). 16,381 tokens: 26
-// us, 3.6 TB/s of x, and 27 for k_route_top; 5 tokens 3 and 4 in a captured graph.
+// us, 3.6 TB/s of x, and 15 for k_route_top; 5 tokens 3 and 4 in a captured graph.
 //
 // Precision. Which experts a token takes is a whole number that hangs on logits that
 // may lie next to each other, so it goes by the exact ones. k_route_top knows a bound
@@ -242,44 +242,68 @@ struct TopArgs {
     int32_t *status;
 };
 
-constexpr int kTopWarps = 2;                    // (a CTA holds its place until its last token is done, one in twenty of which takes longer)
+constexpr int kTopWarps = 4;                    // tokens of a CTA, and the parts of K that its warps take of a near expert's logit
+constexpr int kUnits = kH / 256;                 // of 256 elements, eight a lane
+static_assert(kH % 256 == 0, "whole units");
 
-// x . w of two experts by one warp: two sums a lane of each, each addition's rounding error
-// added up beside it.
-__device__ __forceinline__ void exact_dots(const uint16_t *x, const uint16_t *w0, const uint16_t *w1, int lane, double &d0, double &d1)
+// (s, c) += v, s the rounded sum and c the sum of the roundings' errors.
+__device__ __forceinline__ void sum_exactly(float &s, float &c, float v)
+{
+    const float t = __fadd_rn(s, v), z = __fsub_rn(t, s);
+    c = __fadd_rn(c, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(v, z)));
+    s = t;
+}
+
+// A warp's part of x . w of two experts: two sums a lane of each. (Three units' loads on their way at
+// once, and a loop: its instructions are seldom in a cache.)
+__device__ __forceinline__ void exact_parts(const uint16_t *x, const uint16_t *w0, const uint16_t *w1, int part, int lane, double &d0, double &d1)
 {
     float s[2][2], c[2][2];
 #pragma unroll
     for (int q = 0; q < 2; ++q)
         s[0][q] = s[1][q] = c[0][q] = c[1][q] = 0.0f;
-#pragma unroll 4
-    for (int i = 0; i < kH / 256; ++i) {
-        const uint4 a = __ldcg(reinterpret_cast<const uint4 *>(x) + i * 32 + lane), b0 = __ldcg(reinterpret_cast<const uint4 *>(w0) + i * 32 + lane),
-                    b1 = __ldcg(reinterpret_cast<const uint4 *>(w1) + i * 32 + lane);
-        const uint32_t as[4] = {a.x, a.y, a.z, a.w}, bs[2][4] = {{b0.x, b0.y, b0.z, b0.w}, {b1.x, b1.y, b1.z, b1.w}};
+    constexpr int kMine = 3;
+#pragma unroll 1
+    for (int first = part; first < kUnits; first += kMine * kTopWarps) {
+        uint4 a[kMine], b[2][kMine];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const float2 u = bf16x2_to_f32(as[q]);
+        for (int i = 0; i < kMine; ++i) {
+            const int u = first + i * kTopWarps;
+            a[i] = u < kUnits ? __ldcg(reinterpret_cast<const uint4 *>(x) + u * 32 + lane) : make_uint4(0, 0, 0, 0);
+            b[0][i] = u < kUnits ? __ldcg(reinterpret_cast<const uint4 *>(w0) + u * 32 + lane) : make_uint4(0, 0, 0, 0);
+            b[1][i] = u < kUnits ? __ldcg(reinterpret_cast<const uint4 *>(w1) + u * 32 + lane) : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float2 v = bf16x2_to_f32(bs[k][q]);
+        for (int i = 0; i < kMine; ++i) {
+            const uint32_t as[4] = {a[i].x, a[i].y, a[i].z, a[i].w},
+                           bs[2][4] = {{b[0][i].x, b[0][i].y, b[0][i].z, b[0][i].w}, {b[1][i].x, b[1][i].y, b[1][i].z, b[1][i].w}};
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float prod = __fmul_rn(h ? u.y : u.x, h ? v.y : v.x);    // (16 bits: exact)
-                    const float t = __fadd_rn(s[k][h], prod), z = __fsub_rn(t, s[k][h]);
-                    c[k][h] = __fadd_rn(c[k][h], __fadd_rn(__fsub_rn(s[k][h], __fsub_rn(t, z)), __fsub_rn(prod, z)));
-                    s[k][h] = t;
+            for (int q = 0; q < 4; ++q) {
+                const float2 u = bf16x2_to_f32(as[q]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float2 v = bf16x2_to_f32(bs[k][q]);
+                    sum_exactly(s[k][0], c[k][0], __fmul_rn(u.x, v.x));    // (16 bits: exact products)
+                    sum_exactly(s[k][1], c[k][1], __fmul_rn(u.y, v.y));
                 }
             }
         }
     }
-    d0 = (static_cast<double>(s[0][0]) + static_cast<double>(c[0][0])) + (static_cast<double>(s[0][1]) + static_cast<double>(c[0][1]));
-    d1 = (static_cast<double>(s[1][0]) + static_cast<double>(c[1][0])) + (static_cast<double>(s[1][1]) + static_cast<double>(c[1][1]));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        d0 += __shfl_xor_sync(0xFFFFFFFFu, d0, o);
-        d1 += __shfl_xor_sync(0xFFFFFFFFu, d1, o);
+    for (int k = 0; k < 2; ++k) {
+        c[k][0] = __fadd_rn(c[k][0], c[k][1]);
+        sum_exactly(s[k][0], c[k][0], s[k][1]);
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float s1 = __shfl_xor_sync(0xFFFFFFFFu, s[k][0], o), c1 = __shfl_xor_sync(0xFFFFFFFFu, c[k][0], o);
+            c[k][0] = __fadd_rn(c[k][0], c1);
+            sum_exactly(s[k][0], c[k][0], s1);
+        }
+    d0 = static_cast<double>(s[0][0]) + static_cast<double>(c[0][0]);
+    d1 = static_cast<double>(s[1][0]) + static_cast<double>(c[1][0]);
 }
 
 // Order-preserving whole numbers of floats (-0 as +0; NaNs do not occur here).
@@ -291,19 +315,41 @@ __device__ __forceinline__ uint32_t order_key(float v)
 
 __device__ __forceinline__ float key_value(uint32_t k) { return __int_as_float(static_cast<int>(k & 0x80000000u ? k ^ 0x80000000u : ~k)); }
 
-// A warp per token; lane l has experts l, l + 32, l + 64, l + 96. MOST: splits at most.
-template <int MOST>
-__global__ void __launch_bounds__(32 * kTopWarps, MOST == 1 ? 16 : 14) k_route_top(const TopArgs p)
+// The same of doubles. (A comparison of doubles takes this GPU 16 cycles.)
+__device__ __forceinline__ uint64_t order_key(double v)
 {
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kTopWarps + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
+    const long long b = __double_as_longlong(v + 0.0);
+    return static_cast<uint64_t>(b ^ ((b >> 63) | (1LL << 63)));
+}
+
+__device__ __forceinline__ double key_value(uint64_t k) { return __longlong_as_double(static_cast<long long>(k >> 63 ? k ^ (1ULL << 63) : ~k)); }
+
+// A token's candidates, in the order of their experts.
+struct Candidates {
+    uint64_t key[kE];
+    float v[kE];
+    uint8_t e[kE], near[kE];                     // near: those with another candidate within the gap
+    float pick_v[kK];
+    int pick_i[kK];
+};
+
+// A warp per token; lane l has experts l, l + 32, l + 64, l + 96. MOST: splits at most. The
+// CTA's warps share out the near experts' logits of all its tokens: one token in twenty has
+// some (a token a warp for itself: 100 tokens 17.7 us in all, now 14.6; 16,381 tokens 53 and 48).
+template <int MOST>
+__global__ void __launch_bounds__(32 * kTopWarps, MOST == 1 ? 8 : 7) k_route_top(const TopArgs p)
+{
+    __shared__ int ask[kTopWarps];               // two experts of each warp's token, or -1
+    __shared__ double answer[kTopWarps][kTopWarps][2];
+    __shared__ Candidates cands[kTopWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTopWarps, t = t0 + warp;
+    const bool has = t < p.T;
     tc::after_previous();
     tc::let_next_start();
-    if (t >= p.T)
-        return;
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, b[4], part[MOST][4];
     // (all of a token's parts on their way at once)
-    const float x2_part = lane < p.splits ? __ldcg(p.xn2 + lane * p.T + t) : 0.0f;
+    const float x2_part = has && lane < p.splits ? __ldcg(p.xn2 + lane * p.T + t) : 0.0f;
     float w2_part = 0.0f;
     if (lane < 4)
 #pragma unroll
@@ -316,7 +362,7 @@ __global__ void __launch_bounds__(32 * kTopWarps, MOST == 1 ? 16 : 14) k_route_t
     for (int s = 0; s < MOST; ++s)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            part[s][q] = s < p.splits ? __ldcg(p.part + (s * p.T + t) * kE + lane + 32 * q) : 0.0f;
+            part[s][q] = has && s < p.splits ? __ldcg(p.part + (s * p.T + t) * kE + lane + 32 * q) : 0.0f;
 #pragma unroll
     for (int s = 0; s < MOST; ++s)
 #pragma unroll
@@ -381,82 +427,86 @@ __global__ void __launch_bounds__(32 * kTopWarps, MOST == 1 ? 16 : 14) k_route_t
     // (in order, only neighbours can be the nearest)
     const float next = __shfl_down_sync(0xFFFFFFFFu, top_v, 1);
     const bool close = lane < kK && next > -INFINITY && (top_v - next <= gap || next >= top_v - gap);
+    Candidates &cand = cands[warp];
+    int n = 0, nears = 0;
     if (gap > 0.0f && gap < INFINITY && __any_sync(0xFFFFFFFFu, close)) {
-        // candidates with another candidate within the gap
-        const float last = __shfl_sync(0xFFFFFFFFu, top_v, kK - 1);
-        unsigned cand = 0, near = 0;
+        const float low = __shfl_sync(0xFFFFFFFFu, top_v, kK - 1) - gap;
+        const unsigned before = (1u << lane) - 1;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            cand |= v[q] >= last - gap ? 1u << q : 0u;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            for (unsigned m = __ballot_sync(0xFFFFFFFFu, cand >> q & 1); m; m &= m - 1) {
-                const int at = __ffs(m) - 1;
-                const float other = __shfl_sync(0xFFFFFFFFu, v[q], at);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if ((cand >> j & 1) && !(at == lane && q == j) && fabsf(v[j] - other) <= gap)
-                        near |= 1u << j;
+        for (int q = 0; q < 4; ++q) {
+            const unsigned m = __ballot_sync(0xFFFFFFFFu, v[q] >= low);
+            if (v[q] >= low) {
+                const int at = n + __popc(m & before);
+                cand.e[at] = static_cast<uint8_t>(q * 32 + lane);
+                cand.v[at] = v[q];
+                cand.key[at] = order_key(static_cast<double>(v[q]));
             }
-        if (__any_sync(0xFFFFFFFFu, near != 0)) {
-            double z[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                z[q] = static_cast<double>(v[q]);
-            // (two at a time: near ones come in pairs)
-            unsigned left[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                left[q] = __ballot_sync(0xFFFFFFFFu, near >> q & 1);
-            auto first = [&]() {
-                int e = -1;
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (e < 0 && left[q]) {
-                        e = q * 32 + __ffs(left[q]) - 1;
-                        left[q] &= left[q] - 1;
-                    }
-                return e;
-            };
-            for (int e0 = first(); e0 >= 0; e0 = first()) {
-                int e1 = first();
-                e1 = e1 < 0 ? e0 : e1;
+            n += __popc(m);
+        }
+        __syncwarp();
+        for (int j = lane; j - lane < n; j += 32) {
+            const float mine = cand.v[j < n ? j : 0];
+            bool near = false;
+            for (int i = 0; i < n; ++i)
+                near |= i != j && fabsf(mine - cand.v[i]) <= gap;
+            near &= j < n;
+            const unsigned m = __ballot_sync(0xFFFFFFFFu, near);
+            if (near)
+                cand.near[nears + __popc(m & before)] = static_cast<uint8_t>(j);
+            nears += __popc(m);
+        }
+        __syncwarp();
+    }
+    if (__syncthreads_or(nears)) {
+        // (two at a time: near ones come in pairs)
+        for (int r = 0;; r += 2) {
+            const bool more = r < nears;
+            const int at = more ? cand.near[r + (lane == 1 && r + 1 < nears)] : 0, e = more ? cand.e[at] : 0,
+                      e1 = __shfl_sync(0xFFFFFFFFu, e, 1);
+            if (lane == 0)
+                ask[warp] = more ? e | e1 << 8 : -1;
+            if (!__syncthreads_or(more))
+                break;
+            const float bias = more && lane < 2 && p.b ? __ldcg(p.b + e) : 0.0f;
+            for (int k = 0; k < kTopWarps; ++k) {
+                const int pair = ask[k];
+                if (pair < 0)
+                    continue;
                 double d0, d1;
-                exact_dots(p.x + t * p.stride, p.w + static_cast<int64_t>(e0) * kH, p.w + static_cast<int64_t>(e1) * kH, lane, d0, d1);
+                exact_parts(p.x + (t0 + k) * p.stride, p.w + static_cast<int64_t>(pair & 255) * kH, p.w + static_cast<int64_t>(pair >> 8) * kH, warp,
+                            lane, d0, d1);
+                if (lane < 2)
+                    answer[k][warp][lane] = lane ? d1 : d0;
+            }
+            __syncthreads();
+            if (more && lane < 2) {
+                double d = 0.0;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (lane + 32 * q == e0)
-                        z[q] = d0 + static_cast<double>(b[q]);
-                    if (lane + 32 * q == e1)
-                        z[q] = d1 + static_cast<double>(b[q]);
+                for (int k = 0; k < kTopWarps; ++k)
+                    d += answer[warp][k][lane];
+                cand.key[at] = order_key(d + static_cast<double>(bias));
+            }
+        }
+        if (nears) {
+            // each candidate's place: as many as are before it
+            __syncwarp();
+            for (int j = lane; j < n; j += 32) {
+                const uint64_t mine = cand.key[j];
+                int place = 0;
+                for (int i = 0; i < n; ++i) {
+                    const uint64_t other = cand.key[i];
+                    place += other > mine || (other == mine && i < j);
+                }
+                if (place < kK) {
+                    cand.pick_i[place] = cand.e[j];
+                    cand.pick_v[place] = static_cast<float>(key_value(mine));
                 }
             }
-            // each candidate's place by these: as many as are before it (as whole numbers in their order: a comparison of
-            // doubles takes this GPU 16 cycles)
-            uint64_t order[4];
-            int place[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const long long bits = __double_as_longlong(z[q] + 0.0);
-                order[q] = static_cast<uint64_t>(bits ^ ((bits >> 63) | (1LL << 63)));
+            __syncwarp();
+            if (lane < kK) {
+                top_i = cand.pick_i[lane];
+                top_v = cand.pick_v[lane];
             }
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                for (unsigned m = __ballot_sync(0xFFFFFFFFu, cand >> q & 1); m; m &= m - 1) {
-                    const int at = __ffs(m) - 1;
-                    const uint64_t other = __shfl_sync(0xFFFFFFFFu, order[q], at);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        place[j] += other > order[j] || (other == order[j] && at + 32 * q < lane + 32 * j);
-                }
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                for (unsigned m = __ballot_sync(0xFFFFFFFFu, cand >> q & 1); m; m &= m - 1) {
-                    const int at = __ffs(m) - 1, r = __shfl_sync(0xFFFFFFFFu, place[q], at);
-                    const float value = __shfl_sync(0xFFFFFFFFu, static_cast<float>(z[q]), at);
-                    top_i = lane == r ? q * 32 + at : top_i;
-                    top_v = lane == r ? value : top_v;
-                }
         }
     }
     const float largest = __shfl_sync(0xFFFFFFFFu, top_v, 0), ex = largest == -INFINITY ? 1.0f : expf(top_v - largest);
@@ -464,7 +514,7 @@ __global__ void __launch_bounds__(32 * kTopWarps, MOST == 1 ? 16 : 14) k_route_t
 #pragma unroll
     for (int r = 0; r < kK; ++r)
         sum += __shfl_sync(0xFFFFFFFFu, ex, r);
-    if (lane < kK) {
+    if (has && lane < kK) {
         p.ids[t * kK + lane] = top_i;
         p.wts[t * kK + lane] = ex / sum;
     }

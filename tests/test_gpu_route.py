@@ -68,6 +68,18 @@ def test_equal_rows_take_the_lower_index(fgm):
     check(fgm, x, w[:1].repeat(E, 1).contiguous(), None)
 
 
+@pytest.mark.parametrize("T", [7, 2500])
+@pytest.mark.parametrize("alike", [3, 9, 33, 40, 65])
+def test_many_near_experts(fgm, T, alike):
+    """Tokens side by side of which some have none, some few and some many logits that are near."""
+    x, w, b = inputs(T, 10 + alike)
+    w[20:20 + alike] = w[20]
+    b[20:20 + alike] = b[20] + torch.arange(alike, device="cuda") % 3 * 2.0 ** -20
+    check(fgm, x, w, b)
+    w[21:20 + alike:2, ::401] *= 1 + 2.0 ** -7
+    check(fgm, x, w, b)
+
+
 def test_tokens_of_zeros(fgm):
     x, w, b = inputs(33, 5)
     x[::3] = 0
