@@ -11,7 +11,7 @@ namespace rows {
 // ---------------------------------------------------------------- grouping
 //
 // Slots 0 .. n - 1 with ids[i] in [0, E) (others belong to no expert), stably sorted
-// by id: each chunk of slots is counted by a CTA; then each adds up the counts before
+// by id: each chunk of slots is counted by a CTA (a router's by k_route_top); then each adds up the counts before
 // it (of smaller ids, and of its own id in earlier chunks) and deals its slots, a
 // warp a run of consecutive ones. From 33 chunks on a kernel between them adds up the
 // counts once for all. No order of CTAs or atomics enters the result.

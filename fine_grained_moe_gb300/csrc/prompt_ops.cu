@@ -282,14 +282,6 @@ int fgm_moe_route(const uint16_t *router_w, const float *router_b, const uint16_
     a.wn2 = region<float>(ws, o.wn2);
     a.status = status_word(ws);
     a.timeout_ns = host_wait_limit_ns();
-    FGM_HOST_TRY(launch_overlapped(route::k_router_logits_tc, dim3(static_cast<unsigned>((T + 127) / 128), a.splits), route::kThreads,
-                                   route::kSmem, st, xmap, wmap, a));
-    const route::TopArgs b{a.part, a.xn2, a.wn2, router_b, x, x_stride, router_w, T, a.splits, ids, w, a.status};
-    const dim3 tops(static_cast<unsigned>((T + route::kTopWarps - 1) / route::kTopWarps));
-    FGM_HOST_TRY(a.splits == 1 ? launch_overlapped(route::k_route_top<1>, tops, 32 * route::kTopWarps, 0, st, b)
-                               : launch_overlapped(route::k_route_top<route::kChunks>, tops, 32 * route::kTopWarps, 0, st, b));
-    if (!offsets)
-        return FGM_OK;
     rows::GroupArgs g = {};
     g.ids = ids;
     g.n = T * kK;
@@ -298,7 +290,20 @@ int fgm_moe_route(const uint16_t *router_w, const float *router_b, const uint16_
     g.offsets = offsets;
     g.order = order;
     g.per = 1;
-    return launch_group(g, st);
+    cut_group(g);
+    if (offsets && g.chunks > 1) {               // (counted by the choice)
+        a.count = g.count;
+        a.counts = g.chunks * kE;
+    }
+    FGM_HOST_TRY(launch_overlapped(route::k_router_logits_tc, dim3(static_cast<unsigned>((T + 127) / 128), a.splits), route::kThreads,
+                                   route::kSmem, st, xmap, wmap, a));
+    const route::TopArgs b{a.part, a.xn2, a.wn2, router_b, x, x_stride, router_w, T, a.splits, ids, w, a.count, static_cast<unsigned>(g.chunk / kK), a.status};
+    const dim3 tops(static_cast<unsigned>((T + route::kTopWarps - 1) / route::kTopWarps));
+    FGM_HOST_TRY(a.splits == 1 ? launch_overlapped(route::k_route_top<1>, tops, 32 * route::kTopWarps, 0, st, b)
+                               : launch_overlapped(route::k_route_top<route::kChunks>, tops, 32 * route::kTopWarps, 0, st, b));
+    if (!offsets)
+        return FGM_OK;
+    return launch_deal(g, st);
 }
 
 size_t fgm_moe_group_workspace_bytes(int64_t n, int E)

@@ -38,6 +38,8 @@ struct LogitArgs {
     float *part;             // [splits][T][128]
     float *xn2;              // [splits][T] sums of squares
     float *wn2;              // [splits][4] the largest of each 32 experts
+    int32_t *count;          // the grouping's counts, made 0 for k_route_top
+    int counts;
     int32_t *status;
     long long timeout_ns;
 };
@@ -107,6 +109,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc::fence_after();
     tc::let_next_start();
+    for (int i = (blockIdx.y * gridDim.x + blockIdx.x) * kThreads + tid; i < p.counts; i += gridDim.x * gridDim.y * kThreads)
+        p.count[i] = 0;
     const uint32_t tmem = sh.tmem;
     const tc::Waiter wait{&sh.abort, p.status, p.timeout_ns};
 
@@ -239,6 +243,8 @@ struct TopArgs {
     int splits;
     int32_t *ids;            // [T][8]
     float *wts;              // [T][8]
+    int32_t *count;          // [chunks][128] choices of each expert by a chunk's tokens, or NULL
+    unsigned chunk;          // tokens of a chunk
     int32_t *status;
 };
 
@@ -517,6 +523,8 @@ __global__ void __launch_bounds__(32 * kTopWarps, MOST == 1 ? 8 : 7) k_route_top
     if (has && lane < kK) {
         p.ids[t * kK + lane] = top_i;
         p.wts[t * kK + lane] = ex / sum;
+        if (p.count)                             // (whole numbers: their order does not matter)
+            atomicAdd(p.count + static_cast<unsigned>(t) / p.chunk * kE + top_i, 1);
     }
 }
 
