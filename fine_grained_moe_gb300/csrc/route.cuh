@@ -3,7 +3,7 @@
 //
 // 2 * 128 * 2816 operations and 5.6 KB a token: bound by HBM at long prompts, by
 // latency at a few tokens, so K is split over CTAs while there are fewer tiles of
-// 128 tokens than SMs. k_router_logits runs M = 128 tokens x N = 128 experts on
+// 128 tokens than SMs. k_router_logits_tc runs M = 128 tokens x N = 128 experts on
 // tcgen05 and takes the accumulator out every 256 elements of K, to add it in fp32
 // registers: the tensor pipe truncates each addition, and 16 of them at a time stay
 // within 2^-18 |x| |w| in all (16 of 2^-23 of a partial sum, twice over). 16,381 tokens: 26

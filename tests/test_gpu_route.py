@@ -150,6 +150,28 @@ def test_groups_of_nothing_and_of_one(fgm):
     assert off.tolist() == [0] * 5 + [3000] and order.tolist() == list(range(3000))
 
 
+@pytest.mark.parametrize("T", [4097, 32769, 40961])
+def test_long_prompts_grouped_again(fgm, T):
+    """Chunks of 1,024 slots and of more, one workspace for other tokens, in a replayed graph, too."""
+    x, w, b = inputs(T, T)
+    ws = fgm.Workspace("cuda", nbytes=fgm.moe_route_workspace_bytes(T))
+    r = fgm.moe_route(w, x, b, ws=ws)
+    ids = r.ids.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fgm.moe_route(w, x, b, out=r, ws=ws)
+    for _ in range(3):
+        order = torch.sort(r.ids.flatten(), stable=True).indices
+        assert torch.equal(r.order.long(), order)
+        assert r.offsets.tolist() == [0] + torch.bincount(r.ids.flatten(), minlength=E).cumsum(0).tolist()
+        x.copy_(x.flip(0))
+        graph.replay()
+        ids = ids.flip(0)
+        assert torch.equal(r.ids, ids)
+    assert ws.status() == 0
+
+
 def test_binding_refusals(fgm):
     x, w, b = inputs(4, 1)
     for call in (lambda: fgm.moe_route(w, x.float()), lambda: fgm.moe_route(w, x[:, :2800]), lambda: fgm.moe_route(w[:64], x),
