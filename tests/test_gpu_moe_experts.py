@@ -57,6 +57,19 @@ def test_tokens(fgm, layer, T, shared):
     assert float((y.double() - want).norm() / want.norm()) < 2.0 ** -8
 
 
+@pytest.mark.parametrize("T", [4097, 33001])
+def test_long_prompts(fgm, layer, T):
+    """Chunks of 1,024 slots and of more: the same 300 tokens over and over, each time within the bound."""
+    x, ids, w = tokens(300, 12)
+    again = torch.arange(T, device="cuda") % 300
+    want, err = p64.experts(layer, x, ids, w, True)
+    bound = p64.rounded(want, err, torch.bfloat16)
+    y = run(fgm, layer, x[again], ids[again], w[again])
+    for t in range(0, T, 300):
+        n = min(300, T - t)
+        p64.within(y[t:t + n], want[:n], bound[:n])
+
+
 def test_one_expert_for_all(fgm, layer):
     x, ids, w = tokens(700, 5)
     ids[:] = 17                                    # all eight choices the same
