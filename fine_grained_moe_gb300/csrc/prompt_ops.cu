@@ -42,9 +42,10 @@ int group_chunk(int64_t n)
     return each <= 1024 ? 1024 : static_cast<int>(align_up(each, rows::kGroupThreads));
 }
 
+// Room for the counts of n slots, and of fewer (262,144 have more chunks than 262,145).
 size_t group_count_bytes(int64_t n, int E)
 {
-    const int64_t chunks = (n + group_chunk(n) - 1) / group_chunk(n);
+    const int64_t most = (n + 1023) / 1024, chunks = most < rows::kMaxChunks ? most : rows::kMaxChunks;
     return chunks > 1 ? sizeof(int32_t) * chunks * E : 0;
 }
 
@@ -73,10 +74,12 @@ int launch_group(rows::GroupArgs a, cudaStream_t st)
 
 // ---------------------------------------------------------------- routing
 
+constexpr int64_t kRouteCtas = 152;
+
 // K is split while the tiles of 128 tokens leave SMs idle.
 int route_splits(int64_t T)
 {
-    const int64_t s = 152 / ((T + 127) / 128);
+    const int64_t s = kRouteCtas / ((T + 127) / 128);
     return static_cast<int>(s < 1 ? 1 : s > route::kChunks ? route::kChunks : s);
 }
 
@@ -88,10 +91,12 @@ RouteWs route_ws(int64_t T)
 {
     RouteWs o;
     Carve c;
-    const int64_t s = route_splits(T);
-    o.part = c.take(sizeof(float) * s * T * kE);
-    o.xn2 = c.take(sizeof(float) * s * T);
-    o.wn2 = c.take(sizeof(float) * s * 4);
+    // Rows of partial sums, for T tokens and for fewer, whose K may be cut into more parts: a split K has at
+    // most 128 rows a CTA.
+    const int64_t split = route::kChunks * T < kRouteCtas * 128 ? route::kChunks * T : kRouteCtas * 128, n = split < T ? T : split;
+    o.part = c.take(sizeof(float) * n * kE);
+    o.xn2 = c.take(sizeof(float) * n);
+    o.wn2 = c.take(sizeof(float) * route::kChunks * 4);
     o.count = c.take(group_count_bytes(T * kK, kE));
     o.total = c.at;
     return o;

@@ -484,8 +484,9 @@ enum { FGM_E4M3 = 3 };
 #define FGM_MAX_GROUPS 1024       /* experts of fgm_moe_group and fgm_grouped_gemm */
 
 /* Bytes of workspace of fgm_moe_route, fgm_moe_group, fgm_grouped_gemm and
- * fgm_moe_experts_fwd (0 for sizes out of range). Such a workspace serves every other
- * entry point too, and fgm_workspace_init prepares it. */
+ * fgm_moe_experts_fwd (0 for sizes out of range). They never fall as a size grows: the
+ * largest call's workspace serves every smaller one. It serves every other entry point
+ * too, and fgm_workspace_init prepares it. */
 size_t fgm_moe_route_workspace_bytes(int64_t T);
 size_t fgm_moe_group_workspace_bytes(int64_t n, int E);
 size_t fgm_grouped_gemm_workspace_bytes(int64_t x_rows, int64_t R, int E, int N, int K);
