@@ -5,8 +5,10 @@
 // latency at a few tokens, so K is split over CTAs while there are fewer tiles of
 // 128 tokens than SMs. k_router_logits_tc runs M = 128 tokens x N = 128 experts on
 // tcgen05 and takes the accumulator out every 256 elements of K, to add it in fp32
-// registers: the tensor pipe truncates each addition, and 16 of them at a time stay
-// within 2^-18 |x| |w| in all (16 of 2^-23 of a partial sum, twice over). 16,381 tokens: 26
+// registers: the tensor pipe truncates each addition, to 2^-22 of what it has added, and 16
+// of them a chunk are within 2^-18 |x| |w| in all. The 11 chunks' additions in fp32 (and
+// splits') are within 2^-24 of their sum each, 0.18 of 2^-18: kLogitError covers both, and what
+// |x| itself is off by. 16,381 tokens: 26
 // us, 3.6 TB/s of x, and 15 for k_route_top; 5 tokens 3 and 4 in a captured graph.
 //
 // Precision. Which experts a token takes is a whole number that hangs on logits that
@@ -30,6 +32,7 @@ constexpr int kBox = 128 * 128;                  // 128 rows x 64 elements
 constexpr int kChunkBoxes = 4;                   // 256 elements of K between readings of the accumulator
 constexpr int kChunks = kH / 256;
 constexpr int kSmem = kStages * 2 * kBox + 1024;
+constexpr float kLogitError = 0x1.4p-18f;        // of |x| |w|
 static_assert(kH % 256 == 0 && kE == 128 && kK == 8, "the tiles are cut for these");
 
 struct LogitArgs {
@@ -425,11 +428,11 @@ __global__ void __launch_bounds__(32 * kTopWarps, MOST == 1 ? 8 : 7) k_route_top
         key[3] = mine ? 0u : key[3];             // (below every number's)
     }
     float top_v = key_value(top_k);
-    // Twice the bound of a candidate's error: 2^-18 |x| |w| of its products, 2^-23 of the sum with the bias
+    // Twice the bound of a candidate's error: kLogitError |x| |w| of its products, 2^-23 of the sum with the bias
     // (without an x the logits are the biases; experts masked by a bias of -inf have no near one).
     const float most = __uint_as_float(
         __reduce_max_sync(0xFFFFFFFFu, lane < kK && fabsf(top_v) < INFINITY ? __float_as_uint(fabsf(top_v)) : 0u));
-    const float gap = x2 > 0.0f ? 2.0f * (0x1p-18f * sqrtf(x2) * sqrtf(w2) + 0x1p-23f * most) : 0.0f;
+    const float gap = x2 > 0.0f ? 2.0f * (kLogitError * sqrtf(x2) * sqrtf(w2) + 0x1p-23f * most) : 0.0f;
     // (in order, only neighbours can be the nearest)
     const float next = __shfl_down_sync(0xFFFFFFFFu, top_v, 1);
     const bool close = lane < kK && next > -INFINITY && (top_v - next <= gap || next >= top_v - gap);
