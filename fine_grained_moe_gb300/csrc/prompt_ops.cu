@@ -285,6 +285,7 @@ int fgm_moe_route(const uint16_t *router_w, const float *router_b, const uint16_
     a.part = region<float>(ws, o.part);
     a.xn2 = region<float>(ws, o.xn2);
     a.wn2 = region<float>(ws, o.wn2);
+    a.w = router_w;
     a.status = status_word(ws);
     a.timeout_ns = host_wait_limit_ns();
     rows::GroupArgs g = {};

@@ -8,8 +8,8 @@
 // registers: the tensor pipe truncates each addition, to 2^-22 of what it has added, and 16
 // of them a chunk are within 2^-18 |x| |w| in all. The 11 chunks' additions in fp32 (and
 // splits') are within 2^-24 of their sum each, 0.18 of 2^-18: kLogitError covers both, and what
-// |x| itself is off by. 16,381 tokens: 26
-// us, 3.6 TB/s of x, and 15 for k_route_top; 5 tokens 3 and 4 in a captured graph.
+// |x| itself is off by. 16,381 tokens: 26 us, 3.6 TB/s of x, and 16 for k_route_top; 5 tokens 3
+// and 4 in a captured graph.
 //
 // Precision. Which experts a token takes is a whole number that hangs on logits that
 // may lie next to each other, so it goes by the exact ones. k_route_top knows a bound
@@ -18,6 +18,11 @@
 // 2 d from every other candidate are in order; the others' logits are summed again
 // without rounding error to speak of (each addition's error is kept, 2^-40 of the sum
 // remains), and the 8 chosen by these. About one token in twenty has such a pair.
+//
+// The bound holds over bf16's range, whose squares fp32 does not hold: a row whose sum of
+// squares is outside [kLow, kHigh] is read again and its norm taken under a power of two, which
+// enters the exact sums, too. Experts' rows that are not finite have no finite logits and stay
+// out of |w|; with one as large as 2^60 every two finite logits are near.
 #pragma once
 
 #include "tensor.cuh"
@@ -33,6 +38,10 @@ constexpr int kChunkBoxes = 4;                   // 256 elements of K between re
 constexpr int kChunks = kH / 256;
 constexpr int kSmem = kStages * 2 * kBox + 1024;
 constexpr float kLogitError = 0x1.4p-18f;        // of |x| |w|
+// Sums of squares that are taken as they are: between rows of such norms no sum of products overflows, and what products
+// below fp32's normal numbers lose is less than 2^-48 of |x| |w|.
+constexpr float kLow = 0x1p-90f, kHigh = 0x1p100f;
+constexpr float kHuge = 0x1p120f;                // stands for squares above it
 static_assert(kH % 256 == 0 && kE == 128 && kK == 8, "the tiles are cut for these");
 
 struct LogitArgs {
@@ -40,7 +49,8 @@ struct LogitArgs {
     int splits;              // of K
     float *part;             // [splits][T][128]
     float *xn2;              // [splits][T] sums of squares
-    float *wn2;              // [splits][4] the largest of each 32 experts
+    float *wn2;              // [splits][4] the largest of each 32 experts whose rows are finite
+    const uint16_t *w;       // [128][2816]
     int32_t *count;          // the grouping's counts, made 0 for k_route_top
     int counts;
     int32_t *status;
@@ -80,6 +90,17 @@ __device__ __forceinline__ float squares(uint32_t at, int first, float s)
         }
     }
     return s;
+}
+
+// The largest of eight bf16's bits without their signs.
+__device__ __forceinline__ uint32_t largest(const uint4 &v)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        m = max(m, max(w[q] & 0x7FFFu, w[q] >> 16 & 0x7FFFu));
+    return m;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -177,6 +198,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0)
                 tc::bar_arrive(tc::saddr(&sh.empty[slot]));
         }
+        if (experts && ok) {
+            // Rows whose squares fp32 does not hold, by the warp: zeros, not finite themselves, or beyond its range at either end.
+            for (uint32_t odd = __ballot_sync(0xFFFFFFFFu, !(sum > 0.0f && sum < INFINITY)); odd; odd &= odd - 1) {
+                const int row = __ffs(odd) - 1;
+                const uint16_t *w = p.w + static_cast<int64_t>((norm & 3) * 32 + row) * kH;
+                uint32_t m = 0;
+                for (int k = b0 * 64 + lane * 8; k < b1 * 64; k += 256)
+                    m = max(m, largest(__ldcg(reinterpret_cast<const uint4 *>(w + k))));
+                m = __reduce_max_sync(0xFFFFFFFFu, m);
+                if (lane == row)
+                    sum = m == 0 || m >= 0x7F80u ? 0.0f : sum == 0.0f ? 0x1p-149f : kHuge;
+            }
+        }
         if (experts) {
             const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(sum));
             if (tile == 0 && lane == 0)
@@ -263,9 +297,46 @@ __device__ __forceinline__ void sum_exactly(float &s, float &c, float v)
     s = t;
 }
 
-// A warp's part of x . w of two experts: two sums a lane of each. (Three units' loads on their way at
+// A power of two s that brings a row of x's largest element (its bits) to 1, and its inverse.
+__device__ __forceinline__ float row_power(uint32_t m, float &inverse)
+{
+    const int e = static_cast<int>(m >> 7), up = e > 253 ? 1 : e < 1 ? 253 : 254 - e;
+    inverse = __int_as_float((254 - up) << 23);
+    return __int_as_float(up << 23);
+}
+
+// |x| by a warp: the square root of a sum of squares under the row's power of two. 0: x is 0 or not finite.
+__device__ __noinline__ float row_norm(const uint16_t *x, int lane, float &power, float &inverse)
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u)
+        m = max(m, largest(__ldcg(reinterpret_cast<const uint4 *>(x) + u * 32 + lane)));
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    power = inverse = 1.0f;
+    if (m == 0 || m >= 0x7F80u)
+        return 0.0f;
+    power = row_power(m, inverse);
+    float s = 0.0f;
+#pragma unroll 1
+    for (int u = 0; u < kUnits; ++u) {
+        const uint4 v = __ldcg(reinterpret_cast<const uint4 *>(x) + u * 32 + lane);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float2 f = bf16x2_to_f32(w[q]);
+            s = fmaf(f.x * power, f.x * power, s);
+            s = fmaf(f.y * power, f.y * power, s);
+        }
+    }
+    return sqrtf(warp_sum(s));
+}
+
+// A warp's part of x . w of two experts, x times a power of two: two sums a lane of each. (Three units' loads on their way at
 // once, and a loop: its instructions are seldom in a cache.)
-__device__ __forceinline__ void exact_parts(const uint16_t *x, const uint16_t *w0, const uint16_t *w1, int part, int lane, double &d0, double &d1)
+template <bool SCALED>
+__device__ __forceinline__ void exact_parts(const uint16_t *x, const uint16_t *w0, const uint16_t *w1, float power, int part, int lane, double &d0,
+                                            double &d1)
 {
     float s[2][2], c[2][2];
 #pragma unroll
@@ -288,7 +359,11 @@ __device__ __forceinline__ void exact_parts(const uint16_t *x, const uint16_t *w
                            bs[2][4] = {{b[0][i].x, b[0][i].y, b[0][i].z, b[0][i].w}, {b[1][i].x, b[1][i].y, b[1][i].z, b[1][i].w}};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const float2 u = bf16x2_to_f32(as[q]);
+                float2 u = bf16x2_to_f32(as[q]);
+                if (SCALED) {
+                    u.x *= power;
+                    u.y *= power;
+                }
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const float2 v = bf16x2_to_f32(bs[k][q]);
@@ -341,6 +416,24 @@ struct Candidates {
     float pick_v[kK];
     int pick_i[kK];
 };
+
+// The near experts' logits of one token, x times a power of two, by its warp alone. (Seldom, and out of
+// line: in the choice's own code this took a microsecond of 16,381 tokens' 48.)
+__device__ __noinline__ void scaled_logits(Candidates &cand, int nears, const uint16_t *x, const uint16_t *w, const float *b, float power, int lane)
+{
+    for (int r = 0; r < nears; r += 2) {
+        const int at = cand.near[r + (lane == 1 && r + 1 < nears)], e = cand.e[at], e0 = __shfl_sync(0xFFFFFFFFu, e, 0),
+                  e1 = __shfl_sync(0xFFFFFFFFu, e, 1);
+        double d = 0.0;
+        for (int part = 0; part < kTopWarps; ++part) {
+            double d0, d1;
+            exact_parts<true>(x, w + static_cast<int64_t>(e0) * kH, w + static_cast<int64_t>(e1) * kH, power, part, lane, d0, d1);
+            d += lane ? d1 : d0;
+        }
+        if (lane < 2)
+            cand.key[at] = order_key(d / static_cast<double>(power) + static_cast<double>(b ? __ldcg(b + e) : 0.0f));
+    }
+}
 
 // A warp per token; lane l has experts l, l + 32, l + 64, l + 96. MOST: splits at most. The
 // CTA's warps share out the near experts' logits of all its tokens: one token in twenty has
@@ -432,13 +525,23 @@ __global__ void __launch_bounds__(32 * kTopWarps, MOST == 1 ? 8 : 7) k_route_top
     // (without an x the logits are the biases; experts masked by a bias of -inf have no near one).
     const float most = __uint_as_float(
         __reduce_max_sync(0xFFFFFFFFu, lane < kK && fabsf(top_v) < INFINITY ? __float_as_uint(fabsf(top_v)) : 0u));
-    const float gap = x2 > 0.0f ? 2.0f * (kLogitError * sqrtf(x2) * sqrtf(w2) + 0x1p-23f * most) : 0.0f;
+    float gap = 0.0f, power = 1.0f;
+    if (x2 >= kLow && x2 <= kHigh && w2 >= kLow && w2 <= kHigh) {
+        gap = 2.0f * (kLogitError * (x2 * rsqrtf(x2)) * (w2 * rsqrtf(w2)) + 0x1p-23f * most);
+    } else if (has && w2 != 0.0f) {
+        float inverse;
+        const float x1 = row_norm(p.x + t * p.stride, lane, power, inverse), w1 = w2 < kHuge ? sqrtf(fmaxf(w2, kLow)) : INFINITY;
+        // (2^-112: what products that fall below fp32's normal numbers may lose; elements of rows above kHigh and below kLow
+        // meet x at a size that keeps products and sums within fp32's range)
+        gap = x1 > 0.0f ? fmaxf(2.0f * (kLogitError * x1 * w1 * inverse + 0x1p-23f * most), 0x1p-112f) : 0.0f;
+        power = fminf(power * (w2 > kHigh ? 0x1p-20f : w2 < kLow ? 0x1p60f : 1.0f), 0x1p126f);
+    }
     // (in order, only neighbours can be the nearest)
     const float next = __shfl_down_sync(0xFFFFFFFFu, top_v, 1);
     const bool close = lane < kK && next > -INFINITY && (top_v - next <= gap || next >= top_v - gap);
     Candidates &cand = cands[warp];
     int n = 0, nears = 0;
-    if (gap > 0.0f && gap < INFINITY && __any_sync(0xFFFFFFFFu, close)) {
+    if (gap > 0.0f && __any_sync(0xFFFFFFFFu, close)) {
         const float low = __shfl_sync(0xFFFFFFFFu, top_v, kK - 1) - gap;
         const unsigned before = (1u << lane) - 1;
 #pragma unroll
@@ -456,8 +559,10 @@ __global__ void __launch_bounds__(32 * kTopWarps, MOST == 1 ? 8 : 7) k_route_top
         for (int j = lane; j - lane < n; j += 32) {
             const float mine = cand.v[j < n ? j : 0];
             bool near = false;
-            for (int i = 0; i < n; ++i)
-                near |= i != j && fabsf(mine - cand.v[i]) <= gap;
+            for (int i = 0; i < n; ++i) {
+                const float d = fabsf(mine - cand.v[i]);
+                near |= i != j && d <= gap && d < INFINITY;
+            }
             near &= j < n;
             const unsigned m = __ballot_sync(0xFFFFFFFFu, near);
             if (near)
@@ -466,11 +571,16 @@ __global__ void __launch_bounds__(32 * kTopWarps, MOST == 1 ? 8 : 7) k_route_top
         }
         __syncwarp();
     }
-    if (__syncthreads_or(nears)) {
+    int asks = nears;
+    if (power != 1.0f) {
+        scaled_logits(cand, nears, p.x + t * p.stride, p.w, p.b, power, lane);
+        asks = 0;
+    }
+    if (__syncthreads_or(asks)) {
         // (two at a time: near ones come in pairs)
         for (int r = 0;; r += 2) {
-            const bool more = r < nears;
-            const int at = more ? cand.near[r + (lane == 1 && r + 1 < nears)] : 0, e = more ? cand.e[at] : 0,
+            const bool more = r < asks;
+            const int at = more ? cand.near[r + (lane == 1 && r + 1 < asks)] : 0, e = more ? cand.e[at] : 0,
                       e1 = __shfl_sync(0xFFFFFFFFu, e, 1);
             if (lane == 0)
                 ask[warp] = more ? e | e1 << 8 : -1;
@@ -482,8 +592,8 @@ __global__ void __launch_bounds__(32 * kTopWarps, MOST == 1 ? 8 : 7) k_route_top
                 if (pair < 0)
                     continue;
                 double d0, d1;
-                exact_parts(p.x + (t0 + k) * p.stride, p.w + static_cast<int64_t>(pair & 255) * kH, p.w + static_cast<int64_t>(pair >> 8) * kH, warp,
-                            lane, d0, d1);
+                exact_parts<false>(p.x + (t0 + k) * p.stride, p.w + static_cast<int64_t>(pair & 255) * kH, p.w + static_cast<int64_t>(pair >> 8) * kH,
+                                   1.0f, warp, lane, d0, d1);
                 if (lane < 2)
                     answer[k][warp][lane] = lane ? d1 : d0;
             }
@@ -496,26 +606,26 @@ __global__ void __launch_bounds__(32 * kTopWarps, MOST == 1 ? 8 : 7) k_route_top
                 cand.key[at] = order_key(d + static_cast<double>(bias));
             }
         }
-        if (nears) {
-            // each candidate's place: as many as are before it
-            __syncwarp();
-            for (int j = lane; j < n; j += 32) {
-                const uint64_t mine = cand.key[j];
-                int place = 0;
-                for (int i = 0; i < n; ++i) {
-                    const uint64_t other = cand.key[i];
-                    place += other > mine || (other == mine && i < j);
-                }
-                if (place < kK) {
-                    cand.pick_i[place] = cand.e[j];
-                    cand.pick_v[place] = static_cast<float>(key_value(mine));
-                }
+    }
+    if (nears) {
+        // each candidate's place: as many as are before it
+        __syncwarp();
+        for (int j = lane; j < n; j += 32) {
+            const uint64_t mine = cand.key[j];
+            int place = 0;
+            for (int i = 0; i < n; ++i) {
+                const uint64_t other = cand.key[i];
+                place += other > mine || (other == mine && i < j);
             }
-            __syncwarp();
-            if (lane < kK) {
-                top_i = cand.pick_i[lane];
-                top_v = cand.pick_v[lane];
+            if (place < kK) {
+                cand.pick_i[place] = cand.e[j];
+                cand.pick_v[place] = static_cast<float>(key_value(mine));
             }
+        }
+        __syncwarp();
+        if (lane < kK) {
+            top_i = cand.pick_i[lane];
+            top_v = cand.pick_v[lane];
         }
     }
     const float largest = __shfl_sync(0xFFFFFFFFu, top_v, 0), ex = largest == -INFINITY ? 1.0f : expf(top_v - largest);

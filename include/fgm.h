@@ -495,8 +495,11 @@ size_t fgm_moe_experts_workspace_bytes(int64_t T);
 /* Routing of T tokens: l = router_w x + router_b, the 8 experts with the largest
  * logits (descending; ties to the lower index) and w = softmax over these 8, which is
  * the renormalised softmax over all. Chosen by the exact logits: where fp32 could
- * misplace two, they are summed again to 2^-40. A NaN logit counts as -inf
- * (FGM_STATUS_NONFINITE_LOGITS); a bias of -inf masks an expert.
+ * misplace two, they are summed again to 2^-40 of |x| |w|, |w| the largest norm of a row
+ * of router_w. That holds for finite rows as long as |x| |w| stays below 2^120. The
+ * weights are those of logits within 1.25 * 2^-18 |x| |w| (of those summed again, 2^-24 of
+ * themselves). A NaN logit counts as -inf (FGM_STATUS_NONFINITE_LOGITS); a bias of -inf
+ * masks an expert, also one whose row is not finite.
  *  router_w  bf16 [128][2816], router_b fp32 [128] or NULL
  *  x         bf16 [T] rows of 2816, x_stride elements apart (a multiple of 8, at least
  *            2816), 16-byte aligned; 1 <= T <= FGM_MAX_TOKENS
