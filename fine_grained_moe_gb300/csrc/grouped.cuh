@@ -84,7 +84,7 @@ struct Shared {
     unsigned long long full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], drained;
     uint32_t tmem;
     int abort;
-    uint32_t issued;
+    uint32_t issued, passed;  // stages that the weights' warp has copied for at the end, and that it has found free
     uint32_t bytes[kMaxStages], others[kMaxStages];
     int row0[kMaxExperts], count[kMaxExperts], cum[kMaxExperts + 1];   // rows and tiles before, by expert
 };
@@ -143,6 +143,13 @@ struct Place {
             slot = 0;
             phase ^= 1;
         }
+    }
+    // n places on (once a tile at most)
+    __device__ __forceinline__ void skip(uint32_t n, uint32_t stages)
+    {
+        const uint32_t to = slot + n;
+        phase ^= to / stages & 1;
+        slot = to % stages;
     }
 };
 
@@ -236,6 +243,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
         }
         tc::bar_init(&sh.drained, 1);
         sh.abort = 0;
+        sh.passed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     tc::after_previous();
@@ -310,6 +318,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
                 for (int ks = 0; ks < steps; ++ks, ++n, at.next(stages)) {
                     if (n >= stages && !(ok = wait(&sh.empty[at.slot], at.phase ^ 1, 34, ks)))
                         break;
+                    if (p.src)
+                        asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(tc::saddr(&sh.passed)), "r"(n + 1) : "memory");
                     const uint32_t bar = full0 + at.slot * 8, dst = ring + at.slot * stage;
                     if (rank == 0)
                         tc::bar_expect(bar0 + at.slot * 8, 2 * mine);
@@ -381,13 +391,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
         // ------------------------------------------------------------ rows: gathered ones four a copy, a lane's of one half of K; else boxes
         if (p.src) {
             const int mate = warp < 4 ? warp - 2 : warp - kEpilogue - 2, h = lane & 1, group = (lane >> 1) * kGatherWarps + mate;
-            bool ok = true;
+            // A warp that has rows in a tile keeps the products from running on, so that no stage is used again behind its back.
+            // Without any it would have to see each of their phases in time (they turn after two); it leaves the tile out,
+            // and goes by the weights' warp when it comes back.
+            bool ok = true, left = false;
             uint32_t n = 0;
             Place place;
             for (int item = pair; item < items && ok; item += pairs) {
                 t.find(sh, p, item);
                 const int half = t.half(), at = rank * half + 4 * group;
                 const bool mine = 4 * group < half;
+                if (4 * mate >= half) {
+                    n += steps;
+                    place.skip(steps, stages);
+                    left = true;
+                    continue;
+                }
+                if (left && !(ok = __all_sync(0xFFFFFFFFu, wait.passed(&sh.passed, n, 43, t.e))))
+                    break;
+                left = false;
                 int v[4] = {0, 0, 0, 0};
                 // (places behind the tile's rows, and rows of x that are not there, take row 0: never stored)
 #pragma unroll

@@ -64,6 +64,25 @@ struct Waiter {
     int32_t *status;
     long long timeout_ns;
 
+    // Whether a wait is to give up; asked now and then.
+    __device__ __forceinline__ bool over(long long &since, int site, int index) const
+    {
+        if (*reinterpret_cast<volatile int *>(abort))
+            return true;
+        if (since == 0)
+            since = now_ns();
+        if (now_ns() - since <= timeout_ns)
+            return false;
+        *reinterpret_cast<volatile int *>(abort) = 1;
+        if ((atomicOr(status, FGM_STATUS_WAIT_TIMEOUT) & FGM_STATUS_WAIT_TIMEOUT) == 0) {
+            status[1] = site;
+            status[2] = blockIdx.x;
+            status[3] = threadIdx.x >> 5;
+            status[4] = index;
+        }
+        return true;
+    }
+
     __device__ __forceinline__ bool operator()(unsigned long long *bar, uint32_t phase, int site, int index) const
     {
         const uint32_t a = saddr(bar);
@@ -71,22 +90,23 @@ struct Waiter {
         for (int it = 0;; ++it) {
             if (bar_try(a, phase & 1))
                 return true;
-            if ((it & 255) == 255) {
-                if (*reinterpret_cast<volatile int *>(abort))
-                    return false;
-                if (since == 0)
-                    since = now_ns();
-                if (now_ns() - since > timeout_ns) {
-                    *reinterpret_cast<volatile int *>(abort) = 1;
-                    if ((atomicOr(status, FGM_STATUS_WAIT_TIMEOUT) & FGM_STATUS_WAIT_TIMEOUT) == 0) {
-                        status[1] = site;
-                        status[2] = blockIdx.x;
-                        status[3] = threadIdx.x >> 5;
-                        status[4] = index;
-                    }
-                    return false;
-                }
-            }
+            if ((it & 255) == 255 && over(since, site, index))
+                return false;
+        }
+    }
+
+    // The same for a count in shared memory to pass n.
+    __device__ __forceinline__ bool passed(const uint32_t *count, uint32_t n, int site, int index) const
+    {
+        const uint32_t a = saddr(count);
+        long long since = 0;
+        for (int it = 0;; ++it) {
+            uint32_t v;
+            asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+            if (v > n)
+                return true;
+            if ((it & 255) == 255 && over(since, site, index))
+                return false;
         }
     }
 };
