@@ -85,7 +85,8 @@ struct Shared {
     uint32_t tmem;
     int abort;
     uint32_t issued, passed;  // stages that the weights' warp has copied for at the end, and that it has found free
-    uint32_t bytes[kMaxStages], others[kMaxStages];
+    uint32_t bytes[kMaxStages];                  // of a CTA in each stage
+    score::StageNote sent[kGatherWarps][kMaxStages];         // what each rows' warp copied last to each place of the ring
     int row0[kMaxExperts], count[kMaxExperts], cum[kMaxExperts + 1];   // rows and tiles before, by expert
 };
 
@@ -220,6 +221,36 @@ struct Tile {
     __device__ __forceinline__ int half() const { return (live + 15) / 16 * 8; }
 };
 
+// After waits that ran out (pair_copies.h), in the pair's first CTA: the stages' barriers made up for what was not sent, of which
+// each CTA's weights are `weights` bytes a stage. Returns how far to wait for stages.
+__device__ __noinline__ uint32_t settle(Shared &sh, uint32_t stages, uint32_t weights)
+{
+    const uint32_t here = sh.issued, there = tc::of_second(tc::saddr(&sh.issued));
+    auto second = [&](int w, uint32_t slot) {
+        const uint32_t at = tc::saddr(&sh.sent[w][slot]);
+        return score::StageNote{tc::of_second(at), tc::of_second(at + 4)};
+    };
+    score::StagesLeft left;
+    left.note({here, weights});
+    left.note({there, weights});
+    for (int w = 0; w < kGatherWarps; ++w)
+        for (uint32_t slot = 0; slot < stages; ++slot) {
+            left.note(sh.sent[w][slot]);
+            left.note(second(w, slot));
+        }
+    for (uint32_t i = left.first(stages); i < left.to; ++i) {
+        const uint32_t slot = i % stages, bar = tc::saddr(&sh.full[slot]);
+        uint32_t sent = (i < here ? weights : 0) + (i < there ? weights : 0);
+        for (int w = 0; w < kGatherWarps; ++w)
+            sent += score::sent_bytes(sh.sent[w][slot], i) + score::sent_bytes(second(w, slot), i);
+        if (i >= here)
+            tc::bar_expect(bar, sent);
+        else if (sent != 2 * sh.bytes[slot])
+            asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(2 * sh.bytes[slot] - sent) : "memory");
+    }
+    return left.to;
+}
+
 template <Mode MODE, bool BYTES>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k_grouped(const __grid_constant__ Maps maps, const Args p)
 {
@@ -246,6 +277,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
         sh.passed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    for (int i = tid; i < kGatherWarps * kMaxStages; i += blockDim.x)
+        sh.sent[i / kMaxStages][i % kMaxStages].stage = 0;
     tc::after_previous();
     if (warp == 1)
         tc::memory_take<2>(&sh.tmem);
@@ -323,7 +356,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
                     const uint32_t bar = full0 + at.slot * 8, dst = ring + at.slot * stage;
                     if (rank == 0)
                         tc::bar_expect(bar0 + at.slot * 8, 2 * mine);
-                    sh.bytes[at.slot] = sh.others[at.slot] = mine;
+                    sh.bytes[at.slot] = mine;
                     copy_weights(dst, &maps.w, ks * kStageK, w0, t.e, bar, policy);
                     if (MODE == kGated)
                         copy_weights(dst + kBox, &maps.w2, ks * kStageK, w0, t.e, bar, policy);
@@ -419,11 +452,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
                         v[j] = s >= 0 && s / p.per < p.x_rows ? s / p.per : 0;
                     }
                 const int4 idx = make_int4(v[0], v[1], v[2], v[3]);
+                const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, mine)) * 512;
                 for (int ks = 0; ks < steps; ++ks, ++n, place.next(stages)) {
                     if (n >= stages)
                         ok = wait(&sh.empty[place.slot], place.phase ^ 1, 43, ks);
                     if (!(ok = __all_sync(0xFFFFFFFFu, ok)))
                         break;
+                    if (lane == 0)
+                        sh.sent[mate][place.slot] = {n + 1, bytes};
                     if (mine)
                         copy_gathered(ring + place.slot * stage + rows_at + h * xbox + group * 512, &maps.x[0], ks * 256 + h * 128, idx,
                                       full0 + place.slot * 8);
@@ -442,6 +478,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
                     if (n >= stages && !(ok = wait(&sh.empty[place.slot], place.phase ^ 1, 43, ks)))
                         break;
                     const uint32_t dst = ring + place.slot * stage + rows_at, bar = full0 + place.slot * 8;
+                    sh.sent[0][place.slot] = {n + 1, static_cast<uint32_t>(box.rows() * 256)};
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         copy_rows(dst + h * xbox, &maps.x[box.first], ks * 256 + h * 128, row, bar);
@@ -621,24 +658,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
     tc::cluster_sync();
     // nor before every copy that either issued has landed (the first sees both CTAs' bytes)
     if (rank == 0 && tid == 0) {
-        const uint32_t here = sh.issued;
-        const score::PairEnd e = score::pair_end(here, tc::of_second(tc::saddr(&sh.issued)), stages);
-        for (uint32_t i = e.only_from; i < e.to; ++i) {
-            const uint32_t slot = i % stages, bar = tc::saddr(&sh.full[slot]);
-            if (i < here)
-                asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(sh.others[slot]) : "memory");
-            else
-                tc::bar_expect(bar, tc::of_second(tc::saddr(&sh.bytes[slot])));
-        }
-        for (uint32_t i = e.first; i < e.to; ++i)
+        // (without a wait that ran out all warps have copied for all stages)
+        const uint32_t to = sh.abort || tc::of_second(tc::saddr(&sh.abort)) ? settle(sh, stages, kWBoxes * kBox) : sh.issued;
+        for (uint32_t i = to > stages ? to - stages : 0; i < to; ++i)
             tc::bar_drain(tc::saddr(&sh.full[i % stages]), (i / stages) & 1);
-    }
-    // (the count goes by the weights' copies: after a wait that ran out, rows may have been sent for further on; a
-    // millisecond is a thousand times what they take)
-    if (tid == 0 && sh.abort) {
-        const long long end = tc::now_ns() + 1000000;
-        while (tc::now_ns() < end)
-            ;
     }
     __syncthreads();
     tc::cluster_sync();

@@ -36,5 +36,28 @@ FGM_HOST_DEVICE PairEnd pair_end(uint32_t issued_here, uint32_t issued_there, ui
     return e;
 }
 
+// The same where several warps of each CTA bring parts of a stage (grouped.cuh: one
+// weights, others rows), each at its own pace: a warp's copies for stage n need the
+// products of stage n - stages, and those all warps' copies for it, so that no copy
+// is a ring ahead of what is to come. The first CTA arrives for all bytes of a stage
+// with its weights. Weights are the same bytes in every stage; a warp of rows notes its
+// copies' bytes by their place in the ring, with the stage, as it may have none in some. When waits ran out, the first CTA goes
+// through the notes: for the stages [first(), to) that are left to wait for, and in
+// each for the bytes that were sent, of which it takes the others out, or arrives for
+// these alone.
+struct StageNote {
+    uint32_t stage, bytes;   // stage: counted from 1; 0: none yet
+};
+
+struct StagesLeft {
+    uint32_t to = 0;
+
+    FGM_HOST_DEVICE void note(const StageNote &n) { to = n.stage > to ? n.stage : to; }
+    FGM_HOST_DEVICE uint32_t first(uint32_t stages) const { return to > stages ? to - stages : 0; }
+};
+
+// Bytes of a warp's copies for stage n (from 0), by its note at that place.
+FGM_HOST_DEVICE uint32_t sent_bytes(const StageNote &note, uint32_t n) { return note.stage == n + 1 ? note.bytes : 0; }
+
 }  // namespace score
 }  // namespace fgm

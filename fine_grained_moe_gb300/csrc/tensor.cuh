@@ -95,8 +95,8 @@ struct Waiter {
         }
     }
 
-    // The same for a count in shared memory to pass n.
-    __device__ __forceinline__ bool passed(const uint32_t *count, uint32_t n, int site, int index) const
+    // The same for a count in shared memory to pass n. (Seldom; out of line it costs its caller no registers.)
+    __device__ __noinline__ bool passed(const uint32_t *count, uint32_t n, int site, int index) const
     {
         const uint32_t a = saddr(count);
         long long since = 0;
