@@ -519,7 +519,7 @@ int fgm_moe_group(const int32_t *ids, int64_t n, int E, int32_t *offsets, int32_
 /* Products grouped by expert: for the rows r of expert e, offsets[e] <= r < offsets[e + 1],
  *   out[r][n] = w_s[e][n] * sum_k W_e[n][k] x[src(r)][k],
  * src(r) = rows[r] / per, or r without `rows`. With E4M3 weights x enters exactly
- * where an element is 2^-10 of its row's largest or more, the others to 2^-18 of that;
+ * where an element is 2^-9 of its row's largest or more, the others to 2^-17 of that;
  * fp32 accumulation on the tensor pipe, which truncates (each addition within 2^-22
  * of a partial sum). An x row with an element that is not finite gives NaN (E4M3).
  * Rows of no expert, and behind offsets[E], are left as they are; a row whose src(r)
@@ -539,9 +539,13 @@ int fgm_grouped_gemm(const uint16_t *x, int64_t x_stride, int64_t x_rows, const 
 /* A layer's experts on T tokens whose experts are chosen (by fgm_moe_route, or otherwise):
  *   y_t = sum_{i < 8} w[t][i] * expert_{ids[t][i]}(x_t) (+ expert_128(x_t) with `shared`),
  * expert_e as in fgm_moe_layer_fwd. An id outside [0, 128) adds nothing (a place of a
- * padded batch); an expert chosen twice counts twice. Activations enter the down
- * products as two E4M3 terms (2^-9 of themselves), an expert's output is rounded to 11
- * bits before the weighted sum, which is fp32.
+ * padded batch); an expert chosen twice counts twice. x enters as in fgm_grouped_gemm.
+ * Activations enter the down products as f16 (2^-11 of themselves) and then as two E4M3
+ * terms, to 2^-9 of themselves or 2^-17 of the token's largest in that expert, a,
+ * whichever is more (fgm_moe_layer_fwd keeps three terms, 2^-12). An expert's output is
+ * rounded before the weighted sum, which is fp32, to 2^-11 of itself or 2^-19 of a times
+ * the expert's largest down_s, whichever is more: a feature whose down_s is below about
+ * 2^-18 of that largest keeps fewer bits.
  *  layer  the experts' weights (router_w and router_b are not read)
  *  x      bf16 [T] rows of 2816, x_stride elements apart (a multiple of 8, at least 2816),
  *         16-byte aligned; 1 <= T <= FGM_MAX_TOKENS
