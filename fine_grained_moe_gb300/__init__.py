@@ -947,7 +947,10 @@ def grouped_gemm(x: torch.Tensor, w: torch.Tensor, w_s: torch.Tensor | None, off
 
     def body(s):
         o = torch.empty((R, N), dtype=_BF16, device=dev) if out is None else out
-        v = Workspace(dev, nbytes=grouped_gemm_workspace_bytes(x.shape[0], R, E, N, K)) if ws is None else ws
+        if ws is None:
+            v = Workspace(dev, nbytes=grouped_gemm_workspace_bytes(x.shape[0], R, E, N, K) if w.dtype is _U8 else 0)
+        else:
+            v = ws
         _check(lib().fgm_grouped_gemm(x.data_ptr(), stride, x.shape[0], r_at, per, o_at, w_at, E4M3 if w.dtype is _U8 else 1, s_at,
                                       E, N, K, o.data_ptr(), R, v.t.data_ptr(), v.nbytes, s))
         return o

@@ -369,12 +369,12 @@ int fgm_grouped_gemm(const uint16_t *x, int64_t x_stride, int64_t x_rows, const 
         return failf(FGM_ERR_INVALID_ARG, "w NULL or not 16-byte aligned");
     if (!out || !is_aligned(out, 2))
         return failf(FGM_ERR_INVALID_ARG, "out NULL or not aligned to an element");
+    const bool bytes = w_type == FGM_E4M3;
     const GemmWs o = gemm_ws(x_rows, K);
-    FGM_HOST_TRY(host_check_ws(ws, ws_bytes, o.total));
+    FGM_HOST_TRY(host_check_ws(ws, ws_bytes, bytes ? o.total : common_bytes()));      // (bf16 rows enter as they are)
     int sms = 0;
     FGM_HOST_TRY(host_device_ready(&sms));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool bytes = w_type == FGM_E4M3;
     grouped::Maps m;
     FGM_HOST_TRY(weight_map(&m.w, w, bytes ? 1 : 2, E, N, K));
     m.w2 = m.w;
@@ -393,7 +393,7 @@ int fgm_grouped_gemm(const uint16_t *x, int64_t x_stride, int64_t x_rows, const 
     a.N = N;
     a.K = K;
     a.s0 = w_s;
-    a.xs = region<float>(ws, o.xs);
+    a.xs = bytes ? region<float>(ws, o.xs) : nullptr;
     a.out = out;
     a.wide = N % 8 == 0 && is_aligned(out, 16);
     a.cols = tile_cols(R, E, 256);

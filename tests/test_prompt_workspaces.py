@@ -61,3 +61,13 @@ def test_a_workspace_for_the_largest_serves_the_smaller(lib):
         assert lib.fgm_moe_route(at, at, at, 2816, small, at, at, at, at, at, n, None) in (-3, -4), (small, large)
         n = lib.fgm_moe_group_workspace_bytes(8 * large, 128)
         assert lib.fgm_moe_group(at, 8 * small, 128, at + (1 << 40), at + (1 << 41), at, n, None) in (-3, -4), (small, large)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="host addresses must not reach a GPU")
+def test_bf16_weights_need_no_room_for_terms(lib):
+    at = 1 << 20
+    call = lambda kind, n: lib.fgm_grouped_gemm(at, 64, 1 << 20, None, 1, at, at, kind, None, 3, 10, 64, at, 1 << 20, at, n, None)      # noqa: E731
+    assert call(1, fgm.workspace_bytes(1)) in (-3, -4)
+    assert call(1, fgm.workspace_bytes(1) - 256) == -2
+    full = lib.fgm_grouped_gemm_workspace_bytes(1 << 20, 1 << 20, 3, 10, 64)
+    assert call(3, fgm.workspace_bytes(1)) == -2 and call(3, full) in (-3, -4) and call(3, full - 256) == -2
