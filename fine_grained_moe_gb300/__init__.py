@@ -653,6 +653,25 @@ def _call(device: torch.device, stream, body):
         return body(stream.cuda_stream)
 
 
+def _space(ws: Workspace | None, device: torch.device, size=None, *args) -> Workspace:
+    """The caller's workspace, or one of size(*args) bytes for this call."""
+    if ws is None:
+        return Workspace(device, nbytes=size(*args) if size else 0)
+    if ws.t.device != device:
+        raise FgmError(f"the workspace is on {ws.t.device}, the tensors on {device}")
+    return ws
+
+
+def _layer_on(layer, device: torch.device) -> fgm_layer:
+    """A layer's struct, its experts on ``device``."""
+    L = layer if isinstance(layer, Layer) else Layer.from_dict(layer)
+    for name in ("gate_q", "gate_s", "up_q", "up_s", "down_q", "down_s"):
+        t = getattr(L, name)
+        if t.device != device:
+            raise FgmError(f"{name}: expected a tensor on {device}, got {t.device}")
+    return L.struct()
+
+
 def _token_rows(name: str, t: torch.Tensor, heads: int, D: int, device) -> int:
     """bf16 [B, N, heads, D] whose tokens are dense and evenly spaced over the
     whole batch (a slice of a fused projection's output qualifies); returns the
@@ -700,7 +719,7 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, lens: torch.Tens
     at = _expect("lens", lens, (B,), _I32, dev)
 
     def body(s):
-        w = Workspace(dev) if ws is None else ws
+        w = _space(ws, dev)
         _check(lib().fgm_kv_append(C, k.data_ptr(), v.data_ptr(), step, B, N, at, table, mb, w.t.data_ptr(), w.nbytes, s))
     _call(dev, stream, body)
 
@@ -731,7 +750,7 @@ def attn_fwd(cache: KVCache, q: torch.Tensor, lens: torch.Tensor, scale: float,
 
     def body(s):
         o = torch.empty((B, M, Hq, D), dtype=_BF16, device=dev) if out is None else out
-        w = Workspace(dev, nbytes=attn_workspace_bytes(B, M, Hq, C.n_kv_heads, D)) if ws is None else ws
+        w = _space(ws, dev, attn_workspace_bytes, B, M, Hq, C.n_kv_heads, D)
         _check(lib().fgm_attn_fwd(C, q.data_ptr(), step, B, M, Hq, at, table, mb, scale, window,
                                   _expect("out", o, (B, M, Hq, D), _BF16, dev), lse_at, w.t.data_ptr(), w.nbytes, s))
         return o
@@ -794,7 +813,7 @@ def logprobs(z: torch.Tensor, tokens: torch.Tensor | None = None, k: int = 0, T:
 
     def body(s):
         r = _score_outs(N, k, tokens, entropy, out, dev)
-        w = Workspace(dev, nbytes=logprobs_workspace_bytes(N, V, k)) if ws is None else ws
+        w = _space(ws, dev, logprobs_workspace_bytes, N, V, k)
         _check(lib().fgm_logprobs(z.data_ptr(), _DTYPES[z.dtype], stride if N > 1 else V, N, V, T, at, k, _at(r.logp),
                                   _at(r.entropy), _at(r.top_ids), _at(r.top_logp), w.t.data_ptr(), w.nbytes, s))
         return r
@@ -823,7 +842,7 @@ def lm_head_logprobs(emb: torch.Tensor, h: torch.Tensor, tokens: torch.Tensor | 
 
     def body(s):
         r = _score_outs(N, k, tokens, entropy, out, dev)
-        w = Workspace(dev, nbytes=lm_head_logprobs_workspace_bytes(N, V, k)) if ws is None else ws
+        w = _space(ws, dev, lm_head_logprobs_workspace_bytes, N, V, k)
         _check(lib().fgm_lm_head_logprobs(e_at, V, h_at, N, T, at, k, _at(r.logp), _at(r.entropy), _at(r.top_ids),
                                           _at(r.top_logp), w.t.data_ptr(), w.nbytes, s))
         return r
@@ -879,7 +898,7 @@ def moe_route(router_w: torch.Tensor, x: torch.Tensor, router_b: torch.Tensor | 
                         torch.empty(EXPERTS + 1, dtype=_I32, device=dev), torch.empty(T * TOPK, dtype=_I32, device=dev))
         else:
             r = out
-        w = Workspace(dev, nbytes=moe_route_workspace_bytes(T)) if ws is None else ws
+        w = _space(ws, dev, moe_route_workspace_bytes, T)
         i, t, o, n = r
         _check(lib().fgm_moe_route(w_at, b_at, x.data_ptr(), stride, T, i.data_ptr(), t.data_ptr(), o.data_ptr(), n.data_ptr(),
                                    w.t.data_ptr(), w.nbytes, s))
@@ -906,7 +925,7 @@ def moe_group(ids: torch.Tensor, E: int, offsets: torch.Tensor | None = None, or
     def body(s):
         o = torch.empty(E + 1, dtype=_I32, device=dev) if offsets is None else offsets
         r = torch.empty(n, dtype=_I32, device=dev) if order is None else order
-        w = Workspace(dev, nbytes=moe_group_workspace_bytes(n, E)) if ws is None else ws
+        w = _space(ws, dev, moe_group_workspace_bytes, n, E)
         _check(lib().fgm_moe_group(at, n, E, _expect("offsets", o, (E + 1,), _I32, dev), _expect("order", r, (n,), _I32, dev),
                                    w.t.data_ptr(), w.nbytes, s))
         return o, r
@@ -947,10 +966,7 @@ def grouped_gemm(x: torch.Tensor, w: torch.Tensor, w_s: torch.Tensor | None, off
 
     def body(s):
         o = torch.empty((R, N), dtype=_BF16, device=dev) if out is None else out
-        if ws is None:
-            v = Workspace(dev, nbytes=grouped_gemm_workspace_bytes(x.shape[0], R, E, N, K) if w.dtype is _U8 else 0)
-        else:
-            v = ws
+        v = _space(ws, dev, grouped_gemm_workspace_bytes, x.shape[0], R, E, N, K) if w.dtype is _U8 else _space(ws, dev)
         _check(lib().fgm_grouped_gemm(x.data_ptr(), stride, x.shape[0], r_at, per, o_at, w_at, E4M3 if w.dtype is _U8 else 1, s_at,
                                       E, N, K, o.data_ptr(), R, v.t.data_ptr(), v.nbytes, s))
         return o
@@ -970,13 +986,13 @@ def moe_experts_fwd(layer, x: torch.Tensor, ids: torch.Tensor, weights: torch.Te
     dev = x.device
     stride = _dense_rows("x", x, HIDDEN)
     T = x.shape[0]
-    L = (layer if isinstance(layer, Layer) else Layer.from_dict(layer)).struct()
+    L = _layer_on(layer, dev)
     i_at = _expect("ids", ids, (T, TOPK), _I32, dev)
     w_at = _expect("weights", weights, (T, TOPK), _F32, dev)
 
     def body(s):
         o = torch.empty((T, HIDDEN), dtype=_BF16, device=dev) if y is None else y
-        w = Workspace(dev, nbytes=moe_experts_workspace_bytes(T)) if ws is None else ws
+        w = _space(ws, dev, moe_experts_workspace_bytes, T)
         _check(lib().fgm_moe_experts_fwd(ctypes.byref(L), x.data_ptr(), stride, T, i_at, w_at, int(shared),
                                          _expect("y", o, (T, HIDDEN), _BF16, dev), w.t.data_ptr(), w.nbytes, s))
         return o
