@@ -329,6 +329,13 @@ int fgm_moe_group(const int32_t *ids, int64_t n, int E, int32_t *offsets, int32_
     FGM_HOST_TRY(check_words("offsets", offsets));
     FGM_HOST_TRY(check_words("order", order));
     FGM_HOST_TRY(host_check_ws(ws, ws_bytes, fgm_moe_group_workspace_bytes(n, E)));
+    // (a CTA may read its ids when others have written)
+    auto meet = [](const void *a, int64_t na, const void *b, int64_t nb) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+        return x < y + 4 * nb && y < x + 4 * na;
+    };
+    if (meet(ids, n, offsets, E + 1) || meet(ids, n, order, n) || meet(offsets, E + 1, order, n))
+        return failf(FGM_ERR_INVALID_ARG, "ids, offsets and order overlap");
     FGM_HOST_TRY(host_device_ready(nullptr));
     rows::GroupArgs g = {};
     g.ids = ids;

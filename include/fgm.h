@@ -513,7 +513,7 @@ int fgm_moe_route(const uint16_t *router_w, const float *router_b, const uint16_
  * in ascending order. Slots whose id is outside [0, E) belong to none; the places
  * behind offsets[E] are left as they are.
  *  ids      int32 [n], 1 <= n <= 8 * FGM_MAX_TOKENS;  1 <= E <= FGM_MAX_GROUPS
- *  offsets  int32 [E + 1] output;  order  int32 [n] output */
+ *  offsets  int32 [E + 1] output;  order  int32 [n] output; apart from ids and each other */
 int fgm_moe_group(const int32_t *ids, int64_t n, int E, int32_t *offsets, int32_t *order, void *ws, size_t ws_bytes, void *stream);
 
 /* Products grouped by expert: for the rows r of expert e, offsets[e] <= r < offsets[e + 1],
