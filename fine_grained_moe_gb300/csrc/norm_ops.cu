@@ -33,10 +33,11 @@ bool apart(const Span &a, const Span &b)
     const uintptr_t a1 = a.at + (a.rows - 1) * a.stride + a.width, b1 = b.at + (b.rows - 1) * b.stride + b.width;
     if (a1 <= b.at || b1 <= a.at)
         return true;
-    if (a.stride != b.stride || a.stride <= 0)
+    // (a single row goes with any stride)
+    const int64_t s = a.rows == 1 ? b.stride : a.stride;
+    if ((b.rows != 1 && b.stride != s) || s <= 0)
         return false;
-    const int64_t s = a.stride, d = a.at <= b.at ? static_cast<int64_t>((b.at - a.at) % s)
-                                                 : static_cast<int64_t>((s - (a.at - b.at) % s) % s);
+    const int64_t d = a.at <= b.at ? static_cast<int64_t>((b.at - a.at) % s) : static_cast<int64_t>((s - (a.at - b.at) % s) % s);
     return d >= a.width && d + b.width <= s;
 }
 
