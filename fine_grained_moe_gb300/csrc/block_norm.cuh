@@ -237,7 +237,8 @@ __device__ __forceinline__ float row_gate(const Args &p, int64_t row)
 // Bytes of a row's pieces of a tensor in shared memory: padded to whole vectors of all threads.
 __host__ __device__ __forceinline__ int piece_bytes(const Rows &r, int type, int vectors) { return r.p && r.step ? vectors * 8 * (type == FGM_F32 ? 4 : 2) : 0; }
 
-// Rows of 16-byte accesses; STAGES rows in shared memory, the current one and those ahead.
+// Rows of 16-byte accesses; STAGES rows in shared memory, the current one and those ahead. (Beyond 8,192 elements
+// its 1,024 threads' two vectors each spill some 200 bytes: 8,191 bf16 rows of 8,200 167 us, of 8,192 the same.)
 template <int VPT, int STAGES>
 __global__ void __launch_bounds__(1024) k_block_norm(const Args p)
 {
@@ -325,10 +326,11 @@ __global__ void __launch_bounds__(1024) k_block_norm(const Args p)
 
 // ---------------------------------------------------------------- the usual rows
 //
-// bf16 y and xn, bf16 or fp32 h, no gate of an element each, up to 384 eights of elements: a
-// vector a thread. The general kernel above spends 490 instructions a warp and row, most of
+// bf16 y and xn, bf16 or fp32 h, no gate of an element each, up to 512 eights of elements (a sum's
+// warps are 16 at most): a vector a thread. The general kernel above spends 490 instructions a warp and row, most of
 // them on types and options (16,381 rows of 2,816: 114 us, issue-bound); this one has the
-// types built in, addresses that advance, and two fp32 operations to an instruction.
+// types built in, addresses that advance, and two fp32 operations to an instruction. 16,381 bf16
+// rows of 3,080 take 82 us here and 153 there, of 4,096 102 and 170.
 
 __device__ __forceinline__ uint64_t pair(float a, float b) { return static_cast<uint64_t>(__float_as_uint(a)) | static_cast<uint64_t>(__float_as_uint(b)) << 32; }
 __device__ __forceinline__ float low(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
@@ -404,12 +406,12 @@ __device__ __forceinline__ void give8(uint8_t *to, const uint64_t (&v)[4])
     }
 }
 
-constexpr int kUsualThreads = 384;               // at most
+constexpr int kUsualThreads = 512;               // at most
 constexpr int kUsualStages = 3;
 
 // F32: h. The gate is one value a row, or a channel's, which joins post's gain.
 template <bool F32>
-__global__ void __launch_bounds__(kUsualThreads, 4) k_block_norm_usual(const Args p)
+__global__ void __launch_bounds__(kUsualThreads, 3) k_block_norm_usual(const Args p)
 {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float part[2][16];
@@ -637,7 +639,8 @@ __global__ void __launch_bounds__(1024) k_block_norm_odd(const Args p)
     }
 }
 
-// Rows of any alignment, element by element, the next row's on their way (VPT = 4).
+// Rows of any alignment, element by element, the next row's on their way (VPT = 4). (VPT = 16, beyond 4,096 elements,
+// spills some 200 bytes and is slow: 4,099 bf16 rows of 8,195 643 us.)
 template <int VPT>
 __global__ void __launch_bounds__(1024) k_block_norm_any(const Args p)
 {
