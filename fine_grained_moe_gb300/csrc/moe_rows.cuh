@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(kCombineThreads, 1) k_combine(const CombineArg
                              "l"(reinterpret_cast<uint64_t>(p.rows + static_cast<int64_t>(at) * kH)), "r"(2 * kH), "r"(bar)
                              : "memory");
             if (lane <= kK)
-                factor[slot][lane] = at >= 0 ? w * (__ldcg(p.sa + at) * (__ldcg(p.smax + e) * 4096.0f)) : 0.0f;
+                factor[slot][lane] = at >= 0 ? w * (__ldcg(p.sa + at) * __ldcg(p.smax + e) * 4096.0f) : 0.0f;
             if (lane == 0)
                 present[slot] = rows_of;         // (without a row a place of the ring holds anything)
             __syncwarp();

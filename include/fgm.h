@@ -530,7 +530,8 @@ int fgm_moe_group(const int32_t *ids, int64_t n, int E, int32_t *offsets, int32_
  *  offsets  int32 [E + 1] (device), ascending
  *  w        [E][N][K] of w_type FGM_E4M3 (K a multiple of 16) or FGM_BF16 (K a multiple of
  *           8), 16-byte aligned;  1 <= N, K <= 65536
- *  w_s      fp32 [E][N], or NULL: 1
+ *  w_s      fp32 [E][N], or NULL: 1; with E4M3 weights below 2^111 / K (products meet it before
+ *           their row's power of two)
  *  out      bf16 [R][N] output, 1 <= R <= 2^24, apart from x
  *  ws       holds x's terms: 2 K bytes a row; with FGM_BF16 fgm_workspace_bytes(1, 0) are enough */
 int fgm_grouped_gemm(const uint16_t *x, int64_t x_stride, int64_t x_rows, const int32_t *rows, int per, const int32_t *offsets,
