@@ -12,11 +12,11 @@
 // the products' time again, and a prompt's are bound by it; the experts' outputs are 1.8e-3 off 64 bits
 // (root mean square), of which their own rounding to bf16 is 1.65e-3.
 //
-// 2 N K operations a row: bound by the weights' bytes while experts have few rows (1,024
-// rows on 128 experts of 1408 x 2816 take 88 us, 5.7 TB/s), by the tensor pipe from a few
-// hundred a piece on (32,768 rows of 2816 x 2816 320 us, 1.6 PFLOP/s, in bf16 275 us, 1.9;
-// a 16,381-token prompt's gate and up products 735 us, 1.6; its down products, whose 704 of
-// K end a tile every 6 stages, 415 us, 1.4). Weights are the products' first operand:
+// 2 N K operations a row: bound by the weights' bytes while experts have few rows (208
+// rows on 128 experts of 1408 x 2816 take 87 us, 5.8 TB/s), by the tensor pipe from a few
+// hundred a piece on (32,768 rows on 8 experts of 2816 x 2816 336 us, 1.55 PFLOP/s, of which 16
+// for the terms, in bf16 281 us, 1.85; a 16,381-token prompt's gate and up products 737 us, 1.6;
+// its down products, whose 704 of K end a tile every 6 stages, 414 us, 1.4). Weights are the products' first operand:
 //  * A pair of CTAs (cta_group::2) holds 256 features x up to 256 rows (gate and up: two
 //    such products of up to 128 rows) in one of two halves of tensor memory; an expert's
 //    rows are cut into equal tiles, whose width is the products' N, so that a few rows
@@ -25,7 +25,8 @@
 //    bytes with both terms of 64 elements (blocks of 32 of one and then of the other).
 //    Gathered rows come four a copy (tile::gather4) from six warps' lanes, the others in
 //    boxes of 8 to 128; a copy costs its warp some 80 cycles, whatever it brings
-//    (32,768 gathered rows of 2816 by one warp 1103 us, by these 441).
+//    (32,768 gathered rows of 2816 on 2816 features of 128 experts: 1103 us by one warp in the
+//    first kernel, 404 now; in order 369).
 //  * Both terms' products take the weights from one reading (collector::a).
 //  * Tiles of an expert go feature by feature, so that its rows are read from HBM once
 //    and its weights stay in L2 (rows first: 412 us where 344).
@@ -86,9 +87,10 @@ struct Shared {
     unsigned long long full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], drained;
     uint32_t tmem;
     int abort;
-    uint32_t issued, passed;  // stages that the weights' warp has copied for at the end, and that it has found free
+    uint32_t issued, passed;  // stages that the weights' warp has copied for at the end, and up to the first one of its tile, found free
     uint32_t bytes[kMaxStages];                  // of a CTA in each stage
-    score::StageNote sent[kGatherWarps][kMaxStages];         // what each rows' warp copied last to each place of the ring
+    uint32_t rows_issued[kGatherWarps];          // stages that each rows' warp has copied for at the end,
+    score::TileNote sent[kGatherWarps][kMaxStages];          // and its last tiles
     int row0[kMaxExperts], count[kMaxExperts], cum[kMaxExperts + 1];   // rows and tiles before, by expert
 };
 
@@ -225,26 +227,28 @@ struct Tile {
 
 // After waits that ran out (pair_copies.h), in the pair's first CTA: the stages' barriers made up for what was not sent, of which
 // each CTA's weights are `weights` bytes a stage. Returns how far to wait for stages.
-__device__ __noinline__ uint32_t settle(Shared &sh, uint32_t stages, uint32_t weights)
+__device__ __noinline__ uint32_t settle(Shared &sh, uint32_t stages, uint32_t K, uint32_t weights)
 {
+    const uint32_t steps = (K + kStageK - 1) / kStageK;
     const uint32_t here = sh.issued, there = tc::of_second(tc::saddr(&sh.issued));
-    auto second = [&](int w, uint32_t slot) {
-        const uint32_t at = tc::saddr(&sh.sent[w][slot]);
-        return score::StageNote{tc::of_second(at), tc::of_second(at + 4)};
-    };
     score::StagesLeft left;
-    left.note({here, weights});
-    left.note({there, weights});
-    for (int w = 0; w < kGatherWarps; ++w)
-        for (uint32_t slot = 0; slot < stages; ++slot) {
-            left.note(sh.sent[w][slot]);
-            left.note(second(w, slot));
-        }
+    left.warp(here);
+    left.warp(there);
+    for (int w = 0; w < kGatherWarps; ++w) {
+        left.warp(sh.rows_issued[w]);
+        left.warp(tc::of_second(tc::saddr(&sh.rows_issued[w])));
+    }
     for (uint32_t i = left.first(stages); i < left.to; ++i) {
         const uint32_t slot = i % stages, bar = tc::saddr(&sh.full[slot]);
         uint32_t sent = (i < here ? weights : 0) + (i < there ? weights : 0);
-        for (int w = 0; w < kGatherWarps; ++w)
-            sent += score::sent_bytes(sh.sent[w][slot], i) + score::sent_bytes(second(w, slot), i);
+        for (int w = 0; w < kGatherWarps; ++w) {
+            const uint32_t got = tc::of_second(tc::saddr(&sh.rows_issued[w]));
+            for (int k = 0; k < kMaxStages; ++k) {
+                const uint32_t at = tc::saddr(&sh.sent[w][k]);
+                sent += score::sent_bytes(sh.sent[w][k], steps, sh.rows_issued[w], i) +
+                        score::sent_bytes({tc::of_second(at), tc::of_second(at + 4)}, steps, got, i);
+            }
+        }
         if (i >= here)
             tc::bar_expect(bar, sent);
         else if (sent != 2 * sh.bytes[slot])
@@ -280,7 +284,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     for (int i = tid; i < kGatherWarps * kMaxStages; i += blockDim.x)
-        sh.sent[i / kMaxStages][i % kMaxStages].stage = 0;
+        sh.sent[i / kMaxStages][i % kMaxStages].first = ~0u;
+    if (tid < kGatherWarps)
+        sh.rows_issued[tid] = 0;
     tc::after_previous();
     if (warp == 1)
         tc::memory_take<2>(&sh.tmem);
@@ -353,7 +359,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
                 for (int ks = 0; ks < steps; ++ks, ++n, at.next(stages)) {
                     if (n >= stages && !(ok = wait(&sh.empty[at.slot], at.phase ^ 1, 34, ks)))
                         break;
-                    if (p.src)
+                    if (p.src && ks == 0)
                         asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(tc::saddr(&sh.passed)), "r"(n + 1) : "memory");
                     const uint32_t bar = full0 + at.slot * 8, dst = ring + at.slot * stage;
                     if (rank == 0)
@@ -442,6 +448,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
                     left = true;
                     continue;
                 }
+                if (lane == 0)                   // (its groups of four rows, in two copies each)
+                    sh.sent[mate][n / steps % kMaxStages] = {n, ((half >> 2) - mate + kGatherWarps - 1u) / kGatherWarps * 1024};
                 if (left && !(ok = __all_sync(0xFFFFFFFFu, wait.passed(&sh.passed, n, 43, t.e))))
                     break;
                 left = false;
@@ -454,19 +462,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
                         v[j] = s >= 0 && s / p.per < p.x_rows ? s / p.per : 0;
                     }
                 const int4 idx = make_int4(v[0], v[1], v[2], v[3]);
-                const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, mine)) * 512;
                 for (int ks = 0; ks < steps; ++ks, ++n, place.next(stages)) {
-                    if (n >= stages)
-                        ok = wait(&sh.empty[place.slot], place.phase ^ 1, 43, ks);
+                    ok = wait(&sh.empty[place.slot], place.phase ^ 1, 43, ks);       // (a new barrier has this parity behind it)
                     if (!(ok = __all_sync(0xFFFFFFFFu, ok)))
                         break;
-                    if (lane == 0)
-                        sh.sent[mate][place.slot] = {n + 1, bytes};
                     if (mine)
                         copy_gathered(ring + place.slot * stage + rows_at + h * xbox + group * 512, &maps.x[0], ks * 256 + h * 128, idx,
                                       full0 + place.slot * 8);
                     __syncwarp();
                 }
+                if (lane == 0)
+                    sh.rows_issued[mate] = n;
             }
         } else if (warp == 2 && lane == 0) {
             bool ok = true;
@@ -476,11 +482,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
                 t.find(sh, p, item);
                 const int half = t.half(), row = t.r0 + rank * half;
                 const RowBoxes box(half);
+                sh.sent[0][n / steps % kMaxStages] = {n, static_cast<uint32_t>(box.rows() * 256)};
                 for (int ks = 0; ks < steps; ++ks, ++n, place.next(stages)) {
                     if (n >= stages && !(ok = wait(&sh.empty[place.slot], place.phase ^ 1, 43, ks)))
                         break;
                     const uint32_t dst = ring + place.slot * stage + rows_at, bar = full0 + place.slot * 8;
-                    sh.sent[0][place.slot] = {n + 1, static_cast<uint32_t>(box.rows() * 256)};
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         copy_rows(dst + h * xbox, &maps.x[box.first], ks * 256 + h * 128, row, bar);
@@ -489,6 +495,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
                     }
                 }
             }
+            sh.rows_issued[0] = n;
         }
     } else {
         // ------------------------------------------------------------ epilogue: a lane is an output feature, a column a row of x
@@ -662,7 +669,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatherThreads, 1) k
     // nor before every copy that either issued has landed (the first sees both CTAs' bytes)
     if (rank == 0 && tid == 0) {
         // (without a wait that ran out all warps have copied for all stages)
-        const uint32_t to = sh.abort || tc::of_second(tc::saddr(&sh.abort)) ? settle(sh, stages, kWBoxes * kBox) : sh.issued;
+        const uint32_t to = sh.abort || tc::of_second(tc::saddr(&sh.abort)) ? settle(sh, p.stages, p.K, kWBoxes * kBox) : sh.issued;
         for (uint32_t i = to > stages ? to - stages : 0; i < to; ++i)
             tc::bar_drain(tc::saddr(&sh.full[i % stages]), (i / stages) & 1);
     }

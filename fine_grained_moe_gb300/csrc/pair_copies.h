@@ -40,24 +40,28 @@ FGM_HOST_DEVICE PairEnd pair_end(uint32_t issued_here, uint32_t issued_there, ui
 // weights, others rows), each at its own pace: a warp's copies for stage n need the
 // products of stage n - stages, and those all warps' copies for it, so that no copy
 // is a ring ahead of what is to come. The first CTA arrives for all bytes of a stage
-// with its weights. Weights are the same bytes in every stage; a warp of rows notes its
-// copies' bytes by their place in the ring, with the stage, as it may have none in some. When waits ran out, the first CTA goes
+// with its weights. Weights are the same bytes in every stage, rows in those of a tile,
+// of which each warp notes the first stage and its bytes a stage (tiles where it has
+// none, none), and at the end how far it got. When waits ran out, the first CTA goes
 // through the notes: for the stages [first(), to) that are left to wait for, and in
 // each for the bytes that were sent, of which it takes the others out, or arrives for
-// these alone.
-struct StageNote {
-    uint32_t stage, bytes;   // stage: counted from 1; 0: none yet
+// these alone. The stages of a ring belong to at most as many tiles.
+struct TileNote {
+    uint32_t first, bytes;   // first ~0: none yet
 };
 
 struct StagesLeft {
     uint32_t to = 0;
 
-    FGM_HOST_DEVICE void note(const StageNote &n) { to = n.stage > to ? n.stage : to; }
+    FGM_HOST_DEVICE void warp(uint32_t issued) { to = issued > to ? issued : to; }
     FGM_HOST_DEVICE uint32_t first(uint32_t stages) const { return to > stages ? to - stages : 0; }
 };
 
-// Bytes of a warp's copies for stage n (from 0), by its note at that place.
-FGM_HOST_DEVICE uint32_t sent_bytes(const StageNote &note, uint32_t n) { return note.stage == n + 1 ? note.bytes : 0; }
+// Bytes that a warp sent for stage n, if this tile's: of `steps` stages, of all of which it got to `issued`.
+FGM_HOST_DEVICE uint32_t sent_bytes(const TileNote &note, uint32_t steps, uint32_t issued, uint32_t n)
+{
+    return n >= note.first && n - note.first < steps && n < issued ? note.bytes : 0;
+}
 
 }  // namespace score
 }  // namespace fgm

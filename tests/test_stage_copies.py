@@ -25,49 +25,55 @@ def count(tmp_path_factory):
     d = tmp_path_factory.mktemp("stage")
     (d / "p.cpp").write_text(
         '#include "pair_copies.h"\nusing namespace fgm::score;\n'
-        'extern "C" void left(const StageNote *notes, int n, uint32_t stages, uint32_t *o)\n'
-        "{ StagesLeft l; for (int i = 0; i < n; ++i) l.note(notes[i]); o[0] = l.first(stages); o[1] = l.to; }\n"
-        'extern "C" uint32_t sent(uint32_t stage, uint32_t bytes, uint32_t n) { return sent_bytes({stage, bytes}, n); }\n')
+        'extern "C" void left(const uint32_t *issued, int n, uint32_t stages, uint32_t *o)\n'
+        "{ StagesLeft l; for (int i = 0; i < n; ++i) l.warp(issued[i]); o[0] = l.first(stages); o[1] = l.to; }\n"
+        'extern "C" uint32_t sent(uint32_t first, uint32_t bytes, uint32_t steps, uint32_t issued, uint32_t n)\n'
+        "{ return sent_bytes({first, bytes}, steps, issued, n); }\n")
     subprocess.run(["g++", "-O1", "-std=c++17", "-shared", "-fPIC", "-I", CSRC, "-o", str(d / "p.so"), str(d / "p.cpp")], check=True)
     lib = ctypes.CDLL(str(d / "p.so"))
     lib.sent.restype = ctypes.c_uint32
 
-    def left(notes, stages):
-        flat = [v for note in notes for v in note]
+    def left(issued, stages):
         o = (ctypes.c_uint32 * 2)()
-        lib.left((ctypes.c_uint32 * len(flat))(*flat), len(notes), stages, o)
+        lib.left((ctypes.c_uint32 * len(issued))(*issued), len(issued), stages, o)
         return tuple(o)
     return left, lib.sent
 
 
-def size(n, w):
-    """Bytes of warp w's copies for stage n: weights alike in both CTAs, rows by the tile (none in some)."""
-    return 64 if w < 2 else (n // 3 * 7 + w // 2 * 5) % 4 * 16
+NOTES = 12             # tiles that a warp's notes hold, and the longest ring
 
 
-def run(count, rng, total, stages, warps, by_weights=False):
-    """Warps 0 and 1 bring the CTAs' weights, the others rows in turn of the CTAs. Returns what was in flight when the
-    kernel left, whether it waited for what nobody sent, and how far the warps with copies were apart."""
+def size(tile, w):
+    """Bytes of warp w's copies for a stage of a tile: weights alike in both CTAs, rows by the tile (none in some)."""
+    return 64 if w < 2 else (tile * 7 + w // 2 * 5) % 4 * 16
+
+
+def run(count, rng, total, stages, steps, warps, by_weights=False):
+    """Warps 0 and 1 bring the CTAs' weights, the others rows in turn of the CTAs, for tiles of `steps` stages. Returns
+    what was in flight when the kernel left, whether it waited for what nobody sent, and how far the warps were apart."""
     left, sent = count
     full = [Barrier() for _ in range(stages)]
-    issued, alive, done, consumer = [0] * warps, [True] * warps, 0, True
-    notes = [[(0, 0)] * stages for _ in range(warps)]
+    at, alive, done, consumer = [0] * warps, [True] * warps, 0, True      # at: the stage that a warp is at
+    issued = [0] * warps                                         # and how far it has copied
+    notes = [[(0xFFFFFFFF, 0)] * NOTES for _ in range(warps)]
     flying = []
-    named = lambda n: sum(size(n, w) for w in range(warps))      # noqa: E731
+    named = lambda n: sum(size(n // steps, w) for w in range(warps))      # noqa: E731
     give_up = rng.random() < 0.9
     for _ in range(rng.randint(0, 30 * total * warps)):          # (then every wait that is left runs out)
         what = rng.random()
         if what < 0.6:
             w = rng.randrange(warps)
-            n = issued[w]
-            if alive[w] and n < total and size(n, w) == 0:       # (no rows: nothing to wait for)
-                issued[w] += 1
+            n = at[w]
+            b = size(n // steps, w)
+            if alive[w] and n < total and b == 0:                # (no rows: nothing to wait for)
+                at[w] += steps
             elif alive[w] and n < total and n - stages < done:
                 if w == 0:
                     full[n % stages].arrive(named(n))
-                flying.append((n, size(n, w)))
-                notes[w][n % stages] = (n + 1, size(n, w))
-                issued[w] += 1
+                flying.append((n, b))
+                if n % steps == 0:
+                    notes[w][n // steps % NOTES] = (n, b)
+                at[w] = issued[w] = n + 1
             elif give_up and rng.random() < 0.05:
                 alive[w] = False
         elif what < 0.85 and flying:
@@ -80,25 +86,25 @@ def run(count, rng, total, stages, warps, by_weights=False):
                 consumer = False
         if give_up and rng.random() < 0.02:
             alive[rng.randrange(warps)] = False
-    first, to = left([n for w in notes[:2 if by_weights else warps] for n in w], stages)
+    first, to = left(issued[:2] if by_weights else issued, stages)
     for n in range(first, to):
         if by_weights and min(issued[:2]) > n:                   # (a stage that both CTAs' weights were copied for counts as whole)
             continue
-        total_sent = sum(sent(*notes[w][n % stages], n) for w in range(warps))
+        total_sent = 64 * ((n < issued[0]) + (n < issued[1]))
+        total_sent += sum(sent(*note, steps, issued[w], n) for w in range(2, warps) for note in notes[w])
         if n >= issued[0]:
             assert full[n % stages].phase == n // stages, "arrives in the wrong phase"
             full[n % stages].arrive(total_sent)
         elif total_sent != named(n):
             assert full[n % stages].phase == n // stages, "makes up for the wrong phase"
             full[n % stages].land(named(n) - total_sent)
-    last = [max(n[0] for n in w) for w in notes]
     rng.shuffle(flying)
     while not all(full[n % stages].phase > n // stages for n in range(first, to)):
         if not flying:
-            return 0, True, max(last) - min(last)
+            return 0, True, max(issued) - min(issued)
         n, b = flying.pop()
         full[n % stages].land(b)
-    return len(flying), False, max(last) - min(last)
+    return len(flying), False, max(issued) - min(issued)
 
 
 @pytest.mark.parametrize("warps", [4, 14])          # rows by a warp of each CTA, and gathered by six
@@ -106,7 +112,8 @@ def test_no_copy_outlives_the_pair(count, warps):
     rng = random.Random(warps)
     apart = set()
     for _ in range(1500):
-        flying, stuck, d = run(count, rng, rng.randint(1, 30), rng.choice([1, 2, 4, 8, 12]), warps)
+        steps = rng.choice([1, 1, 2, 3, 5, 15, 22])
+        flying, stuck, d = run(count, rng, steps * rng.randint(1, 30 // steps), rng.choice([1, 2, 4, 8, 12]), steps, warps)
         assert flying == 0 and not stuck
         apart.add(d)
     assert 0 in apart and 12 in apart               # all together, and as far apart as the longest ring allows
@@ -116,5 +123,5 @@ def test_no_copy_outlives_the_pair(count, warps):
 def test_the_model_sees_a_count_of_weights_alone(count, warps):
     """Going by the weights' copies leaves rows in flight, or waits for rows that nobody sent."""
     rng = random.Random(warps)
-    ends = [run(count, rng, rng.randint(1, 30), rng.choice([1, 2, 4, 8, 12]), warps, True) for _ in range(1500)]
+    ends = [run(count, rng, 2 * rng.randint(1, 15), rng.choice([1, 2, 4, 8, 12]), 2, warps, True) for _ in range(1500)]
     assert any(e[0] for e in ends) and any(e[1] for e in ends)
