@@ -475,7 +475,9 @@ int fgm_lm_head_logprobs(const uint16_t *emb, int64_t V, const uint16_t *h, int6
  * The layer's experts on any number of tokens ("llm-decoding", §"The exact
  * architecture": top 8 of 128 and one shared): a prompt, or a batch of requests with
  * a token each. A slot is a (token, choice) pair, numbered 8 * token + choice.
- * Every call gives the same bits again. */
+ * Every call gives the same bits again. Up to FGM_MAX_M tokens fgm_moe_layer_fwd routes
+ * and computes a layer in one launch, faster (1 token 22 us in a captured graph, 8 tokens
+ * 46, where fgm_moe_route and fgm_moe_experts_fwd take 51 and 67) and with one term more. */
 
 /* Also an element type, of fgm_grouped_gemm's weights: codes with a scale per row. */
 enum { FGM_E4M3 = 3 };
@@ -552,7 +554,8 @@ int fgm_grouped_gemm(const uint16_t *x, int64_t x_stride, int64_t x_rows, const 
  *  x      bf16 [T] rows of 2816, x_stride elements apart (a multiple of 8, at least 2816),
  *         16-byte aligned; 1 <= T <= FGM_MAX_TOKENS
  *  ids    int32 [T][8];  w  fp32 [T][8]
- *  y      bf16 [T][2816] output, 16-byte aligned, apart from x */
+ *  y      bf16 [T][2816] output, 16-byte aligned, apart from x
+ *  ws     69 KB a token: 1.1 GB for 16,381 tokens, 18 GB for FGM_MAX_TOKENS */
 int fgm_moe_experts_fwd(const fgm_layer *layer, const uint16_t *x, int64_t x_stride, int64_t T, const int32_t *ids, const float *w,
                         int shared, uint16_t *y, void *ws, size_t ws_bytes, void *stream);
 
