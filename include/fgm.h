@@ -501,7 +501,8 @@ size_t fgm_moe_experts_workspace_bytes(int64_t T);
  * of router_w. That holds for finite rows as long as |x| |w| stays below 2^120. The
  * weights are those of logits within 1.25 * 2^-18 |x| |w| (of those summed again, 2^-24 of
  * themselves). A NaN logit counts as -inf (FGM_STATUS_NONFINITE_LOGITS); a bias of -inf
- * masks an expert, also one whose row is not finite.
+ * masks an expert, also one whose row is not finite. A logit of +inf comes first, and its
+ * token's weights are NaN.
  *  router_w  bf16 [128][2816], router_b fp32 [128] or NULL
  *  x         bf16 [T] rows of 2816, x_stride elements apart (a multiple of 8, at least
  *            2816), 16-byte aligned; 1 <= T <= FGM_MAX_TOKENS

@@ -103,3 +103,16 @@ def test_routers_of_zeros(fgm):
     assert (check(fgm, x, torch.zeros_like(w), None).ids == torch.arange(8, device="cuda")).all()
     r = fgm.moe_route(torch.zeros_like(w), x, b)
     assert torch.equal(r.ids.long(), torch.sort(b, descending=True, stable=True).indices[:8].expand(70, 8))
+
+
+@pytest.mark.parametrize("T", [9, 9729])
+def test_logits_of_plus_infinity(fgm, T):
+    """First in order, lower indices first; without a distribution, as in 64 bits."""
+    x, w, b = inputs(T, 10)
+    w = near_rows(w)
+    b[:] = 0
+    b[90] = b[33] = math.inf
+    ids, wt, _ = p64.route(w, x, b)
+    r = fgm.moe_route(w, x, b)
+    assert torch.equal(r.ids.long(), ids) and (r.ids[:, :2] == torch.tensor([33, 90], device="cuda")).all()
+    assert r.weights.isnan().all() and wt.isnan().all()
