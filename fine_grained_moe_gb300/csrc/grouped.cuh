@@ -14,8 +14,8 @@
 //
 // 2 N K operations a row: bound by the weights' bytes while experts have few rows (208
 // rows on 128 experts of 1408 x 2816 take 87 us, 5.8 TB/s), by the tensor pipe from a few
-// hundred a piece on (32,768 rows on 8 experts of 2816 x 2816 336 us, 1.55 PFLOP/s, of which 16
-// for the terms, in bf16 281 us, 1.85; a 16,381-token prompt's gate and up products 737 us, 1.6;
+// hundred a piece on (32,768 rows on 8 experts of 2816 x 2816 336 us with their terms,
+// 1.55 PFLOP/s, in bf16 281 us, 1.85; a 16,381-token prompt's gate and up products 737 us, 1.6;
 // its down products, whose 704 of K end a tile every 6 stages, 414 us, 1.4). Weights are the products' first operand:
 //  * A pair of CTAs (cta_group::2) holds 256 features x up to 256 rows (gate and up: two
 //    such products of up to 128 rows) in one of two halves of tensor memory; an expert's
